@@ -323,6 +323,41 @@ int32_t attn_kv_append_global(const void* qkv, const void* w_q, const void* w_k,
                               int32_t max_blocks, int64_t num_pages, int32_t* status, void* stream);
 
 /*
+ * attn_kv_append_sliding_chunk / attn_kv_append_global_chunk -- the same steps
+ * for any number of new tokens per sequence (a prompt, a piece of one, or a
+ * mix with single tokens), packed as the multi-query attention below takes
+ * its queries: sequence b caches seq_lens[b] tokens once the call is done,
+ * its new ones are rows cu_q[b] .. cu_q[b+1]-1 of qkv, and row i of them sits
+ * at position seq_lens[b] - (cu_q[b+1] - cu_q[b]) + i.  So q_out, seq_lens and
+ * cu_q go straight into attn_prefill_*.
+ *
+ * qkv          bf16 [total_q, row], rows as above
+ * block_table  int32 [batch, max_blocks]; only the pages of new tokens are read
+ * seq_lens     int32 [batch], new tokens included; <= max_blocks*16
+ * cu_q         int32 [batch + 1], cu_q[0] = 0, non-decreasing, cu_q[batch] <=
+ *              total_q; rows behind cu_q[batch] are neither read nor written
+ * q_out        bf16 [total_q, 16, D] (written)
+ * k_pool, v_pool  the decode's pools; attn_kv_append_global_chunk: k_pool may
+ *              be NULL for a values-only cache
+ * status       a sequence with more new tokens than seq_lens[b], a length
+ *              beyond the table, rows past total_q or a decreasing cu_q raises
+ *              ATTN_DEV_BAD_SEQ_LEN and nothing of it is written; a page id
+ *              outside [0, num_pages) raises ATTN_DEV_BAD_PAGE and that token's
+ *              cache row is not written (its q is)
+ *
+ * Two tokens of one call must not share a cache slot.  total_q 0 launches
+ * nothing.  Arithmetic and rounding as above.
+ */
+int32_t attn_kv_append_sliding_chunk(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
+                                     const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
+                                     void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
+                                     int64_t num_pages, int32_t* status, void* stream);
+int32_t attn_kv_append_global_chunk(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
+                                    const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
+                                    void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
+                                    int64_t num_pages, int32_t* status, void* stream);
+
+/*
  * attn_prefill_sliding / attn_prefill_global -- multi-query attention over the
  * paged cache, for a chunk of new tokens per sequence whose keys and values
  * are already in the cache (Attention.lean `causalGQA` / `slidingGQA` with

@@ -9,6 +9,13 @@ it is missing, ``load()`` raises instead of falling back to anything.
 
     attn_decode_sliding(q, k_pool, v_pool, block_table, seq_lens, ...)  -> o
     attn_decode_global(q, k_pool, v_pool, block_table, seq_lens, ...)   -> o
+
+Chunks of new tokens per sequence enter a bf16 cache through
+``attn_kv_append_{sliding,global}_chunk``.  An 8-bit cache (e4m3 values,
+power-of-two scales; ``include/attn_fp8.h``) is written by
+``attn_kv_append_{sliding,global}_fp8``, decoded over by
+``attn_decode_{sliding,global}_fp8`` and read back into bf16 pages by
+``attn_kv_read_{sliding,global}_fp8``; ``new_fp8_cache`` allocates one.
 """
 
 import ctypes
@@ -22,6 +29,12 @@ __all__ = [
     "attn_decode_sliding", "attn_decode_global", "attn_decode_global_shared", "attn_decode_plan",
     "attn_decode_workspace_size", "attn_decode_launches", "new_workspace", "WORKSPACE_ZERO_BYTES",
     "PreparedDecode", "prepare_decode_sliding", "prepare_decode_global", "prepare_decode_global_shared", "Step",
+    "attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk",
+    "attn_kv_append_sliding_fp8", "attn_kv_append_global_fp8", "attn_kv_read_sliding_fp8", "attn_kv_read_global_fp8",
+    "attn_decode_sliding_fp8", "attn_decode_global_fp8", "new_fp8_cache", "PreparedCall",
+    "prepare_kv_append_sliding_chunk", "prepare_kv_append_global_chunk", "prepare_kv_append_sliding_fp8",
+    "prepare_kv_append_global_fp8", "prepare_kv_read_sliding_fp8", "prepare_kv_read_global_fp8",
+    "prepare_decode_sliding_fp8", "prepare_decode_global_fp8",
     "attn_last_error", "load", "library_path", "AttnDecodeError",
     "KIND_SLIDING", "KIND_GLOBAL", "DEV_WAIT_TIMEOUT", "DEV_BAD_PAGE", "DEV_BAD_SEQ_LEN",
 ]
@@ -42,7 +55,13 @@ EXPORTS = ("attn_decode_sliding", "attn_decode_global", "attn_decode_global_shar
            "attn_step_create", "attn_step_destroy", "attn_step_add_decode_sliding", "attn_step_add_decode_global",
            "attn_step_add_decode_global_shared", "attn_step_add_kv_append_sliding", "attn_step_add_kv_append_global",
            "attn_step_num_calls", "attn_step_num_kernels", "attn_step_set_launch_mode", "attn_step_launch_mode",
-           "attn_step_finalize", "attn_step_launch", "attn_last_error", "attn_abi_version")
+           "attn_step_finalize", "attn_step_launch", "attn_last_error", "attn_abi_version",
+           "attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk", "attn_kv_append_sliding_fp8",
+           "attn_kv_append_global_fp8", "attn_kv_read_sliding_fp8", "attn_kv_read_global_fp8",
+           "attn_decode_sliding_fp8", "attn_decode_global_fp8", "attn_step_add_kv_append_sliding_chunk",
+           "attn_step_add_kv_append_global_chunk", "attn_step_add_kv_append_sliding_fp8",
+           "attn_step_add_kv_append_global_fp8", "attn_step_add_decode_sliding_fp8",
+           "attn_step_add_decode_global_fp8")
 # attn_step launch modes (attn_step.h)
 STEP_LAUNCH_AUTO, STEP_LAUNCH_GRAPH, STEP_LAUNCH_DIRECT = 0, 1, 2
 STEP_LAUNCH_MODES = {"auto": STEP_LAUNCH_AUTO, "graph": STEP_LAUNCH_GRAPH, "direct": STEP_LAUNCH_DIRECT}
@@ -102,6 +121,23 @@ def load(path=None):
         fn = getattr(lib, name)
         fn.restype = c_i32
         fn.argtypes = pre
+    chunk = [c_vp] * 9 + [c_i32, c_i32, c_i32, c_i64, c_vp, c_vp]  # qkv w_q w_k block_table seq_lens cu_q q_out k_pool
+    #                                v_pool; batch total_q max_blocks num_pages status stream
+    chunk8 = [c_vp] * 11 + chunk[9:]                                # ... and k_scale v_scale after v_pool
+    read8 = [c_vp] * 9 + [c_i32, c_i32, c_i64, c_i64, c_i32, c_i32, c_vp, c_vp]  # k_pool v_pool k_scale v_scale
+    #            block_table seq_lens k_out v_out out_table; batch max_blocks num_pages out_pages max_seq_len span ...
+    call8 = call[:3] + [c_vp, c_vp] + call[3:]                      # k_scale v_scale after v_pool
+    for names, types in ((("attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk"), chunk),
+                         (("attn_kv_append_sliding_fp8", "attn_kv_append_global_fp8"), chunk8),
+                         (("attn_kv_read_sliding_fp8", "attn_kv_read_global_fp8"), read8),
+                         (("attn_decode_sliding_fp8", "attn_decode_global_fp8"), call8)):
+        for name in names:
+            getattr(lib, name).restype = c_i32
+            getattr(lib, name).argtypes = types
+            if types is not read8:
+                step_name = name.replace("attn_", "attn_step_add_")
+                getattr(lib, step_name).restype = c_i32
+                getattr(lib, step_name).argtypes = [c_vp] + types[:-1]
     c_step = ctypes.c_void_p
     lib.attn_step_create.restype = c_i32
     lib.attn_step_create.argtypes = [ctypes.POINTER(c_step)]
@@ -347,6 +383,32 @@ class Step:
         return self._add_append(KIND_GLOBAL, "attn_step_add_kv_append_global", qkv, w_q, w_k, block_table,
                                 positions, k_pool, v_pool, q_out, status)
 
+    def _add(self, fn_name, args, keep, out, device):
+        """Record a checked, marshalled call under attn_step_add_*; returns its output."""
+        with torch.cuda.device(device):
+            self._check(getattr(self._lib, fn_name.replace("attn_", "attn_step_add_"))(self._h, *args))
+        self._keep.append(keep)
+        self.device = device
+        return out
+
+    def add_kv_append_sliding_chunk(self, *args, **kw):
+        return self._add(*_chunk_args(KIND_SLIDING, *args, **kw))
+
+    def add_kv_append_global_chunk(self, *args, **kw):
+        return self._add(*_chunk_args(KIND_GLOBAL, *args, **kw))
+
+    def add_kv_append_sliding_fp8(self, *args, **kw):
+        return self._add(*_append_fp8_args(KIND_SLIDING, *args, **kw))
+
+    def add_kv_append_global_fp8(self, *args, **kw):
+        return self._add(*_append_fp8_args(KIND_GLOBAL, *args, **kw))
+
+    def add_decode_sliding_fp8(self, *args, **kw):
+        return self._add(*_decode_fp8_args(KIND_SLIDING, *args, **kw))
+
+    def add_decode_global_fp8(self, *args, **kw):
+        return self._add(*_decode_fp8_args(KIND_GLOBAL, *args, **kw))
+
     @property
     def num_calls(self):
         return self._lib.attn_step_num_calls(self._h)
@@ -553,3 +615,287 @@ def selftest_delayed_copy(dst, src, delay_ns=5000, stream=None):
     rc = load().attn_selftest_delayed_copy(dst.data_ptr(), src.data_ptr(), dst.numel() * 4, int(delay_ns), s_ptr)
     if rc != ATTN_OK:
         raise AttnDecodeError(rc, attn_last_error())
+
+
+# ---------------------------------------------------------------------------
+# Chunk appends and the 8-bit cache (include/attn_fp8.h).  Every call has three
+# forms: the one-shot function, prepare_* (a PreparedCall for buffers used
+# again and again) and, but for the read, Step.add_*.
+# ---------------------------------------------------------------------------
+
+FP8 = torch.float8_e4m3fn    # cache values
+E8M0 = torch.float8_e8m0fnu  # cache scales: 2^(byte - 127)
+
+
+class PreparedCall:
+    """A call whose arguments are checked and marshalled once, as PreparedDecode does for a decode.
+
+    ``run(stream)`` enqueues it with one C call and returns its output; the
+    tensors must stay in place (the object keeps them alive), their contents
+    may change between runs.
+    """
+
+    def __init__(self, fn_name, args, keep, out, device):
+        self._fn = getattr(load(), fn_name)
+        self._args, self._keep, self.out, self._device = args, keep, out, device
+
+    def run(self, stream=None):
+        """Enqueue the call on `stream` (default: the current stream of its device); returns its output."""
+        s_ptr = _stream_ptr(stream, self._device)
+        if torch.cuda.current_device() == self._device.index:
+            st = self._fn(*self._args, s_ptr)
+        else:
+            with torch.cuda.device(self._device):
+                st = self._fn(*self._args, s_ptr)
+        if st != ATTN_OK:
+            raise AttnDecodeError(st, attn_last_error())
+        return self.out
+
+
+def _one_device(tensors):
+    """The device that all of the tensors (None left out) are on."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError("all tensors must be on one device, got %s" % ", ".join(sorted(map(str, devices))))
+    return devices.pop()
+
+
+def _dims(t, n, what):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % what.split(" ")[0])
+    if t.dim() != n:
+        raise ValueError("%s" % what)
+
+
+def _status_ptr(status):
+    return None if status is None else _ptr(status, "status", torch.int32, (1,))
+
+
+def new_fp8_cache(kind, num_pages, device):
+    """An empty 8-bit cache of one layer: (k_pool, v_pool, k_scale, v_scale), zeros."""
+    _, Hkv, D = SHAPES[kind]
+    pools = [torch.zeros((num_pages, PAGE_SIZE, Hkv, D), dtype=torch.uint8, device=device).view(FP8) for _ in range(2)]
+    scales = [torch.zeros((num_pages, Hkv, PAGE_SIZE), dtype=torch.uint8, device=device).view(E8M0) for _ in range(2)]
+    return tuple(pools + scales)
+
+
+def _fp8_ptrs(kind, k_pool, v_pool, k_scale, v_scale):
+    _, Hkv, D = SHAPES[kind]
+    _dims(k_pool, 4, "k_pool must be [num_pages, 16, %d, %d]" % (Hkv, D))
+    n = k_pool.shape[0]
+    return [_ptr(k_pool, "k_pool", FP8, (n, PAGE_SIZE, Hkv, D)), _ptr(v_pool, "v_pool", FP8, (n, PAGE_SIZE, Hkv, D)),
+            _ptr(k_scale, "k_scale", E8M0, (n, Hkv, PAGE_SIZE)), _ptr(v_scale, "v_scale", E8M0, (n, Hkv, PAGE_SIZE))], n
+
+
+def _append_common(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out):
+    """Pointers and sizes of the arguments that both cache types share; q_out made if None."""
+    Hq, _, D = SHAPES[kind]
+    _dims(qkv, 2, "qkv must be [total_q, %d]" % APPEND_ROW[kind])
+    _dims(block_table, 2, "block_table must be [batch, max_blocks]")
+    total_q, (batch, max_blocks) = qkv.shape[0], block_table.shape
+    ptrs = [_ptr(qkv, "qkv", torch.bfloat16, (total_q, APPEND_ROW[kind])), _ptr(w_q, "w_q", torch.bfloat16, (D,)),
+            _ptr(w_k, "w_k", torch.bfloat16, (D,)),
+            _ptr(block_table, "block_table", torch.int32, (batch, max_blocks)),
+            _ptr(seq_lens, "seq_lens", torch.int32, (batch,)), _ptr(cu_q, "cu_q", torch.int32, (batch + 1,))]
+    if q_out is None:
+        q_out = torch.empty((total_q, Hq, D), dtype=torch.bfloat16, device=qkv.device)
+    ptrs.append(_ptr(q_out, "q_out", torch.bfloat16, (total_q, Hq, D)))
+    return ptrs, q_out, batch, total_q, max_blocks
+
+
+def _kind_name(kind):
+    return "sliding" if kind == KIND_SLIDING else "global"
+
+
+def _chunk_args(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out=None, *, status=None):
+    """(fn_name, args without the stream, tensors to keep, output, device) of a chunk append."""
+    _, Hkv, D = SHAPES[kind]
+    ptrs, q_out, batch, total_q, max_blocks = _append_common(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out)
+    _dims(v_pool, 4, "v_pool must be [num_pages, 16, %d, %d]" % (Hkv, D))
+    n = v_pool.shape[0]
+    k_ptr = None if k_pool is None and kind == KIND_GLOBAL else \
+        _ptr(k_pool, "k_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D))
+    keep = (qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, status)
+    device = _one_device(keep)
+    args = tuple(ptrs) + (k_ptr, _ptr(v_pool, "v_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D)), batch, total_q,
+                          max_blocks, n, _status_ptr(status))
+    return "attn_kv_append_%s_chunk" % _kind_name(kind), args, keep, q_out, device
+
+
+def _append_fp8_args(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, k_scale, v_scale, q_out=None, *,
+                     status=None):
+    ptrs, q_out, batch, total_q, max_blocks = _append_common(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out)
+    cache, n = _fp8_ptrs(kind, k_pool, v_pool, k_scale, v_scale)
+    keep = (qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, k_scale, v_scale, status)
+    device = _one_device(keep)
+    args = tuple(ptrs + cache) + (batch, total_q, max_blocks, n, _status_ptr(status))
+    return "attn_kv_append_%s_fp8" % _kind_name(kind), args, keep, q_out, device
+
+
+def _read_fp8_args(kind, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table=None, *,
+                   span=0, max_seq_len=None, status=None):
+    _, Hkv, D = SHAPES[kind]
+    cache, n = _fp8_ptrs(kind, k_pool, v_pool, k_scale, v_scale)
+    _dims(block_table, 2, "block_table must be [batch, max_blocks]")
+    _dims(k_out, 4, "k_out must be [out_pages, 16, %d, %d]" % (Hkv, D))
+    batch, max_blocks = block_table.shape
+    out_pages = k_out.shape[0]
+    if out_table is None:
+        out_table = block_table
+    keep = (k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table, status)
+    device = _one_device(keep)
+    if max_seq_len is None:
+        max_seq_len = min(max_blocks * PAGE_SIZE, 262144)
+    args = tuple(cache) + (_ptr(block_table, "block_table", torch.int32, (batch, max_blocks)),
+                           _ptr(seq_lens, "seq_lens", torch.int32, (batch,)),
+                           _ptr(k_out, "k_out", torch.bfloat16, (out_pages, PAGE_SIZE, Hkv, D)),
+                           _ptr(v_out, "v_out", torch.bfloat16, (out_pages, PAGE_SIZE, Hkv, D)),
+                           _ptr(out_table, "out_table", torch.int32, (batch, max_blocks)), batch, max_blocks, n,
+                           out_pages, int(max_seq_len), int(span), _status_ptr(status))
+    return "attn_kv_read_%s_fp8" % _kind_name(kind), args, keep, (k_out, v_out), device
+
+
+def _decode_fp8_args(kind, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o=None, *, window=None,
+                     max_seq_len=None, out_dtype=torch.bfloat16, num_splits=0, workspace=None, status=None):
+    Hq, Hkv, D = SHAPES[kind]
+    _dims(q, 3, "q must be [batch, %d, %d]" % (Hq, D))
+    _dims(block_table, 2, "block_table must be [batch, max_blocks]")
+    batch, max_blocks = block_table.shape
+    cache, n = _fp8_ptrs(kind, k_pool, v_pool, k_scale, v_scale)
+    q_ptr = _ptr(q, "q", torch.bfloat16, (batch, Hq, D))
+    if o is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        o = torch.empty((batch, Hq, D), dtype=out_dtype, device=q.device)
+    elif not isinstance(o, torch.Tensor) or o.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("o must be a torch.bfloat16 or torch.float32 tensor")
+    if window is None:
+        window = 1024 if kind == KIND_SLIDING else 0
+    if max_seq_len is None:
+        max_seq_len = min(max_blocks * PAGE_SIZE, 262144)
+    device = _one_device((q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o, workspace, status))
+    tables = [_ptr(block_table, "block_table", torch.int32, (batch, max_blocks)),
+              _ptr(seq_lens, "seq_lens", torch.int32, (batch,)), _ptr(o, "o", o.dtype, (batch, Hq, D))]
+    if workspace is None:
+        with torch.cuda.device(device):
+            workspace = new_workspace(attn_decode_workspace_size(kind, batch, max_seq_len, window, num_splits), device)
+    keep = (q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o, workspace, status)
+    args = tuple([q_ptr] + cache + tables) + (
+        batch, max_blocks, n, int(max_seq_len), int(window), OUT_F32 if o.dtype == torch.float32 else OUT_BF16,
+        int(num_splits), _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _status_ptr(status))
+    return "attn_decode_%s_fp8" % _kind_name(kind), args, keep, o, device
+
+
+def _once(stream, prepared):
+    return PreparedCall(*prepared).run(stream)
+
+
+def attn_kv_append_sliding_chunk(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out=None, *,
+                                 status=None, stream=None):
+    """Norms, RoPE and cache append of a chunk of new tokens per sequence (sliding layers).
+
+    qkv [T, 8192] bf16, rows as attn_kv_append_sliding; sequence b's new tokens
+    are rows cu_q[b] .. cu_q[b+1]-1 (int32 [B+1]) and the last of its
+    seq_lens[b] cached ones (int32 [B], new tokens included).  Returns q_out
+    [T,16,256], which with seq_lens and cu_q is what attn_prefill_sliding takes.
+    """
+    return _once(stream, _chunk_args(KIND_SLIDING, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out,
+                                     status=status))
+
+
+def attn_kv_append_global_chunk(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out=None, *,
+                                status=None, stream=None):
+    """attn_kv_append_sliding_chunk for global layers: qkv [T, 8704]; k_pool may be None (values-only cache)."""
+    return _once(stream, _chunk_args(KIND_GLOBAL, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out,
+                                     status=status))
+
+
+def attn_kv_append_sliding_fp8(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, k_scale, v_scale,
+                               q_out=None, *, status=None, stream=None):
+    """attn_kv_append_sliding_chunk into an 8-bit cache: pools [P,16,8,256] float8_e4m3fn, scales [P,8,16]
+    float8_e8m0fnu (new_fp8_cache).  A decode step is cu_q = arange(B + 1)."""
+    return _once(stream, _append_fp8_args(KIND_SLIDING, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool,
+                                          k_scale, v_scale, q_out, status=status))
+
+
+def attn_kv_append_global_fp8(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, k_scale, v_scale,
+                              q_out=None, *, status=None, stream=None):
+    """attn_kv_append_global_chunk into an 8-bit cache: pools [P,16,1,512] float8_e4m3fn, scales [P,1,16]
+    float8_e8m0fnu; keys and values are both kept."""
+    return _once(stream, _append_fp8_args(KIND_GLOBAL, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool,
+                                          k_scale, v_scale, q_out, status=status))
+
+
+def attn_kv_read_sliding_fp8(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table=None, *,
+                             span=0, max_seq_len=None, status=None, stream=None):
+    """The last min(L, span) positions of every sequence (span <= 0: all) of an 8-bit cache into the bf16 pools k_out
+    and v_out [out_pages,16,8,256], page by page as out_table (default block_table) says; returns (k_out, v_out)."""
+    return _once(stream, _read_fp8_args(KIND_SLIDING, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out,
+                                        v_out, out_table, span=span, max_seq_len=max_seq_len, status=status))
+
+
+def attn_kv_read_global_fp8(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table=None, *,
+                            span=0, max_seq_len=None, status=None, stream=None):
+    """attn_kv_read_sliding_fp8 for global layers (pools [P,16,1,512])."""
+    return _once(stream, _read_fp8_args(KIND_GLOBAL, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out,
+                                        v_out, out_table, span=span, max_seq_len=max_seq_len, status=status))
+
+
+def attn_decode_sliding_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o=None, *, window=1024,
+                            max_seq_len=None, out_dtype=torch.bfloat16, num_splits=0, workspace=None, status=None,
+                            stream=None):
+    """attn_decode_sliding over an 8-bit cache: q [B,16,256] bf16, pools [P,16,8,256] float8_e4m3fn, scales [P,8,16]
+    float8_e8m0fnu -> o [B,16,256].  Plan and workspace are attn_decode_sliding's."""
+    return _once(stream, _decode_fp8_args(KIND_SLIDING, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o,
+                                          window=window, max_seq_len=max_seq_len, out_dtype=out_dtype,
+                                          num_splits=num_splits, workspace=workspace, status=status))
+
+
+def attn_decode_global_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o=None, *, window=0,
+                           max_seq_len=None, out_dtype=torch.bfloat16, num_splits=0, workspace=None, status=None,
+                           stream=None):
+    """attn_decode_global over an 8-bit cache: q [B,16,512] bf16, pools [P,16,1,512] float8_e4m3fn, scales [P,1,16]
+    float8_e8m0fnu -> o [B,16,512].  Plan and workspace are attn_decode_global's."""
+    return _once(stream, _decode_fp8_args(KIND_GLOBAL, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o,
+                                          window=window, max_seq_len=max_seq_len, out_dtype=out_dtype,
+                                          num_splits=num_splits, workspace=workspace, status=status))
+
+
+def prepare_kv_append_sliding_chunk(*args, **kw):
+    """PreparedCall for attn_kv_append_sliding_chunk (same arguments, minus the stream)."""
+    return PreparedCall(*_chunk_args(KIND_SLIDING, *args, **kw))
+
+
+def prepare_kv_append_global_chunk(*args, **kw):
+    """PreparedCall for attn_kv_append_global_chunk (same arguments, minus the stream)."""
+    return PreparedCall(*_chunk_args(KIND_GLOBAL, *args, **kw))
+
+
+def prepare_kv_append_sliding_fp8(*args, **kw):
+    """PreparedCall for attn_kv_append_sliding_fp8 (same arguments, minus the stream)."""
+    return PreparedCall(*_append_fp8_args(KIND_SLIDING, *args, **kw))
+
+
+def prepare_kv_append_global_fp8(*args, **kw):
+    """PreparedCall for attn_kv_append_global_fp8 (same arguments, minus the stream)."""
+    return PreparedCall(*_append_fp8_args(KIND_GLOBAL, *args, **kw))
+
+
+def prepare_kv_read_sliding_fp8(*args, **kw):
+    """PreparedCall for attn_kv_read_sliding_fp8 (same arguments, minus the stream)."""
+    return PreparedCall(*_read_fp8_args(KIND_SLIDING, *args, **kw))
+
+
+def prepare_kv_read_global_fp8(*args, **kw):
+    """PreparedCall for attn_kv_read_global_fp8 (same arguments, minus the stream)."""
+    return PreparedCall(*_read_fp8_args(KIND_GLOBAL, *args, **kw))
+
+
+def prepare_decode_sliding_fp8(*args, **kw):
+    """PreparedCall for attn_decode_sliding_fp8 (same arguments, minus the stream)."""
+    return PreparedCall(*_decode_fp8_args(KIND_SLIDING, *args, **kw))
+
+
+def prepare_decode_global_fp8(*args, **kw):
+    """PreparedCall for attn_decode_global_fp8 (same arguments, minus the stream)."""
+    return PreparedCall(*_decode_fp8_args(KIND_GLOBAL, *args, **kw))

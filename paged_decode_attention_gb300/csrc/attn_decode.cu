@@ -863,4 +863,5 @@ extern "C" int32_t attn_decode_sliding_noalloc(const void* q, const void* k_pool
                     status, stream);
 }
 
+#include "serving.cuh"
 #include "step.cuh"

@@ -1,0 +1,401 @@
+// global_fp8.cuh -- decodeGQA over an 8-bit cache (fp8.cuh): 16 query heads
+// over 1 KV head, D = 512, scale 1.  The formulas are sliding_fp8.cuh's.
+//
+// A page is 16 KB here (K and V) against 32 KB in bf16, so at the rate of
+// memory the bf16 kernel's work per page, four copies of the softmax and an
+// exchange of partial logits for every page, would take twice the share of
+// the time.  Instead the four consumer warps take a group of up to four
+// consecutive pages of a segment together:
+//   * warp w computes the logits of page w alone, over all 512 dims (64
+//     MMAs, q as A fragments from shared memory), scales and masks them;
+//   * the row maxima of the four pages meet in shared memory (barrier);
+//   * warp w turns its page's logits into weights and leaves them in shared
+//     memory as the A fragment of the second product (barrier);
+//   * every warp multiplies all pages' weights with its own 128 of the 512
+//     output dims, so that no output is ever merged between warps.
+// So each byte is widened once, the softmax runs once per page, and two
+// barriers serve four pages.
+//
+// Tiles: 128 dims of a page are [16 rows][128 bytes] with the 128-byte
+// swizzle; the fragment order is sliding_fp8.cuh's with the cache as the B
+// operand: K: lane (g, tq) reads rows g and g + 8 at unit 2 tq + j; V: the
+// n-tiles of a 16-dim block are its even and its odd dims.
+#pragma once
+
+#include "fp8.cuh"
+#include "global.cuh"
+
+namespace pda {
+namespace global_fp8 {
+
+using global::kD;
+using global::kHq;
+
+constexpr int kConsumerWarps = 4;
+constexpr int kThreads = (kConsumerWarps + 1) * 32;
+constexpr int kChunks = kD / 128;                     // 4: one per consumer warp in the second product
+constexpr int kPageBytes = kPage * kD;                // 8 KB
+constexpr int kStages = 5;
+constexpr int kStageTx = 2 * kPageBytes + 2 * kPage;  // K, V and their scales
+constexpr int kBlocksPerSm = global::kBlocksPerSm;    // the plan of the bf16 kernel
+constexpr int kWarmPages = 4;
+constexpr int kKSteps = kD / 16;                      // 32
+
+static_assert(kChunks == kConsumerWarps, "128 output dims per warp");
+static_assert(kStages > kConsumerWarps, "a group of pages and the next one's first");
+
+struct Smem {
+  alignas(1024) uint8_t k[kStages][kPageBytes];  // kChunks tiles of [16 rows][128 dims], swizzled
+  alignas(1024) uint8_t v[kStages][kPageBytes];
+  alignas(128) uint8_t k_scale[kStages][128];  // 16 bytes used: a copy lands on a 128-byte boundary
+  alignas(128) uint8_t v_scale[kStages][128];
+  alignas(16) uint4 qfrag[kKSteps][32];          // q A fragments
+  alignas(16) uint4 pfrag[kConsumerWarps][32];   // weights of the group's pages, as A fragments
+  float2 row_max[kConsumerWarps][kHq];           // the pages' row maxima of x and of x + kv (fp8.cuh)
+  uint32_t q_max[kConsumerWarps][kHq];
+  float row_sum[kConsumerWarps][kHq];
+  SeqTable table;
+  alignas(8) uint64_t full[kStages];
+  alignas(8) uint64_t empty[kStages];
+};
+
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + alignment slack
+static_assert(kBlocksPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of the resident blocks");
+
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
+                  const __grid_constant__ DecodeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+
+  const int gb = blockIdx.x;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(&s.full[st], 1);
+      mbar_init(&s.empty[st], kConsumerWarps);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kConsumerWarps && lane == 0) {
+    prefetch_tensor_map(&tm_k);
+    prefetch_tensor_map(&tm_v);
+    prefetch_tensor_map(&tm_ks);
+    prefetch_tensor_map(&tm_vs);
+  }
+  // The prologue overlaps the previous kernel; see global.cuh.
+  build_seq_table_hint(p, s.table, gb);  // ends with __syncthreads
+  if (warp == kConsumerWarps) {
+    warm_first_pages(p, s.table, kWarmPages, [&](int32_t y) {
+      // (pools of bytes, so the typed pointers of the parameters are cast)
+      bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(p.k_pool) + static_cast<size_t>(y) * kD, kPageBytes);
+      bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(p.v_pool) + static_cast<size_t>(y) * kD, kPageBytes);
+    });
+  } else {
+    warm_q(p, s.table, kHq * kD, 0, kHq * kD * 2, kConsumerWarps * 32);
+  }
+  wait_for_primary_grid();
+  allow_dependent_launch();
+  int first = warp == kConsumerWarps ? page_entry(p, s.table, s.table.span, lane, false) : 0;
+  confirm_seq_table(p, s.table, gb);  // ends with __syncthreads
+  const SeqTable& t = s.table;
+  const Span sp = t.span;
+  const int n_pages = sp.end - sp.begin;
+  if (n_pages <= 0) return;
+
+  if (warp == kConsumerWarps) {
+    // ---------------- producer ----------------
+    const uint64_t policy = l2_policy_evict_first();
+    if (t.rebuilt) first = page_entry(p, t, sp, lane, true);
+    produce_pages<kStages, kStageTx>(p, t, sp, s.full, s.empty, first, [&](int stage, int32_t y) {
+      tma_load_3d_hint(s.k[stage], &tm_k, 0, y, 0, &s.full[stage], policy);
+      tma_load_3d_hint(s.v[stage], &tm_v, 0, y, 0, &s.full[stage], policy);
+      const int32_t ys = y < 0 ? -1 : y / kPage;  // 16 bytes per page in the scale pools
+      tma_load_2d(s.k_scale[stage], &tm_ks, 0, ys, &s.full[stage]);
+      tma_load_2d(s.v_scale[stage], &tm_vs, 0, ys, &s.full[stage]);
+    });
+    return;
+  }
+
+  // ---------------- consumers ----------------
+  const int g = lane >> 2;  // fragment row: query heads g and g + 8
+  const int tq = lane & 3;
+  const int mi = lane >> 3;  // ldmatrix: which 8x8 matrix this lane addresses
+  const int lr = lane & 7;
+  constexpr int kConsumers = kConsumerWarps * 32;
+
+  PageCursor cur;
+  cur.start(p, t, sp);
+
+  // q of the sequence into shared memory as A fragments: warp w prepares the
+  // k-steps of chunk w (8 steps (j, word): dims 128 w + 16 (2 tq + j) + 4 word
+  // .. + 3 of rows g and g + 8), scaled by each row's power of two.
+  float qs[2];  // logit factor 2^k log2(e) of rows g and g + 8
+  auto load_q = [&]() {
+    uint32_t w[2][2][8];  // row, j, words
+    uint32_t amax[2] = {0, 0};
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const __nv_bfloat16* src = p.q + (static_cast<size_t>(cur.b) * kHq + g + 8 * r) * kD + 128 * warp +
+                                   16 * (2 * tq + j);
+        const uint4 a = ld_global_nc_v4(src), b = ld_global_nc_v4(src + 8);
+        w[r][j][0] = a.x; w[r][j][1] = a.y; w[r][j][2] = a.z; w[r][j][3] = a.w;
+        w[r][j][4] = b.x; w[r][j][5] = b.y; w[r][j][6] = b.z; w[r][j][7] = b.w;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          amax[r] = max(amax[r], max(w[r][j][k] << 16 & 0x7fff0000u, w[r][j][k] & 0x7fff0000u));
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      amax[r] = max(amax[r], __shfl_xor_sync(0xffffffffu, amax[r], 1));
+      amax[r] = max(amax[r], __shfl_xor_sync(0xffffffffu, amax[r], 2));
+      if (tq == 0) s.q_max[warp][g + 8 * r] = amax[r];
+    }
+    named_barrier_sync(1, kConsumers);  // the other warps' maxima; and every warp is done with the old fragments
+    float inv[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int k = 0; k < kConsumerWarps; ++k) a = max(a, s.q_max[k][g + 8 * r]);
+      const int e = fp8::q_exponent(a, inv[r]);
+      qs[r] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * kLog2e;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        s.qfrag[8 * warp + 4 * j + k][lane] =
+            make_uint4(fp8::q_f16x2(w[0][j][2 * k], inv[0]), fp8::q_f16x2(w[1][j][2 * k], inv[1]),
+                       fp8::q_f16x2(w[0][j][2 * k + 1], inv[0]), fp8::q_f16x2(w[1][j][2 * k + 1], inv[1]));
+    named_barrier_sync(1, kConsumers);
+  };
+  auto prefetch_next_q = [&]() {
+    const int nb = next_seq_in_span(p, t, sp, cur.b);
+    if (nb >= 0)
+      prefetch_l2(reinterpret_cast<const uint8_t*>(p.q + static_cast<size_t>(nb) * kHq * kD) + threadIdx.x * 128);
+  };
+  load_q();
+  prefetch_next_q();
+
+  fp8::Reference ref[2];  // rows g, g + 8 (the same in every warp)
+  float l[2];             // this lane's share of the sums
+  float acc[16][4];  // per 16-dim block: even dims (n-tile 2n), odd dims (2n + 1)
+  auto reset = [&]() {
+    ref[0].reset();
+    ref[1].reset();
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+  };
+  reset();
+  bool ok = true;
+  auto wait_page = [&](int i) {
+    if (ok) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&s.full[i % kStages], (i / kStages) & 1));
+      if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+    }
+  };
+
+  for (int i = 0; i < n_pages;) {
+    const int f = sp.begin + i;
+    if (f >= t.prefix[cur.b + 1]) {
+      cur.advance(p, t, sp, f);
+      load_q();
+      prefetch_next_q();
+    }
+    const int n = min(kConsumerWarps, cur.seg_end - f);  // pages of this group
+    const int gpos0 = cur.pos0(t, f);                    // position of its first row
+
+    // ---- logits of page w: x[nt][e]: head g + 8 (e >> 1), position pos0 + 8 nt + 2 tq + (e & 1) ----
+    float x[2][4];
+    float kv[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // log2 of those positions' value scales
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[nt][e] = -INFINITY;
+    if (warp < n) {
+      wait_page(i + warp);
+      const int st = (i + warp) % kStages;
+      const int pos0 = gpos0 + warp * kPage;
+      const uint32_t kst = smem_addr(s.k[st]);
+      float sc[2][2][4];  // n-tile, even / odd k-steps
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[a][b][e] = 0.f;
+#pragma unroll 2
+      for (int k = 0; k < kChunks * 2; ++k) {  // chunk, j
+        const uint32_t base = kst + (k >> 1) * fp8::kChunkBytes;
+        const uint4 a = ld_shared_v4(base + fp8::swz(g, 2 * tq + (k & 1)));
+        const uint4 b = ld_shared_v4(base + fp8::swz(g + 8, 2 * tq + (k & 1)));
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint4 q = s.qfrag[4 * k + w][lane];
+          fp8::mma_f16_16816(sc[0][w & 1], q.x, q.y, q.z, q.w, fp8::lo_f16x2(aw[w]), fp8::hi_f16x2(aw[w]));
+          fp8::mma_f16_16816(sc[1][w & 1], q.x, q.y, q.z, q.w, fp8::lo_f16x2(bw[w]), fp8::hi_f16x2(bw[w]));
+        }
+      }
+      const bool edge = pos0 < cur.lo || pos0 + kPage > cur.L;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = 8 * nt + 2 * tq + u;
+          const float kf = fp8::scale_value(s.k_scale[st][r]);
+          const bool in = !edge || (pos0 + r >= cur.lo && pos0 + r < cur.L);
+          if (in) {
+            kv[nt][u] = fp8::scale_log2(s.v_scale[st][r]);
+            x[nt][u] = (sc[nt][0][u] + sc[nt][1][u]) * kf * qs[0];
+            x[nt][2 + u] = (sc[nt][0][2 + u] + sc[nt][1][2 + u]) * kf * qs[1];
+          }
+        }
+    }
+    // ---- the group's row maxima ----
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float mx = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+      float mt = fmaxf(fmaxf(x[0][2 * r] + kv[0][0], x[0][2 * r + 1] + kv[0][1]),
+                       fmaxf(x[1][2 * r] + kv[1][0], x[1][2 * r + 1] + kv[1][1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+      if (tq == 0) s.row_max[warp][g + 8 * r] = make_float2(mx, mt);
+    }
+    named_barrier_sync(1, kConsumers);
+    float scale[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float2 mx = s.row_max[0][g + 8 * r];
+#pragma unroll
+      for (int w = 1; w < kConsumerWarps; ++w) {
+        const float2 o = s.row_max[w][g + 8 * r];
+        mx = make_float2(fmaxf(mx.x, o.x), fmaxf(mx.y, o.y));
+      }
+      float ls;
+      ref[r].move(mx.x, mx.y, ls, scale[r]);
+      l[r] *= ls;
+    }
+    // ---- page w's weights ----
+    if (warp < n) {
+      float pr[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const fp8::Reference& r = ref[e >> 1];
+          const float d = x[nt][e] - r.m_use();
+          l[e >> 1] += ex2_approx(d);
+          pr[nt][e] = ex2_approx(d + (r.weight_bias() + kv[nt][e & 1]));
+        }
+      s.pfrag[warp][lane] = make_uint4(fp8::pack_f16x2(pr[0][0], pr[0][1]), fp8::pack_f16x2(pr[0][2], pr[0][3]),
+                                       fp8::pack_f16x2(pr[1][0], pr[1][1]), fp8::pack_f16x2(pr[1][2], pr[1][3]));
+    }
+    named_barrier_sync(1, kConsumers);
+
+    // ---- O += P V over this warp's 128 dims ----
+    if (__any_sync(0xffffffffu, scale[0] != 1.f || scale[1] != 1.f)) {
+#pragma unroll
+      for (int b = 0; b < 16; ++b) {
+        acc[b][0] *= scale[0];
+        acc[b][1] *= scale[0];
+        acc[b][2] *= scale[1];
+        acc[b][3] *= scale[1];
+      }
+    }
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      wait_page(i + j);
+      const int st = (i + j) % kStages;
+      const int pos0 = gpos0 + j * kPage;
+      const uint32_t vst = smem_addr(s.v[st]) + warp * fp8::kChunkBytes;
+      if (pos0 < cur.lo || pos0 + kPage > cur.L) {
+        // zero this warp's V rows outside [lo, L): weight 0 times NaN would be NaN
+#pragma unroll 1
+        for (int rr = 0; rr < kPage; ++rr) {
+          const int pos = pos0 + rr;
+          if ((pos < cur.lo || pos >= cur.L) && lane < 8)
+            st_shared_v4(vst + rr * 128 + lane * 16, make_uint4(0, 0, 0, 0));
+        }
+        fence_proxy_async_smem();  // before TMA rewrites this stage
+        __syncwarp();
+      }
+      const uint4 pa = s.pfrag[j][lane];
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {  // 32 dims each
+        uint32_t r[4];
+        ldmatrix_x4_trans(vst + fp8::swz(((mi & 1) << 3) + lr, 2 * np + (mi >> 1)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t e0, o0, e1, o1;
+          fp8::split_pair(r[2 * u], e0, o0);
+          fp8::split_pair(r[2 * u + 1], e1, o1);
+          fp8::mma_f16_16816(acc[4 * np + 2 * u], pa.x, pa.y, pa.z, pa.w, e0, e1);
+          fp8::mma_f16_16816(acc[4 * np + 2 * u + 1], pa.x, pa.y, pa.z, pa.w, o0, o1);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.empty[st]);
+    }
+    i += n;
+
+    if (f + n == cur.seg_end) {
+      // ---------------- finish this sequence's segment ----------------
+      float lt[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        lt[r] = l[r] + __shfl_xor_sync(0xffffffffu, l[r], 1);
+        lt[r] += __shfl_xor_sync(0xffffffffu, lt[r], 2);
+        if (tq == 0) s.row_sum[warp][g + 8 * r] = lt[r];
+      }
+      named_barrier_sync(1, kConsumers);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        lt[r] = s.row_sum[0][g + 8 * r];
+#pragma unroll
+        for (int w = 1; w < kConsumerWarps; ++w) lt[r] += s.row_sum[w][g + 8 * r];
+      }
+      const bool whole = cur.whole(t, sp);
+      if (!whole && (static_cast<int64_t>(gb) + cur.b + 1) * kHq > p.part_rows) {
+        if (lane == 0) report(p.status, ATTN_DEV_INTERNAL);  // cannot happen: slot beyond the workspace
+      } else {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const size_t row = static_cast<size_t>(whole ? cur.b : gb + cur.b) * kHq + g + 8 * r;
+          const float inv = lt[r] > 0.f ? 1.f / lt[r] : lt[r];  // 0, or a NaN that has to show
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            const float4 v = make_float4(fp8::unscale(acc[2 * b][2 * r], ref[r].R),
+                                         fp8::unscale(acc[2 * b + 1][2 * r], ref[r].R),
+                                         fp8::unscale(acc[2 * b][2 * r + 1], ref[r].R),
+                                         fp8::unscale(acc[2 * b + 1][2 * r + 1], ref[r].R));
+            const size_t at = row * kD + 128 * warp + 16 * b + 4 * tq;
+            if (whole)
+              store_out4(p, at, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+            else
+              *reinterpret_cast<float4*>(p.part_o + at) = v;
+          }
+          // a NaN sum is handed on as (inf, 1): the combine skips partials whose sum is not positive
+          if (!whole && warp == 0 && tq == 0)
+            p.part_ml[row] = lt[r] == lt[r] ? make_float2(ref[r].m, lt[r]) : make_float2(INFINITY, 1.f);
+        }
+      }
+      named_barrier_sync(1, kConsumers);  // row_sum read
+      reset();
+    }
+  }
+}
+
+}  // namespace global_fp8
+}  // namespace pda

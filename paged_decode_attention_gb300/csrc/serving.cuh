@@ -1,0 +1,382 @@
+// serving.cuh -- host side of the chunk appends, the 8-bit cache
+// (include/attn_fp8.h) and their launches.  Included in attn_decode.cu, whose
+// validation helpers, plan, tensor-map encoder and launch recording it shares.
+#pragma once
+
+#include "attn_fp8.h"
+#include "fp8_read.cuh"
+#include "global_fp8.cuh"
+#include "kv_chunk.cuh"
+#include "sliding_fp8.cuh"
+
+namespace {
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// num_pages of a pool whose row coordinate (16 rows per page) is an int32
+int32_t check_pages(const char* name, const char* what, int64_t num_pages) {
+  if (num_pages < 1 || num_pages > (int64_t{1} << 31) / ATTN_PAGE_SIZE - 1)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: %s %lld out of range", name, what, static_cast<long long>(num_pages));
+  return ATTN_OK;
+}
+
+int32_t check_batch(const char* name, int32_t batch, int32_t max_blocks) {
+  if (batch < 1) return fail(ATTN_ERR_INVALID_ARG, "%s: batch must be >= 1 (got %d)", name, batch);
+  if (batch > ATTN_MAX_BATCH)
+    return fail(ATTN_ERR_UNSUPPORTED, "%s: batch %d outside [1, %d]", name, batch, ATTN_MAX_BATCH);
+  if (max_blocks < 1) return fail(ATTN_ERR_INVALID_ARG, "%s: max_blocks must be >= 1", name);
+  return ATTN_OK;
+}
+
+int32_t check_max_seq_len(const char* name, int32_t max_seq_len, int32_t max_blocks) {
+  if (max_seq_len < 0 || static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_blocks) * ATTN_PAGE_SIZE)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: max_seq_len %d not in [0, max_blocks*16 = %lld]", name, max_seq_len,
+                static_cast<long long>(max_blocks) * ATTN_PAGE_SIZE);
+  if (max_seq_len > ATTN_MAX_SEQ_LEN)
+    return fail(ATTN_ERR_UNSUPPORTED, "%s: max_seq_len %d beyond the model's domain (%d)", name, max_seq_len,
+                ATTN_MAX_SEQ_LEN);
+  return ATTN_OK;
+}
+
+int32_t launched(const char* name, cudaError_t e) {
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "%s: launch failed: %s", name, cudaGetErrorString(e));
+  return ATTN_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Norms, RoPE and cache append of a chunk of tokens per sequence
+// ---------------------------------------------------------------------------
+int32_t run_chunk(int32_t kind, bool fp8, const void* qkv, const void* w_q, const void* w_k,
+                  const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
+                  void* v_pool, uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q, int32_t max_blocks,
+                  int64_t num_pages, int32_t* status, void* stream) {
+  g_err[0] = '\0';
+  const bool sliding = kind == ATTN_KIND_SLIDING;
+  const char* name = fp8 ? (sliding ? "attn_kv_append_sliding_fp8" : "attn_kv_append_global_fp8")
+                         : (sliding ? "attn_kv_append_sliding_chunk" : "attn_kv_append_global_chunk");
+  const bool values_only = !sliding && !fp8;  // may leave the keys out
+  if (!w_q || !w_k || !block_table || !seq_lens || !cu_q || (total_q > 0 && (!qkv || !q_out)) ||
+      (!k_pool && !values_only) || !v_pool || (fp8 && (!k_scale || !v_scale)))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (!aligned_to(qkv, 16) || !aligned_to(w_q, 16) || !aligned_to(w_k, 16) || !aligned_to(q_out, 16) ||
+      !aligned_to(k_pool, 16) || !aligned_to(v_pool, 16) || !aligned_to(k_scale, 16) || !aligned_to(v_scale, 16) ||
+      !aligned_to(block_table, 4) || !aligned_to(seq_lens, 4) || !aligned_to(cu_q, 4) || !aligned_to(status, 4))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: misaligned pointer (qkv, w_q, w_k, q_out, pools and scales 16 bytes, "
+                "tables 4)", name);
+  int32_t st;
+  if ((st = check_batch(name, batch, max_blocks)) || (st = check_pages(name, "num_pages", num_pages))) return st;
+  if (total_q < 0) return fail(ATTN_ERR_INVALID_ARG, "%s: total_q must be >= 0", name);
+  g_last_launches = total_q > 0 ? 1 : 0;
+  if (total_q == 0) return ATTN_OK;  // no tokens
+  int dev = 0, num_sms = 0;
+  if ((st = current_device(&dev, &num_sms)) != ATTN_OK) return st;
+  if (g_validate_only) return ATTN_OK;
+
+  const int D = sliding ? ATTN_SLIDING_D : ATTN_GLOBAL_D;
+  const double theta = sliding ? ATTN_SLIDING_ROPE_THETA : ATTN_GLOBAL_ROPE_THETA;
+  pda::chunk::ChunkParams p{};
+  p.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  p.w_q = static_cast<const __nv_bfloat16*>(w_q);
+  p.w_k = static_cast<const __nv_bfloat16*>(w_k);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.status = status;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.total_q = total_q;
+  p.max_blocks = max_blocks;
+  p.eps = 1e-6f;
+  p.two_pi = split_two_pi();
+  for (int k = 0; k < pda::chunk::kPairBits; ++k)
+    p.bit_factor[k] = split_float_pair(std::pow(theta, -2.0 * (1 << k) / D));
+
+  const int blocks = std::min(total_q, num_sms * pda::chunk::kBlocksPerSm);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const auto launch = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(blocks), pda::chunk::kThreads, 0, s, p);
+  };
+  namespace ch = pda::chunk;
+  cudaError_t e;
+  if (sliding)
+    e = fp8 ? launch(ch::chunk_kernel<ATTN_SLIDING_D, ATTN_SLIDING_HQ, ATTN_SLIDING_HKV, ATTN_SLIDING_ROPE_PAIRS,
+                                      false, true>)
+            : launch(ch::chunk_kernel<ATTN_SLIDING_D, ATTN_SLIDING_HQ, ATTN_SLIDING_HKV, ATTN_SLIDING_ROPE_PAIRS,
+                                      false, false>);
+  else
+    e = fp8 ? launch(ch::chunk_kernel<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ, ATTN_GLOBAL_HKV, ATTN_GLOBAL_ROPE_PAIRS, true,
+                                      true>)
+            : launch(ch::chunk_kernel<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ, ATTN_GLOBAL_HKV, ATTN_GLOBAL_ROPE_PAIRS, true,
+                                      false>);
+  return launched(name, e);
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit cache: read back into bf16 pages
+// ---------------------------------------------------------------------------
+int32_t run_read(int32_t kind, const void* k_pool, const void* v_pool, const uint8_t* k_scale, const uint8_t* v_scale,
+                 const int32_t* block_table, const int32_t* seq_lens, void* k_out, void* v_out,
+                 const int32_t* out_table, int32_t batch, int32_t max_blocks, int64_t num_pages, int64_t out_pages,
+                 int32_t max_seq_len, int32_t span, int32_t* status, void* stream) {
+  g_err[0] = '\0';
+  const bool sliding = kind == ATTN_KIND_SLIDING;
+  const char* name = sliding ? "attn_kv_read_sliding_fp8" : "attn_kv_read_global_fp8";
+  if (!k_pool || !v_pool || !k_scale || !v_scale || !block_table || !seq_lens || !k_out || !v_out || !out_table)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (!aligned_to(k_pool, 16) || !aligned_to(v_pool, 16) || !aligned_to(k_scale, 16) || !aligned_to(v_scale, 16) ||
+      !aligned_to(k_out, 16) || !aligned_to(v_out, 16) || !aligned_to(block_table, 4) || !aligned_to(seq_lens, 4) ||
+      !aligned_to(out_table, 4) || !aligned_to(status, 4))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: misaligned pointer (pools and scales 16 bytes, tables 4)", name);
+  int32_t st;
+  if ((st = check_batch(name, batch, max_blocks)) || (st = check_pages(name, "num_pages", num_pages)) ||
+      (st = check_pages(name, "out_pages", out_pages)) || (st = check_max_seq_len(name, max_seq_len, max_blocks)))
+    return st;
+  int dev = 0, num_sms = 0;
+  if ((st = current_device(&dev, &num_sms)) != ATTN_OK) return st;
+  g_last_launches = 1;
+  if (g_validate_only) return ATTN_OK;
+
+  pda::fp8_read::ReadParams p{};
+  p.d.block_table = block_table;
+  p.d.seq_lens = seq_lens;
+  p.d.status = status;
+  p.d.num_pages = num_pages;
+  p.d.batch = batch;
+  p.d.max_blocks = max_blocks;
+  p.d.window = span;
+  p.d.min_pages = 1;
+  p.src[0] = static_cast<const uint8_t*>(k_pool);
+  p.src[1] = static_cast<const uint8_t*>(v_pool);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.dst[0] = static_cast<__nv_bfloat16*>(k_out);
+  p.dst[1] = static_cast<__nv_bfloat16*>(v_out);
+  p.out_table = out_table;
+  p.out_pages = out_pages;
+  // one wave of blocks, half for the keys and half for the values; no more
+  // than the (weighted) pages that max_seq_len allows
+  int64_t pages = (max_seq_len + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE;
+  if (span > 0) pages = std::min<int64_t>(pages, (static_cast<int64_t>(span) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE + 1);
+  const int64_t want = (pages + pda::kSeqWeight) * batch;
+  p.d.grid_x = static_cast<int32_t>(
+      std::max<int64_t>(1, std::min<int64_t>(want, num_sms * pda::fp8_read::kBlocksPerSm / 2)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid(p.d.grid_x, 2);
+  const cudaError_t e =
+      sliding ? launch_pdl(pda::fp8_read::read_kernel<ATTN_SLIDING_HKV, ATTN_SLIDING_D>, grid, pda::fp8_read::kThreads, 0,
+                           s, p)
+              : launch_pdl(pda::fp8_read::read_kernel<ATTN_GLOBAL_HKV, ATTN_GLOBAL_D>, grid, pda::fp8_read::kThreads, 0,
+                           s, p);
+  return launched(name, e);
+}
+
+// ---------------------------------------------------------------------------
+// Decode over an 8-bit cache
+// ---------------------------------------------------------------------------
+
+// An e4m3 pool [num_pages*16 rows][row_bytes] as a 3-D tensor (x: 128 dims
+// of a chunk, y: row, z: chunk): a box {128, 16, chunks} copies one KV head of
+// a page as 128-byte-swizzled [16 rows][128 dims] tiles.
+int32_t encode_fp8_map(CUtensorMap* map, const void* pool, int64_t num_pages, int row_bytes, int chunks) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(num_pages) * ATTN_PAGE_SIZE,
+                              static_cast<cuuint64_t>(row_bytes / 128)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), 128};
+  const cuuint32_t box[3] = {128, ATTN_PAGE_SIZE, static_cast<cuuint32_t>(chunks)};
+  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box, elem_strides,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled (e4m3 map) failed (%d)", static_cast<int>(r));
+  return ATTN_OK;
+}
+
+// A scale pool as rows of 16 bytes, one per (page, KV head).
+int32_t encode_scale_map(CUtensorMap* map, const void* scales, int64_t rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[2] = {ATTN_PAGE_SIZE, static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {ATTN_PAGE_SIZE};
+  const cuuint32_t box[2] = {ATTN_PAGE_SIZE, 1};
+  const cuuint32_t elem_strides[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(scales), dims, strides, box, elem_strides,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled (scale map) failed (%d)", static_cast<int>(r));
+  return ATTN_OK;
+}
+
+int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const void* v_pool, const uint8_t* k_scale,
+                       const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* o,
+                       int32_t batch, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len, int32_t window,
+                       int32_t out_dtype, int32_t num_splits, void* workspace, size_t workspace_bytes, int32_t* status,
+                       void* stream) {
+  g_err[0] = '\0';
+  const bool sliding = kind == ATTN_KIND_SLIDING;
+  const char* name = sliding ? "attn_decode_sliding_fp8" : "attn_decode_global_fp8";
+  if (!q || !k_pool || !v_pool || !k_scale || !v_scale || !block_table || !seq_lens || !o)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: null array pointer", name);
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_scale) || !aligned16(v_scale) ||
+      !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(o))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: every array must be 16-byte aligned", name);
+  if (!aligned_to(status, 4)) return fail(ATTN_ERR_INVALID_ARG, "%s: status must be 4-byte aligned", name);
+  int32_t st;
+  if ((st = check_batch(name, batch, max_blocks)) || (st = check_pages(name, "num_pages", num_pages)) ||
+      (st = check_max_seq_len(name, max_seq_len, max_blocks)))
+    return st;
+  if (sliding && window <= 0)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: window must be > 0 (the node's is 1024)", name);
+  if (out_dtype != ATTN_OUT_BF16 && out_dtype != ATTN_OUT_F32)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: out_dtype must be ATTN_OUT_BF16 or ATTN_OUT_F32", name);
+  if (num_splits < 0) return fail(ATTN_ERR_INVALID_ARG, "%s: num_splits must be >= 0", name);
+
+  int dev = 0, num_sms = 0;
+  if ((st = current_device(&dev, &num_sms)) != ATTN_OK) return st;
+  Plan plan;
+  st = make_plan(kind, batch, max_seq_len, window, num_splits, num_sms, &plan);
+  if (st != ATTN_OK) return st;
+  if (!workspace || workspace_bytes < plan.workspace_bytes)
+    return fail(ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)", name, plan.workspace_bytes,
+                workspace ? workspace_bytes : size_t{0});
+  if (!aligned16(workspace)) return fail(ATTN_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", name);
+  g_last_launches = plan.merge_in_grid ? 1 : 2;
+  if (g_validate_only) return ATTN_OK;
+
+  pda::DecodeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);  // bytes; addressed as such by the kernels
+  p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.o = o;
+  p.counters = static_cast<int32_t*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ATTN_WORKSPACE_ZERO_BYTES);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ATTN_WORKSPACE_ZERO_BYTES +
+                                        plan.part_o_bytes);
+  p.status = status;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.max_blocks = max_blocks;
+  p.window = window;
+  p.grid_x = plan.grid_x;
+  p.min_pages = plan.min_pages;
+  p.out_f32 = out_dtype == ATTN_OUT_F32;
+  p.part_rows = (static_cast<int64_t>(plan.grid_x) + batch) * (sliding ? ATTN_SLIDING_HQ : ATTN_GLOBAL_HQ);
+  p.merge_in_grid = plan.merge_in_grid;
+
+  const int hkv = sliding ? ATTN_SLIDING_HKV : ATTN_GLOBAL_HKV;
+  const int d = sliding ? ATTN_SLIDING_D : ATTN_GLOBAL_D;
+  CUtensorMap tm_k, tm_v, tm_ks, tm_vs;
+  if ((st = encode_fp8_map(&tm_k, k_pool, num_pages, hkv * d, d / 128)) ||
+      (st = encode_fp8_map(&tm_v, v_pool, num_pages, hkv * d, d / 128)) ||
+      (st = encode_scale_map(&tm_ks, k_scale, num_pages * hkv)) ||
+      (st = encode_scale_map(&tm_vs, v_scale, num_pages * hkv)))
+    return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (sliding) {
+    static bool smem_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false};
+    if ((st = ensure_smem(pda::sliding_fp8::decode_kernel, pda::sliding_fp8::kSmemBytes, dev, smem_set)) ||
+        (st = ensure_smem(pda::combine_kernel<ATTN_SLIDING_D>, 0, dev, comb_set)))
+      return st;
+    e = launch_pdl(pda::sliding_fp8::decode_kernel, dim3(plan.grid_x, ATTN_SLIDING_HKV), pda::sliding_fp8::kThreads,
+                   pda::sliding_fp8::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
+    if (e == cudaSuccess && !plan.merge_in_grid)
+      e = launch_pdl(pda::combine_kernel<ATTN_SLIDING_D>,
+                     dim3(ATTN_SLIDING_HQ * (ATTN_SLIDING_D / pda::kCombineCols), batch), pda::kCombineWarps * 32, 0,
+                     s, p);
+  } else {
+    static bool smem_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false};
+    if ((st = ensure_smem(pda::global_fp8::decode_kernel, pda::global_fp8::kSmemBytes, dev, smem_set)) ||
+        (st = ensure_smem(pda::combine_kernel<ATTN_GLOBAL_D>, 0, dev, comb_set)))
+      return st;
+    e = launch_pdl(pda::global_fp8::decode_kernel, dim3(plan.grid_x), pda::global_fp8::kThreads,
+                   pda::global_fp8::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
+    if (e == cudaSuccess)
+      e = launch_pdl(pda::combine_kernel<ATTN_GLOBAL_D>,
+                     dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / pda::kCombineCols), batch), pda::kCombineWarps * 32, 0, s,
+                     p);
+  }
+  return launched(name, e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t attn_kv_append_sliding_chunk(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
+                                     const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
+                                     void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
+                                     int64_t num_pages, int32_t* status, void* stream) {
+  return run_chunk(ATTN_KIND_SLIDING, false, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, nullptr,
+                   nullptr, batch, total_q, max_blocks, num_pages, status, stream);
+}
+
+int32_t attn_kv_append_global_chunk(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
+                                    const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
+                                    void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
+                                    int64_t num_pages, int32_t* status, void* stream) {
+  return run_chunk(ATTN_KIND_GLOBAL, false, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, nullptr,
+                   nullptr, batch, total_q, max_blocks, num_pages, status, stream);
+}
+
+int32_t attn_kv_append_sliding_fp8(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
+                                   const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
+                                   void* v_pool, uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q,
+                                   int32_t max_blocks, int64_t num_pages, int32_t* status, void* stream) {
+  return run_chunk(ATTN_KIND_SLIDING, true, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, k_scale,
+                   v_scale, batch, total_q, max_blocks, num_pages, status, stream);
+}
+
+int32_t attn_kv_append_global_fp8(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
+                                  const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool, void* v_pool,
+                                  uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q,
+                                  int32_t max_blocks, int64_t num_pages, int32_t* status, void* stream) {
+  return run_chunk(ATTN_KIND_GLOBAL, true, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, k_scale,
+                   v_scale, batch, total_q, max_blocks, num_pages, status, stream);
+}
+
+int32_t attn_kv_read_sliding_fp8(const void* k_pool, const void* v_pool, const uint8_t* k_scale, const uint8_t* v_scale,
+                                 const int32_t* block_table, const int32_t* seq_lens, void* k_out, void* v_out,
+                                 const int32_t* out_table, int32_t batch, int32_t max_blocks, int64_t num_pages,
+                                 int64_t out_pages, int32_t max_seq_len, int32_t span, int32_t* status, void* stream) {
+  return run_read(ATTN_KIND_SLIDING, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table,
+                  batch, max_blocks, num_pages, out_pages, max_seq_len, span, status, stream);
+}
+
+int32_t attn_kv_read_global_fp8(const void* k_pool, const void* v_pool, const uint8_t* k_scale, const uint8_t* v_scale,
+                                const int32_t* block_table, const int32_t* seq_lens, void* k_out, void* v_out,
+                                const int32_t* out_table, int32_t batch, int32_t max_blocks, int64_t num_pages,
+                                int64_t out_pages, int32_t max_seq_len, int32_t span, int32_t* status, void* stream) {
+  return run_read(ATTN_KIND_GLOBAL, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table,
+                  batch, max_blocks, num_pages, out_pages, max_seq_len, span, status, stream);
+}
+
+int32_t attn_decode_sliding_fp8(const void* q, const void* k_pool, const void* v_pool, const uint8_t* k_scale,
+                                const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* o,
+                                int32_t batch, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len,
+                                int32_t window, int32_t out_dtype, int32_t num_splits, void* workspace,
+                                size_t workspace_bytes, int32_t* status, void* stream) {
+  return run_decode_fp8(ATTN_KIND_SLIDING, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o, batch,
+                        max_blocks, num_pages, max_seq_len, window, out_dtype, num_splits, workspace, workspace_bytes,
+                        status, stream);
+}
+
+int32_t attn_decode_global_fp8(const void* q, const void* k_pool, const void* v_pool, const uint8_t* k_scale,
+                               const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* o,
+                               int32_t batch, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len,
+                               int32_t window, int32_t out_dtype, int32_t num_splits, void* workspace,
+                               size_t workspace_bytes, int32_t* status, void* stream) {
+  return run_decode_fp8(ATTN_KIND_GLOBAL, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o, batch,
+                        max_blocks, num_pages, max_seq_len, window, out_dtype, num_splits, workspace, workspace_bytes,
+                        status, stream);
+}
+
+}  // extern "C"

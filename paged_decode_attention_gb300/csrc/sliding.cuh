@@ -74,7 +74,8 @@ static_assert(kBlocksPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory o
 //     o = sum_g 2^{m_g - M} O_g / sum_g 2^{m_g - M} l_g,
 // writes o and puts the counter back to 0 for the next call (no other block
 // of this call touches it again).  Partials read back bypass L1.
-__device__ __forceinline__ void merge_partials(const DecodeParams& p, const SeqTable& t, Smem& s, int b, int g,
+template <typename SmemT>
+__device__ __forceinline__ void merge_partials(const DecodeParams& p, const SeqTable& t, SmemT& s, int b, int g,
                                                int c, int h, int d0, float M, float Lsum, float4 O) {
   const int tt = threadIdx.x;
   int cnt = 0;  // non-empty sequences before b among b' = tt, tt + 128

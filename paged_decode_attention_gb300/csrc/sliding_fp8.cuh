@@ -1,0 +1,389 @@
+// sliding_fp8.cuh -- slidingDecodeGQA over an 8-bit cache (fp8.cuh): 16 query
+// heads over 8 KV heads, D = 256, G = 2, scale 1.
+//
+//   o[h] = sum_l 2^{kv_l} w_l v8_l / sum_l w_l,
+//   w_l = exp(2^{kk_l} <q[h], k8_l> - max),  v8, k8 e4m3, kk, kv their scales.
+//
+// A page's head is 8 KB here, half of the bf16 cache's, so at the rate of
+// memory a page has half the time.  On the CUDA cores every value would cost
+// a conversion more than in the bf16 kernel; so both products run on
+// mma.m16n8k16 with the cache as the A operand (16 positions, or 16 dims, by
+// 16) and the two query heads in B's eight columns (each four times), which costs 16
+// MMAs, 96 conversions and 16 shared-memory reads per page and product pair
+// instead of some 1300 FMA-pipe instructions.
+//
+// Grid (grid_x, 8) and the balanced spans as in sliding.cuh.  Warp 4 copies
+// pages; each of the warps 0..3 takes every fourth page whole and keeps its
+// own running max, sum and output, so no barrier is met between a segment's
+// first page and its end, where the four are merged through shared memory
+// exactly as in sliding.cuh.
+//
+// S^T[pos, h] = K q^T: lane (g = lane/4, tq = lane%4) reads 16 consecutive
+// bytes of rows g and g + 8 at unit 2 tq + j of each 128-byte chunk; the
+// units even and odd in j make the 128-byte swizzle conflict free, and the
+// order of the dims inside the contraction is the same for q.
+// O^T[d, h] = V^T P^T: ldmatrix.trans brings pairs of dims for two rows,
+// which a byte permutation and the widening turn into A fragments with rows
+// g and g + 8 = dims 2g and 2g + 1 of 16; P^T is S^T's fragment transposed in
+// place (movmatrix).
+#pragma once
+
+#include "fp8.cuh"
+#include "sliding.cuh"
+
+namespace pda {
+namespace sliding_fp8 {
+
+using sliding::kD;
+using sliding::kG;
+using sliding::kHkv;
+using sliding::kHq;
+
+constexpr int kConsumerWarps = 4;
+constexpr int kThreads = (kConsumerWarps + 1) * 32;
+constexpr int kChunks = kD / 128;                      // 2
+constexpr int kTileBytes = kPage * kD;                 // 4 KB per K (or V) page-head
+constexpr int kStages = 7;
+constexpr int kStageTx = 2 * kTileBytes + 2 * kPage;   // K, V and their scales
+constexpr int kBlocksPerSm = sliding::kBlocksPerSm;    // the plan of the bf16 kernel
+constexpr int kWarmPages = 8;
+
+struct Smem {
+  alignas(1024) uint8_t k[kStages][kTileBytes];  // kChunks tiles of [16 rows][128 dims], swizzled
+  alignas(1024) uint8_t v[kStages][kTileBytes];
+  alignas(128) uint8_t k_scale[kStages][128];  // 16 bytes used: a copy lands on a 128-byte boundary
+  alignas(128) uint8_t v_scale[kStages][128];
+  alignas(16) uint4 qfrag[kConsumerWarps][kChunks * 4][4 * kG];  // q B fragments, per warp
+  alignas(16) float merge_o[kConsumerWarps][kG][kD];
+  float merge_m[kConsumerWarps][kG];
+  float merge_l[kConsumerWarps][kG];
+  int32_t merge_last;
+  int32_t merge_cnt[kConsumerWarps];
+  SeqTable table;
+  alignas(8) uint64_t full[kStages];
+  alignas(8) uint64_t empty[kStages];
+};
+
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + alignment slack
+static_assert(kBlocksPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of the resident blocks");
+
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
+                  const __grid_constant__ DecodeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+
+  const int gb = blockIdx.x;
+  const int c = blockIdx.y;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(&s.full[st], 1);
+      mbar_init(&s.empty[st], 1);  // the one warp that takes the page
+    }
+    fence_mbar_init();
+  }
+  if (warp == kConsumerWarps && lane == 0) {
+    prefetch_tensor_map(&tm_k);
+    prefetch_tensor_map(&tm_v);
+    prefetch_tensor_map(&tm_ks);
+    prefetch_tensor_map(&tm_vs);
+  }
+  // The prologue overlaps the previous kernel; see sliding.cuh.
+  build_seq_table_hint(p, s.table, gb);  // ends with __syncthreads
+  if (warp == kConsumerWarps) {
+    warm_first_pages(p, s.table, kWarmPages, [&](int32_t y) {
+      tma_prefetch_3d(&tm_k, 0, y, c * kChunks);
+      tma_prefetch_3d(&tm_v, 0, y, c * kChunks);
+    });
+  } else {
+    warm_q(p, s.table, kHq * kD, c * kG * kD, kG * kD * 2, kConsumerWarps * 32);
+  }
+  wait_for_primary_grid();
+  int first = warp == kConsumerWarps ? page_entry(p, s.table, s.table.span, lane, false) : 0;
+  confirm_seq_table(p, s.table, gb);  // ends with __syncthreads
+  const SeqTable& t = s.table;
+  const Span sp = t.span;
+  const int n_pages = sp.end - sp.begin;
+  if (p.merge_in_grid && gb == 0 && warp < kConsumerWarps) {
+    // no combine kernel: block 0 of each column writes the empty sums (L = 0)
+    for (int b = 0; b < p.batch; ++b) {
+      if (t.prefix[b + 1] != t.prefix[b]) continue;
+      const size_t row = static_cast<size_t>(b) * kHq + c * kG + (threadIdx.x >> 6);
+      store_out4(p, row * kD + (threadIdx.x & 63) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  }
+  if (n_pages <= 0) return;
+
+  if (warp == kConsumerWarps) {
+    // ---------------- producer ----------------
+    const uint64_t policy = l2_policy_evict_first();
+    if (t.rebuilt) first = page_entry(p, t, sp, lane, true);
+    produce_pages<kStages, kStageTx>(p, t, sp, s.full, s.empty, first, [&](int stage, int32_t y) {
+      tma_load_3d_hint(s.k[stage], &tm_k, 0, y, c * kChunks, &s.full[stage], policy);
+      tma_load_3d_hint(s.v[stage], &tm_v, 0, y, c * kChunks, &s.full[stage], policy);
+      // the scales of this head: 16 bytes in row (page * Hkv + c) of the scale pools
+      const int32_t ys = y < 0 ? -1 : y / kPage * kHkv + c;
+      tma_load_2d(s.k_scale[stage], &tm_ks, 0, ys, &s.full[stage]);
+      tma_load_2d(s.v_scale[stage], &tm_vs, 0, ys, &s.full[stage]);
+    });
+    allow_dependent_launch();
+    return;
+  }
+
+  // ---------------- consumers ----------------
+  const int hq0 = c * kG;
+  const int g = lane >> 2;
+  const int tq = lane & 3;
+  const int mi = lane >> 3;  // ldmatrix: which 8x8 matrix this lane addresses
+  const int lr = lane & 7;
+
+  PageCursor cur;
+  cur.start(p, t, sp);
+
+  // q as B fragments, one copy per warp in shared memory (32 registers would
+  // spill): column n = g holds head g % 2 (the products' columns beyond the
+  // two heads repeat them and are never read), k-step (chunk, j, word): dims
+  // 128 chunk + 16 (2 tq + j) + 4 word .. + 3.  Two k-steps per 16 bytes.
+  const int qlane = (g & 1) * 4 + tq;
+  const uint32_t qaddr = smem_addr(&s.qfrag[warp][0][qlane]);
+  float qs[2];  // logit factor 2^k log2(e) of heads 0 and 1
+  auto load_q = [&]() {
+    uint32_t w[kChunks * 2][8];  // chunk and j
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < kChunks * 2; ++i) {
+      const __nv_bfloat16* src = p.q + (static_cast<size_t>(cur.b) * kHq + hq0 + (g & 1)) * kD + 128 * (i >> 1) +
+                                 16 * (2 * tq + (i & 1));
+      const uint4 a = ld_global_nc_v4(src), b = ld_global_nc_v4(src + 8);
+      w[i][0] = a.x; w[i][1] = a.y; w[i][2] = a.z; w[i][3] = a.w;
+      w[i][4] = b.x; w[i][5] = b.y; w[i][6] = b.z; w[i][7] = b.w;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) amax = max(amax, max(w[i][k] << 16 & 0x7fff0000u, w[i][k] & 0x7fff0000u));
+    }
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));  // over the row's four lanes
+    float inv;
+    const int e = fp8::q_exponent(amax, inv);
+    __syncwarp();  // the warp is done with the previous sequence's fragments
+#pragma unroll
+    for (int i = 0; i < kChunks * 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (g < kG)
+          s.qfrag[warp][2 * i + k][qlane] =
+              make_uint4(fp8::q_f16x2(w[i][4 * k], inv), fp8::q_f16x2(w[i][4 * k + 1], inv),
+                         fp8::q_f16x2(w[i][4 * k + 2], inv), fp8::q_f16x2(w[i][4 * k + 3], inv));
+    __syncwarp();
+    const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * kLog2e;
+    qs[0] = __shfl_sync(0xffffffffu, f, 0);
+    qs[1] = __shfl_sync(0xffffffffu, f, 4);
+  };
+  load_q();
+  auto prefetch_next_q = [&]() {
+    const int nb = next_seq_in_span(p, t, sp, cur.b);
+    if (nb >= 0 && threadIdx.x < kG * kD * 2 / 128)
+      prefetch_l2(reinterpret_cast<const uint8_t*>(p.q + (static_cast<size_t>(nb) * kHq + hq0) * kD) +
+                  threadIdx.x * 128);
+  };
+  prefetch_next_q();
+
+  fp8::Reference ref[2];  // heads 0 and 1
+  float l[2];             // this lane's share of the sums
+  float acc[16][4];    // 16-dim blocks: (dim 2g; heads 0, 1), (dim 2g + 1; heads 0, 1)
+  auto reset = [&]() {
+    ref[0].reset();
+    ref[1].reset();
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+  };
+  reset();
+  bool ok = true;
+
+  for (int i = 0; i < n_pages; ++i) {
+    const int f = sp.begin + i;
+    if (f >= t.prefix[cur.b + 1]) {
+      cur.advance(p, t, sp, f);
+      load_q();
+      prefetch_next_q();
+    }
+    if ((i & (kConsumerWarps - 1)) == warp) {
+      const int st = i % kStages;
+      if (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.full[st], (i / kStages) & 1));
+        if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+      }
+      const int pos0 = cur.pos0(t, f);
+      const uint32_t kst = smem_addr(s.k[st]), vst = smem_addr(s.v[st]);
+      const bool edge = pos0 < cur.lo || pos0 + kPage > cur.L;
+      const bool in0 = pos0 + g >= cur.lo && pos0 + g < cur.L;          // row g is visible
+      const bool in1 = pos0 + g + 8 >= cur.lo && pos0 + g + 8 < cur.L;  // row g + 8
+
+      // ---- S^T = K q^T: four chains of MMAs ----
+      float sc[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[k][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kChunks * 2; ++k) {  // chunk, j
+        const uint32_t base = kst + (k >> 1) * fp8::kChunkBytes;
+        const uint4 a = ld_shared_v4(base + fp8::swz(g, 2 * tq + (k & 1)));
+        const uint4 b = ld_shared_v4(base + fp8::swz(g + 8, 2 * tq + (k & 1)));
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int w = 0; w < 4; w += 2) {
+          const uint4 q = ld_shared_v4(qaddr + (2 * k + w / 2) * 128);
+          fp8::mma_f16_16816(sc[w], fp8::lo_f16x2(aw[w]), fp8::lo_f16x2(bw[w]), fp8::hi_f16x2(aw[w]),
+                             fp8::hi_f16x2(bw[w]), q.x, q.y);
+          fp8::mma_f16_16816(sc[w + 1], fp8::lo_f16x2(aw[w + 1]), fp8::lo_f16x2(bw[w + 1]), fp8::hi_f16x2(aw[w + 1]),
+                             fp8::hi_f16x2(bw[w + 1]), q.z, q.w);
+        }
+      }
+      const float kf0 = fp8::scale_value(s.k_scale[st][g]), kf1 = fp8::scale_value(s.k_scale[st][g + 8]);
+      float kv0 = fp8::scale_log2(s.v_scale[st][g]), kv1 = fp8::scale_log2(s.v_scale[st][g + 8]);
+      // x[0..3]: (row g; heads 0, 1), (row g + 8; heads 0, 1), in log2 units
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[e] = ((sc[0][e] + sc[1][e]) + (sc[2][e] + sc[3][e])) * (e < 2 ? kf0 : kf1) * qs[e & 1];
+      if (edge) {
+        if (!in0) { x[0] = x[1] = -INFINITY; kv0 = 0.f; }
+        if (!in1) { x[2] = x[3] = -INFINITY; kv1 = 0.f; }
+        // zero V rows outside [lo, L): weight 0 times NaN would be NaN
+#pragma unroll 1
+        for (int rr = 0; rr < kPage; ++rr) {
+          const int pos = pos0 + rr;
+          if ((pos < cur.lo || pos >= cur.L) && lane < 16)
+            st_shared_v4(vst + (lane >> 3) * fp8::kChunkBytes + rr * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
+        }
+        fence_proxy_async_smem();  // before TMA rewrites this stage
+        __syncwarp();
+      }
+
+      // ---- online softmax, in log2 units ----
+      float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+      float mt[2] = {fmaxf(x[0] + kv0, x[2] + kv1), fmaxf(x[1] + kv0, x[3] + kv1)};
+      if (__any_sync(0xffffffffu, mx[0] > ref[0].m || mx[1] > ref[1].m || mt[0] > ref[0].T || mt[1] > ref[1].T)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], o));
+            mt[h] = fmaxf(mt[h], __shfl_xor_sync(0xffffffffu, mt[h], o));
+          }
+          float ls, as;
+          ref[h].move(mx[h], mt[h], ls, as);
+          l[h] *= ls;
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            acc[n][h] *= as;
+            acc[n][2 + h] *= as;
+          }
+        }
+      }
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const fp8::Reference& r = ref[e & 1];
+        const float d = x[e] - r.m_use();
+        l[e & 1] += ex2_approx(d);
+        w[e] = ex2_approx(d + (r.weight_bias() + (e < 2 ? kv0 : kv1)));
+      }
+      const uint32_t pb0 = fp8::transpose_8x8(fp8::pack_f16x2(w[0], w[1]));  // rows 0..7
+      const uint32_t pb1 = fp8::transpose_8x8(fp8::pack_f16x2(w[2], w[3]));  // rows 8..15
+
+      // ---- O^T += V^T P^T ----
+#pragma unroll
+      for (int np = 0; np < 8; ++np) {  // 32 dims each
+        const int ch = np >> 2;
+        const int row = ((mi & 1) << 3) + lr;
+        uint32_t r[4];
+        ldmatrix_x4_trans(vst + ch * fp8::kChunkBytes + fp8::swz(row, 2 * (np & 3) + (mi >> 1)), r[0], r[1], r[2],
+                          r[3]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t a0, a1, a2, a3;
+          fp8::split_pair(r[2 * u], a0, a1);
+          fp8::split_pair(r[2 * u + 1], a2, a3);
+          fp8::mma_f16_16816(acc[2 * np + u], a0, a1, a2, a3, pb0, pb1);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.empty[st]);
+    }
+
+    if (f + 1 == cur.seg_end) {
+      // ---------------- finish this sequence's segment (as in sliding.cuh) ----------------
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+      if (tq == 0) {  // columns 0 and 1: the two heads
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+#pragma unroll
+          for (int h = 0; h < kG; ++h)
+            *reinterpret_cast<float2*>(&s.merge_o[warp][h][16 * n + 2 * g]) =
+                make_float2(fp8::unscale(acc[n][h], ref[h].R), fp8::unscale(acc[n][2 + h], ref[h].R));
+      }
+      if (lane == 0) {
+#pragma unroll
+        for (int h = 0; h < kG; ++h) {
+          s.merge_m[warp][h] = ref[h].m;
+          s.merge_l[warp][h] = l[h];
+        }
+      }
+      named_barrier_sync(1, kConsumerWarps * 32);
+      const int tt = threadIdx.x;  // 0..127: 2 heads x 64 groups of 4 dims
+      const int h = tt >> 6;
+      const int d0 = (tt & 63) * 4;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, s.merge_m[w][h]);
+      float Lsum = 0.f;
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+      // (with M = -inf every weight was 0 or NaN; a NaN has to show)
+      const float M_use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < kConsumerWarps; ++w) {
+        const float fw = exp2f(s.merge_m[w][h] - M_use);
+        Lsum += (s.merge_m[w][h] == -INFINITY ? 1.f : fw) * s.merge_l[w][h];
+        const float4 a = *reinterpret_cast<const float4*>(&s.merge_o[w][h][d0]);
+        O.x += fw * a.x;
+        O.y += fw * a.y;
+        O.z += fw * a.z;
+        O.w += fw * a.w;
+      }
+      if (cur.whole(t, sp)) {
+        const float inv = Lsum > 0.f ? 1.f / Lsum : Lsum;
+        const size_t row = static_cast<size_t>(cur.b) * kHq + hq0 + h;
+        store_out4(p, row * kD + d0, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+      } else if ((static_cast<int64_t>(gb) + cur.b + 1) * kHq > p.part_rows) {
+        if (tt == 0) report(p.status, ATTN_DEV_INTERNAL);  // cannot happen: slot beyond the workspace
+      } else {
+        // a NaN sum is handed on as (inf, 1): the merges skip partials whose sum is not positive
+        if (Lsum != Lsum) {
+          M = INFINITY;
+          Lsum = 1.f;
+        }
+        const size_t slot = (static_cast<size_t>(gb) + cur.b) * kHq + hq0 + h;
+        *reinterpret_cast<float4*>(p.part_o + slot * kD + d0) = O;
+        if (d0 == 0) p.part_ml[slot] = make_float2(M, Lsum);
+        if (p.merge_in_grid) sliding::merge_partials(p, t, s, cur.b, gb, c, h, d0, M, Lsum, O);
+      }
+      named_barrier_sync(1, kConsumerWarps * 32);  // merge buffers free again
+      reset();
+    }
+  }
+  allow_dependent_launch();
+}
+
+}  // namespace sliding_fp8
+}  // namespace pda

@@ -27,7 +27,8 @@ namespace {
 
 // Validates `call` (its launches suppressed) and, if it passes, appends it
 // with the number of kernels it launches.
-int32_t record(attn_step* step, std::function<int32_t(void*)> call, const char* name) {
+template <typename Call>
+int32_t record(attn_step* step, const Call& call, const char* name) {
   g_err[0] = '\0';
   if (!step) return fail(ATTN_ERR_INVALID_ARG, "%s: null step", name);
   if (step->finalized) return fail(ATTN_ERR_INVALID_ARG, "%s: the step is already finalized", name);
@@ -38,7 +39,7 @@ int32_t record(attn_step* step, std::function<int32_t(void*)> call, const char* 
   if (st != ATTN_OK) return st;
   const int32_t kernels = g_last_launches;
   try {
-    step->calls.push_back(std::move(call));
+    step->calls.emplace_back(call);  // the std::function is made here, so that its allocation is caught too
   } catch (...) {  // no exception may leave the C ABI
     return fail(ATTN_ERR_INVALID_ARG, "%s: out of host memory", name);
   }
@@ -118,6 +119,62 @@ int32_t attn_step_add_kv_append_global(attn_step* step, const void* qkv, const v
     return attn_kv_append_global(qkv, w_q, w_k, block_table, positions, q_out, k_pool, v_pool, batch, max_blocks,
                                  num_pages, status, s);
   }, "attn_step_add_kv_append_global");
+}
+
+int32_t attn_step_add_kv_append_sliding_chunk(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+    const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool, void* v_pool,
+    int32_t batch, int32_t total_q, int32_t max_blocks, int64_t num_pages, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_kv_append_sliding_chunk(qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, batch, total_q,
+        max_blocks, num_pages, status, s);
+  }, "attn_step_add_kv_append_sliding_chunk");
+}
+
+int32_t attn_step_add_kv_append_sliding_fp8(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+    const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool, void* v_pool,
+    uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q, int32_t max_blocks, int64_t num_pages, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_kv_append_sliding_fp8(qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, k_scale, v_scale, batch, total_q,
+        max_blocks, num_pages, status, s);
+  }, "attn_step_add_kv_append_sliding_fp8");
+}
+
+int32_t attn_step_add_decode_sliding_fp8(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
+    const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* o,
+    int32_t batch, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len, int32_t window, int32_t out_dtype,
+    int32_t num_splits, void* workspace, size_t workspace_bytes, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_decode_sliding_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o, batch, max_blocks,
+        num_pages, max_seq_len, window, out_dtype, num_splits, workspace, workspace_bytes, status, s);
+  }, "attn_step_add_decode_sliding_fp8");
+}
+
+int32_t attn_step_add_kv_append_global_chunk(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+    const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool, void* v_pool,
+    int32_t batch, int32_t total_q, int32_t max_blocks, int64_t num_pages, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_kv_append_global_chunk(qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, batch, total_q,
+        max_blocks, num_pages, status, s);
+  }, "attn_step_add_kv_append_global_chunk");
+}
+
+int32_t attn_step_add_kv_append_global_fp8(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+    const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool, void* v_pool,
+    uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q, int32_t max_blocks, int64_t num_pages, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_kv_append_global_fp8(qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, k_scale, v_scale, batch, total_q,
+        max_blocks, num_pages, status, s);
+  }, "attn_step_add_kv_append_global_fp8");
+}
+
+int32_t attn_step_add_decode_global_fp8(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
+    const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* o,
+    int32_t batch, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len, int32_t window, int32_t out_dtype,
+    int32_t num_splits, void* workspace, size_t workspace_bytes, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_decode_global_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o, batch, max_blocks,
+        num_pages, max_seq_len, window, out_dtype, num_splits, workspace, workspace_bytes, status, s);
+  }, "attn_step_add_decode_global_fp8");
 }
 
 int32_t attn_step_num_calls(const attn_step* step) { return step ? static_cast<int32_t>(step->calls.size()) : 0; }

@@ -1,0 +1,141 @@
+"""Refusals of the chunk appends and the 8-bit cache calls, without a GPU: error codes before anything is launched."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import paged_decode_attention_gb300 as pda
+from paged_decode_attention_gb300 import _build
+
+from _fp8 import dequantise, e4m3_table, quantise
+
+FAKE = 1 << 20  # an aligned, never dereferenced address
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return pda.load()
+
+
+ARGS = {
+    "chunk": ["qkv", "w_q", "w_k", "table", "lens", "cu_q", "q_out", "k", "v", "batch", "total_q", "max_blocks",
+              "num_pages", "status"],
+    "fp8": ["qkv", "w_q", "w_k", "table", "lens", "cu_q", "q_out", "k", "v", "ks", "vs", "batch", "total_q",
+            "max_blocks", "num_pages", "status"],
+    "read": ["k", "v", "ks", "vs", "table", "lens", "k_out", "v_out", "out_table", "batch", "max_blocks", "num_pages",
+             "out_pages", "max_seq_len", "span", "status"],
+    "decode": ["q", "k", "v", "ks", "vs", "table", "lens", "o", "batch", "max_blocks", "num_pages", "max_seq_len",
+               "window", "out_dtype", "num_splits", "ws", "ws_bytes", "status"],
+}
+DEFAULTS = dict(batch=4, total_q=9, max_blocks=70, num_pages=300, out_pages=200, max_seq_len=1100, span=0, window=1024,
+                out_dtype=0, num_splits=0, ws=None, ws_bytes=0, status=None)
+NAMES = {"attn_kv_append_%s_chunk": "chunk", "attn_kv_append_%s_fp8": "fp8", "attn_kv_read_%s_fp8": "read",
+         "attn_decode_%s_fp8": "decode"}
+
+
+def call(lib, name, form, step=None, **kw):
+    values = [kw.get(a, DEFAULTS.get(a, FAKE)) for a in ARGS[form]]
+    if step is not None:
+        return getattr(lib, name.replace("attn_", "attn_step_add_"))(step, *values)
+    return getattr(lib, name)(*values, None)
+
+
+def bad_calls():
+    for pattern, form in NAMES.items():
+        for kind in ("sliding", "global"):
+            name = pattern % kind
+            pointers = [a for a in ARGS[form] if a not in DEFAULTS]
+            for a in pointers:
+                if not (a == "k" and form == "chunk" and kind == "global"):
+                    yield name, form, {a: None}, INVALID
+                yield name, form, {a: FAKE + 2}, INVALID
+            yield name, form, dict(status=FAKE + 1), INVALID
+            yield name, form, dict(batch=0), INVALID
+            yield name, form, dict(batch=257), UNSUPPORTED
+            yield name, form, dict(max_blocks=0), INVALID
+            yield name, form, dict(num_pages=0), INVALID
+            yield name, form, dict(num_pages=1 << 27), INVALID
+            if form in ("chunk", "fp8"):
+                yield name, form, dict(total_q=-1), INVALID
+            if form == "read":
+                yield name, form, dict(out_pages=0), INVALID
+            if form in ("read", "decode"):
+                yield name, form, dict(max_seq_len=-1), INVALID
+                yield name, form, dict(max_seq_len=70 * 16 + 1), INVALID
+                yield name, form, dict(max_blocks=20000, max_seq_len=262145), UNSUPPORTED
+            if form == "decode":
+                yield name, form, dict(out_dtype=2), INVALID
+                yield name, form, dict(num_splits=-1), INVALID
+                if kind == "sliding":
+                    yield name, form, dict(window=0), INVALID
+
+
+@pytest.mark.parametrize("name,form,bad,code", list(bad_calls()), ids=lambda x: str(x))
+def test_bad_arguments_are_refused_before_launch(lib, name, form, bad, code):
+    assert call(lib, name, form, **bad) == code
+    assert name in pda.attn_last_error()
+    if form != "read":  # the read is not part of a decode step
+        h = ctypes.c_void_p()
+        assert lib.attn_step_create(ctypes.byref(h)) == 0
+        try:
+            assert call(lib, name, form, step=h, **bad) == code
+            assert lib.attn_step_num_calls(h) == 0
+        finally:
+            lib.attn_step_destroy(h)
+
+
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_no_tokens_is_a_call_without_a_launch(lib, kind):
+    for suffix, form in (("chunk", "chunk"), ("fp8", "fp8")):
+        assert call(lib, "attn_kv_append_%s_%s" % (kind, suffix), form, total_q=0, qkv=None, q_out=None) == 0
+
+
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_binding_refuses_cpu_tensors(lib, kind):
+    k = getattr(pda, "KIND_" + kind.upper())
+    cache = pda.new_fp8_cache(k, 2, "cpu")
+    Hq, Hkv, D = pda.SHAPES[k]
+    assert cache[0].shape == (2, 16, Hkv, D) and cache[2].shape == (2, Hkv, 16)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    with pytest.raises(ValueError, match="CUDA"):
+        getattr(pda, "attn_decode_%s_fp8" % kind)(bf(1, Hq, D), *cache, i32(1, 1), i32(1))
+    with pytest.raises(ValueError, match="CUDA"):
+        getattr(pda, "attn_kv_append_%s_fp8" % kind)(bf(1, pda.APPEND_ROW[k]), bf(D), bf(D), i32(1, 1), i32(1), i32(2),
+                                                     *cache)
+    pools = [bf(2, 16, Hkv, D), bf(2, 16, Hkv, D)]
+    with pytest.raises(ValueError, match="CUDA"):
+        getattr(pda, "attn_kv_append_%s_chunk" % kind)(bf(1, pda.APPEND_ROW[k]), bf(D), bf(D), i32(1, 1), i32(1),
+                                                       i32(2), *pools)
+    with pytest.raises(ValueError, match="CUDA"):
+        getattr(pda, "attn_kv_read_%s_fp8" % kind)(*cache, i32(1, 1), i32(1), *pools)
+    step = pda.Step()
+    with pytest.raises(ValueError, match="CUDA"):
+        getattr(step, "add_decode_%s_fp8" % kind)(bf(1, Hq, D), *cache, i32(1, 1), i32(1))
+    assert step.num_calls == 0
+    step.close()
+
+
+def test_the_plain_format_agrees_with_torch():
+    # e4m3 as torch reads it, and the quantiser's rounding on torch's conversion of the scaled values
+    codes = torch.arange(256, dtype=torch.uint8)
+    assert torch.allclose(codes.view(torch.float8_e4m3fn).double(), e4m3_table(), equal_nan=True, rtol=0, atol=0)
+    r = np.random.RandomState(1)
+    y = r.standard_normal((400, 64)) * np.exp(r.uniform(-20, 20, (400, 1)))
+    y[3] = 0
+    y[4, 2] = np.nan
+    y[5, :] = 448.0 * 2.0 ** 3
+    y[6, :] = np.nextafter(448.0, 500)
+    c, s = quantise(y)
+    k = s.astype(np.int64) - 127
+    assert s[3] == 1 and s[4] == 255 and k[5] == 3 and k[6] == 1
+    ok = np.arange(400) != 4
+    z = torch.from_numpy(y[ok] / 2.0 ** k[ok, None])
+    assert np.array_equal(z.float().to(torch.float8_e4m3fn).view(torch.uint8).numpy(), c[ok])
+    back = dequantise(torch.from_numpy(c.reshape(25, 16, 1, 64)), torch.from_numpy(s.reshape(25, 1, 16)))
+    err = np.abs(back.numpy().reshape(400, 64) - y)[ok]
+    assert (err <= 2.0 ** -4 * np.abs(y[ok]) + 2.0 ** -10 * 2.0 ** k[ok, None]).all()
