@@ -209,6 +209,59 @@ int32_t attn_decode_global_shared(const void* q, const void* kv_pool, const void
                                   int32_t* status, void* stream);
 
 /*
+ * attn_decode_global_prefix -- decodeGQA for a batch that shares a long
+ * prefix (a system prompt, a document): sequence b sees the prefix's
+ * positions and then its own,
+ *
+ *   o[b,h] = sum over both of softmax_l( <q[b,h], k_l> ) * v_l,
+ *
+ * what attn_decode_global computes with the prefix's pages listed in front of
+ * every sequence's own, but the prefix's pages are read once for the whole
+ * batch, with its products on the tensor cores as one matrix product.
+ *
+ * q             bf16 [batch, 16, 512]
+ * k_pool, v_pool  bf16 [num_pages, 16, 1, 512]: prefix and own pages
+ * prefix_table  int32 [prefix_blocks]: the prefix's pages
+ * prefix_len    int32 [1] (device): its positions, 0 .. prefix_blocks*16; need
+ *               not fill its last page, whose other rows are never used
+ * block_table   int32 [batch, max_blocks], seq_lens int32 [batch]: the own
+ *               positions, numbered from 0 behind the prefix; 0 is allowed (the
+ *               sequence then sees the prefix alone, and with an empty prefix
+ *               its output is 0)
+ * o             [batch, 16, 512], bf16 or fp32 per out_dtype
+ * max_prefix_len, max_seq_len  host bounds; they size the launches only and
+ *               never change which positions are read
+ * num_splits    thread blocks for the own positions, as for attn_decode_global
+ * prefix_splits spans the prefix is cut into: 0 = automatic, at most 128
+ * workspace     at least attn_decode_prefix_workspace_size(...) bytes, its
+ *               first ATTN_WORKSPACE_ZERO_BYTES as for the decode calls; not
+ *               shared by calls that may overlap
+ * status        as for attn_decode_global; a prefix_len outside its range
+ *               raises ATTN_DEV_BAD_SEQ_LEN and is clamped
+ *
+ * Every array 16 bytes aligned (prefix_table, prefix_len 4).  Three kernels.
+ * Weights are rounded to bf16 for their product with the values.
+ */
+int32_t attn_decode_global_prefix(const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+                                  const int32_t* prefix_len, const int32_t* block_table, const int32_t* seq_lens,
+                                  void* o, int32_t batch, int32_t prefix_blocks, int32_t max_blocks, int64_t num_pages,
+                                  int32_t max_prefix_len, int32_t max_seq_len, int32_t out_dtype, int32_t num_splits,
+                                  int32_t prefix_splits, void* workspace, size_t workspace_bytes, int32_t* status,
+                                  void* stream);
+
+/*
+ * attn_decode_prefix_plan -- attn_decode_global_prefix's plan on a device of
+ * num_sms multiprocessors, as pure host arithmetic; attn_decode_prefix_workspace_size
+ * -- its workspace for the current CUDA device (0, with attn_last_error, on bad
+ * arguments or when no device can be queried).
+ */
+int32_t attn_decode_prefix_plan(int32_t batch, int32_t max_prefix_len, int32_t max_seq_len, int32_t num_splits,
+                                int32_t prefix_splits, int32_t num_sms, int32_t* out_num_splits,
+                                int32_t* out_prefix_splits, size_t* out_workspace_bytes);
+size_t attn_decode_prefix_workspace_size(int32_t batch, int32_t max_prefix_len, int32_t max_seq_len,
+                                         int32_t num_splits, int32_t prefix_splits);
+
+/*
  * attn_decode_plan -- the launch plan, as pure host arithmetic (no CUDA call).
  *
  * kind         ATTN_KIND_SLIDING or ATTN_KIND_GLOBAL

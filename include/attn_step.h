@@ -103,7 +103,8 @@ int32_t attn_step_add_kv_append_global(attn_step* step, const void* qkv, const v
                                        void* k_pool, void* v_pool, int32_t batch, int32_t max_blocks,
                                        int64_t num_pages, int32_t* status);
 
-/* Chunk appends (attn_decode.h) and the 8-bit cache (attn_fp8.h). */
+/* Chunk appends and the decode behind a shared prefix (attn_decode.h), and
+ * the 8-bit cache (attn_fp8.h). */
 int32_t attn_step_add_kv_append_sliding_chunk(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
                                               const int32_t* block_table, const int32_t* seq_lens,
                                               const int32_t* cu_q, void* q_out, void* k_pool, void* v_pool,
@@ -136,6 +137,14 @@ int32_t attn_step_add_decode_global_fp8(attn_step* step, const void* q, const vo
                                         int64_t num_pages, int32_t max_seq_len, int32_t window, int32_t out_dtype,
                                         int32_t num_splits, void* workspace, size_t workspace_bytes,
                                         int32_t* status);
+
+int32_t attn_step_add_decode_global_prefix(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
+                                           const int32_t* prefix_table, const int32_t* prefix_len,
+                                           const int32_t* block_table, const int32_t* seq_lens, void* o,
+                                           int32_t batch, int32_t prefix_blocks, int32_t max_blocks,
+                                           int64_t num_pages, int32_t max_prefix_len, int32_t max_seq_len,
+                                           int32_t out_dtype, int32_t num_splits, int32_t prefix_splits,
+                                           void* workspace, size_t workspace_bytes, int32_t* status);
 
 /* Calls recorded so far, and kernels they launch per step. */
 int32_t attn_step_num_calls(const attn_step* step);

@@ -16,6 +16,7 @@ power-of-two scales; ``include/attn_fp8.h``) is written by
 ``attn_kv_append_{sliding,global}_fp8``, decoded over by
 ``attn_decode_{sliding,global}_fp8`` and read back into bf16 pages by
 ``attn_kv_read_{sliding,global}_fp8``; ``new_fp8_cache`` allocates one.
+``attn_decode_global_prefix`` decodes a batch behind a prefix that it shares.
 """
 
 import ctypes
@@ -31,7 +32,8 @@ __all__ = [
     "PreparedDecode", "prepare_decode_sliding", "prepare_decode_global", "prepare_decode_global_shared", "Step",
     "attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk",
     "attn_kv_append_sliding_fp8", "attn_kv_append_global_fp8", "attn_kv_read_sliding_fp8", "attn_kv_read_global_fp8",
-    "attn_decode_sliding_fp8", "attn_decode_global_fp8", "new_fp8_cache", "PreparedCall",
+    "attn_decode_sliding_fp8", "attn_decode_global_fp8", "attn_decode_global_prefix", "attn_decode_prefix_plan",
+    "attn_decode_prefix_workspace_size", "prepare_decode_global_prefix", "new_fp8_cache", "PreparedCall",
     "prepare_kv_append_sliding_chunk", "prepare_kv_append_global_chunk", "prepare_kv_append_sliding_fp8",
     "prepare_kv_append_global_fp8", "prepare_kv_read_sliding_fp8", "prepare_kv_read_global_fp8",
     "prepare_decode_sliding_fp8", "prepare_decode_global_fp8",
@@ -61,7 +63,8 @@ EXPORTS = ("attn_decode_sliding", "attn_decode_global", "attn_decode_global_shar
            "attn_decode_sliding_fp8", "attn_decode_global_fp8", "attn_step_add_kv_append_sliding_chunk",
            "attn_step_add_kv_append_global_chunk", "attn_step_add_kv_append_sliding_fp8",
            "attn_step_add_kv_append_global_fp8", "attn_step_add_decode_sliding_fp8",
-           "attn_step_add_decode_global_fp8")
+           "attn_step_add_decode_global_fp8", "attn_decode_global_prefix", "attn_decode_prefix_plan",
+           "attn_decode_prefix_workspace_size", "attn_step_add_decode_global_prefix")
 # attn_step launch modes (attn_step.h)
 STEP_LAUNCH_AUTO, STEP_LAUNCH_GRAPH, STEP_LAUNCH_DIRECT = 0, 1, 2
 STEP_LAUNCH_MODES = {"auto": STEP_LAUNCH_AUTO, "graph": STEP_LAUNCH_GRAPH, "direct": STEP_LAUNCH_DIRECT}
@@ -127,10 +130,19 @@ def load(path=None):
     read8 = [c_vp] * 9 + [c_i32, c_i32, c_i64, c_i64, c_i32, c_i32, c_vp, c_vp]  # k_pool v_pool k_scale v_scale
     #            block_table seq_lens k_out v_out out_table; batch max_blocks num_pages out_pages max_seq_len span ...
     call8 = call[:3] + [c_vp, c_vp] + call[3:]                      # k_scale v_scale after v_pool
+    prefix = [c_vp] * 8 + [c_i32, c_i32, c_i32, c_i64, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_sz, c_vp, c_vp]
+    #        q k_pool v_pool prefix_table prefix_len block_table seq_lens o; batch prefix_blocks max_blocks num_pages
+    #        max_prefix_len max_seq_len out_dtype num_splits prefix_splits workspace workspace_bytes status stream
+    lib.attn_decode_prefix_plan.restype = c_i32
+    lib.attn_decode_prefix_plan.argtypes = [c_i32] * 6 + [ctypes.POINTER(c_i32), ctypes.POINTER(c_i32),
+                                                          ctypes.POINTER(c_sz)]
+    lib.attn_decode_prefix_workspace_size.restype = c_sz
+    lib.attn_decode_prefix_workspace_size.argtypes = [c_i32] * 5
     for names, types in ((("attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk"), chunk),
                          (("attn_kv_append_sliding_fp8", "attn_kv_append_global_fp8"), chunk8),
                          (("attn_kv_read_sliding_fp8", "attn_kv_read_global_fp8"), read8),
-                         (("attn_decode_sliding_fp8", "attn_decode_global_fp8"), call8)):
+                         (("attn_decode_sliding_fp8", "attn_decode_global_fp8"), call8),
+                         (("attn_decode_global_prefix",), prefix)):
         for name in names:
             getattr(lib, name).restype = c_i32
             getattr(lib, name).argtypes = types
@@ -408,6 +420,9 @@ class Step:
 
     def add_decode_global_fp8(self, *args, **kw):
         return self._add(*_decode_fp8_args(KIND_GLOBAL, *args, **kw))
+
+    def add_decode_global_prefix(self, *args, **kw):
+        return self._add(*_prefix_args(*args, **kw))
 
     @property
     def num_calls(self):
@@ -763,12 +778,7 @@ def _decode_fp8_args(kind, q, k_pool, v_pool, k_scale, v_scale, block_table, seq
     batch, max_blocks = block_table.shape
     cache, n = _fp8_ptrs(kind, k_pool, v_pool, k_scale, v_scale)
     q_ptr = _ptr(q, "q", torch.bfloat16, (batch, Hq, D))
-    if o is None:
-        if out_dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-        o = torch.empty((batch, Hq, D), dtype=out_dtype, device=q.device)
-    elif not isinstance(o, torch.Tensor) or o.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("o must be a torch.bfloat16 or torch.float32 tensor")
+    o = _output(o, (batch, Hq, D), out_dtype, q.device)
     if window is None:
         window = 1024 if kind == KIND_SLIDING else 0
     if max_seq_len is None:
@@ -784,6 +794,70 @@ def _decode_fp8_args(kind, q, k_pool, v_pool, k_scale, v_scale, block_table, seq
         batch, max_blocks, n, int(max_seq_len), int(window), OUT_F32 if o.dtype == torch.float32 else OUT_BF16,
         int(num_splits), _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _status_ptr(status))
     return "attn_decode_%s_fp8" % _kind_name(kind), args, keep, o, device
+
+
+def attn_decode_prefix_plan(batch, max_prefix_len, max_seq_len, num_splits=0, prefix_splits=0, num_sms=152):
+    """(num_splits, prefix_splits, workspace_bytes) of attn_decode_global_prefix; pure host arithmetic."""
+    lib = load()
+    ns, ps, ws = ctypes.c_int32(0), ctypes.c_int32(0), ctypes.c_size_t(0)
+    st = lib.attn_decode_prefix_plan(batch, max_prefix_len, max_seq_len, num_splits, prefix_splits, num_sms,
+                                     ctypes.byref(ns), ctypes.byref(ps), ctypes.byref(ws))
+    if st != ATTN_OK:
+        raise AttnDecodeError(st, attn_last_error())
+    return ns.value, ps.value, ws.value
+
+
+def attn_decode_prefix_workspace_size(batch, max_prefix_len, max_seq_len, num_splits=0, prefix_splits=0):
+    """Workspace bytes of attn_decode_global_prefix for the current CUDA device."""
+    n = load().attn_decode_prefix_workspace_size(batch, max_prefix_len, max_seq_len, num_splits, prefix_splits)
+    if n == 0:
+        raise AttnDecodeError(1, attn_last_error())
+    return n
+
+
+def _output(o, shape, out_dtype, device):
+    """o, checked, or a new output tensor."""
+    if o is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        return torch.empty(shape, dtype=out_dtype, device=device)
+    if not isinstance(o, torch.Tensor) or o.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("o must be a torch.bfloat16 or torch.float32 tensor")
+    return o
+
+
+def _prefix_args(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o=None, *, max_prefix_len=None,
+                 max_seq_len=None, out_dtype=torch.bfloat16, num_splits=0, prefix_splits=0, workspace=None,
+                 status=None):
+    Hq, Hkv, D = SHAPES[KIND_GLOBAL]
+    _dims(q, 3, "q must be [batch, %d, %d]" % (Hq, D))
+    _dims(k_pool, 4, "k_pool must be [num_pages, 16, %d, %d]" % (Hkv, D))
+    _dims(prefix_table, 1, "prefix_table must be [prefix_blocks]")
+    _dims(block_table, 2, "block_table must be [batch, max_blocks]")
+    (batch, max_blocks), n, blocks = block_table.shape, k_pool.shape[0], prefix_table.shape[0]
+    ptrs = [_ptr(q, "q", torch.bfloat16, (batch, Hq, D)),
+            _ptr(k_pool, "k_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D)),
+            _ptr(v_pool, "v_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D)),
+            _ptr(prefix_table, "prefix_table", torch.int32, (blocks,)),
+            _ptr(prefix_len, "prefix_len", torch.int32, (1,)),
+            _ptr(block_table, "block_table", torch.int32, (batch, max_blocks)),
+            _ptr(seq_lens, "seq_lens", torch.int32, (batch,))]
+    o = _output(o, (batch, Hq, D), out_dtype, q.device)
+    ptrs.append(_ptr(o, "o", o.dtype, (batch, Hq, D)))
+    device = _one_device((q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o, workspace, status))
+    if max_prefix_len is None:
+        max_prefix_len = min(blocks * PAGE_SIZE, 262144)
+    if max_seq_len is None:
+        max_seq_len = min(max_blocks * PAGE_SIZE, 262144)
+    if workspace is None:
+        with torch.cuda.device(device):
+            workspace = new_workspace(attn_decode_prefix_workspace_size(batch, max_prefix_len, max_seq_len, num_splits,
+                                                                        prefix_splits), device)
+    keep = (q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o, workspace, status)
+    args = tuple(ptrs) + (batch, blocks, max_blocks, n, int(max_prefix_len), int(max_seq_len),
+                          OUT_F32 if o.dtype == torch.float32 else OUT_BF16, int(num_splits), int(prefix_splits),
+                          _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _status_ptr(status))
+    return "attn_decode_global_prefix", args, keep, o, device
 
 
 def _once(stream, prepared):
@@ -859,6 +933,24 @@ def attn_decode_global_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq
     return _once(stream, _decode_fp8_args(KIND_GLOBAL, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o,
                                           window=window, max_seq_len=max_seq_len, out_dtype=out_dtype,
                                           num_splits=num_splits, workspace=workspace, status=status))
+
+
+def attn_decode_global_prefix(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o=None, *,
+                              max_prefix_len=None, max_seq_len=None, out_dtype=torch.bfloat16, num_splits=0,
+                              prefix_splits=0, workspace=None, status=None, stream=None):
+    """attn_decode_global for a batch behind one shared prefix: prefix_table int32 [prefix_blocks] and prefix_len int32
+    [1] name its positions, block_table and seq_lens each sequence's own (0 allowed) behind it; all pages in the same
+    pools.  max_prefix_len, max_seq_len: host bounds for the plan (default: what the tables hold).  workspace: at least
+    attn_decode_prefix_workspace_size(...) bytes from new_workspace; allocated per call when None."""
+    return _once(stream, _prefix_args(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o,
+                                      max_prefix_len=max_prefix_len, max_seq_len=max_seq_len, out_dtype=out_dtype,
+                                      num_splits=num_splits, prefix_splits=prefix_splits, workspace=workspace,
+                                      status=status))
+
+
+def prepare_decode_global_prefix(*args, **kw):
+    """PreparedCall for attn_decode_global_prefix (same arguments, minus the stream)."""
+    return PreparedCall(*_prefix_args(*args, **kw))
 
 
 def prepare_kv_append_sliding_chunk(*args, **kw):

@@ -129,7 +129,9 @@ __device__ __forceinline__ int s_kstep_dim(int w, int ks) {
   }
 }
 
-template <bool kShared>
+// kPartial: every segment is left as a partial, a whole sequence's too, for a
+// caller that merges it with others (prefix.cuh).
+template <bool kShared, bool kPartial = false>
 __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const DecodeParams& p,
                                             const KeyRebuild* kr) {
   extern __shared__ uint8_t smem_raw[];
@@ -731,7 +733,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
           lt[rr] = l[rr] + __shfl_xor_sync(0xffffffffu, l[rr], 1);
           lt[rr] += __shfl_xor_sync(0xffffffffu, lt[rr], 2);
         }
-        if (cur.whole(t, sp)) {
+        if (!kPartial && cur.whole(t, sp)) {
           const size_t row0 = static_cast<size_t>(cur.b) * kHq + g;
           const float inv0 = lt[0] > 0.f ? 1.f / lt[0] : 0.f;
           const float inv1 = lt[1] > 0.f ? 1.f / lt[1] : 0.f;
@@ -767,6 +769,13 @@ __global__ void __launch_bounds__(kThreads)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ DecodeParams p) {
   decode_body<false>(&tm_k, &tm_v, p, nullptr);
+}
+
+// The same, with every segment left as a partial.
+__global__ void __launch_bounds__(kThreads)
+    decode_kernel_partial(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ DecodeParams p) {
+  decode_body<false, true>(&tm_k, &tm_v, p, nullptr);
 }
 
 // Values-only cache: p.v_pool holds V; keys are rebuilt as rope(V * w_k).

@@ -36,12 +36,37 @@
 // bounded.
 #pragma once
 
+#include <type_traits>
+
 #include "prefill_tc.cuh"
 
 namespace pda {
 namespace prefill_pair {
 
 using prefill_tc::PrefillParams;
+
+// The shared prefix of a decode batch (prefix.cuh) as the same computation:
+// the batch's sequences are the queries (q [batch, 16, D] is already their
+// packed layout), every one sees every key of the prefix, the keys are cut
+// into spans of whole steps (blockIdx.z), and each span leaves a partial
+// result instead of o.
+struct PrefixParams : PrefillParams {  // block_table, max_blocks: the prefix's; seq_lens: its length, one int32
+  float* part_o;    // [splits, batch, Hq, D]: unnormalised outputs
+  float2* part_ml;  // [splits, kSlices, batch, Hq]: (reference max in log2 units, sum)
+  int32_t splits;   // spans the keys are cut into, at most
+};
+
+// The prefix's clamped length and its pages per span, the same in every kernel that asks.
+struct PrefixSpans {
+  int len, pages, per, used;
+  __device__ __forceinline__ PrefixSpans(int raw, int max_blocks, int splits, int step_pages) {
+    const int cap = max_blocks < ATTN_MAX_SEQ_LEN / kPage ? max_blocks * kPage : ATTN_MAX_SEQ_LEN;
+    len = raw < 0 ? 0 : raw < cap ? raw : cap;
+    pages = (len + kPage - 1) / kPage;
+    per = ((pages + splits - 1) / splits + step_pages - 1) / step_pages * step_pages;
+    used = pages > 0 ? (pages + per - 1) / per : 0;
+  }
+};
 
 template <int kD_, int kDS_, int kG_, int kHkv_, int kStages_, int kSoftmaxGroups_, int kRotate_, int kSBufs_ = 2,
           int kPBufs_ = 2, int kSIssuers_ = 1, int kPPS_ = 2>
@@ -133,10 +158,11 @@ struct PairConfig {
   static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM within the 227 KB a CTA may have");
 };
 
-template <typename C>
+template <typename C, typename Params = PrefillParams>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::kThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                        const __grid_constant__ PrefillParams p) {
+                        const __grid_constant__ Params p) {
+  constexpr bool kPrefix = std::is_same<Params, PrefixParams>::value;
   using prefill_tc::kSlack;
   using prefill_tc::kHeadroom;
   using prefill_tc::kRoundTrip;
@@ -194,14 +220,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::kThreads, 1)
   allow_dependent_launch();
 
   // ---- the pair's queries and the keys they can see (uniform over the pair) ----
-  const int q0 = p.cu_q[b];
-  const int n = p.cu_q[b + 1] - q0;
+  int q0 = 0, n = 0, L = 0;
+  if constexpr (!kPrefix) {
+    q0 = p.cu_q[b];
+    n = p.cu_q[b + 1] - q0;
+    L = p.seq_lens[b];
+  }
   const int i0p = pair * 2 * kQ;  // the pair's first query
   const int i0 = tile * kQ;       // this CTA's first query
-  const int L = p.seq_lens[b];
   const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
   bool run = true;
-  if (n < 0 || q0 < 0 || static_cast<int64_t>(q0) + n > p.total_q) {
+  int span0 = 0, span1 = 0;  // prefix: this span's pages
+  if constexpr (kPrefix) {
+    const int raw = p.seq_lens[0];
+    if ((raw < 0 || raw > cap) && blockIdx.x == 0 && blockIdx.y == 0 && b == 0 && threadIdx.x == 0)
+      report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+    const PrefixSpans ps(raw, p.max_blocks, p.splits, kPPS);
+    n = p.total_q;
+    L = ps.len;
+    span0 = b * ps.per;
+    span1 = span0 + ps.per < ps.pages ? span0 + ps.per : ps.pages;
+    run = i0p < n && span0 < span1;
+  } else if (n < 0 || q0 < 0 || static_cast<int64_t>(q0) + n > p.total_q) {
     if (threadIdx.x == 0 && rank == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
     run = false;
   } else {
@@ -216,13 +256,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::kThreads, 1)
   }
 
   if (run) {
-    const int n_run = n < p.max_q ? n : p.max_q;                  // queries computed
+    const int n_run = kPrefix || n < p.max_q ? n : p.max_q;       // queries computed
     const int nqp = n_run - i0p < 2 * kQ ? n_run - i0p : 2 * kQ;  // valid queries of the pair
     const int nq = n_run - i0 < 0 ? 0 : (n_run - i0 < kQ ? n_run - i0 : kQ);  // of this CTA
     const int P0p = L - n + i0p;   // position of the pair's first query
     const int P0 = L - n + i0;     // of this CTA's first query
-    const int k_hi = P0p + nqp - 1;  // last key the pair sees (inclusive)
-    const int k_lo = p.window > 0 ? (P0p - p.window + 1 > 0 ? P0p - p.window + 1 : 0) : 0;
+    // last and first key the pair sees (inclusive)
+    const int k_hi = kPrefix ? (span1 * kPage < L ? span1 * kPage : L) - 1 : P0p + nqp - 1;
+    const int k_lo = kPrefix ? span0 * kPage
+                             : p.window > 0 ? (P0p - p.window + 1 > 0 ? P0p - p.window + 1 : 0) : 0;
     const int page0 = k_lo / kPage;
     const int n_pages = k_hi / kPage - page0 + 1;
     const int n_steps = (n_pages + kPPS - 1) / kPPS;
@@ -239,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::kThreads, 1)
       const bool is_k = warp == 4;
       uint64_t* const full = is_k ? s.k_full : s.v_full;
       uint64_t* const empty = is_k ? s.k_empty : s.v_empty;
-      const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
+      const int32_t* bt = p.block_table + (kPrefix ? 0 : static_cast<int64_t>(b) * p.max_blocks);
       bool ok = true;
       int issued = 0;
       const auto entry = [&](int gp) {
@@ -414,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::kThreads, 1)
       const int qi = r % kQ;
       const bool valid = qi < nq;
       const int head = c * kG + g;
-      const int pos = P0 + qi;
+      const int pos = kPrefix ? k_hi : P0 + qi;
       const int lo_r = p.window > 0 ? pos - p.window + 1 : 0;
       const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 
@@ -558,6 +600,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::kThreads, 1)
         named_barrier_sync(1, C::kSoftmaxThreads);
         l += s.half_sum[1 - h][r];
       }
+      if constexpr (kPrefix) {
+        // unnormalised, with its reference max and sum
+        const size_t row = (static_cast<size_t>(b) * n + i0 + qi) * kHq + head;
+        if (valid && h == 0)
+          p.part_ml[((static_cast<size_t>(b) * C::kSlices + slice) * n + i0 + qi) * kHq + head] = make_float2(m, l);
+#pragma unroll 1
+        for (int col0 = oc0; col0 < oc0 + kOCols; col0 += 16 * kRoundTrip) {
+          float ovs[kRoundTrip][16];
+#pragma unroll
+          for (int u = 0; u < kRoundTrip; ++u) tmem_ld16(t_row + col0 + 16 * u, ovs[u]);
+          tmem_wait_ld();
+          if (!valid) continue;
+          float4* dst = reinterpret_cast<float4*>(p.part_o + row * kD + slice * kDS + col0);
+#pragma unroll
+          for (int u = 0; u < kRoundTrip; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[4 * u + k] = make_float4(ovs[u][4 * k], ovs[u][4 * k + 1], ovs[u][4 * k + 2], ovs[u][4 * k + 3]);
+        }
+      } else {
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const size_t o_off = (static_cast<size_t>(q0 + i0 + qi) * kHq + head) * kD + slice * kDS;
 #pragma unroll 1
@@ -584,6 +646,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C::kThreads, 1)
                                 pack_bf16x2(ov[12] * inv, ov[13] * inv), pack_bf16x2(ov[14] * inv, ov[15] * inv));
           }
         }
+      }
       }
     }
   }

@@ -1,5 +1,5 @@
 // serving.cuh -- host side of the chunk appends, the 8-bit cache
-// (include/attn_fp8.h) and their launches.  Included in attn_decode.cu, whose
+// (include/attn_fp8.h) and the decode behind a shared prefix.  Included in attn_decode.cu, whose
 // validation helpers, plan, tensor-map encoder and launch recording it shares.
 #pragma once
 
@@ -7,6 +7,7 @@
 #include "fp8_read.cuh"
 #include "global_fp8.cuh"
 #include "kv_chunk.cuh"
+#include "prefix.cuh"
 #include "sliding_fp8.cuh"
 
 namespace {
@@ -307,9 +308,188 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
   return launched(name, e);
 }
 
+// ---------------------------------------------------------------------------
+// Decode behind a prefix that the batch shares
+// ---------------------------------------------------------------------------
+using PrefixConfig = pda::prefill_pair::GlobalPairConfig;
+constexpr int kMaxPrefixSplits = 128;
+constexpr int kPrefixMinSteps = 4;  // steps of 64 keys a span is given at least
+
+struct PrefixPlan {
+  Plan own;           // the own positions' decode
+  int splits;         // spans of the prefix
+  size_t part_o_off, part_ml_off, workspace_bytes;
+};
+
+int32_t make_prefix_plan(int32_t batch, int32_t max_prefix_len, int32_t max_seq_len, int32_t num_splits,
+                         int32_t prefix_splits, int32_t num_sms, PrefixPlan* out) {
+  const int32_t st = make_plan(ATTN_KIND_GLOBAL, batch, max_seq_len, 0, num_splits, num_sms, &out->own);
+  if (st != ATTN_OK) return st;
+  if (max_prefix_len < 0) return fail(ATTN_ERR_INVALID_ARG, "max_prefix_len must be >= 0");
+  if (prefix_splits < 0) return fail(ATTN_ERR_INVALID_ARG, "prefix_splits must be >= 0");
+  // One CTA pair per SM pair: 2 query tiles (of kQ sequences each) and one
+  // slice of the output dims per cluster, the rest of the GPU by spans.
+  const int64_t pairs = (batch + 2 * PrefixConfig::kQ - 1) / (2 * PrefixConfig::kQ) * PrefixConfig::kSlices;
+  const int64_t steps = (static_cast<int64_t>(max_prefix_len) + PrefixConfig::kKeys - 1) / PrefixConfig::kKeys;
+  int64_t splits = prefix_splits;
+  if (splits == 0) {
+    splits = num_sms / 2 / pairs;
+    if (splits > steps / kPrefixMinSteps) splits = steps / kPrefixMinSteps;
+  }
+  out->splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(splits, kMaxPrefixSplits)));
+  const size_t rows = static_cast<size_t>(out->splits) * batch * ATTN_GLOBAL_HQ;
+  out->part_o_off = out->own.workspace_bytes;
+  out->part_ml_off = out->part_o_off + align256(rows * ATTN_GLOBAL_D * sizeof(float));
+  out->workspace_bytes = out->part_ml_off + align256(rows * PrefixConfig::kSlices * sizeof(float2));
+  return ATTN_OK;
+}
+
+int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+                   const int32_t* prefix_len, const int32_t* block_table, const int32_t* seq_lens, void* o,
+                   int32_t batch, int32_t prefix_blocks, int32_t max_blocks, int64_t num_pages, int32_t max_prefix_len,
+                   int32_t max_seq_len, int32_t out_dtype, int32_t num_splits, int32_t prefix_splits, void* workspace,
+                   size_t workspace_bytes, int32_t* status, void* stream) {
+  g_err[0] = '\0';
+  const char* name = "attn_decode_global_prefix";
+  if (!q || !k_pool || !v_pool || !prefix_table || !prefix_len || !block_table || !seq_lens || !o)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: null array pointer", name);
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(block_table) || !aligned16(seq_lens) ||
+      !aligned16(o) || !aligned_to(prefix_table, 4) || !aligned_to(prefix_len, 4) || !aligned_to(status, 4))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: misaligned pointer (arrays 16 bytes; prefix_table, prefix_len, status 4)",
+                name);
+  int32_t st;
+  if ((st = check_batch(name, batch, max_blocks)) || (st = check_pages(name, "num_pages", num_pages)) ||
+      (st = check_max_seq_len(name, max_seq_len, max_blocks)))
+    return st;
+  if (prefix_blocks < 1) return fail(ATTN_ERR_INVALID_ARG, "%s: prefix_blocks must be >= 1", name);
+  if (max_prefix_len < 0 || static_cast<int64_t>(max_prefix_len) > static_cast<int64_t>(prefix_blocks) * ATTN_PAGE_SIZE)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: max_prefix_len %d not in [0, prefix_blocks*16 = %lld]", name, max_prefix_len,
+                static_cast<long long>(prefix_blocks) * ATTN_PAGE_SIZE);
+  if (max_prefix_len > ATTN_MAX_SEQ_LEN)
+    return fail(ATTN_ERR_UNSUPPORTED, "%s: max_prefix_len %d beyond the model's domain (%d)", name, max_prefix_len,
+                ATTN_MAX_SEQ_LEN);
+  if (out_dtype != ATTN_OUT_BF16 && out_dtype != ATTN_OUT_F32)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: out_dtype must be ATTN_OUT_BF16 or ATTN_OUT_F32", name);
+  if (num_splits < 0 || prefix_splits < 0)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: num_splits and prefix_splits must be >= 0", name);
+  int dev = 0, num_sms = 0;
+  if ((st = current_device(&dev, &num_sms)) != ATTN_OK) return st;
+  PrefixPlan plan;
+  st = make_prefix_plan(batch, max_prefix_len, max_seq_len, num_splits, prefix_splits, num_sms, &plan);
+  if (st != ATTN_OK) return st;
+  if (!workspace || workspace_bytes < plan.workspace_bytes)
+    return fail(ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)", name, plan.workspace_bytes,
+                workspace ? workspace_bytes : size_t{0});
+  if (!aligned16(workspace)) return fail(ATTN_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", name);
+  g_last_launches = 3;
+  if (g_validate_only) return ATTN_OK;
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  pda::prefill_pair::PrefixParams pp{};
+  pp.q = static_cast<const __nv_bfloat16*>(q);
+  pp.block_table = prefix_table;
+  pp.seq_lens = prefix_len;
+  pp.status = status;
+  pp.num_pages = num_pages;
+  pp.batch = 1;
+  pp.max_blocks = prefix_blocks;
+  pp.total_q = batch;
+  pp.max_q = batch;
+  pp.part_o = reinterpret_cast<float*>(ws + plan.part_o_off);
+  pp.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml_off);
+  pp.splits = plan.splits;
+
+  pda::prefix::MergeParams mp{};
+  pda::DecodeParams& p = mp.d;
+  p.q = pp.q;
+  p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
+  p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.o = o;
+  p.counters = static_cast<int32_t*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws + ATTN_WORKSPACE_ZERO_BYTES);
+  p.part_ml = reinterpret_cast<float2*>(ws + ATTN_WORKSPACE_ZERO_BYTES + plan.own.part_o_bytes);
+  p.status = status;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.max_blocks = max_blocks;
+  p.grid_x = plan.own.grid_x;
+  p.min_pages = plan.own.min_pages;
+  p.out_f32 = out_dtype == ATTN_OUT_F32;
+  p.part_rows = (static_cast<int64_t>(plan.own.grid_x) + batch) * ATTN_GLOBAL_HQ;
+  mp.part_o = pp.part_o;
+  mp.part_ml = pp.part_ml;
+  mp.prefix_len = prefix_len;
+  mp.prefix_blocks = prefix_blocks;
+  mp.splits = plan.splits;
+
+  using C = PrefixConfig;
+  const auto prefix_kernel = pda::prefill_pair::prefill_pair_kernel<C, pda::prefill_pair::PrefixParams>;
+  const auto merge_kernel = pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS>;
+  static bool pre_set[kMaxDevices] = {false}, dec_set[kMaxDevices] = {false}, merge_set[kMaxDevices] = {false};
+  if ((st = ensure_smem(prefix_kernel, C::kSmemBytes, dev, pre_set)) ||
+      (st = ensure_smem(pda::global::decode_kernel_partial, pda::global::kSmemBytes, dev, dec_set)) ||
+      (st = ensure_smem(merge_kernel, 0, dev, merge_set)))
+    return st;
+  CUtensorMap tm_pk, tm_pv, tm_k, tm_v;
+  if ((st = encode_chunk_map(&tm_pk, k_pool, num_pages, C::kHkv * C::kD, C::kKBoxChunks)) ||
+      (st = encode_chunk_map(&tm_pv, v_pool, num_pages, C::kHkv * C::kD, C::kDS / 128)) ||
+      (st = encode_global_page_map(&tm_k, k_pool, num_pages)) ||
+      (st = encode_global_page_map(&tm_v, v_pool, num_pages)))
+    return st;
+  int tiles = (batch + C::kQ - 1) / C::kQ;
+  tiles += tiles & 1;  // whole clusters of two query tiles
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pdl(prefix_kernel, dim3(tiles, C::kHkv * C::kSlices, plan.splits), C::kThreads, C::kSmemBytes, s,
+                             tm_pk, tm_pv, pp);
+  if (e == cudaSuccess)
+    e = launch_pdl(pda::global::decode_kernel_partial, dim3(plan.own.grid_x), pda::global::kThreads,
+                   pda::global::kSmemBytes, s, tm_k, tm_v, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(merge_kernel, dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / pda::kCombineCols), batch),
+                   pda::kCombineWarps * 32, 0, s, mp);
+  return launched(name, e);
+}
+
 }  // namespace
 
 extern "C" {
+
+int32_t attn_decode_global_prefix(const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+                                  const int32_t* prefix_len, const int32_t* block_table, const int32_t* seq_lens,
+                                  void* o, int32_t batch, int32_t prefix_blocks, int32_t max_blocks, int64_t num_pages,
+                                  int32_t max_prefix_len, int32_t max_seq_len, int32_t out_dtype, int32_t num_splits,
+                                  int32_t prefix_splits, void* workspace, size_t workspace_bytes, int32_t* status,
+                                  void* stream) {
+  return run_prefix(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o, batch, prefix_blocks,
+                    max_blocks, num_pages, max_prefix_len, max_seq_len, out_dtype, num_splits, prefix_splits, workspace,
+                    workspace_bytes, status, stream);
+}
+
+int32_t attn_decode_prefix_plan(int32_t batch, int32_t max_prefix_len, int32_t max_seq_len, int32_t num_splits,
+                                int32_t prefix_splits, int32_t num_sms, int32_t* out_num_splits,
+                                int32_t* out_prefix_splits, size_t* out_workspace_bytes) {
+  g_err[0] = '\0';
+  PrefixPlan plan;
+  const int32_t st = make_prefix_plan(batch, max_prefix_len, max_seq_len, num_splits, prefix_splits, num_sms, &plan);
+  if (st != ATTN_OK) return st;
+  if (out_num_splits) *out_num_splits = plan.own.grid_x;
+  if (out_prefix_splits) *out_prefix_splits = plan.splits;
+  if (out_workspace_bytes) *out_workspace_bytes = plan.workspace_bytes;
+  return ATTN_OK;
+}
+
+size_t attn_decode_prefix_workspace_size(int32_t batch, int32_t max_prefix_len, int32_t max_seq_len,
+                                         int32_t num_splits, int32_t prefix_splits) {
+  g_err[0] = '\0';
+  int dev = 0, num_sms = 0;
+  if (current_device(&dev, &num_sms) != ATTN_OK) return 0;
+  PrefixPlan plan;
+  if (make_prefix_plan(batch, max_prefix_len, max_seq_len, num_splits, prefix_splits, num_sms, &plan) != ATTN_OK)
+    return 0;
+  return plan.workspace_bytes;
+}
 
 int32_t attn_kv_append_sliding_chunk(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
                                      const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,

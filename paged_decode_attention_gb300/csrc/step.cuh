@@ -177,6 +177,18 @@ int32_t attn_step_add_decode_global_fp8(attn_step* step, const void* q, const vo
   }, "attn_step_add_decode_global_fp8");
 }
 
+int32_t attn_step_add_decode_global_prefix(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
+    const int32_t* prefix_table, const int32_t* prefix_len, const int32_t* block_table, const int32_t* seq_lens,
+    void* o, int32_t batch, int32_t prefix_blocks, int32_t max_blocks, int64_t num_pages, int32_t max_prefix_len,
+    int32_t max_seq_len, int32_t out_dtype, int32_t num_splits, int32_t prefix_splits, void* workspace,
+    size_t workspace_bytes, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_decode_global_prefix(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o, batch,
+        prefix_blocks, max_blocks, num_pages, max_prefix_len, max_seq_len, out_dtype, num_splits, prefix_splits,
+        workspace, workspace_bytes, status, s);
+  }, "attn_step_add_decode_global_prefix");
+}
+
 int32_t attn_step_num_calls(const attn_step* step) { return step ? static_cast<int32_t>(step->calls.size()) : 0; }
 
 int32_t attn_step_num_kernels(const attn_step* step) { return step ? step->kernels : 0; }

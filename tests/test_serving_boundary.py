@@ -1,4 +1,4 @@
-"""Refusals of the chunk appends and the 8-bit cache calls, without a GPU: error codes before anything is launched."""
+"""Refusals of the chunk appends, the 8-bit cache and the shared-prefix calls, without a GPU: error codes before anything is launched."""
 
 import ctypes
 
@@ -30,11 +30,14 @@ ARGS = {
              "out_pages", "max_seq_len", "span", "status"],
     "decode": ["q", "k", "v", "ks", "vs", "table", "lens", "o", "batch", "max_blocks", "num_pages", "max_seq_len",
                "window", "out_dtype", "num_splits", "ws", "ws_bytes", "status"],
+    "prefix": ["q", "k", "v", "prefix_table", "prefix_len", "table", "lens", "o", "batch", "prefix_blocks",
+               "max_blocks", "num_pages", "max_prefix_len", "max_seq_len", "out_dtype", "num_splits", "prefix_splits",
+               "ws", "ws_bytes", "status"],
 }
 DEFAULTS = dict(batch=4, total_q=9, max_blocks=70, num_pages=300, out_pages=200, max_seq_len=1100, span=0, window=1024,
-                out_dtype=0, num_splits=0, ws=None, ws_bytes=0, status=None)
+                out_dtype=0, num_splits=0, prefix_blocks=30, max_prefix_len=480, prefix_splits=0, ws=None, ws_bytes=0, status=None)
 NAMES = {"attn_kv_append_%s_chunk": "chunk", "attn_kv_append_%s_fp8": "fp8", "attn_kv_read_%s_fp8": "read",
-         "attn_decode_%s_fp8": "decode"}
+         "attn_decode_%s_fp8": "decode", "attn_decode_%s_prefix": "prefix"}
 
 
 def call(lib, name, form, step=None, **kw):
@@ -47,6 +50,8 @@ def call(lib, name, form, step=None, **kw):
 def bad_calls():
     for pattern, form in NAMES.items():
         for kind in ("sliding", "global"):
+            if form == "prefix" and kind == "sliding":
+                continue
             name = pattern % kind
             pointers = [a for a in ARGS[form] if a not in DEFAULTS]
             for a in pointers:
@@ -63,14 +68,20 @@ def bad_calls():
                 yield name, form, dict(total_q=-1), INVALID
             if form == "read":
                 yield name, form, dict(out_pages=0), INVALID
-            if form in ("read", "decode"):
+            if form == "prefix":
+                yield name, form, dict(prefix_blocks=0), INVALID
+                yield name, form, dict(max_prefix_len=-1), INVALID
+                yield name, form, dict(max_prefix_len=481), INVALID
+                yield name, form, dict(prefix_blocks=20000, max_prefix_len=262145), UNSUPPORTED
+                yield name, form, dict(prefix_splits=-1), INVALID
+            if form in ("read", "decode", "prefix"):
                 yield name, form, dict(max_seq_len=-1), INVALID
                 yield name, form, dict(max_seq_len=70 * 16 + 1), INVALID
                 yield name, form, dict(max_blocks=20000, max_seq_len=262145), UNSUPPORTED
-            if form == "decode":
+            if form in ("decode", "prefix"):
                 yield name, form, dict(out_dtype=2), INVALID
                 yield name, form, dict(num_splits=-1), INVALID
-                if kind == "sliding":
+                if kind == "sliding" and form == "decode":
                     yield name, form, dict(window=0), INVALID
 
 
@@ -94,6 +105,24 @@ def test_no_tokens_is_a_call_without_a_launch(lib, kind):
         assert call(lib, "attn_kv_append_%s_%s" % (kind, suffix), form, total_q=0, qkv=None, q_out=None) == 0
 
 
+def test_prefix_plan(lib):
+    # 64 sequences: 4 pairs of query tiles x 2 slices = 8 clusters, 76 SM pairs -> 9 spans
+    ns, ps, ws = pda.attn_decode_prefix_plan(64, 32768, 2048)
+    own, own_ws = pda.attn_decode_plan(pda.KIND_GLOBAL, 64, 2048, 0)
+    rows = ps * 64 * 16
+    assert (ns, ps) == (own, 9) and ws == own_ws + rows * 512 * 4 + rows * 2 * 8
+    # a short prefix is cut into spans of no less than four steps of 64 keys; one span at least
+    assert pda.attn_decode_prefix_plan(1, 1024, 16)[1] == 4
+    assert pda.attn_decode_prefix_plan(1, 100, 16)[1] == 1
+    assert pda.attn_decode_prefix_plan(1, 0, 0)[1] == 1
+    assert pda.attn_decode_prefix_plan(256, 262144, 16)[1] == 2
+    assert pda.attn_decode_prefix_plan(8, 262144, 16, prefix_splits=7)[1] == 7
+    assert pda.attn_decode_prefix_plan(8, 262144, 16, prefix_splits=5000)[1] == 128
+    for bad in ((0, 16, 16), (1, -1, 16), (1, 16, -1), (1, 16, 16, -1), (1, 16, 16, 0, -1), (1, 16, 16, 0, 0, 0)):
+        with pytest.raises(pda.AttnDecodeError):
+            pda.attn_decode_prefix_plan(*bad)
+
+
 @pytest.mark.parametrize("kind", ["sliding", "global"])
 def test_binding_refuses_cpu_tensors(lib, kind):
     k = getattr(pda, "KIND_" + kind.upper())
@@ -113,6 +142,9 @@ def test_binding_refuses_cpu_tensors(lib, kind):
                                                        i32(2), *pools)
     with pytest.raises(ValueError, match="CUDA"):
         getattr(pda, "attn_kv_read_%s_fp8" % kind)(*cache, i32(1, 1), i32(1), *pools)
+    if kind == "global":
+        with pytest.raises(ValueError, match="CUDA"):
+            pda.attn_decode_global_prefix(bf(1, Hq, D), *pools, i32(1), i32(1), i32(1, 1), i32(1))
     step = pda.Step()
     with pytest.raises(ValueError, match="CUDA"):
         getattr(step, "add_decode_%s_fp8" % kind)(bf(1, Hq, D), *cache, i32(1, 1), i32(1))
