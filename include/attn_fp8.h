@@ -12,7 +12,8 @@
  *   k_pool, v_pool    e4m3 [num_pages, 16, Hkv, D]: sign, 4 exponent bits
  *                     (bias 7), 3 mantissa bits; largest 448, no infinity
  *   k_scale, v_scale  E8M0 [num_pages, Hkv, 16]: one byte s per position and
- *                     KV head, standing for 2^(s - 127); 255 is NaN
+ *                     KV head, standing for 2^(s - 127); 255 is NaN, and 0
+ *                     (which no append writes: a cleared page) reads as zero
  * Position l of sequence b, KV head c, page P = block_table[b][l / 16], row
  * r = l % 16 holds  k[i] = e4m3(k_pool[P][r][c][i]) * 2^(k_scale[P][c][r] - 127),
  * and v alike.

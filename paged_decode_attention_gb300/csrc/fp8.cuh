@@ -3,7 +3,8 @@
 //
 // A row y[0..D) (the key or the value of one head at one position) is stored
 // as bytes c_i and one scale byte s with
-//   y_i ~ e4m3(c_i) * 2^(s - 127).
+//   y_i ~ e4m3(c_i) * 2^(s - 127);
+// s = 255 reads as NaN, s = 0 (no append writes it: a cleared page) as zero.
 // The writer takes the smallest k with max|y| <= 448 * 2^k (448 is the
 // largest e4m3 value) and s = k + 127, clamped to [1, 254], and rounds
 // y_i * 2^-k to e4m3 once, to nearest even.  Multiplying by a power of two is
@@ -43,9 +44,9 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax, float& inv) {
   return static_cast<uint32_t>(k + 127);
 }
 
-// 2^(s - 127); 255 gives NaN.
+// 2^(s - 127); 255 gives NaN, 0 gives 0.
 __device__ __forceinline__ float scale_value(uint32_t s) {
-  return s == kNanScale ? __uint_as_float(0x7fc00000u) : __uint_as_float(s == 0 ? 0x00400000u : s << 23);
+  return s == kNanScale ? __uint_as_float(0x7fc00000u) : __uint_as_float(s << 23);
 }
 
 // Four fp32 -> four e4m3 bytes, first value lowest (nearest even, saturating).
@@ -70,7 +71,11 @@ __device__ __forceinline__ uint32_t hi_f16x2(uint32_t w) { return e4m3x2_to_f16x
 // e4m3 values widen to f16 exactly, so both contractions run as
 // mma.m16n8k16 f16 -> fp32 on unscaled values, with the power-of-two scales
 // applied exactly in fp32 outside the products: a key's to its logits, a
-// value's to its weight.
+// value's to its weight.  (mma.m16n8k32 on the bytes themselves is no way
+// around the conversion: with q and the weights split into e4m3 terms it is
+// right, but it executed 1049 instructions per page and head against 845, and
+// the f16 tensor pipe was active four times as long as 24 such MMAs would
+// need at the rate of their constant-operand loop: 5.2 -> 3.8 TB/s.)
 //
 // q is bf16, whose range f16 has not: each q row is multiplied by 2^-k with
 // 2^14 <= max|q| 2^-k < 2^15 (exact), rounded to f16 and the 2^k goes to the
@@ -85,17 +90,30 @@ __device__ __forceinline__ uint32_t hi_f16x2(uint32_t w) { return e4m3x2_to_f16x
 //     w_l = 2^{(x_l - m) + kv_l - R + 15}  <=  2^15,
 // so the largest lies in (2^14, 2^15], and in the usual case that the largest
 // p has the largest scale it is a power of two, exact in f16.  A weight is
-// rounded by 2^-11 at most, down to 2^-29 of the largest, and below never by
-// more than 2^-40 of it: 262,144 weights rounded to nothing lose 2^-22.  With
+// rounded by 2^-11 at most, down to 2^-28 of the largest, and below never by
+// more than 2^-39 of it: 262,144 weights rounded to nothing lose 2^-21.  With
 // one reference per page for the scales alone, a large scale on a row of no
 // weight would take the bits of the others.  Accumulators hold 2^{15 - R}
 // times the output sum relative to m and follow both references.
+//
+// Fragments.  A cache row's bytes are read 16 at a time: lane (g, t) = (lane/4,
+// lane%4) takes unit 2t + j of a 128-byte chunk (even and odd units make the
+// 128-byte swizzle conflict free), 16 dims that it contracts with the same
+// dims of q, so their order does not matter.  The positions of a page are
+// dealt to the N (or M) index of the first product so that position 4t + i is
+// where a transposing byte load (ldmatrix .b8) of the value page puts it in
+// the second: index n of the first half is row 4 (n/2) + n%2, of the second
+// half two rows below.
 // ---------------------------------------------------------------------------
 constexpr int kWeightBias = 15;  // weights are at most 2^15 in f16 (largest finite 65504)
 
-// log2 of a scale: s - 127, NaN for 255.
+// Page row of index n (0..7) of the first half; the second half's is 2 below.
+__device__ __forceinline__ int dealt_row(int n) { return 4 * (n >> 1) + (n & 1); }
+
+// log2 of a scale: s - 127, NaN for 255, -inf for 0.
 __device__ __forceinline__ float scale_log2(uint32_t s) {
-  return s == kNanScale ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(s) - 127);
+  const float f = s == 0 ? -INFINITY : static_cast<float>(static_cast<int>(s) - 127);
+  return s == kNanScale ? __uint_as_float(0x7fc00000u) : f;
 }
 
 // The references of one query row, moved by the maxima mx of x and mt of
@@ -154,7 +172,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // D = A(16x16, row) * B(16x8, col) + D, f16 inputs, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -165,17 +183,26 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
 // (row lane / 4, columns 2 (lane % 4), +1).
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t r) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(r));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(r));
   return d;
 }
 
-// A word of ldmatrix.trans over e4m3 rows holds, for two rows, the two bytes
-// of one dim pair: bytes {row 0: d, d + 1; row 1: d, d + 1}.  -> f16x2 of
-// (row 0, row 1) for dim d and for dim d + 1.
-__device__ __forceinline__ void split_pair(uint32_t w, uint32_t& even, uint32_t& odd) {
-  const uint32_t u = __byte_perm(w, 0, 0x3120);
-  even = lo_f16x2(u);
-  odd = hi_f16x2(u);
+// Two 16x16 byte matrices (row addresses from lanes 0..15 and 16..31),
+// transposed: lane (g = lane/4, t = lane%4) gets, of each, rows 4t .. 4t + 3 of
+// column g and of column g + 8, one byte each.
+__device__ __forceinline__ void ldmatrix_b8_x2_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+// The dynamic shared memory rounded up to 1024 bytes.  By adding an offset to
+// the array itself, so that accesses compile to shared-memory instructions: a
+// pointer rounded as an integer is generic (with this, and the MMAs free to be
+// scheduled, 16 global contexts of 131072 went from 443 to 410 us).
+template <typename S>
+__device__ __forceinline__ S& aligned_smem(uint8_t* raw) {
+  return *reinterpret_cast<S*>(raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u));
 }
 
 // byte offset of 16-byte unit `unit` of row `row` in a 128B-swizzled [16][128 B] tile

@@ -16,14 +16,11 @@
 // So each byte is widened once, the softmax runs once per page, and two
 // barriers serve four pages.
 //
-// Tiles: 128 dims of a page are [16 rows][128 bytes] with the 128-byte
-// swizzle; the fragment order is sliding_fp8.cuh's with the cache as the B
-// operand: K: lane (g, tq) reads rows g and g + 8 at unit 2 tq + j; V: the
-// n-tiles of a 16-dim block are its even and its odd dims.
 #pragma once
 
 #include "fp8.cuh"
 #include "global.cuh"
+#include "tcgen05.cuh"
 
 namespace pda {
 namespace global_fp8 {
@@ -67,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
                   const __grid_constant__ DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
-  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem& s = fp8::aligned_smem<Smem>(smem_raw);
 
   const int gb = blockIdx.x;
   const int warp = threadIdx.x >> 5;
@@ -123,8 +120,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   // ---------------- consumers ----------------
   const int g = lane >> 2;  // fragment row: query heads g and g + 8
   const int tq = lane & 3;
-  const int mi = lane >> 3;  // ldmatrix: which 8x8 matrix this lane addresses
-  const int lr = lane & 7;
   constexpr int kConsumers = kConsumerWarps * 32;
 
   PageCursor cur;
@@ -185,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 
   fp8::Reference ref[2];  // rows g, g + 8 (the same in every warp)
   float l[2];             // this lane's share of the sums
-  float acc[16][4];  // per 16-dim block: even dims (n-tile 2n), odd dims (2n + 1)
+  float acc[16][4];  // 16 n-tiles of 8 dims
   auto reset = [&]() {
     ref[0].reset();
     ref[1].reset();
@@ -199,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   bool ok = true;
   auto wait_page = [&](int i) {
     if (ok) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&s.full[i % kStages], (i / kStages) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.full[i % kStages], (i / kStages) & 1));
       if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
     }
   };
@@ -214,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int n = min(kConsumerWarps, cur.seg_end - f);  // pages of this group
     const int gpos0 = cur.pos0(t, f);                    // position of its first row
 
-    // ---- logits of page w: x[nt][e]: head g + 8 (e >> 1), position pos0 + 8 nt + 2 tq + (e & 1) ----
+    // ---- logits of page w: x[nt][e]: head g + 8 (e >> 1), position pos0 + 4 tq + 2 nt + (e & 1) ----
     float x[2][4];
     float kv[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // log2 of those positions' value scales
 #pragma unroll
@@ -225,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       wait_page(i + warp);
       const int st = (i + warp) % kStages;
       const int pos0 = gpos0 + warp * kPage;
-      const uint32_t kst = smem_addr(s.k[st]);
+      const uint8_t* kst = s.k[st];
       float sc[2][2][4];  // n-tile, even / odd k-steps
 #pragma unroll
       for (int a = 0; a < 2; ++a)
@@ -235,9 +230,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           for (int e = 0; e < 4; ++e) sc[a][b][e] = 0.f;
 #pragma unroll 2
       for (int k = 0; k < kChunks * 2; ++k) {  // chunk, j
-        const uint32_t base = kst + (k >> 1) * fp8::kChunkBytes;
-        const uint4 a = ld_shared_v4(base + fp8::swz(g, 2 * tq + (k & 1)));
-        const uint4 b = ld_shared_v4(base + fp8::swz(g + 8, 2 * tq + (k & 1)));
+        const uint8_t* base = kst + (k >> 1) * fp8::kChunkBytes;
+        const uint4 a = *reinterpret_cast<const uint4*>(base + fp8::swz(fp8::dealt_row(g), 2 * tq + (k & 1)));
+        const uint4 b = *reinterpret_cast<const uint4*>(base + fp8::swz(fp8::dealt_row(g) + 2, 2 * tq + (k & 1)));
         const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -251,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int r = 8 * nt + 2 * tq + u;
+          const int r = 4 * tq + 2 * nt + u;
           const float kf = fp8::scale_value(s.k_scale[st][r]);
           const bool in = !edge || (pos0 + r >= cur.lo && pos0 + r < cur.L);
           if (in) {
@@ -332,18 +327,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         __syncwarp();
       }
       const uint4 pa = s.pfrag[j][lane];
+      const uint32_t vrow = vst + (lane & 15) * 128;
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {  // 32 dims each
+      for (int np = 0; np < 4; ++np) {  // 32 dims each: lanes 0..15 address the first 16, lanes 16..31 the others
         uint32_t r[4];
-        ldmatrix_x4_trans(vst + fp8::swz(((mi & 1) << 3) + lr, 2 * np + (mi >> 1)), r[0], r[1], r[2], r[3]);
+        fp8::ldmatrix_b8_x2_trans(vrow + (((2 * np + (lane >> 4)) ^ (lane & 7)) << 4), r);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t e0, o0, e1, o1;
-          fp8::split_pair(r[2 * u], e0, o0);
-          fp8::split_pair(r[2 * u + 1], e1, o1);
-          fp8::mma_f16_16816(acc[4 * np + 2 * u], pa.x, pa.y, pa.z, pa.w, e0, e1);
-          fp8::mma_f16_16816(acc[4 * np + 2 * u + 1], pa.x, pa.y, pa.z, pa.w, o0, o1);
-        }
+        for (int u = 0; u < 4; ++u)  // 8 dims each
+          fp8::mma_f16_16816(acc[4 * np + u], pa.x, pa.y, pa.z, pa.w, fp8::lo_f16x2(r[u]), fp8::hi_f16x2(r[u]));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.empty[st]);
@@ -375,16 +366,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           const size_t row = static_cast<size_t>(whole ? cur.b : gb + cur.b) * kHq + g + 8 * r;
           const float inv = lt[r] > 0.f ? 1.f / lt[r] : lt[r];  // 0, or a NaN that has to show
 #pragma unroll
-          for (int b = 0; b < 8; ++b) {
-            const float4 v = make_float4(fp8::unscale(acc[2 * b][2 * r], ref[r].R),
-                                         fp8::unscale(acc[2 * b + 1][2 * r], ref[r].R),
-                                         fp8::unscale(acc[2 * b][2 * r + 1], ref[r].R),
-                                         fp8::unscale(acc[2 * b + 1][2 * r + 1], ref[r].R));
-            const size_t at = row * kD + 128 * warp + 16 * b + 4 * tq;
+          for (int b = 0; b < 16; ++b) {
+            const float v0 = fp8::unscale(acc[b][2 * r], ref[r].R), v1 = fp8::unscale(acc[b][2 * r + 1], ref[r].R);
+            const size_t at = row * kD + 128 * warp + 8 * b + 2 * tq;
             if (whole)
-              store_out4(p, at, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+              store_out2(p, at, v0 * inv, v1 * inv);
             else
-              *reinterpret_cast<float4*>(p.part_o + at) = v;
+              *reinterpret_cast<float2*>(p.part_o + at) = make_float2(v0, v1);
           }
           // a NaN sum is handed on as (inf, 1): the combine skips partials whose sum is not positive
           if (!whole && warp == 0 && tq == 0)

@@ -8,9 +8,8 @@
 // memory a page has half the time.  On the CUDA cores every value would cost
 // a conversion more than in the bf16 kernel; so both products run on
 // mma.m16n8k16 with the cache as the A operand (16 positions, or 16 dims, by
-// 16) and the two query heads in B's eight columns (each four times), which costs 16
-// MMAs, 96 conversions and 16 shared-memory reads per page and product pair
-// instead of some 1300 FMA-pipe instructions.
+// 16) and the two query heads in B's eight columns, each four times over, so
+// that every lane has both heads' logits of its positions.
 //
 // Grid (grid_x, 8) and the balanced spans as in sliding.cuh.  Warp 4 copies
 // pages; each of the warps 0..3 takes every fourth page whole and keeps its
@@ -18,18 +17,14 @@
 // first page and its end, where the four are merged through shared memory
 // exactly as in sliding.cuh.
 //
-// S^T[pos, h] = K q^T: lane (g = lane/4, tq = lane%4) reads 16 consecutive
-// bytes of rows g and g + 8 at unit 2 tq + j of each 128-byte chunk; the
-// units even and odd in j make the 128-byte swizzle conflict free, and the
-// order of the dims inside the contraction is the same for q.
-// O^T[d, h] = V^T P^T: ldmatrix.trans brings pairs of dims for two rows,
-// which a byte permutation and the widening turn into A fragments with rows
-// g and g + 8 = dims 2g and 2g + 1 of 16; P^T is S^T's fragment transposed in
-// place (movmatrix).
+// S^T[pos, h] = K q^T, then O^T[d, h] = V^T P^T: the weights of a lane's two
+// positions, packed, become B fragments by one transposition in registers
+// (movmatrix), and V^T comes as A fragments from the transposing byte load.
 #pragma once
 
 #include "fp8.cuh"
 #include "sliding.cuh"
+#include "tcgen05.cuh"
 
 namespace pda {
 namespace sliding_fp8 {
@@ -43,7 +38,7 @@ constexpr int kConsumerWarps = 4;
 constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kChunks = kD / 128;                      // 2
 constexpr int kTileBytes = kPage * kD;                 // 4 KB per K (or V) page-head
-constexpr int kStages = 7;
+constexpr int kStages = 8;  // two per consumer warp: page i of the span is warp i % 4's, in stage i % 8
 constexpr int kStageTx = 2 * kTileBytes + 2 * kPage;   // K, V and their scales
 constexpr int kBlocksPerSm = sliding::kBlocksPerSm;    // the plan of the bf16 kernel
 constexpr int kWarmPages = 8;
@@ -53,10 +48,10 @@ struct Smem {
   alignas(1024) uint8_t v[kStages][kTileBytes];
   alignas(128) uint8_t k_scale[kStages][128];  // 16 bytes used: a copy lands on a 128-byte boundary
   alignas(128) uint8_t v_scale[kStages][128];
-  alignas(16) uint4 qfrag[kConsumerWarps][kChunks * 4][4 * kG];  // q B fragments, per warp
-  alignas(16) float merge_o[kConsumerWarps][kG][kD];
-  float merge_m[kConsumerWarps][kG];
-  float merge_l[kConsumerWarps][kG];
+  alignas(16) uint4 qfrag[kChunks * 4][4 * kG];  // q B fragments
+  alignas(16) float merge_o[kConsumerWarps / 2][kG][kD];
+  float merge_m[kConsumerWarps / 2][kG];
+  float merge_l[kConsumerWarps / 2][kG];
   int32_t merge_last;
   int32_t merge_cnt[kConsumerWarps];
   SeqTable table;
@@ -65,6 +60,8 @@ struct Smem {
 };
 
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + alignment slack
+static_assert(kConsumerWarps == 2 * kChunks, "a (chunk, j) of q per warp");
+static_assert(kStages % kConsumerWarps == 0, "a stage belongs to one warp, which sees each of its phases");
 static_assert(kBlocksPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of the resident blocks");
 
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
@@ -72,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
                   const __grid_constant__ DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
-  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem& s = fp8::aligned_smem<Smem>(smem_raw);
 
   const int gb = blockIdx.x;
   const int c = blockIdx.y;
@@ -138,49 +135,48 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   const int hq0 = c * kG;
   const int g = lane >> 2;
   const int tq = lane & 3;
-  const int mi = lane >> 3;  // ldmatrix: which 8x8 matrix this lane addresses
-  const int lr = lane & 7;
+  const int r0 = fp8::dealt_row(g);  // this lane's rows of a page: r0 and r0 + 2
 
   PageCursor cur;
   cur.start(p, t, sp);
 
-  // q as B fragments, one copy per warp in shared memory (32 registers would
-  // spill): column n = g holds head g % 2 (the products' columns beyond the
-  // two heads repeat them and are never read), k-step (chunk, j, word): dims
-  // 128 chunk + 16 (2 tq + j) + 4 word .. + 3.  Two k-steps per 16 bytes.
+  // q as B fragments in shared memory (32 registers would spill): column n = g
+  // holds head g % 2 (the products' columns beyond the two heads repeat them),
+  // k-step (chunk, j, word): dims 128 chunk + 16 (2 tq + j) + 4 word .. + 3.  Two
+  // k-steps per 16 bytes.  Every warp reads all of the two heads for their
+  // exponents and writes the fragments of one (chunk, j).
   const int qlane = (g & 1) * 4 + tq;
-  const uint32_t qaddr = smem_addr(&s.qfrag[warp][0][qlane]);
   float qs[2];  // logit factor 2^k log2(e) of heads 0 and 1
   auto load_q = [&]() {
-    uint32_t w[kChunks * 2][8];  // chunk and j
+    const __nv_bfloat16* src = p.q + (static_cast<size_t>(cur.b) * kHq + hq0 + (g & 1)) * kD + 32 * tq;
+    uint4 mine[2] = {};
     uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < kChunks * 2; ++i) {
-      const __nv_bfloat16* src = p.q + (static_cast<size_t>(cur.b) * kHq + hq0 + (g & 1)) * kD + 128 * (i >> 1) +
-                                 16 * (2 * tq + (i & 1));
-      const uint4 a = ld_global_nc_v4(src), b = ld_global_nc_v4(src + 8);
-      w[i][0] = a.x; w[i][1] = a.y; w[i][2] = a.z; w[i][3] = a.w;
-      w[i][4] = b.x; w[i][5] = b.y; w[i][6] = b.z; w[i][7] = b.w;
+      const uint4 v[2] = {ld_global_nc_v4(src + 128 * (i >> 1) + 16 * (i & 1)),
+                          ld_global_nc_v4(src + 128 * (i >> 1) + 16 * (i & 1) + 8)};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) amax = max(amax, max(w[i][k] << 16 & 0x7fff0000u, w[i][k] & 0x7fff0000u));
+      for (int k = 0; k < 2; ++k) {
+        if (i == warp) mine[k] = v[k];
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = max(amax, max(w[e] << 16 & 0x7fff0000u, w[e] & 0x7fff0000u));
+      }
     }
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));  // over the row's four lanes
     float inv;
     const int e = fp8::q_exponent(amax, inv);
-    __syncwarp();  // the warp is done with the previous sequence's fragments
-#pragma unroll
-    for (int i = 0; i < kChunks * 2; ++i)
+    if (g < kG) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (g < kG)
-          s.qfrag[warp][2 * i + k][qlane] =
-              make_uint4(fp8::q_f16x2(w[i][4 * k], inv), fp8::q_f16x2(w[i][4 * k + 1], inv),
-                         fp8::q_f16x2(w[i][4 * k + 2], inv), fp8::q_f16x2(w[i][4 * k + 3], inv));
-    __syncwarp();
+        s.qfrag[2 * warp + k][qlane] = make_uint4(fp8::q_f16x2(mine[k].x, inv), fp8::q_f16x2(mine[k].y, inv),
+                                                  fp8::q_f16x2(mine[k].z, inv), fp8::q_f16x2(mine[k].w, inv));
+    }
     const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * kLog2e;
     qs[0] = __shfl_sync(0xffffffffu, f, 0);
     qs[1] = __shfl_sync(0xffffffffu, f, 4);
+    named_barrier_sync(1, kConsumerWarps * 32);
   };
   load_q();
   auto prefetch_next_q = [&]() {
@@ -193,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 
   fp8::Reference ref[2];  // heads 0 and 1
   float l[2];             // this lane's share of the sums
-  float acc[16][4];    // 16-dim blocks: (dim 2g; heads 0, 1), (dim 2g + 1; heads 0, 1)
+  float acc[16][4];    // 16-dim blocks: (dim g; heads 0, 1), (dim g + 8; heads 0, 1)
   auto reset = [&]() {
     ref[0].reset();
     ref[1].reset();
@@ -206,24 +202,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   reset();
   bool ok = true;
 
-  for (int i = 0; i < n_pages; ++i) {
-    const int f = sp.begin + i;
-    if (f >= t.prefix[cur.b + 1]) {
-      cur.advance(p, t, sp, f);
-      load_q();
-      prefetch_next_q();
-    }
-    if ((i & (kConsumerWarps - 1)) == warp) {
+  for (int f0 = sp.begin; f0 < sp.end;) {
+    const int seg_end = cur.seg_end;
+    // this warp's pages of the segment: i % 4 == warp, i counted from the span's start
+    for (int i = f0 - sp.begin + ((warp - (f0 - sp.begin)) & (kConsumerWarps - 1)); i < seg_end - sp.begin;
+         i += kConsumerWarps) {
+      const int f = sp.begin + i;
       const int st = i % kStages;
       if (ok) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s.full[st], (i / kStages) & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.full[st], (i / kStages) & 1));
         if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
       }
       const int pos0 = cur.pos0(t, f);
-      const uint32_t kst = smem_addr(s.k[st]), vst = smem_addr(s.v[st]);
+      const uint8_t* kst = s.k[st];
+      const uint32_t vst = smem_addr(s.v[st]);
       const bool edge = pos0 < cur.lo || pos0 + kPage > cur.L;
-      const bool in0 = pos0 + g >= cur.lo && pos0 + g < cur.L;          // row g is visible
-      const bool in1 = pos0 + g + 8 >= cur.lo && pos0 + g + 8 < cur.L;  // row g + 8
+      const bool in0 = pos0 + r0 >= cur.lo && pos0 + r0 < cur.L;          // row r0 is visible
+      const bool in1 = pos0 + r0 + 2 >= cur.lo && pos0 + r0 + 2 < cur.L;  // row r0 + 2
 
       // ---- S^T = K q^T: four chains of MMAs ----
       float sc[4][4];
@@ -233,22 +228,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         for (int e = 0; e < 4; ++e) sc[k][e] = 0.f;
 #pragma unroll
       for (int k = 0; k < kChunks * 2; ++k) {  // chunk, j
-        const uint32_t base = kst + (k >> 1) * fp8::kChunkBytes;
-        const uint4 a = ld_shared_v4(base + fp8::swz(g, 2 * tq + (k & 1)));
-        const uint4 b = ld_shared_v4(base + fp8::swz(g + 8, 2 * tq + (k & 1)));
+        const uint8_t* base = kst + (k >> 1) * fp8::kChunkBytes;
+        const uint4 a = *reinterpret_cast<const uint4*>(base + fp8::swz(r0, 2 * tq + (k & 1)));
+        const uint4 b = *reinterpret_cast<const uint4*>(base + fp8::swz(r0 + 2, 2 * tq + (k & 1)));
         const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int w = 0; w < 4; w += 2) {
-          const uint4 q = ld_shared_v4(qaddr + (2 * k + w / 2) * 128);
+          const uint4 q = s.qfrag[2 * k + w / 2][qlane];
           fp8::mma_f16_16816(sc[w], fp8::lo_f16x2(aw[w]), fp8::lo_f16x2(bw[w]), fp8::hi_f16x2(aw[w]),
                              fp8::hi_f16x2(bw[w]), q.x, q.y);
           fp8::mma_f16_16816(sc[w + 1], fp8::lo_f16x2(aw[w + 1]), fp8::lo_f16x2(bw[w + 1]), fp8::hi_f16x2(aw[w + 1]),
                              fp8::hi_f16x2(bw[w + 1]), q.z, q.w);
         }
       }
-      const float kf0 = fp8::scale_value(s.k_scale[st][g]), kf1 = fp8::scale_value(s.k_scale[st][g + 8]);
-      float kv0 = fp8::scale_log2(s.v_scale[st][g]), kv1 = fp8::scale_log2(s.v_scale[st][g + 8]);
-      // x[0..3]: (row g; heads 0, 1), (row g + 8; heads 0, 1), in log2 units
+      const float kf0 = fp8::scale_value(s.k_scale[st][r0]), kf1 = fp8::scale_value(s.k_scale[st][r0 + 2]);
+      float kv0 = fp8::scale_log2(s.v_scale[st][r0]), kv1 = fp8::scale_log2(s.v_scale[st][r0 + 2]);
+      // x[0..3]: (row r0; heads 0, 1), (row r0 + 2; heads 0, 1), in log2 units
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -296,63 +291,80 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         l[e & 1] += ex2_approx(d);
         w[e] = ex2_approx(d + (r.weight_bias() + (e < 2 ? kv0 : kv1)));
       }
-      const uint32_t pb0 = fp8::transpose_8x8(fp8::pack_f16x2(w[0], w[1]));  // rows 0..7
-      const uint32_t pb1 = fp8::transpose_8x8(fp8::pack_f16x2(w[2], w[3]));  // rows 8..15
+      const uint32_t pb0 = fp8::transpose_8x8(fp8::pack_f16x2(w[0], w[1]));  // positions 4 t, 4 t + 1
+      const uint32_t pb1 = fp8::transpose_8x8(fp8::pack_f16x2(w[2], w[3]));  // 4 t + 2, 4 t + 3
 
       // ---- O^T += V^T P^T ----
+      const uint32_t vrow = vst + (lane & 15) * 128;
 #pragma unroll
-      for (int np = 0; np < 8; ++np) {  // 32 dims each
-        const int ch = np >> 2;
-        const int row = ((mi & 1) << 3) + lr;
+      for (int np = 0; np < 8; ++np) {  // 32 dims each: lanes 0..15 address the first 16, lanes 16..31 the others
         uint32_t r[4];
-        ldmatrix_x4_trans(vst + ch * fp8::kChunkBytes + fp8::swz(row, 2 * (np & 3) + (mi >> 1)), r[0], r[1], r[2],
-                          r[3]);
+        fp8::ldmatrix_b8_x2_trans(
+            vrow + (np >> 2) * fp8::kChunkBytes + (((2 * (np & 3) + (lane >> 4)) ^ (lane & 7)) << 4), r);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t a0, a1, a2, a3;
-          fp8::split_pair(r[2 * u], a0, a1);
-          fp8::split_pair(r[2 * u + 1], a2, a3);
-          fp8::mma_f16_16816(acc[2 * np + u], a0, a1, a2, a3, pb0, pb1);
-        }
+        for (int u = 0; u < 2; ++u)
+          fp8::mma_f16_16816(acc[2 * np + u], fp8::lo_f16x2(r[2 * u]), fp8::lo_f16x2(r[2 * u + 1]),
+                             fp8::hi_f16x2(r[2 * u]), fp8::hi_f16x2(r[2 * u + 1]), pb0, pb1);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.empty[st]);
     }
 
-    if (f + 1 == cur.seg_end) {
-      // ---------------- finish this sequence's segment (as in sliding.cuh) ----------------
+    {
+      // ---------------- finish this sequence's segment ----------------
+      // The four warps' results are merged two by two: warps 2 and 3 hand
+      // theirs to warps 0 and 1 through shared memory, and all threads join
+      // what those leave there.  Lane t of the four that hold the same values
+      // takes every fourth 16-dim block.
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-      if (tq == 0) {  // columns 0 and 1: the two heads
-#pragma unroll
-        for (int n = 0; n < 16; ++n)
-#pragma unroll
-          for (int h = 0; h < kG; ++h)
-            *reinterpret_cast<float2*>(&s.merge_o[warp][h][16 * n + 2 * g]) =
-                make_float2(fp8::unscale(acc[n][h], ref[h].R), fp8::unscale(acc[n][2 + h], ref[h].R));
-      }
-      if (lane == 0) {
+      const auto hand_over = [&](bool join) {
+        const int slot = warp & 1;
+        float fm[2], fo[2];  // factors of this warp's values and of the slot's
 #pragma unroll
         for (int h = 0; h < kG; ++h) {
-          s.merge_m[warp][h] = ref[h].m;
-          s.merge_l[warp][h] = l[h];
+          const float mo = join ? s.merge_m[slot][h] : -INFINITY, lo = join ? s.merge_l[slot][h] : 0.f;
+          const float M = fmaxf(ref[h].m, mo), M_use = M == -INFINITY ? 0.f : M;
+          fm[h] = exp2f(ref[h].m - M_use);
+          fo[h] = exp2f(mo - M_use);
+          // (a sum under m = -inf is 0, or a NaN that has to show)
+          l[h] = (ref[h].m == -INFINITY ? l[h] : fm[h] * l[h]) + (mo == -INFINITY ? lo : fo[h] * lo);
+          if (!join) fm[h] = 1.f;
+          __syncwarp();
+          if (lane == 0) {
+            s.merge_m[slot][h] = M;
+            s.merge_l[slot][h] = l[h];
+          }
         }
-      }
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+          if ((n & 3) == tq) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float* dst = &s.merge_o[slot][e & 1][16 * n + g + 8 * (e >> 1)];
+              const float mine = fp8::unscale(acc[n][e], ref[e & 1].R) * fm[e & 1];
+              *dst = join ? mine + *dst * fo[e & 1] : mine;
+            }
+          }
+      };
+      if (warp >= kConsumerWarps / 2) hand_over(false);
+      named_barrier_sync(1, kConsumerWarps * 32);
+      if (warp < kConsumerWarps / 2) hand_over(true);
       named_barrier_sync(1, kConsumerWarps * 32);
       const int tt = threadIdx.x;  // 0..127: 2 heads x 64 groups of 4 dims
       const int h = tt >> 6;
       const int d0 = (tt & 63) * 4;
       float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, s.merge_m[w][h]);
+      for (int w = 0; w < kConsumerWarps / 2; ++w) M = fmaxf(M, s.merge_m[w][h]);
       float Lsum = 0.f;
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
       // (with M = -inf every weight was 0 or NaN; a NaN has to show)
       const float M_use = M == -INFINITY ? 0.f : M;
 #pragma unroll
-      for (int w = 0; w < kConsumerWarps; ++w) {
+      for (int w = 0; w < kConsumerWarps / 2; ++w) {
         const float fw = exp2f(s.merge_m[w][h] - M_use);
         Lsum += (s.merge_m[w][h] == -INFINITY ? 1.f : fw) * s.merge_l[w][h];
         const float4 a = *reinterpret_cast<const float4*>(&s.merge_o[w][h][d0]);
@@ -378,8 +390,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (d0 == 0) p.part_ml[slot] = make_float2(M, Lsum);
         if (p.merge_in_grid) sliding::merge_partials(p, t, s, cur.b, gb, c, h, d0, M, Lsum, O);
       }
-      named_barrier_sync(1, kConsumerWarps * 32);  // merge buffers free again
+      named_barrier_sync(1, kConsumerWarps * 32);  // merge buffers (and q) free again
       reset();
+    }
+    f0 = seg_end;
+    if (f0 < sp.end) {
+      cur.advance(p, t, sp, f0);
+      load_q();
+      prefetch_next_q();
     }
   }
   allow_dependent_launch();

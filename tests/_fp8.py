@@ -46,6 +46,7 @@ def dequantise(codes, scales):
     c = codes.view(torch.uint8)
     s = scales.view(torch.uint8).transpose(1, 2).to(torch.float64)
     f = torch.where(s == 255, torch.full_like(s, float("nan")), torch.pow(2.0, s - 127))
+    f = torch.where(s == 0, torch.zeros_like(s), f)
     return e4m3_table().to(c.device)[c.long()] * f[..., None]
 
 
@@ -67,15 +68,19 @@ class Fp8Case:
                 self.vs.view(E8).to(dev), c.block_table, c.seq_lens)
 
 
-def attention_rows(q, k_pool, v_pool, block_table, seq_lens, window, prefix=None):
+def attention_rows(q, k_pool, v_pool, block_table, seq_lens, window, prefix=None, v_scale=None):
     """o [B, Hq, D] in 64 bits over float64 pools, and what a tolerance needs: A = sum w |v| / sum w of every element
-    and the largest sum |q_i k_i| of every row.  prefix: (table, length) seen by every sequence before its own."""
+    and the largest sum |q_i k_i| of every row.  prefix: (table, length) seen by every sequence before its own.
+
+    With the 8-bit cache's value scales (v_scale [P, Hkv, 16]) also the floors of its f16 operands (decode_bound): Q, the
+    largest max|q| sum |k_i| of every row, and F = max_l(w_l s_l) * sum_l |v_l| / s_l / sum w of every element."""
     q = q.double().cpu()
     k_pool, v_pool = k_pool.cpu(), v_pool.cpu()
     B, Hq, D = q.shape
     Hkv = k_pool.shape[2]
     G = Hq // Hkv
     o, A, S = torch.zeros_like(q), torch.zeros_like(q), torch.zeros((B, Hq, 1), dtype=torch.float64)
+    Q, F = torch.zeros_like(S), torch.zeros_like(q)
     for b in range(B):
         L = int(seq_lens[b])
         lo = max(0, L - window) if window > 0 else 0
@@ -94,10 +99,15 @@ def attention_rows(q, k_pool, v_pool, block_table, seq_lens, window, prefix=None
             o[b, c * G:(c + 1) * G] = w @ v
             A[b, c * G:(c + 1) * G] = w @ v.abs()
             S[b, c * G:(c + 1) * G, 0] = (qh.abs() @ k.abs().t()).max(-1).values
-    return o, A, S
+            if v_scale is not None:
+                byte = v_scale.view(torch.uint8).cpu()[page, c, row].double()
+                scale = torch.pow(2.0, byte - 127)
+                Q[b, c * G:(c + 1) * G, 0] = qh.abs().max(-1).values * k.abs().sum(-1).max()
+                F[b, c * G:(c + 1) * G] = (w * scale).max(-1, keepdim=True).values * (v.abs() / scale[:, None]).sum(0)
+    return (o, A, S) if v_scale is None else (o, A, S, Q, F)
 
 
-def decode_bound(o, A, S, D, out_dtype, weight_eps):
+def decode_bound(o, A, S, D, out_dtype, weight_eps, Q=0, F=0):
     """|got - o| allowed, element by element.
 
     Logits: D / 16 products accumulated in one chain, and at most 8 more
@@ -106,11 +116,15 @@ def decode_bound(o, A, S, D, out_dtype, weight_eps):
     by a factor exp(delta) up and its sum by as much down.  Weights are rounded
     to their type (weight_eps) and their 2^x is off by at most 2^-21.  Sums are
     fp32 (2^-18 for their chains).  The output is rounded once.
+
+    Over an 8-bit cache (Q, F): q and the weights w_l s_l (s_l the value row's scale) are f16 numbers whose largest is
+    above 2^14, so half the smallest step, 2^-25, is 2^-39 of the largest: a logit moves by 2^-39 Q more, and against
+    the values v_l / s_l the weights lose 2^-39 F.
     """
-    delta = (D / 16 + 8) * 2.0 ** -23 * S
+    delta = (D / 16 + 8) * 2.0 ** -23 * S + 2.0 ** -39 * Q
     rel = torch.expm1(2 * delta) + weight_eps + 2.0 ** -20 + 2.0 ** -18
     out = torch.finfo(out_dtype).eps / 2
-    return rel * A * (1 + out) + out * o.abs() + 1e-30
+    return (rel * A + 2.0 ** -39 * F) * (1 + out) + out * o.abs() + 1e-30
 
 
 def append_rows(kind, qkv, w_q, w_k, positions, Hq, Hkv, D):

@@ -28,14 +28,14 @@ def decode(kind, args, window, status=None, **kw):
 
 def reference(args, window):
     q, k, v, ks, vs, bt, sl = args
-    return attention_rows(q, dequantise(k, ks), dequantise(v, vs), bt, sl, window)
+    return attention_rows(q, dequantise(k, ks), dequantise(v, vs), bt, sl, window, v_scale=vs)
 
 
 def check(kind, args, window, label="", **kw):
     o, st = decode(kind, args, window, **kw)
     assert st == 0, "%s: status %d" % (label, st)
-    want, A, S = reference(args, window)
-    bound = decode_bound(want, A, S, args[0].shape[2], o.dtype, WEIGHT_EPS)
+    want, A, S, Q, F = reference(args, window)
+    bound = decode_bound(want, A, S, args[0].shape[2], o.dtype, WEIGHT_EPS, Q, F)
     got = o.double().cpu()
     assert torch.isfinite(got).all(), label
     err = (got - want).abs()
@@ -370,7 +370,8 @@ def test_serving_run_prompt_read_back_prefill_and_decode_steps(cuda_lib, kind):
         step.launch()
         torch.cuda.synchronize()
         assert int(st.item()) == 0
-        want, A, S = attention_rows(q1, dequantise(cache[0], cache[2]), dequantise(cache[1], cache[3]), table, lens, w)
-        bound = decode_bound(want, A, S, D, torch.float32, WEIGHT_EPS)
+        want, A, S, Q, F = attention_rows(q1, dequantise(cache[0], cache[2]), dequantise(cache[1], cache[3]), table,
+                                          lens, w, v_scale=cache[3])
+        bound = decode_bound(want, A, S, D, torch.float32, WEIGHT_EPS, Q, F)
         assert ((o1.double().cpu() - want).abs() <= bound).all()
     step.close()
