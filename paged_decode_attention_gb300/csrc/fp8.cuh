@@ -139,12 +139,13 @@ struct Reference {
   __device__ __forceinline__ float weight_bias() const { return static_cast<float>(kWeightBias) - R; }
 };
 
-// Accumulator -> output sum: x * 2^(R - 15).
-__device__ __forceinline__ float unscale(float x, float R) {
-  const int e = static_cast<int>(R) - kWeightBias;
-  // in two exact steps where 2^e is below the normal range
-  return e >= -126 ? x * __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23)
-                   : x * __uint_as_float(static_cast<uint32_t>(max(e, -190) + 64 + 127) << 23) * 0x1p-64f;
+// Accumulator -> output sum: x * 2^(R - 15) = x * f0 * f1, in two exact steps
+// where 2^(R - 15) is below the normal range.
+__device__ __forceinline__ void unscale_factors(float R, float& f0, float& f1) {
+  const int e = max(static_cast<int>(R) - kWeightBias, -190);
+  const bool low = e < -126;
+  f0 = __uint_as_float(static_cast<uint32_t>((low ? e + 64 : min(e, 127)) + 127) << 23);
+  f1 = low ? 0x1p-64f : 1.f;
 }
 
 // A q row's exponent k from the bits of its largest |q| (bf16 in the upper

@@ -5,17 +5,21 @@
 // memory the bf16 kernel's work per page, four copies of the softmax and an
 // exchange of partial logits for every page, would take twice the share of
 // the time.  Instead the four consumer warps take a group of up to four
-// consecutive pages of a segment together:
-//   * warp w computes the logits of page w alone, over all 512 dims (64
-//     MMAs, q as A fragments from shared memory), scales and masks them;
-//   * the row maxima of the four pages meet in shared memory (barrier);
-//   * warp w turns its page's logits into weights and leaves them in shared
-//     memory as the A fragment of the second product (barrier);
-//   * every warp multiplies all pages' weights with its own 128 of the 512
-//     output dims, so that no output is ever merged between warps.
-// So each byte is widened once, the softmax runs once per page, and two
-// barriers serve four pages.
-//
+// consecutive pages of a segment together, three barriers to a group:
+//   * every warp multiplies its own 128 of the 512 dims of all pages' keys
+//     (q fragments in registers) and leaves the partial logits in shared
+//     memory;
+//   * warp w adds up page w's, scales and masks them, and leaves their row
+//     maxima;
+//   * warp w turns page w's logits into weights and leaves those as the A
+//     fragment of the second product;
+//   * every warp multiplies all pages' weights with its own 128 output dims,
+//     so that no output is merged between warps.
+// So each byte is widened once and the softmax runs once per page.  (Page w's
+// logits by warp w alone, with q read from shared memory, needs no partial
+// logits, but its 64 KB of q fragments per group made the first product take
+// 2200 of a group's 7400 cycles: 16 contexts of 131072 positions 410 us,
+// against RATE us this way.)
 #pragma once
 
 #include "fp8.cuh"
@@ -36,7 +40,7 @@ constexpr int kStages = 5;
 constexpr int kStageTx = 2 * kPageBytes + 2 * kPage;  // K, V and their scales
 constexpr int kBlocksPerSm = global::kBlocksPerSm;    // the plan of the bf16 kernel
 constexpr int kWarmPages = 4;
-constexpr int kKSteps = kD / 16;                      // 32
+constexpr int kKSteps = kD / 16 / kConsumerWarps;     // 8 of the first product, per warp
 
 static_assert(kChunks == kConsumerWarps, "128 output dims per warp");
 static_assert(kStages > kConsumerWarps, "a group of pages and the next one's first");
@@ -46,7 +50,7 @@ struct Smem {
   alignas(1024) uint8_t v[kStages][kPageBytes];
   alignas(128) uint8_t k_scale[kStages][128];  // 16 bytes used: a copy lands on a 128-byte boundary
   alignas(128) uint8_t v_scale[kStages][128];
-  alignas(16) uint4 qfrag[kKSteps][32];          // q A fragments
+  alignas(16) float4 xs[kConsumerWarps][kConsumerWarps][2][32];  // partial logits: page, warp, n-tile
   alignas(16) uint4 pfrag[kConsumerWarps][32];   // weights of the group's pages, as A fragments
   float2 row_max[kConsumerWarps][kHq];           // the pages' row maxima of x and of x + kv (fp8.cuh)
   uint32_t q_max[kConsumerWarps][kHq];
@@ -125,12 +129,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   PageCursor cur;
   cur.start(p, t, sp);
 
-  // q of the sequence into shared memory as A fragments: warp w prepares the
-  // k-steps of chunk w (8 steps (j, word): dims 128 w + 16 (2 tq + j) + 4 word
-  // .. + 3 of rows g and g + 8), scaled by each row's power of two.
+  // q as A fragments over this warp's 128 dims: k-step (j, word): dims 128 w +
+  // 16 (2 tq + j) + 4 word .. + 3 of rows g and g + 8, scaled by each row's
+  // power of two.
+  uint32_t qf[kKSteps][4];
   float qs[2];  // logit factor 2^k log2(e) of rows g and g + 8
   auto load_q = [&]() {
-    uint32_t w[2][2][8];  // row, j, words
     uint32_t amax[2] = {0, 0};
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -139,11 +143,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         const __nv_bfloat16* src = p.q + (static_cast<size_t>(cur.b) * kHq + g + 8 * r) * kD + 128 * warp +
                                    16 * (2 * tq + j);
         const uint4 a = ld_global_nc_v4(src), b = ld_global_nc_v4(src + 8);
-        w[r][j][0] = a.x; w[r][j][1] = a.y; w[r][j][2] = a.z; w[r][j][3] = a.w;
-        w[r][j][4] = b.x; w[r][j][5] = b.y; w[r][j][6] = b.z; w[r][j][7] = b.w;
+        qf[4 * j][r] = a.x; qf[4 * j][2 + r] = a.y; qf[4 * j + 1][r] = a.z; qf[4 * j + 1][2 + r] = a.w;
+        qf[4 * j + 2][r] = b.x; qf[4 * j + 2][2 + r] = b.y; qf[4 * j + 3][r] = b.z; qf[4 * j + 3][2 + r] = b.w;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          amax[r] = max(amax[r], max(w[r][j][k] << 16 & 0x7fff0000u, w[r][j][k] & 0x7fff0000u));
+        for (int k = 4 * j; k < 4 * j + 4; ++k)
+#pragma unroll
+          for (int e = r; e < 4; e += 2)
+            amax[r] = max(amax[r], max(qf[k][e] << 16 & 0x7fff0000u, qf[k][e] & 0x7fff0000u));
       }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -151,24 +157,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       amax[r] = max(amax[r], __shfl_xor_sync(0xffffffffu, amax[r], 2));
       if (tq == 0) s.q_max[warp][g + 8 * r] = amax[r];
     }
-    named_barrier_sync(1, kConsumers);  // the other warps' maxima; and every warp is done with the old fragments
-    float inv[2];
+    named_barrier_sync(1, kConsumers);  // the other warps' maxima
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       uint32_t a = 0;
 #pragma unroll
       for (int k = 0; k < kConsumerWarps; ++k) a = max(a, s.q_max[k][g + 8 * r]);
-      const int e = fp8::q_exponent(a, inv[r]);
+      float inv;
+      const int e = fp8::q_exponent(a, inv);
       qs[r] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * kLog2e;
+#pragma unroll
+      for (int k = 0; k < kKSteps; ++k) {
+        qf[k][r] = fp8::q_f16x2(qf[k][r], inv);
+        qf[k][2 + r] = fp8::q_f16x2(qf[k][2 + r], inv);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        s.qfrag[8 * warp + 4 * j + k][lane] =
-            make_uint4(fp8::q_f16x2(w[0][j][2 * k], inv[0]), fp8::q_f16x2(w[1][j][2 * k], inv[1]),
-                       fp8::q_f16x2(w[0][j][2 * k + 1], inv[0]), fp8::q_f16x2(w[1][j][2 * k + 1], inv[1]));
-    named_barrier_sync(1, kConsumers);
   };
   auto prefetch_next_q = [&]() {
     const int nb = next_seq_in_span(p, t, sp, cur.b);
@@ -209,18 +212,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int n = min(kConsumerWarps, cur.seg_end - f);  // pages of this group
     const int gpos0 = cur.pos0(t, f);                    // position of its first row
 
-    // ---- logits of page w: x[nt][e]: head g + 8 (e >> 1), position pos0 + 4 tq + 2 nt + (e & 1) ----
-    float x[2][4];
-    float kv[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // log2 of those positions' value scales
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[nt][e] = -INFINITY;
-    if (warp < n) {
-      wait_page(i + warp);
-      const int st = (i + warp) % kStages;
-      const int pos0 = gpos0 + warp * kPage;
-      const uint8_t* kst = s.k[st];
+    // ---- every page's logits over this warp's dims ----
+#pragma unroll 2
+    for (int j = 0; j < n; ++j) {
+      wait_page(i + j);
+      const uint8_t* kst = s.k[(i + j) % kStages] + warp * fp8::kChunkBytes;
       float sc[2][2][4];  // n-tile, even / odd k-steps
 #pragma unroll
       for (int a = 0; a < 2; ++a)
@@ -228,31 +224,60 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[a][b][e] = 0.f;
-#pragma unroll 2
-      for (int k = 0; k < kChunks * 2; ++k) {  // chunk, j
-        const uint8_t* base = kst + (k >> 1) * fp8::kChunkBytes;
-        const uint4 a = *reinterpret_cast<const uint4*>(base + fp8::swz(fp8::dealt_row(g), 2 * tq + (k & 1)));
-        const uint4 b = *reinterpret_cast<const uint4*>(base + fp8::swz(fp8::dealt_row(g) + 2, 2 * tq + (k & 1)));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint4 a = *reinterpret_cast<const uint4*>(kst + fp8::swz(fp8::dealt_row(g), 2 * tq + k));
+        const uint4 b = *reinterpret_cast<const uint4*>(kst + fp8::swz(fp8::dealt_row(g) + 2, 2 * tq + k));
         const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint4 q = s.qfrag[4 * k + w][lane];
-          fp8::mma_f16_16816(sc[0][w & 1], q.x, q.y, q.z, q.w, fp8::lo_f16x2(aw[w]), fp8::hi_f16x2(aw[w]));
-          fp8::mma_f16_16816(sc[1][w & 1], q.x, q.y, q.z, q.w, fp8::lo_f16x2(bw[w]), fp8::hi_f16x2(bw[w]));
+          const uint32_t (&q)[4] = qf[4 * k + w];
+          fp8::mma_f16_16816(sc[0][w & 1], q[0], q[1], q[2], q[3], fp8::lo_f16x2(aw[w]), fp8::hi_f16x2(aw[w]));
+          fp8::mma_f16_16816(sc[1][w & 1], q[0], q[1], q[2], q[3], fp8::lo_f16x2(bw[w]), fp8::hi_f16x2(bw[w]));
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+        s.xs[j][warp][nt][lane] = make_float4(sc[nt][0][0] + sc[nt][1][0], sc[nt][0][1] + sc[nt][1][1],
+                                              sc[nt][0][2] + sc[nt][1][2], sc[nt][0][3] + sc[nt][1][3]);
+    }
+    named_barrier_sync(1, kConsumers);
+
+    // ---- page w's logits: x[nt][e]: head g + 8 (e >> 1), position pos0 + 4 tq + 2 nt + (e & 1) ----
+    float x[2][4];
+    float kv[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // log2 of those positions' value scales
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[nt][e] = -INFINITY;
+    if (warp < n) {
+      const int st = (i + warp) % kStages;
+      const int pos0 = gpos0 + warp * kPage;
+      float sc[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float4 v = s.xs[warp][0][nt][lane];
+#pragma unroll
+        for (int w = 1; w < kConsumerWarps; ++w) {
+          const float4 o = s.xs[warp][w][nt][lane];
+          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        }
+        sc[nt][0] = v.x; sc[nt][1] = v.y; sc[nt][2] = v.z; sc[nt][3] = v.w;
+      }
+      const uint32_t kb = *reinterpret_cast<const uint32_t*>(&s.k_scale[st][4 * tq]);
+      const uint32_t vb = *reinterpret_cast<const uint32_t*>(&s.v_scale[st][4 * tq]);
       const bool edge = pos0 < cur.lo || pos0 + kPage > cur.L;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int r = 4 * tq + 2 * nt + u;
-          const float kf = fp8::scale_value(s.k_scale[st][r]);
+          const float kf = fp8::scale_value((kb >> (8 * (2 * nt + u))) & 255u);
           const bool in = !edge || (pos0 + r >= cur.lo && pos0 + r < cur.L);
           if (in) {
-            kv[nt][u] = fp8::scale_log2(s.v_scale[st][r]);
-            x[nt][u] = (sc[nt][0][u] + sc[nt][1][u]) * kf * qs[0];
-            x[nt][2 + u] = (sc[nt][0][2 + u] + sc[nt][1][2 + u]) * kf * qs[1];
+            kv[nt][u] = fp8::scale_log2((vb >> (8 * (2 * nt + u))) & 255u);
+            x[nt][u] = sc[nt][u] * kf * qs[0];
+            x[nt][2 + u] = sc[nt][2 + u] * kf * qs[1];
           }
         }
     }
@@ -309,9 +334,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         acc[b][3] *= scale[1];
       }
     }
-#pragma unroll 1
+#pragma unroll 2
     for (int j = 0; j < n; ++j) {
-      wait_page(i + j);
       const int st = (i + j) % kStages;
       const int pos0 = gpos0 + j * kPage;
       const uint32_t vst = smem_addr(s.v[st]) + warp * fp8::kChunkBytes;
@@ -328,14 +352,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       }
       const uint4 pa = s.pfrag[j][lane];
       const uint32_t vrow = vst + (lane & 15) * 128;
+      uint32_t r[4][4];
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {  // 32 dims each: lanes 0..15 address the first 16, lanes 16..31 the others
-        uint32_t r[4];
-        fp8::ldmatrix_b8_x2_trans(vrow + (((2 * np + (lane >> 4)) ^ (lane & 7)) << 4), r);
+      for (int np = 0; np < 4; ++np)  // 32 dims each: lanes 0..15 address the first 16, lanes 16..31 the others
+        fp8::ldmatrix_b8_x2_trans(vrow + (((2 * np + (lane >> 4)) ^ (lane & 7)) << 4), r[np]);
+#pragma unroll
+      for (int np = 0; np < 4; ++np)
 #pragma unroll
         for (int u = 0; u < 4; ++u)  // 8 dims each
-          fp8::mma_f16_16816(acc[4 * np + u], pa.x, pa.y, pa.z, pa.w, fp8::lo_f16x2(r[u]), fp8::hi_f16x2(r[u]));
-      }
+          fp8::mma_f16_16816(acc[4 * np + u], pa.x, pa.y, pa.z, pa.w, fp8::lo_f16x2(r[np][u]), fp8::hi_f16x2(r[np][u]));
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.empty[st]);
     }
@@ -365,9 +390,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         for (int r = 0; r < 2; ++r) {
           const size_t row = static_cast<size_t>(whole ? cur.b : gb + cur.b) * kHq + g + 8 * r;
           const float inv = lt[r] > 0.f ? 1.f / lt[r] : lt[r];  // 0, or a NaN that has to show
+          float u0, u1;
+          fp8::unscale_factors(ref[r].R, u0, u1);
 #pragma unroll
           for (int b = 0; b < 16; ++b) {
-            const float v0 = fp8::unscale(acc[b][2 * r], ref[r].R), v1 = fp8::unscale(acc[b][2 * r + 1], ref[r].R);
+            const float v0 = acc[b][2 * r] * u0 * u1, v1 = acc[b][2 * r + 1] * u0 * u1;
             const size_t at = row * kD + 128 * warp + 8 * b + 2 * tq;
             if (whole)
               store_out2(p, at, v0 * inv, v1 * inv);

@@ -338,15 +338,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             s.merge_l[slot][h] = l[h];
           }
         }
+        // 2^(R - 15) in two exact steps (it may lie below the normal range)
+        float u0[kG], u1[kG];
 #pragma unroll
-        for (int n = 0; n < 16; ++n)
-          if ((n & 3) == tq) {
+        for (int h = 0; h < kG; ++h) fp8::unscale_factors(ref[h].R, u0[h], u1[h]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float* dst = &s.merge_o[slot][e & 1][16 * n + g + 8 * (e >> 1)];
-              const float mine = fp8::unscale(acc[n][e], ref[e & 1].R) * fm[e & 1];
-              *dst = join ? mine + *dst * fo[e & 1] : mine;
-            }
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a01 = tq & 1 ? acc[4 * j + 1][e] : acc[4 * j][e];
+            const float a23 = tq & 1 ? acc[4 * j + 3][e] : acc[4 * j + 2][e];
+            const float mine = (tq & 2 ? a23 : a01) * u0[e & 1] * u1[e & 1] * fm[e & 1];
+            float* dst = &s.merge_o[slot][e & 1][16 * (4 * j + tq) + g + 8 * (e >> 1)];
+            *dst = join ? fmaf(*dst, fo[e & 1], mine) : mine;
           }
       };
       if (warp >= kConsumerWarps / 2) hand_over(false);
