@@ -4,22 +4,18 @@
 // A page is 16 KB here (K and V) against 32 KB in bf16, so at the rate of
 // memory the bf16 kernel's work per page, four copies of the softmax and an
 // exchange of partial logits for every page, would take twice the share of
-// the time.  Instead the four consumer warps take a group of up to four
-// consecutive pages of a segment together, three barriers to a group:
-//   * every warp multiplies its own 128 of the 512 dims of all pages' keys
-//     (q fragments in registers) and leaves the partial logits in shared
-//     memory;
-//   * warp w adds up page w's, scales and masks them, and leaves their row
-//     maxima;
-//   * warp w turns page w's logits into weights and leaves those as the A
-//     fragment of the second product;
-//   * every warp multiplies all pages' weights with its own 128 output dims,
+// the time.  Instead the four consumer warps take two consecutive pages of a
+// segment together, with two barriers to a group:
+//   * every warp multiplies its own 128 of the 512 dims of both pages' keys (q
+//     fragments in registers) and leaves the partial logits in shared memory;
+//   * each warp adds up those of eight of the 32 positions, scales and masks
+//     them, and leaves their weights as A fragments of the second product;
+//   * every warp multiplies both pages' weights with its own 128 output dims,
 //     so that no output is merged between warps.
-// So each byte is widened once and the softmax runs once per page.  (Page w's
-// logits by warp w alone, with q read from shared memory, needs no partial
-// logits, but its 64 KB of q fragments per group made the first product take
-// 2200 of a group's 7400 cycles: 16 contexts of 131072 positions 410 us,
-// against RATE us this way.)
+// So each byte is widened once and the softmax runs once per position.
+// On 16 contexts of 131072 positions: 343 us, 0.92 of the measured copy rate; with groups of four pages, which
+// hold more of the ring (five stages beside their partial logits), 381 us;
+// with page w's logits by warp w alone and q read from shared memory 410 us.
 #pragma once
 
 #include "fp8.cuh"
@@ -32,27 +28,29 @@ namespace global_fp8 {
 using global::kD;
 using global::kHq;
 
-constexpr int kConsumerWarps = 4;
+constexpr int kGroup = 2;          // pages taken together
+constexpr int kConsumerWarps = 4;  // a chunk of 128 dims each in the products, a (page, n-tile) in the softmax
 constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kChunks = kD / 128;                     // 4: one per consumer warp in the second product
 constexpr int kPageBytes = kPage * kD;                // 8 KB
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr int kStageTx = 2 * kPageBytes + 2 * kPage;  // K, V and their scales
 constexpr int kBlocksPerSm = global::kBlocksPerSm;    // the plan of the bf16 kernel
 constexpr int kWarmPages = 4;
 constexpr int kKSteps = kD / 16 / kConsumerWarps;     // 8 of the first product, per warp
 
 static_assert(kChunks == kConsumerWarps, "128 output dims per warp");
-static_assert(kStages > kConsumerWarps, "a group of pages and the next one's first");
+static_assert(2 * kGroup == kConsumerWarps, "two warps per page of a group");
 
 struct Smem {
   alignas(1024) uint8_t k[kStages][kPageBytes];  // kChunks tiles of [16 rows][128 dims], swizzled
   alignas(1024) uint8_t v[kStages][kPageBytes];
   alignas(128) uint8_t k_scale[kStages][128];  // 16 bytes used: a copy lands on a 128-byte boundary
   alignas(128) uint8_t v_scale[kStages][128];
-  alignas(16) float4 xs[kConsumerWarps][kConsumerWarps][2][32];  // partial logits: page, warp, n-tile
-  alignas(16) uint4 pfrag[kConsumerWarps][32];   // weights of the group's pages, as A fragments
-  float2 row_max[kConsumerWarps][kHq];           // the pages' row maxima of x and of x + kv (fp8.cuh)
+  alignas(16) float4 xs[kGroup][kConsumerWarps][2][32];  // partial logits: page, chunk, n-tile
+  alignas(16) uint2 pfrag[kGroup][2][32];        // weights of the group's pages, as A fragments by n-tile
+  float2 row_max[kConsumerWarps][kHq];           // the warps' row maxima of x and of x + kv (fp8.cuh)
+  alignas(16) int32_t moves[kConsumerWarps];     // a warp's positions move a reference
   uint32_t q_max[kConsumerWarps][kHq];
   float row_sum[kConsumerWarps][kHq];
   SeqTable table;
@@ -125,6 +123,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   const int g = lane >> 2;  // fragment row: query heads g and g + 8
   const int tq = lane & 3;
   constexpr int kConsumers = kConsumerWarps * 32;
+  const int page = warp >> 1;  // of the group, and its n-tile, in the softmax
+  const int tile = warp & 1;
 
   PageCursor cur;
   cur.start(p, t, sp);
@@ -195,11 +195,179 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   };
   reset();
   bool ok = true;
-  auto wait_page = [&](int i) {
-    if (ok) {
-      ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.full[i % kStages], (i / kStages) & 1));
+  // NP (1 or 2) pages from page i of the span, page f of the list
+  auto page_group = [&](auto np_c, int i, int f) {
+    constexpr int NP = decltype(np_c)::value;
+    const int gpos0 = cur.pos0(t, f);  // position of the group's first row
+    const bool edge = gpos0 < cur.lo || gpos0 + NP * kPage > cur.L;
+    int st[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) st[j] = (i + j) % kStages;
+    if (ok) {  // lane j waits for page j: one wait's latency for both
+      ok = __all_sync(0xffffffffu,
+                      lane >= NP || mbar_wait_fast(&s.full[(i + lane) % kStages], ((i + lane) / kStages) & 1));
       if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
     }
+
+    // ---- every page's logits over this warp's dims ----
+    float sc[NP][2][2][4];  // page, n-tile, even / odd k-steps
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[j][a][b][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const uint8_t* kst = s.k[st[j]] + warp * fp8::kChunkBytes;
+        const uint4 a = *reinterpret_cast<const uint4*>(kst + fp8::swz(fp8::dealt_row(g), 2 * tq + k));
+        const uint4 b = *reinterpret_cast<const uint4*>(kst + fp8::swz(fp8::dealt_row(g) + 2, 2 * tq + k));
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t (&q)[4] = qf[4 * k + w];
+          fp8::mma_f16_16816(sc[j][0][w & 1], q[0], q[1], q[2], q[3], fp8::lo_f16x2(aw[w]), fp8::hi_f16x2(aw[w]));
+          fp8::mma_f16_16816(sc[j][1][w & 1], q[0], q[1], q[2], q[3], fp8::lo_f16x2(bw[w]), fp8::hi_f16x2(bw[w]));
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+        s.xs[j][warp][nt][lane] =
+            make_float4(sc[j][nt][0][0] + sc[j][nt][1][0], sc[j][nt][0][1] + sc[j][nt][1][1],
+                        sc[j][nt][0][2] + sc[j][nt][1][2], sc[j][nt][0][3] + sc[j][nt][1][3]);
+    named_barrier_sync(1, kConsumers);
+
+    // ---- this warp's eight positions: x[e]: head g + 8 (e >> 1), position pos0 + 4 tq + 2 tile + (e & 1) ----
+    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    float kv[2] = {0.f, 0.f};  // log2 of those positions' value scales
+    if (page < NP) {
+      const int sp_ = NP == 2 && page ? st[NP - 1] : st[0];
+      const int pos = gpos0 + page * kPage + 4 * tq + 2 * tile;
+      float4 v = s.xs[page][0][tile][lane];
+#pragma unroll
+      for (int w = 1; w < kConsumerWarps; ++w) {
+        const float4 o = s.xs[page][w][tile][lane];
+        v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+      }
+      const uint32_t kb = *reinterpret_cast<const uint16_t*>(&s.k_scale[sp_][4 * tq + 2 * tile]);
+      const uint32_t vb = *reinterpret_cast<const uint16_t*>(&s.v_scale[sp_][4 * tq + 2 * tile]);
+      const float k0 = fp8::scale_value(kb & 255u), k1 = fp8::scale_value(kb >> 8);
+      if (!edge || (pos >= cur.lo && pos < cur.L)) {
+        kv[0] = fp8::scale_log2(vb & 255u);
+        x[0] = v.x * k0 * qs[0];
+        x[2] = v.z * k0 * qs[1];
+      }
+      if (!edge || (pos + 1 >= cur.lo && pos + 1 < cur.L)) {
+        kv[1] = fp8::scale_log2(vb >> 8);
+        x[1] = v.y * k1 * qs[0];
+        x[3] = v.w * k1 * qs[1];
+      }
+    }
+    // ---- weights ----
+    // The references move only when some position exceeds them, which after a
+    // sequence's first pages is rare.  So the weights are formed with the
+    // references as they are, and with them goes a note whether this warp's
+    // positions exceed one; if any warp's do, all maxima are exchanged and the
+    // weights formed anew.
+    float ps[2];  // this group's share of the sums
+    auto weights = [&]() {
+      float pr[4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float mu = ref[r].m_use(), bias = ref[r].weight_bias();
+        const float d0 = x[2 * r] - mu, d1 = x[2 * r + 1] - mu;
+        ps[r] = ex2_approx(d0) + ex2_approx(d1);
+        pr[2 * r] = ex2_approx(d0 + (bias + kv[0]));
+        pr[2 * r + 1] = ex2_approx(d1 + (bias + kv[1]));
+      }
+      if (page < NP)
+        s.pfrag[page][tile][lane] = make_uint2(fp8::pack_f16x2(pr[0], pr[1]), fp8::pack_f16x2(pr[2], pr[3]));
+    };
+    float mx[2], mt[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[r] = fmaxf(x[2 * r], x[2 * r + 1]);
+      mt[r] = fmaxf(x[2 * r] + kv[0], x[2 * r + 1] + kv[1]);
+    }
+    const bool moves = __any_sync(0xffffffffu, mx[0] > ref[0].m || mx[1] > ref[1].m || mt[0] > ref[0].T ||
+                                                   mt[1] > ref[1].T);
+    weights();
+    if (lane == 0) s.moves[warp] = moves;
+    named_barrier_sync(1, kConsumers);
+    const int4 mv = *reinterpret_cast<const int4*>(s.moves);
+    if (mv.x | mv.y | mv.z | mv.w) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 2));
+        if (tq == 0) s.row_max[warp][g + 8 * r] = make_float2(mx[r], mt[r]);
+      }
+      named_barrier_sync(1, kConsumers);
+      float scale[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float2 m2 = s.row_max[0][g + 8 * r];
+#pragma unroll
+        for (int w = 1; w < kConsumerWarps; ++w) {
+          const float2 o = s.row_max[w][g + 8 * r];
+          m2 = make_float2(fmaxf(m2.x, o.x), fmaxf(m2.y, o.y));
+        }
+        float ls;
+        ref[r].move(m2.x, m2.y, ls, scale[r]);
+        l[r] *= ls;
+      }
+#pragma unroll
+      for (int b = 0; b < 16; ++b) {
+        acc[b][0] *= scale[0];
+        acc[b][1] *= scale[0];
+        acc[b][2] *= scale[1];
+        acc[b][3] *= scale[1];
+      }
+      weights();
+      named_barrier_sync(1, kConsumers);
+    }
+    l[0] += ps[0];
+    l[1] += ps[1];
+
+    // ---- O += P V over this warp's 128 dims ----
+    const uint32_t vst = smem_addr(s.v[0]) + warp * fp8::kChunkBytes;
+    if (edge) {
+      // zero this warp's V rows outside [lo, L): weight 0 times NaN would be NaN
+#pragma unroll 1
+      for (int rr = 0; rr < NP * kPage; ++rr) {
+        const int pos = gpos0 + rr;
+        if ((pos < cur.lo || pos >= cur.L) && lane < 8)
+          st_shared_v4(vst + (NP == 2 && rr >= kPage ? st[NP - 1] : st[0]) * kPageBytes + (rr & (kPage - 1)) * 128 +
+                           lane * 16,
+                       make_uint4(0, 0, 0, 0));
+      }
+      fence_proxy_async_smem();  // before TMA rewrites these stages
+      __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const uint2 p0 = s.pfrag[j][0][lane], p1 = s.pfrag[j][1][lane];
+      const uint32_t vrow = vst + st[j] * kPageBytes + (lane & 15) * 128;
+      uint32_t r[4][4];
+#pragma unroll
+      for (int np = 0; np < 4; ++np)  // 32 dims each: lanes 0..15 address the first 16, lanes 16..31 the others
+        fp8::ldmatrix_b8_x2_trans(vrow + (((2 * np + (lane >> 4)) ^ (lane & 7)) << 4), r[np]);
+#pragma unroll
+      for (int np = 0; np < 4; ++np)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)  // 8 dims each
+          fp8::mma_f16_16816(acc[4 * np + u], p0.x, p0.y, p1.x, p1.y, fp8::lo_f16x2(r[np][u]), fp8::hi_f16x2(r[np][u]));
+    }
+    __syncwarp();
+    if (lane < NP) mbar_arrive(&s.empty[(i + lane) % kStages]);
   };
 
   for (int i = 0; i < n_pages;) {
@@ -209,161 +377,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       load_q();
       prefetch_next_q();
     }
-    const int n = min(kConsumerWarps, cur.seg_end - f);  // pages of this group
-    const int gpos0 = cur.pos0(t, f);                    // position of its first row
-
-    // ---- every page's logits over this warp's dims ----
-#pragma unroll 2
-    for (int j = 0; j < n; ++j) {
-      wait_page(i + j);
-      const uint8_t* kst = s.k[(i + j) % kStages] + warp * fp8::kChunkBytes;
-      float sc[2][2][4];  // n-tile, even / odd k-steps
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[a][b][e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint4 a = *reinterpret_cast<const uint4*>(kst + fp8::swz(fp8::dealt_row(g), 2 * tq + k));
-        const uint4 b = *reinterpret_cast<const uint4*>(kst + fp8::swz(fp8::dealt_row(g) + 2, 2 * tq + k));
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t (&q)[4] = qf[4 * k + w];
-          fp8::mma_f16_16816(sc[0][w & 1], q[0], q[1], q[2], q[3], fp8::lo_f16x2(aw[w]), fp8::hi_f16x2(aw[w]));
-          fp8::mma_f16_16816(sc[1][w & 1], q[0], q[1], q[2], q[3], fp8::lo_f16x2(bw[w]), fp8::hi_f16x2(bw[w]));
-        }
-      }
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-        s.xs[j][warp][nt][lane] = make_float4(sc[nt][0][0] + sc[nt][1][0], sc[nt][0][1] + sc[nt][1][1],
-                                              sc[nt][0][2] + sc[nt][1][2], sc[nt][0][3] + sc[nt][1][3]);
-    }
-    named_barrier_sync(1, kConsumers);
-
-    // ---- page w's logits: x[nt][e]: head g + 8 (e >> 1), position pos0 + 4 tq + 2 nt + (e & 1) ----
-    float x[2][4];
-    float kv[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // log2 of those positions' value scales
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[nt][e] = -INFINITY;
-    if (warp < n) {
-      const int st = (i + warp) % kStages;
-      const int pos0 = gpos0 + warp * kPage;
-      float sc[2][4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float4 v = s.xs[warp][0][nt][lane];
-#pragma unroll
-        for (int w = 1; w < kConsumerWarps; ++w) {
-          const float4 o = s.xs[warp][w][nt][lane];
-          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-        }
-        sc[nt][0] = v.x; sc[nt][1] = v.y; sc[nt][2] = v.z; sc[nt][3] = v.w;
-      }
-      const uint32_t kb = *reinterpret_cast<const uint32_t*>(&s.k_scale[st][4 * tq]);
-      const uint32_t vb = *reinterpret_cast<const uint32_t*>(&s.v_scale[st][4 * tq]);
-      const bool edge = pos0 < cur.lo || pos0 + kPage > cur.L;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int r = 4 * tq + 2 * nt + u;
-          const float kf = fp8::scale_value((kb >> (8 * (2 * nt + u))) & 255u);
-          const bool in = !edge || (pos0 + r >= cur.lo && pos0 + r < cur.L);
-          if (in) {
-            kv[nt][u] = fp8::scale_log2((vb >> (8 * (2 * nt + u))) & 255u);
-            x[nt][u] = sc[nt][u] * kf * qs[0];
-            x[nt][2 + u] = sc[nt][2 + u] * kf * qs[1];
-          }
-        }
-    }
-    // ---- the group's row maxima ----
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float mx = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
-      float mt = fmaxf(fmaxf(x[0][2 * r] + kv[0][0], x[0][2 * r + 1] + kv[0][1]),
-                       fmaxf(x[1][2 * r] + kv[1][0], x[1][2 * r + 1] + kv[1][1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-      if (tq == 0) s.row_max[warp][g + 8 * r] = make_float2(mx, mt);
-    }
-    named_barrier_sync(1, kConsumers);
-    float scale[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float2 mx = s.row_max[0][g + 8 * r];
-#pragma unroll
-      for (int w = 1; w < kConsumerWarps; ++w) {
-        const float2 o = s.row_max[w][g + 8 * r];
-        mx = make_float2(fmaxf(mx.x, o.x), fmaxf(mx.y, o.y));
-      }
-      float ls;
-      ref[r].move(mx.x, mx.y, ls, scale[r]);
-      l[r] *= ls;
-    }
-    // ---- page w's weights ----
-    if (warp < n) {
-      float pr[2][4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const fp8::Reference& r = ref[e >> 1];
-          const float d = x[nt][e] - r.m_use();
-          l[e >> 1] += ex2_approx(d);
-          pr[nt][e] = ex2_approx(d + (r.weight_bias() + kv[nt][e & 1]));
-        }
-      s.pfrag[warp][lane] = make_uint4(fp8::pack_f16x2(pr[0][0], pr[0][1]), fp8::pack_f16x2(pr[0][2], pr[0][3]),
-                                       fp8::pack_f16x2(pr[1][0], pr[1][1]), fp8::pack_f16x2(pr[1][2], pr[1][3]));
-    }
-    named_barrier_sync(1, kConsumers);
-
-    // ---- O += P V over this warp's 128 dims ----
-    if (__any_sync(0xffffffffu, scale[0] != 1.f || scale[1] != 1.f)) {
-#pragma unroll
-      for (int b = 0; b < 16; ++b) {
-        acc[b][0] *= scale[0];
-        acc[b][1] *= scale[0];
-        acc[b][2] *= scale[1];
-        acc[b][3] *= scale[1];
-      }
-    }
-#pragma unroll 2
-    for (int j = 0; j < n; ++j) {
-      const int st = (i + j) % kStages;
-      const int pos0 = gpos0 + j * kPage;
-      const uint32_t vst = smem_addr(s.v[st]) + warp * fp8::kChunkBytes;
-      if (pos0 < cur.lo || pos0 + kPage > cur.L) {
-        // zero this warp's V rows outside [lo, L): weight 0 times NaN would be NaN
-#pragma unroll 1
-        for (int rr = 0; rr < kPage; ++rr) {
-          const int pos = pos0 + rr;
-          if ((pos < cur.lo || pos >= cur.L) && lane < 8)
-            st_shared_v4(vst + rr * 128 + lane * 16, make_uint4(0, 0, 0, 0));
-        }
-        fence_proxy_async_smem();  // before TMA rewrites this stage
-        __syncwarp();
-      }
-      const uint4 pa = s.pfrag[j][lane];
-      const uint32_t vrow = vst + (lane & 15) * 128;
-      uint32_t r[4][4];
-#pragma unroll
-      for (int np = 0; np < 4; ++np)  // 32 dims each: lanes 0..15 address the first 16, lanes 16..31 the others
-        fp8::ldmatrix_b8_x2_trans(vrow + (((2 * np + (lane >> 4)) ^ (lane & 7)) << 4), r[np]);
-#pragma unroll
-      for (int np = 0; np < 4; ++np)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)  // 8 dims each
-          fp8::mma_f16_16816(acc[4 * np + u], pa.x, pa.y, pa.z, pa.w, fp8::lo_f16x2(r[np][u]), fp8::hi_f16x2(r[np][u]));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.empty[st]);
-    }
+    const int n = min(kGroup, cur.seg_end - f);  // pages of this group
+    if (n == 2)
+      page_group(std::integral_constant<int, 2>{}, i, f);
+    else
+      page_group(std::integral_constant<int, 1>{}, i, f);
     i += n;
 
     if (f + n == cur.seg_end) {
