@@ -103,6 +103,12 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
       : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// Copies `bytes` (a multiple of 16) of shared memory to global memory in the
+// issuing thread's bulk async-group; both addresses 16-byte aligned.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
 // Waits until this thread's bulk stores have read their shared memory ...
 __device__ __forceinline__ void tma_store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");

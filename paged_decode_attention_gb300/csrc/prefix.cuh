@@ -13,9 +13,14 @@
 //     segment left as a partial;
 //   * this merge.
 //
-// One 4-warp block per (row b*Hq + h, slice of 128 dims), as combine.cuh; a
-// row's partials are its prefix spans followed by its blocks of the balanced
-// schedule.
+// One block per row b*Hq + h, a row's partials being its prefix spans followed
+// by its blocks of the balanced schedule: two or four groups of 128 threads,
+// four dims a thread, each group takes every second or fourth partial with
+// kInFlight loads in flight, and the groups meet in shared memory.  Bound by
+// latency: the schedule is worked out before the block waits for the kernels
+// ahead of it.  Four groups where the rows' blocks are resident at once (8
+// sequences, 21 partials a row: a call takes 29.8 us with four, 31.2 with two),
+// two where they come in waves (64 sequences, 15 partials: 131.4 and 127.5).
 #pragma once
 
 #include "combine.cuh"
@@ -33,30 +38,32 @@ struct MergeParams {
   int32_t splits;
 };
 
-template <int kD, int kPrefixSlices, int kStepPages>
-__global__ void __launch_bounds__(kCombineWarps * 32) merge_kernel(const __grid_constant__ MergeParams mp) {
+constexpr int kGroupThreads = 128;
+constexpr int kInFlight = 4;  // partials in flight per thread
+
+template <int kD, int kPrefixSlices, int kStepPages, int kMergeGroups>
+__global__ void __launch_bounds__(kMergeGroups* kGroupThreads) merge_kernel(const __grid_constant__ MergeParams mp) {
   const DecodeParams& p = mp.d;
-  constexpr int kSlices = kD / kCombineCols;
-  __shared__ float s_max[kCombineWarps];
-  __shared__ float s_l[kCombineWarps];
-  __shared__ float4 s_o[kCombineWarps][32];
-  __shared__ int s_sched[3];
+  static_assert(kD == 4 * kGroupThreads, "four dims per thread");
+  __shared__ int s_sched[kGroupThreads / 32][3];
+  __shared__ float s_m[kMergeGroups][kGroupThreads];  // per thread: the two dim slices differ
+  __shared__ float s_l[kMergeGroups][kGroupThreads];
+  __shared__ float4 s_o[kMergeGroups][kGroupThreads];
 
-  const int h = blockIdx.x / kSlices;
-  const int slice = blockIdx.x % kSlices;
+  const int h = blockIdx.x;
+  const int Hq = gridDim.x;
   const int b = blockIdx.y;
-  const int Hq = gridDim.x / kSlices;
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
+  const int tid = threadIdx.x % kGroupThreads;
+  const int group = threadIdx.x / kGroupThreads;
+  const int d0 = 4 * tid;
   const size_t row = static_cast<size_t>(b) * Hq + h;
-  const int d0 = slice * kCombineCols + lane * 4;
 
-  wait_for_primary_grid();
-  allow_dependent_launch();
-  // weighted pages before sequence b, its own pages, the weighted total (common.cuh)
-  if (warp == 0) {
+  // The schedule: weighted pages before sequence b, its own pages, the weighted
+  // total (common.cuh).  The kernel ahead lets this one launch only after its
+  // own wait, so the lengths are final and visible already.
+  if (group == 0) {
     int before = 0, mine = 0, total = 0;
-    for (int j = lane; j < p.batch; j += 32) {
+    for (int j = tid; j < p.batch; j += kGroupThreads) {
       const int n = visible_pages(clamp_len(p, p.seq_lens[j], false), p.window);
       const int wn = n > 0 ? n + kSeqWeight : 0;
       total += wn;
@@ -66,14 +73,21 @@ __global__ void __launch_bounds__(kCombineWarps * 32) merge_kernel(const __grid_
     before = __reduce_add_sync(0xffffffffu, before);
     mine = __reduce_add_sync(0xffffffffu, mine);
     total = __reduce_add_sync(0xffffffffu, total);
-    if (lane == 0) {
-      s_sched[0] = before;
-      s_sched[1] = mine;
-      s_sched[2] = total;
+    if ((tid & 31) == 0) {
+      s_sched[tid >> 5][0] = before;
+      s_sched[tid >> 5][1] = mine;
+      s_sched[tid >> 5][2] = total;
     }
   }
+  const prefill_pair::PrefixSpans ps(*mp.prefix_len, mp.prefix_blocks, mp.splits, kStepPages);
   __syncthreads();
-  const int before = s_sched[0], mine = s_sched[1], total = s_sched[2];
+  int before = 0, mine = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kGroupThreads / 32; ++w) {
+    before += s_sched[w][0];
+    mine += s_sched[w][1];
+    total += s_sched[w][2];
+  }
   const int per = span_pages(total, p.grid_x, p.min_pages);
   const int g0 = mine > 0 ? (before + kSeqWeight) / per : 0;
   const int g1 = mine > 0 ? (before + kSeqWeight + mine - 1) / per : -1;
@@ -82,76 +96,73 @@ __global__ void __launch_bounds__(kCombineWarps * 32) merge_kernel(const __grid_
     if (threadIdx.x == 0) report(p.status, ATTN_DEV_INTERNAL);  // cannot happen: partials beyond the workspace
     own = 0;
   }
-  const prefill_pair::PrefixSpans ps(*mp.prefix_len, mp.prefix_blocks, mp.splits, kStepPages);
   const int ns = ps.used + own;
 
   // partial i: prefix span i, or block g0 + i - used of the own positions
   const size_t rows = static_cast<size_t>(p.batch) * Hq;
   const float* pre_o = mp.part_o + row * kD + d0;
-  const float2* pre_ml = mp.part_ml + (slice / (kSlices / kPrefixSlices)) * rows + row;
+  const float2* pre_ml = mp.part_ml + (d0 / (kD / kPrefixSlices)) * rows + row;
   const float* own_o = p.part_o + ((static_cast<size_t>(g0) + b) * Hq + h) * kD + d0;
   const float2* own_ml = p.part_ml + (static_cast<size_t>(g0) + b) * Hq + h;
-  float wm = -INFINITY, wl = 0.f;
-  float4 wo = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int r0 = warp; r0 < ns; r0 += kCombineWarps * kPerWarp) {
-    float2 e[kPerWarp];
-    float4 a[kPerWarp];
+
+  wait_for_primary_grid();
+  allow_dependent_launch();
+  float M = -INFINITY, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r0 = group; r0 < ns; r0 += kMergeGroups * kInFlight) {
+    float2 e[kInFlight];
+    float4 a[kInFlight];
 #pragma unroll
-    for (int j = 0; j < kPerWarp; ++j) {
-      const int i = r0 + j * kCombineWarps;
+    for (int j = 0; j < kInFlight; ++j) {
+      const int i = r0 + j * kMergeGroups;
       e[j] = make_float2(-INFINITY, 0.f);
       a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < ps.used) {
         e[j] = pre_ml[static_cast<size_t>(i) * kPrefixSlices * rows];
-        a[j] = *reinterpret_cast<const float4*>(pre_o + static_cast<size_t>(i) * rows * kD);
+        a[j] = __ldcs(reinterpret_cast<const float4*>(pre_o + static_cast<size_t>(i) * rows * kD));
       } else if (i < ns) {
         e[j] = own_ml[static_cast<size_t>(i - ps.used) * Hq];
-        a[j] = *reinterpret_cast<const float4*>(own_o + static_cast<size_t>(i - ps.used) * Hq * kD);
+        a[j] = __ldcs(reinterpret_cast<const float4*>(own_o + static_cast<size_t>(i - ps.used) * Hq * kD));
       }
-    }
-    float rm = wm;
-#pragma unroll
-    for (int j = 0; j < kPerWarp; ++j)
       if (e[j].y != e[j].y) e[j] = make_float2(INFINITY, 1.f);  // a NaN sum has to show: inf - inf below
+    }
+    float m = M;
 #pragma unroll
-    for (int j = 0; j < kPerWarp; ++j)
-      if (e[j].y > 0.f) rm = fmaxf(rm, e[j].x);
-    if (rm == -INFINITY) continue;
-    const float cw = wm == -INFINITY ? 0.f : exp2f(wm - rm);
-    wl *= cw;
-    wo.x *= cw; wo.y *= cw; wo.z *= cw; wo.w *= cw;
+    for (int j = 0; j < kInFlight; ++j)
+      if (e[j].y > 0.f) m = fmaxf(m, e[j].x);
+    if (m == -INFINITY) continue;
+    const float f = M == -INFINITY ? 0.f : exp2f(M - m);
+    L *= f;
+    O.x *= f; O.y *= f; O.z *= f; O.w *= f;
 #pragma unroll
-    for (int j = 0; j < kPerWarp; ++j) {
+    for (int j = 0; j < kInFlight; ++j) {
       if (e[j].y > 0.f) {
-        const float w = exp2f(e[j].x - rm);
-        wl += w * e[j].y;
-        wo.x += w * a[j].x; wo.y += w * a[j].y; wo.z += w * a[j].z; wo.w += w * a[j].w;
+        const float w = exp2f(e[j].x - m);
+        L += w * e[j].y;
+        O.x += w * a[j].x; O.y += w * a[j].y; O.z += w * a[j].z; O.w += w * a[j].w;
       }
     }
-    wm = rm;
+    M = m;
   }
-
-  if (lane == 0) s_max[warp] = wm;
+  s_m[group][tid] = M;
+  s_l[group][tid] = L;
+  s_o[group][tid] = O;
   __syncthreads();
-  float M = s_max[0];
+  if (group != 0) return;
+  float m = M;
 #pragma unroll
-  for (int w = 1; w < kCombineWarps; ++w) M = fmaxf(M, s_max[w]);
-  const float f = (M == -INFINITY || wm == -INFINITY) ? 0.f : exp2f(wm - M);
-  if (lane == 0) s_l[warp] = f * wl;
-  s_o[warp][lane] = make_float4(f * wo.x, f * wo.y, f * wo.z, f * wo.w);
-  __syncthreads();
-  if (warp == 0) {
-    float L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int w = 1; w < kMergeGroups; ++w) m = fmaxf(m, s_m[w][tid]);
+  L = 0.f;
+  O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kCombineWarps; ++w) {
-      L += s_l[w];
-      const float4 v = s_o[w][lane];
-      O.x += v.x; O.y += v.y; O.z += v.z; O.w += v.w;
-    }
-    const float inv = L > 0.f ? 1.f / L : 0.f;  // 0: no visible position at all
-    store_out4(p, row * kD + d0, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+  for (int w = 0; w < kMergeGroups; ++w) {
+    const float f = s_m[w][tid] == -INFINITY ? 0.f : exp2f(s_m[w][tid] - m);
+    const float4 v = s_o[w][tid];
+    L += f * s_l[w][tid];
+    O.x += f * v.x; O.y += f * v.y; O.z += f * v.z; O.w += f * v.w;
   }
+  const float inv = L > 0.f ? 1.f / L : L;  // 0: no visible position at all
+  store_out4(p, row * kD + d0, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
 }
 
 }  // namespace prefix

@@ -426,11 +426,13 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
 
   using C = PrefixConfig;
   const auto prefix_kernel = pda::prefill_pair::prefill_pair_kernel<C, pda::prefill_pair::PrefixParams>;
-  const auto merge_kernel = pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS>;
-  static bool pre_set[kMaxDevices] = {false}, dec_set[kMaxDevices] = {false}, merge_set[kMaxDevices] = {false};
+  const bool few_rows = batch * ATTN_GLOBAL_HQ <= 2 * num_sms;  // the merge's blocks are resident at once
+  const auto merge_kernel = few_rows ? pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, 4>
+                                     : pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, 2>;
+  static bool pre_set[kMaxDevices] = {false}, dec_set[kMaxDevices] = {false}, merge_set[2][kMaxDevices] = {{false}};
   if ((st = ensure_smem(prefix_kernel, C::kSmemBytes, dev, pre_set)) ||
       (st = ensure_smem(pda::global::decode_kernel_partial, pda::global::kSmemBytes, dev, dec_set)) ||
-      (st = ensure_smem(merge_kernel, 0, dev, merge_set)))
+      (st = ensure_smem(merge_kernel, 0, dev, merge_set[few_rows])))
     return st;
   CUtensorMap tm_pk, tm_pv, tm_k, tm_v;
   if ((st = encode_chunk_map(&tm_pk, k_pool, num_pages, C::kHkv * C::kD, C::kKBoxChunks)) ||
@@ -447,8 +449,7 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
     e = launch_pdl(pda::global::decode_kernel_partial, dim3(plan.own.grid_x), pda::global::kThreads,
                    pda::global::kSmemBytes, s, tm_k, tm_v, p);
   if (e == cudaSuccess)
-    e = launch_pdl(merge_kernel, dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / pda::kCombineCols), batch),
-                   pda::kCombineWarps * 32, 0, s, mp);
+    e = launch_pdl(merge_kernel, dim3(ATTN_GLOBAL_HQ, batch), (few_rows ? 4 : 2) * pda::prefix::kGroupThreads, 0, s, mp);
   return launched(name, e);
 }
 
