@@ -125,6 +125,17 @@ int32_t attn_step_add_kv_append_global_fp8(attn_step* step, const void* qkv, con
                                            void* q_out, void* k_pool, void* v_pool, uint8_t* k_scale,
                                            uint8_t* v_scale, int32_t batch, int32_t total_q, int32_t max_blocks,
                                            int64_t num_pages, int32_t* status);
+int32_t attn_step_add_kv_read_sliding_fp8(attn_step* step, const void* k_pool, const void* v_pool,
+                                          const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                                          const int32_t* seq_lens, void* k_out, void* v_out,
+                                          const int32_t* out_table, int32_t batch, int32_t max_blocks,
+                                          int64_t num_pages, int64_t out_pages, int32_t max_seq_len, int32_t span,
+                                          int32_t* status);
+int32_t attn_step_add_kv_read_global_fp8(attn_step* step, const void* k_pool, const void* v_pool,
+                                         const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                                         const int32_t* seq_lens, void* k_out, void* v_out, const int32_t* out_table,
+                                         int32_t batch, int32_t max_blocks, int64_t num_pages, int64_t out_pages,
+                                         int32_t max_seq_len, int32_t span, int32_t* status);
 int32_t attn_step_add_decode_sliding_fp8(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
                                          const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
                                          const int32_t* seq_lens, void* o, int32_t batch, int32_t max_blocks,

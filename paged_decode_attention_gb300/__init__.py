@@ -64,7 +64,8 @@ EXPORTS = ("attn_decode_sliding", "attn_decode_global", "attn_decode_global_shar
            "attn_step_add_kv_append_global_chunk", "attn_step_add_kv_append_sliding_fp8",
            "attn_step_add_kv_append_global_fp8", "attn_step_add_decode_sliding_fp8",
            "attn_step_add_decode_global_fp8", "attn_decode_global_prefix", "attn_decode_prefix_plan",
-           "attn_decode_prefix_workspace_size", "attn_step_add_decode_global_prefix")
+           "attn_decode_prefix_workspace_size", "attn_step_add_decode_global_prefix",
+           "attn_step_add_kv_read_sliding_fp8", "attn_step_add_kv_read_global_fp8")
 # attn_step launch modes (attn_step.h)
 STEP_LAUNCH_AUTO, STEP_LAUNCH_GRAPH, STEP_LAUNCH_DIRECT = 0, 1, 2
 STEP_LAUNCH_MODES = {"auto": STEP_LAUNCH_AUTO, "graph": STEP_LAUNCH_GRAPH, "direct": STEP_LAUNCH_DIRECT}
@@ -146,10 +147,9 @@ def load(path=None):
         for name in names:
             getattr(lib, name).restype = c_i32
             getattr(lib, name).argtypes = types
-            if types is not read8:
-                step_name = name.replace("attn_", "attn_step_add_")
-                getattr(lib, step_name).restype = c_i32
-                getattr(lib, step_name).argtypes = [c_vp] + types[:-1]
+            step_name = name.replace("attn_", "attn_step_add_")
+            getattr(lib, step_name).restype = c_i32
+            getattr(lib, step_name).argtypes = [c_vp] + types[:-1]
     c_step = ctypes.c_void_p
     lib.attn_step_create.restype = c_i32
     lib.attn_step_create.argtypes = [ctypes.POINTER(c_step)]
@@ -415,6 +415,12 @@ class Step:
     def add_kv_append_global_fp8(self, *args, **kw):
         return self._add(*_append_fp8_args(KIND_GLOBAL, *args, **kw))
 
+    def add_kv_read_sliding_fp8(self, *args, **kw):
+        return self._add(*_read_fp8_args(KIND_SLIDING, *args, **kw))
+
+    def add_kv_read_global_fp8(self, *args, **kw):
+        return self._add(*_read_fp8_args(KIND_GLOBAL, *args, **kw))
+
     def add_decode_sliding_fp8(self, *args, **kw):
         return self._add(*_decode_fp8_args(KIND_SLIDING, *args, **kw))
 
@@ -633,9 +639,9 @@ def selftest_delayed_copy(dst, src, delay_ns=5000, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# Chunk appends and the 8-bit cache (include/attn_fp8.h).  Every call has three
-# forms: the one-shot function, prepare_* (a PreparedCall for buffers used
-# again and again) and, but for the read, Step.add_*.
+# Chunk appends, the 8-bit cache (include/attn_fp8.h) and the decode behind a
+# shared prefix.  Every call has three forms: the one-shot function, prepare_*
+# (a PreparedCall for buffers used again and again) and Step.add_*.
 # ---------------------------------------------------------------------------
 
 FP8 = torch.float8_e4m3fn    # cache values
@@ -643,25 +649,23 @@ E8M0 = torch.float8_e8m0fnu  # cache scales: 2^(byte - 127)
 
 
 class PreparedCall:
-    """A call whose arguments are checked and marshalled once, as PreparedDecode does for a decode.
+    """A call on buffers that are used again and again: checked, marshalled and recorded once.
 
-    ``run(stream)`` enqueues it with one C call and returns its output; the
-    tensors must stay in place (the object keeps them alive), their contents
-    may change between runs.
+    Construction records the call's kernel launches (attn_step, direct mode),
+    tensor maps included; ``run(stream)`` enqueues them with one C call and
+    returns the call's output.  The tensors must stay in place (the object
+    keeps them alive), their contents may change between runs.
     """
 
     def __init__(self, fn_name, args, keep, out, device):
-        self._fn = getattr(load(), fn_name)
-        self._args, self._keep, self.out, self._device = args, keep, out, device
+        self._step = Step()
+        self._step._add(fn_name, args, keep, out, device)
+        self._step.finalize("direct")
+        self._launch, self._handle, self._device, self.out = load().attn_step_launch, self._step._h, device, out
 
     def run(self, stream=None):
         """Enqueue the call on `stream` (default: the current stream of its device); returns its output."""
-        s_ptr = _stream_ptr(stream, self._device)
-        if torch.cuda.current_device() == self._device.index:
-            st = self._fn(*self._args, s_ptr)
-        else:
-            with torch.cuda.device(self._device):
-                st = self._fn(*self._args, s_ptr)
+        st = self._launch(self._handle, _stream_ptr(stream, self._device))
         if st != ATTN_OK:
             raise AttnDecodeError(st, attn_last_error())
         return self.out
@@ -860,8 +864,14 @@ def _prefix_args(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_l
     return "attn_decode_global_prefix", args, keep, o, device
 
 
-def _once(stream, prepared):
-    return PreparedCall(*prepared).run(stream)
+def _once(stream, call):
+    fn_name, args, _, out, device = call
+    s_ptr = _stream_ptr(stream, device)
+    with torch.cuda.device(device):
+        st = getattr(load(), fn_name)(*args, s_ptr)
+    if st != ATTN_OK:
+        raise AttnDecodeError(st, attn_last_error())
+    return out
 
 
 def attn_kv_append_sliding_chunk(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out=None, *,

@@ -13,16 +13,23 @@
 // Bound by memory: a sliding token moves 32 KB (28 KB with an 8-bit cache), a
 // global one 35 KB (34 KB).  So every byte is read once and written once, and
 // the arithmetic that several rows share is done once: a block of 8 warps
-// takes one token at a time, each thread below kPairs turns one pair's angle
-// into (cos, sin) for all of the token's heads, and each warp holds the norm
-// weights of its lanes in registers for as long as the block lives.  The pair
+// takes kTokens tokens at a time, each thread below kTokens kPairs turns one
+// pair's angle into (cos, sin) for all heads of its token, one barrier a round.  The pair
 // frequencies theta^(-2i/D) are products of at most 7 host-computed factors
 // (one per set bit of i, in float pairs: 2^-43 relative), formed before the
-// block waits for the previous kernel; the angles are rope.cuh's.
+// block waits for the previous kernel; the angles are rope.cuh's.  The row
+// arithmetic runs on pairs of dims (packed fp32 instructions).
 //
 // Warp w of a sliding token takes q heads 2w and 2w+1, key head w and value
 // head w; of a global one q heads 2w and 2w+1, and the warp that t mod 8
-// names also the key/value head.  Lane l holds dims [V l, V l + V) and their
+// names also the key/value head: one warp in eight has half as much again to
+// do, and the others wait for it at the barrier.  So global layers take two
+// tokens a round once there are more tokens than SMs (2432 tokens 18.9 -> 16.8 us,
+// 304 tokens 4.6 -> 3.7 us; 64 tokens, on half as many SMs, 3.0 -> 3.7 us) and
+// one below; sliding layers always one (8192 tokens: 43.3 us, 0.91 of the
+// measured copy rate, against 44.7 us).  Tasks that each warp takes on its own,
+// without barrier or shared angles, were slower on both (46.4 us sliding; 34.8
+// against 27.0 us for 4096 global tokens into an 8-bit cache).  Lane l holds dims [V l, V l + V) and their
 // rotation partners, V = D / 64, as in kv_append.cuh.
 #pragma once
 
@@ -32,11 +39,9 @@
 namespace pda {
 namespace chunk {
 
-using append::Row;
-
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlocksPerSm = 4;
+constexpr int kMaxTokens = 2;  // per round of a block
 constexpr int kPairBits = 7;  // pairs 0..127
 
 struct ChunkParams {
@@ -63,7 +68,10 @@ struct ChunkParams {
 
 struct Smem {
   int32_t cu_q[kMaxBatch + 1];
-  alignas(16) float2 turn[2][1 << kPairBits];  // (cos, sin) of the token's pairs, double-buffered
+  int32_t len[kMaxBatch];
+  // cos and sin of the tokens' pairs, double-buffered
+  alignas(16) float cos[2][kMaxTokens][1 << kPairBits];
+  alignas(16) float sin[2][kMaxTokens][1 << kPairBits];
 };
 
 // One row as raw bf16 words: dims [V l, +V) and [D/2 + V l, +V).
@@ -90,53 +98,107 @@ __device__ __forceinline__ void load_raw(const __nv_bfloat16* src, RawRow<kD>& r
   }
 }
 
+// The row in fp32, pairs of dims.
+template <int kD>
+struct Row {
+  static constexpr int kWords = kD / 64 / 2;  // per half
+  float2 lo[kWords], hi[kWords];
+};
+
 template <int kD>
 __device__ __forceinline__ void widen(const RawRow<kD>& r, Row<kD>& x) {
 #pragma unroll
   for (int j = 0; j < RawRow<kD>::kWords; ++j) {
-    const float2 a = bf16x2_to_float2(r.lo[j]), b = bf16x2_to_float2(r.hi[j]);
-    x.lo[2 * j] = a.x; x.lo[2 * j + 1] = a.y;
-    x.hi[2 * j] = b.x; x.hi[2 * j + 1] = b.y;
+    x.lo[j] = bf16x2_to_float2(r.lo[j]);
+    x.hi[j] = bf16x2_to_float2(r.hi[j]);
   }
 }
 
-// Rotation by the token's shared (cos, sin) table; kPairs is a multiple of V.
+// x / sqrt(mean(x^2) + eps)
+template <int kD>
+__device__ __forceinline__ void normalise(Row<kD>& r, float eps) {
+  float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < Row<kD>::kWords; ++j) ss = __ffma2_rn(r.lo[j], r.lo[j], __ffma2_rn(r.hi[j], r.hi[j], ss));
+  float sum = ss.x + ss.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = rsqrtf(sum / static_cast<float>(kD) + eps);
+  const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+  for (int j = 0; j < Row<kD>::kWords; ++j) {
+    r.lo[j] = __fmul2_rn(r.lo[j], inv2);
+    r.hi[j] = __fmul2_rn(r.hi[j], inv2);
+  }
+}
+
+template <int kD>
+__device__ __forceinline__ void scale(Row<kD>& r, const Row<kD>& w) {
+#pragma unroll
+  for (int j = 0; j < Row<kD>::kWords; ++j) {
+    r.lo[j] = __fmul2_rn(r.lo[j], w.lo[j]);
+    r.hi[j] = __fmul2_rn(r.hi[j], w.hi[j]);
+  }
+}
+
+// Rotation by the token's shared tables; kPairs is a multiple of V.
 template <int kD, int kPairs>
-__device__ __forceinline__ void rotate(const float2* turn, Row<kD>& r) {
+__device__ __forceinline__ void rotate(const float* cs, const float* sn, Row<kD>& r) {
   constexpr int kV = kD / 64;
   const int lane = threadIdx.x & 31;
   if (kV * lane >= kPairs) return;
-  const float4* t4 = reinterpret_cast<const float4*>(turn + kV * lane);
 #pragma unroll
-  for (int j = 0; j < kV; j += 2) {
-    const float4 t = t4[j / 2];  // cos, sin of pairs j, j + 1
-    const float a0 = r.lo[j], b0 = r.hi[j], a1 = r.lo[j + 1], b1 = r.hi[j + 1];
-    r.lo[j] = a0 * t.x - b0 * t.y;
-    r.hi[j] = b0 * t.x + a0 * t.y;
-    r.lo[j + 1] = a1 * t.z - b1 * t.w;
-    r.hi[j + 1] = b1 * t.z + a1 * t.w;
+  for (int j = 0; j < kV / 2; ++j) {
+    const float2 c = *reinterpret_cast<const float2*>(cs + kV * lane + 2 * j);
+    const float2 t = *reinterpret_cast<const float2*>(sn + kV * lane + 2 * j);
+    const float2 a = r.lo[j], b = r.hi[j];
+    r.lo[j] = __ffma2_rn(make_float2(-b.x, -b.y), t, __fmul2_rn(a, c));
+    r.hi[j] = __ffma2_rn(a, t, __fmul2_rn(b, c));
+  }
+}
+
+template <int kD>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const Row<kD>& r) {
+  constexpr int kV = kD / 64;
+  const int lane = threadIdx.x & 31;
+  uint32_t lo[kV / 2], hi[kV / 2];
+#pragma unroll
+  for (int j = 0; j < kV / 2; ++j) {
+    lo[j] = pack_bf16x2(r.lo[j].x, r.lo[j].y);
+    hi[j] = pack_bf16x2(r.hi[j].x, r.hi[j].y);
+  }
+  if constexpr (kV == 8) {
+    *reinterpret_cast<uint4*>(dst + kV * lane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(dst + kD / 2 + kV * lane) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  } else {
+    *reinterpret_cast<uint2*>(dst + kV * lane) = make_uint2(lo[0], lo[1]);
+    *reinterpret_cast<uint2*>(dst + kD / 2 + kV * lane) = make_uint2(hi[0], hi[1]);
   }
 }
 
 // The row as e4m3 with its scale byte (fp8.cuh).
 template <int kD>
-__device__ __forceinline__ void store_fp8(uint8_t* dst, uint8_t* scale, const Row<kD>& r) {
+__device__ __forceinline__ void store_fp8(uint8_t* dst, uint8_t* scale, Row<kD>& r) {
   constexpr int kV = kD / 64;
   const int lane = threadIdx.x & 31;
   uint32_t amax = 0;  // non-negative floats order like their bits; a NaN lies above everything
 #pragma unroll
-  for (int j = 0; j < kV; ++j) {
-    const uint32_t a = __float_as_uint(r.lo[j]) & 0x7fffffffu, b = __float_as_uint(r.hi[j]) & 0x7fffffffu;
+  for (int j = 0; j < kV / 2; ++j) {
+    const uint32_t a = max(__float_as_uint(r.lo[j].x) & 0x7fffffffu, __float_as_uint(r.lo[j].y) & 0x7fffffffu);
+    const uint32_t b = max(__float_as_uint(r.hi[j].x) & 0x7fffffffu, __float_as_uint(r.hi[j].y) & 0x7fffffffu);
     amax = max(amax, max(a, b));
   }
   amax = __reduce_max_sync(0xffffffffu, amax);
   float inv;
   const uint32_t s = fp8::scale_byte(amax, inv);
+  const float2 inv2 = make_float2(inv, inv);
   uint32_t lo[kV / 4], hi[kV / 4];
 #pragma unroll
   for (int j = 0; j < kV / 4; ++j) {
-    lo[j] = fp8::pack_e4m3x4(r.lo[4 * j] * inv, r.lo[4 * j + 1] * inv, r.lo[4 * j + 2] * inv, r.lo[4 * j + 3] * inv);
-    hi[j] = fp8::pack_e4m3x4(r.hi[4 * j] * inv, r.hi[4 * j + 1] * inv, r.hi[4 * j + 2] * inv, r.hi[4 * j + 3] * inv);
+    const float2 a = __fmul2_rn(r.lo[2 * j], inv2), b = __fmul2_rn(r.lo[2 * j + 1], inv2);
+    const float2 c = __fmul2_rn(r.hi[2 * j], inv2), d = __fmul2_rn(r.hi[2 * j + 1], inv2);
+    lo[j] = fp8::pack_e4m3x4(a.x, a.y, b.x, b.y);
+    hi[j] = fp8::pack_e4m3x4(c.x, c.y, d.x, d.y);
   }
   if constexpr (kV == 8) {
     *reinterpret_cast<uint2*>(dst + kV * lane) = make_uint2(lo[0], lo[1]);
@@ -148,111 +210,134 @@ __device__ __forceinline__ void store_fp8(uint8_t* dst, uint8_t* scale, const Ro
   if (lane == 0) *scale = static_cast<uint8_t>(s);
 }
 
-template <int kD, int kHq, int kHkv, int kPairs, bool kShared, bool kFp8>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) chunk_kernel(const __grid_constant__ ChunkParams p) {
+// Blocks per SM that the registers of kTokens tokens' rows allow.
+template <int kTokens>
+constexpr int kBlocksPerSm = kTokens == 1 ? 3 : 2;
+
+template <int kD, int kHq, int kHkv, int kPairs, bool kShared, bool kFp8, int kTokens>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<kTokens>) chunk_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int kRowLen = kHq * kD + (kShared ? kD : 2 * kHkv * kD);
   static_assert(kHq == 2 * kWarps && (kShared ? kHkv == 1 : kHkv == kWarps), "rows of a token by warp");
-  static_assert(kPairs <= kThreads && kPairs <= (1 << kPairBits) && kPairs % (kD / 64) == 0, "pairs by thread");
+  static_assert(kTokens * kPairs <= kThreads && kPairs <= (1 << kPairBits) && kPairs % (kD / 64) == 0, "pairs by thread");
   __shared__ Smem s;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
   // this thread's pair frequency, while the previous kernel finishes
   FloatPair freq{1.f, 0.f};
-  if (threadIdx.x < kPairs) {
 #pragma unroll
-    for (int k = 0; k < kPairBits; ++k)
-      if ((threadIdx.x >> k) & 1) freq = df_mul(freq, p.bit_factor[k]);
-  }
+  for (int k = 0; k < kPairBits; ++k)
+    if ((threadIdx.x % kPairs >> k) & 1) freq = df_mul(freq, p.bit_factor[k]);
   // The previous kernel in the stream may still be writing qkv, the lengths
   // or the tables, or reading the cache.
   wait_for_primary_grid();
   allow_dependent_launch();
-  for (int i = threadIdx.x; i <= p.batch; i += kThreads) s.cu_q[i] = p.cu_q[i];
+  for (int i = threadIdx.x; i <= p.batch; i += kThreads) {
+    s.cu_q[i] = p.cu_q[i];
+    if (i < p.batch) s.len[i] = p.seq_lens[i];
+  }
   RawRow<kD> wq_raw, wk_raw;
   load_raw<kD>(p.w_q, wq_raw);
   load_raw<kD>(p.w_k, wk_raw);
   __syncthreads();
 
   int buf = 0;
-  for (int t = blockIdx.x; t < p.total_q; t += gridDim.x) {
-    // the token's sequence: the number of sequences that end at or before t
-    // (the same in every warp of the block)
-    int b = 0;
-    for (int j0 = 0; j0 < p.batch; j0 += 32) {
-      const int j = j0 + lane;
-      b += __popc(__ballot_sync(0xffffffffu, j < p.batch && s.cu_q[j + 1] <= t));
-    }
-    if (b >= p.batch) continue;  // rows behind the last sequence are left alone
-    const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1];
-    const int L = p.seq_lens[b];
-    const int n = q1 - q0;
-    const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
-    // a sequence whose numbers do not fit together is left alone as a whole
-    if (q0 < 0 || t < q0 || q1 > p.total_q || n > L || L > cap) {
-      if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
-      continue;
-    }
-    const int pos = L - n + (t - q0);
-    const __nv_bfloat16* row = p.qkv + static_cast<size_t>(t) * kRowLen;
-
-    // this warp's rows, all in flight together
-    const bool has_kv = !kShared || warp == (t & (kWarps - 1));
-    RawRow<kD> rq[2], rk, rv;
-    load_raw<kD>(row + (2 * warp) * kD, rq[0]);
-    load_raw<kD>(row + (2 * warp + 1) * kD, rq[1]);
-    if (has_kv) load_raw<kD>(row + (kHq + (kShared ? 0 : warp)) * kD, rk);
-    if constexpr (!kShared) load_raw<kD>(row + (kHq + kHkv + warp) * kD, rv);
-    const int32_t phys = has_kv ? p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kPage] : 0;
-
-    if (threadIdx.x < kPairs) {
-      float c, sn;
-      rope_angle(p.two_pi, freq, pos, c, sn);
-      s.turn[buf][threadIdx.x] = make_float2(c, sn);
-    }
-    __syncthreads();  // one per token: the buffer written next was read before this barrier
-    const float2* turn = s.turn[buf];
-    buf ^= 1;
-
-    Row<kD> x, w;
-    widen<kD>(wq_raw, w);
+  for (int t0 = blockIdx.x * kTokens; t0 < p.total_q; t0 += gridDim.x * kTokens) {
+    // this warp's rows of both tokens, all in flight together
+    RawRow<kD> rq[kTokens][2], rk[kTokens], rv[kTokens];
+    int pos[kTokens];  // -1: the token is left alone
+    int32_t phys[kTokens];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      widen<kD>(rq[i], x);
-      append::normalise<kD>(x, p.eps);
-      append::scale<kD>(x, w);
-      rotate<kD, kPairs>(turn, x);
-      append::store_row<kD>(p.q_out + (static_cast<size_t>(t) * kHq + 2 * warp + i) * kD, x);
+    for (int n = 0; n < kTokens; ++n) {
+      const int t = t0 + n;
+      pos[n] = -1;
+      phys[n] = 0;
+      if (t >= p.total_q) continue;
+      const __nv_bfloat16* row = p.qkv + static_cast<size_t>(t) * kRowLen;
+      const bool has_kv = !kShared || warp == (t & (kWarps - 1));
+      load_raw<kD>(row + (2 * warp) * kD, rq[n][0]);
+      load_raw<kD>(row + (2 * warp + 1) * kD, rq[n][1]);
+      if (has_kv) load_raw<kD>(row + (kHq + (kShared ? 0 : warp)) * kD, rk[n]);
+      if constexpr (!kShared) load_raw<kD>(row + (kHq + kHkv + warp) * kD, rv[n]);
+      // the token's sequence: the number of sequences that end at or before t
+      // (the same in every warp of the block)
+      int b = 0;
+      for (int j0 = 0; j0 < p.batch; j0 += 32) {
+        const int j = j0 + lane;
+        b += __popc(__ballot_sync(0xffffffffu, j < p.batch && s.cu_q[j + 1] <= t));
+      }
+      if (b >= p.batch) continue;  // rows behind the last sequence are left alone
+      const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1];
+      const int L = s.len[b];
+      const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
+      // a sequence whose numbers do not fit together is left alone as a whole
+      if (q0 < 0 || t < q0 || q1 > p.total_q || q1 - q0 > L || L > cap) {
+        if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+        continue;
+      }
+      pos[n] = L - (q1 - q0) + (t - q0);
+      if (has_kv) phys[n] = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos[n] / kPage];
     }
-    if (!has_kv) continue;
-    if (phys < 0 || static_cast<int64_t>(phys) >= p.num_pages) {
-      if (lane == 0) report(p.status, ATTN_DEV_BAD_PAGE);
-      continue;
+    if (threadIdx.x < kTokens * kPairs) {
+      const int n = threadIdx.x / kPairs;
+      int at = pos[0];
+#pragma unroll
+      for (int k = 1; k < kTokens; ++k) at = n == k ? pos[k] : at;
+      float c, sn;
+      rope_angle(p.two_pi, freq, at < 0 ? 0 : at, c, sn);
+      s.cos[buf][n][threadIdx.x % kPairs] = c;
+      s.sin[buf][n][threadIdx.x % kPairs] = sn;
     }
-    const int c = kShared ? 0 : warp;
-    const size_t off = ((static_cast<size_t>(phys) * kPage + pos % kPage) * kHkv + c) * kD;
-    const size_t soff = (static_cast<size_t>(phys) * kHkv + c) * kPage + pos % kPage;
-    const auto store = [&](void* pool, uint8_t* scales, const Row<kD>& y) {
-      if constexpr (kFp8)
-        store_fp8<kD>(static_cast<uint8_t*>(pool) + off, scales + soff, y);
-      else
-        append::store_row<kD>(static_cast<__nv_bfloat16*>(pool) + off, y);
-    };
-    if constexpr (!kShared) {
-      widen<kD>(rv, x);
-      append::normalise<kD>(x, p.eps);
-      store(p.v_pool, p.v_scale, x);
+    __syncthreads();  // one per round: the buffer written next was read before this barrier
+
+#pragma unroll
+    for (int n = 0; n < kTokens; ++n) {
+      if (pos[n] < 0) continue;
+      const int t = t0 + n;
+      const float* cs = s.cos[buf][n];
+      const float* sn = s.sin[buf][n];
+      Row<kD> x, w;
+      widen<kD>(wq_raw, w);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        widen<kD>(rq[n][i], x);
+        normalise<kD>(x, p.eps);
+        scale<kD>(x, w);
+        rotate<kD, kPairs>(cs, sn, x);
+        store_bf16<kD>(p.q_out + (static_cast<size_t>(t) * kHq + 2 * warp + i) * kD, x);
+      }
+      if (kShared && warp != (t & (kWarps - 1))) continue;
+      if (phys[n] < 0 || static_cast<int64_t>(phys[n]) >= p.num_pages) {
+        if (lane == 0) report(p.status, ATTN_DEV_BAD_PAGE);
+        continue;
+      }
+      const int c = kShared ? 0 : warp;
+      const int row = pos[n] % kPage;
+      const size_t off = ((static_cast<size_t>(phys[n]) * kPage + row) * kHkv + c) * kD;
+      const size_t soff = (static_cast<size_t>(phys[n]) * kHkv + c) * kPage + row;
+      const auto store = [&](void* pool, uint8_t* scales, Row<kD>& y) {
+        if constexpr (kFp8)
+          store_fp8<kD>(static_cast<uint8_t*>(pool) + off, scales + soff, y);
+        else
+          store_bf16<kD>(static_cast<__nv_bfloat16*>(pool) + off, y);
+      };
+      if constexpr (!kShared) {
+        widen<kD>(rv[n], x);
+        normalise<kD>(x, p.eps);
+        store(p.v_pool, p.v_scale, x);
+      }
+      widen<kD>(rk[n], x);
+      normalise<kD>(x, p.eps);
+      if constexpr (kShared) {
+        store(p.v_pool, p.v_scale, x);
+        if (p.k_pool == nullptr) continue;  // a values-only cache
+      }
+      widen<kD>(wk_raw, w);
+      scale<kD>(x, w);
+      rotate<kD, kPairs>(cs, sn, x);
+      store(p.k_pool, p.k_scale, x);
     }
-    widen<kD>(rk, x);
-    append::normalise<kD>(x, p.eps);
-    if constexpr (kShared) {
-      store(p.v_pool, p.v_scale, x);
-      if (p.k_pool == nullptr) continue;  // a values-only cache
-    }
-    widen<kD>(wk_raw, w);
-    append::scale<kD>(x, w);
-    rotate<kD, kPairs>(turn, x);
-    store(p.k_pool, p.k_scale, x);
+    buf ^= 1;
   }
 }
 

@@ -177,6 +177,26 @@ int32_t attn_step_add_decode_global_fp8(attn_step* step, const void* q, const vo
   }, "attn_step_add_decode_global_fp8");
 }
 
+int32_t attn_step_add_kv_read_sliding_fp8(attn_step* step, const void* k_pool, const void* v_pool,
+    const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* k_out,
+    void* v_out, const int32_t* out_table, int32_t batch, int32_t max_blocks, int64_t num_pages, int64_t out_pages,
+    int32_t max_seq_len, int32_t span, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_kv_read_sliding_fp8(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table, batch,
+        max_blocks, num_pages, out_pages, max_seq_len, span, status, s);
+  }, "attn_step_add_kv_read_sliding_fp8");
+}
+
+int32_t attn_step_add_kv_read_global_fp8(attn_step* step, const void* k_pool, const void* v_pool,
+    const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* k_out,
+    void* v_out, const int32_t* out_table, int32_t batch, int32_t max_blocks, int64_t num_pages, int64_t out_pages,
+    int32_t max_seq_len, int32_t span, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_kv_read_global_fp8(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table, batch,
+        max_blocks, num_pages, out_pages, max_seq_len, span, status, s);
+  }, "attn_step_add_kv_read_global_fp8");
+}
+
 int32_t attn_step_add_decode_global_prefix(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
     const int32_t* prefix_table, const int32_t* prefix_len, const int32_t* block_table, const int32_t* seq_lens,
     void* o, int32_t batch, int32_t prefix_blocks, int32_t max_blocks, int64_t num_pages, int32_t max_prefix_len,

@@ -279,6 +279,28 @@ def test_read_back_flags_bad_pages(cuda_lib):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_read_back_prepared_and_in_a_step(cuda_lib, kind):
+    c = Fp8Case(make_case(kind, [70, 5, 300], seed=48))
+    args = list(c.on(DEV))
+    shape = tuple(c.k.shape)
+    outs = [[torch.zeros(shape, dtype=torch.bfloat16, device=DEV) for _ in range(2)] for _ in range(3)]
+    name = "kv_read_%s_fp8" % kind
+    call = getattr(pda, "prepare_" + name)(*args[1:], *outs[1], span=100)
+    step = pda.Step()
+    getattr(step, "add_" + name)(*args[1:], *outs[2], span=100)
+    step.finalize()
+    for lens in ([70, 5, 300], [3, 0, 290]):  # contents change between runs
+        args[6].copy_(torch.tensor(lens, dtype=torch.int32))
+        getattr(pda, "attn_" + name)(*args[1:], *outs[0], span=100)
+        assert call.run()[0] is outs[1][0]
+        step.launch()
+        torch.cuda.synchronize()
+        for o in outs[1:]:
+            assert torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1])
+    step.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_streams_graphs_and_steps(cuda_lib, kind):
     # the same workspace by two captured graphs and a step in turn, contents changing between replays
     lens = [5, 700, 1300, 64]

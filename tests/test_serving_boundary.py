@@ -89,14 +89,13 @@ def bad_calls():
 def test_bad_arguments_are_refused_before_launch(lib, name, form, bad, code):
     assert call(lib, name, form, **bad) == code
     assert name in pda.attn_last_error()
-    if form != "read":  # the read is not part of a decode step
-        h = ctypes.c_void_p()
-        assert lib.attn_step_create(ctypes.byref(h)) == 0
-        try:
-            assert call(lib, name, form, step=h, **bad) == code
-            assert lib.attn_step_num_calls(h) == 0
-        finally:
-            lib.attn_step_destroy(h)
+    h = ctypes.c_void_p()
+    assert lib.attn_step_create(ctypes.byref(h)) == 0
+    try:
+        assert call(lib, name, form, step=h, **bad) == code
+        assert lib.attn_step_num_calls(h) == 0
+    finally:
+        lib.attn_step_destroy(h)
 
 
 @pytest.mark.parametrize("kind", ["sliding", "global"])
