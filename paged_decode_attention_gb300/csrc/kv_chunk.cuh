@@ -17,7 +17,8 @@
 // pair's angle into (cos, sin) for all heads of its token, one barrier a round.  The pair
 // frequencies theta^(-2i/D) are products of at most 7 host-computed factors
 // (one per set bit of i, in float pairs: 2^-43 relative), formed before the
-// block waits for the previous kernel; the angles are rope.cuh's.  The row
+// block waits for the previous kernel; the angles are exact to
+// 2^-24 of a half turn.  The row
 // arithmetic runs on pairs of dims (packed fp32 instructions).
 //
 // Warp w of a sliding token takes q heads 2w and 2w+1, key head w and value
@@ -62,7 +63,7 @@ struct ChunkParams {
   int32_t total_q;
   int32_t max_blocks;
   float eps;
-  TwoPi two_pi;
+  FloatPair inv_pi;
   FloatPair bit_factor[kPairBits];  // theta^(-2 * 2^k / D)
 };
 
@@ -73,6 +74,19 @@ struct Smem {
   alignas(16) float cos[2][kMaxTokens][1 << kPairBits];
   alignas(16) float sin[2][kMaxTokens][1 << kPairBits];
 };
+
+// pos * (f.hi + f.lo), a frequency in half turns, less its whole turns, in
+// [-1, 1]: for an integer 0 <= pos < 2^24 the float product and its fma remainder
+// hold pos * f.hi exactly, and subtracting an even integer is exact.  Off by
+// 2^-24 of a half turn; sincospif adds 2 units in the last place, where the
+// 2^-21 of __sincosf would move three times as many values across a border
+// of e4m3.
+__device__ __forceinline__ float half_turns(FloatPair f, int pos) {
+  const float fp = static_cast<float>(pos);  // exact
+  const float hi = fp * f.hi;
+  const float rest = fmaf(fp, f.lo, fmaf(fp, f.hi, -hi));
+  return fmaf(-2.f, rintf(0.5f * hi), hi) + rest;
+}
 
 // One row as raw bf16 words: dims [V l, +V) and [D/2 + V l, +V).
 template <int kD>
@@ -123,7 +137,9 @@ __device__ __forceinline__ void normalise(Row<kD>& r, float eps) {
   float sum = ss.x + ss.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = rsqrtf(sum / static_cast<float>(kD) + eps);
+  const float mean = sum / static_cast<float>(kD) + eps;
+  float inv = rsqrtf(mean);
+  inv = fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.f), inv);  // one Newton step: the root to its last bit
   const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
   for (int j = 0; j < Row<kD>::kWords; ++j) {
@@ -224,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<kTokens>) chunk_kernel(
   const int lane = threadIdx.x & 31;
 
   // this thread's pair frequency, while the previous kernel finishes
-  FloatPair freq{1.f, 0.f};
+  FloatPair freq = p.inv_pi;
 #pragma unroll
   for (int k = 0; k < kPairBits; ++k)
     if ((threadIdx.x % kPairs >> k) & 1) freq = df_mul(freq, p.bit_factor[k]);
@@ -284,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<kTokens>) chunk_kernel(
 #pragma unroll
       for (int k = 1; k < kTokens; ++k) at = n == k ? pos[k] : at;
       float c, sn;
-      rope_angle(p.two_pi, freq, at < 0 ? 0 : at, c, sn);
+      sincospif(half_turns(freq, at < 0 ? 0 : at), &sn, &c);
       s.cos[buf][n][threadIdx.x % kPairs] = c;
       s.sin[buf][n][threadIdx.x % kPairs] = sn;
     }

@@ -94,7 +94,7 @@ int32_t run_chunk(int32_t kind, bool fp8, const void* qkv, const void* w_q, cons
   p.total_q = total_q;
   p.max_blocks = max_blocks;
   p.eps = 1e-6f;
-  p.two_pi = split_two_pi();
+  p.inv_pi = split_float_pair(0.31830988618379067154);
   for (int k = 0; k < pda::chunk::kPairBits; ++k)
     p.bit_factor[k] = split_float_pair(std::pow(theta, -2.0 * (1 << k) / D));
 
@@ -160,13 +160,12 @@ int32_t run_read(int32_t kind, const void* k_pool, const void* v_pool, const uin
   p.dst[1] = static_cast<__nv_bfloat16*>(v_out);
   p.out_table = out_table;
   p.out_pages = out_pages;
-  // one wave of blocks, half for the keys and half for the values; no more
-  // than the (weighted) pages that max_seq_len allows
+  // no more blocks than the (weighted) pages that max_seq_len allows
   int64_t pages = (max_seq_len + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE;
   if (span > 0) pages = std::min<int64_t>(pages, (static_cast<int64_t>(span) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE + 1);
   const int64_t want = (pages + pda::kSeqWeight) * batch;
   p.d.grid_x = static_cast<int32_t>(
-      std::max<int64_t>(1, std::min<int64_t>(want, num_sms * pda::fp8_read::kBlocksPerSm / 2)));
+      std::max<int64_t>(1, std::min<int64_t>(want, num_sms * pda::fp8_read::kGridPerSm)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid(p.d.grid_x, 2);
   const cudaError_t e =
