@@ -388,7 +388,7 @@ int32_t attn_kv_append_global(const void* qkv, const void* w_q, const void* w_k,
  * block_table  int32 [batch, max_blocks]; only the pages of new tokens are read
  * seq_lens     int32 [batch], new tokens included; <= max_blocks*16
  * cu_q         int32 [batch + 1], cu_q[0] = 0, non-decreasing, cu_q[batch] <=
- *              total_q; rows behind cu_q[batch] are neither read nor written
+ *              total_q; rows behind cu_q[batch] are ignored (q_out keeps theirs)
  * q_out        bf16 [total_q, 16, D] (written)
  * k_pool, v_pool  the decode's pools; attn_kv_append_global_chunk: k_pool may
  *              be NULL for a values-only cache

@@ -86,8 +86,8 @@ int32_t attn_kv_read_global_fp8(const void* k_pool, const void* v_pool, const ui
 /*
  * attn_decode_sliding_fp8 / attn_decode_global_fp8 -- attn_decode_sliding and
  * attn_decode_global over an 8-bit cache: the same softmax over the keys and
- * values as they read back, with the same plan (attn_decode_plan,
- * attn_decode_workspace_size, attn_decode_launches).
+ * values as they read back.  num_splits as there; the automatic plan and the
+ * workspace are attn_decode_fp8_plan's.
  *
  * q is bf16.  Products run in f16 on e4m3 values (exact), scales are applied
  * in fp32, sums are fp32; the weights are rounded to f16 (2^-11 relative at
@@ -106,6 +106,20 @@ int32_t attn_decode_global_fp8(const void* q, const void* k_pool, const void* v_
                                int32_t batch, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len,
                                int32_t window, int32_t out_dtype, int32_t num_splits, void* workspace,
                                size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * attn_decode_fp8_plan -- the launch plan of the calls above, as pure host
+ * arithmetic: thread blocks per KV head, kernels launched (1 or 2) and workspace
+ * bytes (any of the three may be NULL) on a device of num_sms multiprocessors.
+ * Arguments and errors as attn_decode_plan.  attn_decode_fp8_workspace_size --
+ * the workspace for the current CUDA device (0, with attn_last_error, on bad
+ * arguments or when no device can be queried).
+ */
+int32_t attn_decode_fp8_plan(int32_t kind, int32_t batch, int32_t max_seq_len, int32_t window, int32_t num_splits,
+                             int32_t num_sms, int32_t* out_num_splits, int32_t* out_launches,
+                             size_t* out_workspace_bytes);
+size_t attn_decode_fp8_workspace_size(int32_t kind, int32_t batch, int32_t max_seq_len, int32_t window,
+                                      int32_t num_splits);
 
 #ifdef __cplusplus
 }

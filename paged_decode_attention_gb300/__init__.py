@@ -33,7 +33,8 @@ __all__ = [
     "attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk",
     "attn_kv_append_sliding_fp8", "attn_kv_append_global_fp8", "attn_kv_read_sliding_fp8", "attn_kv_read_global_fp8",
     "attn_decode_sliding_fp8", "attn_decode_global_fp8", "attn_decode_global_prefix", "attn_decode_prefix_plan",
-    "attn_decode_prefix_workspace_size", "prepare_decode_global_prefix", "new_fp8_cache", "PreparedCall",
+    "attn_decode_prefix_workspace_size", "attn_decode_fp8_plan", "attn_decode_fp8_workspace_size",
+    "prepare_decode_global_prefix", "new_fp8_cache", "PreparedCall",
     "prepare_kv_append_sliding_chunk", "prepare_kv_append_global_chunk", "prepare_kv_append_sliding_fp8",
     "prepare_kv_append_global_fp8", "prepare_kv_read_sliding_fp8", "prepare_kv_read_global_fp8",
     "prepare_decode_sliding_fp8", "prepare_decode_global_fp8",
@@ -65,7 +66,8 @@ EXPORTS = ("attn_decode_sliding", "attn_decode_global", "attn_decode_global_shar
            "attn_step_add_kv_append_global_fp8", "attn_step_add_decode_sliding_fp8",
            "attn_step_add_decode_global_fp8", "attn_decode_global_prefix", "attn_decode_prefix_plan",
            "attn_decode_prefix_workspace_size", "attn_step_add_decode_global_prefix",
-           "attn_step_add_kv_read_sliding_fp8", "attn_step_add_kv_read_global_fp8")
+           "attn_step_add_kv_read_sliding_fp8", "attn_step_add_kv_read_global_fp8", "attn_decode_fp8_plan",
+           "attn_decode_fp8_workspace_size")
 # attn_step launch modes (attn_step.h)
 STEP_LAUNCH_AUTO, STEP_LAUNCH_GRAPH, STEP_LAUNCH_DIRECT = 0, 1, 2
 STEP_LAUNCH_MODES = {"auto": STEP_LAUNCH_AUTO, "graph": STEP_LAUNCH_GRAPH, "direct": STEP_LAUNCH_DIRECT}
@@ -137,6 +139,11 @@ def load(path=None):
     lib.attn_decode_prefix_plan.restype = c_i32
     lib.attn_decode_prefix_plan.argtypes = [c_i32] * 6 + [ctypes.POINTER(c_i32), ctypes.POINTER(c_i32),
                                                           ctypes.POINTER(c_sz)]
+    lib.attn_decode_fp8_plan.restype = c_i32
+    lib.attn_decode_fp8_plan.argtypes = [c_i32] * 6 + [ctypes.POINTER(c_i32), ctypes.POINTER(c_i32),
+                                                       ctypes.POINTER(c_sz)]
+    lib.attn_decode_fp8_workspace_size.restype = c_sz
+    lib.attn_decode_fp8_workspace_size.argtypes = [c_i32] * 5
     lib.attn_decode_prefix_workspace_size.restype = c_sz
     lib.attn_decode_prefix_workspace_size.argtypes = [c_i32] * 5
     for names, types in ((("attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk"), chunk),
@@ -792,12 +799,32 @@ def _decode_fp8_args(kind, q, k_pool, v_pool, k_scale, v_scale, block_table, seq
               _ptr(seq_lens, "seq_lens", torch.int32, (batch,)), _ptr(o, "o", o.dtype, (batch, Hq, D))]
     if workspace is None:
         with torch.cuda.device(device):
-            workspace = new_workspace(attn_decode_workspace_size(kind, batch, max_seq_len, window, num_splits), device)
+            workspace = new_workspace(attn_decode_fp8_workspace_size(kind, batch, max_seq_len, window, num_splits),
+                                      device)
     keep = (q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o, workspace, status)
     args = tuple([q_ptr] + cache + tables) + (
         batch, max_blocks, n, int(max_seq_len), int(window), OUT_F32 if o.dtype == torch.float32 else OUT_BF16,
         int(num_splits), _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _status_ptr(status))
     return "attn_decode_%s_fp8" % _kind_name(kind), args, keep, o, device
+
+
+def attn_decode_fp8_plan(kind, batch, max_seq_len, window, num_splits=0, num_sms=152):
+    """(num_splits, launches, workspace_bytes) of attn_decode_*_fp8; pure host arithmetic."""
+    lib = load()
+    ns, n, ws = ctypes.c_int32(0), ctypes.c_int32(0), ctypes.c_size_t(0)
+    st = lib.attn_decode_fp8_plan(kind, batch, max_seq_len, window, num_splits, num_sms, ctypes.byref(ns),
+                                  ctypes.byref(n), ctypes.byref(ws))
+    if st != ATTN_OK:
+        raise AttnDecodeError(st, attn_last_error())
+    return ns.value, n.value, ws.value
+
+
+def attn_decode_fp8_workspace_size(kind, batch, max_seq_len, window, num_splits=0):
+    """Workspace bytes of attn_decode_*_fp8 for the current CUDA device."""
+    n = load().attn_decode_fp8_workspace_size(kind, batch, max_seq_len, window, num_splits)
+    if n == 0:
+        raise AttnDecodeError(1, attn_last_error())
+    return n
 
 
 def attn_decode_prefix_plan(batch, max_prefix_len, max_seq_len, num_splits=0, prefix_splits=0, num_sms=152):
@@ -929,7 +956,8 @@ def attn_decode_sliding_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, se
                             max_seq_len=None, out_dtype=torch.bfloat16, num_splits=0, workspace=None, status=None,
                             stream=None):
     """attn_decode_sliding over an 8-bit cache: q [B,16,256] bf16, pools [P,16,8,256] float8_e4m3fn, scales [P,8,16]
-    float8_e8m0fnu -> o [B,16,256].  Plan and workspace are attn_decode_sliding's."""
+    float8_e8m0fnu -> o [B,16,256].  workspace: at least
+    attn_decode_fp8_workspace_size(...) bytes from new_workspace; allocated per call when None."""
     return _once(stream, _decode_fp8_args(KIND_SLIDING, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o,
                                           window=window, max_seq_len=max_seq_len, out_dtype=out_dtype,
                                           num_splits=num_splits, workspace=workspace, status=status))
@@ -939,7 +967,8 @@ def attn_decode_global_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq
                            max_seq_len=None, out_dtype=torch.bfloat16, num_splits=0, workspace=None, status=None,
                            stream=None):
     """attn_decode_global over an 8-bit cache: q [B,16,512] bf16, pools [P,16,1,512] float8_e4m3fn, scales [P,1,16]
-    float8_e8m0fnu -> o [B,16,512].  Plan and workspace are attn_decode_global's."""
+    float8_e8m0fnu -> o [B,16,512].  workspace: at least
+    attn_decode_fp8_workspace_size(...) bytes from new_workspace; allocated per call when None."""
     return _once(stream, _decode_fp8_args(KIND_GLOBAL, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o,
                                           window=window, max_seq_len=max_seq_len, out_dtype=out_dtype,
                                           num_splits=num_splits, workspace=workspace, status=status))

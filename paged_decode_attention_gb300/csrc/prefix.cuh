@@ -11,7 +11,8 @@
 //     products run on tcgen05, 2048 flops x batch per byte pair;
 //   * the sequences' own positions with the decode kernel (global.cuh), every
 //     segment left as a partial;
-//   * this merge.
+//   * this merge, which also serves the 8-bit global decode (no prefix, and the
+//     rows that one block finished whole are left alone).
 //
 // One block per row b*Hq + h, a row's partials being its prefix spans followed
 // by its blocks of the balanced schedule: two or four groups of 128 threads,
@@ -41,6 +42,8 @@ struct MergeParams {
 constexpr int kGroupThreads = 128;
 constexpr int kInFlight = 4;  // partials in flight per thread
 
+// kPrefixSlices: slices of the output dims the prefix partials' (max, sum) come
+// in; 0 for no prefix.
 template <int kD, int kPrefixSlices, int kStepPages, int kMergeGroups>
 __global__ void __launch_bounds__(kMergeGroups* kGroupThreads) merge_kernel(const __grid_constant__ MergeParams mp) {
   const DecodeParams& p = mp.d;
@@ -79,7 +82,9 @@ __global__ void __launch_bounds__(kMergeGroups* kGroupThreads) merge_kernel(cons
       s_sched[tid >> 5][2] = total;
     }
   }
-  const prefill_pair::PrefixSpans ps(*mp.prefix_len, mp.prefix_blocks, mp.splits, kStepPages);
+  int used = 0;  // prefix spans
+  if constexpr (kPrefixSlices > 0)
+    used = prefill_pair::PrefixSpans(*mp.prefix_len, mp.prefix_blocks, mp.splits, kStepPages).used;
   __syncthreads();
   int before = 0, mine = 0, total = 0;
 #pragma unroll
@@ -96,12 +101,17 @@ __global__ void __launch_bounds__(kMergeGroups* kGroupThreads) merge_kernel(cons
     if (threadIdx.x == 0) report(p.status, ATTN_DEV_INTERNAL);  // cannot happen: partials beyond the workspace
     own = 0;
   }
-  const int ns = ps.used + own;
+  const int ns = used + own;
+  if (kPrefixSlices == 0 && own == 1) {  // one block held the whole sequence and wrote o
+    // (the grid must not complete before the decode grid: see combine.cuh)
+    if (blockIdx.x == 0 && blockIdx.y == 0) wait_for_primary_grid();
+    return;
+  }
 
   // partial i: prefix span i, or block g0 + i - used of the own positions
   const size_t rows = static_cast<size_t>(p.batch) * Hq;
   const float* pre_o = mp.part_o + row * kD + d0;
-  const float2* pre_ml = mp.part_ml + (d0 / (kD / kPrefixSlices)) * rows + row;
+  const float2* pre_ml = mp.part_ml + (kPrefixSlices > 0 ? d0 / (kD / (kPrefixSlices > 0 ? kPrefixSlices : 1)) * rows + row : 0);
   const float* own_o = p.part_o + ((static_cast<size_t>(g0) + b) * Hq + h) * kD + d0;
   const float2* own_ml = p.part_ml + (static_cast<size_t>(g0) + b) * Hq + h;
 
@@ -117,12 +127,12 @@ __global__ void __launch_bounds__(kMergeGroups* kGroupThreads) merge_kernel(cons
       const int i = r0 + j * kMergeGroups;
       e[j] = make_float2(-INFINITY, 0.f);
       a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < ps.used) {
+      if (i < used) {
         e[j] = pre_ml[static_cast<size_t>(i) * kPrefixSlices * rows];
         a[j] = __ldcs(reinterpret_cast<const float4*>(pre_o + static_cast<size_t>(i) * rows * kD));
       } else if (i < ns) {
-        e[j] = own_ml[static_cast<size_t>(i - ps.used) * Hq];
-        a[j] = __ldcs(reinterpret_cast<const float4*>(own_o + static_cast<size_t>(i - ps.used) * Hq * kD));
+        e[j] = own_ml[static_cast<size_t>(i - used) * Hq];
+        a[j] = __ldcs(reinterpret_cast<const float4*>(own_o + static_cast<size_t>(i - used) * Hq * kD));
       }
       if (e[j].y != e[j].y) e[j] = make_float2(INFINITY, 1.f);  // a NaN sum has to show: inf - inf below
     }

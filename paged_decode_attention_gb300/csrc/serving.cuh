@@ -46,6 +46,39 @@ int32_t launched(const char* name, cudaError_t e) {
 }
 
 // ---------------------------------------------------------------------------
+// Launch plan of the 8-bit decode and of the own positions behind a prefix:
+// make_plan's, but for the smallest spans.  A sequence that a block starts costs
+// it some 2 us (its q, its end), so many short sequences want a block each: the
+// grid covers the weighted list (a virtual page per sequence, common.cuh), and
+// spans go down to two pages.  A span cut off a long sequence costs the merge a
+// partial row, so where a sequence may have many pages the spans stay longer.
+// Global layers, automatic plan, two-page and four-page spans: 30 sequences of up
+// to 15 positions 7.9 and 11.7 us (19.0 with make_plan's four pages per block), 4 of
+// up to 600 8.2 and 10.9 us, one of 4000 11.0 and 9.3 us.
+// ---------------------------------------------------------------------------
+int32_t make_serving_plan(int32_t kind, int32_t batch, int32_t max_seq_len, int32_t window, int32_t forced_blocks,
+                          int32_t num_sms, Plan* out) {
+  const int32_t st = make_plan(kind, batch, max_seq_len, window, forced_blocks, num_sms, out);
+  if (st != ATTN_OK) return st;
+  const bool sliding = kind == ATTN_KIND_SLIDING;
+  int64_t pages = (max_seq_len + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE;
+  if (window > 0) pages = std::min<int64_t>(pages, (static_cast<int64_t>(window) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE + 1);
+  constexpr int kPartials = 32;  // per sequence, before spans grow
+  out->min_pages = static_cast<int>(std::min<int64_t>(4, std::max<int64_t>(2, (pages + kPartials - 1) / kPartials)));
+  if (forced_blocks == 0) {
+    const int64_t resident = sliding ? static_cast<int64_t>(num_sms) * pda::sliding::kBlocksPerSm / ATTN_SLIDING_HKV
+                                     : static_cast<int64_t>(num_sms) * pda::global::kBlocksPerSm;
+    const int64_t useful = ((pages + pda::kSeqWeight) * batch + out->min_pages - 1) / out->min_pages;
+    out->grid_x = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({resident, useful, pda::kMaxSplits})));
+  }
+  const int d = sliding ? ATTN_SLIDING_D : ATTN_GLOBAL_D;
+  const size_t rows = (static_cast<size_t>(out->grid_x) + batch) * (sliding ? ATTN_SLIDING_HQ : ATTN_GLOBAL_HQ);
+  out->part_o_bytes = align256(rows * d * sizeof(float));
+  out->workspace_bytes = ATTN_WORKSPACE_ZERO_BYTES + out->part_o_bytes + align256(rows * sizeof(float2));
+  return ATTN_OK;
+}
+
+// ---------------------------------------------------------------------------
 // Norms, RoPE and cache append of a chunk of tokens per sequence
 // ---------------------------------------------------------------------------
 int32_t run_chunk(int32_t kind, bool fp8, const void* qkv, const void* w_q, const void* w_k,
@@ -68,6 +101,7 @@ int32_t run_chunk(int32_t kind, bool fp8, const void* qkv, const void* w_q, cons
   int32_t st;
   if ((st = check_batch(name, batch, max_blocks)) || (st = check_pages(name, "num_pages", num_pages))) return st;
   if (total_q < 0) return fail(ATTN_ERR_INVALID_ARG, "%s: total_q must be >= 0", name);
+  if (total_q > 1 << 28) return fail(ATTN_ERR_UNSUPPORTED, "%s: total_q %d too large", name, total_q);
   g_last_launches = total_q > 0 ? 1 : 0;
   if (total_q == 0) return ATTN_OK;  // no tokens
   int dev = 0, num_sms = 0;
@@ -240,7 +274,7 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
   int dev = 0, num_sms = 0;
   if ((st = current_device(&dev, &num_sms)) != ATTN_OK) return st;
   Plan plan;
-  st = make_plan(kind, batch, max_seq_len, window, num_splits, num_sms, &plan);
+  st = make_serving_plan(kind, batch, max_seq_len, window, num_splits, num_sms, &plan);
   if (st != ATTN_OK) return st;
   if (!workspace || workspace_bytes < plan.workspace_bytes)
     return fail(ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)", name, plan.workspace_bytes,
@@ -293,16 +327,25 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
                      dim3(ATTN_SLIDING_HQ * (ATTN_SLIDING_D / pda::kCombineCols), batch), pda::kCombineWarps * 32, 0,
                      s, p);
   } else {
-    static bool smem_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false};
+    // Few rows may have many partials each: combine.cuh's four blocks per row
+    // (8 sequences of up to 8192 positions: 21.4 us a call, 23.9 with one block per
+    // row).  Many rows: one block per row (64 of 500: 22.5 us, against 29.4).
+    const bool few_rows = batch * ATTN_GLOBAL_HQ <= 2 * num_sms;
+    const auto merge_kernel = pda::prefix::merge_kernel<ATTN_GLOBAL_D, 0, 1, 2>;
+    static bool smem_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false}, merge_set[kMaxDevices] = {false};
     if ((st = ensure_smem(pda::global_fp8::decode_kernel, pda::global_fp8::kSmemBytes, dev, smem_set)) ||
-        (st = ensure_smem(pda::combine_kernel<ATTN_GLOBAL_D>, 0, dev, comb_set)))
+        (st = ensure_smem(pda::combine_kernel<ATTN_GLOBAL_D>, 0, dev, comb_set)) ||
+        (st = ensure_smem(merge_kernel, 0, dev, merge_set)))
       return st;
+    pda::prefix::MergeParams mp{};
+    mp.d = p;
     e = launch_pdl(pda::global_fp8::decode_kernel, dim3(plan.grid_x), pda::global_fp8::kThreads,
                    pda::global_fp8::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
     if (e == cudaSuccess)
-      e = launch_pdl(pda::combine_kernel<ATTN_GLOBAL_D>,
-                     dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / pda::kCombineCols), batch), pda::kCombineWarps * 32, 0, s,
-                     p);
+      e = few_rows ? launch_pdl(pda::combine_kernel<ATTN_GLOBAL_D>,
+                                dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / pda::kCombineCols), batch),
+                                pda::kCombineWarps * 32, 0, s, p)
+                   : launch_pdl(merge_kernel, dim3(ATTN_GLOBAL_HQ, batch), 2 * pda::prefix::kGroupThreads, 0, s, mp);
   }
   return launched(name, e);
 }
@@ -312,7 +355,7 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
 // ---------------------------------------------------------------------------
 using PrefixConfig = pda::prefill_pair::GlobalPairConfig;
 constexpr int kMaxPrefixSplits = 128;
-constexpr int kPrefixMinSteps = 4;  // steps of 64 keys a span is given at least
+constexpr int kPrefixMinSteps = 2;  // steps of 64 keys a span is given at least (8 sequences, 1000 positions: 24.5 us, with 4 26.5)
 
 struct PrefixPlan {
   Plan own;           // the own positions' decode
@@ -322,7 +365,7 @@ struct PrefixPlan {
 
 int32_t make_prefix_plan(int32_t batch, int32_t max_prefix_len, int32_t max_seq_len, int32_t num_splits,
                          int32_t prefix_splits, int32_t num_sms, PrefixPlan* out) {
-  const int32_t st = make_plan(ATTN_KIND_GLOBAL, batch, max_seq_len, 0, num_splits, num_sms, &out->own);
+  const int32_t st = make_serving_plan(ATTN_KIND_GLOBAL, batch, max_seq_len, 0, num_splits, num_sms, &out->own);
   if (st != ATTN_OK) return st;
   if (max_prefix_len < 0) return fail(ATTN_ERR_INVALID_ARG, "max_prefix_len must be >= 0");
   if (prefix_splits < 0) return fail(ATTN_ERR_INVALID_ARG, "prefix_splits must be >= 0");
@@ -465,6 +508,29 @@ int32_t attn_decode_global_prefix(const void* q, const void* k_pool, const void*
   return run_prefix(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o, batch, prefix_blocks,
                     max_blocks, num_pages, max_prefix_len, max_seq_len, out_dtype, num_splits, prefix_splits, workspace,
                     workspace_bytes, status, stream);
+}
+
+int32_t attn_decode_fp8_plan(int32_t kind, int32_t batch, int32_t max_seq_len, int32_t window, int32_t num_splits,
+                             int32_t num_sms, int32_t* out_num_splits, int32_t* out_launches,
+                             size_t* out_workspace_bytes) {
+  g_err[0] = '\0';
+  Plan plan;
+  const int32_t st = make_serving_plan(kind, batch, max_seq_len, window, num_splits, num_sms, &plan);
+  if (st != ATTN_OK) return st;
+  if (out_num_splits) *out_num_splits = plan.grid_x;
+  if (out_launches) *out_launches = plan.merge_in_grid ? 1 : 2;
+  if (out_workspace_bytes) *out_workspace_bytes = plan.workspace_bytes;
+  return ATTN_OK;
+}
+
+size_t attn_decode_fp8_workspace_size(int32_t kind, int32_t batch, int32_t max_seq_len, int32_t window,
+                                      int32_t num_splits) {
+  g_err[0] = '\0';
+  int dev = 0, num_sms = 0;
+  if (current_device(&dev, &num_sms) != ATTN_OK) return 0;
+  Plan plan;
+  if (make_serving_plan(kind, batch, max_seq_len, window, num_splits, num_sms, &plan) != ATTN_OK) return 0;
+  return plan.workspace_bytes;
 }
 
 int32_t attn_decode_prefix_plan(int32_t batch, int32_t max_prefix_len, int32_t max_seq_len, int32_t num_splits,

@@ -50,6 +50,7 @@ struct Smem {
   alignas(128) uint8_t v_scale[kStages][128];
   alignas(16) uint4 qfrag[kChunks * 4][4 * kG];  // q B fragments
   alignas(16) float merge_o[kConsumerWarps / 2][kG][kD];
+  uint32_t q_max[kConsumerWarps][kG];
   float merge_m[kConsumerWarps / 2][kG];
   float merge_l[kConsumerWarps / 2][kG];
   int32_t merge_last;
@@ -143,49 +144,55 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   // q as B fragments in shared memory (32 registers would spill): column n = g
   // holds head g % 2 (the products' columns beyond the two heads repeat them),
   // k-step (chunk, j, word): dims 128 chunk + 16 (2 tq + j) + 4 word .. + 3.  Two
-  // k-steps per 16 bytes.  Every warp reads all of the two heads for their
-  // exponents and writes the fragments of one (chunk, j).
+  // k-steps per 16 bytes.  Each warp prepares one (chunk, j): it loads its dims
+  // of the next sequence while it works on this one, leaves their largest for
+  // the other warps, and writes the fragments once all have.
   const int qlane = (g & 1) * 4 + tq;
   float qs[2];  // logit factor 2^k log2(e) of heads 0 and 1
-  auto load_q = [&]() {
-    const __nv_bfloat16* src = p.q + (static_cast<size_t>(cur.b) * kHq + hq0 + (g & 1)) * kD + 32 * tq;
-    uint4 mine[2] = {};
+  uint4 qn[2];  // the next sequence's q: 16 dims of head g % 2
+  auto fetch_q = [&](int b) {
+    const __nv_bfloat16* src = p.q + (static_cast<size_t>(b) * kHq + hq0 + (g & 1)) * kD + 128 * (warp >> 1) +
+                               16 * (2 * tq + (warp & 1));
+    qn[0] = ld_global_nc_v4(src);
+    qn[1] = ld_global_nc_v4(src + 8);
+  };
+  auto publish_q = [&]() {  // a barrier of the consumers follows
     uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < kChunks * 2; ++i) {
-      const uint4 v[2] = {ld_global_nc_v4(src + 128 * (i >> 1) + 16 * (i & 1)),
-                          ld_global_nc_v4(src + 128 * (i >> 1) + 16 * (i & 1) + 8)};
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t w[4] = {qn[k].x, qn[k].y, qn[k].z, qn[k].w};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (i == warp) mine[k] = v[k];
-        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) amax = max(amax, max(w[e] << 16 & 0x7fff0000u, w[e] & 0x7fff0000u));
-      }
+      for (int e = 0; e < 4; ++e) amax = max(amax, max(w[e] << 16 & 0x7fff0000u, w[e] & 0x7fff0000u));
     }
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));  // over the row's four lanes
-    float inv;
-    const int e = fp8::q_exponent(amax, inv);
+    if (g < kG && tq == 0) s.q_max[warp][g] = amax;
+  };
+  auto take_q = [&]() {
+    float inv[kG];
+#pragma unroll
+    for (int h = 0; h < kG; ++h) {
+      uint32_t amax = s.q_max[0][h];
+#pragma unroll
+      for (int w = 1; w < kConsumerWarps; ++w) amax = max(amax, s.q_max[w][h]);
+      const int e = fp8::q_exponent(amax, inv[h]);
+      qs[h] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * kLog2e;
+    }
+    const float f = g & 1 ? inv[1] : inv[0];
     if (g < kG) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        s.qfrag[2 * warp + k][qlane] = make_uint4(fp8::q_f16x2(mine[k].x, inv), fp8::q_f16x2(mine[k].y, inv),
-                                                  fp8::q_f16x2(mine[k].z, inv), fp8::q_f16x2(mine[k].w, inv));
+        s.qfrag[2 * warp + k][qlane] = make_uint4(fp8::q_f16x2(qn[k].x, f), fp8::q_f16x2(qn[k].y, f),
+                                                  fp8::q_f16x2(qn[k].z, f), fp8::q_f16x2(qn[k].w, f));
     }
-    const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * kLog2e;
-    qs[0] = __shfl_sync(0xffffffffu, f, 0);
-    qs[1] = __shfl_sync(0xffffffffu, f, 4);
+    const int nb = next_seq_in_span(p, t, sp, cur.b);
+    if (nb >= 0) fetch_q(nb);
     named_barrier_sync(1, kConsumerWarps * 32);
   };
-  load_q();
-  auto prefetch_next_q = [&]() {
-    const int nb = next_seq_in_span(p, t, sp, cur.b);
-    if (nb >= 0 && threadIdx.x < kG * kD * 2 / 128)
-      prefetch_l2(reinterpret_cast<const uint8_t*>(p.q + (static_cast<size_t>(nb) * kHq + hq0) * kD) +
-                  threadIdx.x * 128);
-  };
-  prefetch_next_q();
+  fetch_q(cur.b);
+  publish_q();
+  named_barrier_sync(1, kConsumerWarps * 32);
+  take_q();
 
   fp8::Reference ref[2];  // heads 0 and 1
   float l[2];             // this lane's share of the sums
@@ -320,7 +327,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-      const auto hand_over = [&](bool join) {
+      // (one copy of the code for both turns: it runs rarely, and what it costs is
+      // mostly fetching its instructions)
+#pragma unroll 1
+      for (int turn = 0; turn < 2; ++turn) {
+       const bool join = turn == 1;
+       if ((warp < kConsumerWarps / 2) == join) {
         const int slot = warp & 1;
         float fm[2], fo[2];  // factors of this warp's values and of the slot's
 #pragma unroll
@@ -342,6 +354,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         float u0[kG], u1[kG];
 #pragma unroll
         for (int h = 0; h < kG; ++h) fp8::unscale_factors(ref[h].R, u0[h], u1[h]);
+        float* dst = &s.merge_o[slot][0][16 * tq + g];
+        float old[4][4];
+        if (join) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) old[j][e] = dst[(e & 1) * kD + 64 * j + 8 * (e >> 1)];
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -349,14 +369,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             const float a01 = tq & 1 ? acc[4 * j + 1][e] : acc[4 * j][e];
             const float a23 = tq & 1 ? acc[4 * j + 3][e] : acc[4 * j + 2][e];
             const float mine = (tq & 2 ? a23 : a01) * u0[e & 1] * u1[e & 1] * fm[e & 1];
-            float* dst = &s.merge_o[slot][e & 1][16 * (4 * j + tq) + g + 8 * (e >> 1)];
-            *dst = join ? fmaf(*dst, fo[e & 1], mine) : mine;
+            dst[(e & 1) * kD + 64 * j + 8 * (e >> 1)] = join ? fmaf(old[j][e], fo[e & 1], mine) : mine;
           }
-      };
-      if (warp >= kConsumerWarps / 2) hand_over(false);
-      named_barrier_sync(1, kConsumerWarps * 32);
-      if (warp < kConsumerWarps / 2) hand_over(true);
-      named_barrier_sync(1, kConsumerWarps * 32);
+       }
+       named_barrier_sync(1, kConsumerWarps * 32);
+      }
       const int tt = threadIdx.x;  // 0..127: 2 heads x 64 groups of 4 dims
       const int h = tt >> 6;
       const int d0 = (tt & 63) * 4;
@@ -394,14 +411,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (d0 == 0) p.part_ml[slot] = make_float2(M, Lsum);
         if (p.merge_in_grid) sliding::merge_partials(p, t, s, cur.b, gb, c, h, d0, M, Lsum, O);
       }
-      named_barrier_sync(1, kConsumerWarps * 32);  // merge buffers (and q) free again
+      if (seg_end < sp.end) publish_q();
+      named_barrier_sync(1, kConsumerWarps * 32);  // merge buffers and q free again
       reset();
     }
     f0 = seg_end;
     if (f0 < sp.end) {
-      cur.advance(p, t, sp, f0);
-      load_q();
-      prefetch_next_q();
+      cur.advance(p, t, sp, f0);  // lands on the sequence whose q is in qn
+      take_q();
     }
   }
   allow_dependent_launch();

@@ -307,7 +307,7 @@ def test_streams_graphs_and_steps(cuda_lib, kind):
     cases = [Fp8Case(make_case(kind, lens, seed=46 + i, layout_seed=46)) for i in range(3)]
     args = list(cases[0].on(DEV))
     w = window_of(kind)
-    ws = pda.new_workspace(pda.attn_decode_workspace_size(getattr(pda, "KIND_" + kind.upper()), 4, 1300, w), DEV)
+    ws = pda.new_workspace(pda.attn_decode_fp8_workspace_size(getattr(pda, "KIND_" + kind.upper()), 4, 1300, w), DEV)
     kw = dict(window=w, max_seq_len=1300, workspace=ws, out_dtype=torch.float32)
     fn = getattr(pda, "attn_decode_%s_fp8" % kind)
     side = torch.cuda.Stream()

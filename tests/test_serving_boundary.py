@@ -66,6 +66,7 @@ def bad_calls():
             yield name, form, dict(num_pages=1 << 27), INVALID
             if form in ("chunk", "fp8"):
                 yield name, form, dict(total_q=-1), INVALID
+                yield name, form, dict(total_q=(1 << 28) + 1), UNSUPPORTED
             if form == "read":
                 yield name, form, dict(out_pages=0), INVALID
             if form == "prefix":
@@ -104,14 +105,38 @@ def test_no_tokens_is_a_call_without_a_launch(lib, kind):
         assert call(lib, "attn_kv_append_%s_%s" % (kind, suffix), form, total_q=0, qkv=None, q_out=None) == 0
 
 
+def test_fp8_plan(lib):
+    S, G = pda.KIND_SLIDING, pda.KIND_GLOBAL
+
+    def a256(x):
+        return (x + 255) // 256 * 256
+
+    # a block for every short sequence: a page and a virtual page each, two-page spans
+    for kind, D, n in ((S, 256, 30), (G, 512, 30)):
+        gx, _, ws = pda.attn_decode_fp8_plan(kind, n, 15, 1024 if kind == S else 0)
+        assert gx == n
+        rows = (gx + n) * 16
+        assert ws == pda.WORKSPACE_ZERO_BYTES + a256(rows * D * 4) + a256(rows * 8)
+    # one wave of resident blocks; long sequences keep four-page spans (250 pages + 1 -> 63 blocks)
+    assert pda.attn_decode_fp8_plan(G, 4, 262144, 0)[0] == 304
+    assert pda.attn_decode_fp8_plan(S, 256, 32768, 1024)[:2] == (57, 1)
+    assert pda.attn_decode_fp8_plan(G, 1, 4000, 0)[:2] == (63, 2)
+    assert pda.attn_decode_fp8_plan(G, 1, 0, 0)[0] == 1
+    assert pda.attn_decode_fp8_plan(G, 2, 100, 0, num_splits=7)[0] == 7
+    assert pda.attn_decode_fp8_plan(G, 2, 100, 0, num_splits=5000)[0] == 1024
+    for bad in ((7, 1, 16, 0), (G, 0, 16, 0), (G, 1, -1, 0), (G, 1, 16, 0, -1), (G, 1, 16, 0, 0, 0)):
+        with pytest.raises(pda.AttnDecodeError):
+            pda.attn_decode_fp8_plan(*bad)
+
+
 def test_prefix_plan(lib):
     # 64 sequences: 4 pairs of query tiles x 2 slices = 8 clusters, 76 SM pairs -> 9 spans
     ns, ps, ws = pda.attn_decode_prefix_plan(64, 32768, 2048)
-    own, own_ws = pda.attn_decode_plan(pda.KIND_GLOBAL, 64, 2048, 0)
+    own, _, own_ws = pda.attn_decode_fp8_plan(pda.KIND_GLOBAL, 64, 2048, 0)
     rows = ps * 64 * 16
     assert (ns, ps) == (own, 9) and ws == own_ws + rows * 512 * 4 + rows * 2 * 8
-    # a short prefix is cut into spans of no less than four steps of 64 keys; one span at least
-    assert pda.attn_decode_prefix_plan(1, 1024, 16)[1] == 4
+    # a short prefix is cut into spans of no less than two steps of 64 keys; one span at least
+    assert pda.attn_decode_prefix_plan(1, 1024, 16)[1] == 8
     assert pda.attn_decode_prefix_plan(1, 100, 16)[1] == 1
     assert pda.attn_decode_prefix_plan(1, 0, 0)[1] == 1
     assert pda.attn_decode_prefix_plan(256, 262144, 16)[1] == 2
