@@ -232,14 +232,17 @@ int32_t attn_decode_global_shared(const void* q, const void* kv_pool, const void
  * max_prefix_len, max_seq_len  host bounds; they size the launches only and
  *               never change which positions are read
  * num_splits    thread blocks for the own positions, as for attn_decode_global
- * prefix_splits spans the prefix is cut into: 0 = automatic, at most 128
+ * prefix_splits spans the prefix is cut into, at most 128: 0 = automatic, and
+ *               without spans for a short prefix or a small batch, where every
+ *               sequence reads the prefix for itself
  * workspace     at least attn_decode_prefix_workspace_size(...) bytes, its
  *               first ATTN_WORKSPACE_ZERO_BYTES as for the decode calls; not
  *               shared by calls that may overlap
  * status        as for attn_decode_global; a prefix_len outside its range
  *               raises ATTN_DEV_BAD_SEQ_LEN and is clamped
  *
- * Every array 16 bytes aligned (prefix_table, prefix_len 4).  Three kernels.
+ * Every array 16 bytes aligned (prefix_table, prefix_len 4).  Three kernels
+ * with spans, two without.
  * Weights are rounded to bf16 for their product with the values.
  */
 int32_t attn_decode_global_prefix(const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,

@@ -29,8 +29,8 @@ constexpr int kCombineWarps = 4;
 constexpr int kPerWarp = 8;        // partials a warp keeps in flight per round (74 registers: one
                                    // block fits beside the decode blocks of an SM)
 
-template <int kD>
-__global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __grid_constant__ DecodeParams p) {
+template <int kD, typename Params = DecodeParams>
+__global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __grid_constant__ Params p) {
   constexpr int kSlices = kD / kCombineCols;
   __shared__ float s_max[kCombineWarps];
   __shared__ float s_l[kCombineWarps];
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int j = 4 * v + k;
-        const int n = j < p.batch ? visible_pages(clamp_len(p, L[k], false), p.window) : 0;
+        const int n = j < p.batch ? visible_pages(schedule_len(p, L[k], false), p.window) : 0;
         const int wn = n > 0 ? n + kSeqWeight : 0;
         total += wn;
         before += j < b ? wn : 0;

@@ -91,6 +91,24 @@ __device__ __forceinline__ int clamp_len(const DecodeParams& p, int L, bool repo
   return L;
 }
 
+// The length the schedule works with: L_b, clamped.  (Another kind of call
+// overloads this and table_entry for its own parameter type, see joined.cuh.)
+__device__ __forceinline__ int schedule_len(const DecodeParams& p, int L, bool report_it) {
+  return clamp_len(p, L, report_it);
+}
+
+// Where logical page lp of sequence b is listed; null outside the table.
+__device__ __forceinline__ const int32_t* table_entry(const DecodeParams& p, int b, int lp) {
+  return lp < 0 || lp >= p.max_blocks ? nullptr : p.block_table + static_cast<int64_t>(b) * p.max_blocks + lp;
+}
+
+// Positions between a sequence's first and its last that are none of its:
+// covers() tells whether one of the n from pos on is.
+struct NoHole {
+  __device__ __forceinline__ bool covers(int, int) const { return false; }
+};
+__device__ __forceinline__ NoHole hole_of(const DecodeParams&) { return {}; }
+
 __device__ __forceinline__ int span_pages(int total, int grid_x, int min_pages) {
   const int per = (total + grid_x - 1) / grid_x;
   return per > min_pages ? per : min_pages;
@@ -100,8 +118,8 @@ __device__ __forceinline__ int span_pages(int total, int grid_x, int min_pages) 
 // that runs before griddepcontrol.wait, whose results only aim prefetches.
 // Its seq_lens reads go through ld.global.cg, so no line that might still
 // change is kept in L1, and it reports nothing.
-template <bool kHint>
-__device__ __forceinline__ void scan_seq_lens(const DecodeParams& p, SeqTable& t, int g) {
+template <bool kHint, typename Params>
+__device__ __forceinline__ void scan_seq_lens(const Params& p, SeqTable& t, int g) {
   const int lane = threadIdx.x;
   {
     // pass 1: lengths, prefix sums of visible pages, non-empty sequences
@@ -109,7 +127,7 @@ __device__ __forceinline__ void scan_seq_lens(const DecodeParams& p, SeqTable& t
     if (lane == 0) t.prefix[0] = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + lane;
-      const int L = b < p.batch ? clamp_len(p, kHint ? __ldcg(p.seq_lens + b) : p.seq_lens[b], !kHint) : 0;
+      const int L = b < p.batch ? schedule_len(p, kHint ? __ldcg(p.seq_lens + b) : p.seq_lens[b], !kHint) : 0;
       int v = visible_pages(L, p.window);
       nonempty += __popc(__ballot_sync(0xffffffffu, v > 0));
 #pragma unroll
@@ -167,7 +185,8 @@ __device__ __forceinline__ void scan_seq_lens(const DecodeParams& p, SeqTable& t
 
 // Before griddepcontrol.wait: the table from hint reads.  Called by every
 // thread of the block; ends with __syncthreads.
-__device__ __forceinline__ void build_seq_table_hint(const DecodeParams& p, SeqTable& t, int g) {
+template <typename Params>
+__device__ __forceinline__ void build_seq_table_hint(const Params& p, SeqTable& t, int g) {
   if (threadIdx.x < 32) scan_seq_lens<true>(p, t, g);
   __syncthreads();
 }
@@ -177,13 +196,14 @@ __device__ __forceinline__ void build_seq_table_hint(const DecodeParams& p, SeqT
 // the usual case the schedule costs one read here.  Called by every thread of
 // the block; ends with a __syncthreads that also publishes anything written
 // before it.  From here on the table is exact.
-__device__ __forceinline__ void confirm_seq_table(const DecodeParams& p, SeqTable& t, int g) {
+template <typename Params>
+__device__ __forceinline__ void confirm_seq_table(const Params& p, SeqTable& t, int g) {
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     bool differ = false;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + lane;
-      const int L = b < p.batch ? clamp_len(p, p.seq_lens[b], true) : 0;
+      const int L = b < p.batch ? schedule_len(p, p.seq_lens[b], true) : 0;
       differ |= __any_sync(0xffffffffu, b < p.batch && L != t.len[b]);
     }
     __syncwarp();
@@ -210,15 +230,16 @@ __device__ __forceinline__ int seq_of(const SeqTable& t, int batch, int f) {
 // the stream finishes.  Anything read here may be stale, which costs at most
 // a useless prefetch: every index is range-checked, the block-table read
 // bypasses L1, and nothing is written.
-template <typename Warm>
-__device__ __forceinline__ void warm_first_pages(const DecodeParams& p, const SeqTable& t, int n, Warm warm) {
+template <typename Params, typename Warm>
+__device__ __forceinline__ void warm_first_pages(const Params& p, const SeqTable& t, int n, Warm warm) {
   const int lane = threadIdx.x & 31;
   const int f = t.span.begin + lane;
   if (lane >= n || f >= t.span.end) return;
   const int b = seq_of(t, p.batch, f);
   const int lp = first_visible(t.len[b], p.window) / kPage + (f - t.prefix[b]);
-  if (lp < 0 || lp >= p.max_blocks) return;
-  const int phys = __ldcg(p.block_table + static_cast<int64_t>(b) * p.max_blocks + lp);
+  const int32_t* entry = table_entry(p, b, lp);
+  if (entry == nullptr) return;
+  const int phys = __ldcg(entry);
   if (phys >= 0 && static_cast<int64_t>(phys) < p.num_pages) warm(phys * kPage);
 }
 
@@ -271,23 +292,24 @@ __device__ __forceinline__ void store_out2(const DecodeParams& p, size_t idx, fl
 // with report_it, ATTN_DEV_INTERNAL.  The producer also calls it while the
 // table may still be rebuilt (report_it false, result discarded then), so
 // every index is range-checked whatever the table holds.
-__device__ __forceinline__ int page_entry(const DecodeParams& p, const SeqTable& t, const Span& sp, int i,
-                                          bool report_it) {
+template <typename Params>
+__device__ __forceinline__ int page_entry(const Params& p, const SeqTable& t, const Span& sp, int i, bool report_it) {
   if (i < 0 || i >= sp.end - sp.begin) return 0;
   const int f = sp.begin + i;
   const int b = seq_of(t, p.batch, f);
   const int lp = first_visible(t.len[b], p.window) / kPage + (f - t.prefix[b]);
-  if (lp < 0 || lp >= p.max_blocks) {
+  const int32_t* entry = table_entry(p, b, lp);
+  if (entry == nullptr) {
     if (report_it) report(p.status, ATTN_DEV_INTERNAL);
     return -1;
   }
-  return p.block_table[static_cast<int64_t>(b) * p.max_blocks + lp];
+  return *entry;
 }
 
 // first: this lane's page_entry(sp, lane), read ahead by the caller.
-template <int kStages, int kTxBytes, typename Issue>
-__device__ __forceinline__ void produce_pages(const DecodeParams& p, const SeqTable& t, const Span& sp,
-                                              uint64_t* full, uint64_t* empty, int first, Issue issue) {
+template <int kStages, int kTxBytes, typename Params, typename Issue>
+__device__ __forceinline__ void produce_pages(const Params& p, const SeqTable& t, const Span& sp, uint64_t* full,
+                                               uint64_t* empty, int first, Issue issue) {
   const int lane = threadIdx.x & 31;
   const int n_pages = sp.end - sp.begin;
   auto entry = [&](int i) -> int { return page_entry(p, t, sp, i, true); };

@@ -131,8 +131,8 @@ __device__ __forceinline__ int s_kstep_dim(int w, int ks) {
 
 // kPartial: every segment is left as a partial, a whole sequence's too, for a
 // caller that merges it with others (prefix.cuh).
-template <bool kShared, bool kPartial = false>
-__device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const DecodeParams& p,
+template <bool kShared, bool kPartial = false, typename Params>
+__device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const Params& p,
                                             const KeyRebuild* kr) {
   extern __shared__ uint8_t smem_raw[];
   using S = Smem<kShared>;
@@ -214,6 +214,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
 
   PageCursor cur;
   cur.start(p, t, sp);
+  const auto hole = hole_of(p);
 
   // q as m16n8k16 A fragments over this warp's 128 S dims (8 k-steps of 16)
   // With a values-only cache each lane parks its fragments in shared memory
@@ -637,13 +638,13 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
       // sc[nt][e]: head g + 8*(e>>1), position pos0 + 8*nt + 2*tq + (e&1).
       // Positions outside [lo, L) get -inf (pages inside the range skip the
       // test); the factor log2(e) is applied inside the exponent.
-      if (pos0 < cur.lo || pos0 + kPage > cur.L) {
+      if (pos0 < cur.lo || pos0 + kPage > cur.L || hole.covers(pos0, kPage)) {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int pos = pos0 + 8 * nt + 2 * tq + (e & 1);
-            if (pos < cur.lo || pos >= cur.L) sc[nt][e] = -INFINITY;
+            if (pos < cur.lo || pos >= cur.L || hole.covers(pos, 1)) sc[nt][e] = -INFINITY;
           }
       }
       float mx[2];
@@ -690,11 +691,11 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
                               pack_bf16x2(pr[1][0], pr[1][1]), pack_bf16x2(pr[1][2], pr[1][3])};
 
       // ---- zero V rows outside [lo, L) in this warp's two chunks ----
-      if (pos0 < cur.lo || pos0 + kPage > cur.L) {
+      if (pos0 < cur.lo || pos0 + kPage > cur.L || hole.covers(pos0, kPage)) {
 #pragma unroll 1
         for (int rr = 0; rr < kPage; ++rr) {
           const int pos = pos0 + rr;
-          if ((pos < cur.lo || pos >= cur.L) && lane < 16) {
+          if ((pos < cur.lo || pos >= cur.L || hole.covers(pos, 1)) && lane < 16) {
             const int ch = 2 * warp + (lane >> 3);
             st_shared_v4(vst + ch * kChunkBytes + rr * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
           }
@@ -763,6 +764,14 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
       }
     }
   }
+}
+
+// The same over another list of pages (joined.cuh).
+template <typename Params>
+__global__ void __launch_bounds__(kThreads)
+    decode_kernel_listed(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ Params p) {
+  decode_body<false>(&tm_k, &tm_v, p, nullptr);
 }
 
 __global__ void __launch_bounds__(kThreads)

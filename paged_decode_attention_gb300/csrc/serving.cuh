@@ -6,6 +6,7 @@
 #include "attn_fp8.h"
 #include "fp8_read.cuh"
 #include "global_fp8.cuh"
+#include "joined.cuh"
 #include "kv_chunk.cuh"
 #include "prefix.cuh"
 #include "sliding_fp8.cuh"
@@ -355,20 +356,41 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
 // ---------------------------------------------------------------------------
 using PrefixConfig = pda::prefill_pair::GlobalPairConfig;
 constexpr int kMaxPrefixSplits = 128;
-constexpr int kPrefixMinSteps = 2;  // steps of 64 keys a span is given at least (8 sequences, 1000 positions: 24.5 us, with 4 26.5)
+// Whether every sequence reads the prefix for itself (joined.cuh).  That costs
+// a pass of L2 over the prefix per sequence and two kernels instead of three.
+// One call in us, joined and in spans: 1 sequence, 1 position 8.1 and 14.8,
+// 32768 28.9 and 41.8, 262144 98 and 202; 2 sequences, 65536 39.9 and 66.6,
+// 262144 164 and 203; 8 sequences, 1000 12.2 and 23.0, 5003 20.2 and 26.5, 12000
+// 30.9 and 32.3; 16 sequences, 4000 26.5 and 28.1, 5000 30.4 and 28.1; 32
+// sequences, 1200 24.9 and 26.9, 2000 30.5 and 28.8; 64 sequences, 16 25.3 and
+// 29.6, 600 34.4 and 32.2; 128 sequences, 200 49.2 and 40.2.
+bool join_prefix(int32_t batch, int32_t max_prefix_len) {
+  return batch <= 2 || static_cast<int64_t>(batch) * (static_cast<int64_t>(max_prefix_len) + 1536) <= 98304;
+}
+constexpr int kPrefixMinSteps = 2;  // steps of 64 keys a span is given at least (32 sequences, 2000 positions: 28.8 us)
 
 struct PrefixPlan {
-  Plan own;           // the own positions' decode
-  int splits;         // spans of the prefix
+  bool joined;        // prefix and own pages as one list per sequence (joined.cuh): two kernels
+  Plan own;           // the decode over the own positions, or over the joined list
+  int splits;         // spans of the prefix; 0 when joined
   size_t part_o_off, part_ml_off, workspace_bytes;
 };
 
 int32_t make_prefix_plan(int32_t batch, int32_t max_prefix_len, int32_t max_seq_len, int32_t num_splits,
                          int32_t prefix_splits, int32_t num_sms, PrefixPlan* out) {
-  const int32_t st = make_serving_plan(ATTN_KIND_GLOBAL, batch, max_seq_len, 0, num_splits, num_sms, &out->own);
-  if (st != ATTN_OK) return st;
   if (max_prefix_len < 0) return fail(ATTN_ERR_INVALID_ARG, "max_prefix_len must be >= 0");
   if (prefix_splits < 0) return fail(ATTN_ERR_INVALID_ARG, "prefix_splits must be >= 0");
+  if (max_seq_len < 0) return fail(ATTN_ERR_INVALID_ARG, "max_seq_len must be >= 0");
+  out->joined = prefix_splits == 0 && join_prefix(batch, max_prefix_len);
+  const int64_t joined_len =
+      (static_cast<int64_t>(max_prefix_len) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE * ATTN_PAGE_SIZE + max_seq_len;
+  const int32_t len = out->joined ? static_cast<int32_t>(std::min<int64_t>(joined_len, INT32_MAX)) : max_seq_len;
+  const int32_t st = make_serving_plan(ATTN_KIND_GLOBAL, batch, len, 0, num_splits, num_sms, &out->own);
+  if (st != ATTN_OK) return st;
+  out->splits = 0;
+  out->part_o_off = out->part_ml_off = 0;
+  out->workspace_bytes = out->own.workspace_bytes;
+  if (out->joined) return ATTN_OK;
   // One CTA pair per SM pair: 2 query tiles (of kQ sequences each) and one
   // slice of the output dims per cluster, the rest of the GPU by spans.
   const int64_t pairs = (batch + 2 * PrefixConfig::kQ - 1) / (2 * PrefixConfig::kQ) * PrefixConfig::kSlices;
@@ -423,27 +445,13 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
     return fail(ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)", name, plan.workspace_bytes,
                 workspace ? workspace_bytes : size_t{0});
   if (!aligned16(workspace)) return fail(ATTN_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", name);
-  g_last_launches = 3;
+  g_last_launches = plan.joined ? 2 : 3;
   if (g_validate_only) return ATTN_OK;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  pda::prefill_pair::PrefixParams pp{};
-  pp.q = static_cast<const __nv_bfloat16*>(q);
-  pp.block_table = prefix_table;
-  pp.seq_lens = prefix_len;
-  pp.status = status;
-  pp.num_pages = num_pages;
-  pp.batch = 1;
-  pp.max_blocks = prefix_blocks;
-  pp.total_q = batch;
-  pp.max_q = batch;
-  pp.part_o = reinterpret_cast<float*>(ws + plan.part_o_off);
-  pp.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml_off);
-  pp.splits = plan.splits;
-
-  pda::prefix::MergeParams mp{};
-  pda::DecodeParams& p = mp.d;
-  p.q = pp.q;
+  pda::JoinedParams jp{};
+  pda::DecodeParams& p = jp;
+  p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
   p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
   p.block_table = block_table;
@@ -460,6 +468,42 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
   p.min_pages = plan.own.min_pages;
   p.out_f32 = out_dtype == ATTN_OUT_F32;
   p.part_rows = (static_cast<int64_t>(plan.own.grid_x) + batch) * ATTN_GLOBAL_HQ;
+  jp.prefix_table = prefix_table;
+  jp.prefix_len = prefix_len;
+  jp.prefix_blocks = prefix_blocks;
+  CUtensorMap tm_k, tm_v;
+  if ((st = encode_global_page_map(&tm_k, k_pool, num_pages)) || (st = encode_global_page_map(&tm_v, v_pool, num_pages)))
+    return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (plan.joined) {
+    const auto decode = pda::global::decode_kernel_listed<pda::JoinedParams>;
+    const auto combine = pda::combine_kernel<ATTN_GLOBAL_D, pda::JoinedParams>;
+    static bool dec_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false};
+    if ((st = ensure_smem(decode, pda::global::kSmemBytes, dev, dec_set)) || (st = ensure_smem(combine, 0, dev, comb_set)))
+      return st;
+    cudaError_t e = launch_pdl(decode, dim3(plan.own.grid_x), pda::global::kThreads, pda::global::kSmemBytes, s, tm_k,
+                               tm_v, jp);
+    if (e == cudaSuccess)
+      e = launch_pdl(combine, dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / pda::kCombineCols), batch),
+                     pda::kCombineWarps * 32, 0, s, jp);
+    return launched(name, e);
+  }
+  pda::prefill_pair::PrefixParams pp{};
+  pp.q = p.q;
+  pp.block_table = prefix_table;
+  pp.seq_lens = prefix_len;
+  pp.status = status;
+  pp.num_pages = num_pages;
+  pp.batch = 1;
+  pp.max_blocks = prefix_blocks;
+  pp.total_q = batch;
+  pp.max_q = batch;
+  pp.part_o = reinterpret_cast<float*>(ws + plan.part_o_off);
+  pp.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml_off);
+  pp.splits = plan.splits;
+
+  pda::prefix::MergeParams mp{};
+  mp.d = p;
   mp.part_o = pp.part_o;
   mp.part_ml = pp.part_ml;
   mp.prefix_len = prefix_len;
@@ -476,15 +520,12 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
       (st = ensure_smem(pda::global::decode_kernel_partial, pda::global::kSmemBytes, dev, dec_set)) ||
       (st = ensure_smem(merge_kernel, 0, dev, merge_set[few_rows])))
     return st;
-  CUtensorMap tm_pk, tm_pv, tm_k, tm_v;
+  CUtensorMap tm_pk, tm_pv;
   if ((st = encode_chunk_map(&tm_pk, k_pool, num_pages, C::kHkv * C::kD, C::kKBoxChunks)) ||
-      (st = encode_chunk_map(&tm_pv, v_pool, num_pages, C::kHkv * C::kD, C::kDS / 128)) ||
-      (st = encode_global_page_map(&tm_k, k_pool, num_pages)) ||
-      (st = encode_global_page_map(&tm_v, v_pool, num_pages)))
+      (st = encode_chunk_map(&tm_pv, v_pool, num_pages, C::kHkv * C::kD, C::kDS / 128)))
     return st;
   int tiles = (batch + C::kQ - 1) / C::kQ;
   tiles += tiles & 1;  // whole clusters of two query tiles
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_pdl(prefix_kernel, dim3(tiles, C::kHkv * C::kSlices, plan.splits), C::kThreads, C::kSmemBytes, s,
                              tm_pk, tm_pv, pp);
   if (e == cudaSuccess)

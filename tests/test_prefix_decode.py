@@ -35,6 +35,10 @@ class Case:
                                     torch.tensor(self.lens, dtype=torch.int32))]
 
 
+# prefix_splits=0 takes one list of pages per sequence for small cases; the cases below run both ways
+BOTH = pytest.mark.parametrize("splits", [0, 2])
+
+
 def decode(args, **kw):
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     kw.setdefault("out_dtype", torch.float32)
@@ -57,15 +61,17 @@ def check(c, label="", **kw):
     return o
 
 
+@BOTH
 @pytest.mark.parametrize("prefix", [0, 1, 15, 16, 17, 63, 64, 65, 255, 257, 1000, 1024])
-def test_prefix_lengths(cuda_lib, prefix):
-    check(Case(prefix, [0, 1, 17, 300, 64], seed=61, spare_blocks=2), "prefix %d" % prefix)
+def test_prefix_lengths(cuda_lib, prefix, splits):
+    check(Case(prefix, [0, 1, 17, 300, 64], seed=61, spare_blocks=2), "prefix %d" % prefix, prefix_splits=splits)
 
 
+@BOTH
 @pytest.mark.parametrize("batch", [1, 7, 8, 9, 15, 16, 17, 33, 100])
-def test_batches(cuda_lib, batch):
+def test_batches(cuda_lib, batch, splits):
     r = np.random.RandomState(batch)
-    check(Case(700, r.randint(0, 60, batch).tolist(), seed=62))
+    check(Case(700, r.randint(0, 60, batch).tolist(), seed=62), prefix_splits=splits)
 
 
 def test_full_batch(cuda_lib):
@@ -78,39 +84,43 @@ def test_a_long_prefix(cuda_lib, out_dtype):
     check(Case(9001, [0, 5, 1500, 33, 16, 1, 0, 700, 80], seed=64), out_dtype=out_dtype)
 
 
-@pytest.mark.parametrize("prefix_splits", [1, 2, 3, 16, 128, 1000])
+@pytest.mark.parametrize("prefix_splits", [0, 1, 2, 3, 16, 128, 1000])
 @pytest.mark.parametrize("num_splits", [0, 1, 50])
 def test_forced_splits(cuda_lib, num_splits, prefix_splits):
     check(Case(1300, [3, 0, 600, 1100], seed=65), num_splits=num_splits, prefix_splits=prefix_splits)
 
 
-def test_nothing_visible_gives_zero(cuda_lib):
+@BOTH
+def test_nothing_visible_gives_zero(cuda_lib, splits):
     c = Case(0, [0, 40, 0], seed=66)
-    o = check(c)
+    o = check(c, prefix_splits=splits)
     assert (o[0] == 0).all() and (o[2] == 0).all()
 
 
+@BOTH
 @pytest.mark.parametrize("q_scale", [0.0, 0.05, 8.0])
-def test_flat_and_dominated_weights(cuda_lib, q_scale):
-    check(Case(900, [5, 0, 1200], seed=67, q_scale=q_scale))
+def test_flat_and_dominated_weights(cuda_lib, q_scale, splits):
+    check(Case(900, [5, 0, 1200], seed=67, q_scale=q_scale), prefix_splits=splits)
 
 
-def test_bounds_size_the_launches_only(cuda_lib):
+@BOTH
+def test_bounds_size_the_launches_only(cuda_lib, splits):
     c = Case(1000, [5, 0, 700, 33], seed=68)
     args = c.args()
-    o, st = decode(args)
+    o, st = decode(args, prefix_splits=splits)
     assert st == 0
     want, A, S = attention_rows(args[0], args[1], args[2], args[5], args[6], 0, prefix=(args[3], c.prefix))
     for bounds in (dict(max_prefix_len=0, max_seq_len=0), dict(max_prefix_len=16, max_seq_len=700)):
-        o, st = decode(args, **bounds)
+        o, st = decode(args, prefix_splits=splits, **bounds)
         assert st == 0
         assert ((o.double().cpu() - want).abs() <= decode_bound(want, A, S, 512, o.dtype, WEIGHT_EPS)).all()
 
 
-def test_whole_pages_equal_the_plain_decode_over_joined_tables(cuda_lib):
+@BOTH
+def test_whole_pages_equal_the_plain_decode_over_joined_tables(cuda_lib, splits):
     c = Case(640, [5, 17, 700], seed=69)
     q, k, v, pt, _, bt, sl = c.args()
-    o, _ = decode(c.args())
+    o, _ = decode(c.args(), prefix_splits=splits)
     joined = torch.cat([pt[None].expand(3, -1), bt], 1).contiguous()
     plain = pda.attn_decode_global(q, k, v, joined, sl + 640, out_dtype=torch.float32)
     torch.cuda.synchronize()
@@ -119,36 +129,39 @@ def test_whole_pages_equal_the_plain_decode_over_joined_tables(cuda_lib):
     assert ((o - plain).abs().double().cpu() <= 2 * bound).all()
 
 
-def test_runs_repeat_bitwise(cuda_lib):
+@BOTH
+def test_runs_repeat_bitwise(cuda_lib, splits):
     args = Case(2100, [5, 700, 0, 33], seed=70).args()
-    assert torch.equal(decode(args)[0], decode(args)[0])
+    assert torch.equal(decode(args, prefix_splits=splits)[0], decode(args, prefix_splits=splits)[0])
 
 
-def test_bad_prefix_length_is_flagged_and_clamped(cuda_lib):
+@BOTH
+def test_bad_prefix_length_is_flagged_and_clamped(cuda_lib, splits):
     c = Case(64, [5, 33], seed=71)
     args = c.args()
-    o, _ = decode(args)
+    o, _ = decode(args, prefix_splits=splits)
     args[4].fill_(65)  # beyond the prefix's table
-    got, st = decode(args, max_prefix_len=64)
+    got, st = decode(args, max_prefix_len=64, prefix_splits=splits)
     assert st == pda.DEV_BAD_SEQ_LEN and torch.equal(got, o)
     args[4].fill_(-2)
-    got, st = decode(args, max_prefix_len=64)
+    got, st = decode(args, max_prefix_len=64, prefix_splits=splits)
     args[4].fill_(0)
-    want, st0 = decode(args, max_prefix_len=64)
+    want, st0 = decode(args, max_prefix_len=64, prefix_splits=splits)
     assert st == pda.DEV_BAD_SEQ_LEN and st0 == 0 and torch.equal(got, want)
 
 
+@BOTH
 @pytest.mark.parametrize("page", [-1, 1 << 20])
-def test_bad_prefix_page_is_flagged_and_reads_as_zeros(cuda_lib, page):
+def test_bad_prefix_page_is_flagged_and_reads_as_zeros(cuda_lib, page, splits):
     c = Case(200, [5, 33], seed=72)
     args = c.args()
     args[3][4] = page
-    o, st = decode(args)
+    o, st = decode(args, prefix_splits=splits)
     assert st == pda.DEV_BAD_PAGE
     z = int(c.prefix_table[4])
     c.k[z] = 0
     c.v[z] = 0
-    want, st = decode(c.args())
+    want, st = decode(c.args(), prefix_splits=splits)
     assert st == 0 and torch.equal(o, want)
 
 
@@ -182,7 +195,7 @@ def test_streams_graphs_and_steps(cuda_lib):
         graphs.append(g)
     step = pda.Step()
     outs.append(step.add_decode_global_prefix(*args, **kw))
-    assert step.num_kernels == 3
+    assert step.num_kernels == 2  # 4 x 1008 positions: one list per sequence
     step.finalize("graph")
     call = pda.prepare_decode_global_prefix(*args, **kw)
     for prefix, lens in ((1000, [5, 700, 0, 33]), (17, [0, 16, 0, 20]), (640, [3, 600, 0, 33])):

@@ -135,12 +135,16 @@ def test_prefix_plan(lib):
     own, _, own_ws = pda.attn_decode_fp8_plan(pda.KIND_GLOBAL, 64, 2048, 0)
     rows = ps * 64 * 16
     assert (ns, ps) == (own, 9) and ws == own_ws + rows * 512 * 4 + rows * 2 * 8
-    # a short prefix is cut into spans of no less than two steps of 64 keys; one span at least
-    assert pda.attn_decode_prefix_plan(1, 1024, 16)[1] == 8
-    assert pda.attn_decode_prefix_plan(1, 100, 16)[1] == 1
-    assert pda.attn_decode_prefix_plan(1, 0, 0)[1] == 1
+    # short prefixes, small batches: one list of pages per sequence, no spans
+    for B, n in ((16, 4608), (1, 262144), (2, 131072), (64, 0), (4, 0)):
+        gx, ps, ws = pda.attn_decode_prefix_plan(B, n, 100)
+        assert (gx, ps, ws) == (pda.attn_decode_fp8_plan(pda.KIND_GLOBAL, B, -(-n // 16) * 16 + 100, 0)[0], 0,
+                                pda.attn_decode_fp8_plan(pda.KIND_GLOBAL, B, -(-n // 16) * 16 + 100, 0)[2])
+    assert pda.attn_decode_prefix_plan(16, 4609, 100)[1] == 36  # spans of no less than two steps of 64 keys
+    assert pda.attn_decode_prefix_plan(65, 0, 16)[1] == 1 and pda.attn_decode_prefix_plan(2, 2**31 - 1, 2**31 - 1)[1] == 0
     assert pda.attn_decode_prefix_plan(256, 262144, 16)[1] == 2
     assert pda.attn_decode_prefix_plan(8, 262144, 16, prefix_splits=7)[1] == 7
+    assert pda.attn_decode_prefix_plan(8, 100, 16, prefix_splits=1)[1] == 1
     assert pda.attn_decode_prefix_plan(8, 262144, 16, prefix_splits=5000)[1] == 128
     for bad in ((0, 16, 16), (1, -1, 16), (1, 16, -1), (1, 16, 16, -1), (1, 16, 16, 0, -1), (1, 16, 16, 0, 0, 0)):
         with pytest.raises(pda.AttnDecodeError):
