@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
       for (int k = 0; k < 4; ++k) {
         const int j = 4 * v + k;
         const int n = j < p.batch ? visible_pages(schedule_len(p, L[k], false), p.window) : 0;
-        const int wn = n > 0 ? n + kSeqWeight : 0;
+        const int wn = n > 0 ? n + Params::kSeqWeight : 0;
         total += wn;
         before += j < b ? wn : 0;
         mine += j == b ? n : 0;
@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
     return;
   }
   const int per = span_pages(total, p.grid_x, p.min_pages);
-  const int g0 = (before + kSeqWeight) / per;
-  const int g1 = (before + kSeqWeight + mine - 1) / per;
+  const int g0 = (before + Params::kSeqWeight) / per;
+  const int g1 = (before + Params::kSeqWeight + mine - 1) / per;
   if (g0 == g1) {  // one block held the whole sequence and wrote o
     done();
     return;

@@ -16,6 +16,7 @@ constexpr int kMaxSplits = 1024;       // blocks per KV head the host plan may l
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct DecodeParams {
+  static constexpr int kSeqWeight = 1;  // virtual pages charged per sequence start (the schedule, below)
   const __nv_bfloat16* q;      // [batch, Hq, D]
   const __nv_bfloat16* k_pool; // [num_pages, 16, Hkv, D] (read through the tensor maps; raw for L2 prefetches)
   const __nv_bfloat16* v_pool;
@@ -57,8 +58,6 @@ struct DecodeParams {
 // and sequences are both in order; the combine kernel, or the last of the
 // sequence's blocks (sliding kernel, merge in the grid), merges them.
 // ---------------------------------------------------------------------------
-constexpr int kSeqWeight = 1;  // virtual pages charged per sequence start
-
 struct Span {
   int begin, end;  // flattened real pages of this block
 };
@@ -143,7 +142,7 @@ __device__ __forceinline__ void scan_seq_lens(const Params& p, SeqTable& t, int 
     }
     __syncwarp();
     // block g's weighted range [w0, w1) and the real pages it maps to
-    const int total = carry + kSeqWeight * nonempty;
+    const int total = carry + Params::kSeqWeight * nonempty;
     const int per = span_pages(total, p.grid_x, p.min_pages);
     const long long u0 = static_cast<long long>(g) * per;
     const int w0 = u0 < total ? static_cast<int>(u0) : total;
@@ -158,7 +157,7 @@ __device__ __forceinline__ void scan_seq_lens(const Params& p, SeqTable& t, int 
       const int b = b0 + lane;
       const bool in = b < p.batch;
       const unsigned ne = __ballot_sync(0xffffffffu, in && t.len[b] > 0);
-      const int wp = in ? t.prefix[b] + kSeqWeight * (before + __popc(ne & lt)) : 0;
+      const int wp = in ? t.prefix[b] + Params::kSeqWeight * (before + __popc(ne & lt)) : 0;
       const unsigned c0 = __ballot_sync(0xffffffffu, in && wp <= w0);
       const unsigned c1 = __ballot_sync(0xffffffffu, in && wp <= w1);
       if (c0) {
@@ -175,7 +174,7 @@ __device__ __forceinline__ void scan_seq_lens(const Params& p, SeqTable& t, int 
     }
     if (lane == 0) {
       t.per = per;
-      const int o0 = w0 - wp0 - kSeqWeight, o1 = w1 - wp1 - kSeqWeight;
+      const int o0 = w0 - wp0 - Params::kSeqWeight, o1 = w1 - wp1 - Params::kSeqWeight;
       t.span.begin = w0 >= total ? carry : t.prefix[own0] + (o0 > 0 ? o0 : 0);
       t.span.end = w1 >= total ? carry : t.prefix[own1] + (o1 > 0 ? o1 : 0);
     }
@@ -401,8 +400,9 @@ __device__ __forceinline__ int next_seq_in_span(const DecodeParams& p, const Seq
 // the number of non-empty sequences before it: its real pages sit at weighted
 // positions prefix[b] + kSeqWeight * (nonempty_before + 1) onwards.  The
 // combine kernel derives the same range from seq_lens.
+template <typename Params>
 __device__ __forceinline__ void seq_blocks(const SeqTable& t, int b, int nonempty_before, int& g0, int& g1) {
-  const int w = t.prefix[b] + kSeqWeight * (nonempty_before + 1);
+  const int w = t.prefix[b] + Params::kSeqWeight * (nonempty_before + 1);
   const int n = t.prefix[b + 1] - t.prefix[b];
   g0 = w / t.per;
   g1 = (w + n - 1) / t.per;

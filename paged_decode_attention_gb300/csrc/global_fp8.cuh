@@ -64,7 +64,7 @@ static_assert(kBlocksPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory o
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
-                  const __grid_constant__ DecodeParams p) {
+                  const __grid_constant__ Fp8DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
   Smem& s = fp8::aligned_smem<Smem>(smem_raw);
 

@@ -15,14 +15,15 @@
 //   * this merge, which also serves the 8-bit global decode (no prefix, and the
 //     rows that one block finished whole are left alone).
 //
-// One block per row b*Hq + h, a row's partials being its prefix spans followed
-// by its blocks of the balanced schedule: two or four groups of 128 threads,
-// four dims a thread, each group takes every second or fourth partial with
-// kInFlight loads in flight, and the groups meet in shared memory.  Bound by
-// latency: the schedule is worked out before the block waits for the kernels
-// ahead of it.  Four groups where the rows' blocks are resident at once (8
-// sequences, 21 partials a row: a call takes 29.8 us with four, 31.2 with two),
-// two where they come in waves (64 sequences, 15 partials: 131.4 and 127.5).
+// A block takes kDims dims of row b*Hq + h, a row's partials being its prefix
+// spans followed by its blocks of the balanced schedule: groups of kDims / 4
+// threads, four dims a thread, group i takes partials i, i + kMergeGroups, ..
+// with kInFlight loads in flight, and the groups meet in shared memory.  Bound
+// by latency: the schedule is worked out before the block waits for the kernels
+// ahead of it.  With a prefix one block takes a row, in four groups where the
+// rows' blocks are resident at once (16 sequences, 16384 positions: a call takes
+// 35.4 us; with four blocks of four groups 39.5), in two where they come in
+// waves (64 sequences, 15 partials: 127.5 us, with four groups 131.4).
 #pragma once
 
 #include "combine.cuh"
@@ -31,8 +32,9 @@
 namespace pda {
 namespace prefix {
 
+template <typename Params>
 struct MergeParams {
-  DecodeParams d;            // the own positions' call: schedule, partials, output
+  Params d;                  // the own positions' call: schedule, partials, output
   const float* part_o;       // prefix partials (PrefixParams)
   const float2* part_ml;
   const int32_t* prefix_len;
@@ -40,36 +42,37 @@ struct MergeParams {
   int32_t splits;
 };
 
-constexpr int kGroupThreads = 128;
-constexpr int kInFlight = 4;  // partials in flight per thread
-
 // kPrefixSlices: slices of the output dims the prefix partials' (max, sum) come
 // in; 0 for no prefix.
-template <int kD, int kPrefixSlices, int kStepPages, int kMergeGroups>
-__global__ void __launch_bounds__(kMergeGroups* kGroupThreads) merge_kernel(const __grid_constant__ MergeParams mp) {
-  const DecodeParams& p = mp.d;
-  static_assert(kD == 4 * kGroupThreads, "four dims per thread");
-  __shared__ int s_sched[kGroupThreads / 32][3];
+template <int kD, int kPrefixSlices, int kStepPages, int kDims, int kMergeGroups, typename Params>
+__global__ void __launch_bounds__(kMergeGroups* kDims / 4) merge_kernel(const __grid_constant__ MergeParams<Params> mp) {
+  const Params& p = mp.d;
+  constexpr int kGroupThreads = kDims / 4;  // four dims per thread
+  constexpr int kBlocks = kD / kDims;       // per row
+  constexpr int kInFlight = kBlocks > 1 ? 8 : 4;  // partials in flight per thread
+  constexpr int kSched = 128;  // threads that work out the schedule
+  static_assert(kMergeGroups * kGroupThreads >= kSched, "they must exist");
+  __shared__ int s_sched[kSched / 32][3];
   __shared__ float s_m[kMergeGroups][kGroupThreads];  // per thread: the two dim slices differ
   __shared__ float s_l[kMergeGroups][kGroupThreads];
   __shared__ float4 s_o[kMergeGroups][kGroupThreads];
 
-  const int h = blockIdx.x;
-  const int Hq = gridDim.x;
+  const int h = blockIdx.x / kBlocks;
+  const int Hq = gridDim.x / kBlocks;
   const int b = blockIdx.y;
   const int tid = threadIdx.x % kGroupThreads;
   const int group = threadIdx.x / kGroupThreads;
-  const int d0 = 4 * tid;
+  const int d0 = blockIdx.x % kBlocks * kDims + 4 * tid;
   const size_t row = static_cast<size_t>(b) * Hq + h;
 
   // The schedule: weighted pages before sequence b, its own pages, the weighted
   // total (common.cuh).  The kernel ahead lets this one launch only after its
   // own wait, so the lengths are final and visible already.
-  if (group == 0) {
+  if (threadIdx.x < kSched) {
     int before = 0, mine = 0, total = 0;
-    for (int j = tid; j < p.batch; j += kGroupThreads) {
-      const int n = visible_pages(clamp_len(p, p.seq_lens[j], false), p.window);
-      const int wn = n > 0 ? n + kSeqWeight : 0;
+    for (int j = threadIdx.x; j < p.batch; j += kSched) {
+      const int n = visible_pages(schedule_len(p, p.seq_lens[j], false), p.window);
+      const int wn = n > 0 ? n + Params::kSeqWeight : 0;
       total += wn;
       before += j < b ? wn : 0;
       mine += j == b ? n : 0;
@@ -77,10 +80,10 @@ __global__ void __launch_bounds__(kMergeGroups* kGroupThreads) merge_kernel(cons
     before = __reduce_add_sync(0xffffffffu, before);
     mine = __reduce_add_sync(0xffffffffu, mine);
     total = __reduce_add_sync(0xffffffffu, total);
-    if ((tid & 31) == 0) {
-      s_sched[tid >> 5][0] = before;
-      s_sched[tid >> 5][1] = mine;
-      s_sched[tid >> 5][2] = total;
+    if ((threadIdx.x & 31) == 0) {
+      s_sched[threadIdx.x >> 5][0] = before;
+      s_sched[threadIdx.x >> 5][1] = mine;
+      s_sched[threadIdx.x >> 5][2] = total;
     }
   }
   int used = 0;  // prefix spans
@@ -89,14 +92,14 @@ __global__ void __launch_bounds__(kMergeGroups* kGroupThreads) merge_kernel(cons
   __syncthreads();
   int before = 0, mine = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kGroupThreads / 32; ++w) {
+  for (int w = 0; w < kSched / 32; ++w) {
     before += s_sched[w][0];
     mine += s_sched[w][1];
     total += s_sched[w][2];
   }
   const int per = span_pages(total, p.grid_x, p.min_pages);
-  const int g0 = mine > 0 ? (before + kSeqWeight) / per : 0;
-  const int g1 = mine > 0 ? (before + kSeqWeight + mine - 1) / per : -1;
+  const int g0 = mine > 0 ? (before + Params::kSeqWeight) / per : 0;
+  const int g1 = mine > 0 ? (before + Params::kSeqWeight + mine - 1) / per : -1;
   int own = g1 - g0 + 1;
   if (own > kMaxSplits || (own > 0 && (static_cast<int64_t>(g1) + b + 1) * Hq > p.part_rows)) {
     if (threadIdx.x == 0) report(p.status, ATTN_DEV_INTERNAL);  // cannot happen: partials beyond the workspace

@@ -69,7 +69,7 @@ int32_t make_serving_plan(int32_t kind, int32_t batch, int32_t max_seq_len, int3
   if (forced_blocks == 0) {
     const int64_t resident = sliding ? static_cast<int64_t>(num_sms) * pda::sliding::kBlocksPerSm / ATTN_SLIDING_HKV
                                      : static_cast<int64_t>(num_sms) * pda::global::kBlocksPerSm;
-    const int64_t useful = ((pages + pda::kSeqWeight) * batch + out->min_pages - 1) / out->min_pages;
+    const int64_t useful = ((pages + pda::DecodeParams::kSeqWeight) * batch + out->min_pages - 1) / out->min_pages;
     out->grid_x = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({resident, useful, pda::kMaxSplits})));
   }
   const int d = sliding ? ATTN_SLIDING_D : ATTN_GLOBAL_D;
@@ -198,7 +198,7 @@ int32_t run_read(int32_t kind, const void* k_pool, const void* v_pool, const uin
   // no more blocks than the (weighted) pages that max_seq_len allows
   int64_t pages = (max_seq_len + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE;
   if (span > 0) pages = std::min<int64_t>(pages, (static_cast<int64_t>(span) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE + 1);
-  const int64_t want = (pages + pda::kSeqWeight) * batch;
+  const int64_t want = (pages + pda::DecodeParams::kSeqWeight) * batch;
   p.d.grid_x = static_cast<int32_t>(
       std::max<int64_t>(1, std::min<int64_t>(want, num_sms * pda::fp8_read::kGridPerSm)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -209,6 +209,40 @@ int32_t run_read(int32_t kind, const void* k_pool, const void* v_pool, const uin
               : launch_pdl(pda::fp8_read::read_kernel<ATTN_GLOBAL_HKV, ATTN_GLOBAL_D>, grid, pda::fp8_read::kThreads, 0,
                            s, p);
   return launched(name, e);
+}
+
+// ---------------------------------------------------------------------------
+// The merge of global layers' partials where rows are few: combine.cuh's four
+// blocks per row, of 128 threads, which start beside the decode blocks, and
+// hold 32 partials in flight per round.  Where a sequence may have more than
+// two rounds of them, 16 blocks per row with 128 in flight.  One call over the
+// 8-bit cache in us, 4 blocks and 16: one sequence of 38656 (152 partials)
+// 28.8 and 21.2, one of 4000 (63) 9.2 and 9.8, 8 of 4700 17.2 and 21.2.
+// ---------------------------------------------------------------------------
+constexpr int kMergeDims = 32;  // of a row, per block of the second kind
+constexpr int kMergeThreads = 128;
+
+template <typename Params>
+constexpr auto kWideMerge = pda::prefix::merge_kernel<ATTN_GLOBAL_D, 0, 1, kMergeDims, kMergeThreads * 4 / kMergeDims, Params>;
+
+template <typename Params>
+int32_t ensure_merge(int dev) {
+  static bool comb_set[kMaxDevices] = {false}, wide_set[kMaxDevices] = {false};
+  const int32_t st = ensure_smem(pda::combine_kernel<ATTN_GLOBAL_D, Params>, 0, dev, comb_set);
+  return st != ATTN_OK ? st : ensure_smem(kWideMerge<Params>, 0, dev, wide_set);
+}
+
+template <typename Params>
+cudaError_t launch_merge(const Params& p, cudaStream_t s) {
+  if (p.grid_x > 64 * p.batch) {
+    pda::prefix::MergeParams<Params> mp{};
+    mp.d = p;
+    return launch_pdl(kWideMerge<Params>, dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / kMergeDims), p.batch), kMergeThreads, 0,
+                      s, mp);
+  }
+  return launch_pdl(pda::combine_kernel<ATTN_GLOBAL_D, Params>,
+                    dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / pda::kCombineCols), p.batch), pda::kCombineWarps * 32, 0, s,
+                    p);
 }
 
 // ---------------------------------------------------------------------------
@@ -284,7 +318,7 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
   g_last_launches = plan.merge_in_grid ? 1 : 2;
   if (g_validate_only) return ATTN_OK;
 
-  pda::DecodeParams p{};
+  pda::Fp8DecodeParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);  // bytes; addressed as such by the kernels
   p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
@@ -319,34 +353,29 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
   if (sliding) {
     static bool smem_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false};
     if ((st = ensure_smem(pda::sliding_fp8::decode_kernel, pda::sliding_fp8::kSmemBytes, dev, smem_set)) ||
-        (st = ensure_smem(pda::combine_kernel<ATTN_SLIDING_D>, 0, dev, comb_set)))
+        (st = ensure_smem(pda::combine_kernel<ATTN_SLIDING_D, pda::Fp8DecodeParams>, 0, dev, comb_set)))
       return st;
     e = launch_pdl(pda::sliding_fp8::decode_kernel, dim3(plan.grid_x, ATTN_SLIDING_HKV), pda::sliding_fp8::kThreads,
                    pda::sliding_fp8::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
     if (e == cudaSuccess && !plan.merge_in_grid)
-      e = launch_pdl(pda::combine_kernel<ATTN_SLIDING_D>,
+      e = launch_pdl(pda::combine_kernel<ATTN_SLIDING_D, pda::Fp8DecodeParams>,
                      dim3(ATTN_SLIDING_HQ * (ATTN_SLIDING_D / pda::kCombineCols), batch), pda::kCombineWarps * 32, 0,
                      s, p);
   } else {
-    // Few rows may have many partials each: combine.cuh's four blocks per row
-    // (8 sequences of up to 8192 positions: 21.4 us a call, 23.9 with one block per
-    // row).  Many rows: one block per row (64 of 500: 22.5 us, against 29.4).
+    // Many rows: one merge block per row (64 sequences of 500: 22.5 us a call,
+    // against 29.4 with launch_merge's four).
     const bool few_rows = batch * ATTN_GLOBAL_HQ <= 2 * num_sms;
-    const auto merge_kernel = pda::prefix::merge_kernel<ATTN_GLOBAL_D, 0, 1, 2>;
-    static bool smem_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false}, merge_set[kMaxDevices] = {false};
+    const auto row_kernel = pda::prefix::merge_kernel<ATTN_GLOBAL_D, 0, 1, ATTN_GLOBAL_D, 2, pda::Fp8DecodeParams>;
+    static bool smem_set[kMaxDevices] = {false}, row_set[kMaxDevices] = {false};
     if ((st = ensure_smem(pda::global_fp8::decode_kernel, pda::global_fp8::kSmemBytes, dev, smem_set)) ||
-        (st = ensure_smem(pda::combine_kernel<ATTN_GLOBAL_D>, 0, dev, comb_set)) ||
-        (st = ensure_smem(merge_kernel, 0, dev, merge_set)))
+        (st = ensure_smem(row_kernel, 0, dev, row_set)) || (st = ensure_merge<pda::Fp8DecodeParams>(dev)))
       return st;
-    pda::prefix::MergeParams mp{};
+    pda::prefix::MergeParams<pda::Fp8DecodeParams> mp{};
     mp.d = p;
     e = launch_pdl(pda::global_fp8::decode_kernel, dim3(plan.grid_x), pda::global_fp8::kThreads,
                    pda::global_fp8::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
     if (e == cudaSuccess)
-      e = few_rows ? launch_pdl(pda::combine_kernel<ATTN_GLOBAL_D>,
-                                dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / pda::kCombineCols), batch),
-                                pda::kCombineWarps * 32, 0, s, p)
-                   : launch_pdl(merge_kernel, dim3(ATTN_GLOBAL_HQ, batch), 2 * pda::prefix::kGroupThreads, 0, s, mp);
+      e = few_rows ? launch_merge(p, s) : launch_pdl(row_kernel, dim3(ATTN_GLOBAL_HQ, batch), 256, 0, s, mp);
   }
   return launched(name, e);
 }
@@ -359,7 +388,7 @@ constexpr int kMaxPrefixSplits = 128;
 // Whether every sequence reads the prefix for itself (joined.cuh).  That costs
 // a pass of L2 over the prefix per sequence and two kernels instead of three.
 // One call in us, joined and in spans: 1 sequence, 1 position 8.1 and 14.8,
-// 32768 28.9 and 41.8, 262144 98 and 202; 2 sequences, 65536 39.9 and 66.6,
+// 32768 19.3 and 41.8, 262144 88 and 202; 2 sequences, 65536 36.9 and 66.6,
 // 262144 164 and 203; 8 sequences, 1000 12.2 and 23.0, 5003 20.2 and 26.5, 12000
 // 30.9 and 32.3; 16 sequences, 4000 26.5 and 28.1, 5000 30.4 and 28.1; 32
 // sequences, 1200 24.9 and 26.9, 2000 30.5 and 28.8; 64 sequences, 16 25.3 and
@@ -477,15 +506,12 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (plan.joined) {
     const auto decode = pda::global::decode_kernel_listed<pda::JoinedParams>;
-    const auto combine = pda::combine_kernel<ATTN_GLOBAL_D, pda::JoinedParams>;
-    static bool dec_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false};
-    if ((st = ensure_smem(decode, pda::global::kSmemBytes, dev, dec_set)) || (st = ensure_smem(combine, 0, dev, comb_set)))
+    static bool dec_set[kMaxDevices] = {false};
+    if ((st = ensure_smem(decode, pda::global::kSmemBytes, dev, dec_set)) || (st = ensure_merge<pda::JoinedParams>(dev)))
       return st;
     cudaError_t e = launch_pdl(decode, dim3(plan.own.grid_x), pda::global::kThreads, pda::global::kSmemBytes, s, tm_k,
                                tm_v, jp);
-    if (e == cudaSuccess)
-      e = launch_pdl(combine, dim3(ATTN_GLOBAL_HQ * (ATTN_GLOBAL_D / pda::kCombineCols), batch),
-                     pda::kCombineWarps * 32, 0, s, jp);
+    if (e == cudaSuccess) e = launch_merge(jp, s);
     return launched(name, e);
   }
   pda::prefill_pair::PrefixParams pp{};
@@ -502,7 +528,7 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
   pp.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml_off);
   pp.splits = plan.splits;
 
-  pda::prefix::MergeParams mp{};
+  pda::prefix::MergeParams<pda::DecodeParams> mp{};
   mp.d = p;
   mp.part_o = pp.part_o;
   mp.part_ml = pp.part_ml;
@@ -513,8 +539,9 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
   using C = PrefixConfig;
   const auto prefix_kernel = pda::prefill_pair::prefill_pair_kernel<C, pda::prefill_pair::PrefixParams>;
   const bool few_rows = batch * ATTN_GLOBAL_HQ <= 2 * num_sms;  // the merge's blocks are resident at once
-  const auto merge_kernel = few_rows ? pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, 4>
-                                     : pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, 2>;
+  const auto merge_kernel =
+      few_rows ? pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, ATTN_GLOBAL_D, 4, pda::DecodeParams>
+               : pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, ATTN_GLOBAL_D, 2, pda::DecodeParams>;
   static bool pre_set[kMaxDevices] = {false}, dec_set[kMaxDevices] = {false}, merge_set[2][kMaxDevices] = {{false}};
   if ((st = ensure_smem(prefix_kernel, C::kSmemBytes, dev, pre_set)) ||
       (st = ensure_smem(pda::global::decode_kernel_partial, pda::global::kSmemBytes, dev, dec_set)) ||
@@ -532,7 +559,7 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
     e = launch_pdl(pda::global::decode_kernel_partial, dim3(plan.own.grid_x), pda::global::kThreads,
                    pda::global::kSmemBytes, s, tm_k, tm_v, p);
   if (e == cudaSuccess)
-    e = launch_pdl(merge_kernel, dim3(ATTN_GLOBAL_HQ, batch), (few_rows ? 4 : 2) * pda::prefix::kGroupThreads, 0, s, mp);
+    e = launch_pdl(merge_kernel, dim3(ATTN_GLOBAL_HQ, batch), few_rows ? 512 : 256, 0, s, mp);
   return launched(name, e);
 }
 

@@ -74,8 +74,8 @@ static_assert(kBlocksPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory o
 //     o = sum_g 2^{m_g - M} O_g / sum_g 2^{m_g - M} l_g,
 // writes o and puts the counter back to 0 for the next call (no other block
 // of this call touches it again).  Partials read back bypass L1.
-template <typename SmemT>
-__device__ __forceinline__ void merge_partials(const DecodeParams& p, const SeqTable& t, SmemT& s, int b, int g,
+template <typename Params, typename SmemT>
+__device__ __forceinline__ void merge_partials(const Params& p, const SeqTable& t, SmemT& s, int b, int g,
                                                int c, int h, int d0, float M, float Lsum, float4 O) {
   const int tt = threadIdx.x;
   int cnt = 0;  // non-empty sequences before b among b' = tt, tt + 128
@@ -86,7 +86,7 @@ __device__ __forceinline__ void merge_partials(const DecodeParams& p, const SeqT
   __threadfence();
   named_barrier_sync(1, kConsumerWarps * 32);
   int g0, g1;
-  seq_blocks(t, b, s.merge_cnt[0] + s.merge_cnt[1] + s.merge_cnt[2] + s.merge_cnt[3], g0, g1);
+  seq_blocks<Params>(t, b, s.merge_cnt[0] + s.merge_cnt[1] + s.merge_cnt[2] + s.merge_cnt[3], g0, g1);
   if (tt == 0) {
     const int before_me = atomicAdd(counter, 1);
     s.merge_last = before_me == g1 - g0;
