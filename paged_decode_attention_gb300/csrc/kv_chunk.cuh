@@ -75,17 +75,23 @@ struct Smem {
   alignas(16) float sin[2][kMaxTokens][1 << kPairBits];
 };
 
-// pos * (f.hi + f.lo), a frequency in half turns, less its whole turns, in
-// [-1, 1]: for an integer 0 <= pos < 2^24 the float product and its fma remainder
-// hold pos * f.hi exactly, and subtracting an even integer is exact.  Off by
-// 2^-24 of a half turn; sincospif adds 2 units in the last place, where the
-// 2^-21 of __sincosf would move three times as many values across a border
-// of e4m3.
-__device__ __forceinline__ float half_turns(FloatPair f, int pos) {
+// cos and sin of pos * (f.hi + f.lo), a frequency in half turns.  For an integer
+// 0 <= pos < 2^24 the float product and its fma remainder hold pos * f.hi
+// exactly, and subtracting whole turns, an even integer, is exact.  What the
+// last sum rounds away, up to 2^-25 half turns, turns the result by a first-order
+// step, so that the units in the last place of sincospif are all that is left:
+// an angle off by more moves values across the borders of e4m3.
+__device__ __forceinline__ void sincos_at(FloatPair f, int pos, float* sn, float* cs) {
   const float fp = static_cast<float>(pos);  // exact
   const float hi = fp * f.hi;
   const float rest = fmaf(fp, f.lo, fmaf(fp, f.hi, -hi));
-  return fmaf(-2.f, rintf(0.5f * hi), hi) + rest;
+  const float turn = fmaf(-2.f, rintf(0.5f * hi), hi);
+  const float x = turn + rest;
+  const float d = 3.14159265f * (rest - (x - turn));
+  float s0, c0;
+  sincospif(x, &s0, &c0);
+  *sn = fmaf(d, c0, s0);
+  *cs = fmaf(-d, s0, c0);
 }
 
 // One row as raw bf16 words: dims [V l, +V) and [D/2 + V l, +V).
@@ -128,9 +134,9 @@ __device__ __forceinline__ void widen(const RawRow<kD>& r, Row<kD>& x) {
   }
 }
 
-// x / sqrt(mean(x^2) + eps)
+// 1 / sqrt(mean(x^2) + eps)
 template <int kD>
-__device__ __forceinline__ void normalise(Row<kD>& r, float eps) {
+__device__ __forceinline__ float norm_factor(const Row<kD>& r, float eps) {
   float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < Row<kD>::kWords; ++j) ss = __ffma2_rn(r.lo[j], r.lo[j], __ffma2_rn(r.hi[j], r.hi[j], ss));
@@ -138,16 +144,22 @@ __device__ __forceinline__ void normalise(Row<kD>& r, float eps) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float mean = sum / static_cast<float>(kD) + eps;
-  float inv = rsqrtf(mean);
-  inv = fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.f), inv);  // one Newton step: the root to its last bit
-  const float2 inv2 = make_float2(inv, inv);
+  const float inv = rsqrtf(mean);
+  return fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.f), inv);  // one Newton step: the root to its last bit
+}
+
+template <int kD>
+__device__ __forceinline__ void times(Row<kD>& r, float f) {
+  const float2 f2 = make_float2(f, f);
 #pragma unroll
   for (int j = 0; j < Row<kD>::kWords; ++j) {
-    r.lo[j] = __fmul2_rn(r.lo[j], inv2);
-    r.hi[j] = __fmul2_rn(r.hi[j], inv2);
+    r.lo[j] = __fmul2_rn(r.lo[j], f2);
+    r.hi[j] = __fmul2_rn(r.hi[j], f2);
   }
 }
 
+// The norm's weights come first where they can: the product of two bf16 values
+// is exact in fp32, so a weighted row is rounded once, by its norm factor.
 template <int kD>
 __device__ __forceinline__ void scale(Row<kD>& r, const Row<kD>& w) {
 #pragma unroll
@@ -300,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<kTokens>) chunk_kernel(
 #pragma unroll
       for (int k = 1; k < kTokens; ++k) at = n == k ? pos[k] : at;
       float c, sn;
-      sincospif(half_turns(freq, at < 0 ? 0 : at), &sn, &c);
+      sincos_at(freq, at < 0 ? 0 : at, &sn, &c);
       s.cos[buf][n][threadIdx.x % kPairs] = c;
       s.sin[buf][n][threadIdx.x % kPairs] = sn;
     }
@@ -317,8 +329,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<kTokens>) chunk_kernel(
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         widen<kD>(rq[n][i], x);
-        normalise<kD>(x, p.eps);
+        const float f = norm_factor<kD>(x, p.eps);
         scale<kD>(x, w);
+        times<kD>(x, f);
         rotate<kD, kPairs>(cs, sn, x);
         store_bf16<kD>(p.q_out + (static_cast<size_t>(t) * kHq + 2 * warp + i) * kD, x);
       }
@@ -339,17 +352,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<kTokens>) chunk_kernel(
       };
       if constexpr (!kShared) {
         widen<kD>(rv[n], x);
-        normalise<kD>(x, p.eps);
+        times<kD>(x, norm_factor<kD>(x, p.eps));
         store(p.v_pool, p.v_scale, x);
       }
       widen<kD>(rk[n], x);
-      normalise<kD>(x, p.eps);
-      if constexpr (kShared) {
+      const float f = norm_factor<kD>(x, p.eps);
+      if constexpr (kShared) {  // (the keys are rounded after each of the two products: fetching the raw row
+        times<kD>(x, f);        // again for one rounding costs 4 % of a call)
         store(p.v_pool, p.v_scale, x);
         if (p.k_pool == nullptr) continue;  // a values-only cache
       }
       widen<kD>(wk_raw, w);
       scale<kD>(x, w);
+      if constexpr (!kShared) times<kD>(x, f);
       rotate<kD, kPairs>(cs, sn, x);
       store(p.k_pool, p.k_scale, x);
     }
