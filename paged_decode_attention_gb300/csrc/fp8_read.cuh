@@ -4,12 +4,15 @@
 // For every sequence the last min(L, span) positions (all for span <= 0) are
 // copied row by row from page block_table[b, l/16] to page out_table[b, l/16]
 // of the bf16 pools as e4m3(c) * 2^(s - 127).  The product is exact in fp32
-// and, in bf16's range, in bf16.  Rows outside are neither read nor written.
+// and, in bf16's range, in bf16.  Rows outside are not written.
 //
 // Bound by memory: D + 1 bytes in and 2 D out per row.  The concatenated
 // pages of all sequences are cut into equal spans (the balanced schedule of
-// common.cuh), one per block; blockIdx.y takes the keys or the values.  A thread converts 8 values at a time (8 bytes in, 16 out, both
-// coalesced) and keeps all of a page's loads in flight.
+// common.cuh), one per block; blockIdx.y takes the keys or the values.  A thread
+// converts 8 values at a time (8 bytes in, 16 out, both coalesced) and keeps up
+// to 8 such loads in flight.  Eight sliding contexts of 2047 positions: 34 us,
+// 0.87 of the measured rate of a copy, which writes one byte per byte read and
+// not two.
 #pragma once
 
 #include "fp8.cuh"

@@ -14,12 +14,11 @@
 // global one 35 KB (34 KB).  So every byte is read once and written once, and
 // the arithmetic that several rows share is done once: a block of 8 warps
 // takes kTokens tokens at a time, each thread below kTokens kPairs turns one
-// pair's angle into (cos, sin) for all heads of its token, one barrier a round.  The pair
-// frequencies theta^(-2i/D) are products of at most 7 host-computed factors
-// (one per set bit of i, in float pairs: 2^-43 relative), formed before the
-// block waits for the previous kernel; the angles are exact to
-// 2^-24 of a half turn.  The row
-// arithmetic runs on pairs of dims (packed fp32 instructions).
+// pair's angle into (cos, sin) for all heads of its token, one barrier a round.
+// The pair frequencies theta^(-2i/D) are products of at most 7 host-computed
+// factors (one per set bit of i, in float pairs: 2^-43 relative), formed before
+// the block waits for the previous kernel.  The row arithmetic runs on pairs of
+// dims (packed fp32 instructions).
 //
 // Warp w of a sliding token takes q heads 2w and 2w+1, key head w and value
 // head w; of a global one q heads 2w and 2w+1, and the warp that t mod 8
@@ -30,8 +29,10 @@
 // one below; sliding layers always one (8192 tokens: 43.3 us, 0.91 of the
 // measured copy rate, against 44.7 us).  Tasks that each warp takes on its own,
 // without barrier or shared angles, were slower on both (46.4 us sliding; 34.8
-// against 27.0 us for 4096 global tokens into an 8-bit cache).  Lane l holds dims [V l, V l + V) and their
-// rotation partners, V = D / 64, as in kv_append.cuh.
+// against 27.0 us for 4096 global tokens into an 8-bit cache, 0.77 of the copy
+// rate: the pair of warps with the shared head and the e4m3 conversions bound it).
+// Lane l holds dims [V l, V l + V) and their rotation partners, V = D / 64, as in
+// kv_append.cuh.
 #pragma once
 
 #include "fp8.cuh"

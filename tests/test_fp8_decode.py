@@ -83,6 +83,13 @@ def test_forced_splits(cuda_lib, kind, num_splits):
     check(kind, c.on(DEV), window_of(kind), num_splits=num_splits)
 
 
+@pytest.mark.parametrize("lens", [[20000], [0, 17000], [1, 6001], [9000, 0, 5]])
+@pytest.mark.parametrize("num_splits", [0, 500])
+def test_long_sequences_in_many_partials(cuda_lib, lens, num_splits):
+    c = Fp8Case(make_case("global", lens, seed=49, window=0))
+    check("global", c.on(DEV), 0, num_splits=num_splits)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_full_batch_of_mixed_lengths(cuda_lib, kind):
     r = np.random.RandomState(35)

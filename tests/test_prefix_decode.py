@@ -84,6 +84,12 @@ def test_a_long_prefix(cuda_lib, out_dtype):
     check(Case(9001, [0, 5, 1500, 33, 16, 1, 0, 700, 80], seed=64), out_dtype=out_dtype)
 
 
+@BOTH
+@pytest.mark.parametrize("prefix,lens", [(20001, [0]), (9000, [700]), (15, [16000]), (8192, [0, 33])])
+def test_one_or_two_sequences_in_many_partials(cuda_lib, prefix, lens, splits):
+    check(Case(prefix, lens, seed=77), prefix_splits=splits)
+
+
 @pytest.mark.parametrize("prefix_splits", [0, 1, 2, 3, 16, 128, 1000])
 @pytest.mark.parametrize("num_splits", [0, 1, 50])
 def test_forced_splits(cuda_lib, num_splits, prefix_splits):
@@ -165,7 +171,7 @@ def test_bad_prefix_page_is_flagged_and_reads_as_zeros(cuda_lib, page, splits):
     assert st == 0 and torch.equal(o, want)
 
 
-@pytest.mark.parametrize("prefix_splits", [1, 3])
+@pytest.mark.parametrize("prefix_splits", [0, 1, 3])
 def test_a_visible_nan_shows(cuda_lib, prefix_splits):
     c = Case(500, [5, 700], seed=73)
     clean, _ = decode(c.args(), prefix_splits=prefix_splits)
