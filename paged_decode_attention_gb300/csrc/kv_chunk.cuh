@@ -12,25 +12,22 @@
 //
 // Bound by memory: a sliding token moves 32 KB (28 KB with an 8-bit cache), a
 // global one 35 KB (34 KB).  So every byte is read once and written once, and
-// the arithmetic that several rows share is done once: a block of 8 warps
-// takes kTokens tokens at a time, each thread below kTokens kPairs turns one
-// pair's angle into (cos, sin) for all heads of its token, one barrier a round.
-// The pair frequencies theta^(-2i/D) are products of at most 7 host-computed
-// factors (one per set bit of i, in float pairs: 2^-43 relative), formed before
-// the block waits for the previous kernel.  The row arithmetic runs on pairs of
-// dims (packed fp32 instructions).
+// the arithmetic that several rows share is done once: a block takes a token at
+// a time, each thread below kPairs turns one pair's angle into (cos, sin) for all
+// heads of the token, one barrier a token.  The pair frequencies theta^(-2i/D)
+// are products of at most 7 host-computed factors (one per set bit of i, in float
+// pairs: 2^-43 relative), formed before the block waits for the previous kernel.
+// The row arithmetic runs on pairs of dims (packed fp32 instructions).
 //
-// Warp w of a sliding token takes q heads 2w and 2w+1, key head w and value
-// head w; of a global one q heads 2w and 2w+1, and the warp that t mod 8
-// names also the key/value head: one warp in eight has half as much again to
-// do, and the others wait for it at the barrier.  So global layers take two
-// tokens a round once there are more tokens than SMs (2432 tokens 18.9 -> 16.8 us,
-// 304 tokens 4.6 -> 3.7 us; 64 tokens, on half as many SMs, 3.0 -> 3.7 us) and
-// one below; sliding layers always one (8192 tokens: 43.3 us, 0.91 of the
-// measured copy rate, against 44.7 us).  Tasks that each warp takes on its own,
-// without barrier or shared angles, were slower on both (46.4 us sliding; 34.8
-// against 27.0 us for 4096 global tokens into an 8-bit cache, 0.77 of the copy
-// rate: the pair of warps with the shared head and the e4m3 conversions bound it).
+// Warp w of the first eight takes q heads 2w and 2w+1, on sliding layers also key
+// head w and value head w; on global layers a ninth warp takes the head that is
+// key and value.  8192 sliding tokens: 43.2 us, 0.92 of the measured copy rate;
+// 4096 global tokens into an 8-bit cache 23.6 us, 0.89.  Slower, on the latter:
+// the shared head as a second job of one of eight warps, for which the others
+// wait at the barrier (27.0 us with two tokens a round, 31.5 with one), two tokens
+// a round of the nine warps (25.2; 608 tokens 4.1 us against 5.1, more than three
+// blocks per SM holding one each), two blocks per SM instead of three (26.8), tasks
+// that each warp takes on its own, without barrier or shared angles (34.8).
 // Lane l holds dims [V l, V l + V) and their rotation partners, V = D / 64, as in
 // kv_append.cuh.
 #pragma once
@@ -41,9 +38,10 @@
 namespace pda {
 namespace chunk {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kMaxTokens = 2;  // per round of a block
+constexpr int kQWarps = 8;  // two query heads each
+template <bool kShared>
+constexpr int kThreads = (kShared ? kQWarps + 1 : kQWarps) * 32;
+constexpr int kBlocksPerSm = 3;
 constexpr int kPairBits = 7;  // pairs 0..127
 
 struct ChunkParams {
@@ -71,9 +69,9 @@ struct ChunkParams {
 struct Smem {
   int32_t cu_q[kMaxBatch + 1];
   int32_t len[kMaxBatch];
-  // cos and sin of the tokens' pairs, double-buffered
-  alignas(16) float cos[2][kMaxTokens][1 << kPairBits];
-  alignas(16) float sin[2][kMaxTokens][1 << kPairBits];
+  // cos and sin of the token's pairs, double-buffered
+  alignas(16) float cos[2][1 << kPairBits];
+  alignas(16) float sin[2][1 << kPairBits];
 };
 
 // cos and sin of pos * (f.hi + f.lo), a frequency in half turns.  For an integer
@@ -239,15 +237,11 @@ __device__ __forceinline__ void store_fp8(uint8_t* dst, uint8_t* scale, Row<kD>&
   if (lane == 0) *scale = static_cast<uint8_t>(s);
 }
 
-// Blocks per SM that the registers of kTokens tokens' rows allow.
-template <int kTokens>
-constexpr int kBlocksPerSm = kTokens == 1 ? 3 : 2;
-
-template <int kD, int kHq, int kHkv, int kPairs, bool kShared, bool kFp8, int kTokens>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm<kTokens>) chunk_kernel(const __grid_constant__ ChunkParams p) {
+template <int kD, int kHq, int kHkv, int kPairs, bool kShared, bool kFp8>
+__global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int kRowLen = kHq * kD + (kShared ? kD : 2 * kHkv * kD);
-  static_assert(kHq == 2 * kWarps && (kShared ? kHkv == 1 : kHkv == kWarps), "rows of a token by warp");
-  static_assert(kTokens * kPairs <= kThreads && kPairs <= (1 << kPairBits) && kPairs % (kD / 64) == 0, "pairs by thread");
+  static_assert(kHq == 2 * kQWarps && (kShared ? kHkv == 1 : kHkv == kQWarps), "rows of a token by warp");
+  static_assert(kPairs <= kThreads<kShared> && kPairs <= (1 << kPairBits) && kPairs % (kD / 64) == 0, "pairs by thread");
   __shared__ Smem s;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -261,115 +255,101 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<kTokens>) chunk_kernel(
   // or the tables, or reading the cache.
   wait_for_primary_grid();
   allow_dependent_launch();
-  for (int i = threadIdx.x; i <= p.batch; i += kThreads) {
+  for (int i = threadIdx.x; i <= p.batch; i += kThreads<kShared>) {
     s.cu_q[i] = p.cu_q[i];
     if (i < p.batch) s.len[i] = p.seq_lens[i];
   }
-  RawRow<kD> wq_raw, wk_raw;
-  load_raw<kD>(p.w_q, wq_raw);
-  load_raw<kD>(p.w_k, wk_raw);
+  const bool has_kv = !kShared || warp == kQWarps;
+  RawRow<kD> w_raw, wk_raw;  // the warp's weights; of a warp with both, the keys'
+  load_raw<kD>(kShared && has_kv ? p.w_k : p.w_q, w_raw);
+  if constexpr (!kShared) load_raw<kD>(p.w_k, wk_raw);
   __syncthreads();
 
   int buf = 0;
-  for (int t0 = blockIdx.x * kTokens; t0 < p.total_q; t0 += gridDim.x * kTokens) {
-    // this warp's rows of both tokens, all in flight together
-    RawRow<kD> rq[kTokens][2], rk[kTokens], rv[kTokens];
-    int pos[kTokens];  // -1: the token is left alone
-    int32_t phys[kTokens];
-#pragma unroll
-    for (int n = 0; n < kTokens; ++n) {
-      const int t = t0 + n;
-      pos[n] = -1;
-      phys[n] = 0;
-      if (t >= p.total_q) continue;
-      const __nv_bfloat16* row = p.qkv + static_cast<size_t>(t) * kRowLen;
-      const bool has_kv = !kShared || warp == (t & (kWarps - 1));
-      load_raw<kD>(row + (2 * warp) * kD, rq[n][0]);
-      load_raw<kD>(row + (2 * warp + 1) * kD, rq[n][1]);
-      if (has_kv) load_raw<kD>(row + (kHq + (kShared ? 0 : warp)) * kD, rk[n]);
-      if constexpr (!kShared) load_raw<kD>(row + (kHq + kHkv + warp) * kD, rv[n]);
-      // the token's sequence: the number of sequences that end at or before t
-      // (the same in every warp of the block)
-      int b = 0;
-      for (int j0 = 0; j0 < p.batch; j0 += 32) {
-        const int j = j0 + lane;
-        b += __popc(__ballot_sync(0xffffffffu, j < p.batch && s.cu_q[j + 1] <= t));
-      }
-      if (b >= p.batch) continue;  // rows behind the last sequence are left alone
+  for (int t = blockIdx.x; t < p.total_q; t += gridDim.x) {
+    // this warp's rows, all in flight together
+    const __nv_bfloat16* src = p.qkv + static_cast<size_t>(t) * kRowLen;
+    RawRow<kD> rq[2], rk, rv;  // (global layers: the shared head, head kHq, in the ninth warp's rq[0])
+    load_raw<kD>(src + (2 * warp) * kD, rq[0]);
+    if (!kShared || warp < kQWarps) load_raw<kD>(src + (2 * warp + 1) * kD, rq[1]);
+    if constexpr (!kShared) {
+      load_raw<kD>(src + (kHq + warp) * kD, rk);
+      load_raw<kD>(src + (kHq + kHkv + warp) * kD, rv);
+    }
+    // the token's sequence: the number of sequences that end at or before t
+    // (the same in every warp of the block)
+    int pos = -1;  // the token is left alone
+    int32_t phys = 0;
+    int b = 0;
+    for (int j0 = 0; j0 < p.batch; j0 += 32) {
+      const int j = j0 + lane;
+      b += __popc(__ballot_sync(0xffffffffu, j < p.batch && s.cu_q[j + 1] <= t));
+    }
+    if (b < p.batch) {  // rows behind the last sequence are left alone
       const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1];
       const int L = s.len[b];
       const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
       // a sequence whose numbers do not fit together is left alone as a whole
       if (q0 < 0 || t < q0 || q1 > p.total_q || q1 - q0 > L || L > cap) {
         if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
-        continue;
+      } else {
+        pos = L - (q1 - q0) + (t - q0);
+        if (has_kv) phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kPage];
       }
-      pos[n] = L - (q1 - q0) + (t - q0);
-      if (has_kv) phys[n] = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos[n] / kPage];
     }
-    if (threadIdx.x < kTokens * kPairs) {
-      const int n = threadIdx.x / kPairs;
-      int at = pos[0];
-#pragma unroll
-      for (int k = 1; k < kTokens; ++k) at = n == k ? pos[k] : at;
-      float c, sn;
-      sincos_at(freq, at < 0 ? 0 : at, &sn, &c);
-      s.cos[buf][n][threadIdx.x % kPairs] = c;
-      s.sin[buf][n][threadIdx.x % kPairs] = sn;
-    }
-    __syncthreads();  // one per round: the buffer written next was read before this barrier
+    if (threadIdx.x < kPairs)
+      sincos_at(freq, pos < 0 ? 0 : pos, &s.sin[buf][threadIdx.x], &s.cos[buf][threadIdx.x]);
+    __syncthreads();  // one per token: the buffer written next was read before this barrier
+    const float* cs = s.cos[buf];
+    const float* sn = s.sin[buf];
+    buf ^= 1;
+    if (pos < 0) continue;
 
-#pragma unroll
-    for (int n = 0; n < kTokens; ++n) {
-      if (pos[n] < 0) continue;
-      const int t = t0 + n;
-      const float* cs = s.cos[buf][n];
-      const float* sn = s.sin[buf][n];
-      Row<kD> x, w;
-      widen<kD>(wq_raw, w);
+    Row<kD> x, w;
+    if (!kShared || warp < kQWarps) {
+      widen<kD>(w_raw, w);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        widen<kD>(rq[n][i], x);
+        widen<kD>(rq[i], x);
         const float f = norm_factor<kD>(x, p.eps);
         scale<kD>(x, w);
         times<kD>(x, f);
         rotate<kD, kPairs>(cs, sn, x);
         store_bf16<kD>(p.q_out + (static_cast<size_t>(t) * kHq + 2 * warp + i) * kD, x);
       }
-      if (kShared && warp != (t & (kWarps - 1))) continue;
-      if (phys[n] < 0 || static_cast<int64_t>(phys[n]) >= p.num_pages) {
-        if (lane == 0) report(p.status, ATTN_DEV_BAD_PAGE);
-        continue;
-      }
-      const int c = kShared ? 0 : warp;
-      const int row = pos[n] % kPage;
-      const size_t off = ((static_cast<size_t>(phys[n]) * kPage + row) * kHkv + c) * kD;
-      const size_t soff = (static_cast<size_t>(phys[n]) * kHkv + c) * kPage + row;
-      const auto store = [&](void* pool, uint8_t* scales, Row<kD>& y) {
-        if constexpr (kFp8)
-          store_fp8<kD>(static_cast<uint8_t*>(pool) + off, scales + soff, y);
-        else
-          store_bf16<kD>(static_cast<__nv_bfloat16*>(pool) + off, y);
-      };
-      if constexpr (!kShared) {
-        widen<kD>(rv[n], x);
-        times<kD>(x, norm_factor<kD>(x, p.eps));
-        store(p.v_pool, p.v_scale, x);
-      }
-      widen<kD>(rk[n], x);
-      const float f = norm_factor<kD>(x, p.eps);
-      if constexpr (kShared) {  // (the keys are rounded after each of the two products: fetching the raw row
-        times<kD>(x, f);        // again for one rounding costs 4 % of a call)
-        store(p.v_pool, p.v_scale, x);
-        if (p.k_pool == nullptr) continue;  // a values-only cache
-      }
-      widen<kD>(wk_raw, w);
-      scale<kD>(x, w);
-      if constexpr (!kShared) times<kD>(x, f);
-      rotate<kD, kPairs>(cs, sn, x);
-      store(p.k_pool, p.k_scale, x);
+      if (kShared) continue;
     }
-    buf ^= 1;
+    if (phys < 0 || static_cast<int64_t>(phys) >= p.num_pages) {
+      if (lane == 0) report(p.status, ATTN_DEV_BAD_PAGE);
+      continue;
+    }
+    const int c = kShared ? 0 : warp;
+    const int row = pos % kPage;
+    const size_t off = ((static_cast<size_t>(phys) * kPage + row) * kHkv + c) * kD;
+    const size_t soff = (static_cast<size_t>(phys) * kHkv + c) * kPage + row;
+    const auto store = [&](void* pool, uint8_t* scales, Row<kD>& y) {
+      if constexpr (kFp8)
+        store_fp8<kD>(static_cast<uint8_t*>(pool) + off, scales + soff, y);
+      else
+        store_bf16<kD>(static_cast<__nv_bfloat16*>(pool) + off, y);
+    };
+    if constexpr (!kShared) {
+      widen<kD>(rv, x);
+      times<kD>(x, norm_factor<kD>(x, p.eps));
+      store(p.v_pool, p.v_scale, x);
+    }
+    widen<kD>(kShared ? rq[0] : rk, x);
+    const float f = norm_factor<kD>(x, p.eps);
+    if constexpr (kShared) {  // (the keys are rounded after each of the two products: the raw row once
+      times<kD>(x, f);        // more, for one rounding, costs 8 % of a call in registers)
+      store(p.v_pool, p.v_scale, x);
+      if (p.k_pool == nullptr) continue;  // a values-only cache
+    }
+    widen<kD>(kShared ? w_raw : wk_raw, w);
+    scale<kD>(x, w);
+    if constexpr (!kShared) times<kD>(x, f);
+    rotate<kD, kPairs>(cs, sn, x);
+    store(p.k_pool, p.k_scale, x);
   }
 }
 

@@ -135,19 +135,16 @@ int32_t run_chunk(int32_t kind, bool fp8, const void* qkv, const void* w_q, cons
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   namespace ch = pda::chunk;
-  const bool two = !sliding && total_q > num_sms;  // tokens a round (kv_chunk.cuh)
-  const int tokens = two ? 2 : 1;
-  const int blocks = std::min((total_q - 1) / tokens + 1, num_sms * (two ? ch::kBlocksPerSm<2> : ch::kBlocksPerSm<1>));
-  const auto launch = [&](auto kernel) { return launch_pdl(kernel, dim3(blocks), ch::kThreads, 0, s, p); };
+  const int blocks = std::min(total_q, num_sms * ch::kBlocksPerSm);
   const auto kernels = [&](auto fp8_c) {
     constexpr bool kFp8 = decltype(fp8_c)::value;
     if (sliding)
-      return launch(ch::chunk_kernel<ATTN_SLIDING_D, ATTN_SLIDING_HQ, ATTN_SLIDING_HKV, ATTN_SLIDING_ROPE_PAIRS, false,
-                                     kFp8, 1>);
-    return two ? launch(ch::chunk_kernel<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ, ATTN_GLOBAL_HKV, ATTN_GLOBAL_ROPE_PAIRS, true,
-                                         kFp8, 2>)
-               : launch(ch::chunk_kernel<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ, ATTN_GLOBAL_HKV, ATTN_GLOBAL_ROPE_PAIRS, true,
-                                         kFp8, 1>);
+      return launch_pdl(ch::chunk_kernel<ATTN_SLIDING_D, ATTN_SLIDING_HQ, ATTN_SLIDING_HKV, ATTN_SLIDING_ROPE_PAIRS,
+                                         false, kFp8>,
+                        dim3(blocks), ch::kThreads<false>, 0, s, p);
+    return launch_pdl(ch::chunk_kernel<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ, ATTN_GLOBAL_HKV, ATTN_GLOBAL_ROPE_PAIRS, true,
+                                       kFp8>,
+                      dim3(blocks), ch::kThreads<true>, 0, s, p);
   };
   const cudaError_t e = fp8 ? kernels(std::true_type{}) : kernels(std::false_type{});
   return launched(name, e);
