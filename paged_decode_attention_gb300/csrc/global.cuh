@@ -130,7 +130,11 @@ __device__ __forceinline__ int s_kstep_dim(int w, int ks) {
 }
 
 // kPartial: every segment is left as a partial, a whole sequence's too, for a
-// caller that merges it with others (prefix.cuh).
+// caller that merges it with others (prefix.cuh).  The kernel ahead in the stream
+// is then one that this one takes nothing from, and that let it launch after its
+// own wait: what came before that one is complete, so the blocks start at once
+// beside it.  Block 0 alone waits for it, at its end, so that this grid does not
+// complete before it and the merge, which waits for this grid, finds both.
 template <bool kShared, bool kPartial = false, typename Params>
 __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const Params& p,
                                             const KeyRebuild* kr) {
@@ -169,7 +173,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
   } else {
     warm_q(p, s.table, kHq * kD, 0, kHq * kD * 2, kConsumerWarps * 32);
   }
-  wait_for_primary_grid();
+  if constexpr (!kPartial) wait_for_primary_grid();
   allow_dependent_launch();
   if constexpr (kShared) {
     if (warp < kConsumerWarps) {  // w_k to shared memory; published by confirm_seq_table's barrier
@@ -185,7 +189,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
   const SeqTable& t = s.table;
   const Span sp = t.span;
   const int n_pages = sp.end - sp.begin;
-  if (n_pages <= 0) return;
+  if (n_pages <= 0) {
+    if (kPartial && gb == 0) wait_for_primary_grid();
+    return;
+  }
 
   if (warp == kConsumerWarps) {
     // ---------------- producer ----------------
@@ -202,6 +209,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
         tma_load_3d_hint(s.v[stage], tm_v, 0, y, 0, &s.full[stage], policy);
       });
     }
+    if (kPartial && gb == 0) wait_for_primary_grid();
     return;
   }
 

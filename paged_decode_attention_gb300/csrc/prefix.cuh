@@ -23,7 +23,8 @@
 // ahead of it.  With a prefix one block takes a row, in four groups where the
 // rows' blocks are resident at once (16 sequences, 16384 positions: a call takes
 // 35.4 us; with four blocks of four groups 39.5), in two where they come in
-// waves (64 sequences, 15 partials: 127.5 us, with four groups 131.4).
+// waves (64 sequences, 15 partials: 127.5 us, with four groups 131.4; 120.6 since
+// the own positions' kernel no longer waits for the prefix kernel).
 #pragma once
 
 #include "combine.cuh"

@@ -383,15 +383,16 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
 using PrefixConfig = pda::prefill_pair::GlobalPairConfig;
 constexpr int kMaxPrefixSplits = 128;
 // Whether every sequence reads the prefix for itself (joined.cuh).  That costs
-// a pass of L2 over the prefix per sequence and two kernels instead of three.
-// One call in us, joined and in spans: 1 sequence, 1 position 8.1 and 14.8,
-// 32768 19.3 and 41.8, 262144 88 and 202; 2 sequences, 65536 36.9 and 66.6,
-// 262144 164 and 203; 8 sequences, 1000 12.2 and 23.0, 5003 20.2 and 26.5, 12000
-// 30.9 and 32.3; 16 sequences, 4000 26.5 and 28.1, 5000 30.4 and 28.1; 32
-// sequences, 1200 24.9 and 26.9, 2000 30.5 and 28.8; 64 sequences, 16 25.3 and
-// 29.6, 600 34.4 and 32.2; 128 sequences, 200 49.2 and 40.2.
+// a pass of L2 over the prefix per sequence and saves a kernel and a merge of
+// spans.  One call in us, joined and in spans: 1 sequence, 16 positions 8.2 and
+// 12.1, 32768 18.9 and 36.7, 262144 88 and 202; 2 sequences, 16384 17.0 and 25.7,
+// 262144 160 and 197; 3 of 65536 51 and 62; 4 of 22000 30.0 and 32.4; 8 of 2000 14.1
+// and 19.5, 8000 24.2 and 24.6, 10500 28.6 and 26.5; 12 of 2000 15.9 and 20.2,
+// 6500 27.6 and 23.4; 16 of 1000 16.5 and 19.2, 3000 24.1 and 21.4; 24 of 500 18.2
+// and 20.4, 2500 27.9 and 22.7; 32 of 100 17.8 and 19.8, 500 21.7 and 20.6.  The
+// rule runs through the crossings.
 bool join_prefix(int32_t batch, int32_t max_prefix_len) {
-  return batch <= 2 || static_cast<int64_t>(batch) * (static_cast<int64_t>(max_prefix_len) + 1536) <= 98304;
+  return batch <= 2 || static_cast<int64_t>(batch) * batch * (static_cast<int64_t>(max_prefix_len) + 300) <= 560000;
 }
 constexpr int kPrefixMinSteps = 2;  // steps of 64 keys a span is given at least (32 sequences, 2000 positions: 28.8 us)
 

@@ -136,11 +136,11 @@ def test_prefix_plan(lib):
     rows = ps * 64 * 16
     assert (ns, ps) == (own, 9) and ws == own_ws + rows * 512 * 4 + rows * 2 * 8
     # short prefixes, small batches: one list of pages per sequence, no spans
-    for B, n in ((16, 4608), (1, 262144), (2, 131072), (64, 0), (4, 0)):
+    for B, n in ((16, 1887), (8, 8450), (1, 262144), (2, 131072), (43, 2), (4, 0)):
         gx, ps, ws = pda.attn_decode_prefix_plan(B, n, 100)
         assert (gx, ps, ws) == (pda.attn_decode_fp8_plan(pda.KIND_GLOBAL, B, -(-n // 16) * 16 + 100, 0)[0], 0,
                                 pda.attn_decode_fp8_plan(pda.KIND_GLOBAL, B, -(-n // 16) * 16 + 100, 0)[2])
-    assert pda.attn_decode_prefix_plan(16, 4609, 100)[1] == 36  # spans of no less than two steps of 64 keys
+    assert pda.attn_decode_prefix_plan(16, 1888, 100)[1] == 15  # spans of no less than two steps of 64 keys
     assert pda.attn_decode_prefix_plan(65, 0, 16)[1] == 1 and pda.attn_decode_prefix_plan(2, 2**31 - 1, 2**31 - 1)[1] == 0
     assert pda.attn_decode_prefix_plan(256, 262144, 16)[1] == 2
     assert pda.attn_decode_prefix_plan(8, 262144, 16, prefix_splits=7)[1] == 7
