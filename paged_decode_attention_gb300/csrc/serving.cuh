@@ -352,7 +352,7 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
     if ((st = ensure_smem(pda::sliding_fp8::decode_kernel, pda::sliding_fp8::kSmemBytes, dev, smem_set)) ||
         (st = ensure_smem(pda::combine_kernel<ATTN_SLIDING_D, pda::Fp8DecodeParams>, 0, dev, comb_set)))
       return st;
-    e = launch_pdl(pda::sliding_fp8::decode_kernel, dim3(plan.grid_x, ATTN_SLIDING_HKV), pda::sliding_fp8::kThreads,
+    e = launch_pdl(pda::sliding_fp8::decode_kernel, dim3(ATTN_SLIDING_HKV, plan.grid_x), pda::sliding_fp8::kThreads,
                    pda::sliding_fp8::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
     if (e == cudaSuccess && !plan.merge_in_grid)
       e = launch_pdl(pda::combine_kernel<ATTN_SLIDING_D, pda::Fp8DecodeParams>,
