@@ -242,7 +242,7 @@ int32_t attn_decode_global_shared(const void* q, const void* kv_pool, const void
  *               raises ATTN_DEV_BAD_SEQ_LEN and is clamped
  *
  * Every array 16 bytes aligned (prefix_table, prefix_len 4).  Three kernels
- * with spans, two without.
+ * with spans, one or two without.
  * Weights are rounded to bf16 for their product with the values.
  */
 int32_t attn_decode_global_prefix(const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,

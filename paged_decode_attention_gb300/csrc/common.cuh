@@ -108,6 +108,9 @@ struct NoHole {
 };
 __device__ __forceinline__ NoHole hole_of(const DecodeParams&) { return {}; }
 
+// Whether block g takes sequence g whole, instead of its span of the list.
+__device__ __forceinline__ bool by_sequence(const DecodeParams&) { return false; }
+
 __device__ __forceinline__ int span_pages(int total, int grid_x, int min_pages) {
   const int per = (total + grid_x - 1) / grid_x;
   return per > min_pages ? per : min_pages;
@@ -141,6 +144,15 @@ __device__ __forceinline__ void scan_seq_lens(const Params& p, SeqTable& t, int 
       carry += __shfl_sync(0xffffffffu, v, 31);
     }
     __syncwarp();
+    if (by_sequence(p)) {
+      if (lane == 0) {
+        t.per = 1;
+        t.span.begin = g < p.batch ? t.prefix[g] : carry;
+        t.span.end = g < p.batch ? t.prefix[g + 1] : carry;
+      }
+      __syncwarp();
+      return;
+    }
     // block g's weighted range [w0, w1) and the real pages it maps to
     const int total = carry + Params::kSeqWeight * nonempty;
     const int per = span_pages(total, p.grid_x, p.min_pages);

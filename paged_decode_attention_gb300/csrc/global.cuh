@@ -191,6 +191,9 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
   const int n_pages = sp.end - sp.begin;
   if (n_pages <= 0) {
     if (kPartial && gb == 0) wait_for_primary_grid();
+    if (by_sequence(p) && gb < p.batch)  // there is no merge to write the empty sums
+      for (int i = threadIdx.x; i < kHq * kD / 4; i += kThreads)
+        store_out4(p, static_cast<size_t>(gb) * kHq * kD + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
   }
 

@@ -62,10 +62,11 @@ struct Smem {
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;  // + alignment slack
 static_assert(kBlocksPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of the resident blocks");
 
+template <typename Params>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
-                  const __grid_constant__ Fp8DecodeParams p) {
+                  const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   Smem& s = fp8::aligned_smem<Smem>(smem_raw);
 
@@ -104,7 +105,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   const SeqTable& t = s.table;
   const Span sp = t.span;
   const int n_pages = sp.end - sp.begin;
-  if (n_pages <= 0) return;
+  if (n_pages <= 0) {
+    if (by_sequence(p) && gb < p.batch)  // there is no merge to write the empty sums
+      for (int i = threadIdx.x; i < kHq * kD / 4; i += kThreads)
+        store_out4(p, static_cast<size_t>(gb) * kHq * kD + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+    return;
+  }
 
   if (warp == kConsumerWarps) {
     // ---------------- producer ----------------

@@ -9,8 +9,9 @@
 // lies between is a hole.  (Decode attention does not depend on the numbers.)
 //
 // Every sequence reads the prefix's pages for itself, from L2 after the first,
-// but there is no second and third kernel: the better way where the prefix is
-// short or the batch small (attn_decode_global_prefix chooses).
+// but there is no kernel for the prefix, and where the lists are short, with a
+// block for each, no merge either: the better way where the prefix is short or
+// the batch small (attn_decode_global_prefix chooses).
 #pragma once
 
 #include "combine.cuh"
@@ -22,7 +23,9 @@ struct JoinedParams : DecodeParams {
   const int32_t* prefix_table;  // [prefix_blocks]
   const int32_t* prefix_len;    // one int32 on the device
   int32_t prefix_blocks;
+  int32_t whole_sequences;      // block g takes sequence g: no partials, no merge
 };
+__device__ __forceinline__ bool by_sequence(const JoinedParams& p) { return p.whole_sequences; }
 
 // (Read past L1: asked before the previous kernel is done, too.)
 __device__ __forceinline__ int joined_prefix(const JoinedParams& p, bool report_it) {

@@ -5,7 +5,7 @@
 //
 // The softmax over the union is regrouped exactly from partial results (O, m,
 // sum) as in combine.cuh.  Three kernels (short prefixes and small batches take
-// joined.cuh's two):
+// joined.cuh's way):
 //   * the prefix as a multi-query attention whose queries are the batch's
 //     sequences (prefill_pair.cuh with PrefixParams): its pages are read once
 //     for 16 sequences x 16 heads instead of once per sequence, and the

@@ -46,6 +46,13 @@ int32_t launched(const char* name, cudaError_t e) {
   return ATTN_OK;
 }
 
+// Pages that a sequence of up to max_len positions shows, at most.
+int64_t visible_pages_bound(int32_t max_len, int32_t window) {
+  const int64_t pages = (static_cast<int64_t>(max_len) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE;
+  if (window <= 0) return pages;
+  return std::min<int64_t>(pages, (static_cast<int64_t>(window) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE + 1);
+}
+
 // ---------------------------------------------------------------------------
 // Launch plan of the 8-bit decode and of the own positions behind a prefix:
 // make_plan's, but for the smallest spans.  A sequence that a block starts costs
@@ -62,8 +69,7 @@ int32_t make_serving_plan(int32_t kind, int32_t batch, int32_t max_seq_len, int3
   const int32_t st = make_plan(kind, batch, max_seq_len, window, forced_blocks, num_sms, out);
   if (st != ATTN_OK) return st;
   const bool sliding = kind == ATTN_KIND_SLIDING;
-  int64_t pages = (max_seq_len + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE;
-  if (window > 0) pages = std::min<int64_t>(pages, (static_cast<int64_t>(window) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE + 1);
+  const int64_t pages = visible_pages_bound(max_seq_len, window);
   constexpr int kPartials = 32;  // per sequence, before spans grow
   out->min_pages = static_cast<int>(std::min<int64_t>(4, std::max<int64_t>(2, (pages + kPartials - 1) / kPartials)));
   if (forced_blocks == 0) {
@@ -76,6 +82,45 @@ int32_t make_serving_plan(int32_t kind, int32_t batch, int32_t max_seq_len, int3
   const size_t rows = (static_cast<size_t>(out->grid_x) + batch) * (sliding ? ATTN_SLIDING_HQ : ATTN_GLOBAL_HQ);
   out->part_o_bytes = align256(rows * d * sizeof(float));
   out->workspace_bytes = ATTN_WORKSPACE_ZERO_BYTES + out->part_o_bytes + align256(rows * sizeof(float2));
+  return ATTN_OK;
+}
+
+// Visible pages up to which every sequence gets a block of its own (per KV
+// head): no partials and no merge kernel, but a sequence's pages one after
+// another.  One call in us, in balanced spans and by sequence:
+//   8-bit, global: 1 sequence of 64 positions 7.4 and 6.8, of 128 8.6 and 9.6; 4 of
+//     16 7.3 and 5.0, of 128 10.2 and 9.7, of 256 9.9 and 15.4; 64 of 256 16.6 and
+//     16.2, of 512 18.8 and 27.1; 128 of 128 21.9 and 11.0, of 512 32.3 and 27.5; 256
+//     of 16 19.2 and 10.3, of 512 58.2 and 36.0;
+//   8-bit, sliding: 1 of 128 6.6 and 6.0; 4 of 256 8.2 and 9.6; 32 of 128 13.1 and 8.2;
+//     64 of 64 13.7 and 12.3, of 128 15.5 and 15.9; 128 of 32 14.3 and 19.7 (the
+//     blocks of 57 sequences are resident at once);
+//   bf16 behind a prefix, both in one list: 1 of 32 positions 6.3 and 4.8, of 80 8.1
+//     and 10.4; 4 of 56 8.4 and 7.7, of 128 7.9 and 9.8; 16 of 128 12.0 and 10.9; 32 of
+//     120 16.8 and 12.2.
+// Uneven lengths favour the spans, so long sequences take them unless the batch
+// has eight for every page of the longest.
+enum class Serving { kSlidingFp8, kGlobalFp8, kJoined };
+
+int64_t whole_pages(Serving call, int32_t batch) {
+  switch (call) {
+    case Serving::kSlidingFp8: return batch <= 57 ? 8 : 0;
+    case Serving::kGlobalFp8: return batch >= 64 ? std::max(16, batch / 8) : batch >= 4 ? 8 : 4;
+    default: return batch >= 16 ? 8 : 4;
+  }
+}
+
+// make_serving_plan's, or a block per sequence (its workspace is not used then).
+int32_t make_whole_plan(Serving call, int32_t batch, int32_t max_seq_len, int32_t window, int32_t forced_blocks,
+                        int32_t num_sms, Plan* out, bool* whole) {
+  const int32_t kind = call == Serving::kSlidingFp8 ? ATTN_KIND_SLIDING : ATTN_KIND_GLOBAL;
+  const int32_t st = make_serving_plan(kind, batch, max_seq_len, window, forced_blocks, num_sms, out);
+  if (st != ATTN_OK) return st;
+  *whole = forced_blocks == 0 && visible_pages_bound(max_seq_len, window) <= whole_pages(call, batch);
+  if (*whole) {
+    out->grid_x = batch;
+    out->merge_in_grid = true;  // (nothing to merge)
+  }
   return ATTN_OK;
 }
 
@@ -193,9 +238,7 @@ int32_t run_read(int32_t kind, const void* k_pool, const void* v_pool, const uin
   p.out_table = out_table;
   p.out_pages = out_pages;
   // no more blocks than the (weighted) pages that max_seq_len allows
-  int64_t pages = (max_seq_len + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE;
-  if (span > 0) pages = std::min<int64_t>(pages, (static_cast<int64_t>(span) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE + 1);
-  const int64_t want = (pages + pda::DecodeParams::kSeqWeight) * batch;
+  const int64_t want = (visible_pages_bound(max_seq_len, span) + pda::DecodeParams::kSeqWeight) * batch;
   p.d.grid_x = static_cast<int32_t>(
       std::max<int64_t>(1, std::min<int64_t>(want, num_sms * pda::fp8_read::kGridPerSm)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -306,7 +349,9 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
   int dev = 0, num_sms = 0;
   if ((st = current_device(&dev, &num_sms)) != ATTN_OK) return st;
   Plan plan;
-  st = make_serving_plan(kind, batch, max_seq_len, window, num_splits, num_sms, &plan);
+  bool whole = false;
+  st = make_whole_plan(sliding ? Serving::kSlidingFp8 : Serving::kGlobalFp8, batch, max_seq_len, window, num_splits,
+                       num_sms, &plan, &whole);
   if (st != ATTN_OK) return st;
   if (!workspace || workspace_bytes < plan.workspace_bytes)
     return fail(ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)", name, plan.workspace_bytes,
@@ -315,7 +360,7 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
   g_last_launches = plan.merge_in_grid ? 1 : 2;
   if (g_validate_only) return ATTN_OK;
 
-  pda::Fp8DecodeParams p{};
+  pda::Fp8WholeParams p{};  // (sliced to its base for the kernels in spans)
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);  // bytes; addressed as such by the kernels
   p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
@@ -347,32 +392,45 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
     return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
+  const pda::Fp8DecodeParams& cut = p;
   if (sliding) {
-    static bool smem_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false};
-    if ((st = ensure_smem(pda::sliding_fp8::decode_kernel, pda::sliding_fp8::kSmemBytes, dev, smem_set)) ||
-        (st = ensure_smem(pda::combine_kernel<ATTN_SLIDING_D, pda::Fp8DecodeParams>, 0, dev, comb_set)))
+    namespace sl = pda::sliding_fp8;
+    const auto decode = sl::decode_kernel<pda::Fp8DecodeParams>;
+    const auto decode_whole = sl::decode_kernel<pda::Fp8WholeParams>;
+    const auto combine = pda::combine_kernel<ATTN_SLIDING_D, pda::Fp8DecodeParams>;
+    static bool smem_set[kMaxDevices] = {false}, whole_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false};
+    if ((st = ensure_smem(decode, sl::kSmemBytes, dev, smem_set)) ||
+        (st = ensure_smem(decode_whole, sl::kSmemBytes, dev, whole_set)) ||
+        (st = ensure_smem(combine, 0, dev, comb_set)))
       return st;
-    e = launch_pdl(pda::sliding_fp8::decode_kernel, dim3(ATTN_SLIDING_HKV, plan.grid_x), pda::sliding_fp8::kThreads,
-                   pda::sliding_fp8::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
+    const dim3 grid(ATTN_SLIDING_HKV, plan.grid_x);
+    e = whole ? launch_pdl(decode_whole, grid, sl::kThreads, sl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p)
+              : launch_pdl(decode, grid, sl::kThreads, sl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, cut);
     if (e == cudaSuccess && !plan.merge_in_grid)
-      e = launch_pdl(pda::combine_kernel<ATTN_SLIDING_D, pda::Fp8DecodeParams>,
-                     dim3(ATTN_SLIDING_HQ * (ATTN_SLIDING_D / pda::kCombineCols), batch), pda::kCombineWarps * 32, 0,
-                     s, p);
+      e = launch_pdl(combine, dim3(ATTN_SLIDING_HQ * (ATTN_SLIDING_D / pda::kCombineCols), batch),
+                     pda::kCombineWarps * 32, 0, s, cut);
   } else {
+    namespace gl = pda::global_fp8;
+    const auto decode = gl::decode_kernel<pda::Fp8DecodeParams>;
+    const auto decode_whole = gl::decode_kernel<pda::Fp8WholeParams>;
     // Many rows: one merge block per row (64 sequences of 500: 22.5 us a call,
     // against 29.4 with launch_merge's four).
     const bool few_rows = batch * ATTN_GLOBAL_HQ <= 2 * num_sms;
     const auto row_kernel = pda::prefix::merge_kernel<ATTN_GLOBAL_D, 0, 1, ATTN_GLOBAL_D, 2, pda::Fp8DecodeParams>;
-    static bool smem_set[kMaxDevices] = {false}, row_set[kMaxDevices] = {false};
-    if ((st = ensure_smem(pda::global_fp8::decode_kernel, pda::global_fp8::kSmemBytes, dev, smem_set)) ||
+    static bool smem_set[kMaxDevices] = {false}, whole_set[kMaxDevices] = {false}, row_set[kMaxDevices] = {false};
+    if ((st = ensure_smem(decode, gl::kSmemBytes, dev, smem_set)) ||
+        (st = ensure_smem(decode_whole, gl::kSmemBytes, dev, whole_set)) ||
         (st = ensure_smem(row_kernel, 0, dev, row_set)) || (st = ensure_merge<pda::Fp8DecodeParams>(dev)))
       return st;
-    pda::prefix::MergeParams<pda::Fp8DecodeParams> mp{};
-    mp.d = p;
-    e = launch_pdl(pda::global_fp8::decode_kernel, dim3(plan.grid_x), pda::global_fp8::kThreads,
-                   pda::global_fp8::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
-    if (e == cudaSuccess)
-      e = few_rows ? launch_merge(p, s) : launch_pdl(row_kernel, dim3(ATTN_GLOBAL_HQ, batch), 256, 0, s, mp);
+    if (whole) {
+      e = launch_pdl(decode_whole, dim3(plan.grid_x), gl::kThreads, gl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
+    } else {
+      pda::prefix::MergeParams<pda::Fp8DecodeParams> mp{};
+      mp.d = cut;
+      e = launch_pdl(decode, dim3(plan.grid_x), gl::kThreads, gl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, cut);
+      if (e == cudaSuccess)
+        e = few_rows ? launch_merge(cut, s) : launch_pdl(row_kernel, dim3(ATTN_GLOBAL_HQ, batch), 256, 0, s, mp);
+    }
   }
   return launched(name, e);
 }
@@ -398,6 +456,7 @@ constexpr int kPrefixMinSteps = 2;  // steps of 64 keys a span is given at least
 
 struct PrefixPlan {
   bool joined;        // prefix and own pages as one list per sequence (joined.cuh): two kernels
+  bool whole;         // joined, a block per sequence: one kernel
   Plan own;           // the decode over the own positions, or over the joined list
   int splits;         // spans of the prefix; 0 when joined
   size_t part_o_off, part_ml_off, workspace_bytes;
@@ -411,8 +470,11 @@ int32_t make_prefix_plan(int32_t batch, int32_t max_prefix_len, int32_t max_seq_
   out->joined = prefix_splits == 0 && join_prefix(batch, max_prefix_len);
   const int64_t joined_len =
       (static_cast<int64_t>(max_prefix_len) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE * ATTN_PAGE_SIZE + max_seq_len;
-  const int32_t len = out->joined ? static_cast<int32_t>(std::min<int64_t>(joined_len, INT32_MAX)) : max_seq_len;
-  const int32_t st = make_serving_plan(ATTN_KIND_GLOBAL, batch, len, 0, num_splits, num_sms, &out->own);
+  const int32_t len = static_cast<int32_t>(std::min<int64_t>(joined_len, INT32_MAX));
+  out->whole = false;
+  const int32_t st =
+      out->joined ? make_whole_plan(Serving::kJoined, batch, len, 0, num_splits, num_sms, &out->own, &out->whole)
+                  : make_serving_plan(ATTN_KIND_GLOBAL, batch, max_seq_len, 0, num_splits, num_sms, &out->own);
   if (st != ATTN_OK) return st;
   out->splits = 0;
   out->part_o_off = out->part_ml_off = 0;
@@ -472,7 +534,7 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
     return fail(ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)", name, plan.workspace_bytes,
                 workspace ? workspace_bytes : size_t{0});
   if (!aligned16(workspace)) return fail(ATTN_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", name);
-  g_last_launches = plan.joined ? 2 : 3;
+  g_last_launches = plan.whole ? 1 : plan.joined ? 2 : 3;
   if (g_validate_only) return ATTN_OK;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -498,6 +560,7 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
   jp.prefix_table = prefix_table;
   jp.prefix_len = prefix_len;
   jp.prefix_blocks = prefix_blocks;
+  jp.whole_sequences = plan.whole;
   CUtensorMap tm_k, tm_v;
   if ((st = encode_global_page_map(&tm_k, k_pool, num_pages)) || (st = encode_global_page_map(&tm_v, v_pool, num_pages)))
     return st;
@@ -509,7 +572,7 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
       return st;
     cudaError_t e = launch_pdl(decode, dim3(plan.own.grid_x), pda::global::kThreads, pda::global::kSmemBytes, s, tm_k,
                                tm_v, jp);
-    if (e == cudaSuccess) e = launch_merge(jp, s);
+    if (e == cudaSuccess && !plan.whole) e = launch_merge(jp, s);
     return launched(name, e);
   }
   pda::prefill_pair::PrefixParams pp{};
@@ -581,7 +644,11 @@ int32_t attn_decode_fp8_plan(int32_t kind, int32_t batch, int32_t max_seq_len, i
                              size_t* out_workspace_bytes) {
   g_err[0] = '\0';
   Plan plan;
-  const int32_t st = make_serving_plan(kind, batch, max_seq_len, window, num_splits, num_sms, &plan);
+  bool whole = false;
+  int32_t st = make_serving_plan(kind, batch, max_seq_len, window, num_splits, num_sms, &plan);  // (refuses a bad kind)
+  if (st != ATTN_OK) return st;
+  st = make_whole_plan(kind == ATTN_KIND_SLIDING ? Serving::kSlidingFp8 : Serving::kGlobalFp8, batch, max_seq_len,
+                       window, num_splits, num_sms, &plan, &whole);
   if (st != ATTN_OK) return st;
   if (out_num_splits) *out_num_splits = plan.grid_x;
   if (out_launches) *out_launches = plan.merge_in_grid ? 1 : 2;

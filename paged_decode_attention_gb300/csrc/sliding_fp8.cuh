@@ -69,10 +69,11 @@ static_assert(kConsumerWarps == 2 * kChunks, "a (chunk, j) of q per warp");
 static_assert(kStages % kConsumerWarps == 0, "a stage belongs to one warp, which sees each of its phases");
 static_assert(kBlocksPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of the resident blocks");
 
+template <typename Params>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
-                  const __grid_constant__ Fp8DecodeParams p) {
+                  const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   Smem& s = fp8::aligned_smem<Smem>(smem_raw);
 

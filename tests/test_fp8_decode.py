@@ -83,6 +83,25 @@ def test_forced_splits(cuda_lib, kind, num_splits):
     check(kind, c.on(DEV), window_of(kind), num_splits=num_splits)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens", [[1], [64], [0, 0, 33], [16, 17, 0, 128, 1, 100], [5] * 57])
+@pytest.mark.parametrize("kind", KINDS)
+def test_short_sequences_whole(cuda_lib, kind, lens, out_dtype):
+    c = Fp8Case(make_case(kind, lens, seed=50, window=window_of(kind)))
+    assert pda.attn_decode_fp8_plan(pda.KIND_GLOBAL if kind == "global" else pda.KIND_SLIDING, len(lens), max(lens),
+                                    window_of(kind))[:2] == (len(lens), 1)
+    for bound in (max(lens), 1):  # (the bound sizes the launch only)
+        o = check(kind, c.on(DEV), window_of(kind), out_dtype=out_dtype, max_seq_len=bound)
+        for b, n in enumerate(lens):
+            assert n or (o[b] == 0).all()
+
+
+def test_a_large_batch_whole(cuda_lib):
+    lens = torch.randint(0, 300, (200,), generator=torch.Generator().manual_seed(51)).tolist()
+    c = Fp8Case(make_case("global", lens, seed=51, window=0))
+    check("global", c.on(DEV), 0, max_seq_len=300)
+
+
 @pytest.mark.parametrize("lens", [[20000], [0, 17000], [1, 6001], [9000, 0, 5]])
 @pytest.mark.parametrize("num_splits", [0, 500])
 def test_long_sequences_in_many_partials(cuda_lib, lens, num_splits):

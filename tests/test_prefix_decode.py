@@ -84,6 +84,13 @@ def test_a_long_prefix(cuda_lib, out_dtype):
     check(Case(9001, [0, 5, 1500, 33, 16, 1, 0, 700, 80], seed=64), out_dtype=out_dtype)
 
 
+@pytest.mark.parametrize("num_splits", [0, 2])
+@pytest.mark.parametrize("prefix,lens", [(0, [0, 3]), (1, [0, 0]), (17, [0, 30, 1]), (16, [48]),
+                                         (50, [r % 60 for r in range(20)])])
+def test_short_lists_whole_and_cut(cuda_lib, prefix, lens, num_splits):
+    check(Case(prefix, lens, seed=78), num_splits=num_splits)
+
+
 @BOTH
 @pytest.mark.parametrize("prefix,lens", [(20001, [0]), (9000, [700]), (15, [16000]), (8192, [0, 33])])
 def test_one_or_two_sequences_in_many_partials(cuda_lib, prefix, lens, splits):

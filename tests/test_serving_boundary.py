@@ -124,6 +124,14 @@ def test_fp8_plan(lib):
     assert pda.attn_decode_fp8_plan(G, 1, 0, 0)[0] == 1
     assert pda.attn_decode_fp8_plan(G, 2, 100, 0, num_splits=7)[0] == 7
     assert pda.attn_decode_fp8_plan(G, 2, 100, 0, num_splits=5000)[0] == 1024
+    # short sequences whole, a block each, no merge
+    for kind, n, longest in ((G, 1, 64), (G, 4, 128), (G, 64, 256), (G, 256, 512), (S, 57, 128)):
+        window = 1024 if kind == S else 0
+        assert pda.attn_decode_fp8_plan(kind, n, longest, window)[:2] == (n, 1)
+        assert pda.attn_decode_fp8_plan(kind, n, longest, window, num_splits=7)[0] == 7
+    assert pda.attn_decode_fp8_plan(G, 1, 65, 0)[:2] == (3, 2)
+    assert pda.attn_decode_fp8_plan(G, 256, 513, 0)[:2] == (304, 2)
+    assert pda.attn_decode_fp8_plan(S, 58, 16, 1024)[0] == 57
     for bad in ((7, 1, 16, 0), (G, 0, 16, 0), (G, 1, -1, 0), (G, 1, 16, 0, -1), (G, 1, 16, 0, 0, 0)):
         with pytest.raises(pda.AttnDecodeError):
             pda.attn_decode_fp8_plan(*bad)
@@ -136,7 +144,7 @@ def test_prefix_plan(lib):
     rows = ps * 64 * 16
     assert (ns, ps) == (own, 9) and ws == own_ws + rows * 512 * 4 + rows * 2 * 8
     # short prefixes, small batches: one list of pages per sequence, no spans
-    for B, n in ((16, 1887), (8, 8450), (1, 262144), (2, 131072), (43, 2), (4, 0)):
+    for B, n in ((16, 1887), (8, 8450), (1, 262144), (2, 131072), (43, 2), (16, 0)):
         gx, ps, ws = pda.attn_decode_prefix_plan(B, n, 100)
         assert (gx, ps, ws) == (pda.attn_decode_fp8_plan(pda.KIND_GLOBAL, B, -(-n // 16) * 16 + 100, 0)[0], 0,
                                 pda.attn_decode_fp8_plan(pda.KIND_GLOBAL, B, -(-n // 16) * 16 + 100, 0)[2])
