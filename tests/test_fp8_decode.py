@@ -326,15 +326,16 @@ def test_read_back_prepared_and_in_a_step(cuda_lib, kind):
     step.close()
 
 
+@pytest.mark.parametrize("bound", [1300, 40])  # (sizes the launch only: 40 gives every sequence a block)
 @pytest.mark.parametrize("kind", KINDS)
-def test_streams_graphs_and_steps(cuda_lib, kind):
+def test_streams_graphs_and_steps(cuda_lib, kind, bound):
     # the same workspace by two captured graphs and a step in turn, contents changing between replays
     lens = [5, 700, 1300, 64]
     cases = [Fp8Case(make_case(kind, lens, seed=46 + i, layout_seed=46)) for i in range(3)]
     args = list(cases[0].on(DEV))
     w = window_of(kind)
-    ws = pda.new_workspace(pda.attn_decode_fp8_workspace_size(getattr(pda, "KIND_" + kind.upper()), 4, 1300, w), DEV)
-    kw = dict(window=w, max_seq_len=1300, workspace=ws, out_dtype=torch.float32)
+    ws = pda.new_workspace(pda.attn_decode_fp8_workspace_size(getattr(pda, "KIND_" + kind.upper()), 4, bound, w), DEV)
+    kw = dict(window=w, max_seq_len=bound, workspace=ws, out_dtype=torch.float32)
     fn = getattr(pda, "attn_decode_%s_fp8" % kind)
     side = torch.cuda.Stream()
     graphs, outs = [], []
@@ -356,7 +357,7 @@ def test_streams_graphs_and_steps(cuda_lib, kind):
             else:
                 x.copy_(y)
         torch.cuda.synchronize()
-        want, _ = decode(kind, new, w, max_seq_len=1300)
+        want, _ = decode(kind, new, w, max_seq_len=bound)
         for g in graphs:
             g.replay()
         step.launch()

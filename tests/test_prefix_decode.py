@@ -193,11 +193,14 @@ def test_a_visible_nan_shows(cuda_lib, prefix_splits):
     assert torch.isnan(o[1]).all() and torch.equal(o[0], clean[0])
 
 
-def test_streams_graphs_and_steps(cuda_lib):
+# (the bounds size the launches only: with the last ones every sequence has a block)
+@pytest.mark.parametrize("kernels,max_prefix,max_seq,splits", [(3, 1008, 704, 2), (2, 1008, 704, 0), (1, 16, 16, 0)])
+def test_streams_graphs_and_steps(cuda_lib, kernels, max_prefix, max_seq, splits):
     # two captured graphs and a step share one workspace in turn; lengths and contents change between replays
     args = Case(1000, [5, 700, 0, 33], seed=74).args()
-    ws = pda.new_workspace(pda.attn_decode_prefix_workspace_size(4, 1008, 704), DEV)
-    kw = dict(max_prefix_len=1008, max_seq_len=704, workspace=ws, out_dtype=torch.float32)
+    ws = pda.new_workspace(pda.attn_decode_prefix_workspace_size(4, max_prefix, max_seq, 0, splits), DEV)
+    bounds = dict(max_prefix_len=max_prefix, max_seq_len=max_seq, prefix_splits=splits)
+    kw = dict(bounds, workspace=ws, out_dtype=torch.float32)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     graphs, outs = [], []
@@ -208,7 +211,7 @@ def test_streams_graphs_and_steps(cuda_lib):
         graphs.append(g)
     step = pda.Step()
     outs.append(step.add_decode_global_prefix(*args, **kw))
-    assert step.num_kernels == 2  # 4 x 1008 positions: one list per sequence
+    assert step.num_kernels == kernels
     step.finalize("graph")
     call = pda.prepare_decode_global_prefix(*args, **kw)
     for prefix, lens in ((1000, [5, 700, 0, 33]), (17, [0, 16, 0, 20]), (640, [3, 600, 0, 33])):
@@ -217,7 +220,7 @@ def test_streams_graphs_and_steps(cuda_lib):
         args[0].mul_(0.5)
         # (no length above goes beyond the first ones, whose pages are mapped)
         torch.cuda.synchronize()
-        want, st = decode(args, max_prefix_len=1008, max_seq_len=704)
+        want, st = decode(args, **bounds)
         assert st == 0 and torch.isfinite(want).all()
         for g in graphs:
             g.replay()
