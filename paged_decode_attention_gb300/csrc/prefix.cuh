@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kMergeGroups* kDims / 4) merge_kernel(const __
   // partial i: prefix span i, or block g0 + i - used of the own positions
   const size_t rows = static_cast<size_t>(p.batch) * Hq;
   const float* pre_o = mp.part_o + row * kD + d0;
-  const float2* pre_ml = mp.part_ml + (kPrefixSlices > 0 ? d0 / (kD / (kPrefixSlices > 0 ? kPrefixSlices : 1)) * rows + row : 0);
+  const int slice = d0 * kPrefixSlices / kD;
+  const float2* pre_ml = mp.part_ml + slice * rows + row;  // (not read without a prefix)
   const float* own_o = p.part_o + ((static_cast<size_t>(g0) + b) * Hq + h) * kD + d0;
   const float2* own_ml = p.part_ml + (static_cast<size_t>(g0) + b) * Hq + h;
 

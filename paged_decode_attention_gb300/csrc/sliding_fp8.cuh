@@ -13,13 +13,12 @@
 //
 // The balanced spans as in sliding.cuh, grid (8, grid_x): the eight heads of a
 // span run at the same time, so that a row is read whole (256 windows 182 us,
-// 184.5 with the spans along x).  Warp 4 copies
-// pages; each of the warps 0..3 takes every fourth page whole and keeps its
-// own running max, sum and output, so no barrier is met between a segment's
-// first page and its end, where the four are merged two by two through shared
-// memory.  256 windows of 1024: 182 us, 0.875 of the measured copy rate; the page
-// copies alone, with nothing computed, take 171 to 174 us (a head's share of a
-// row is 256 bytes, a page 16 such pieces).
+// 184.5 with the spans along x).  Warp 4 copies pages; each of the warps 0..3
+// takes every fourth page whole and keeps its own running max, sum and output,
+// so no barrier is met between a segment's first page and its end, where the
+// four are merged two by two through shared memory.  256 windows of 1024: 182 us,
+// 0.875 of the measured copy rate; the page copies alone, with nothing computed,
+// take 171 to 174 us (a head's share of a row is 256 bytes, a page 16 such pieces).
 //
 // S^T[pos, h] = K q^T, then O^T[d, h] = V^T P^T: the weights of a lane's two
 // positions, packed, become B fragments by one transposition in registers
