@@ -798,9 +798,10 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // The same, with every segment left as a partial.
+template <typename Params>
 __global__ void __launch_bounds__(kThreads)
     decode_kernel_partial(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                          const __grid_constant__ DecodeParams p) {
+                          const __grid_constant__ Params p) {
   decode_body<false, true>(&tm_k, &tm_v, p, nullptr);
 }
 

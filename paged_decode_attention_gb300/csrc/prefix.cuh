@@ -23,8 +23,8 @@
 // ahead of it.  With a prefix one block takes a row, in four groups where the
 // rows' blocks are resident at once (16 sequences, 16384 positions: a call takes
 // 35.4 us; with four blocks of four groups 39.5), in two where they come in
-// waves (64 sequences, 15 partials: 127.5 us, with four groups 131.4; 120.6 since
-// the own positions' kernel no longer waits for the prefix kernel).
+// waves (64 sequences, 15 partials: 127.5 us, with four groups 131.4; 119 since the
+// own positions' kernel no longer waits for the prefix kernel).
 #pragma once
 
 #include "combine.cuh"
@@ -32,6 +32,12 @@
 
 namespace pda {
 namespace prefix {
+
+// The own positions' call.  Weight of a sequence's start 1 and 4, us: 32 sequences
+// of up to 2000 behind 16384 56.2 and 53.8, 64 of up to 1000 behind 500 36.8 and 35.1.
+struct OwnParams : DecodeParams {
+  static constexpr int kSeqWeight = 4;
+};
 
 template <typename Params>
 struct MergeParams {

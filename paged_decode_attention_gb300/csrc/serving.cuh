@@ -589,8 +589,10 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
   pp.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml_off);
   pp.splits = plan.splits;
 
-  pda::prefix::MergeParams<pda::DecodeParams> mp{};
-  mp.d = p;
+  pda::prefix::OwnParams own{};
+  static_cast<pda::DecodeParams&>(own) = p;
+  pda::prefix::MergeParams<pda::prefix::OwnParams> mp{};
+  mp.d = own;
   mp.part_o = pp.part_o;
   mp.part_ml = pp.part_ml;
   mp.prefix_len = prefix_len;
@@ -601,11 +603,12 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
   const auto prefix_kernel = pda::prefill_pair::prefill_pair_kernel<C, pda::prefill_pair::PrefixParams>;
   const bool few_rows = batch * ATTN_GLOBAL_HQ <= 2 * num_sms;  // the merge's blocks are resident at once
   const auto merge_kernel =
-      few_rows ? pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, ATTN_GLOBAL_D, 4, pda::DecodeParams>
-               : pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, ATTN_GLOBAL_D, 2, pda::DecodeParams>;
+      few_rows ? pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, ATTN_GLOBAL_D, 4, pda::prefix::OwnParams>
+               : pda::prefix::merge_kernel<ATTN_GLOBAL_D, C::kSlices, C::kPPS, ATTN_GLOBAL_D, 2, pda::prefix::OwnParams>;
+  const auto own_kernel = pda::global::decode_kernel_partial<pda::prefix::OwnParams>;
   static bool pre_set[kMaxDevices] = {false}, dec_set[kMaxDevices] = {false}, merge_set[2][kMaxDevices] = {{false}};
   if ((st = ensure_smem(prefix_kernel, C::kSmemBytes, dev, pre_set)) ||
-      (st = ensure_smem(pda::global::decode_kernel_partial, pda::global::kSmemBytes, dev, dec_set)) ||
+      (st = ensure_smem(own_kernel, pda::global::kSmemBytes, dev, dec_set)) ||
       (st = ensure_smem(merge_kernel, 0, dev, merge_set[few_rows])))
     return st;
   CUtensorMap tm_pk, tm_pv;
@@ -617,8 +620,8 @@ int32_t run_prefix(const void* q, const void* k_pool, const void* v_pool, const 
   cudaError_t e = launch_pdl(prefix_kernel, dim3(tiles, C::kHkv * C::kSlices, plan.splits), C::kThreads, C::kSmemBytes, s,
                              tm_pk, tm_pv, pp);
   if (e == cudaSuccess)
-    e = launch_pdl(pda::global::decode_kernel_partial, dim3(plan.own.grid_x), pda::global::kThreads,
-                   pda::global::kSmemBytes, s, tm_k, tm_v, p);
+    e = launch_pdl(own_kernel, dim3(plan.own.grid_x), pda::global::kThreads,
+                   pda::global::kSmemBytes, s, tm_k, tm_v, own);
   if (e == cudaSuccess)
     e = launch_pdl(merge_kernel, dim3(ATTN_GLOBAL_HQ, batch), few_rows ? 512 : 256, 0, s, mp);
   return launched(name, e);
