@@ -29,17 +29,22 @@ namespace pda {
 
 // The decode calls over this cache: a sequence's start (scaling q, the first
 // pages' latency, closing the segment) costs a block as much as a few pages.
-// Weight 1 and 4, us: global layers, 8 sequences of 4700 19.0 and 17.2, 16 of
-// 5000 27.8 and 25.8, 32 of 1000 18.1 and 16.5; sliding layers, 64 of 300 26.5
-// and 23.0, 16 of 5000 21.8 and 21.1, 256 of 200 56.0 and 57.7.
-struct Fp8DecodeParams : DecodeParams {
+// Global layers, weight 1 and 4, us: 8 sequences of 4700 19.0 and 17.2, 16 of 5000
+// 27.8 and 25.8, 32 of 1000 18.1 and 16.5.  Sliding layers, 4 and 12 (their pages
+// are half as long and four warps take them side by side): 8 of 1000 15.3 and
+// 13.0, 16 of 5000 21.5 and 18.6, 32 of 200 15.2 and 12.0, 4 of 800 8.8 and 9.3, 256
+// of 500 101.5 and 102.8.
+struct Fp8GlobalParams : DecodeParams {
   static constexpr int kSeqWeight = 4;
+};
+struct Fp8SlidingParams : DecodeParams {
+  static constexpr int kSeqWeight = 12;
 };
 
 // Block g takes sequence g: no partials, no merge.  (A type of its own: as a
 // field it cost the kernel in spans registers, 347 us instead of 340 for 16
 // global sequences of 131072.)
-struct Fp8WholeParams : Fp8DecodeParams {};
+struct Fp8WholeParams : DecodeParams {};
 __device__ __forceinline__ bool by_sequence(const Fp8WholeParams&) { return true; }
 
 namespace fp8 {

@@ -360,7 +360,8 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
   g_last_launches = plan.merge_in_grid ? 1 : 2;
   if (g_validate_only) return ATTN_OK;
 
-  pda::Fp8WholeParams p{};  // (sliced to its base for the kernels in spans)
+  pda::Fp8WholeParams all{};
+  pda::DecodeParams& p = all;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);  // bytes; addressed as such by the kernels
   p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
@@ -392,40 +393,43 @@ int32_t run_decode_fp8(int32_t kind, const void* q, const void* k_pool, const vo
     return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  const pda::Fp8DecodeParams& cut = p;
   if (sliding) {
+    pda::Fp8SlidingParams cut{};
+    static_cast<pda::DecodeParams&>(cut) = p;
     namespace sl = pda::sliding_fp8;
-    const auto decode = sl::decode_kernel<pda::Fp8DecodeParams>;
+    const auto decode = sl::decode_kernel<pda::Fp8SlidingParams>;
     const auto decode_whole = sl::decode_kernel<pda::Fp8WholeParams>;
-    const auto combine = pda::combine_kernel<ATTN_SLIDING_D, pda::Fp8DecodeParams>;
+    const auto combine = pda::combine_kernel<ATTN_SLIDING_D, pda::Fp8SlidingParams>;
     static bool smem_set[kMaxDevices] = {false}, whole_set[kMaxDevices] = {false}, comb_set[kMaxDevices] = {false};
     if ((st = ensure_smem(decode, sl::kSmemBytes, dev, smem_set)) ||
         (st = ensure_smem(decode_whole, sl::kSmemBytes, dev, whole_set)) ||
         (st = ensure_smem(combine, 0, dev, comb_set)))
       return st;
     const dim3 grid(ATTN_SLIDING_HKV, plan.grid_x);
-    e = whole ? launch_pdl(decode_whole, grid, sl::kThreads, sl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p)
+    e = whole ? launch_pdl(decode_whole, grid, sl::kThreads, sl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, all)
               : launch_pdl(decode, grid, sl::kThreads, sl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, cut);
     if (e == cudaSuccess && !plan.merge_in_grid)
       e = launch_pdl(combine, dim3(ATTN_SLIDING_HQ * (ATTN_SLIDING_D / pda::kCombineCols), batch),
                      pda::kCombineWarps * 32, 0, s, cut);
   } else {
+    pda::Fp8GlobalParams cut{};
+    static_cast<pda::DecodeParams&>(cut) = p;
     namespace gl = pda::global_fp8;
-    const auto decode = gl::decode_kernel<pda::Fp8DecodeParams>;
+    const auto decode = gl::decode_kernel<pda::Fp8GlobalParams>;
     const auto decode_whole = gl::decode_kernel<pda::Fp8WholeParams>;
     // Many rows: one merge block per row (64 sequences of 500: 22.5 us a call,
     // against 29.4 with launch_merge's four).
     const bool few_rows = batch * ATTN_GLOBAL_HQ <= 2 * num_sms;
-    const auto row_kernel = pda::prefix::merge_kernel<ATTN_GLOBAL_D, 0, 1, ATTN_GLOBAL_D, 2, pda::Fp8DecodeParams>;
+    const auto row_kernel = pda::prefix::merge_kernel<ATTN_GLOBAL_D, 0, 1, ATTN_GLOBAL_D, 2, pda::Fp8GlobalParams>;
     static bool smem_set[kMaxDevices] = {false}, whole_set[kMaxDevices] = {false}, row_set[kMaxDevices] = {false};
     if ((st = ensure_smem(decode, gl::kSmemBytes, dev, smem_set)) ||
         (st = ensure_smem(decode_whole, gl::kSmemBytes, dev, whole_set)) ||
-        (st = ensure_smem(row_kernel, 0, dev, row_set)) || (st = ensure_merge<pda::Fp8DecodeParams>(dev)))
+        (st = ensure_smem(row_kernel, 0, dev, row_set)) || (st = ensure_merge<pda::Fp8GlobalParams>(dev)))
       return st;
     if (whole) {
-      e = launch_pdl(decode_whole, dim3(plan.grid_x), gl::kThreads, gl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, p);
+      e = launch_pdl(decode_whole, dim3(plan.grid_x), gl::kThreads, gl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, all);
     } else {
-      pda::prefix::MergeParams<pda::Fp8DecodeParams> mp{};
+      pda::prefix::MergeParams<pda::Fp8GlobalParams> mp{};
       mp.d = cut;
       e = launch_pdl(decode, dim3(plan.grid_x), gl::kThreads, gl::kSmemBytes, s, tm_k, tm_v, tm_ks, tm_vs, cut);
       if (e == cudaSuccess)
