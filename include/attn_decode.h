@@ -396,10 +396,12 @@ int32_t attn_kv_append_global(const void* qkv, const void* w_q, const void* w_k,
  * k_pool, v_pool  the decode's pools; attn_kv_append_global_chunk: k_pool may
  *              be NULL for a values-only cache
  * status       a sequence with more new tokens than seq_lens[b], a length
- *              beyond the table, rows past total_q or a decreasing cu_q raises
- *              ATTN_DEV_BAD_SEQ_LEN and nothing of it is written; a page id
- *              outside [0, num_pages) raises ATTN_DEV_BAD_PAGE and that token's
- *              cache row is not written (its q is)
+ *              beyond the table or rows past total_q raises
+ *              ATTN_DEV_BAD_SEQ_LEN and nothing of it is written; a cu_q that
+ *              decreases anywhere raises it too and nothing of the call is
+ *              written; a page id outside [0, num_pages) raises
+ *              ATTN_DEV_BAD_PAGE and that token's cache row is not written
+ *              (its q is)
  *
  * Two tokens of one call must not share a cache slot.  total_q 0 launches
  * nothing.  Arithmetic and rounding as above.

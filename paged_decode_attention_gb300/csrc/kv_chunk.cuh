@@ -255,15 +255,26 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
   // or the tables, or reading the cache.
   wait_for_primary_grid();
   allow_dependent_launch();
+  bool decreasing = false;
   for (int i = threadIdx.x; i <= p.batch; i += kThreads<kShared>) {
-    s.cu_q[i] = p.cu_q[i];
-    if (i < p.batch) s.len[i] = p.seq_lens[i];
+    const int q0 = p.cu_q[i];
+    s.cu_q[i] = q0;
+    if (i < p.batch) {
+      s.len[i] = p.seq_lens[i];
+      decreasing |= p.cu_q[i + 1] < q0;
+    }
   }
   const bool has_kv = !kShared || warp == kQWarps;
   RawRow<kD> w_raw, wk_raw;  // the warp's weights; of a warp with both, the keys'
   load_raw<kD>(kShared && has_kv ? p.w_k : p.w_q, w_raw);
   if constexpr (!kShared) load_raw<kD>(p.w_k, wk_raw);
-  __syncthreads();
+  // Where cu_q decreases, sequences overlap or run backwards: a token found by
+  // counting ends may lie behind its sequence, at a position beyond the table.
+  // The call is left alone as a whole.
+  if (__syncthreads_or(decreasing)) {
+    if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+    return;
+  }
 
   int buf = 0;
   for (int t = blockIdx.x; t < p.total_q; t += gridDim.x) {
