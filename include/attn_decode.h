@@ -404,7 +404,9 @@ int32_t attn_kv_append_global(const void* qkv, const void* w_q, const void* w_k,
  *              (its q is)
  *
  * Two tokens of one call must not share a cache slot.  total_q 0 launches
- * nothing.  Arithmetic and rounding as above.
+ * nothing.  Arithmetic and rounding as above, and rows whose squares add up
+ * beyond fp32's range (a root mean square above about 2^59) come out as the
+ * formula says too, where the single-token calls write zeros.
  */
 int32_t attn_kv_append_sliding_chunk(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
                                      const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,

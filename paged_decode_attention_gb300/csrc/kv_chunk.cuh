@@ -32,6 +32,8 @@
 // kv_append.cuh.
 #pragma once
 
+#include <type_traits>
+
 #include "fp8.cuh"
 #include "kv_append.cuh"
 
@@ -133,20 +135,6 @@ __device__ __forceinline__ void widen(const RawRow<kD>& r, Row<kD>& x) {
   }
 }
 
-// 1 / sqrt(mean(x^2) + eps)
-template <int kD>
-__device__ __forceinline__ float norm_factor(const Row<kD>& r, float eps) {
-  float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int j = 0; j < Row<kD>::kWords; ++j) ss = __ffma2_rn(r.lo[j], r.lo[j], __ffma2_rn(r.hi[j], r.hi[j], ss));
-  float sum = ss.x + ss.y;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float mean = sum / static_cast<float>(kD) + eps;
-  const float inv = rsqrtf(mean);
-  return fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.f), inv);  // one Newton step: the root to its last bit
-}
-
 template <int kD>
 __device__ __forceinline__ void times(Row<kD>& r, float f) {
   const float2 f2 = make_float2(f, f);
@@ -155,6 +143,41 @@ __device__ __forceinline__ void times(Row<kD>& r, float f) {
     r.lo[j] = __fmul2_rn(r.lo[j], f2);
     r.hi[j] = __fmul2_rn(r.hi[j], f2);
   }
+}
+
+// sum(x^2), the same in every lane
+template <int kD>
+__device__ __forceinline__ float sum_squares(const Row<kD>& r) {
+  float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < Row<kD>::kWords; ++j) ss = __ffma2_rn(r.lo[j], r.lo[j], __ffma2_rn(r.hi[j], r.hi[j], ss));
+  float sum = ss.x + ss.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// 1 / sqrt(mean(x^2) + eps).  The squares of a finite row can add up beyond
+// fp32's range (a mean square above 2^119).  Without kWide the factor is NaN then
+// and `beyond` is set; with it such a row is first brought down by 2^70: 512
+// squares of at most 2^116 stay below 2^126, and eps no longer counts.  (Exact but
+// for elements below 2^-56, of which less than 2^-115 is left.)  An infinity gives
+// NaN either way, through the Newton step.
+template <int kD, bool kWide>
+__device__ __forceinline__ float norm_factor(Row<kD>& r, float eps, bool& beyond) {
+  float sum = sum_squares<kD>(r);
+  if constexpr (kWide) {
+    if (sum == INFINITY) {
+      times<kD>(r, 0x1p-70f);
+      sum = sum_squares<kD>(r);
+      eps = 0.f;
+    }
+  } else {
+    beyond |= sum == INFINITY;
+  }
+  const float mean = sum / static_cast<float>(kD) + eps;
+  const float inv = rsqrtf(mean);
+  return fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.f), inv);  // one Newton step: the root to its last bit
 }
 
 // The norm's weights come first where they can: the product of two bf16 values
@@ -277,91 +300,102 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
   }
 
   int buf = 0;
-  for (int t = blockIdx.x; t < p.total_q; t += gridDim.x) {
-    // this warp's rows, all in flight together
-    const __nv_bfloat16* src = p.qkv + static_cast<size_t>(t) * kRowLen;
-    RawRow<kD> rq[2], rk, rv;  // (global layers: the shared head, head kHq, in the ninth warp's rq[0])
-    load_raw<kD>(src + (2 * warp) * kD, rq[0]);
-    if (!kShared || warp < kQWarps) load_raw<kD>(src + (2 * warp + 1) * kD, rq[1]);
-    if constexpr (!kShared) {
-      load_raw<kD>(src + (kHq + warp) * kD, rk);
-      load_raw<kD>(src + (kHq + kHkv + warp) * kD, rv);
-    }
-    // the token's sequence: the number of sequences that end at or before t
-    // (the same in every warp of the block)
-    int pos = -1;  // the token is left alone
-    int32_t phys = 0;
-    int b = 0;
-    for (int j0 = 0; j0 < p.batch; j0 += 32) {
-      const int j = j0 + lane;
-      b += __popc(__ballot_sync(0xffffffffu, j < p.batch && s.cu_q[j + 1] <= t));
-    }
-    if (b < p.batch) {  // rows behind the last sequence are left alone
-      const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1];
-      const int L = s.len[b];
-      const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
-      // a sequence whose numbers do not fit together is left alone as a whole
-      if (q0 < 0 || t < q0 || q1 > p.total_q || q1 - q0 > L || L > cap) {
-        if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
-      } else {
-        pos = L - (q1 - q0) + (t - q0);
-        if (has_kv) phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kPage];
+  bool beyond = false;
+  const auto tokens = [&](auto wide_c) {
+    constexpr bool kWide = decltype(wide_c)::value;
+    for (int t = blockIdx.x; t < p.total_q; t += gridDim.x) {
+      // this warp's rows, all in flight together
+      const __nv_bfloat16* src = p.qkv + static_cast<size_t>(t) * kRowLen;
+      RawRow<kD> rq[2];  // (global layers: the shared head, head kHq, in the ninth warp's rq[0])
+      [[maybe_unused]] RawRow<kD> rk, rv;
+      load_raw<kD>(src + (2 * warp) * kD, rq[0]);
+      if (!kShared || warp < kQWarps) load_raw<kD>(src + (2 * warp + 1) * kD, rq[1]);
+      if constexpr (!kShared) {
+        load_raw<kD>(src + (kHq + warp) * kD, rk);
+        load_raw<kD>(src + (kHq + kHkv + warp) * kD, rv);
       }
-    }
-    if (threadIdx.x < kPairs)
-      sincos_at(freq, pos < 0 ? 0 : pos, &s.sin[buf][threadIdx.x], &s.cos[buf][threadIdx.x]);
-    __syncthreads();  // one per token: the buffer written next was read before this barrier
-    const float* cs = s.cos[buf];
-    const float* sn = s.sin[buf];
-    buf ^= 1;
-    if (pos < 0) continue;
+      // the token's sequence: the number of sequences that end at or before t
+      // (the same in every warp of the block)
+      int pos = -1;  // the token is left alone
+      int32_t phys = 0;
+      int b = 0;
+      for (int j0 = 0; j0 < p.batch; j0 += 32) {
+        const int j = j0 + lane;
+        b += __popc(__ballot_sync(0xffffffffu, j < p.batch && s.cu_q[j + 1] <= t));
+      }
+      if (b < p.batch) {  // rows behind the last sequence are left alone
+        const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1];
+        const int L = s.len[b];
+        const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
+        // a sequence whose numbers do not fit together is left alone as a whole
+        if (q0 < 0 || t < q0 || q1 > p.total_q || q1 - q0 > L || L > cap) {
+          if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+        } else {
+          pos = L - (q1 - q0) + (t - q0);
+          if (has_kv) phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kPage];
+        }
+      }
+      if (threadIdx.x < kPairs)
+        sincos_at(freq, pos < 0 ? 0 : pos, &s.sin[buf][threadIdx.x], &s.cos[buf][threadIdx.x]);
+      __syncthreads();  // one per token: the buffer written next was read before this barrier
+      const float* cs = s.cos[buf];
+      const float* sn = s.sin[buf];
+      buf ^= 1;
+      if (pos < 0) continue;
 
-    Row<kD> x, w;
-    if (!kShared || warp < kQWarps) {
-      widen<kD>(w_raw, w);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        widen<kD>(rq[i], x);
-        const float f = norm_factor<kD>(x, p.eps);
-        scale<kD>(x, w);
-        times<kD>(x, f);
-        rotate<kD, kPairs>(cs, sn, x);
-        store_bf16<kD>(p.q_out + (static_cast<size_t>(t) * kHq + 2 * warp + i) * kD, x);
+      Row<kD> x, w;
+      if (!kShared || warp < kQWarps) {
+        widen<kD>(w_raw, w);
+  #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          widen<kD>(rq[i], x);
+          const float f = norm_factor<kD, kWide>(x, p.eps, beyond);
+          scale<kD>(x, w);
+          times<kD>(x, f);
+          rotate<kD, kPairs>(cs, sn, x);
+          store_bf16<kD>(p.q_out + (static_cast<size_t>(t) * kHq + 2 * warp + i) * kD, x);
+        }
+        if (kShared) continue;
       }
-      if (kShared) continue;
+      if (phys < 0 || static_cast<int64_t>(phys) >= p.num_pages) {
+        if (lane == 0) report(p.status, ATTN_DEV_BAD_PAGE);
+        continue;
+      }
+      const int c = kShared ? 0 : warp;
+      const int row = pos % kPage;
+      const size_t off = ((static_cast<size_t>(phys) * kPage + row) * kHkv + c) * kD;
+      [[maybe_unused]] const size_t soff = (static_cast<size_t>(phys) * kHkv + c) * kPage + row;
+      const auto store = [&](void* pool, uint8_t* scales, Row<kD>& y) {
+        if constexpr (kFp8)
+          store_fp8<kD>(static_cast<uint8_t*>(pool) + off, scales + soff, y);
+        else
+          store_bf16<kD>(static_cast<__nv_bfloat16*>(pool) + off, y);
+      };
+      if constexpr (!kShared) {
+        widen<kD>(rv, x);
+        times<kD>(x, norm_factor<kD, kWide>(x, p.eps, beyond));
+        store(p.v_pool, p.v_scale, x);
+      }
+      widen<kD>(kShared ? rq[0] : rk, x);
+      const float f = norm_factor<kD, kWide>(x, p.eps, beyond);
+      if constexpr (kShared) {  // (the keys are rounded after each of the two products: the raw row once
+        times<kD>(x, f);        // more, for one rounding, costs 8 % of a call in registers)
+        store(p.v_pool, p.v_scale, x);
+        if (p.k_pool == nullptr) continue;  // a values-only cache
+      }
+      widen<kD>(kShared ? w_raw : wk_raw, w);
+      scale<kD>(x, w);
+      if constexpr (!kShared) times<kD>(x, f);
+      rotate<kD, kPairs>(cs, sn, x);
+      store(p.k_pool, p.k_scale, x);
     }
-    if (phys < 0 || static_cast<int64_t>(phys) >= p.num_pages) {
-      if (lane == 0) report(p.status, ATTN_DEV_BAD_PAGE);
-      continue;
-    }
-    const int c = kShared ? 0 : warp;
-    const int row = pos % kPage;
-    const size_t off = ((static_cast<size_t>(phys) * kPage + row) * kHkv + c) * kD;
-    const size_t soff = (static_cast<size_t>(phys) * kHkv + c) * kPage + row;
-    const auto store = [&](void* pool, uint8_t* scales, Row<kD>& y) {
-      if constexpr (kFp8)
-        store_fp8<kD>(static_cast<uint8_t*>(pool) + off, scales + soff, y);
-      else
-        store_bf16<kD>(static_cast<__nv_bfloat16*>(pool) + off, y);
-    };
-    if constexpr (!kShared) {
-      widen<kD>(rv, x);
-      times<kD>(x, norm_factor<kD>(x, p.eps));
-      store(p.v_pool, p.v_scale, x);
-    }
-    widen<kD>(kShared ? rq[0] : rk, x);
-    const float f = norm_factor<kD>(x, p.eps);
-    if constexpr (kShared) {  // (the keys are rounded after each of the two products: the raw row once
-      times<kD>(x, f);        // more, for one rounding, costs 8 % of a call in registers)
-      store(p.v_pool, p.v_scale, x);
-      if (p.k_pool == nullptr) continue;  // a values-only cache
-    }
-    widen<kD>(kShared ? w_raw : wk_raw, w);
-    scale<kD>(x, w);
-    if constexpr (!kShared) times<kD>(x, f);
-    rotate<kD, kPairs>(cs, sn, x);
-    store(p.k_pool, p.k_scale, x);
-  }
+  };
+  tokens(std::false_type{});
+  // Rows whose squares left fp32's range (no model's): the block's tokens once more,
+  // with a test in front of every factor.  In the first pass those tests would cost
+  // (8192 sliding tokens 45.8 us; as a call behind the stores 44.2, this way 43.7,
+  // without them 43.4).
+  if (__syncthreads_or(beyond)) tokens(std::true_type{});
 }
 
 }  // namespace chunk

@@ -6,7 +6,7 @@ import torch
 
 import paged_decode_attention_gb300 as pda
 
-from test_chunk_append import Chunk, run_chunk, run_fp8
+from test_chunk_append import Chunk, check_chunk, check_fp8, run_chunk, run_fp8
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,21 @@ def test_equal_ends_are_no_decrease(cuda_lib, kind):
     q, k, v, st = run_chunk(c)
     assert st == 0 and not (q == 7.0).all(-1).any()
     assert np.isfinite(k.double().cpu().numpy()[c.page, c.row]).all()
+
+
+@pytest.mark.parametrize("exponent", [57, 60, 64, 90, 120, 125])
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_rows_whose_squares_leave_the_range_of_fp32(cuda_lib, kind, exponent):
+    # (sum x^2 passes 2^128 from a root mean square of 2^60 (D = 256) or 2^59.5 (D = 512) on)
+    check_chunk(Chunk(kind, [40, 7], [9, 7], 82, scale=2.0 ** exponent))
+    check_fp8(Chunk(kind, [40, 7], [9, 7], 83, scale=2.0 ** exponent))
+
+
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_one_element_at_the_top_of_the_range(cuda_lib, kind):
+    # one element of every head row dominates all others, up to the largest bf16
+    for value in (2.0 ** 64, -(2.0 ** 100), float(torch.finfo(torch.bfloat16).max)):
+        c = Chunk(kind, [40, 7], [9, 7], 84)
+        c.qkv.view(c.qkv.shape[0], -1, c.D)[:, :, 5] = value
+        check_chunk(c)
+        check_fp8(c)
