@@ -17,8 +17,15 @@ power-of-two scales; ``include/attn_fp8.h``) is written by
 ``attn_decode_{sliding,global}_fp8`` and read back into bf16 pages by
 ``attn_kv_read_{sliding,global}_fp8``; ``new_fp8_cache`` allocates one.
 ``attn_decode_global_prefix`` decodes a batch behind a prefix that it shares.
+
+Streams.  A call works on ``stream`` (default: the current one of its device),
+and what it makes for itself, outputs and workspaces not given, is made on that
+stream too.  A prepared call or a step makes its own when it is constructed, on
+the current stream; its first launch waits for that, on whichever stream it is.
+The tensors given are the caller's to order.
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -226,7 +233,8 @@ def attn_decode_launches(kind, batch, max_seq_len, window, num_splits=0, num_sms
 
 
 def new_workspace(nbytes, device):
-    """A decode workspace of nbytes: its first WORKSPACE_ZERO_BYTES zeroed, as a first use requires."""
+    """A decode workspace of nbytes: its first WORKSPACE_ZERO_BYTES zeroed (on the current stream), as a first use
+    requires."""
     ws = torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
     ws[:WORKSPACE_ZERO_BYTES].zero_()
     return ws
@@ -250,8 +258,10 @@ def _decode_args(kind, q, k_pool, v_pool, block_table, seq_lens, o, window, max_
                  num_splits, workspace, status, w_k=None):
     """Checked, marshalled arguments of one decode call (everything but the stream).
 
-    Returns (args, keep, o, fn_name): the C arguments, the tensors they point
-    into (to be kept alive), the output tensor and the C entry point."""
+    Returns (args, keep, o, fn_name, made): the C arguments, the tensors they
+    point into (to be kept alive), the output tensor, the C entry point, and
+    those of the tensors that were made here."""
+    given = (o, workspace)
     Hq, Hkv, D = SHAPES[kind]
     if q.dim() != 3:
         raise ValueError("q must be [batch, %d, %d]" % (Hq, D))
@@ -288,7 +298,7 @@ def _decode_args(kind, q, k_pool, v_pool, block_table, seq_lens, o, window, max_
             int(window), OUT_F32 if o.dtype == torch.float32 else OUT_BF16, int(num_splits), ws_ptr,
             workspace.numel(), st_ptr)
     keep = (q, k_pool, v_pool, block_table, seq_lens, o, workspace, status, w_k)
-    return args, keep, o, fn_name
+    return args, keep, o, fn_name, _made(given, (o, workspace))
 
 
 def _stream_ptr(stream, device):
@@ -297,16 +307,90 @@ def _stream_ptr(stream, device):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _as_stream(stream, device):
+    """A torch stream for a torch stream or a raw cudaStream_t (0, 1: the legacy default stream)."""
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    ptr = int(stream)
+    return torch.cuda.default_stream(device) if ptr in (0, 1) else torch.cuda.ExternalStream(ptr, device=device)
+
+
+def _made(given, used):
+    """Of the tensors used, those that stand for a None among the given ones."""
+    return tuple(u for g, u in zip(given, used) if g is None)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _work_on(stream, tensor, made):
+    """What a one-shot call makes inside is made on its stream: a block of another stream's could still be at work
+    there, and would be handed out there again while the call runs.  What is put into `made` is kept from reuse until
+    the caller's stream is done with it, too."""
+    if stream is None or not isinstance(tensor, torch.Tensor) or tensor.device.type != "cuda":
+        return _HERE
+    here, there = torch.cuda.current_stream(tensor.device), _as_stream(stream, tensor.device)
+    return _HERE if here.cuda_stream == there.cuda_stream else _work_there(here, there, made)
+
+
+@contextlib.contextmanager
+def _work_there(here, there, made):
+    with torch.cuda.stream(there):
+        yield
+    for t in made:
+        t.record_stream(here)
+
+
+class _OwnTensors:
+    """The tensors that a prepared call or a step made for itself: filled before its first launch on any stream, and not
+    handed out again while a launch may be at work on them.
+
+    Launches of one object do not overlap, so the first one waits for all others.  A launch that is being captured
+    waits for nothing (it runs when the graph is replayed; torch.cuda.graph synchronises before it captures)."""
+
+    def __init__(self):
+        self._tensors, self._filled = [], {}
+        self.ordered = set()  # streams that before_launch has nothing more to do for
+
+    def add(self, made, device):
+        if not made:
+            return
+        self._tensors.extend(made)
+        self.ordered.clear()
+        here = torch.cuda.current_stream(device)
+        with torch.cuda.device(device):
+            if not torch.cuda.is_current_stream_capturing():
+                event = torch.cuda.Event()
+                event.record(here)
+                self._filled[here.cuda_stream] = event
+
+    def before_launch(self, s_ptr, device):
+        stream = _as_stream(s_ptr, device)
+        with torch.cuda.stream(stream):
+            if self._tensors and torch.cuda.is_current_stream_capturing():
+                return
+        for made_on, event in self._filled.items():
+            if made_on != s_ptr:
+                stream.wait_event(event)
+        self._filled = {}
+        for t in self._tensors:
+            t.record_stream(stream)
+        self.ordered.add(s_ptr)
+
+
 def _call(kind, q, k_pool, v_pool, block_table, seq_lens, o, window, max_seq_len, out_dtype,
           num_splits, workspace, status, stream, w_k=None):
-    args, _, o, fn_name = _decode_args(kind, q, k_pool, v_pool, block_table, seq_lens, o, window, max_seq_len,
-                                       out_dtype, num_splits, workspace, status, w_k)
-    s_ptr = _stream_ptr(stream, q.device)
-    with torch.cuda.device(q.device):
-        st = getattr(load(), fn_name)(*args, s_ptr)
-    if st != ATTN_OK:
-        raise AttnDecodeError(st, attn_last_error())
-    return o
+    outputs = []
+    with _work_on(stream, q, outputs):
+        args, _, out, fn_name, _ = _decode_args(kind, q, k_pool, v_pool, block_table, seq_lens, o, window, max_seq_len,
+                                                out_dtype, num_splits, workspace, status, w_k)
+        s_ptr = _stream_ptr(stream, q.device)
+        with torch.cuda.device(q.device):
+            st = getattr(load(), fn_name)(*args, s_ptr)
+        if st != ATTN_OK:
+            raise AttnDecodeError(st, attn_last_error())
+        outputs.extend(_made((o,), (out,)))
+    return out
 
 
 class PreparedDecode:
@@ -316,19 +400,25 @@ class PreparedDecode:
     validates the tensors exactly as the one-shot functions do and keeps their
     device pointers; ``run(stream)`` then costs one C call.  The tensors must
     stay alive and in place (the object keeps references to them); their
-    contents may change between runs.
+    contents may change between runs.  Runs on different streams must not
+    overlap: they share the output and the workspace.
     """
 
     def __init__(self, kind, q, k_pool, v_pool, block_table, seq_lens, o=None, *, window, max_seq_len=None,
                  out_dtype=torch.bfloat16, num_splits=0, workspace=None, status=None, w_k=None):
-        self._args, self._keep, self.o, fn_name = _decode_args(
+        self._args, self._keep, self.o, fn_name, made = _decode_args(
             kind, q, k_pool, v_pool, block_table, seq_lens, o, window, max_seq_len, out_dtype, num_splits,
             workspace, status, w_k)
         self._fn = getattr(load(), fn_name)
+        self._device = q.device
+        self._own = _OwnTensors()
+        self._own.add(made, q.device)
 
     def run(self, stream):
         """Enqueue the call on `stream` (a torch.cuda.Stream or a raw cudaStream_t); returns o."""
         s_ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if s_ptr not in self._own.ordered:
+            self._own.before_launch(s_ptr, self._device)
         st = self._fn(*self._args, s_ptr)
         if st != ATTN_OK:
             raise AttnDecodeError(st, attn_last_error())
@@ -346,7 +436,8 @@ class Step:
     graph launch (mode "graph"), or the recorded launches back to back (mode
     "direct"); "auto" picks direct for steps of up to two calls.  The tensors
     are used in place (the object keeps references to them); their contents
-    may change between launches.
+    may change between launches.  Launches on different streams must not
+    overlap.
     """
 
     def __init__(self):
@@ -355,6 +446,7 @@ class Step:
         self._check(self._lib.attn_step_create(ctypes.byref(h)))
         self._h = h
         self._keep = []
+        self._own = _OwnTensors()
         self.device = None
 
     def _check(self, rc):
@@ -363,13 +455,9 @@ class Step:
 
     def _add_decode(self, kind, fn_name, q, k_pool, v_pool, block_table, seq_lens, o, window, max_seq_len=None,
                     out_dtype=torch.bfloat16, num_splits=0, workspace=None, status=None, w_k=None):
-        args, keep, o, name = _decode_args(kind, q, k_pool, v_pool, block_table, seq_lens, o, window, max_seq_len,
-                                           out_dtype, num_splits, workspace, status, w_k)
-        with torch.cuda.device(q.device):
-            self._check(getattr(self._lib, fn_name)(self._h, *args))
-        self._keep.append(keep)
-        self.device = q.device
-        return o
+        args, keep, o, _, made = _decode_args(kind, q, k_pool, v_pool, block_table, seq_lens, o, window, max_seq_len,
+                                              out_dtype, num_splits, workspace, status, w_k)
+        return self._record(fn_name, args, keep, o, q.device, made)
 
     def add_decode_sliding(self, q, k_pool, v_pool, block_table, seq_lens, o=None, *, window=1024, **kw):
         return self._add_decode(KIND_SLIDING, "attn_step_add_decode_sliding", q, k_pool, v_pool, block_table,
@@ -384,13 +472,8 @@ class Step:
                                 seq_lens, o, window, w_k=w_k, **kw)
 
     def _add_append(self, kind, fn_name, qkv, w_q, w_k, block_table, positions, k_pool, v_pool, q_out, status):
-        args, keep, q_out, _ = _append_args(kind, qkv, w_q, w_k, block_table, positions, k_pool, v_pool, q_out,
-                                            status)
-        with torch.cuda.device(qkv.device):
-            self._check(getattr(self._lib, fn_name)(self._h, *args))
-        self._keep.append(keep)
-        self.device = qkv.device
-        return q_out
+        args, keep, out, _ = _append_args(kind, qkv, w_q, w_k, block_table, positions, k_pool, v_pool, q_out, status)
+        return self._record(fn_name, args, keep, out, qkv.device, _made((q_out,), (out,)))
 
     def add_kv_append_sliding(self, qkv, w_q, w_k, block_table, positions, k_pool, v_pool, q_out=None, *,
                               status=None):
@@ -402,11 +485,15 @@ class Step:
         return self._add_append(KIND_GLOBAL, "attn_step_add_kv_append_global", qkv, w_q, w_k, block_table,
                                 positions, k_pool, v_pool, q_out, status)
 
-    def _add(self, fn_name, args, keep, out, device):
+    def _add(self, fn_name, args, keep, out, device, made):
         """Record a checked, marshalled call under attn_step_add_*; returns its output."""
+        return self._record(fn_name.replace("attn_", "attn_step_add_"), args, keep, out, device, made)
+
+    def _record(self, step_fn_name, args, keep, out, device, made):
         with torch.cuda.device(device):
-            self._check(getattr(self._lib, fn_name.replace("attn_", "attn_step_add_"))(self._h, *args))
+            self._check(getattr(self._lib, step_fn_name)(self._h, *args))
         self._keep.append(keep)
+        self._own.add(made, device)
         self.device = device
         return out
 
@@ -464,7 +551,10 @@ class Step:
 
     def launch(self, stream=None):
         """Enqueue the whole step on `stream` (default: the current stream of its device)."""
-        self._check(self._lib.attn_step_launch(self._h, _stream_ptr(stream, self.device)))
+        s_ptr = _stream_ptr(stream, self.device)
+        if s_ptr not in self._own.ordered:
+            self._own.before_launch(s_ptr, self.device)
+        self._check(self._lib.attn_step_launch(self._h, s_ptr))
 
     def close(self):
         if self._h is not None and self._h.value:
@@ -550,12 +640,14 @@ def _append_args(kind, qkv, w_q, w_k, block_table, positions, k_pool, v_pool, q_
 
 
 def _append(kind, qkv, w_q, w_k, block_table, positions, k_pool, v_pool, q_out, status, stream):
-    args, _, q_out, fn_name = _append_args(kind, qkv, w_q, w_k, block_table, positions, k_pool, v_pool, q_out,
-                                           status)
-    rc = getattr(load(), fn_name)(*args, _stream_ptr(stream, qkv.device))
-    if rc != ATTN_OK:
-        raise AttnDecodeError(rc, attn_last_error())
-    return q_out
+    outputs = []
+    with _work_on(stream, qkv, outputs):
+        args, _, out, fn_name = _append_args(kind, qkv, w_q, w_k, block_table, positions, k_pool, v_pool, q_out, status)
+        rc = getattr(load(), fn_name)(*args, _stream_ptr(stream, qkv.device))
+        if rc != ATTN_OK:
+            raise AttnDecodeError(rc, attn_last_error())
+        outputs.extend(_made((q_out,), (out,)))
+    return out
 
 
 def attn_kv_append_sliding(qkv, w_q, w_k, block_table, positions, k_pool, v_pool, q_out=None, *, status=None,
@@ -582,6 +674,16 @@ def attn_kv_append_global(qkv, w_q, w_k, block_table, positions, k_pool, v_pool,
 
 
 def _prefill(kind, q, k_pool, v_pool, block_table, seq_lens, cu_q, o, max_q, window, out_dtype, status, stream):
+    outputs = []
+    with _work_on(stream, q, outputs):
+        out = _prefill_here(kind, q, k_pool, v_pool, block_table, seq_lens, cu_q, o, max_q, window, out_dtype, status,
+                            stream)
+        outputs.extend(_made((o,), (out,)))
+    return out
+
+
+def _prefill_here(kind, q, k_pool, v_pool, block_table, seq_lens, cu_q, o, max_q, window, out_dtype, status, stream):
+    """_prefill's call, what it makes made on the current stream."""
     Hq, Hkv, D = SHAPES[kind]
     if q.dim() != 3:
         raise ValueError("q must be [total_q, %d, %d]" % (Hq, D))
@@ -603,9 +705,7 @@ def _prefill(kind, q, k_pool, v_pool, block_table, seq_lens, cu_q, o, max_q, win
             _ptr(cu_q, "cu_q", torch.int32, (batch + 1,)),
             _ptr(o, "o", o.dtype, (total_q, Hq, D))]
     st_ptr = None if status is None else _ptr(status, "status", torch.int32, (1,))
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
-    s_ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    s_ptr = _stream_ptr(stream, q.device)
     lib = load()
     fn = lib.attn_prefill_sliding if kind == KIND_SLIDING else lib.attn_prefill_global
     rc = fn(*args, batch, total_q, int(max_q), max_blocks, num_pages, int(window), code, st_ptr, s_ptr)
@@ -661,18 +761,24 @@ class PreparedCall:
     Construction records the call's kernel launches (attn_step, direct mode),
     tensor maps included; ``run(stream)`` enqueues them with one C call and
     returns the call's output.  The tensors must stay in place (the object
-    keeps them alive), their contents may change between runs.
+    keeps them alive, for a graph that captured a run too), their contents may
+    change between runs.  Runs on different streams must not overlap: they
+    share the output and the workspace.
     """
 
-    def __init__(self, fn_name, args, keep, out, device):
+    def __init__(self, fn_name, args, keep, out, device, made):
         self._step = Step()
-        self._step._add(fn_name, args, keep, out, device)
+        self._step._add(fn_name, args, keep, out, device, made)
         self._step.finalize("direct")
         self._launch, self._handle, self._device, self.out = load().attn_step_launch, self._step._h, device, out
+        self._ordered = self._step._own.ordered
 
     def run(self, stream=None):
         """Enqueue the call on `stream` (default: the current stream of its device); returns its output."""
-        st = self._launch(self._handle, _stream_ptr(stream, self._device))
+        s_ptr = _stream_ptr(stream, self._device)
+        if s_ptr not in self._ordered:
+            self._step._own.before_launch(s_ptr, self._device)
+        st = self._launch(self._handle, s_ptr)
         if st != ATTN_OK:
             raise AttnDecodeError(st, attn_last_error())
         return self.out
@@ -734,8 +840,9 @@ def _kind_name(kind):
 
 
 def _chunk_args(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out=None, *, status=None):
-    """(fn_name, args without the stream, tensors to keep, output, device) of a chunk append."""
+    """(fn_name, args without the stream, tensors to keep, output, device, tensors made) of a chunk append."""
     _, Hkv, D = SHAPES[kind]
+    given = (q_out,)
     ptrs, q_out, batch, total_q, max_blocks = _append_common(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out)
     _dims(v_pool, 4, "v_pool must be [num_pages, 16, %d, %d]" % (Hkv, D))
     n = v_pool.shape[0]
@@ -745,17 +852,18 @@ def _chunk_args(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool
     device = _one_device(keep)
     args = tuple(ptrs) + (k_ptr, _ptr(v_pool, "v_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D)), batch, total_q,
                           max_blocks, n, _status_ptr(status))
-    return "attn_kv_append_%s_chunk" % _kind_name(kind), args, keep, q_out, device
+    return "attn_kv_append_%s_chunk" % _kind_name(kind), args, keep, q_out, device, _made(given, (q_out,))
 
 
 def _append_fp8_args(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, k_scale, v_scale, q_out=None, *,
                      status=None):
+    given = (q_out,)
     ptrs, q_out, batch, total_q, max_blocks = _append_common(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out)
     cache, n = _fp8_ptrs(kind, k_pool, v_pool, k_scale, v_scale)
     keep = (qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, k_scale, v_scale, status)
     device = _one_device(keep)
     args = tuple(ptrs + cache) + (batch, total_q, max_blocks, n, _status_ptr(status))
-    return "attn_kv_append_%s_fp8" % _kind_name(kind), args, keep, q_out, device
+    return "attn_kv_append_%s_fp8" % _kind_name(kind), args, keep, q_out, device, _made(given, (q_out,))
 
 
 def _read_fp8_args(kind, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table=None, *,
@@ -778,7 +886,7 @@ def _read_fp8_args(kind, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens
                            _ptr(v_out, "v_out", torch.bfloat16, (out_pages, PAGE_SIZE, Hkv, D)),
                            _ptr(out_table, "out_table", torch.int32, (batch, max_blocks)), batch, max_blocks, n,
                            out_pages, int(max_seq_len), int(span), _status_ptr(status))
-    return "attn_kv_read_%s_fp8" % _kind_name(kind), args, keep, (k_out, v_out), device
+    return "attn_kv_read_%s_fp8" % _kind_name(kind), args, keep, (k_out, v_out), device, ()
 
 
 def _decode_fp8_args(kind, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o=None, *, window=None,
@@ -787,6 +895,7 @@ def _decode_fp8_args(kind, q, k_pool, v_pool, k_scale, v_scale, block_table, seq
     _dims(q, 3, "q must be [batch, %d, %d]" % (Hq, D))
     _dims(block_table, 2, "block_table must be [batch, max_blocks]")
     batch, max_blocks = block_table.shape
+    given = (o, workspace)
     cache, n = _fp8_ptrs(kind, k_pool, v_pool, k_scale, v_scale)
     q_ptr = _ptr(q, "q", torch.bfloat16, (batch, Hq, D))
     o = _output(o, (batch, Hq, D), out_dtype, q.device)
@@ -805,7 +914,7 @@ def _decode_fp8_args(kind, q, k_pool, v_pool, k_scale, v_scale, block_table, seq
     args = tuple([q_ptr] + cache + tables) + (
         batch, max_blocks, n, int(max_seq_len), int(window), OUT_F32 if o.dtype == torch.float32 else OUT_BF16,
         int(num_splits), _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _status_ptr(status))
-    return "attn_decode_%s_fp8" % _kind_name(kind), args, keep, o, device
+    return "attn_decode_%s_fp8" % _kind_name(kind), args, keep, o, device, _made(given, (o, workspace))
 
 
 def attn_decode_fp8_plan(kind, batch, max_seq_len, window, num_splits=0, num_sms=152):
@@ -866,6 +975,7 @@ def _prefix_args(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_l
     _dims(prefix_table, 1, "prefix_table must be [prefix_blocks]")
     _dims(block_table, 2, "block_table must be [batch, max_blocks]")
     (batch, max_blocks), n, blocks = block_table.shape, k_pool.shape[0], prefix_table.shape[0]
+    given = (o, workspace)
     ptrs = [_ptr(q, "q", torch.bfloat16, (batch, Hq, D)),
             _ptr(k_pool, "k_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D)),
             _ptr(v_pool, "v_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D)),
@@ -888,16 +998,20 @@ def _prefix_args(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_l
     args = tuple(ptrs) + (batch, blocks, max_blocks, n, int(max_prefix_len), int(max_seq_len),
                           OUT_F32 if o.dtype == torch.float32 else OUT_BF16, int(num_splits), int(prefix_splits),
                           _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _status_ptr(status))
-    return "attn_decode_global_prefix", args, keep, o, device
+    return "attn_decode_global_prefix", args, keep, o, device, _made(given, (o, workspace))
 
 
-def _once(stream, call):
-    fn_name, args, _, out, device = call
-    s_ptr = _stream_ptr(stream, device)
-    with torch.cuda.device(device):
-        st = getattr(load(), fn_name)(*args, s_ptr)
-    if st != ATTN_OK:
-        raise AttnDecodeError(st, attn_last_error())
+def _once(stream, marshal, first, *args, **kw):
+    """The call that marshal(first, *args, **kw) describes, on `stream`; `first` is a tensor, or args[0] is."""
+    outputs = []
+    with _work_on(stream, args[0] if isinstance(first, int) else first, outputs):
+        fn_name, c_args, _, out, device, made = marshal(first, *args, **kw)
+        s_ptr = _stream_ptr(stream, device)
+        with torch.cuda.device(device):
+            st = getattr(load(), fn_name)(*c_args, s_ptr)
+        if st != ATTN_OK:
+            raise AttnDecodeError(st, attn_last_error())
+        outputs.extend(t for t in made if t is out)
     return out
 
 
@@ -910,46 +1024,46 @@ def attn_kv_append_sliding_chunk(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_p
     seq_lens[b] cached ones (int32 [B], new tokens included).  Returns q_out
     [T,16,256], which with seq_lens and cu_q is what attn_prefill_sliding takes.
     """
-    return _once(stream, _chunk_args(KIND_SLIDING, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out,
-                                     status=status))
+    return _once(stream, _chunk_args, KIND_SLIDING, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out,
+                 status=status)
 
 
 def attn_kv_append_global_chunk(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out=None, *,
                                 status=None, stream=None):
     """attn_kv_append_sliding_chunk for global layers: qkv [T, 8704]; k_pool may be None (values-only cache)."""
-    return _once(stream, _chunk_args(KIND_GLOBAL, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out,
-                                     status=status))
+    return _once(stream, _chunk_args, KIND_GLOBAL, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out,
+                 status=status)
 
 
 def attn_kv_append_sliding_fp8(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, k_scale, v_scale,
                                q_out=None, *, status=None, stream=None):
     """attn_kv_append_sliding_chunk into an 8-bit cache: pools [P,16,8,256] float8_e4m3fn, scales [P,8,16]
     float8_e8m0fnu (new_fp8_cache).  A decode step is cu_q = arange(B + 1)."""
-    return _once(stream, _append_fp8_args(KIND_SLIDING, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool,
-                                          k_scale, v_scale, q_out, status=status))
+    return _once(stream, _append_fp8_args, KIND_SLIDING, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool,
+                 k_scale, v_scale, q_out, status=status)
 
 
 def attn_kv_append_global_fp8(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, k_scale, v_scale,
                               q_out=None, *, status=None, stream=None):
     """attn_kv_append_global_chunk into an 8-bit cache: pools [P,16,1,512] float8_e4m3fn, scales [P,1,16]
     float8_e8m0fnu; keys and values are both kept."""
-    return _once(stream, _append_fp8_args(KIND_GLOBAL, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool,
-                                          k_scale, v_scale, q_out, status=status))
+    return _once(stream, _append_fp8_args, KIND_GLOBAL, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool,
+                 k_scale, v_scale, q_out, status=status)
 
 
 def attn_kv_read_sliding_fp8(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table=None, *,
                              span=0, max_seq_len=None, status=None, stream=None):
     """The last min(L, span) positions of every sequence (span <= 0: all) of an 8-bit cache into the bf16 pools k_out
     and v_out [out_pages,16,8,256], page by page as out_table (default block_table) says; returns (k_out, v_out)."""
-    return _once(stream, _read_fp8_args(KIND_SLIDING, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out,
-                                        v_out, out_table, span=span, max_seq_len=max_seq_len, status=status))
+    return _once(stream, _read_fp8_args, KIND_SLIDING, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out,
+                 v_out, out_table, span=span, max_seq_len=max_seq_len, status=status)
 
 
 def attn_kv_read_global_fp8(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out, v_out, out_table=None, *,
                             span=0, max_seq_len=None, status=None, stream=None):
     """attn_kv_read_sliding_fp8 for global layers (pools [P,16,1,512])."""
-    return _once(stream, _read_fp8_args(KIND_GLOBAL, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out,
-                                        v_out, out_table, span=span, max_seq_len=max_seq_len, status=status))
+    return _once(stream, _read_fp8_args, KIND_GLOBAL, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_out,
+                 v_out, out_table, span=span, max_seq_len=max_seq_len, status=status)
 
 
 def attn_decode_sliding_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o=None, *, window=1024,
@@ -958,9 +1072,9 @@ def attn_decode_sliding_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, se
     """attn_decode_sliding over an 8-bit cache: q [B,16,256] bf16, pools [P,16,8,256] float8_e4m3fn, scales [P,8,16]
     float8_e8m0fnu -> o [B,16,256].  workspace: at least
     attn_decode_fp8_workspace_size(...) bytes from new_workspace; allocated per call when None."""
-    return _once(stream, _decode_fp8_args(KIND_SLIDING, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o,
-                                          window=window, max_seq_len=max_seq_len, out_dtype=out_dtype,
-                                          num_splits=num_splits, workspace=workspace, status=status))
+    return _once(stream, _decode_fp8_args, KIND_SLIDING, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o,
+                 window=window, max_seq_len=max_seq_len, out_dtype=out_dtype, num_splits=num_splits,
+                 workspace=workspace, status=status)
 
 
 def attn_decode_global_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o=None, *, window=0,
@@ -969,9 +1083,9 @@ def attn_decode_global_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq
     """attn_decode_global over an 8-bit cache: q [B,16,512] bf16, pools [P,16,1,512] float8_e4m3fn, scales [P,1,16]
     float8_e8m0fnu -> o [B,16,512].  workspace: at least
     attn_decode_fp8_workspace_size(...) bytes from new_workspace; allocated per call when None."""
-    return _once(stream, _decode_fp8_args(KIND_GLOBAL, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o,
-                                          window=window, max_seq_len=max_seq_len, out_dtype=out_dtype,
-                                          num_splits=num_splits, workspace=workspace, status=status))
+    return _once(stream, _decode_fp8_args, KIND_GLOBAL, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, o,
+                 window=window, max_seq_len=max_seq_len, out_dtype=out_dtype, num_splits=num_splits,
+                 workspace=workspace, status=status)
 
 
 def attn_decode_global_prefix(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o=None, *,
@@ -981,10 +1095,9 @@ def attn_decode_global_prefix(q, k_pool, v_pool, prefix_table, prefix_len, block
     [1] name its positions, block_table and seq_lens each sequence's own (0 allowed) behind it; all pages in the same
     pools.  max_prefix_len, max_seq_len: host bounds for the plan (default: what the tables hold).  workspace: at least
     attn_decode_prefix_workspace_size(...) bytes from new_workspace; allocated per call when None."""
-    return _once(stream, _prefix_args(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o,
-                                      max_prefix_len=max_prefix_len, max_seq_len=max_seq_len, out_dtype=out_dtype,
-                                      num_splits=num_splits, prefix_splits=prefix_splits, workspace=workspace,
-                                      status=status))
+    return _once(stream, _prefix_args, q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_lens, o,
+                 max_prefix_len=max_prefix_len, max_seq_len=max_seq_len, out_dtype=out_dtype, num_splits=num_splits,
+                 prefix_splits=prefix_splits, workspace=workspace, status=status)
 
 
 def prepare_decode_global_prefix(*args, **kw):
