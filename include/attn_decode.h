@@ -152,6 +152,9 @@ extern "C" {
  * status       optional device int32 for ATTN_DEV_* bits, or NULL
  * stream       cudaStream_t, as void*
  * returns      ATTN_OK or ATTN_ERR_*
+ *
+ * A NaN at a visible position gives NaN outputs, however the sequences are cut
+ * into blocks; what lies outside the visible positions is never used.
  */
 int32_t attn_decode_sliding(const void* q, const void* k_pool, const void* v_pool,
                             const int32_t* block_table, const int32_t* seq_lens, void* o,

@@ -288,6 +288,12 @@ __device__ __forceinline__ void store_out2(const DecodeParams& p, size_t idx, fl
   }
 }
 
+// (max, sum) of a partial row.  A NaN sum is handed on as (inf, 1): the merges
+// skip partials whose sum is not positive, and the others' inf - inf is NaN.
+__device__ __forceinline__ float2 partial_stats(float m, float l) {
+  return l == l ? make_float2(m, l) : make_float2(INFINITY, 1.f);
+}
+
 // ---------------------------------------------------------------------------
 // Producer side of the page pipeline, run by one whole warp.  Walks the
 // block's span of flattened pages, reads their block-table entries 32 at a

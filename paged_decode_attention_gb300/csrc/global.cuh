@@ -560,8 +560,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
           *reinterpret_cast<float2*>(p.part_o + slot1 * kD + d) = make_float2(acc[n][2], acc[n][3]);
         }
         if (warp == 0 && tq == 0) {
-          p.part_ml[slot0] = make_float2(m[0], lt[0]);
-          p.part_ml[slot1] = make_float2(m[1], lt[1]);
+          p.part_ml[slot0] = partial_stats(m[0], lt[0]);
+          p.part_ml[slot1] = partial_stats(m[1], lt[1]);
         }
       }
       reset();
@@ -767,14 +767,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
             *reinterpret_cast<float2*>(p.part_o + slot1 * kD + d) = make_float2(acc[n][2], acc[n][3]);
           }
           if (warp == 0 && tq == 0) {
-            float2 e0 = make_float2(m[0], lt[0]), e1 = make_float2(m[1], lt[1]);
-            if constexpr (!std::is_same<Params, DecodeParams>::value) {
-              // a NaN sum is handed on as (inf, 1): the merges skip partials whose sum is not positive
-              if (lt[0] != lt[0]) e0 = make_float2(INFINITY, 1.f);
-              if (lt[1] != lt[1]) e1 = make_float2(INFINITY, 1.f);
-            }
-            p.part_ml[slot0] = e0;
-            p.part_ml[slot1] = e1;
+            p.part_ml[slot0] = partial_stats(m[0], lt[0]);
+            p.part_ml[slot1] = partial_stats(m[1], lt[1]);
           }
         }
         reset();

@@ -426,9 +426,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             else
               *reinterpret_cast<float2*>(p.part_o + at) = make_float2(v0, v1);
           }
-          // a NaN sum is handed on as (inf, 1): the combine skips partials whose sum is not positive
-          if (!whole && warp == 0 && tq == 0)
-            p.part_ml[row] = lt[r] == lt[r] ? make_float2(ref[r].m, lt[r]) : make_float2(INFINITY, 1.f);
+          if (!whole && warp == 0 && tq == 0) p.part_ml[row] = partial_stats(ref[r].m, lt[r]);
         }
       }
       named_barrier_sync(1, kConsumers);  // row_sum read

@@ -404,17 +404,17 @@ __global__ void __launch_bounds__(kThreads)
       for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, s.merge_m[w][h]);
       float Lsum = 0.f;
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (M != -INFINITY) {
+      // (with M = -inf every weight was 0 or NaN; a NaN has to show)
+      const float M_use = M == -INFINITY ? 0.f : M;
 #pragma unroll
-        for (int w = 0; w < kConsumerWarps; ++w) {
-          const float fw = exp2f(s.merge_m[w][h] - M);
-          Lsum += fw * s.merge_l[w][h];
-          const float4 a = *reinterpret_cast<const float4*>(&s.merge_o[w][h][d0]);
-          O.x += fw * a.x;
-          O.y += fw * a.y;
-          O.z += fw * a.z;
-          O.w += fw * a.w;
-        }
+      for (int w = 0; w < kConsumerWarps; ++w) {
+        const float fw = exp2f(s.merge_m[w][h] - M_use);
+        Lsum += fw * s.merge_l[w][h];
+        const float4 a = *reinterpret_cast<const float4*>(&s.merge_o[w][h][d0]);
+        O.x += fw * a.x;
+        O.y += fw * a.y;
+        O.z += fw * a.z;
+        O.w += fw * a.w;
       }
       if (cur.whole(t, sp)) {
         const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
@@ -423,10 +423,11 @@ __global__ void __launch_bounds__(kThreads)
       } else if ((static_cast<int64_t>(g) + cur.b + 1) * kHq > p.part_rows) {
         if (tt == 0) report(p.status, ATTN_DEV_INTERNAL);  // cannot happen: slot beyond the workspace
       } else {
+        const float2 ml = partial_stats(M, Lsum);
         const size_t slot = (static_cast<size_t>(g) + cur.b) * kHq + hq0 + h;
         *reinterpret_cast<float4*>(p.part_o + slot * kD + d0) = O;
-        if (d0 == 0) p.part_ml[slot] = make_float2(M, Lsum);
-        if (p.merge_in_grid) merge_partials(p, t, s, cur.b, g, c, h, d0, M, Lsum, O);
+        if (d0 == 0) p.part_ml[slot] = ml;
+        if (p.merge_in_grid) merge_partials(p, t, s, cur.b, g, c, h, d0, ml.x, ml.y, O);
       }
       named_barrier_sync(1, kConsumerWarps * 32);  // merge buffers free again
       reset();

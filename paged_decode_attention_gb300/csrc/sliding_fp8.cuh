@@ -405,15 +405,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       } else if ((static_cast<int64_t>(gb) + cur.b + 1) * kHq > p.part_rows) {
         if (tt == 0) report(p.status, ATTN_DEV_INTERNAL);  // cannot happen: slot beyond the workspace
       } else {
-        // a NaN sum is handed on as (inf, 1): the merges skip partials whose sum is not positive
-        if (Lsum != Lsum) {
-          M = INFINITY;
-          Lsum = 1.f;
-        }
+        const float2 ml = partial_stats(M, Lsum);
         const size_t slot = (static_cast<size_t>(gb) + cur.b) * kHq + hq0 + h;
         *reinterpret_cast<float4*>(p.part_o + slot * kD + d0) = O;
-        if (d0 == 0) p.part_ml[slot] = make_float2(M, Lsum);
-        if (p.merge_in_grid) sliding::merge_partials(p, t, s, cur.b, gb, c, h, d0, M, Lsum, O);
+        if (d0 == 0) p.part_ml[slot] = ml;
+        if (p.merge_in_grid) sliding::merge_partials(p, t, s, cur.b, gb, c, h, d0, ml.x, ml.y, O);
       }
       if (seg_end < sp.end) publish_q();
       named_barrier_sync(1, kConsumerWarps * 32);  // merge buffers and q free again
