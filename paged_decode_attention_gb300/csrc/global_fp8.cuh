@@ -210,11 +210,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     int st[NP];
 #pragma unroll
     for (int j = 0; j < NP; ++j) st[j] = (i + j) % kStages;
-    if (ok) {  // lane j waits for page j: one wait's latency for both
-      ok = __all_sync(0xffffffffu,
-                      lane >= NP || mbar_wait_fast(&s.full[(i + lane) % kStages], ((i + lane) / kStages) & 1));
-      if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+    // lane j waits for page j (one wait's latency for both), and the barrier of the
+    // warp hands on what it sees: a vote would order no memory.  (ok is a lane's own:
+    // a wait that runs out is reported by its lane and ends that lane's waits.)
+    if (ok && lane < NP) {
+      ok = mbar_wait_fast(&s.full[(i + lane) % kStages], ((i + lane) / kStages) & 1);
+      if (!ok) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
     }
+    __syncwarp();
 
     // ---- every page's logits over this warp's dims ----
     float sc[NP][2][2][4];  // page, n-tile, even / odd k-steps
