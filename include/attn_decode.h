@@ -244,6 +244,15 @@ int32_t attn_decode_global_shared(const void* q, const void* kv_pool, const void
  * status        as for attn_decode_global; a prefix_len outside its range
  *               raises ATTN_DEV_BAD_SEQ_LEN and is clamped
  *
+ * The keys are taken as they are cached.  The prefix's own tokens enter by
+ * attn_kv_append_global_chunk with prefix_table as the table of one sequence;
+ * a sequence's own by attn_kv_append_global_prefix, which rotates them behind
+ * the prefix whatever its length.  attn_prefill_global, for prompts behind the
+ * prefix, takes tables that list the prefix's pages in front of the sequence's
+ * own and lengths with the prefix's, so the prefix has to fill its pages then:
+ * share its whole pages and give every sequence the rest as its first own
+ * tokens.
+ *
  * Every array 16 bytes aligned (prefix_table, prefix_len 4).  Three kernels
  * with spans, one or two without.
  * Weights are rounded to bf16 for their product with the values.
@@ -419,6 +428,23 @@ int32_t attn_kv_append_global_chunk(const void* qkv, const void* w_q, const void
                                     const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
                                     void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
                                     int64_t num_pages, int32_t* status, void* stream);
+
+/*
+ * attn_kv_append_global_prefix -- attn_kv_append_global_chunk for the own
+ * tokens of sequences behind a shared prefix (attn_decode_global_prefix): the
+ * token at own position i goes into page block_table[b][i / 16], row i % 16,
+ * where that call looks for it, and its query and key are rotated at position
+ * prefix_len + i, where it stands.
+ *
+ * prefix_len   int32 [1] (device), 0 .. ATTN_MAX_SEQ_LEN, 4 bytes aligned;
+ *              outside, ATTN_DEV_BAD_SEQ_LEN and nothing is written
+ * seq_lens     own tokens, new ones included
+ * Every other argument is attn_kv_append_global_chunk's; k_pool is required.
+ */
+int32_t attn_kv_append_global_prefix(const void* qkv, const void* w_q, const void* w_k, const int32_t* prefix_len,
+                                     const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                                     void* q_out, void* k_pool, void* v_pool, int32_t batch, int32_t total_q,
+                                     int32_t max_blocks, int64_t num_pages, int32_t* status, void* stream);
 
 /*
  * attn_prefill_sliding / attn_prefill_global -- multi-query attention over the

@@ -115,6 +115,11 @@ int32_t attn_step_add_kv_append_global_chunk(attn_step* step, const void* qkv, c
                                              const int32_t* cu_q, void* q_out, void* k_pool, void* v_pool,
                                              int32_t batch, int32_t total_q, int32_t max_blocks, int64_t num_pages,
                                              int32_t* status);
+int32_t attn_step_add_kv_append_global_prefix(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+                                              const int32_t* prefix_len, const int32_t* block_table,
+                                              const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
+                                              void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
+                                              int64_t num_pages, int32_t* status);
 int32_t attn_step_add_kv_append_sliding_fp8(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
                                             const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
                                             void* q_out, void* k_pool, void* v_pool, uint8_t* k_scale,

@@ -16,7 +16,8 @@ power-of-two scales; ``include/attn_fp8.h``) is written by
 ``attn_kv_append_{sliding,global}_fp8``, decoded over by
 ``attn_decode_{sliding,global}_fp8`` and read back into bf16 pages by
 ``attn_kv_read_{sliding,global}_fp8``; ``new_fp8_cache`` allocates one.
-``attn_decode_global_prefix`` decodes a batch behind a prefix that it shares.
+``attn_decode_global_prefix`` decodes a batch behind a prefix that it shares
+(``prefix_len`` of ``attn_kv_append_global_chunk`` appends there).
 
 Streams.  A call works on ``stream`` (default: the current one of its device),
 and what it makes for itself, outputs and workspaces not given, is made on that
@@ -74,7 +75,7 @@ EXPORTS = ("attn_decode_sliding", "attn_decode_global", "attn_decode_global_shar
            "attn_step_add_decode_global_fp8", "attn_decode_global_prefix", "attn_decode_prefix_plan",
            "attn_decode_prefix_workspace_size", "attn_step_add_decode_global_prefix",
            "attn_step_add_kv_read_sliding_fp8", "attn_step_add_kv_read_global_fp8", "attn_decode_fp8_plan",
-           "attn_decode_fp8_workspace_size")
+           "attn_decode_fp8_workspace_size", "attn_kv_append_global_prefix", "attn_step_add_kv_append_global_prefix")
 # attn_step launch modes (attn_step.h)
 STEP_LAUNCH_AUTO, STEP_LAUNCH_GRAPH, STEP_LAUNCH_DIRECT = 0, 1, 2
 STEP_LAUNCH_MODES = {"auto": STEP_LAUNCH_AUTO, "graph": STEP_LAUNCH_GRAPH, "direct": STEP_LAUNCH_DIRECT}
@@ -136,6 +137,7 @@ def load(path=None):
         fn.argtypes = pre
     chunk = [c_vp] * 9 + [c_i32, c_i32, c_i32, c_i64, c_vp, c_vp]  # qkv w_q w_k block_table seq_lens cu_q q_out k_pool
     #                                v_pool; batch total_q max_blocks num_pages status stream
+    chunk_behind = [c_vp] + chunk                                   # prefix_len after w_k
     chunk8 = [c_vp] * 11 + chunk[9:]                                # ... and k_scale v_scale after v_pool
     read8 = [c_vp] * 9 + [c_i32, c_i32, c_i64, c_i64, c_i32, c_i32, c_vp, c_vp]  # k_pool v_pool k_scale v_scale
     #            block_table seq_lens k_out v_out out_table; batch max_blocks num_pages out_pages max_seq_len span ...
@@ -154,6 +156,7 @@ def load(path=None):
     lib.attn_decode_prefix_workspace_size.restype = c_sz
     lib.attn_decode_prefix_workspace_size.argtypes = [c_i32] * 5
     for names, types in ((("attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk"), chunk),
+                         (("attn_kv_append_global_prefix",), chunk_behind),
                          (("attn_kv_append_sliding_fp8", "attn_kv_append_global_fp8"), chunk8),
                          (("attn_kv_read_sliding_fp8", "attn_kv_read_global_fp8"), read8),
                          (("attn_decode_sliding_fp8", "attn_decode_global_fp8"), call8),
@@ -839,19 +842,25 @@ def _kind_name(kind):
     return "sliding" if kind == KIND_SLIDING else "global"
 
 
-def _chunk_args(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out=None, *, status=None):
+def _chunk_args(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out=None, *, prefix_len=None,
+                status=None):
     """(fn_name, args without the stream, tensors to keep, output, device, tensors made) of a chunk append."""
     _, Hkv, D = SHAPES[kind]
     given = (q_out,)
     ptrs, q_out, batch, total_q, max_blocks = _append_common(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out)
     _dims(v_pool, 4, "v_pool must be [num_pages, 16, %d, %d]" % (Hkv, D))
     n = v_pool.shape[0]
-    k_ptr = None if k_pool is None and kind == KIND_GLOBAL else \
+    if prefix_len is not None and kind != KIND_GLOBAL:
+        raise ValueError("prefix_len is for global layers")
+    k_ptr = None if k_pool is None and kind == KIND_GLOBAL and prefix_len is None else \
         _ptr(k_pool, "k_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D))
-    keep = (qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, status)
+    keep = (qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, prefix_len, status)
     device = _one_device(keep)
     args = tuple(ptrs) + (k_ptr, _ptr(v_pool, "v_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D)), batch, total_q,
                           max_blocks, n, _status_ptr(status))
+    if prefix_len is not None:
+        args = args[:3] + (_ptr(prefix_len, "prefix_len", torch.int32, (1,)),) + args[3:]
+        return "attn_kv_append_global_prefix", args, keep, q_out, device, _made(given, (q_out,))
     return "attn_kv_append_%s_chunk" % _kind_name(kind), args, keep, q_out, device, _made(given, (q_out,))
 
 
@@ -1029,10 +1038,14 @@ def attn_kv_append_sliding_chunk(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_p
 
 
 def attn_kv_append_global_chunk(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out=None, *,
-                                status=None, stream=None):
-    """attn_kv_append_sliding_chunk for global layers: qkv [T, 8704]; k_pool may be None (values-only cache)."""
+                                prefix_len=None, status=None, stream=None):
+    """attn_kv_append_sliding_chunk for global layers: qkv [T, 8704]; k_pool may be None (values-only cache).
+
+    prefix_len (int32 [1]): the sequences stand behind a shared prefix of that many positions, for
+    attn_decode_global_prefix: block_table and seq_lens are their own, tokens are rotated at prefix_len + position.
+    """
     return _once(stream, _chunk_args, KIND_GLOBAL, qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, q_out,
-                 status=status)
+                 prefix_len=prefix_len, status=status)
 
 
 def attn_kv_append_sliding_fp8(qkv, w_q, w_k, block_table, seq_lens, cu_q, k_pool, v_pool, k_scale, v_scale,

@@ -5,8 +5,10 @@
 // Token t of the packed chunk belongs to the sequence b with
 // cu_q[b] <= t < cu_q[b+1] and sits at position
 //   pos = seq_lens[b] - (cu_q[b+1] - cu_q[b]) + (t - cu_q[b]),
-// the convention of the multi-query attention (prefill_tc.cuh).  Per head row
-// x of the token:
+// the convention of the multi-query attention (prefill_tc.cuh).  Behind a shared
+// prefix (prefix.cuh) a sequence's own positions are numbered from 0, which is
+// where the cache row goes, and turned by prefix_len + pos.  Per head row x of the
+// token:
 //   q and k:  rope(x / sqrt(sum_j x[j]^2 / D + eps) * w, pos)
 //   v:        x / sqrt(sum_j x[j]^2 / D + eps)
 //
@@ -53,6 +55,7 @@ struct ChunkParams {
   const int32_t* block_table;  // [batch, max_blocks]
   const int32_t* seq_lens;     // [batch], new tokens included
   const int32_t* cu_q;         // [batch + 1]
+  const int32_t* prefix_len;   // one int32 on the device, added to every angle's position; null: 0
   __nv_bfloat16* q_out;        // [total_q, Hq, D]
   void* k_pool;                // [num_pages, 16, Hkv, D] bf16 or e4m3; null: values-only global cache (bf16)
   void* v_pool;
@@ -278,13 +281,14 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
   // or the tables, or reading the cache.
   wait_for_primary_grid();
   allow_dependent_launch();
-  bool decreasing = false;
+  const int base = p.prefix_len != nullptr ? *p.prefix_len : 0;
+  bool refused = base < 0 || base > ATTN_MAX_SEQ_LEN;
   for (int i = threadIdx.x; i <= p.batch; i += kThreads<kShared>) {
     const int q0 = p.cu_q[i];
     s.cu_q[i] = q0;
     if (i < p.batch) {
       s.len[i] = p.seq_lens[i];
-      decreasing |= p.cu_q[i + 1] < q0;
+      refused |= p.cu_q[i + 1] < q0;
     }
   }
   const bool has_kv = !kShared || warp == kQWarps;
@@ -293,8 +297,8 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
   if constexpr (!kShared) load_raw<kD>(p.w_k, wk_raw);
   // Where cu_q decreases, sequences overlap or run backwards: a token found by
   // counting ends may lie behind its sequence, at a position beyond the table.
-  // The call is left alone as a whole.
-  if (__syncthreads_or(decreasing)) {
+  // The call is left alone as a whole, as for a prefix of no length.
+  if (__syncthreads_or(refused)) {
     if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
     return;
   }
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
         }
       }
       if (threadIdx.x < kPairs)
-        sincos_at(freq, pos < 0 ? 0 : pos, &s.sin[buf][threadIdx.x], &s.cos[buf][threadIdx.x]);
+        sincos_at(freq, pos < 0 ? 0 : base + pos, &s.sin[buf][threadIdx.x], &s.cos[buf][threadIdx.x]);
       __syncthreads();  // one per token: the buffer written next was read before this barrier
       const float* cs = s.cos[buf];
       const float* sn = s.sin[buf];

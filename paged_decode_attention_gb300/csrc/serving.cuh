@@ -127,21 +127,26 @@ int32_t make_whole_plan(Serving call, int32_t batch, int32_t max_seq_len, int32_
 // ---------------------------------------------------------------------------
 // Norms, RoPE and cache append of a chunk of tokens per sequence
 // ---------------------------------------------------------------------------
-int32_t run_chunk(int32_t kind, bool fp8, const void* qkv, const void* w_q, const void* w_k,
+enum class Chunk { kBf16, kFp8, kBehindPrefix };
+
+int32_t run_chunk(int32_t kind, Chunk form, const void* qkv, const void* w_q, const void* w_k, const int32_t* prefix_len,
                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
                   void* v_pool, uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q, int32_t max_blocks,
                   int64_t num_pages, int32_t* status, void* stream) {
   g_err[0] = '\0';
   const bool sliding = kind == ATTN_KIND_SLIDING;
-  const char* name = fp8 ? (sliding ? "attn_kv_append_sliding_fp8" : "attn_kv_append_global_fp8")
-                         : (sliding ? "attn_kv_append_sliding_chunk" : "attn_kv_append_global_chunk");
-  const bool values_only = !sliding && !fp8;  // may leave the keys out
+  const bool fp8 = form == Chunk::kFp8, behind = form == Chunk::kBehindPrefix;
+  const char* name = fp8      ? (sliding ? "attn_kv_append_sliding_fp8" : "attn_kv_append_global_fp8")
+                     : behind ? "attn_kv_append_global_prefix"
+                              : (sliding ? "attn_kv_append_sliding_chunk" : "attn_kv_append_global_chunk");
+  const bool values_only = !sliding && form == Chunk::kBf16;  // may leave the keys out
   if (!w_q || !w_k || !block_table || !seq_lens || !cu_q || (total_q > 0 && (!qkv || !q_out)) ||
-      (!k_pool && !values_only) || !v_pool || (fp8 && (!k_scale || !v_scale)))
+      (!k_pool && !values_only) || !v_pool || (fp8 && (!k_scale || !v_scale)) || (behind && !prefix_len))
     return fail(ATTN_ERR_INVALID_ARG, "%s: null pointer argument", name);
   if (!aligned_to(qkv, 16) || !aligned_to(w_q, 16) || !aligned_to(w_k, 16) || !aligned_to(q_out, 16) ||
       !aligned_to(k_pool, 16) || !aligned_to(v_pool, 16) || !aligned_to(k_scale, 16) || !aligned_to(v_scale, 16) ||
-      !aligned_to(block_table, 4) || !aligned_to(seq_lens, 4) || !aligned_to(cu_q, 4) || !aligned_to(status, 4))
+      !aligned_to(prefix_len, 4) || !aligned_to(block_table, 4) || !aligned_to(seq_lens, 4) || !aligned_to(cu_q, 4) ||
+      !aligned_to(status, 4))
     return fail(ATTN_ERR_INVALID_ARG, "%s: misaligned pointer (qkv, w_q, w_k, q_out, pools and scales 16 bytes, "
                 "tables 4)", name);
   int32_t st;
@@ -163,6 +168,7 @@ int32_t run_chunk(int32_t kind, bool fp8, const void* qkv, const void* w_q, cons
   p.block_table = block_table;
   p.seq_lens = seq_lens;
   p.cu_q = cu_q;
+  p.prefix_len = prefix_len;
   p.q_out = static_cast<__nv_bfloat16*>(q_out);
   p.k_pool = k_pool;
   p.v_pool = v_pool;
@@ -701,32 +707,40 @@ int32_t attn_kv_append_sliding_chunk(const void* qkv, const void* w_q, const voi
                                      const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
                                      void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
                                      int64_t num_pages, int32_t* status, void* stream) {
-  return run_chunk(ATTN_KIND_SLIDING, false, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, nullptr,
-                   nullptr, batch, total_q, max_blocks, num_pages, status, stream);
+  return run_chunk(ATTN_KIND_SLIDING, Chunk::kBf16, qkv, w_q, w_k, nullptr, block_table, seq_lens, cu_q, q_out, k_pool,
+                   v_pool, nullptr, nullptr, batch, total_q, max_blocks, num_pages, status, stream);
 }
 
 int32_t attn_kv_append_global_chunk(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
                                     const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
                                     void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
                                     int64_t num_pages, int32_t* status, void* stream) {
-  return run_chunk(ATTN_KIND_GLOBAL, false, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, nullptr,
-                   nullptr, batch, total_q, max_blocks, num_pages, status, stream);
+  return run_chunk(ATTN_KIND_GLOBAL, Chunk::kBf16, qkv, w_q, w_k, nullptr, block_table, seq_lens, cu_q, q_out, k_pool,
+                   v_pool, nullptr, nullptr, batch, total_q, max_blocks, num_pages, status, stream);
+}
+
+int32_t attn_kv_append_global_prefix(const void* qkv, const void* w_q, const void* w_k, const int32_t* prefix_len,
+                                     const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                                     void* q_out, void* k_pool, void* v_pool, int32_t batch, int32_t total_q,
+                                     int32_t max_blocks, int64_t num_pages, int32_t* status, void* stream) {
+  return run_chunk(ATTN_KIND_GLOBAL, Chunk::kBehindPrefix, qkv, w_q, w_k, prefix_len, block_table, seq_lens, cu_q, q_out,
+                   k_pool, v_pool, nullptr, nullptr, batch, total_q, max_blocks, num_pages, status, stream);
 }
 
 int32_t attn_kv_append_sliding_fp8(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
                                    const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
                                    void* v_pool, uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q,
                                    int32_t max_blocks, int64_t num_pages, int32_t* status, void* stream) {
-  return run_chunk(ATTN_KIND_SLIDING, true, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, k_scale,
-                   v_scale, batch, total_q, max_blocks, num_pages, status, stream);
+  return run_chunk(ATTN_KIND_SLIDING, Chunk::kFp8, qkv, w_q, w_k, nullptr, block_table, seq_lens, cu_q, q_out, k_pool,
+                   v_pool, k_scale, v_scale, batch, total_q, max_blocks, num_pages, status, stream);
 }
 
 int32_t attn_kv_append_global_fp8(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
                                   const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool, void* v_pool,
                                   uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q,
                                   int32_t max_blocks, int64_t num_pages, int32_t* status, void* stream) {
-  return run_chunk(ATTN_KIND_GLOBAL, true, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out, k_pool, v_pool, k_scale,
-                   v_scale, batch, total_q, max_blocks, num_pages, status, stream);
+  return run_chunk(ATTN_KIND_GLOBAL, Chunk::kFp8, qkv, w_q, w_k, nullptr, block_table, seq_lens, cu_q, q_out, k_pool,
+                   v_pool, k_scale, v_scale, batch, total_q, max_blocks, num_pages, status, stream);
 }
 
 int32_t attn_kv_read_sliding_fp8(const void* k_pool, const void* v_pool, const uint8_t* k_scale, const uint8_t* v_scale,

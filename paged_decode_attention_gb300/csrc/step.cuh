@@ -158,6 +158,15 @@ int32_t attn_step_add_kv_append_global_chunk(attn_step* step, const void* qkv, c
   }, "attn_step_add_kv_append_global_chunk");
 }
 
+int32_t attn_step_add_kv_append_global_prefix(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+    const int32_t* prefix_len, const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* q_out,
+    void* k_pool, void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks, int64_t num_pages, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_kv_append_global_prefix(qkv, w_q, w_k, prefix_len, block_table, seq_lens, cu_q, q_out, k_pool, v_pool,
+        batch, total_q, max_blocks, num_pages, status, s);
+  }, "attn_step_add_kv_append_global_prefix");
+}
+
 int32_t attn_step_add_kv_append_global_fp8(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
     const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool, void* v_pool,
     uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q, int32_t max_blocks, int64_t num_pages, int32_t* status) {
