@@ -94,7 +94,8 @@ int32_t make_serving_plan(int32_t kind, int32_t batch, int32_t max_seq_len, int3
 //     of 16 19.2 and 10.3, of 512 58.2 and 36.0;
 //   8-bit, sliding: 1 of 128 6.6 and 6.0; 4 of 256 8.2 and 9.6; 32 of 128 13.1 and 8.2;
 //     64 of 64 13.7 and 12.3, of 128 15.5 and 15.9; 128 of 32 14.3 and 19.7 (the
-//     blocks of 57 sequences are resident at once);
+//     blocks of 57 sequences are resident at once on 152 SMs, which is the limit
+//     taken: a second wave wins for the shortest only);
 //   bf16 behind a prefix, both in one list: 1 of 32 positions 6.3 and 4.8, of 80 8.1
 //     and 10.4; 4 of 56 8.4 and 7.7, of 128 7.9 and 9.8; 16 of 128 12.0 and 10.9; 32 of
 //     120 16.8 and 12.2.
@@ -102,9 +103,10 @@ int32_t make_serving_plan(int32_t kind, int32_t batch, int32_t max_seq_len, int3
 // has eight for every page of the longest.
 enum class Serving { kSlidingFp8, kGlobalFp8, kJoined };
 
-int64_t whole_pages(Serving call, int32_t batch) {
+int64_t whole_pages(Serving call, int32_t batch, int32_t num_sms) {
   switch (call) {
-    case Serving::kSlidingFp8: return batch <= 57 ? 8 : 0;
+    case Serving::kSlidingFp8:
+      return batch <= static_cast<int64_t>(num_sms) * pda::sliding::kBlocksPerSm / ATTN_SLIDING_HKV ? 8 : 0;
     case Serving::kGlobalFp8: return batch >= 64 ? std::max(16, batch / 8) : batch >= 4 ? 8 : 4;
     default: return batch >= 16 ? 8 : 4;
   }
@@ -116,7 +118,7 @@ int32_t make_whole_plan(Serving call, int32_t batch, int32_t max_seq_len, int32_
   const int32_t kind = call == Serving::kSlidingFp8 ? ATTN_KIND_SLIDING : ATTN_KIND_GLOBAL;
   const int32_t st = make_serving_plan(kind, batch, max_seq_len, window, forced_blocks, num_sms, out);
   if (st != ATTN_OK) return st;
-  *whole = forced_blocks == 0 && visible_pages_bound(max_seq_len, window) <= whole_pages(call, batch);
+  *whole = forced_blocks == 0 && visible_pages_bound(max_seq_len, window) <= whole_pages(call, batch, num_sms);
   if (*whole) {
     out->grid_x = batch;
     out->merge_in_grid = true;  // (nothing to merge)
