@@ -219,8 +219,10 @@ int32_t attn_decode_global_shared(const void* q, const void* kv_pool, const void
  *   o[b,h] = sum over both of softmax_l( <q[b,h], k_l> ) * v_l,
  *
  * what attn_decode_global computes with the prefix's pages listed in front of
- * every sequence's own, but the prefix's pages are read once for the whole
- * batch, with its products on the tensor cores as one matrix product.
+ * every sequence's own.  For a long prefix the prefix's pages are read once for
+ * the whole batch, with its products on the tensor cores as one matrix product;
+ * behind a short one, or in a batch of one or two, each sequence reads them for
+ * itself (prefix_splits).
  *
  * q             bf16 [batch, 16, 512]
  * k_pool, v_pool  bf16 [num_pages, 16, 1, 512]: prefix and own pages

@@ -23,8 +23,11 @@
 //
 // Warp w of the first eight takes q heads 2w and 2w+1, on sliding layers also key
 // head w and value head w; on global layers a ninth warp takes the head that is
-// key and value.  8192 sliding tokens: 43.2 us, 0.92 of the measured copy rate;
-// 4096 global tokens into an 8-bit cache 23.6 us, 0.89.  Slower, on the latter:
+// key and value.  8192 sliding tokens: 43.7 us, 0.90 of the measured copy rate;
+// 4096 global tokens into an 8-bit cache 24.3 us, 0.86 (8192: 45.3, 0.93); 8192
+// sliding tokens into an 8-bit cache 44.2 us, 0.78: 14 % fewer bytes than into a
+// bf16 one, but two more reductions and the conversions in a token's chain.
+// Slower, on 4096 global tokens at 23.6 us (before the tests for rows beyond range):
 // the shared head as a second job of one of eight warps, for which the others
 // wait at the barrier (27.0 us with two tokens a round, 31.5 with one), two tokens
 // a round of the nine warps (25.2; 608 tokens 4.1 us against 5.1, more than three

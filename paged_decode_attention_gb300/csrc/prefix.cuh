@@ -4,8 +4,15 @@
 //   o[b,h] = sum over prefix and own positions l of softmax_l(<q[b,h], k_l>) v_l
 //
 // The softmax over the union is regrouped exactly from partial results (O, m,
-// sum) as in combine.cuh.  Three kernels (short prefixes and small batches take
-// joined.cuh's way):
+// sum) as in combine.cuh; sums, maxima and partial outputs are fp32.  The weights
+// are rounded to bf16 for their product with the values, here and in joined.cuh,
+// because the tensor cores take two operands of one type and the values are bf16
+// (in f16 one outside 2^-14 .. 2^16 would lose bits); a second product for the
+// rest of the weights would double the time of P V.  64 sequences behind 32768
+// positions: 0.0023 off the 64-bit result (2-norm, bf16 outputs), where unrounded
+// weights leave 0.0017, the rounding of the outputs alone.
+//
+// Three kernels (short prefixes and small batches take joined.cuh's way):
 //   * the prefix as a multi-query attention whose queries are the batch's
 //     sequences (prefill_pair.cuh with PrefixParams): its pages are read once
 //     for 16 sequences x 16 heads instead of once per sequence, and the
@@ -73,8 +80,10 @@ __global__ void __launch_bounds__(kMergeGroups* kDims / 4) merge_kernel(const __
   const size_t row = static_cast<size_t>(b) * Hq + h;
 
   // The schedule: weighted pages before sequence b, its own pages, the weighted
-  // total (common.cuh).  The kernel ahead lets this one launch only after its
-  // own wait, so the lengths are final and visible already.
+  // total (common.cuh).  The lengths are final and visible already: the kernel
+  // ahead lets this one launch only after its own wait, or, where it is the own
+  // positions' and does not wait, was itself let launch by the prefix kernel after
+  // that one's wait.
   if (threadIdx.x < kSched) {
     int before = 0, mine = 0, total = 0;
     for (int j = threadIdx.x; j < p.batch; j += kSched) {

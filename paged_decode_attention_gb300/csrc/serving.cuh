@@ -57,9 +57,14 @@ int64_t visible_pages_bound(int32_t max_len, int32_t window) {
 // Launch plan of the 8-bit decode and of the own positions behind a prefix:
 // make_plan's, but for the smallest spans.  A sequence that a block starts costs
 // it some 2 us (its q, its end), so many short sequences want a block each: the
-// grid covers the weighted list (a virtual page per sequence, common.cuh), and
-// spans go down to two pages.  A span cut off a long sequence costs the merge a
-// partial row, so where a sequence may have many pages the spans stay longer.
+// grid has a virtual page per sequence in its count, and the smallest span is two
+// pages.  A span cut off a long sequence costs the merge a partial row, so where a
+// sequence may have many pages the smallest is longer.
+// The kernels cut by the weights of their own parameters (4, sliding 12, fp8.cuh),
+// which were measured on these grids: spans come out longer and some blocks find
+// virtual pages only (global layers, one sequence of 250 pages: 63 blocks, spans
+// of 5, 51 at work).  Likewise merge_in_grid is make_plan's, for its own spans: a
+// choice between two ways of merging, either of which is right for any schedule.
 // Global layers, automatic plan, two-page and four-page spans: 30 sequences of up
 // to 15 positions 7.9 and 11.7 us (19.0 with make_plan's four pages per block), 4 of
 // up to 600 8.2 and 10.9 us, one of 4000 11.0 and 9.3 us.
@@ -460,7 +465,8 @@ constexpr int kMaxPrefixSplits = 128;
 // and 19.5, 8000 24.2 and 24.6, 10500 28.6 and 26.5; 12 of 2000 15.9 and 20.2,
 // 6500 27.6 and 23.4; 16 of 1000 16.5 and 19.2, 3000 24.1 and 21.4; 24 of 500 18.2
 // and 20.4, 2500 27.9 and 22.7; 32 of 100 17.8 and 19.8, 500 21.7 and 20.6.  The
-// rule runs through the crossings.
+// rule runs through the crossings of 8 to 32 sequences; for 3, and 4 as far as
+// measured, it takes spans before the crossing (3 from 61923 positions on).
 bool join_prefix(int32_t batch, int32_t max_prefix_len) {
   return batch <= 2 || static_cast<int64_t>(batch) * batch * (static_cast<int64_t>(max_prefix_len) + 300) <= 560000;
 }
