@@ -96,9 +96,9 @@ int32_t make_plan(int32_t kind, int32_t batch, int32_t max_seq_len, int32_t wind
   const int min_pages = sliding ? pda::sliding::kMinPages : pda::global::kMinPages;
 
   // visible pages of one sequence, at most
-  int64_t max_pages = (max_seq_len + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE;
+  int64_t max_pages = (static_cast<int64_t>(max_seq_len) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE;
   if (window > 0) {
-    const int64_t wpages = (window + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE + 1;
+    const int64_t wpages = (static_cast<int64_t>(window) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE + 1;
     if (wpages < max_pages) max_pages = wpages;
   }
   const int64_t total_max = max_pages * batch;
