@@ -162,6 +162,46 @@ int32_t attn_step_add_decode_global_prefix(attn_step* step, const void* q, const
                                            int32_t out_dtype, int32_t num_splits, int32_t prefix_splits,
                                            void* workspace, size_t workspace_bytes, int32_t* status);
 
+/* A step that verifies drafted tokens (attn_tree.h).  The host arrays of pool
+ * pointers of a commit are copied. */
+int32_t attn_step_add_decode_sliding_tree(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
+                                          const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                                          const int32_t* parents, void* o, int32_t batch, int32_t total_q,
+                                          int32_t max_q, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len,
+                                          int32_t window, int32_t out_dtype, int32_t num_splits, void* workspace,
+                                          size_t workspace_bytes, int32_t* status);
+int32_t attn_step_add_decode_global_tree(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
+                                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                                         const int32_t* parents, void* o, int32_t batch, int32_t total_q,
+                                         int32_t max_q, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len,
+                                         int32_t window, int32_t out_dtype, int32_t num_splits, void* workspace,
+                                         size_t workspace_bytes, int32_t* status);
+int32_t attn_step_add_kv_append_sliding_tree(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+                                             const int32_t* block_table, const int32_t* seq_lens,
+                                             const int32_t* cu_q, const int32_t* parents, void* q_out, void* k_pool,
+                                             void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
+                                             int64_t num_pages, int32_t* status);
+int32_t attn_step_add_kv_append_global_tree(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+                                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                                            const int32_t* parents, void* q_out, void* k_pool, void* v_pool,
+                                            int32_t batch, int32_t total_q, int32_t max_blocks, int64_t num_pages,
+                                            int32_t* status);
+int32_t attn_step_add_kv_commit_sliding(attn_step* step, const void* const* k_pools, const void* const* v_pools,
+                                        int32_t layers, const int32_t* block_table, const int32_t* seq_lens,
+                                        const int32_t* cu_q, const int32_t* path, const int32_t* path_len,
+                                        int32_t* new_lens, int32_t batch, int32_t max_path, int32_t max_blocks,
+                                        int64_t num_pages, int32_t* status);
+int32_t attn_step_add_kv_commit_global(attn_step* step, const void* const* k_pools, const void* const* v_pools,
+                                       int32_t layers, const int32_t* block_table, const int32_t* seq_lens,
+                                       const int32_t* cu_q, const int32_t* path, const int32_t* path_len,
+                                       int32_t* new_lens, int32_t batch, int32_t max_path, int32_t max_blocks,
+                                       int64_t num_pages, int32_t* status);
+int32_t attn_step_add_pages_assign(attn_step* step, const int32_t* cached_lens, const int32_t* new_tokens,
+                                   int32_t* block_table, const int32_t* held, int32_t* free_list,
+                                   const int32_t* free_state, int32_t* held_out, int32_t* free_state_out,
+                                   int32_t* seq_lens, int32_t* cu_q, int32_t batch, int32_t max_blocks,
+                                   int64_t num_pages, int32_t window, int32_t* status);
+
 /* Calls recorded so far, and kernels they launch per step. */
 int32_t attn_step_num_calls(const attn_step* step);
 int32_t attn_step_num_kernels(const attn_step* step);

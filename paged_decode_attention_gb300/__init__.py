@@ -19,6 +19,12 @@ power-of-two scales; ``include/attn_fp8.h``) is written by
 ``attn_decode_global_prefix`` decodes a batch behind a prefix that it shares
 (``prefix_len`` of ``attn_kv_append_global_chunk`` appends there).
 
+A step that verifies a tree of drafted tokens per sequence
+(``include/attn_tree.h``) is ``attn_pages_assign`` (block tables and lengths on
+the GPU; ``new_page_state`` makes the state),
+``attn_kv_append_{sliding,global}_tree`` and ``attn_decode_{sliding,global}_tree``
+in every layer, and ``attn_kv_commit_{sliding,global}`` with the accepted paths.
+
 Streams.  A call works on ``stream`` (default: the current one of its device),
 and what it makes for itself, outputs and workspaces not given, is made on that
 stream too.  A prepared call or a step makes its own when it is constructed, on
@@ -46,6 +52,11 @@ __all__ = [
     "prepare_kv_append_sliding_chunk", "prepare_kv_append_global_chunk", "prepare_kv_append_sliding_fp8",
     "prepare_kv_append_global_fp8", "prepare_kv_read_sliding_fp8", "prepare_kv_read_global_fp8",
     "prepare_decode_sliding_fp8", "prepare_decode_global_fp8",
+    "attn_decode_sliding_tree", "attn_decode_global_tree", "attn_decode_tree_plan", "attn_decode_tree_workspace_size",
+    "attn_kv_append_sliding_tree", "attn_kv_append_global_tree", "attn_kv_commit_sliding", "attn_kv_commit_global",
+    "attn_pages_assign", "new_page_state", "prepare_decode_sliding_tree", "prepare_decode_global_tree",
+    "prepare_kv_append_sliding_tree", "prepare_kv_append_global_tree", "prepare_kv_commit_sliding",
+    "prepare_kv_commit_global", "prepare_pages_assign", "MAX_TREE", "DEV_BAD_TREE", "DEV_NO_PAGES",
     "attn_last_error", "load", "library_path", "AttnDecodeError",
     "KIND_SLIDING", "KIND_GLOBAL", "DEV_WAIT_TIMEOUT", "DEV_BAD_PAGE", "DEV_BAD_SEQ_LEN",
 ]
@@ -56,6 +67,8 @@ ERROR_NAMES = {1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ER
 OUT_BF16, OUT_F32 = 0, 1
 KIND_SLIDING, KIND_GLOBAL = 0, 1
 DEV_WAIT_TIMEOUT, DEV_BAD_PAGE, DEV_BAD_SEQ_LEN, DEV_INTERNAL = 1, 2, 4, 8
+DEV_BAD_TREE, DEV_NO_PAGES = 16, 32
+MAX_TREE = 64  # ATTN_MAX_TREE: nodes of a sequence's tree of drafted tokens
 PAGE_SIZE = 16
 WORKSPACE_ZERO_BYTES = 8192  # ATTN_WORKSPACE_ZERO_BYTES: zero before a workspace's first use, kept zero
 SHAPES = {KIND_SLIDING: (16, 8, 256), KIND_GLOBAL: (16, 1, 512)}  # Hq, Hkv, D
@@ -75,7 +88,13 @@ EXPORTS = ("attn_decode_sliding", "attn_decode_global", "attn_decode_global_shar
            "attn_step_add_decode_global_fp8", "attn_decode_global_prefix", "attn_decode_prefix_plan",
            "attn_decode_prefix_workspace_size", "attn_step_add_decode_global_prefix",
            "attn_step_add_kv_read_sliding_fp8", "attn_step_add_kv_read_global_fp8", "attn_decode_fp8_plan",
-           "attn_decode_fp8_workspace_size", "attn_kv_append_global_prefix", "attn_step_add_kv_append_global_prefix")
+           "attn_decode_fp8_workspace_size", "attn_kv_append_global_prefix", "attn_step_add_kv_append_global_prefix",
+           "attn_decode_tree_plan", "attn_decode_tree_workspace_size", "attn_decode_sliding_tree",
+           "attn_decode_global_tree", "attn_kv_append_sliding_tree", "attn_kv_append_global_tree",
+           "attn_kv_commit_sliding", "attn_kv_commit_global", "attn_pages_assign",
+           "attn_step_add_decode_sliding_tree", "attn_step_add_decode_global_tree",
+           "attn_step_add_kv_append_sliding_tree", "attn_step_add_kv_append_global_tree",
+           "attn_step_add_kv_commit_sliding", "attn_step_add_kv_commit_global", "attn_step_add_pages_assign")
 # attn_step launch modes (attn_step.h)
 STEP_LAUNCH_AUTO, STEP_LAUNCH_GRAPH, STEP_LAUNCH_DIRECT = 0, 1, 2
 STEP_LAUNCH_MODES = {"auto": STEP_LAUNCH_AUTO, "graph": STEP_LAUNCH_GRAPH, "direct": STEP_LAUNCH_DIRECT}
@@ -155,7 +174,24 @@ def load(path=None):
     lib.attn_decode_fp8_workspace_size.argtypes = [c_i32] * 5
     lib.attn_decode_prefix_workspace_size.restype = c_sz
     lib.attn_decode_prefix_workspace_size.argtypes = [c_i32] * 5
-    for names, types in ((("attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk"), chunk),
+    tree = [c_vp] * 8 + [c_i32] * 4 + [c_i64] + [c_i32] * 4 + [c_vp, c_sz, c_vp, c_vp]  # q k_pool v_pool block_table
+    #      seq_lens cu_q parents o; batch total_q max_q max_blocks num_pages max_seq_len window out_dtype num_splits
+    #      workspace workspace_bytes status stream
+    chunk_tree = [c_vp] + chunk                                     # parents after cu_q
+    commit = [c_vp, c_vp, c_i32] + [c_vp] * 6 + [c_i32, c_i32, c_i32, c_i64, c_vp, c_vp]  # k_pools v_pools; layers;
+    #        block_table seq_lens cu_q path path_len new_lens; batch max_path max_blocks num_pages status stream
+    assign = [c_vp] * 10 + [c_i32, c_i32, c_i64, c_i32, c_vp, c_vp]  # cached_lens new_tokens block_table held free_list
+    #        free_state held_out free_state_out seq_lens cu_q; batch max_blocks num_pages window status stream
+    lib.attn_decode_tree_plan.restype = c_i32
+    lib.attn_decode_tree_plan.argtypes = [c_i32] * 7 + [ctypes.POINTER(c_i32), ctypes.POINTER(c_i32),
+                                                        ctypes.POINTER(c_sz)]
+    lib.attn_decode_tree_workspace_size.restype = c_sz
+    lib.attn_decode_tree_workspace_size.argtypes = [c_i32] * 6
+    for names, types in ((("attn_decode_sliding_tree", "attn_decode_global_tree"), tree),
+                         (("attn_kv_append_sliding_tree", "attn_kv_append_global_tree"), chunk_tree),
+                         (("attn_kv_commit_sliding", "attn_kv_commit_global"), commit),
+                         (("attn_pages_assign",), assign),
+                         (("attn_kv_append_sliding_chunk", "attn_kv_append_global_chunk"), chunk),
                          (("attn_kv_append_global_prefix",), chunk_behind),
                          (("attn_kv_append_sliding_fp8", "attn_kv_append_global_fp8"), chunk8),
                          (("attn_kv_read_sliding_fp8", "attn_kv_read_global_fp8"), read8),
@@ -526,6 +562,27 @@ class Step:
 
     def add_decode_global_prefix(self, *args, **kw):
         return self._add(*_prefix_args(*args, **kw))
+
+    def add_decode_sliding_tree(self, *args, **kw):
+        return self._add(*_tree_args(KIND_SLIDING, *args, **kw))
+
+    def add_decode_global_tree(self, *args, **kw):
+        return self._add(*_tree_args(KIND_GLOBAL, *args, **kw))
+
+    def add_kv_append_sliding_tree(self, *args, **kw):
+        return self._add(*_append_tree_args(KIND_SLIDING, *args, **kw))
+
+    def add_kv_append_global_tree(self, *args, **kw):
+        return self._add(*_append_tree_args(KIND_GLOBAL, *args, **kw))
+
+    def add_kv_commit_sliding(self, *args, **kw):
+        return self._add(*_commit_args(KIND_SLIDING, *args, **kw))
+
+    def add_kv_commit_global(self, *args, **kw):
+        return self._add(*_commit_args(KIND_GLOBAL, *args, **kw))
+
+    def add_pages_assign(self, *args, **kw):
+        return self._add(*_assign_args(*args, **kw))
 
     @property
     def num_calls(self):
@@ -1010,17 +1067,153 @@ def _prefix_args(q, k_pool, v_pool, prefix_table, prefix_len, block_table, seq_l
     return "attn_decode_global_prefix", args, keep, o, device, _made(given, (o, workspace))
 
 
+def attn_decode_tree_plan(kind, batch, max_q, max_seq_len, window, num_splits=0, num_sms=152):
+    """(num_splits, launches, workspace_bytes) of attn_decode_*_tree; pure host arithmetic."""
+    lib = load()
+    ns, n, ws = ctypes.c_int32(0), ctypes.c_int32(0), ctypes.c_size_t(0)
+    st = lib.attn_decode_tree_plan(kind, batch, max_q, max_seq_len, window, num_splits, num_sms, ctypes.byref(ns),
+                                   ctypes.byref(n), ctypes.byref(ws))
+    if st != ATTN_OK:
+        raise AttnDecodeError(st, attn_last_error())
+    return ns.value, n.value, ws.value
+
+
+def attn_decode_tree_workspace_size(kind, batch, max_q, max_seq_len, window, num_splits=0):
+    """Workspace bytes of attn_decode_*_tree for the current CUDA device."""
+    n = load().attn_decode_tree_workspace_size(kind, batch, max_q, max_seq_len, window, num_splits)
+    if n == 0:
+        raise AttnDecodeError(1, attn_last_error())
+    return n
+
+
+def _tree_args(kind, q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o=None, *, max_q=None, max_seq_len=None,
+               window=None, out_dtype=torch.bfloat16, num_splits=0, workspace=None, status=None):
+    Hq, Hkv, D = SHAPES[kind]
+    _dims(q, 3, "q must be [total_q, %d, %d]" % (Hq, D))
+    _dims(k_pool, 4, "k_pool must be [num_pages, 16, %d, %d]" % (Hkv, D))
+    _dims(block_table, 2, "block_table must be [batch, max_blocks]")
+    total_q, (batch, max_blocks), n = q.shape[0], block_table.shape, k_pool.shape[0]
+    given = (o, workspace)
+    ptrs = [_ptr(q, "q", torch.bfloat16, (total_q, Hq, D)),
+            _ptr(k_pool, "k_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D)),
+            _ptr(v_pool, "v_pool", torch.bfloat16, (n, PAGE_SIZE, Hkv, D)),
+            _ptr(block_table, "block_table", torch.int32, (batch, max_blocks)),
+            _ptr(seq_lens, "seq_lens", torch.int32, (batch,)), _ptr(cu_q, "cu_q", torch.int32, (batch + 1,)),
+            _ptr(parents, "parents", torch.int32, (total_q,))]
+    o = _output(o, (total_q, Hq, D), out_dtype, q.device)
+    ptrs.append(_ptr(o, "o", o.dtype, (total_q, Hq, D)))
+    device = _one_device((q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o, workspace, status))
+    if max_q is None:
+        max_q = min(MAX_TREE, total_q)
+    if max_seq_len is None:
+        max_seq_len = min(max_blocks * PAGE_SIZE, 262144)
+    if window is None:
+        window = 1024 if kind == KIND_SLIDING else 0
+    if workspace is None:
+        with torch.cuda.device(device):
+            workspace = torch.empty(attn_decode_tree_workspace_size(kind, batch, max_q, max_seq_len, window, num_splits),
+                                    dtype=torch.uint8, device=device)
+    keep = (q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o, workspace, status)
+    args = tuple(ptrs) + (batch, total_q, int(max_q), max_blocks, n, int(max_seq_len), int(window),
+                          OUT_F32 if o.dtype == torch.float32 else OUT_BF16, int(num_splits),
+                          _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _status_ptr(status))
+    return "attn_decode_%s_tree" % _kind_name(kind), args, keep, o, device, _made(given, (o, workspace))
+
+
+def _append_tree_args(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, parents, k_pool, v_pool, q_out=None, *,
+                      status=None):
+    _, Hkv, D = SHAPES[kind]
+    given = (q_out,)
+    ptrs, q_out, batch, total_q, max_blocks = _append_common(kind, qkv, w_q, w_k, block_table, seq_lens, cu_q, q_out)
+    _dims(v_pool, 4, "v_pool must be [num_pages, 16, %d, %d]" % (Hkv, D))
+    n = v_pool.shape[0]
+    keep = (qkv, w_q, w_k, block_table, seq_lens, cu_q, parents, q_out, k_pool, v_pool, status)
+    ptrs.insert(6, _ptr(parents, "parents", torch.int32, (total_q,)))
+    pools = [_ptr(x, name, torch.bfloat16, (n, PAGE_SIZE, Hkv, D)) for x, name in ((k_pool, "k_pool"),
+                                                                                 (v_pool, "v_pool"))]
+    device = _one_device(keep)
+    args = tuple(ptrs + pools) + (batch, total_q, max_blocks, n, _status_ptr(status))
+    return "attn_kv_append_%s_tree" % _kind_name(kind), args, keep, q_out, device, _made(given, (q_out,))
+
+
+def _commit_args(kind, k_pools, v_pools, block_table, seq_lens, cu_q, path, path_len, new_lens=None, *, status=None):
+    _, Hkv, D = SHAPES[kind]
+    if isinstance(k_pools, torch.Tensor):
+        k_pools = [k_pools]
+    if isinstance(v_pools, torch.Tensor):
+        v_pools = [v_pools]
+    k_pools, v_pools = list(k_pools), list(v_pools)
+    if len(k_pools) != len(v_pools) or not k_pools:
+        raise ValueError("k_pools and v_pools must hold one pool per layer each, of one layer at least")
+    _dims(k_pools[0], 4, "k_pools must be [num_pages, 16, %d, %d] each" % (Hkv, D))
+    _dims(block_table, 2, "block_table must be [batch, max_blocks]")
+    _dims(path, 2, "path must be [batch, max_path]")
+    (batch, max_blocks), n, max_path = block_table.shape, k_pools[0].shape[0], path.shape[1]
+    given = (new_lens,)
+    arrays = []
+    for name, pools in (("k_pools", k_pools), ("v_pools", v_pools)):
+        ptrs = [_ptr(x, "%s[%d]" % (name, i), torch.bfloat16, (n, PAGE_SIZE, Hkv, D)) for i, x in enumerate(pools)]
+        arrays.append((ctypes.c_void_p * len(ptrs))(*ptrs))
+    ptrs = [_ptr(block_table, "block_table", torch.int32, (batch, max_blocks)),
+            _ptr(seq_lens, "seq_lens", torch.int32, (batch,)), _ptr(cu_q, "cu_q", torch.int32, (batch + 1,)),
+            _ptr(path, "path", torch.int32, (batch, max_path)), _ptr(path_len, "path_len", torch.int32, (batch,))]
+    if new_lens is None:
+        new_lens = torch.empty((batch,), dtype=torch.int32, device=block_table.device)
+    ptrs.append(_ptr(new_lens, "new_lens", torch.int32, (batch,)))
+    device = _one_device(k_pools + v_pools + [block_table, seq_lens, cu_q, path, path_len, new_lens, status])
+    keep = (k_pools, v_pools, block_table, seq_lens, cu_q, path, path_len, new_lens, status) + tuple(arrays)
+    args = tuple(arrays) + (len(k_pools),) + tuple(ptrs) + (batch, max_path, max_blocks, n, _status_ptr(status))
+    return "attn_kv_commit_%s" % _kind_name(kind), args, keep, new_lens, device, _made(given, (new_lens,))
+
+
+def new_page_state(num_pages, batch, max_blocks, device):
+    """The state of attn_pages_assign with every page free: (block_table [batch, max_blocks], held [batch, 2], free_list
+    [num_pages], free_state [2])."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return (torch.full((batch, max_blocks), -1, **i32), torch.zeros((batch, 2), **i32), torch.arange(num_pages, **i32),
+            torch.tensor([0, num_pages], **i32))
+
+
+def _assign_args(cached_lens, new_tokens, block_table, held, free_list, free_state, seq_lens=None, cu_q=None, *,
+                 window=0, held_out=None, free_state_out=None, status=None):
+    _dims(block_table, 2, "block_table must be [batch, max_blocks]")
+    _dims(free_list, 1, "free_list must be [num_pages]")
+    (batch, max_blocks), n = block_table.shape, free_list.shape[0]
+    given = (seq_lens, cu_q)
+    held_out = held if held_out is None else held_out
+    free_state_out = free_state if free_state_out is None else free_state_out
+    if seq_lens is None:
+        seq_lens = torch.empty((batch,), dtype=torch.int32, device=block_table.device)
+    if cu_q is None:
+        cu_q = torch.empty((batch + 1,), dtype=torch.int32, device=block_table.device)
+    tensors = dict(cached_lens=(cached_lens, (batch,)), new_tokens=(new_tokens, (batch,)),
+                   block_table=(block_table, (batch, max_blocks)), held=(held, (batch, 2)), free_list=(free_list, (n,)),
+                   free_state=(free_state, (2,)), held_out=(held_out, (batch, 2)),
+                   free_state_out=(free_state_out, (2,)), seq_lens=(seq_lens, (batch,)), cu_q=(cu_q, (batch + 1,)))
+    ptrs = [_ptr(x, name, torch.int32, shape) for name, (x, shape) in tensors.items()]
+    keep = tuple(x for x, _ in tensors.values()) + (status,)
+    device = _one_device(keep)
+    args = tuple(ptrs) + (batch, max_blocks, n, int(window), _status_ptr(status))
+    return "attn_pages_assign", args, keep, (seq_lens, cu_q), device, _made(given, (seq_lens, cu_q))
+
+
+def _first_tensor(x):
+    return x[0] if isinstance(x, (list, tuple)) and x else x
+
+
 def _once(stream, marshal, first, *args, **kw):
-    """The call that marshal(first, *args, **kw) describes, on `stream`; `first` is a tensor, or args[0] is."""
+    """The call that marshal(first, *args, **kw) describes, on `stream`; `first` is a tensor, or args[0] is (or holds
+    one)."""
     outputs = []
-    with _work_on(stream, args[0] if isinstance(first, int) else first, outputs):
+    with _work_on(stream, _first_tensor(args[0] if isinstance(first, int) else first), outputs):
         fn_name, c_args, _, out, device, made = marshal(first, *args, **kw)
         s_ptr = _stream_ptr(stream, device)
         with torch.cuda.device(device):
             st = getattr(load(), fn_name)(*c_args, s_ptr)
         if st != ATTN_OK:
             raise AttnDecodeError(st, attn_last_error())
-        outputs.extend(t for t in made if t is out)
+        outs = out if isinstance(out, tuple) else (out,)
+        outputs.extend(t for t in made if any(t is x for x in outs))
     return out
 
 
@@ -1156,3 +1349,104 @@ def prepare_decode_sliding_fp8(*args, **kw):
 def prepare_decode_global_fp8(*args, **kw):
     """PreparedCall for attn_decode_global_fp8 (same arguments, minus the stream)."""
     return PreparedCall(*_decode_fp8_args(KIND_GLOBAL, *args, **kw))
+
+
+def attn_decode_sliding_tree(q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o=None, *, max_q=None,
+                             max_seq_len=None, window=1024, out_dtype=torch.bfloat16, num_splits=0, workspace=None,
+                             status=None, stream=None):
+    """Attention of a tree of drafted tokens per sequence over its cached context and each node's ancestors: q
+    [T,16,256] packed by sequence (cu_q int32 [B+1]), pools [P,16,8,256], seq_lens int32 [B] with the nodes, parents
+    int32 [T] (node of the same sequence, -1: the context) -> o [T,16,256].
+
+    max_q: host bound on a tree's nodes (default: the most there can be, MAX_TREE or T).  workspace: at least
+    attn_decode_tree_workspace_size(...) bytes; allocated per call when None."""
+    return _once(stream, _tree_args, KIND_SLIDING, q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o,
+                 max_q=max_q, max_seq_len=max_seq_len, window=window, out_dtype=out_dtype, num_splits=num_splits,
+                 workspace=workspace, status=status)
+
+
+def attn_decode_global_tree(q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o=None, *, max_q=None,
+                            max_seq_len=None, window=0, out_dtype=torch.bfloat16, num_splits=0, workspace=None,
+                            status=None, stream=None):
+    """attn_decode_sliding_tree for global layers: q [T,16,512], pools [P,16,1,512] -> o [T,16,512] (window <= 0:
+    none)."""
+    return _once(stream, _tree_args, KIND_GLOBAL, q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o,
+                 max_q=max_q, max_seq_len=max_seq_len, window=window, out_dtype=out_dtype, num_splits=num_splits,
+                 workspace=workspace, status=status)
+
+
+def attn_kv_append_sliding_tree(qkv, w_q, w_k, block_table, seq_lens, cu_q, parents, k_pool, v_pool, q_out=None, *,
+                                status=None, stream=None):
+    """attn_kv_append_sliding_chunk for the nodes of trees (parents int32 [T]): node i of a sequence goes to slot
+    ctx + i and is rotated at ctx + its depth, ctx = seq_lens[b] - nodes.  Returns q_out [T,16,256]."""
+    return _once(stream, _append_tree_args, KIND_SLIDING, qkv, w_q, w_k, block_table, seq_lens, cu_q, parents, k_pool,
+                 v_pool, q_out, status=status)
+
+
+def attn_kv_append_global_tree(qkv, w_q, w_k, block_table, seq_lens, cu_q, parents, k_pool, v_pool, q_out=None, *,
+                               status=None, stream=None):
+    """attn_kv_append_sliding_tree for global layers: qkv [T, 8704]; both pools are written."""
+    return _once(stream, _append_tree_args, KIND_GLOBAL, qkv, w_q, w_k, block_table, seq_lens, cu_q, parents, k_pool,
+                 v_pool, q_out, status=status)
+
+
+def attn_kv_commit_sliding(k_pools, v_pools, block_table, seq_lens, cu_q, path, path_len, new_lens=None, *, status=None,
+                           stream=None):
+    """The accepted paths' cache rows to the front of their nodes, in all layers at once: slot ctx + path[b, j] to slot
+    ctx + j, j < path_len[b].  k_pools, v_pools: a pool [P,16,8,256], or a list of one per layer (64 at most); path
+    int32 [B, max_path], increasing node indices; path_len int32 [B].  Returns new_lens int32 [B] = ctx + path_len."""
+    return _once(stream, _commit_args, KIND_SLIDING, k_pools, v_pools, block_table, seq_lens, cu_q, path, path_len,
+                 new_lens, status=status)
+
+
+def attn_kv_commit_global(k_pools, v_pools, block_table, seq_lens, cu_q, path, path_len, new_lens=None, *, status=None,
+                          stream=None):
+    """attn_kv_commit_sliding for global layers (pools [P,16,1,512])."""
+    return _once(stream, _commit_args, KIND_GLOBAL, k_pools, v_pools, block_table, seq_lens, cu_q, path, path_len,
+                 new_lens, status=status)
+
+
+def attn_pages_assign(cached_lens, new_tokens, block_table, held, free_list, free_state, seq_lens=None, cu_q=None, *,
+                      window=0, held_out=None, free_state_out=None, status=None, stream=None):
+    """The tables of a step on the GPU: request b keeps cached_lens[b] tokens (of a window of them the pages that its
+    next token sees) and brings new_tokens[b]; pages it no longer needs go to the free list, pages it lacks come from
+    there into block_table (new_page_state makes the four state tensors).  Returns (seq_lens int32 [B], cu_q int32
+    [B+1]), what the appends and the attention take.  held_out, free_state_out: the new state's place (default: in
+    place)."""
+    return _once(stream, _assign_args, cached_lens, new_tokens, block_table, held, free_list, free_state, seq_lens, cu_q,
+                 window=window, held_out=held_out, free_state_out=free_state_out, status=status)
+
+
+def prepare_decode_sliding_tree(*args, **kw):
+    """PreparedCall for attn_decode_sliding_tree (same arguments, minus the stream)."""
+    return PreparedCall(*_tree_args(KIND_SLIDING, *args, **kw))
+
+
+def prepare_decode_global_tree(*args, **kw):
+    """PreparedCall for attn_decode_global_tree (same arguments, minus the stream)."""
+    return PreparedCall(*_tree_args(KIND_GLOBAL, *args, **kw))
+
+
+def prepare_kv_append_sliding_tree(*args, **kw):
+    """PreparedCall for attn_kv_append_sliding_tree (same arguments, minus the stream)."""
+    return PreparedCall(*_append_tree_args(KIND_SLIDING, *args, **kw))
+
+
+def prepare_kv_append_global_tree(*args, **kw):
+    """PreparedCall for attn_kv_append_global_tree (same arguments, minus the stream)."""
+    return PreparedCall(*_append_tree_args(KIND_GLOBAL, *args, **kw))
+
+
+def prepare_kv_commit_sliding(*args, **kw):
+    """PreparedCall for attn_kv_commit_sliding (same arguments, minus the stream)."""
+    return PreparedCall(*_commit_args(KIND_SLIDING, *args, **kw))
+
+
+def prepare_kv_commit_global(*args, **kw):
+    """PreparedCall for attn_kv_commit_global (same arguments, minus the stream)."""
+    return PreparedCall(*_commit_args(KIND_GLOBAL, *args, **kw))
+
+
+def prepare_pages_assign(*args, **kw):
+    """PreparedCall for attn_pages_assign (same arguments, minus the stream)."""
+    return PreparedCall(*_assign_args(*args, **kw))

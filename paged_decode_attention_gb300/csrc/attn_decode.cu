@@ -864,4 +864,5 @@ extern "C" int32_t attn_decode_sliding_noalloc(const void* q, const void* k_pool
 }
 
 #include "serving.cuh"
+#include "tree_host.cuh"
 #include "step.cuh"

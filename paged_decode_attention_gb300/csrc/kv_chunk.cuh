@@ -41,6 +41,7 @@
 
 #include "fp8.cuh"
 #include "kv_append.cuh"
+#include "tree_nodes.cuh"
 
 namespace pda {
 namespace chunk {
@@ -59,6 +60,7 @@ struct ChunkParams {
   const int32_t* seq_lens;     // [batch], new tokens included
   const int32_t* cu_q;         // [batch + 1]
   const int32_t* prefix_len;   // one int32 on the device, added to every angle's position; null: 0
+  const int32_t* parents;      // [total_q], nodes of trees only
   __nv_bfloat16* q_out;        // [total_q, Hq, D]
   void* k_pool;                // [num_pages, 16, Hkv, D] bf16 or e4m3; null: values-only global cache (bf16)
   void* v_pool;
@@ -266,11 +268,12 @@ __device__ __forceinline__ void store_fp8(uint8_t* dst, uint8_t* scale, Row<kD>&
   if (lane == 0) *scale = static_cast<uint8_t>(s);
 }
 
-template <int kD, int kHq, int kHkv, int kPairs, bool kShared, bool kFp8>
+template <int kD, int kHq, int kHkv, int kPairs, bool kShared, bool kFp8, bool kTree = false>
 __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int kRowLen = kHq * kD + (kShared ? kD : 2 * kHkv * kD);
   static_assert(kHq == 2 * kQWarps && (kShared ? kHkv == 1 : kHkv == kQWarps), "rows of a token by warp");
-  static_assert(kPairs <= kThreads<kShared> && kPairs <= (1 << kPairBits) && kPairs % (kD / 64) == 0, "pairs by thread");
+  static_assert(kPairs <= kThreads<kShared> && kPairs <= (1 << kPairBits) && kPairs % (kD / 64) == 0 && kPairs % 32 == 0,
+                "pairs by thread");
   __shared__ Smem s;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -324,6 +327,7 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
       // the token's sequence: the number of sequences that end at or before t
       // (the same in every warp of the block)
       int pos = -1;  // the token is left alone
+      [[maybe_unused]] int turned = 0;  // a node's position in its text
       int32_t phys = 0;
       int b = 0;
       for (int j0 = 0; j0 < p.batch; j0 += 32) {
@@ -335,15 +339,24 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
         const int L = s.len[b];
         const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
         // a sequence whose numbers do not fit together is left alone as a whole
-        if (q0 < 0 || t < q0 || q1 > p.total_q || q1 - q0 > L || L > cap) {
+        if (q0 < 0 || t < q0 || q1 > p.total_q || q1 - q0 > L || L > cap || (kTree && q1 - q0 > ATTN_MAX_TREE)) {
           if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
         } else {
           pos = L - (q1 - q0) + (t - q0);
           if (has_kv) phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kPage];
+          if constexpr (kTree) {
+            if (threadIdx.x < kPairs) {  // (whole warps)
+              int parent[2], depth[2];
+              if (tree::load_parents(p.parents + q0, q1 - q0, parent) && threadIdx.x == 0)
+                report(p.status, ATTN_DEV_BAD_TREE);
+              tree::depths(parent, depth);
+              turned = pos - (t - q0) + tree::of_node(depth, t - q0);
+            }
+          }
         }
       }
       if (threadIdx.x < kPairs)
-        sincos_at(freq, pos < 0 ? 0 : base + pos, &s.sin[buf][threadIdx.x], &s.cos[buf][threadIdx.x]);
+        sincos_at(freq, pos < 0 ? 0 : kTree ? turned : base + pos, &s.sin[buf][threadIdx.x], &s.cos[buf][threadIdx.x]);
       __syncthreads();  // one per token: the buffer written next was read before this barrier
       const float* cs = s.cos[buf];
       const float* sn = s.sin[buf];

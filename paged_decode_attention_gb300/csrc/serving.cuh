@@ -134,25 +134,28 @@ int32_t make_whole_plan(Serving call, int32_t batch, int32_t max_seq_len, int32_
 // ---------------------------------------------------------------------------
 // Norms, RoPE and cache append of a chunk of tokens per sequence
 // ---------------------------------------------------------------------------
-enum class Chunk { kBf16, kFp8, kBehindPrefix };
+enum class Chunk { kBf16, kFp8, kBehindPrefix, kTree };
 
-int32_t run_chunk(int32_t kind, Chunk form, const void* qkv, const void* w_q, const void* w_k, const int32_t* prefix_len,
+// extra: prefix_len behind a prefix, parents of a tree's nodes
+int32_t run_chunk(int32_t kind, Chunk form, const void* qkv, const void* w_q, const void* w_k, const int32_t* extra,
                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* q_out, void* k_pool,
                   void* v_pool, uint8_t* k_scale, uint8_t* v_scale, int32_t batch, int32_t total_q, int32_t max_blocks,
                   int64_t num_pages, int32_t* status, void* stream) {
   g_err[0] = '\0';
   const bool sliding = kind == ATTN_KIND_SLIDING;
-  const bool fp8 = form == Chunk::kFp8, behind = form == Chunk::kBehindPrefix;
+  const bool fp8 = form == Chunk::kFp8, behind = form == Chunk::kBehindPrefix, tree = form == Chunk::kTree;
   const char* name = fp8      ? (sliding ? "attn_kv_append_sliding_fp8" : "attn_kv_append_global_fp8")
                      : behind ? "attn_kv_append_global_prefix"
+                     : tree   ? (sliding ? "attn_kv_append_sliding_tree" : "attn_kv_append_global_tree")
                               : (sliding ? "attn_kv_append_sliding_chunk" : "attn_kv_append_global_chunk");
   const bool values_only = !sliding && form == Chunk::kBf16;  // may leave the keys out
   if (!w_q || !w_k || !block_table || !seq_lens || !cu_q || (total_q > 0 && (!qkv || !q_out)) ||
-      (!k_pool && !values_only) || !v_pool || (fp8 && (!k_scale || !v_scale)) || (behind && !prefix_len))
+      (!k_pool && !values_only) || !v_pool || (fp8 && (!k_scale || !v_scale)) || (behind && !extra) ||
+      (tree && total_q > 0 && !extra))
     return fail(ATTN_ERR_INVALID_ARG, "%s: null pointer argument", name);
   if (!aligned_to(qkv, 16) || !aligned_to(w_q, 16) || !aligned_to(w_k, 16) || !aligned_to(q_out, 16) ||
       !aligned_to(k_pool, 16) || !aligned_to(v_pool, 16) || !aligned_to(k_scale, 16) || !aligned_to(v_scale, 16) ||
-      !aligned_to(prefix_len, 4) || !aligned_to(block_table, 4) || !aligned_to(seq_lens, 4) || !aligned_to(cu_q, 4) ||
+      !aligned_to(extra, 4) || !aligned_to(block_table, 4) || !aligned_to(seq_lens, 4) || !aligned_to(cu_q, 4) ||
       !aligned_to(status, 4))
     return fail(ATTN_ERR_INVALID_ARG, "%s: misaligned pointer (qkv, w_q, w_k, q_out, pools and scales 16 bytes, "
                 "tables 4)", name);
@@ -175,7 +178,8 @@ int32_t run_chunk(int32_t kind, Chunk form, const void* qkv, const void* w_q, co
   p.block_table = block_table;
   p.seq_lens = seq_lens;
   p.cu_q = cu_q;
-  p.prefix_len = prefix_len;
+  p.prefix_len = behind ? extra : nullptr;
+  p.parents = tree ? extra : nullptr;
   p.q_out = static_cast<__nv_bfloat16*>(q_out);
   p.k_pool = k_pool;
   p.v_pool = v_pool;
@@ -194,17 +198,19 @@ int32_t run_chunk(int32_t kind, Chunk form, const void* qkv, const void* w_q, co
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   namespace ch = pda::chunk;
   const int blocks = std::min(total_q, num_sms * ch::kBlocksPerSm);
-  const auto kernels = [&](auto fp8_c) {
-    constexpr bool kFp8 = decltype(fp8_c)::value;
+  const auto kernels = [&](auto fp8_c, auto tree_c) {
+    constexpr bool kFp8 = decltype(fp8_c)::value, kTree = decltype(tree_c)::value;
     if (sliding)
       return launch_pdl(ch::chunk_kernel<ATTN_SLIDING_D, ATTN_SLIDING_HQ, ATTN_SLIDING_HKV, ATTN_SLIDING_ROPE_PAIRS,
-                                         false, kFp8>,
+                                         false, kFp8, kTree>,
                         dim3(blocks), ch::kThreads<false>, 0, s, p);
     return launch_pdl(ch::chunk_kernel<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ, ATTN_GLOBAL_HKV, ATTN_GLOBAL_ROPE_PAIRS, true,
-                                       kFp8>,
+                                       kFp8, kTree>,
                       dim3(blocks), ch::kThreads<true>, 0, s, p);
   };
-  const cudaError_t e = fp8 ? kernels(std::true_type{}) : kernels(std::false_type{});
+  const cudaError_t e = fp8    ? kernels(std::true_type{}, std::false_type{})
+                        : tree ? kernels(std::false_type{}, std::true_type{})
+                               : kernels(std::false_type{}, std::false_type{});
   return launched(name, e);
 }
 

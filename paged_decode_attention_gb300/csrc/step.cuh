@@ -5,6 +5,7 @@
 // recording (g_record) and error reporting it shares.
 #pragma once
 
+#include <array>
 #include <functional>
 #include <new>
 #include <utility>
@@ -45,6 +46,23 @@ int32_t record(attn_step* step, const Call& call, const char* name) {
   }
   step->kernels += kernels;
   return ATTN_OK;
+}
+
+// The same for a commit, whose pool pointers are kept with the step.
+template <typename Call>
+int32_t record_commit(attn_step* step, const void* const* k_pools, const void* const* v_pools, int32_t layers,
+                      const Call& call, const char* name) {
+  g_err[0] = '\0';
+  using Pools = std::array<const void*, ATTN_MAX_LAYERS>;
+  if (!k_pools || !v_pools) return fail(ATTN_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (!aligned_to(k_pools, alignof(void*)) || !aligned_to(v_pools, alignof(void*)))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: misaligned pointer", name);
+  Pools k{}, v{};
+  for (int i = 0; i < layers && i < ATTN_MAX_LAYERS; ++i) {  // (the call refuses other numbers of layers)
+    k[i] = k_pools[i];
+    v[i] = v_pools[i];
+  }
+  return record(step, [=](void* s) { return call(k, v, s); }, name);
 }
 
 }  // namespace
@@ -216,6 +234,87 @@ int32_t attn_step_add_decode_global_prefix(attn_step* step, const void* q, const
         prefix_blocks, max_blocks, num_pages, max_prefix_len, max_seq_len, out_dtype, num_splits, prefix_splits,
         workspace, workspace_bytes, status, s);
   }, "attn_step_add_decode_global_prefix");
+}
+
+int32_t attn_step_add_decode_sliding_tree(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
+                                          const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                                          const int32_t* parents, void* o, int32_t batch, int32_t total_q,
+                                          int32_t max_q, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len,
+                                          int32_t window, int32_t out_dtype, int32_t num_splits, void* workspace,
+                                          size_t workspace_bytes, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_decode_sliding_tree(q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o, batch, total_q,
+                                    max_q, max_blocks, num_pages, max_seq_len, window, out_dtype, num_splits,
+                                    workspace, workspace_bytes, status, s);
+  }, "attn_step_add_decode_sliding_tree");
+}
+
+int32_t attn_step_add_decode_global_tree(attn_step* step, const void* q, const void* k_pool, const void* v_pool,
+                                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                                         const int32_t* parents, void* o, int32_t batch, int32_t total_q,
+                                         int32_t max_q, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len,
+                                         int32_t window, int32_t out_dtype, int32_t num_splits, void* workspace,
+                                         size_t workspace_bytes, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_decode_global_tree(q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o, batch, total_q, max_q,
+                                   max_blocks, num_pages, max_seq_len, window, out_dtype, num_splits, workspace,
+                                   workspace_bytes, status, s);
+  }, "attn_step_add_decode_global_tree");
+}
+
+int32_t attn_step_add_kv_append_sliding_tree(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+                                             const int32_t* block_table, const int32_t* seq_lens,
+                                             const int32_t* cu_q, const int32_t* parents, void* q_out, void* k_pool,
+                                             void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
+                                             int64_t num_pages, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_kv_append_sliding_tree(qkv, w_q, w_k, block_table, seq_lens, cu_q, parents, q_out, k_pool, v_pool,
+                                       batch, total_q, max_blocks, num_pages, status, s);
+  }, "attn_step_add_kv_append_sliding_tree");
+}
+
+int32_t attn_step_add_kv_append_global_tree(attn_step* step, const void* qkv, const void* w_q, const void* w_k,
+                                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                                            const int32_t* parents, void* q_out, void* k_pool, void* v_pool,
+                                            int32_t batch, int32_t total_q, int32_t max_blocks, int64_t num_pages,
+                                            int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_kv_append_global_tree(qkv, w_q, w_k, block_table, seq_lens, cu_q, parents, q_out, k_pool, v_pool,
+                                      batch, total_q, max_blocks, num_pages, status, s);
+  }, "attn_step_add_kv_append_global_tree");
+}
+
+int32_t attn_step_add_kv_commit_sliding(attn_step* step, const void* const* k_pools, const void* const* v_pools,
+                                        int32_t layers, const int32_t* block_table, const int32_t* seq_lens,
+                                        const int32_t* cu_q, const int32_t* path, const int32_t* path_len,
+                                        int32_t* new_lens, int32_t batch, int32_t max_path, int32_t max_blocks,
+                                        int64_t num_pages, int32_t* status) {
+  return record_commit(step, k_pools, v_pools, layers, [=](const auto& k, const auto& v, void* s) {
+    return attn_kv_commit_sliding(k.data(), v.data(), layers, block_table, seq_lens, cu_q, path, path_len, new_lens,
+                                  batch, max_path, max_blocks, num_pages, status, s);
+  }, "attn_step_add_kv_commit_sliding");
+}
+
+int32_t attn_step_add_kv_commit_global(attn_step* step, const void* const* k_pools, const void* const* v_pools,
+                                       int32_t layers, const int32_t* block_table, const int32_t* seq_lens,
+                                       const int32_t* cu_q, const int32_t* path, const int32_t* path_len,
+                                       int32_t* new_lens, int32_t batch, int32_t max_path, int32_t max_blocks,
+                                       int64_t num_pages, int32_t* status) {
+  return record_commit(step, k_pools, v_pools, layers, [=](const auto& k, const auto& v, void* s) {
+    return attn_kv_commit_global(k.data(), v.data(), layers, block_table, seq_lens, cu_q, path, path_len, new_lens,
+                                 batch, max_path, max_blocks, num_pages, status, s);
+  }, "attn_step_add_kv_commit_global");
+}
+
+int32_t attn_step_add_pages_assign(attn_step* step, const int32_t* cached_lens, const int32_t* new_tokens,
+                                   int32_t* block_table, const int32_t* held, int32_t* free_list,
+                                   const int32_t* free_state, int32_t* held_out, int32_t* free_state_out,
+                                   int32_t* seq_lens, int32_t* cu_q, int32_t batch, int32_t max_blocks,
+                                   int64_t num_pages, int32_t window, int32_t* status) {
+  return record(step, [=](void* s) {
+    return attn_pages_assign(cached_lens, new_tokens, block_table, held, free_list, free_state, held_out,
+                             free_state_out, seq_lens, cu_q, batch, max_blocks, num_pages, window, status, s);
+  }, "attn_step_add_pages_assign");
 }
 
 int32_t attn_step_num_calls(const attn_step* step) { return step ? static_cast<int32_t>(step->calls.size()) : 0; }

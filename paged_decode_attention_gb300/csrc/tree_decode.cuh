@@ -1,0 +1,1034 @@
+// tree_decode.cuh -- attention of a tree of drafted tokens per sequence over the
+// paged cache (attn_decode_*_tree) on the 5th-generation tensor cores.
+//
+// Node i of a sequence of n nodes behind ctx cached positions sees position l < ctx
+// and the slots ctx + j of its ancestors and itself, within the window where there is
+// one (include/attn_tree.h).  A node brings 16 query heads, so a tree is n * G rows
+// over each KV head: 16 to 1024, where a tensor-core tile has 128.  The products are
+// therefore turned round, keys and dims in the tile's 128 rows, query rows in its
+// columns, of which any multiple of 16 will do:
+//   S^T = K Q^T     M = 128 keys (eight pages), N = rows, K = D: A = the step's K, one
+//                   64-dim chunk [128 keys][128 B] after another, B = Q; one key per
+//                   tensor-memory lane;
+//   P^T = softmax   a thread per key (two warpgroups, half of the columns each):
+//                   masks, weights to bf16 in shared memory, [64 rows][keys] atoms;
+//   O^T += V^T P^T  M = 128 dims (D / 128 tiles), N = rows, K = 16 keys: A = a page of V as
+//                   it was copied, dims contiguous, B = P^T; one dim per lane.
+// So all D dims of the output fit tensor memory at 64 rows (D = 512) or 128 (D =
+// 256): no logit is computed twice, and a chain of few tokens costs few columns.
+//
+// Running max.  A row's (column's) reference max m is shared by all keys of a step.
+// It moves only when a score exceeds it by more than kSlack, and then to kHeadroom
+// above (prefill_tc.cuh has the bounds); a thread compares its own scores with the
+// bounds, and one barrier with an OR tells whether any row moves.  So in nearly all
+// steps nothing is reduced across lanes: each thread sums the weights of its own keys,
+// and the 128 sums per row meet once, at the end of a segment.
+//
+// Schedule.  Rows come in groups of kQueries nodes; group r of KV head c of all
+// sequences that have one is a list of steps of 128 keys, a virtual step in front of
+// every sequence (its Q, its end).  All lists are cut into runs of `per` steps, the
+// smallest that gives no more runs than blocks: every block has the same work whatever
+// the lengths, and blocks of neighbouring groups walk the same keys at the same time.
+// A sequence inside one run is finished there; of a cut one every block leaves a
+// partial (O, m, sum), and merge_kernel joins them.
+//
+// What a node does not see.  Scores are masked, and rows of V that no node sees are
+// zeroed in shared memory.  A row that some nodes see and others do not (a node of the
+// tree, the window's edge) may hold an infinity or NaN, and 0 * inf would reach the
+// others: such elements are zeroed too, and the epilogue adds them to the rows that do
+// see them.
+//
+// Roles: warps 0-7 softmax and epilogue, 8 copies Q and K, 9 copies V, 10 issues S^T,
+// 11 issues O^T.  Every wait is bounded.
+#pragma once
+
+#include "attn_tree.h"
+#include "common.cuh"
+#include "prefill_tc.cuh"
+#include "tcgen05.cuh"
+#include "tree_nodes.cuh"
+
+namespace pda {
+namespace tree {
+
+constexpr int kKeys = 128;                  // per step
+constexpr int kStepPages = kKeys / kPage;
+constexpr int kMaxGroups = 16;              // of rows, per KV head
+constexpr int kMinPer = 2;                  // smallest run: a virtual step and one of keys
+constexpr int kSoftmaxThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kMaxGrid = kMaxSplits;
+
+struct TreeParams {
+  const __nv_bfloat16* v_pool;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  const int32_t* parents;
+  void* o;
+  float* part_o;    // [2 grid][kN][D]: a block's first segment, and its last
+  float2* part_ml;  // [2 grid][kN]: (reference max in log2 units, sum)
+  int4* cuts;       // [grid]: the sequence that is cut first in this block: first node, (nodes, KV head), first
+                    // partial, partials; 0 partials: none
+  int32_t* status;
+  int64_t num_pages;
+  int32_t batch;
+  int32_t max_blocks;
+  int32_t window;
+  int32_t total_q;
+  int32_t max_q;
+  int32_t groups;   // of rows: ceil(max_q / kQueries)
+  int32_t q_box;    // nodes that a copy of Q brings
+  int32_t out_f32;
+  int32_t whole;    // a block per (sequence, group, KV head) instead of runs
+};
+
+template <int kD_, int kG_, int kHkv_, int kN_, int kKStages_, int kVStages_>
+struct Config {
+  static constexpr int kD = kD_, kG = kG_, kHkv = kHkv_, kHq = kG * kHkv;
+  static constexpr int kN = kN_;               // rows per group, at most
+  static constexpr int kHalf = kN / 2;         // columns per softmax warpgroup
+  static constexpr int kQueries = kN / kG;
+  static constexpr int kChunks = kD / 64;
+  static constexpr int kTiles = kD / 128;      // of 128 output dims
+  static constexpr int kKStages = kKStages_;   // K chunks
+  static constexpr int kVStages = kVStages_;   // V pages
+  static constexpr int kKChunk = kKeys * 128;  // bytes: [128 keys][64 dims]
+  static constexpr int kVPage = kPage * kD * 2;
+  static constexpr int kPChunk = kKeys * 128;  // P^T of 64 rows
+  static constexpr int kPBytes = (kN + 63) / 64 * kPChunk;
+  static constexpr uint32_t kSCol = kTiles * kN;  // O^T first, then two S^T buffers
+  static constexpr uint32_t kUsedCols = kSCol + 2 * kN;
+  static constexpr uint32_t kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
+  static_assert(kUsedCols <= 512 && kN % 16 == 0 && kN <= 256, "tensor memory");
+  static_assert(kHalf == 16 || kHalf == 32 || kHalf == 64, "column reductions");
+
+  struct Smem {
+    alignas(1024) uint8_t q[kChunks][kN * 128];
+    alignas(1024) uint8_t p[2][kPBytes];
+    alignas(1024) uint8_t k[kKStages][kKChunk];
+    alignas(1024) uint8_t v[kVStages][kVPage];
+    alignas(16) float m[kN];          // reference max (log2 units), 0 before there is one
+    alignas(16) float bound[kN];      // a score above this moves it; -inf before there is one
+    alignas(16) float f[kN];          // factor of a moved reference; 1 / sum at the end
+    alignas(16) float red[8][kN / 2]; // per softmax warp and column: max, sum
+    alignas(8) unsigned long long anc[ATTN_MAX_TREE];
+    int32_t depth[ATTN_MAX_TREE];
+    int32_t pre[kMaxBatch + 1];       // steps (virtual ones included) before sequence b in this block's list
+    int32_t hist[kMaxGroups + 1];     // steps of the sequences with that many groups
+    int32_t warp_sum[kMaxBatch / 32];
+    int32_t sched[5];                 // group, KV head, per, run, next block's distance
+    int32_t poison;                   // this segment: an element was zeroed that some row sees
+    alignas(8) uint64_t k_full[kKStages], k_empty[kKStages];
+    alignas(8) uint64_t v_full[kVStages], v_empty[kVStages];
+    alignas(8) uint64_t s_full[2], s_free[2];
+    alignas(8) uint64_t p_full[2], p_empty[2];
+    alignas(8) uint64_t q_ready, q_empty;
+    alignas(8) uint64_t o_full, o_free;
+    alignas(8) uint64_t mma_done;
+    uint32_t tmem_base;
+  };
+  static constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM within the 227 KB a CTA may have");
+};
+
+// One sequence as the schedule sees it.
+struct Sequence {
+  int q0, n, L, ctx, lo, page0, pages, steps;  // steps 0: nothing to do
+};
+
+template <typename C>
+__device__ __forceinline__ Sequence load_sequence(const TreeParams& p, int b, bool& refused, bool& backwards) {
+  Sequence s{};
+  s.q0 = p.cu_q[b];
+  const int64_t n = static_cast<int64_t>(p.cu_q[b + 1]) - s.q0;
+  s.L = p.seq_lens[b];
+  const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
+  backwards = n < 0;
+  refused = n < 0 || s.q0 < 0 || s.q0 + n > p.total_q || n > p.max_q || n > s.L || s.L > cap;
+  if (refused || n == 0) return s;
+  s.n = static_cast<int>(n);
+  s.ctx = s.L - s.n;
+  s.lo = p.window > 0 && s.ctx >= p.window ? s.ctx - p.window + 1 : 0;
+  s.page0 = s.lo / kPage;
+  s.pages = (s.L - 1) / kPage - s.page0 + 1;
+  s.steps = (s.pages + kStepPages - 1) / kStepPages;
+  return s;
+}
+
+// A part of one sequence's steps for one group of rows.
+struct Segment {
+  Sequence q;
+  int b, row0, nodes, cols, N;  // first node of the group (packed), its nodes, rows, columns of the products
+  int s0, s1;                   // steps
+  bool whole;
+  int slot;                     // of its partial
+};
+
+// Walks a block's segments; every role does it for itself, with the same result.
+template <typename C>
+struct Walk {
+  int b, w0, w1, group, kv, index;
+  template <typename S>
+  __device__ __forceinline__ void start(const TreeParams& p, const S& s) {
+    group = s.sched[0];
+    kv = s.sched[1];
+    index = 0;
+    const int per = s.sched[2], run = s.sched[3];
+    if (p.whole) {
+      b = run;
+      w0 = s.pre[b];
+      w1 = s.pre[b + 1];
+      return;
+    }
+    const int total = s.pre[p.batch];
+    const long long u0 = static_cast<long long>(run) * per;
+    w0 = run < 0 || u0 >= total ? total : static_cast<int>(u0);
+    w1 = total - w0 < per ? total : w0 + per;
+    int lo = 0, hi = p.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.pre[mid] <= w0) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+  }
+  template <typename S>
+  __device__ __forceinline__ bool next(const TreeParams& p, const S& s, Segment& g) {
+    for (; b < p.batch && s.pre[b] < w1; ++b) {
+      const int steps = s.pre[b + 1] - s.pre[b] - 1;
+      if (steps <= 0) continue;
+      const int first = s.pre[b] + 1;
+      g.s0 = w0 > first ? w0 - first : 0;
+      g.s1 = w1 - first < steps ? w1 - first : steps;
+      if (g.s1 <= g.s0) continue;
+      bool refused, backwards;
+      g.q = load_sequence<C>(p, b, refused, backwards);
+      g.b = b;
+      g.row0 = g.q.q0 + group * C::kQueries;
+      g.nodes = min(C::kQueries, g.q.n - group * C::kQueries);
+      g.cols = g.nodes * C::kG;
+      g.N = (g.cols + 15) & ~15;
+      g.whole = g.s0 == 0 && g.s1 == steps;
+      g.slot = 2 * static_cast<int>(blockIdx.x) + (index > 0);
+      ++index;
+      ++b;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Reduces kW values of every lane across the warp, column by column: lane l gets
+// column l (kW = 32) or l / 2 (kW = 16).
+template <int kW, typename Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[kW], Op op) {
+  const int lane = threadIdx.x & 31;
+  int off = 16;
+#pragma unroll
+  for (int w = kW / 2; w >= 1; w /= 2, off /= 2) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float send = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, off));
+    }
+  }
+  if constexpr (kW == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+  return v[0];
+}
+
+// All columns of a softmax thread into its warp's row of `red`.
+template <int kHalf, typename Op>
+__device__ __forceinline__ void reduce_into(const float (&v)[kHalf], float* red, Op op) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (kHalf == 16) {
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = v[i];
+    const float r = reduce_columns<16>(t, op);
+    red[lane >> 1] = r;  // (two lanes, one value)
+  } else {
+#pragma unroll
+    for (int c0 = 0; c0 < kHalf; c0 += 32) {
+      float t[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) t[i] = v[c0 + i];
+      red[c0 + lane] = reduce_columns<32>(t, op);
+    }
+  }
+}
+
+__device__ __forceinline__ bool barrier_or(uint32_t id, uint32_t threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// Whether node i (depth d, ancestors a) sees position pos.
+template <typename S>
+__device__ __forceinline__ bool sees(const Sequence& q, int window, const S& s, int i, int pos) {
+  const int d = s.depth[i];
+  if (pos < q.ctx) return window <= 0 || q.ctx - pos < window - d;
+  const int j = pos - q.ctx;
+  return j < q.n && ((s.anc[i] >> j) & 1) && (window <= 0 || d - s.depth[j] < window);
+}
+
+// Positions below the first, or from the second on, are not seen by every node.
+__device__ __forceinline__ int all_from(const Sequence& q, int window) {
+  return window > 0 ? q.ctx + (q.n - 1) - window + 1 : 0;  // (a depth is at most n - 1)
+}
+
+__device__ __forceinline__ bool finite_bf16(uint32_t half) { return (half & 0x7f80u) != 0x7f80u; }
+
+// The schedule: this block's list, the running sums over it, its run.  Called by
+// every thread; ends with a barrier.  Returns false when the call is refused.
+template <typename C, typename S>
+__device__ __forceinline__ bool make_schedule(const TreeParams& p, S& s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid <= kMaxGroups) s.hist[tid] = 0;
+  int weight = 0, groups = 0;
+  bool refused = false, backwards = false;
+  Sequence q{};
+  if (tid < p.batch) {
+    q = load_sequence<C>(p, tid, refused, backwards);
+    if (q.steps > 0) {
+      weight = q.steps + 1;
+      groups = (q.n + C::kQueries - 1) / C::kQueries;
+    }
+  }
+  if (refused && blockIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+  if (__syncthreads_or(backwards)) return false;  // sequences overlap
+  if (weight > 0) atomicAdd(&s.hist[groups], weight);
+  __syncthreads();
+  if (warp == 0) {
+    // lane r: the steps of list r (the same for every KV head)
+    int total = 0;
+    for (int g = lane + 1; g <= p.groups; ++g) total += s.hist[g];
+    if (lane >= p.groups) total = 0;
+    const int g = static_cast<int>(blockIdx.x);
+    if (p.whole) {
+      if (lane == 0) {
+        const int per_seq = p.groups * C::kHkv;
+        s.sched[0] = g % per_seq / C::kHkv;
+        s.sched[1] = g % C::kHkv;
+        s.sched[2] = 1;
+        s.sched[3] = g / per_seq;
+        s.sched[4] = 0;
+      }
+    } else {
+      const int grid = static_cast<int>(gridDim.x);
+      const int sum = __reduce_add_sync(0xffffffffu, total);
+      int lo = max(kMinPer, static_cast<int>((static_cast<long long>(sum) * C::kHkv + grid - 1) / grid));
+      int hi = max(lo, __reduce_max_sync(0xffffffffu, total));
+      const auto runs = [&](int per) { return __reduce_add_sync(0xffffffffu, (total + per - 1) / per) * C::kHkv; };
+      if (runs(lo) <= grid) {
+        hi = lo;
+      } else {
+        while (lo + 1 < hi) {  // runs(lo) > grid >= runs(hi)
+          const int mid = (lo + hi) >> 1;
+          if (runs(mid) <= grid) hi = mid; else lo = mid;
+        }
+      }
+      const int per = hi;
+      const int mine = (total + per - 1) / per * C::kHkv;  // this list's blocks
+      int before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += u;
+      }
+      before -= mine;
+      const unsigned here = __ballot_sync(0xffffffffu, mine > 0 && before <= g && g < before + mine);
+      if (lane == 0) {
+        s.sched[0] = 0;
+        s.sched[1] = 0;
+        s.sched[3] = -1;  // no run: the block has nothing to do
+      }
+      __syncwarp();
+      if (here && lane == __ffs(here) - 1) {
+        s.sched[0] = lane;
+        s.sched[1] = (g - before) % C::kHkv;
+        s.sched[3] = (g - before) / C::kHkv;
+      }
+      if (lane == 0) {
+        s.sched[2] = per;
+        s.sched[4] = C::kHkv;
+      }
+    }
+  }
+  __syncthreads();
+  // the running sums of this block's list
+  const int mine = groups > s.sched[0] ? weight : 0;
+  int sum = mine;
+  if (tid < kMaxBatch) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    if (lane == 31) s.warp_sum[warp] = sum;
+  }
+  __syncthreads();
+  if (tid < p.batch) {
+    for (int w = 0; w < warp; ++w) sum += s.warp_sum[w];
+    s.pre[tid + 1] = sum;
+  }
+  if (tid == 0) s.pre[0] = 0;
+  __syncthreads();
+  return true;
+}
+
+// Tells the merge which sequence is cut first in this block; run by one thread.
+template <typename C, typename S>
+__device__ __forceinline__ void note_cut(const TreeParams& p, const S& s) {
+  Walk<C> walk;
+  walk.start(p, s);
+  Segment g;
+  int4 cut = make_int4(0, 0, 0, 0);
+  while (walk.next(p, s, g)) {
+    if (g.s0 == 0 && !g.whole) {
+      const int last = (s.pre[g.b] + g.q.steps) / s.sched[2];  // the run that holds its last step
+      cut = make_int4(g.row0, g.nodes | (walk.kv << 8), g.slot, last - s.sched[3] + 1);
+    }
+  }
+  p.cuts[blockIdx.x] = cut;
+}
+
+template <typename C>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
+  using prefill_tc::kHeadroom;
+  using prefill_tc::kSlack;
+  using prefill_tc::tma_load_3d;
+  using prefill_tc::tma_load_4d;
+  constexpr int kD = C::kD, kG = C::kG, kN = C::kN, kHalf = C::kHalf, kTiles = C::kTiles;
+  extern __shared__ uint8_t smem_raw[];
+  typename C::Smem& s =
+      *reinterpret_cast<typename C::Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kKStages; ++i) {
+      mbar_init(&s.k_full[i], 1);
+      mbar_init(&s.k_empty[i], 1);
+    }
+    for (int i = 0; i < C::kVStages; ++i) {
+      mbar_init(&s.v_full[i], 1);
+      mbar_init(&s.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.s_free[i], 8);
+      mbar_init(&s.p_full[i], 8);
+      mbar_init(&s.p_empty[i], 1);
+    }
+    mbar_init(&s.q_ready, 1);
+    mbar_init(&s.q_empty, 1);
+    mbar_init(&s.o_full, 2);  // the last product's commit, and the issuer (poison)
+    mbar_init(&s.o_free, 8);
+    mbar_init(&s.mma_done, 2);
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tensor_map(&tm_q);
+    prefetch_tensor_map(&tm_k);
+    prefetch_tensor_map(&tm_v);
+  }
+  if (warp == 10) tmem_alloc(&s.tmem_base, C::kTmemCols);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = s.tmem_base;
+
+  // q, the cache and the tables may be written by the previous kernel in the stream.
+  wait_for_primary_grid();
+  allow_dependent_launch();
+  const bool run = make_schedule<C>(p, s);
+  if (!run) {
+    if (threadIdx.x == 0 && !p.whole) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+  } else if (warp == 8) {
+    // ---------------- Q and K producer: lane i < 8 copies page i of a step, chunk by chunk ----------------
+    if (lane == 0 && !p.whole) note_cut<C>(p, s);
+    __syncwarp();
+    bool ok = true;
+    int gt = 0, gk = 0;  // segments, K chunks
+    Walk<C> walk;
+    walk.start(p, s);
+    Segment g;
+    while (ok && walk.next(p, s, g)) {
+      if (gt >= 1) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.q_empty, (gt - 1) & 1));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&s.q_ready, C::kChunks * p.q_box * kG * 128);
+      __syncwarp();
+      if (lane < C::kChunks) tma_load_4d(s.q[lane], &tm_q, 0, lane, walk.kv * kG, g.row0, &s.q_ready);
+      ++gt;
+      const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks + g.q.page0;
+      const auto entry = [&](int j) {
+        const int pg = j * kStepPages + lane;
+        return j < g.s1 && lane < kStepPages && pg < g.q.pages ? table[pg] : 0;
+      };
+      int next_id = entry(g.s0);
+      for (int j = g.s0; j < g.s1 && ok; ++j) {
+        const int id = next_id;
+        next_id = entry(j + 1);
+        const int np = min(kStepPages, g.q.pages - j * kStepPages);
+        int32_t y = id * kPage;
+        if (lane < np && (id < 0 || static_cast<int64_t>(id) >= p.num_pages)) {
+          report(p.status, ATTN_DEV_BAD_PAGE);
+          y = -kPage;
+        }
+        for (int ch = 0; ch < C::kChunks; ++ch) {
+          const int st = gk % C::kKStages;
+          if (gk >= C::kKStages) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.k_empty[st], ((gk / C::kKStages) - 1) & 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&s.k_full[st], np * kPage * 128);
+          __syncwarp();
+          if (lane < np)
+            tma_load_3d(s.k[st] + lane * (kPage * 128), &tm_k, 0, y, walk.kv * C::kChunks + ch, &s.k_full[st]);
+          ++gk;
+          __syncwarp();
+        }
+      }
+    }
+    if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+    if (lane == 0) {  // no copy may still be landing, nor a commit arriving, when the CTA retires
+      if (gt >= 1) {
+        if (!mbar_wait(&s.q_ready, (gt - 1) & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+        if (ok && !mbar_wait(&s.q_empty, (gt - 1) & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+      }
+      for (int st = 0; st < C::kKStages && st < gk; ++st) {
+        const int uses = (gk - 1 - st) / C::kKStages;
+        if (!mbar_wait(&s.k_full[st], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+        if (ok && !mbar_wait(&s.k_empty[st], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------- V producer: a page per stage ----------------
+    bool ok = true;
+    int gv = 0;
+    Walk<C> walk;
+    walk.start(p, s);
+    Segment g;
+    while (ok && walk.next(p, s, g)) {
+      const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks + g.q.page0;
+      const int first = g.s0 * kStepPages;
+      const int last = min(g.s1 * kStepPages, g.q.pages);
+      const auto entry = [&](int pg) { return pg < last ? table[pg] : 0; };
+      int cur = 0, nxt = entry(first + lane);
+      for (int pg = first; pg < last && ok; ++pg) {
+        const int u = (pg - first) & 31;
+        if (u == 0) {
+          cur = nxt;
+          nxt = entry(pg + 32 + lane);
+        }
+        const int id = __shfl_sync(0xffffffffu, cur, u);
+        const int st = gv % C::kVStages;
+        if (gv >= C::kVStages) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.v_empty[st], ((gv / C::kVStages) - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) {
+          const bool there = id >= 0 && static_cast<int64_t>(id) < p.num_pages;  // (the K producer reports)
+          mbar_arrive_expect_tx(&s.v_full[st], C::kVPage);
+          tma_load_3d(s.v[st], &tm_v, 0, there ? id * kPage : -kPage, walk.kv * C::kChunks, &s.v_full[st]);
+        }
+        ++gv;
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+    if (lane == 0) {
+      for (int st = 0; st < C::kVStages && st < gv; ++st) {
+        const int uses = (gv - 1 - st) / C::kVStages;
+        if (!mbar_wait(&s.v_full[st], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+        if (ok && !mbar_wait(&s.v_empty[st], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+      }
+    }
+  } else if (warp == 10) {
+    // ---------------- S^T issuer (whole warp; an elected lane issues) ----------------
+    bool ok = true;
+    int gt = 0, gs = 0, st = 0, st_ph = 0;
+    const uint32_t q_base = smem_addr(s.q[0]);
+    Walk<C> walk;
+    walk.start(p, s);
+    Segment g;
+    while (walk.next(p, s, g)) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.q_ready, gt & 1));
+      const uint32_t idesc = prefill_tc::warp_uniform_int(umma_idesc_bf16(128, g.N, 0, 0));
+      const int steps = prefill_tc::warp_uniform_int(g.s1 - g.s0);
+      for (int j = 0; j < steps; ++j) {
+        const int sb = gs & 1;
+        if (ok && gs >= 2) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.s_free[sb], ((gs >> 1) - 1) & 1));
+        const uint32_t d = tmem + C::kSCol + sb * kN;
+        for (int ch = 0; ch < C::kChunks; ++ch) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.k_full[st], st_ph));
+          tc_fence_after_sync();
+          const uint32_t k_base = smem_addr(s.k[st]);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_warp(d, umma_desc(k_base + kk * 32, 16, 1024, 2),
+                           umma_desc(q_base + ch * (kN * 128) + kk * 32, 16, 1024, 2), idesc, (ch | kk) > 0 ? 1u : 0u);
+          umma_commit_warp(&s.k_empty[st]);
+          if (++st == C::kKStages) st = 0, st_ph ^= 1;
+        }
+        umma_commit_warp(&s.s_full[sb]);
+        ++gs;
+      }
+      umma_commit_warp(&s.q_empty);
+      ++gt;
+    }
+    // the softmax warps' last arrivals on s_free (not waited for above)
+    for (int k = gs >= 2 ? gs - 2 : 0; k < gs; ++k)
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.s_free[k & 1], (k >> 1) & 1));
+    umma_commit_warp(&s.mma_done);
+    if (!__all_sync(0xffffffffu, mbar_wait_fast(&s.mma_done, 0))) ok = false;  // every product done before the memory is freed
+    if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+  } else if (warp == 11) {
+    // ---------------- O^T issuer; it also cleans the rows of V that not every node sees ----------------
+    bool ok = true;
+    int gt = 0, gs = 0, st = 0, st_ph = 0;
+    Walk<C> walk;
+    walk.start(p, s);
+    Segment g;
+    while (walk.next(p, s, g)) {
+      if (ok && gt >= 1) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.o_free, (gt - 1) & 1));
+      const uint32_t idesc = prefill_tc::warp_uniform_int(umma_idesc_bf16(128, g.N, 1, 1));
+      bool poison = false;
+      const int all0 = all_from(g.q, p.window);
+      for (int j = g.s0; j < g.s1; ++j) {
+        const int pb = gs & 1;
+        const int np = prefill_tc::warp_uniform_int(min(kStepPages, g.q.pages - j * kStepPages));
+        const uint32_t p_base = smem_addr(s.p[pb]);
+        for (int kk = 0; kk < np; ++kk) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.v_full[st], st_ph));
+          const uint32_t v_base = smem_addr(s.v[st]);
+          const int pos0 = (g.q.page0 + j * kStepPages + kk) * kPage;
+          if (ok && (pos0 < all0 || pos0 < g.q.lo || pos0 + kPage > g.q.ctx)) {
+            for (int r = 0; r < kPage; ++r) {
+              const int pos = pos0 + r;
+              const bool none = pos < g.q.lo || pos >= g.q.L;
+              if (!none && pos >= all0 && pos < g.q.ctx) continue;
+#pragma unroll
+              for (int c0 = 0; c0 < C::kChunks; c0 += 4) {
+                const uint32_t at = v_base + (c0 + (lane >> 3)) * (kPage * 128) + r * 128 + (lane & 7) * 16;
+                if (none) {
+                  st_shared_v4(at, make_uint4(0, 0, 0, 0));
+                  continue;
+                }
+                const uint4 x = ld_shared_v4(at);
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                bool clean = true;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const bool a = finite_bf16(w[e]), b = finite_bf16(w[e] >> 16);
+                  clean &= a && b;
+                  w[e] &= (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
+                }
+                if (!clean) {
+                  st_shared_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
+                  poison = true;
+                }
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (kk == 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_full[pb], (gs >> 1) & 1));
+          tc_fence_after_sync();
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t)
+            umma_bf16_warp(tmem + t * kN, umma_desc(v_base + t * (2 * kPage * 128), kPage * 128, 1024, 2),
+                           umma_desc(p_base + kk * (kPage * 128), C::kPChunk, 1024, 2), idesc,
+                           (j > g.s0 || kk > 0) ? 1u : 0u);
+          umma_commit_warp(&s.v_empty[st]);
+          if (++st == C::kVStages) st = 0, st_ph ^= 1;
+        }
+        umma_commit_warp(&s.p_empty[pb]);
+        ++gs;
+      }
+      umma_commit_warp(&s.o_full);
+      poison = __any_sync(0xffffffffu, poison);
+      if (lane == 0) {
+        s.poison = poison;
+        mbar_arrive(&s.o_full);
+      }
+      __syncwarp();
+      ++gt;
+    }
+    if (ok && gt >= 1) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.o_free, (gt - 1) & 1));
+    umma_commit_warp(&s.mma_done);
+    if (!__all_sync(0xffffffffu, mbar_wait_fast(&s.mma_done, 0))) ok = false;
+    if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+  } else {
+    // ---------------- softmax and epilogue: thread = key of the step, then dim of a tile ----------------
+    const int h = warp >> 2;                // half of the columns
+    const int key = threadIdx.x & 127;      // tensor-memory lane
+    const int gtid = threadIdx.x & 127;     // thread of the warpgroup
+    const uint32_t bar = 2 + h;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const auto fmax2 = [](float a, float b) { return fmaxf(a, b); };
+    const auto add2 = [](float a, float b) { return a + b; };
+    bool ok = true;
+    int gt = 0, gs = 0;
+    Walk<C> walk;
+    walk.start(p, s);
+    Segment g;
+    while (walk.next(p, s, g)) {
+      // the sequence's tree, once all are done with the last one's
+      named_barrier_sync(1, kSoftmaxThreads);
+      if (warp == 0) {
+        int parent[2], depth[2];
+        unsigned long long mask[2];
+        if (load_parents(p.parents + g.q.q0, g.q.n, parent) && lane == 0) report(p.status, ATTN_DEV_BAD_TREE);
+        depths(parent, depth);
+        ancestors(parent, mask);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          s.anc[lane + 32 * u] = mask[u];
+          s.depth[lane + 32 * u] = depth[u];
+        }
+      }
+      const int half = g.N >> 1;
+      const int c0 = h * half;  // this warpgroup's first column
+      if (gtid < half) {
+        s.m[c0 + gtid] = 0.f;
+        s.bound[c0 + gtid] = -INFINITY;
+      }
+      named_barrier_sync(1, kSoftmaxThreads);
+      const int all0 = all_from(g.q, p.window);
+      const int node0 = walk.group * C::kQueries;
+      float l[kHalf];
+#pragma unroll
+      for (int c = 0; c < kHalf; ++c) l[c] = 0.f;
+
+      for (int j = g.s0; j < g.s1; ++j) {
+        const int sb = gs & 1;
+        const int step0 = (g.q.page0 + j * kStepPages) * kPage;
+        const int pos = step0 + key;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.s_full[sb], (gs >> 1) & 1));
+        tc_fence_after_sync();
+        float sv[kHalf];
+#pragma unroll
+        for (int b8 = 0; b8 < kHalf / 8; ++b8) {
+          if (8 * b8 < half) {
+            tmem_ld8(t_row + C::kSCol + sb * kN + c0 + 8 * b8, *reinterpret_cast<float(*)[8]>(&sv[8 * b8]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sv[8 * b8 + e] = -INFINITY;
+          }
+        }
+        tmem_wait_ld();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.s_free[sb]);
+
+        if (step0 < all0 || step0 + kKeys > g.q.ctx) {
+          unsigned long long vis = 0;
+          for (int i = 0; i < g.nodes; ++i)
+            if (pos >= g.q.lo && sees(g.q, p.window, s, node0 + i, pos)) vis |= 1ull << i;
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c)
+            if (!((vis >> ((c0 + c) / kG)) & 1)) sv[c] = -INFINITY;
+        }
+        bool moves = false;
+#pragma unroll
+        for (int c4 = 0; c4 < kHalf / 4; ++c4) {
+          if (4 * c4 < half) {
+            const float4 t = *reinterpret_cast<const float4*>(&s.bound[c0 + 4 * c4]);
+            moves |= sv[4 * c4] > t.x || sv[4 * c4 + 1] > t.y || sv[4 * c4 + 2] > t.z || sv[4 * c4 + 3] > t.w;
+          }
+        }
+        if (barrier_or(bar, 128, moves)) {
+          reduce_into<kHalf>(sv, s.red[warp], fmax2);
+          named_barrier_sync(bar, 128);
+          if (gtid < half) {
+            const int w0 = h * 4;
+            const float mx = fmaxf(fmaxf(s.red[w0][gtid], s.red[w0 + 1][gtid]), fmaxf(s.red[w0 + 2][gtid], s.red[w0 + 3][gtid]));
+            float f = 1.f;
+            if (mx > s.bound[c0 + gtid]) {
+              const float m = fmaf(mx, kLog2e, kHeadroom);
+              if (s.bound[c0 + gtid] != -INFINITY) f = ex2_approx(s.m[c0 + gtid] - m);
+              s.m[c0 + gtid] = m;
+              s.bound[c0 + gtid] = (m + kSlack) * (1.f / kLog2e);
+            }
+            s.f[c0 + gtid] = f;
+          }
+          named_barrier_sync(bar, 128);
+#pragma unroll
+          for (int c = 0; c < kHalf; ++c)
+            if (c < half) l[c] *= s.f[c0 + c];
+          if (j > g.s0) {
+            // O^T holds the products up to step j - 1: wait for the last, then scale in place
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[(gs - 1) & 1], ((gs - 1) >> 1) & 1));
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int c = 0; c < half; c += 8) {
+              const float4 f0 = *reinterpret_cast<const float4*>(&s.f[c0 + c]);
+              const float4 f1 = *reinterpret_cast<const float4*>(&s.f[c0 + c + 4]);
+              float ov[kTiles][8];
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) tmem_ld8(t_row + t * kN + c0 + c, ov[t]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) {
+                const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(ov[t][e] * f[e]);
+                tmem_st8(t_row + t * kN + c0 + c, w);
+              }
+            }
+            tmem_wait_st();
+          }
+        }
+        // weights; the buffer's last reader was the product of step j - 2
+        if (ok && gs >= 2) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[sb], ((gs >> 1) - 1) & 1));
+#pragma unroll
+        for (int b8 = 0; b8 < kHalf / 8; ++b8) {
+          if (8 * b8 < half) {
+            const float4 m0 = *reinterpret_cast<const float4*>(&s.m[c0 + 8 * b8]);
+            const float4 m1 = *reinterpret_cast<const float4*>(&s.m[c0 + 8 * b8 + 4]);
+            const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              w[e] = ex2_approx(fmaf(sv[8 * b8 + e], kLog2e, -m[e]));
+              l[8 * b8 + e] += w[e];
+            }
+            const int col = c0 + 8 * b8;
+            st_shared_v4(smem_addr(s.p[sb]) + (col >> 6) * C::kPChunk + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4),
+                         make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]),
+                                    pack_bf16x2(w[6], w[7])));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.p_full[sb]);
+        ++gs;
+      }
+
+      // ---- end of the segment: sums, then this thread's dim of every row ----
+      reduce_into<kHalf>(l, s.red[warp], add2);
+      named_barrier_sync(bar, 128);
+      if (gtid < half) {
+        const int w0 = h * 4, col = c0 + gtid;
+        const float sum = (s.red[w0][gtid] + s.red[w0 + 1][gtid]) + (s.red[w0 + 2][gtid] + s.red[w0 + 3][gtid]);
+        if (g.whole)
+          s.f[col] = sum > 0.f ? 1.f / sum : sum;  // 0: a row that sees nothing; NaN stays
+        else if (col < g.cols)
+          p.part_ml[static_cast<size_t>(g.slot) * kN + col] = partial_stats(s.m[col], sum);
+      }
+      named_barrier_sync(bar, 128);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.o_full, gt & 1));
+      tc_fence_after_sync();
+      const bool poison = s.poison != 0;
+#pragma unroll 1
+      for (int c = 0; c < half; c += 8) {
+        float ov[kTiles][8];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) tmem_ld8(t_row + t * kN + c0 + c, ov[t]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          const int d = t * 128 + gtid;
+          if (poison) {
+            // the elements that were zeroed, for the rows that see them
+            const int end = min(g.q.L, (g.q.page0 + g.s1 * kStepPages) * kPage);
+            for (int pos = max(g.q.lo, (g.q.page0 + g.s0 * kStepPages) * kPage); pos < end; ++pos) {
+              if (pos >= all0 && pos < g.q.ctx) {
+                pos = min(g.q.ctx, end) - 1;
+                continue;
+              }
+              const int id = p.block_table[static_cast<int64_t>(g.b) * p.max_blocks + pos / kPage];
+              if (id < 0 || static_cast<int64_t>(id) >= p.num_pages) continue;
+              const size_t row = static_cast<size_t>(id) * kPage + pos % kPage;
+              const float v = __bfloat162float(p.v_pool[(row * C::kHkv + walk.kv) * kD + d]);
+              if (fabsf(v) < INFINITY) continue;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (c0 + c + e < g.cols && sees(g.q, p.window, s, node0 + (c0 + c + e) / kG, pos)) ov[t][e] += v;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int col = c0 + c + e;
+            if (col >= g.cols) continue;
+            if (g.whole) {
+              const size_t at =
+                  (static_cast<size_t>(g.row0 + col / kG) * C::kHq + walk.kv * kG + col % kG) * kD + d;
+              const float v = ov[t][e] * s.f[col];
+              if (p.out_f32)
+                static_cast<float*>(p.o)[at] = v;
+              else
+                static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(v);
+            } else {
+              p.part_o[(static_cast<size_t>(g.slot) * kN + col) * kD + d] = ov[t][e];
+            }
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.o_free);  // the next segment's first product may overwrite O^T
+      ++gt;
+    }
+    // the last products' commits (not all waited for above)
+    for (int k = gs >= 2 ? gs - 2 : 0; k < gs; ++k)
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[k & 1], (k >> 1) & 1));
+    if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+  }
+
+  // ---------------- teardown: free the tensor memory ----------------
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 10) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The cut sequences' rows, joined from their partials: o = sum 2^(m_i - M) O_i /
+// sum 2^(m_i - M) l_i.  Every block reads the cuts that the blocks of the first kernel
+// noted and takes rows blockIdx.x, blockIdx.x + gridDim.x, ... of them all; groups of D / 4
+// threads, four dims a thread, take a row's partials in turn, kInFlight loads in
+// flight, and meet in shared memory.
+// ---------------------------------------------------------------------------
+constexpr int kMergeGroups = 4;
+constexpr int kMergeInFlight = 8;
+
+struct MergeParams {
+  TreeParams t;
+  int32_t grid;    // blocks of the first kernel
+  int32_t stride;  // distance of consecutive blocks of a list: KV heads
+};
+
+template <typename C>
+__global__ void __launch_bounds__(kMergeGroups* C::kD / 4) merge_kernel(const __grid_constant__ MergeParams mp) {
+  const TreeParams& p = mp.t;
+  constexpr int kD = C::kD, kGroupThreads = kD / 4, kThreadsHere = kMergeGroups * kGroupThreads;
+  __shared__ int32_t s_rows[kMaxGrid + 1];
+  __shared__ int32_t s_warp[kThreadsHere / 32];
+  __shared__ float s_m[kMergeGroups], s_l[kMergeGroups];
+  __shared__ float4 s_o[kMergeGroups][kGroupThreads];
+  const int tid = threadIdx.x % kGroupThreads, group = threadIdx.x / kGroupThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_for_primary_grid();
+  allow_dependent_launch();
+  // running sum of the cut rows
+  int carry = 0;
+  if (threadIdx.x == 0) s_rows[0] = 0;
+  for (int g0 = 0; g0 < mp.grid; g0 += kThreadsHere) {
+    const int g = g0 + threadIdx.x;
+    int n = 0;
+    if (g < mp.grid) {
+      const int4 cut = p.cuts[g];
+      n = cut.w > 0 ? (cut.y & 255) * C::kG : 0;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += u;
+    }
+    if (lane == 31) s_warp[warp] = n;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kThreadsHere / 32; ++w) {
+      if (w < warp) n += s_warp[w];
+      total += s_warp[w];
+    }
+    if (g < mp.grid) s_rows[g + 1] = carry + n;
+    carry += total;
+    __syncthreads();
+  }
+  for (int row = blockIdx.x; row < carry; row += gridDim.x) {
+    int lo = 0, hi = mp.grid - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_rows[mid] <= row) lo = mid; else hi = mid - 1;
+    }
+    const int4 cut = p.cuts[lo];
+    const int col = row - s_rows[lo], kv = cut.y >> 8, parts = cut.w;
+    float M = -INFINITY, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = group; i0 < parts; i0 += kMergeGroups * kMergeInFlight) {
+      float2 e[kMergeInFlight];
+      float4 a[kMergeInFlight];
+#pragma unroll
+      for (int u = 0; u < kMergeInFlight; ++u) {
+        const int i = i0 + u * kMergeGroups;
+        e[u] = make_float2(-INFINITY, 0.f);
+        a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < parts) {
+          const size_t at = static_cast<size_t>(i == 0 ? cut.z : 2 * (lo + i * mp.stride)) * C::kN + col;
+          e[u] = p.part_ml[at];
+          a[u] = __ldcs(reinterpret_cast<const float4*>(p.part_o + at * kD + 4 * tid));
+        }
+      }
+      float m = M;
+#pragma unroll
+      for (int u = 0; u < kMergeInFlight; ++u)
+        if (e[u].y > 0.f) m = fmaxf(m, e[u].x);
+      if (m == -INFINITY) continue;
+      const float f = M == -INFINITY ? 0.f : exp2f(M - m);
+      L *= f;
+      O.x *= f; O.y *= f; O.z *= f; O.w *= f;
+#pragma unroll
+      for (int u = 0; u < kMergeInFlight; ++u) {
+        if (e[u].y > 0.f) {
+          const float w = exp2f(e[u].x - m);
+          L += w * e[u].y;
+          O.x += w * a[u].x; O.y += w * a[u].y; O.z += w * a[u].z; O.w += w * a[u].w;
+        }
+      }
+      M = m;
+    }
+    if (tid == 0) {
+      s_m[group] = M;
+      s_l[group] = L;
+    }
+    s_o[group][tid] = O;
+    __syncthreads();
+    if (group == 0) {
+      float m = M;
+#pragma unroll
+      for (int w = 1; w < kMergeGroups; ++w) m = fmaxf(m, s_m[w]);
+      L = 0.f;
+      O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kMergeGroups; ++w) {
+        const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - m);
+        const float4 v = s_o[w][tid];
+        L += f * s_l[w];
+        O.x += f * v.x; O.y += f * v.y; O.z += f * v.z; O.w += f * v.w;
+      }
+      const float inv = L > 0.f ? 1.f / L : L;
+      const size_t at =
+          (static_cast<size_t>(cut.x + col / C::kG) * C::kHq + kv * C::kG + col % C::kG) * kD + 4 * tid;
+      const float4 v = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
+      if (p.out_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = v;
+      } else {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      }
+    }
+    __syncthreads();  // the shared rows were read
+  }
+}
+
+// D = 512: 64 rows, four nodes; D = 256: 128 rows, 64 nodes, or fewer with longer rings.
+using GlobalConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 4, 3>;
+using SlidingWideConfig = Config<ATTN_SLIDING_D, ATTN_SLIDING_HQ / ATTN_SLIDING_HKV, ATTN_SLIDING_HKV, 128, 3, 5>;
+using SlidingConfig = Config<ATTN_SLIDING_D, ATTN_SLIDING_HQ / ATTN_SLIDING_HKV, ATTN_SLIDING_HKV, 32, 6, 8>;
+
+}  // namespace tree
+}  // namespace pda

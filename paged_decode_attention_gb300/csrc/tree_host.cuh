@@ -1,0 +1,363 @@
+// tree_host.cuh -- host side of include/attn_tree.h (the tree append's is
+// serving.cuh's run_chunk).  Included in attn_decode.cu, whose validation helpers,
+// tensor-map encoder and launch recording it shares.
+#pragma once
+
+#include "attn_tree.h"
+#include "kv_commit.cuh"
+#include "pages.cuh"
+#include "tree_decode.cuh"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Attention of trees
+// ---------------------------------------------------------------------------
+// A call of few, short sequences: every (sequence, group, KV head) in a block of its
+// own, and no merge kernel.
+constexpr int kTreeWholeSteps = 2;
+
+struct TreePlan {
+  int rows;      // of the configuration's groups
+  int groups;    // per KV head
+  int grid;
+  bool whole;
+  bool merge;    // a sequence may be cut: a second kernel
+  size_t part_o_bytes, part_ml_bytes, workspace_bytes;
+};
+
+// The sliding configuration for trees of few nodes: 32 rows, longer rings.
+bool narrow_tree(int32_t kind, int32_t max_q) {
+  return kind == ATTN_KIND_SLIDING && max_q <= pda::tree::SlidingConfig::kQueries;
+}
+
+int32_t make_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_seq_len, int32_t window,
+                       int32_t num_splits, int32_t num_sms, TreePlan* out) {
+  namespace tr = pda::tree;
+  if (kind != ATTN_KIND_SLIDING && kind != ATTN_KIND_GLOBAL) return fail(ATTN_ERR_INVALID_ARG, "unknown kind %d", kind);
+  if (batch < 1 || batch > ATTN_MAX_BATCH) return fail(ATTN_ERR_INVALID_ARG, "batch %d outside [1, %d]", batch, ATTN_MAX_BATCH);
+  if (max_q < 0 || max_q > ATTN_MAX_TREE) return fail(ATTN_ERR_INVALID_ARG, "max_q %d outside [0, %d]", max_q, ATTN_MAX_TREE);
+  if (max_seq_len < 0 || max_seq_len > ATTN_MAX_SEQ_LEN)
+    return fail(ATTN_ERR_INVALID_ARG, "max_seq_len %d outside [0, %d]", max_seq_len, ATTN_MAX_SEQ_LEN);
+  if (num_sms < 1) return fail(ATTN_ERR_INVALID_ARG, "num_sms must be >= 1");
+  if (num_splits < 0 || (num_splits > 0 && num_splits < tr::kMaxGroups) || num_splits > tr::kMaxGrid)
+    return fail(ATTN_ERR_INVALID_ARG, "num_splits must be 0 or in [%d, %d]", tr::kMaxGroups, tr::kMaxGrid);
+  const bool sliding = kind == ATTN_KIND_SLIDING;
+  const int d = sliding ? ATTN_SLIDING_D : ATTN_GLOBAL_D;
+  const int hkv = sliding ? ATTN_SLIDING_HKV : ATTN_GLOBAL_HKV;
+  out->rows = !sliding ? tr::GlobalConfig::kN : narrow_tree(kind, max_q) ? tr::SlidingConfig::kN : tr::SlidingWideConfig::kN;
+  const int queries = out->rows * hkv / 16;  // 16 query heads
+  out->groups = std::max(1, (max_q + queries - 1) / queries);
+  // pages of one sequence: with a window those of window + max_q - 1 positions
+  const int64_t span = window > 0 ? std::min<int64_t>(max_seq_len, static_cast<int64_t>(window) + max_q - 1) : max_seq_len;
+  const int64_t pages = std::min<int64_t>((span + 2 * ATTN_PAGE_SIZE - 2) / ATTN_PAGE_SIZE,
+                                          (static_cast<int64_t>(max_seq_len) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE);
+  const int64_t steps = std::max<int64_t>(1, (pages + tr::kStepPages - 1) / tr::kStepPages);
+  const int64_t items = static_cast<int64_t>(batch) * out->groups * hkv;
+  out->whole = num_splits == 0 && items <= num_sms && steps <= kTreeWholeSteps;
+  out->merge = !out->whole && steps > 1;
+  if (out->whole) {
+    out->grid = static_cast<int>(items);
+  } else if (num_splits > 0) {
+    out->grid = num_splits;
+  } else {
+    const int64_t useful = (items * (steps + 1) + tr::kMinPer - 1) / tr::kMinPer;
+    out->grid = static_cast<int>(std::max<int64_t>(tr::kMaxGroups, std::min<int64_t>({num_sms, useful, tr::kMaxGrid})));
+  }
+  const size_t rows = 2 * static_cast<size_t>(out->grid) * out->rows;
+  out->part_o_bytes = out->merge ? align256(rows * d * sizeof(float)) : 0;
+  out->part_ml_bytes = out->merge ? align256(rows * sizeof(float2)) : 0;
+  out->workspace_bytes = out->part_o_bytes + out->part_ml_bytes + align256(static_cast<size_t>(out->grid) * sizeof(int4));
+  return ATTN_OK;
+}
+
+// Q [total_q, Hq, D] as {64 dims, D/64 chunks, Hq heads, total_q nodes}: a box {64, 1, G,
+// nq} copies one 64-dim chunk of nq consecutive nodes' G heads of a KV head as
+// [node][head][128 B], 128-byte swizzled; nodes past total_q read as zeros.
+int32_t encode_tree_q_map(CUtensorMap* map, const void* q, int32_t total_q, int hq, int d, int g, int nq) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(hq),
+                              static_cast<cuuint64_t>(total_q)};
+  const cuuint64_t strides[3] = {128, static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(hq) * d * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(nq)};
+  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, elem_strides,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled (tree q map) failed (%d)", static_cast<int>(r));
+  return ATTN_OK;
+}
+
+template <typename C>
+int32_t launch_tree(const char* name, const void* q, const void* k_pool, const void* v_pool, int32_t total_q,
+                    const TreePlan& plan, int dev, int num_sms, pda::tree::TreeParams& p, cudaStream_t s) {
+  namespace tr = pda::tree;
+  // nodes a copy brings: no more than the longest tree's, whole groups of 16 rows
+  constexpr int kUnit = C::kG < 16 ? 16 / C::kG : 1;
+  p.q_box = std::min(C::kQueries, (p.max_q + kUnit - 1) / kUnit * kUnit);
+  CUtensorMap tm_q, tm_k, tm_v;
+  int32_t st;
+  if ((st = encode_tree_q_map(&tm_q, q, total_q, C::kHq, C::kD, C::kG, p.q_box)) ||
+      (st = encode_chunk_map(&tm_k, k_pool, p.num_pages, C::kHkv * C::kD, 1)) ||
+      (st = encode_chunk_map(&tm_v, v_pool, p.num_pages, C::kHkv * C::kD, C::kChunks)))
+    return st;
+  static bool main_set[kMaxDevices] = {false}, merge_set[kMaxDevices] = {false};
+  if ((st = ensure_smem(tr::tree_kernel<C>, C::kSmemBytes, dev, main_set)) ||
+      (st = ensure_smem(tr::merge_kernel<C>, 0, dev, merge_set)))
+    return st;
+  cudaError_t e = launch_pdl(tr::tree_kernel<C>, dim3(plan.grid), tr::kThreads, C::kSmemBytes, s, tm_q, tm_k, tm_v, p);
+  if (e == cudaSuccess && plan.merge) {
+    tr::MergeParams mp;
+    mp.t = p;
+    mp.grid = plan.grid;
+    mp.stride = C::kHkv;
+    constexpr int kBlockThreads = tr::kMergeGroups * C::kD / 4;
+    const int64_t rows = static_cast<int64_t>(p.batch) * p.max_q * C::kHq;
+    const int blocks = static_cast<int>(std::min<int64_t>(rows, static_cast<int64_t>(num_sms) * (2048 / kBlockThreads)));
+    e = launch_pdl(tr::merge_kernel<C>, dim3(blocks), kBlockThreads, 0, s, mp);
+  }
+  return launched(name, e);
+}
+
+int32_t run_tree(int32_t kind, const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                 const int32_t* seq_lens, const int32_t* cu_q, const int32_t* parents, void* o, int32_t batch,
+                 int32_t total_q, int32_t max_q, int32_t max_blocks, int64_t num_pages, int32_t max_seq_len,
+                 int32_t window, int32_t out_dtype, int32_t num_splits, void* workspace, size_t workspace_bytes,
+                 int32_t* status, void* stream) {
+  g_err[0] = '\0';
+  const bool sliding = kind == ATTN_KIND_SLIDING;
+  const char* name = sliding ? "attn_decode_sliding_tree" : "attn_decode_global_tree";
+  if (!k_pool || !v_pool || !block_table || !seq_lens || !cu_q || (total_q > 0 && (!q || !parents || !o)))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: null array pointer", name);
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || !aligned_to(block_table, 4) ||
+      !aligned_to(seq_lens, 4) || !aligned_to(cu_q, 4) || !aligned_to(parents, 4) || !aligned_to(status, 4))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: misaligned pointer (q, o and the pools 16 bytes, tables 4)", name);
+  int32_t st;
+  if ((st = check_batch(name, batch, max_blocks)) || (st = check_pages(name, "num_pages", num_pages)) ||
+      (st = check_max_seq_len(name, max_seq_len, max_blocks)))
+    return st;
+  if (total_q < 0) return fail(ATTN_ERR_INVALID_ARG, "%s: total_q must be >= 0", name);
+  if (max_q < 0) return fail(ATTN_ERR_INVALID_ARG, "%s: max_q must be >= 0", name);
+  if (max_q > ATTN_MAX_TREE)
+    return fail(ATTN_ERR_UNSUPPORTED, "%s: max_q %d beyond %d nodes", name, max_q, ATTN_MAX_TREE);
+  if (sliding && window <= 0)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: window must be > 0 (the node's is 1024)", name);
+  if (out_dtype != ATTN_OUT_BF16 && out_dtype != ATTN_OUT_F32)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: out_dtype must be ATTN_OUT_BF16 or ATTN_OUT_F32", name);
+  if (num_splits < 0 || (num_splits > 0 && num_splits < pda::tree::kMaxGroups) || num_splits > pda::tree::kMaxGrid)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: num_splits must be 0 or in [%d, %d]", name, pda::tree::kMaxGroups,
+                pda::tree::kMaxGrid);
+  int dev = 0, num_sms = 0;
+  if ((st = current_device(&dev, &num_sms)) != ATTN_OK) return st;
+  TreePlan plan;
+  if ((st = make_tree_plan(kind, batch, max_q, max_seq_len, window, num_splits, num_sms, &plan)) != ATTN_OK) return st;
+  if (!workspace || workspace_bytes < plan.workspace_bytes)
+    return fail(ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)", name, plan.workspace_bytes,
+                workspace ? workspace_bytes : size_t{0});
+  if (!aligned16(workspace)) return fail(ATTN_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", name);
+  const bool idle = total_q == 0 || max_q == 0;  // no nodes
+  g_last_launches = idle ? 0 : plan.merge ? 2 : 1;
+  if (idle || g_validate_only) return ATTN_OK;
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  pda::tree::TreeParams p{};
+  p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.parents = parents;
+  p.o = o;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + plan.part_o_bytes);
+  p.cuts = reinterpret_cast<int4*>(ws + plan.part_o_bytes + plan.part_ml_bytes);
+  p.status = status;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.max_blocks = max_blocks;
+  p.window = window;
+  p.total_q = total_q;
+  p.max_q = max_q;
+  p.groups = plan.groups;
+  p.out_f32 = out_dtype == ATTN_OUT_F32;
+  p.whole = plan.whole;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  namespace tr = pda::tree;
+  if (!sliding) return launch_tree<tr::GlobalConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);
+  return narrow_tree(kind, max_q)
+             ? launch_tree<tr::SlidingConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s)
+             : launch_tree<tr::SlidingWideConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);
+}
+
+// ---------------------------------------------------------------------------
+// Commit of accepted paths
+// ---------------------------------------------------------------------------
+int32_t run_commit(int32_t kind, const void* const* k_pools, const void* const* v_pools, int32_t layers,
+                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, const int32_t* path,
+                   const int32_t* path_len, int32_t* new_lens, int32_t batch, int32_t max_path, int32_t max_blocks,
+                   int64_t num_pages, int32_t* status, void* stream) {
+  g_err[0] = '\0';
+  const bool sliding = kind == ATTN_KIND_SLIDING;
+  const char* name = sliding ? "attn_kv_commit_sliding" : "attn_kv_commit_global";
+  if (!k_pools || !v_pools || !block_table || !seq_lens || !cu_q || !path || !path_len || !new_lens)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (!aligned_to(block_table, 4) || !aligned_to(seq_lens, 4) || !aligned_to(cu_q, 4) || !aligned_to(path, 4) ||
+      !aligned_to(path_len, 4) || !aligned_to(new_lens, 4) || !aligned_to(status, 4) ||
+      !aligned_to(k_pools, alignof(void*)) || !aligned_to(v_pools, alignof(void*)))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: misaligned pointer (tables 4 bytes)", name);
+  if (layers < 1) return fail(ATTN_ERR_INVALID_ARG, "%s: layers must be >= 1", name);
+  if (layers > ATTN_MAX_LAYERS)
+    return fail(ATTN_ERR_UNSUPPORTED, "%s: %d layers, at most %d a call", name, layers, ATTN_MAX_LAYERS);
+  int32_t st;
+  if ((st = check_batch(name, batch, max_blocks)) || (st = check_pages(name, "num_pages", num_pages))) return st;
+  if (max_path < 1) return fail(ATTN_ERR_INVALID_ARG, "%s: max_path must be >= 1", name);
+  if (max_path > ATTN_MAX_TREE)
+    return fail(ATTN_ERR_UNSUPPORTED, "%s: max_path %d beyond %d nodes", name, max_path, ATTN_MAX_TREE);
+  pda::commit::CommitParams p{};
+  for (int i = 0; i < layers; ++i) {
+    if (!k_pools[i] || !v_pools[i]) return fail(ATTN_ERR_INVALID_ARG, "%s: null pool of layer %d", name, i);
+    if (!aligned16(k_pools[i]) || !aligned16(v_pools[i]))
+      return fail(ATTN_ERR_INVALID_ARG, "%s: pool of layer %d not 16-byte aligned", name, i);
+    p.pool[2 * i] = static_cast<uint8_t*>(const_cast<void*>(k_pools[i]));
+    p.pool[2 * i + 1] = static_cast<uint8_t*>(const_cast<void*>(v_pools[i]));
+  }
+  for (int i = 0; i < 2 * layers; ++i)  // a row moved twice would be moved wrongly
+    for (int j = 0; j < i; ++j)
+      if (p.pool[i] == p.pool[j]) return fail(ATTN_ERR_INVALID_ARG, "%s: a pool is given twice", name);
+  g_last_launches = 1;
+  if (g_validate_only) return ATTN_OK;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.path = path;
+  p.path_len = path_len;
+  p.new_lens = new_lens;
+  p.status = status;
+  p.num_pages = num_pages;
+  p.max_path = max_path;
+  p.max_blocks = max_blocks;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid(batch, 2 * layers);
+  constexpr int kSlidingRow = ATTN_SLIDING_HKV * ATTN_SLIDING_D * 2, kGlobalRow = ATTN_GLOBAL_HKV * ATTN_GLOBAL_D * 2;
+  return launched(name, sliding ? launch_pdl(pda::commit::commit_kernel<kSlidingRow>, grid, kSlidingRow / 16, 0, s, p)
+                                : launch_pdl(pda::commit::commit_kernel<kGlobalRow>, grid, kGlobalRow / 16, 0, s, p));
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t attn_decode_sliding_tree(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                                 const int32_t* seq_lens, const int32_t* cu_q, const int32_t* parents, void* o,
+                                 int32_t batch, int32_t total_q, int32_t max_q, int32_t max_blocks, int64_t num_pages,
+                                 int32_t max_seq_len, int32_t window, int32_t out_dtype, int32_t num_splits,
+                                 void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+  return run_tree(ATTN_KIND_SLIDING, q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o, batch, total_q, max_q,
+                  max_blocks, num_pages, max_seq_len, window, out_dtype, num_splits, workspace, workspace_bytes, status,
+                  stream);
+}
+
+int32_t attn_decode_global_tree(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                                const int32_t* seq_lens, const int32_t* cu_q, const int32_t* parents, void* o,
+                                int32_t batch, int32_t total_q, int32_t max_q, int32_t max_blocks, int64_t num_pages,
+                                int32_t max_seq_len, int32_t window, int32_t out_dtype, int32_t num_splits,
+                                void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+  return run_tree(ATTN_KIND_GLOBAL, q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o, batch, total_q, max_q,
+                  max_blocks, num_pages, max_seq_len, window, out_dtype, num_splits, workspace, workspace_bytes, status,
+                  stream);
+}
+
+int32_t attn_decode_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_seq_len, int32_t window,
+                              int32_t num_splits, int32_t num_sms, int32_t* out_num_splits, int32_t* out_launches,
+                              size_t* out_workspace_bytes) {
+  g_err[0] = '\0';
+  TreePlan plan;
+  const int32_t st = make_tree_plan(kind, batch, max_q, max_seq_len, window, num_splits, num_sms, &plan);
+  if (st != ATTN_OK) return st;
+  if (out_num_splits) *out_num_splits = plan.grid;
+  if (out_launches) *out_launches = plan.merge ? 2 : 1;
+  if (out_workspace_bytes) *out_workspace_bytes = plan.workspace_bytes;
+  return ATTN_OK;
+}
+
+size_t attn_decode_tree_workspace_size(int32_t kind, int32_t batch, int32_t max_q, int32_t max_seq_len, int32_t window,
+                                       int32_t num_splits) {
+  g_err[0] = '\0';
+  int dev = 0, num_sms = 0;
+  if (current_device(&dev, &num_sms) != ATTN_OK) return 0;
+  TreePlan plan;
+  if (make_tree_plan(kind, batch, max_q, max_seq_len, window, num_splits, num_sms, &plan) != ATTN_OK) return 0;
+  return plan.workspace_bytes;
+}
+
+int32_t attn_kv_append_sliding_tree(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
+                                    const int32_t* seq_lens, const int32_t* cu_q, const int32_t* parents, void* q_out,
+                                    void* k_pool, void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
+                                    int64_t num_pages, int32_t* status, void* stream) {
+  return run_chunk(ATTN_KIND_SLIDING, Chunk::kTree, qkv, w_q, w_k, parents, block_table, seq_lens, cu_q, q_out, k_pool,
+                   v_pool, nullptr, nullptr, batch, total_q, max_blocks, num_pages, status, stream);
+}
+
+int32_t attn_kv_append_global_tree(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
+                                   const int32_t* seq_lens, const int32_t* cu_q, const int32_t* parents, void* q_out,
+                                   void* k_pool, void* v_pool, int32_t batch, int32_t total_q, int32_t max_blocks,
+                                   int64_t num_pages, int32_t* status, void* stream) {
+  return run_chunk(ATTN_KIND_GLOBAL, Chunk::kTree, qkv, w_q, w_k, parents, block_table, seq_lens, cu_q, q_out, k_pool,
+                   v_pool, nullptr, nullptr, batch, total_q, max_blocks, num_pages, status, stream);
+}
+
+int32_t attn_kv_commit_sliding(const void* const* k_pools, const void* const* v_pools, int32_t layers,
+                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                               const int32_t* path, const int32_t* path_len, int32_t* new_lens, int32_t batch,
+                               int32_t max_path, int32_t max_blocks, int64_t num_pages, int32_t* status, void* stream) {
+  return run_commit(ATTN_KIND_SLIDING, k_pools, v_pools, layers, block_table, seq_lens, cu_q, path, path_len, new_lens,
+                    batch, max_path, max_blocks, num_pages, status, stream);
+}
+
+int32_t attn_kv_commit_global(const void* const* k_pools, const void* const* v_pools, int32_t layers,
+                              const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                              const int32_t* path, const int32_t* path_len, int32_t* new_lens, int32_t batch,
+                              int32_t max_path, int32_t max_blocks, int64_t num_pages, int32_t* status, void* stream) {
+  return run_commit(ATTN_KIND_GLOBAL, k_pools, v_pools, layers, block_table, seq_lens, cu_q, path, path_len, new_lens,
+                    batch, max_path, max_blocks, num_pages, status, stream);
+}
+
+int32_t attn_pages_assign(const int32_t* cached_lens, const int32_t* new_tokens, int32_t* block_table,
+                          const int32_t* held, int32_t* free_list, const int32_t* free_state, int32_t* held_out,
+                          int32_t* free_state_out, int32_t* seq_lens, int32_t* cu_q, int32_t batch, int32_t max_blocks,
+                          int64_t num_pages, int32_t window, int32_t* status, void* stream) {
+  g_err[0] = '\0';
+  const char* name = "attn_pages_assign";
+  if (!cached_lens || !new_tokens || !block_table || !held || !free_list || !free_state || !held_out ||
+      !free_state_out || !seq_lens || !cu_q)
+    return fail(ATTN_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (!aligned_to(cached_lens, 4) || !aligned_to(new_tokens, 4) || !aligned_to(block_table, 4) ||
+      !aligned_to(free_list, 4) || !aligned_to(seq_lens, 4) || !aligned_to(cu_q, 4) || !aligned_to(status, 4) ||
+      !aligned_to(held, 8) || !aligned_to(free_state, 8) || !aligned_to(held_out, 8) || !aligned_to(free_state_out, 8))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: misaligned pointer (held, free_state and their outputs 8 bytes, others 4)",
+                name);
+  int32_t st;
+  if ((st = check_batch(name, batch, max_blocks)) || (st = check_pages(name, "num_pages", num_pages))) return st;
+  g_last_launches = 1;
+  if (g_validate_only) return ATTN_OK;
+  pda::pages::PagesParams p{};
+  p.cached = cached_lens;
+  p.fresh = new_tokens;
+  p.block_table = block_table;
+  p.held = reinterpret_cast<const int2*>(held);
+  p.free_list = free_list;
+  p.free_state = reinterpret_cast<const int2*>(free_state);
+  p.held_out = reinterpret_cast<int2*>(held_out);
+  p.free_state_out = reinterpret_cast<int2*>(free_state_out);
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.status = status;
+  p.num_pages = static_cast<int32_t>(num_pages);
+  p.batch = batch;
+  p.max_blocks = max_blocks;
+  p.window = window;
+  return launched(name, launch_pdl(pda::pages::assign_kernel, dim3(pda::pages::kBlocks), pda::pages::kThreads, 0,
+                                   static_cast<cudaStream_t>(stream), p));
+}
+
+}  // extern "C"
