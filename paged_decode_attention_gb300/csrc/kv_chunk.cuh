@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
           if constexpr (kTree) {
             if (threadIdx.x < kPairs) {  // (whole warps)
               int parent[2], depth[2];
-              if (tree::load_parents(p.parents + q0, q1 - q0, parent) && threadIdx.x == 0)
-                report(p.status, ATTN_DEV_BAD_TREE);
+              tree::read_parents(p.parents + q0, q1 - q0, parent);
+              if (tree::check_parents(q1 - q0, parent) && threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_TREE);
               tree::depths(parent, depth);
               turned = pos - (t - q0) + tree::of_node(depth, t - q0);
             }

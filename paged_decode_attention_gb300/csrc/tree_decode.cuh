@@ -22,15 +22,22 @@
 // above (prefill_tc.cuh has the bounds); a thread compares its own scores with the
 // bounds, and one barrier with an OR tells whether any row moves.  So in nearly all
 // steps nothing is reduced across lanes: each thread sums the weights of its own keys,
-// and the 128 sums per row meet once, at the end of a segment.
+// and the 128 sums per row meet once, at the end of a segment.  A first step whose
+// keys all nodes see takes one key's scores for the first references, which the same
+// bounds then correct.
 //
-// Schedule.  Rows come in groups of kQueries nodes; group r of KV head c of all
-// sequences that have one is a list of steps of 128 keys, a virtual step in front of
-// every sequence (its Q, its end).  All lists are cut into runs of `per` steps, the
-// smallest that gives no more runs than blocks: every block has the same work whatever
-// the lengths, and blocks of neighbouring groups walk the same keys at the same time.
-// A sequence inside one run is finished there; of a cut one every block leaves a
-// partial (O, m, sum), and merge_kernel joins them.
+// Schedule.  Rows come in groups of kQueries nodes; kCluster groups of KV head c of
+// all sequences that have them are a list of pages, with kSegWeight virtual pages in
+// front of every sequence (its Q, its end).  All lists are cut into runs of `per`
+// pages, the fewest that give no more runs than clusters: every cluster has the same
+// work whatever the lengths, and those of neighbouring lists walk the same keys at the
+// same time.  A sequence inside one run is finished there; of a cut one every block
+// leaves a partial (O, m, sum), and merge_kernel joins them.
+//
+// Clusters.  On global layers a tree of more than four nodes has several groups, and
+// every group reads all keys.  Two CTAs walk a run together, a group each: each copies
+// half of the pages of K and V into both (multicast), so that L2 is read once for both;
+// a stage is free again when both have used it.
 //
 // What a node does not see.  Scores are masked, and rows of V that no node sees are
 // zeroed in shared memory.  A row that some nodes see and others do not (a node of the
@@ -54,7 +61,8 @@ namespace tree {
 constexpr int kKeys = 128;                  // per step
 constexpr int kStepPages = kKeys / kPage;
 constexpr int kMaxGroups = 16;              // of rows, per KV head
-constexpr int kMinPer = 2;                  // smallest run: a virtual step and one of keys
+constexpr int kSegWeight = 4;               // virtual pages charged per sequence
+constexpr int kMinPer = 4;                  // pages of the smallest run
 constexpr int kSoftmaxThreads = 256;
 constexpr int kThreads = 384;
 constexpr int kMaxGrid = kMaxSplits;
@@ -77,17 +85,19 @@ struct TreeParams {
   int32_t window;
   int32_t total_q;
   int32_t max_q;
-  int32_t groups;   // of rows: ceil(max_q / kQueries)
+  int32_t lists;    // per KV head: ceil(max_q / (kQueries * kCluster))
   int32_t q_box;    // nodes that a copy of Q brings
   int32_t out_f32;
   int32_t whole;    // a block per (sequence, group, KV head) instead of runs
 };
 
-template <int kD_, int kG_, int kHkv_, int kN_, int kKStages_, int kVStages_>
+template <int kD_, int kG_, int kHkv_, int kN_, int kKStages_, int kVStages_, int kCluster_ = 1>
 struct Config {
+  static constexpr int kCluster = kCluster_;   // CTAs that share their copies of K and V
   static constexpr int kD = kD_, kG = kG_, kHkv = kHkv_, kHq = kG * kHkv;
   static constexpr int kN = kN_;               // rows per group, at most
   static constexpr int kHalf = kN / 2;         // columns per softmax warpgroup
+  static constexpr int kBlock = kHalf < 32 ? kHalf : 32;  // columns at a time
   static constexpr int kQueries = kN / kG;
   static constexpr int kChunks = kD / 64;
   static constexpr int kTiles = kD / 128;      // of 128 output dims
@@ -101,23 +111,25 @@ struct Config {
   static constexpr uint32_t kUsedCols = kSCol + 2 * kN;
   static constexpr uint32_t kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static_assert(kUsedCols <= 512 && kN % 16 == 0 && kN <= 256, "tensor memory");
-  static_assert(kHalf == 16 || kHalf == 32 || kHalf == 64, "column reductions");
+  static_assert(kBlock == 16 || kBlock == 32, "column reductions");
+  static_assert(kCluster == 1 || kCluster == 2, "pages by rank");
 
   struct Smem {
     alignas(1024) uint8_t q[kChunks][kN * 128];
     alignas(1024) uint8_t p[2][kPBytes];
     alignas(1024) uint8_t k[kKStages][kKChunk];
     alignas(1024) uint8_t v[kVStages][kVPage];
-    alignas(16) float m[kN];          // reference max (log2 units), 0 before there is one
+    alignas(16) float neg_m[kN];      // minus the reference max (log2 units), 0 before there is one
     alignas(16) float bound[kN];      // a score above this moves it; -inf before there is one
     alignas(16) float f[kN];          // factor of a moved reference; 1 / sum at the end
     alignas(16) float red[8][kN / 2]; // per softmax warp and column: max, sum
-    alignas(8) unsigned long long anc[ATTN_MAX_TREE];
+    alignas(8) unsigned long long below[ATTN_MAX_TREE];    // nodes that see node j by ancestry
+    alignas(8) unsigned long long shallow[ATTN_MAX_TREE];  // nodes of depth <= x
     int32_t depth[ATTN_MAX_TREE];
-    int32_t pre[kMaxBatch + 1];       // steps (virtual ones included) before sequence b in this block's list
-    int32_t hist[kMaxGroups + 1];     // steps of the sequences with that many groups
+    int32_t pre[kMaxBatch + 1];       // pages (virtual ones included) before sequence b in this block's list
+    int32_t hist[kMaxGroups + 1];     // pages of the sequences with that many clusters of groups
     int32_t warp_sum[kMaxBatch / 32];
-    int32_t sched[5];                 // group, KV head, per, run, next block's distance
+    int32_t sched[4];                 // list, KV head, per, run
     int32_t poison;                   // this segment: an element was zeroed that some row sees
     alignas(8) uint64_t k_full[kKStages], k_empty[kKStages];
     alignas(8) uint64_t v_full[kVStages], v_empty[kVStages];
@@ -134,10 +146,9 @@ struct Config {
 
 // One sequence as the schedule sees it.
 struct Sequence {
-  int q0, n, L, ctx, lo, page0, pages, steps;  // steps 0: nothing to do
+  int q0, n, L, ctx, lo, page0, pages;  // pages 0: nothing to do
 };
 
-template <typename C>
 __device__ __forceinline__ Sequence load_sequence(const TreeParams& p, int b, bool& refused, bool& backwards) {
   Sequence s{};
   s.q0 = p.cu_q[b];
@@ -152,15 +163,19 @@ __device__ __forceinline__ Sequence load_sequence(const TreeParams& p, int b, bo
   s.lo = p.window > 0 && s.ctx >= p.window ? s.ctx - p.window + 1 : 0;
   s.page0 = s.lo / kPage;
   s.pages = (s.L - 1) / kPage - s.page0 + 1;
-  s.steps = (s.pages + kStepPages - 1) / kStepPages;
   return s;
 }
 
-// A part of one sequence's steps for one group of rows.
+// Positions below are not seen by every node.
+__device__ __forceinline__ int all_from(const Sequence& q, int window) {
+  return window > 0 ? q.ctx + (q.n - 1) - window + 1 : 0;  // (a depth is at most n - 1)
+}
+
+// A part of one sequence's pages for one group of rows.
 struct Segment {
   Sequence q;
   int b, row0, nodes, cols, N;  // first node of the group (packed), its nodes, rows, columns of the products
-  int s0, s1;                   // steps
+  int p0, p1, steps;            // pages, and steps of kStepPages
   bool whole;
   int slot;                     // of its partial
 };
@@ -171,7 +186,7 @@ struct Walk {
   int b, w0, w1, group, kv, index;
   template <typename S>
   __device__ __forceinline__ void start(const TreeParams& p, const S& s) {
-    group = s.sched[0];
+    group = s.sched[0] * C::kCluster + static_cast<int>(blockIdx.x % C::kCluster);
     kv = s.sched[1];
     index = 0;
     const int per = s.sched[2], run = s.sched[3];
@@ -195,20 +210,21 @@ struct Walk {
   template <typename S>
   __device__ __forceinline__ bool next(const TreeParams& p, const S& s, Segment& g) {
     for (; b < p.batch && s.pre[b] < w1; ++b) {
-      const int steps = s.pre[b + 1] - s.pre[b] - 1;
-      if (steps <= 0) continue;
-      const int first = s.pre[b] + 1;
-      g.s0 = w0 > first ? w0 - first : 0;
-      g.s1 = w1 - first < steps ? w1 - first : steps;
-      if (g.s1 <= g.s0) continue;
+      const int pages = s.pre[b + 1] - s.pre[b] - kSegWeight;
+      if (pages <= 0) continue;
+      const int first = s.pre[b] + kSegWeight;
+      g.p0 = w0 > first ? w0 - first : 0;
+      g.p1 = w1 - first < pages ? w1 - first : pages;
+      if (g.p1 <= g.p0) continue;
       bool refused, backwards;
-      g.q = load_sequence<C>(p, b, refused, backwards);
+      g.q = load_sequence(p, b, refused, backwards);
       g.b = b;
       g.row0 = g.q.q0 + group * C::kQueries;
-      g.nodes = min(C::kQueries, g.q.n - group * C::kQueries);
+      g.nodes = max(0, min(C::kQueries, g.q.n - group * C::kQueries));  // (0: only the cluster's other groups have any)
       g.cols = g.nodes * C::kG;
-      g.N = (g.cols + 15) & ~15;
-      g.whole = g.s0 == 0 && g.s1 == steps;
+      g.N = max(16, (g.cols + 15) & ~15);
+      g.steps = (g.p1 - g.p0 + kStepPages - 1) / kStepPages;
+      g.whole = g.p0 == 0 && g.p1 == pages;
       g.slot = 2 * static_cast<int>(blockIdx.x) + (index > 0);
       ++index;
       ++b;
@@ -271,21 +287,69 @@ __device__ __forceinline__ bool barrier_or(uint32_t id, uint32_t threads, bool v
   return r != 0;
 }
 
-// Whether node i (depth d, ancestors a) sees position pos.
+// The nodes (bits) that see position pos.  (The masks are there where a segment holds positions that not all nodes see.)
 template <typename S>
-__device__ __forceinline__ bool sees(const Sequence& q, int window, const S& s, int i, int pos) {
-  const int d = s.depth[i];
-  if (pos < q.ctx) return window <= 0 || q.ctx - pos < window - d;
+__device__ __forceinline__ unsigned long long seen_by(const Sequence& q, int window, const S& s, int pos) {
+  if (pos >= all_from(q, window) && pos < q.ctx) return ~0ull;
+  if (pos < q.lo || pos >= q.L) return 0;
+  if (pos < q.ctx) return s.shallow[min(pos - (q.ctx - window + 1), ATTN_MAX_TREE - 1)];
   const int j = pos - q.ctx;
-  return j < q.n && ((s.anc[i] >> j) & 1) && (window <= 0 || d - s.depth[j] < window);
+  const unsigned long long m = s.below[j];
+  return window > 0 && window < ATTN_MAX_TREE ? m & s.shallow[min(s.depth[j] + window - 1, ATTN_MAX_TREE - 1)] : m;
 }
 
-// Positions below the first, or from the second on, are not seen by every node.
-__device__ __forceinline__ int all_from(const Sequence& q, int window) {
-  return window > 0 ? q.ctx + (q.n - 1) - window + 1 : 0;  // (a depth is at most n - 1)
+// bf16 pairs: nonzero where a half is an infinity or NaN (its exponent all ones).
+__device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// A page of V as this lane sees it (16 bytes of every fourth chunk of a row): the rows in `none` zeroed, and every
+// element of the rows in `some` that is not finite.  Returns whether there was one.  Eight rows are read before any is
+// looked at: one after the other they would cost a shared-memory round trip each.
+template <typename C>
+__device__ __forceinline__ bool clean_page(uint32_t at, uint32_t none, uint32_t some) {
+  bool found = false;
+#pragma unroll 1
+  for (int r0 = 0; r0 < kPage; r0 += 8) {
+    if (((none | some) >> r0 & 0xffu) == 0) continue;
+#pragma unroll
+    for (int c0 = 0; c0 < C::kChunks; c0 += 4) {
+      const uint32_t a = at + c0 * (kPage * 128) + r0 * 128;
+      uint4 x[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) x[r] = ld_shared_v4(a + r * 128);
+      uint32_t bad = 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const uint32_t any = nonfinite_bf16x2(x[r].x) | nonfinite_bf16x2(x[r].y) | nonfinite_bf16x2(x[r].z) |
+                             nonfinite_bf16x2(x[r].w);
+        bad |= (any != 0 ? 1u : 0u) << r;
+        if (none >> (r0 + r) & 1) st_shared_v4(a + r * 128, make_uint4(0, 0, 0, 0));
+      }
+      bad &= some >> r0;
+      if (bad == 0) continue;
+      found = true;
+#pragma unroll 1
+      for (int r = 0; r < 8; ++r) {
+        if (!(bad >> r & 1)) continue;
+        const uint4 y = ld_shared_v4(a + r * 128);
+        uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t z = nonfinite_bf16x2(w[e]);
+          w[e] &= (z & 0x8000u ? 0u : 0xffffu) | (z & 0x80000000u ? 0u : 0xffff0000u);
+        }
+        st_shared_v4(a + r * 128, make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+  }
+  return found;
 }
 
-__device__ __forceinline__ bool finite_bf16(uint32_t half) { return (half & 0x7f80u) != 0x7f80u; }
+// Rows [from, to) of a page as bits, for positions relative to its first.
+__device__ __forceinline__ uint32_t row_bits(int from, int to) {
+  from = min(max(from, 0), kPage);
+  to = min(max(to, from), kPage);
+  return ((1u << to) - 1u) & ~((1u << from) - 1u);
+}
 
 // The schedule: this block's list, the running sums over it, its run.  Called by
 // every thread; ends with a barrier.  Returns false when the call is refused.
@@ -295,12 +359,11 @@ __device__ __forceinline__ bool make_schedule(const TreeParams& p, S& s) {
   if (tid <= kMaxGroups) s.hist[tid] = 0;
   int weight = 0, groups = 0;
   bool refused = false, backwards = false;
-  Sequence q{};
   if (tid < p.batch) {
-    q = load_sequence<C>(p, tid, refused, backwards);
-    if (q.steps > 0) {
-      weight = q.steps + 1;
-      groups = (q.n + C::kQueries - 1) / C::kQueries;
+    const Sequence q = load_sequence(p, tid, refused, backwards);
+    if (q.pages > 0) {
+      weight = q.pages + kSegWeight;
+      groups = (q.n + C::kQueries * C::kCluster - 1) / (C::kQueries * C::kCluster);
     }
   }
   if (refused && blockIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
@@ -308,22 +371,21 @@ __device__ __forceinline__ bool make_schedule(const TreeParams& p, S& s) {
   if (weight > 0) atomicAdd(&s.hist[groups], weight);
   __syncthreads();
   if (warp == 0) {
-    // lane r: the steps of list r (the same for every KV head)
+    // lane r: the pages of list r (the same for every KV head)
     int total = 0;
-    for (int g = lane + 1; g <= p.groups; ++g) total += s.hist[g];
-    if (lane >= p.groups) total = 0;
-    const int g = static_cast<int>(blockIdx.x);
+    for (int g = lane + 1; g <= p.lists; ++g) total += s.hist[g];
+    if (lane >= p.lists) total = 0;
+    const int g = static_cast<int>(blockIdx.x / C::kCluster);
     if (p.whole) {
       if (lane == 0) {
-        const int per_seq = p.groups * C::kHkv;
+        const int per_seq = p.lists * C::kHkv;
         s.sched[0] = g % per_seq / C::kHkv;
         s.sched[1] = g % C::kHkv;
         s.sched[2] = 1;
         s.sched[3] = g / per_seq;
-        s.sched[4] = 0;
       }
     } else {
-      const int grid = static_cast<int>(gridDim.x);
+      const int grid = static_cast<int>(gridDim.x / C::kCluster);
       const int sum = __reduce_add_sync(0xffffffffu, total);
       int lo = max(kMinPer, static_cast<int>((static_cast<long long>(sum) * C::kHkv + grid - 1) / grid));
       int hi = max(lo, __reduce_max_sync(0xffffffffu, total));
@@ -337,7 +399,7 @@ __device__ __forceinline__ bool make_schedule(const TreeParams& p, S& s) {
         }
       }
       const int per = hi;
-      const int mine = (total + per - 1) / per * C::kHkv;  // this list's blocks
+      const int mine = (total + per - 1) / per * C::kHkv;  // this list's clusters
       int before = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -349,6 +411,7 @@ __device__ __forceinline__ bool make_schedule(const TreeParams& p, S& s) {
       if (lane == 0) {
         s.sched[0] = 0;
         s.sched[1] = 0;
+        s.sched[2] = per;
         s.sched[3] = -1;  // no run: the block has nothing to do
       }
       __syncwarp();
@@ -356,10 +419,6 @@ __device__ __forceinline__ bool make_schedule(const TreeParams& p, S& s) {
         s.sched[0] = lane;
         s.sched[1] = (g - before) % C::kHkv;
         s.sched[3] = (g - before) / C::kHkv;
-      }
-      if (lane == 0) {
-        s.sched[2] = per;
-        s.sched[4] = C::kHkv;
       }
     }
   }
@@ -393,37 +452,78 @@ __device__ __forceinline__ void note_cut(const TreeParams& p, const S& s) {
   Segment g;
   int4 cut = make_int4(0, 0, 0, 0);
   while (walk.next(p, s, g)) {
-    if (g.s0 == 0 && !g.whole) {
-      const int last = (s.pre[g.b] + g.q.steps) / s.sched[2];  // the run that holds its last step
+    if (g.p0 == 0 && !g.whole) {
+      const int last = (s.pre[g.b] + kSegWeight + g.q.pages - 1) / s.sched[2];  // the run that holds its last page
       cut = make_int4(g.row0, g.nodes | (walk.kv << 8), g.slot, last - s.sched[3] + 1);
     }
   }
   p.cuts[blockIdx.x] = cut;
 }
 
+// Multicast copy of a 3-D tile into the same place of every CTA of the cluster in `mask`, completing on the same
+// barrier of each.
+__device__ __forceinline__ void tma_load_3d_multicast(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                                      uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "h"(mask)
+      : "memory");
+}
+
+template <int kCluster>
+__device__ __forceinline__ void load_page(void* dst, const CUtensorMap* map, int32_t y, int32_t z, uint64_t* bar) {
+  if constexpr (kCluster == 1)
+    prefill_tc::tma_load_3d(dst, map, 0, y, z, bar);
+  else
+    tma_load_3d_multicast(dst, map, 0, y, z, bar, static_cast<uint16_t>((1 << kCluster) - 1));
+}
+
+// Arrives on `bar` of every CTA of the cluster once the products this thread issued before are done.
+template <int kCluster>
+__device__ __forceinline__ void commit_all(uint64_t* bar) {
+  if constexpr (kCluster == 1) {
+    umma_commit_warp(bar);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>((1 << kCluster) - 1))
+        : "memory");
+  }
+}
+
+template <int kCluster>
+__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity) {  // a barrier that the whole cluster arrives on
+  if constexpr (kCluster == 1) return mbar_wait_fast(bar, parity);
+  return mbar_wait_cluster(bar, parity);
+}
+
 template <typename C>
-__global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
+__device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                          const TreeParams& p) {
   using prefill_tc::kHeadroom;
   using prefill_tc::kSlack;
-  using prefill_tc::tma_load_3d;
   using prefill_tc::tma_load_4d;
-  constexpr int kD = C::kD, kG = C::kG, kN = C::kN, kHalf = C::kHalf, kTiles = C::kTiles;
+  constexpr int kD = C::kD, kG = C::kG, kN = C::kN, kHalf = C::kHalf, kTiles = C::kTiles, kBlock = C::kBlock;
+  constexpr int kCluster = C::kCluster;
   extern __shared__ uint8_t smem_raw[];
   typename C::Smem& s =
       *reinterpret_cast<typename C::Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x % kCluster);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(&s.k_full[i], 1);
-      mbar_init(&s.k_empty[i], 1);
+      mbar_init(&s.k_empty[i], kCluster);
     }
     for (int i = 0; i < C::kVStages; ++i) {
       mbar_init(&s.v_full[i], 1);
-      mbar_init(&s.v_empty[i], 1);
+      mbar_init(&s.v_empty[i], kCluster);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
@@ -453,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_primary_grid();
   allow_dependent_launch();
   const bool run = make_schedule<C>(p, s);
+  if constexpr (kCluster > 1) cluster_sync_all();  // the other CTA's barriers are there
   if (!run) {
     if (threadIdx.x == 0 && !p.whole) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp == 8) {
@@ -460,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && !p.whole) note_cut<C>(p, s);
     __syncwarp();
     bool ok = true;
-    int gt = 0, gk = 0;  // segments, K chunks
+    int gt = 0, gk = 0, st = 0, st_ph = 1;  // segments, K chunks; stage and its phase
     Walk<C> walk;
     walk.start(p, s);
     Segment g;
@@ -472,29 +573,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < C::kChunks) tma_load_4d(s.q[lane], &tm_q, 0, lane, walk.kv * kG, g.row0, &s.q_ready);
       ++gt;
       const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks + g.q.page0;
-      const auto entry = [&](int j) {
-        const int pg = j * kStepPages + lane;
-        return j < g.s1 && lane < kStepPages && pg < g.q.pages ? table[pg] : 0;
-      };
-      int next_id = entry(g.s0);
-      for (int j = g.s0; j < g.s1 && ok; ++j) {
+      const auto entry = [&](int pg) { return lane < kStepPages && pg + lane < g.p1 ? table[pg + lane] : 0; };
+      int next_id = entry(g.p0);
+      for (int pg = g.p0; pg < g.p1 && ok; pg += kStepPages) {
         const int id = next_id;
-        next_id = entry(j + 1);
-        const int np = min(kStepPages, g.q.pages - j * kStepPages);
+        next_id = entry(pg + kStepPages);
+        const int np = min(kStepPages, g.p1 - pg);
         int32_t y = id * kPage;
         if (lane < np && (id < 0 || static_cast<int64_t>(id) >= p.num_pages)) {
           report(p.status, ATTN_DEV_BAD_PAGE);
           y = -kPage;
         }
         for (int ch = 0; ch < C::kChunks; ++ch) {
-          const int st = gk % C::kKStages;
-          if (gk >= C::kKStages) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.k_empty[st], ((gk / C::kKStages) - 1) & 1));
+          if (gk >= C::kKStages) ok = __all_sync(0xffffffffu, wait_stage<kCluster>(&s.k_empty[st], st_ph));
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&s.k_full[st], np * kPage * 128);
           __syncwarp();
-          if (lane < np)
-            tma_load_3d(s.k[st] + lane * (kPage * 128), &tm_k, 0, y, walk.kv * C::kChunks + ch, &s.k_full[st]);
+          if (lane < np && lane % kCluster == rank)
+            load_page<kCluster>(s.k[st] + lane * (kPage * 128), &tm_k, y, walk.kv * C::kChunks + ch, &s.k_full[st]);
           ++gk;
+          if (++st == C::kKStages) st = 0, st_ph ^= 1;
           __syncwarp();
         }
       }
@@ -505,50 +603,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&s.q_ready, (gt - 1) & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
         if (ok && !mbar_wait(&s.q_empty, (gt - 1) & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
       }
-      for (int st = 0; st < C::kKStages && st < gk; ++st) {
-        const int uses = (gk - 1 - st) / C::kKStages;
-        if (!mbar_wait(&s.k_full[st], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
-        if (ok && !mbar_wait(&s.k_empty[st], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+      for (int i = 0; i < C::kKStages && i < gk; ++i) {
+        const int uses = (gk - 1 - i) / C::kKStages;
+        if (!mbar_wait(&s.k_full[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+        if (ok && !wait_stage<kCluster>(&s.k_empty[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
       }
     }
   } else if (warp == 9) {
     // ---------------- V producer: a page per stage ----------------
     bool ok = true;
-    int gv = 0;
+    int gv = 0, st = 0, st_ph = 1;
     Walk<C> walk;
     walk.start(p, s);
     Segment g;
     while (ok && walk.next(p, s, g)) {
       const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks + g.q.page0;
-      const int first = g.s0 * kStepPages;
-      const int last = min(g.s1 * kStepPages, g.q.pages);
-      const auto entry = [&](int pg) { return pg < last ? table[pg] : 0; };
-      int cur = 0, nxt = entry(first + lane);
-      for (int pg = first; pg < last && ok; ++pg) {
-        const int u = (pg - first) & 31;
+      const auto entry = [&](int pg) { return pg < g.p1 ? table[pg] : 0; };
+      int cur = 0, nxt = entry(g.p0 + lane);
+      for (int pg = g.p0; pg < g.p1 && ok; ++pg) {
+        const int u = (pg - g.p0) & 31;
         if (u == 0) {
           cur = nxt;
           nxt = entry(pg + 32 + lane);
         }
         const int id = __shfl_sync(0xffffffffu, cur, u);
-        const int st = gv % C::kVStages;
-        if (gv >= C::kVStages) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.v_empty[st], ((gv / C::kVStages) - 1) & 1));
+        if (gv >= C::kVStages) ok = __all_sync(0xffffffffu, wait_stage<kCluster>(&s.v_empty[st], st_ph));
         if (!ok) break;
         if (lane == 0) {
           const bool there = id >= 0 && static_cast<int64_t>(id) < p.num_pages;  // (the K producer reports)
           mbar_arrive_expect_tx(&s.v_full[st], C::kVPage);
-          tma_load_3d(s.v[st], &tm_v, 0, there ? id * kPage : -kPage, walk.kv * C::kChunks, &s.v_full[st]);
+          if (u % kCluster == rank)
+            load_page<kCluster>(s.v[st], &tm_v, there ? id * kPage : -kPage, walk.kv * C::kChunks, &s.v_full[st]);
         }
         ++gv;
+        if (++st == C::kVStages) st = 0, st_ph ^= 1;
         __syncwarp();
       }
     }
     if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
     if (lane == 0) {
-      for (int st = 0; st < C::kVStages && st < gv; ++st) {
-        const int uses = (gv - 1 - st) / C::kVStages;
-        if (!mbar_wait(&s.v_full[st], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
-        if (ok && !mbar_wait(&s.v_empty[st], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+      for (int i = 0; i < C::kVStages && i < gv; ++i) {
+        const int uses = (gv - 1 - i) / C::kVStages;
+        if (!mbar_wait(&s.v_full[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+        if (ok && !wait_stage<kCluster>(&s.v_empty[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
       }
     }
   } else if (warp == 10) {
@@ -562,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (walk.next(p, s, g)) {
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.q_ready, gt & 1));
       const uint32_t idesc = prefill_tc::warp_uniform_int(umma_idesc_bf16(128, g.N, 0, 0));
-      const int steps = prefill_tc::warp_uniform_int(g.s1 - g.s0);
+      const int steps = prefill_tc::warp_uniform_int(g.steps);
       for (int j = 0; j < steps; ++j) {
         const int sb = gs & 1;
         if (ok && gs >= 2) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.s_free[sb], ((gs >> 1) - 1) & 1));
@@ -575,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             umma_bf16_warp(d, umma_desc(k_base + kk * 32, 16, 1024, 2),
                            umma_desc(q_base + ch * (kN * 128) + kk * 32, 16, 1024, 2), idesc, (ch | kk) > 0 ? 1u : 0u);
-          umma_commit_warp(&s.k_empty[st]);
+          commit_all<kCluster>(&s.k_empty[st]);
           if (++st == C::kKStages) st = 0, st_ph ^= 1;
         }
         umma_commit_warp(&s.s_full[sb]);
@@ -602,41 +699,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = prefill_tc::warp_uniform_int(umma_idesc_bf16(128, g.N, 1, 1));
       bool poison = false;
       const int all0 = all_from(g.q, p.window);
-      for (int j = g.s0; j < g.s1; ++j) {
+      for (int pg0 = g.p0; pg0 < g.p1; pg0 += kStepPages) {
         const int pb = gs & 1;
-        const int np = prefill_tc::warp_uniform_int(min(kStepPages, g.q.pages - j * kStepPages));
+        const int np = prefill_tc::warp_uniform_int(min(kStepPages, g.p1 - pg0));
         const uint32_t p_base = smem_addr(s.p[pb]);
         for (int kk = 0; kk < np; ++kk) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.v_full[st], st_ph));
           const uint32_t v_base = smem_addr(s.v[st]);
-          const int pos0 = (g.q.page0 + j * kStepPages + kk) * kPage;
-          if (ok && (pos0 < all0 || pos0 < g.q.lo || pos0 + kPage > g.q.ctx)) {
-            for (int r = 0; r < kPage; ++r) {
-              const int pos = pos0 + r;
-              const bool none = pos < g.q.lo || pos >= g.q.L;
-              if (!none && pos >= all0 && pos < g.q.ctx) continue;
-#pragma unroll
-              for (int c0 = 0; c0 < C::kChunks; c0 += 4) {
-                const uint32_t at = v_base + (c0 + (lane >> 3)) * (kPage * 128) + r * 128 + (lane & 7) * 16;
-                if (none) {
-                  st_shared_v4(at, make_uint4(0, 0, 0, 0));
-                  continue;
-                }
-                const uint4 x = ld_shared_v4(at);
-                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                bool clean = true;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const bool a = finite_bf16(w[e]), b = finite_bf16(w[e] >> 16);
-                  clean &= a && b;
-                  w[e] &= (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
-                }
-                if (!clean) {
-                  st_shared_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
-                  poison = true;
-                }
-              }
-            }
+          const int pos0 = (g.q.page0 + pg0 + kk) * kPage;
+          if (ok && (pos0 < all0 || pos0 + kPage > g.q.ctx)) {  // (lo <= all0)
+            const uint32_t none = row_bits(0, g.q.lo - pos0) | row_bits(g.q.L - pos0, kPage);
+            const uint32_t some = (row_bits(0, all0 - pos0) | row_bits(g.q.ctx - pos0, kPage)) & ~none;
+            poison |= clean_page<C>(v_base + (lane >> 3) * (kPage * 128) + (lane & 7) * 16, none, some);
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -646,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < kTiles; ++t)
             umma_bf16_warp(tmem + t * kN, umma_desc(v_base + t * (2 * kPage * 128), kPage * 128, 1024, 2),
                            umma_desc(p_base + kk * (kPage * 128), C::kPChunk, 1024, 2), idesc,
-                           (j > g.s0 || kk > 0) ? 1u : 0u);
-          umma_commit_warp(&s.v_empty[st]);
+                           (pg0 > g.p0 || kk > 0) ? 1u : 0u);
+          commit_all<kCluster>(&s.v_empty[st]);
           if (++st == C::kVStages) st = 0, st_ph ^= 1;
         }
         umma_commit_warp(&s.p_empty[pb]);
@@ -668,144 +742,184 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
   } else {
     // ---------------- softmax and epilogue: thread = key of the step, then dim of a tile ----------------
-    const int h = warp >> 2;                // half of the columns
-    const int key = threadIdx.x & 127;      // tensor-memory lane
-    const int gtid = threadIdx.x & 127;     // thread of the warpgroup
+    const int h = warp >> 2;             // half of the columns
+    const int key = threadIdx.x & 127;   // tensor-memory lane, thread of the warpgroup
     const uint32_t bar = 2 + h;
     const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const auto fmax2 = [](float a, float b) { return fmaxf(a, b); };
     const auto add2 = [](float a, float b) { return a + b; };
+    const float2 log2e2 = make_float2(kLog2e, kLog2e);
     bool ok = true;
     int gt = 0, gs = 0;
     Walk<C> walk;
     walk.start(p, s);
-    Segment g;
-    while (walk.next(p, s, g)) {
-      // the sequence's tree, once all are done with the last one's
-      named_barrier_sync(1, kSoftmaxThreads);
-      if (warp == 0) {
-        int parent[2], depth[2];
-        unsigned long long mask[2];
-        if (load_parents(p.parents + g.q.q0, g.q.n, parent) && lane == 0) report(p.status, ATTN_DEV_BAD_TREE);
-        depths(parent, depth);
-        ancestors(parent, mask);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          s.anc[lane + 32 * u] = mask[u];
-          s.depth[lane + 32 * u] = depth[u];
-        }
-      }
+    Segment g, ahead;
+    int parent[2], ahead_parent[2] = {-1, -1};  // the next segment and its parents are read before this one's end
+    bool more = walk.next(p, s, ahead);
+    if (more) read_parents(p.parents + ahead.q.q0, ahead.q.n, ahead_parent);
+    while (more) {
+      g = ahead;
+      parent[0] = ahead_parent[0];
+      parent[1] = ahead_parent[1];
       const int half = g.N >> 1;
       const int c0 = h * half;  // this warpgroup's first column
-      if (gtid < half) {
-        s.m[c0 + gtid] = 0.f;
-        s.bound[c0 + gtid] = -INFINITY;
-      }
-      named_barrier_sync(1, kSoftmaxThreads);
       const int all0 = all_from(g.q, p.window);
       const int node0 = walk.group * C::kQueries;
+      const int seg0 = (g.q.page0 + g.p0) * kPage, seg1 = (g.q.page0 + g.p1) * kPage;
+      named_barrier_sync(1, kSoftmaxThreads);  // all are done with the last segment's shared state
+      if (seg0 < all0 || seg1 > g.q.ctx) {
+        // the sequence's tree: every warp works it out and writes its share of the masks
+        int depth[2];
+        unsigned long long mask[2];
+        if (check_parents(g.q.n, parent) && threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_TREE);
+        depths(parent, depth);
+        ancestors(parent, mask);
+        if (warp == 0) {
+          s.depth[lane] = depth[0];
+          s.depth[lane + 32] = depth[1];
+        }
+        const uint32_t m0 = static_cast<uint32_t>(warp < 4 ? mask[0] : mask[0] >> 32);  // ancestors 8 warp .. 8 warp + 7
+        const uint32_t m1 = static_cast<uint32_t>(warp < 4 ? mask[1] : mask[1] >> 32);
+#pragma unroll 4
+        for (int j = 8 * warp; j < 8 * warp + 8; ++j) {
+          const uint32_t b0 = __ballot_sync(0xffffffffu, lane < g.q.n && (m0 >> (j & 31) & 1));
+          const uint32_t b1 = __ballot_sync(0xffffffffu, lane + 32 < g.q.n && (m1 >> (j & 31) & 1));
+          const uint32_t d0 = __ballot_sync(0xffffffffu, depth[0] <= j);
+          const uint32_t d1 = __ballot_sync(0xffffffffu, depth[1] <= j);
+          if (lane == 0) {
+            s.below[j] = b0 | static_cast<unsigned long long>(b1) << 32;
+            s.shallow[j] = d0 | static_cast<unsigned long long>(d1) << 32;
+          }
+        }
+      }
+      if (key < half) {
+        s.neg_m[c0 + key] = 0.f;
+        s.bound[c0 + key] = -INFINITY;
+      }
+      named_barrier_sync(1, kSoftmaxThreads);
       float l[kHalf];
 #pragma unroll
       for (int c = 0; c < kHalf; ++c) l[c] = 0.f;
 
-      for (int j = g.s0; j < g.s1; ++j) {
+      for (int j = 0; j < g.steps; ++j) {
         const int sb = gs & 1;
-        const int step0 = (g.q.page0 + j * kStepPages) * kPage;
-        const int pos = step0 + key;
+        const int step0 = seg0 + j * kKeys;
+        const bool masked = step0 < all0 || step0 + kKeys > min(g.q.ctx, seg1);
+        unsigned long long vis = 0;
+        if (masked && step0 + key < seg1) vis = seen_by(g.q, p.window, s, step0 + key) >> node0;
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.s_full[sb], (gs >> 1) & 1));
         tc_fence_after_sync();
-        float sv[kHalf];
 #pragma unroll
-        for (int b8 = 0; b8 < kHalf / 8; ++b8) {
-          if (8 * b8 < half) {
-            tmem_ld8(t_row + C::kSCol + sb * kN + c0 + 8 * b8, *reinterpret_cast<float(*)[8]>(&sv[8 * b8]));
-          } else {
+        for (int blk = 0; blk < kHalf; blk += kBlock) {
+          if (blk >= half) continue;
+          const int cb = c0 + blk;  // first column of the block
+          float sv[kBlock];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sv[8 * b8 + e] = -INFINITY;
-          }
-        }
-        tmem_wait_ld();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.s_free[sb]);
-
-        if (step0 < all0 || step0 + kKeys > g.q.ctx) {
-          unsigned long long vis = 0;
-          for (int i = 0; i < g.nodes; ++i)
-            if (pos >= g.q.lo && sees(g.q, p.window, s, node0 + i, pos)) vis |= 1ull << i;
+          for (int b8 = 0; b8 < kBlock / 8; ++b8) {
+            if (blk + 8 * b8 < half) {
+              tmem_ld8(t_row + C::kSCol + sb * kN + cb + 8 * b8, *reinterpret_cast<float(*)[8]>(&sv[8 * b8]));
+            } else {
 #pragma unroll
-          for (int c = 0; c < kHalf; ++c)
-            if (!((vis >> ((c0 + c) / kG)) & 1)) sv[c] = -INFINITY;
-        }
-        bool moves = false;
-#pragma unroll
-        for (int c4 = 0; c4 < kHalf / 4; ++c4) {
-          if (4 * c4 < half) {
-            const float4 t = *reinterpret_cast<const float4*>(&s.bound[c0 + 4 * c4]);
-            moves |= sv[4 * c4] > t.x || sv[4 * c4 + 1] > t.y || sv[4 * c4 + 2] > t.z || sv[4 * c4 + 3] > t.w;
-          }
-        }
-        if (barrier_or(bar, 128, moves)) {
-          reduce_into<kHalf>(sv, s.red[warp], fmax2);
-          named_barrier_sync(bar, 128);
-          if (gtid < half) {
-            const int w0 = h * 4;
-            const float mx = fmaxf(fmaxf(s.red[w0][gtid], s.red[w0 + 1][gtid]), fmaxf(s.red[w0 + 2][gtid], s.red[w0 + 3][gtid]));
-            float f = 1.f;
-            if (mx > s.bound[c0 + gtid]) {
-              const float m = fmaf(mx, kLog2e, kHeadroom);
-              if (s.bound[c0 + gtid] != -INFINITY) f = ex2_approx(s.m[c0 + gtid] - m);
-              s.m[c0 + gtid] = m;
-              s.bound[c0 + gtid] = (m + kSlack) * (1.f / kLog2e);
+              for (int e = 0; e < 8; ++e) sv[8 * b8 + e] = -INFINITY;
             }
-            s.f[c0 + gtid] = f;
           }
-          named_barrier_sync(bar, 128);
+          tmem_wait_ld();
+          if (blk + kBlock >= half) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.s_free[sb]);
+          }
+          if (masked) {
 #pragma unroll
-          for (int c = 0; c < kHalf; ++c)
-            if (c < half) l[c] *= s.f[c0 + c];
-          if (j > g.s0) {
-            // O^T holds the products up to step j - 1: wait for the last, then scale in place
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[(gs - 1) & 1], ((gs - 1) >> 1) & 1));
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int c = 0; c < half; c += 8) {
-              const float4 f0 = *reinterpret_cast<const float4*>(&s.f[c0 + c]);
-              const float4 f1 = *reinterpret_cast<const float4*>(&s.f[c0 + c + 4]);
-              float ov[kTiles][8];
+            for (int b8 = 0; b8 < kBlock / 8; ++b8) {
+              const uint32_t bits = static_cast<uint32_t>(vis >> ((cb + 8 * b8) / kG & 63));
 #pragma unroll
-              for (int t = 0; t < kTiles; ++t) tmem_ld8(t_row + t * kN + c0 + c, ov[t]);
-              tmem_wait_ld();
+              for (int e = 0; e < 8; ++e)
+                if (!((bits >> (kG >= 8 ? 0 : e / kG)) & 1)) sv[8 * b8 + e] = -INFINITY;
+            }
+          } else if (j == 0) {
+            if (key == 0) {  // first references
 #pragma unroll
-              for (int t = 0; t < kTiles; ++t) {
-                const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                uint32_t w[8];
+              for (int c = 0; c < kBlock; ++c)
+                if (blk + c < half && sv[c] > -INFINITY && sv[c] < INFINITY) {
+                  const float m = fmaf(sv[c], kLog2e, kHeadroom);
+                  s.neg_m[cb + c] = -m;
+                  s.bound[cb + c] = (m + kSlack) * (1.f / kLog2e);
+                }
+            }
+            named_barrier_sync(bar, 128);
+          }
+          bool moves = false;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(ov[t][e] * f[e]);
-                tmem_st8(t_row + t * kN + c0 + c, w);
+          for (int c4 = 0; c4 < kBlock / 4; ++c4) {
+            if (blk + 4 * c4 < half) {
+              const float4 t = *reinterpret_cast<const float4*>(&s.bound[cb + 4 * c4]);
+              moves |= (sv[4 * c4] > t.x) | (sv[4 * c4 + 1] > t.y) | (sv[4 * c4 + 2] > t.z) | (sv[4 * c4 + 3] > t.w);
+            }
+          }
+          if (barrier_or(bar, 128, moves)) {
+            float* const red = s.red[warp] + blk;
+            reduce_into<kBlock>(sv, red, fmax2);
+            named_barrier_sync(bar, 128);
+            if (key < kBlock && blk + key < half) {
+              const int w0 = h * 4, c = blk + key, col = c0 + c;
+              const float mx = fmaxf(fmaxf(s.red[w0][c], s.red[w0 + 1][c]), fmaxf(s.red[w0 + 2][c], s.red[w0 + 3][c]));
+              float f = 1.f;
+              if (mx > s.bound[col]) {
+                const float m = fmaf(mx, kLog2e, kHeadroom);
+                if (s.bound[col] != -INFINITY) f = ex2_approx(-s.neg_m[col] - m);
+                s.neg_m[col] = -m;
+                s.bound[col] = (m + kSlack) * (1.f / kLog2e);
               }
+              s.f[col] = f;
             }
-            tmem_wait_st();
+            named_barrier_sync(bar, 128);
+#pragma unroll
+            for (int c = 0; c < kBlock; ++c)
+              if (blk + c < half) l[blk + c] *= s.f[cb + c];
+            if (j > 0) {
+              // O^T holds the products up to step j - 1: wait for the last, then scale in place
+              if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[(gs - 1) & 1], ((gs - 1) >> 1) & 1));
+              tc_fence_after_sync();
+#pragma unroll 1
+              for (int c = 0; c < kBlock && blk + c < half; c += 8) {
+#pragma unroll 1
+                for (int t = 0; t < kTiles; ++t) {
+                  float ov[8];
+                  uint32_t w[8];
+                  tmem_ld8(t_row + t * kN + cb + c, ov);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(ov[e] * s.f[cb + c + e]);
+                  tmem_st8(t_row + t * kN + cb + c, w);
+                }
+              }
+              tmem_wait_st();
+            }
           }
-        }
-        // weights; the buffer's last reader was the product of step j - 2
-        if (ok && gs >= 2) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[sb], ((gs >> 1) - 1) & 1));
+          // weights; the buffer's last reader was the product of step j - 2
+          if (blk == 0 && ok && gs >= 2)
+            ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[sb], ((gs >> 1) - 1) & 1));
 #pragma unroll
-        for (int b8 = 0; b8 < kHalf / 8; ++b8) {
-          if (8 * b8 < half) {
-            const float4 m0 = *reinterpret_cast<const float4*>(&s.m[c0 + 8 * b8]);
-            const float4 m1 = *reinterpret_cast<const float4*>(&s.m[c0 + 8 * b8 + 4]);
-            const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-            float w[8];
+          for (int b8 = 0; b8 < kBlock / 8; ++b8) {
+            if (blk + 8 * b8 < half) {
+              float2 w[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              w[e] = ex2_approx(fmaf(sv[8 * b8 + e], kLog2e, -m[e]));
-              l[8 * b8 + e] += w[e];
+              for (int e = 0; e < 4; ++e) {
+                const float2 m = *reinterpret_cast<const float2*>(&s.neg_m[cb + 8 * b8 + 2 * e]);
+                const float2 x = __ffma2_rn(make_float2(sv[8 * b8 + 2 * e], sv[8 * b8 + 2 * e + 1]), log2e2, m);
+                w[e] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                const int c = blk + 8 * b8 + 2 * e;
+                const float2 sum = __fadd2_rn(make_float2(l[c], l[c + 1]), w[e]);
+                l[c] = sum.x;
+                l[c + 1] = sum.y;
+              }
+              const int col = cb + 8 * b8;
+              st_shared_v4(
+                  smem_addr(s.p[sb]) + (col >> 6) * C::kPChunk + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4),
+                  make_uint4(pack_bf16x2(w[0].x, w[0].y), pack_bf16x2(w[1].x, w[1].y), pack_bf16x2(w[2].x, w[2].y),
+                             pack_bf16x2(w[3].x, w[3].y)));
             }
-            const int col = c0 + 8 * b8;
-            st_shared_v4(smem_addr(s.p[sb]) + (col >> 6) * C::kPChunk + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4),
-                         make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]),
-                                    pack_bf16x2(w[6], w[7])));
           }
         }
         fence_proxy_async_smem();
@@ -815,64 +929,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++gs;
       }
 
+      more = walk.next(p, s, ahead);
+      if (more) read_parents(p.parents + ahead.q.q0, ahead.q.n, ahead_parent);
       // ---- end of the segment: sums, then this thread's dim of every row ----
       reduce_into<kHalf>(l, s.red[warp], add2);
       named_barrier_sync(bar, 128);
-      if (gtid < half) {
-        const int w0 = h * 4, col = c0 + gtid;
-        const float sum = (s.red[w0][gtid] + s.red[w0 + 1][gtid]) + (s.red[w0 + 2][gtid] + s.red[w0 + 3][gtid]);
+      if (key < half) {
+        const int w0 = h * 4, col = c0 + key;
+        const float sum = (s.red[w0][key] + s.red[w0 + 1][key]) + (s.red[w0 + 2][key] + s.red[w0 + 3][key]);
         if (g.whole)
           s.f[col] = sum > 0.f ? 1.f / sum : sum;  // 0: a row that sees nothing; NaN stays
         else if (col < g.cols)
-          p.part_ml[static_cast<size_t>(g.slot) * kN + col] = partial_stats(s.m[col], sum);
+          p.part_ml[static_cast<size_t>(g.slot) * kN + col] = partial_stats(-s.neg_m[col], sum);
       }
       named_barrier_sync(bar, 128);
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.o_full, gt & 1));
       tc_fence_after_sync();
       const bool poison = s.poison != 0;
+      // column col's row of the output: node col / kG, head col % kG
+      const size_t row0 = static_cast<size_t>(g.row0) * C::kHq + walk.kv * kG;
 #pragma unroll 1
       for (int c = 0; c < half; c += 8) {
+        const int col = c0 + c;
+        if (col >= g.cols) break;  // (uniform: whole blocks of 8 columns)
         float ov[kTiles][8];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) tmem_ld8(t_row + t * kN + c0 + c, ov[t]);
+        for (int t = 0; t < kTiles; ++t) tmem_ld8(t_row + t * kN + col, ov[t]);
         tmem_wait_ld();
+        if (poison) {
+          // the elements that were zeroed, for the rows that see them
+#pragma unroll 1
+          for (int pos = max(g.q.lo, seg0); pos < min(g.q.L, seg1); ++pos) {
+            if (pos >= all0 && pos < g.q.ctx) {
+              pos = g.q.ctx - 1;
+              continue;
+            }
+            const int id = p.block_table[static_cast<int64_t>(g.b) * p.max_blocks + pos / kPage];
+            if (id < 0 || static_cast<int64_t>(id) >= p.num_pages) continue;
+            const __nv_bfloat16* v = p.v_pool + ((static_cast<size_t>(id) * kPage + pos % kPage) * C::kHkv + walk.kv) * kD;
+            const unsigned long long vis = seen_by(g.q, p.window, s, pos) >> node0;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          const int d = t * 128 + gtid;
-          if (poison) {
-            // the elements that were zeroed, for the rows that see them
-            const int end = min(g.q.L, (g.q.page0 + g.s1 * kStepPages) * kPage);
-            for (int pos = max(g.q.lo, (g.q.page0 + g.s0 * kStepPages) * kPage); pos < end; ++pos) {
-              if (pos >= all0 && pos < g.q.ctx) {
-                pos = min(g.q.ctx, end) - 1;
-                continue;
-              }
-              const int id = p.block_table[static_cast<int64_t>(g.b) * p.max_blocks + pos / kPage];
-              if (id < 0 || static_cast<int64_t>(id) >= p.num_pages) continue;
-              const size_t row = static_cast<size_t>(id) * kPage + pos % kPage;
-              const float v = __bfloat162float(p.v_pool[(row * C::kHkv + walk.kv) * kD + d]);
-              if (fabsf(v) < INFINITY) continue;
+            for (int t = 0; t < kTiles; ++t) {
+              const float x = __bfloat162float(v[t * 128 + key]);
+              if (fabsf(x) < INFINITY) continue;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                if (c0 + c + e < g.cols && sees(g.q, p.window, s, node0 + (c0 + c + e) / kG, pos)) ov[t][e] += v;
+                if ((vis >> ((col + e) / kG & 63)) & 1) ov[t][e] += x;
             }
           }
+        }
+        if (g.whole) {
+          const size_t at = (row0 + static_cast<size_t>(col / kG) * C::kHq + col % kG) * kD;
+          const auto row_of = [](int e) { return (kG >= 8 ? e : (e / kG) * C::kHq + e % kG) * kD; };
+          if (p.out_f32) {
+            float* const out = static_cast<float*>(p.o) + at + key;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int col = c0 + c + e;
-            if (col >= g.cols) continue;
-            if (g.whole) {
-              const size_t at =
-                  (static_cast<size_t>(g.row0 + col / kG) * C::kHq + walk.kv * kG + col % kG) * kD + d;
-              const float v = ov[t][e] * s.f[col];
-              if (p.out_f32)
-                static_cast<float*>(p.o)[at] = v;
-              else
-                static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(v);
-            } else {
-              p.part_o[(static_cast<size_t>(g.slot) * kN + col) * kD + d] = ov[t][e];
+            for (int e = 0; e < 8; ++e) {
+              const float f = s.f[col + e];
+              if (kG < 8 && col + e >= g.cols) continue;
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) out[row_of(e) + t * 128] = ov[t][e] * f;
+            }
+          } else {
+            // two columns at a time: even lanes store dims (d, d + 1) of the first, odd lanes (d - 1, d) of the second
+            const int odd = lane & 1;
+            __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.o) + at + (key & ~1);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float f = s.f[col + e + odd];
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) {
+                const float mine = odd ? ov[t][e + 1] : ov[t][e];
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? ov[t][e] : ov[t][e + 1], 1);
+                const uint32_t w = odd ? pack_bf16x2(other * f, mine * f) : pack_bf16x2(mine * f, other * f);
+                if (kG >= 8 || col + e + odd < g.cols)
+                  *reinterpret_cast<uint32_t*>(out + (odd ? row_of(e + 1) : row_of(e)) + t * 128) = w;
+              }
             }
           }
+        } else {
+          float* const out = p.part_o + (static_cast<size_t>(g.slot) * kN + col) * kD + key;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) out[e * kD + t * 128] = ov[t][e];
         }
       }
       tc_fence_before_sync();
@@ -893,33 +1033,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  if constexpr (kCluster > 1) cluster_sync_all();  // nothing of the other CTA may arrive in one that has left
+}
+
+template <typename C>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
+  tree_body<C>(tm_q, tm_k, tm_v, p);
+}
+
+template <typename C>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
+  tree_body<C>(tm_q, tm_k, tm_v, p);
 }
 
 // ---------------------------------------------------------------------------
 // The cut sequences' rows, joined from their partials: o = sum 2^(m_i - M) O_i /
 // sum 2^(m_i - M) l_i.  Every block reads the cuts that the blocks of the first kernel
-// noted and takes rows blockIdx.x, blockIdx.x + gridDim.x, ... of them all; groups of D / 4
-// threads, four dims a thread, take a row's partials in turn, kInFlight loads in
-// flight, and meet in shared memory.
+// noted; an item is 128 dims of a row, four a lane, a warp's or, where there are fewer
+// items than half the warps, a whole block's, whose warps take the partials in turn and
+// meet in shared memory.  kMergeInFlight partials are in flight a warp.
 // ---------------------------------------------------------------------------
-constexpr int kMergeGroups = 4;
+constexpr int kMergeWarps = 4;
+constexpr int kMergeBlocksPerSm = 5;
 constexpr int kMergeInFlight = 8;
 
 struct MergeParams {
   TreeParams t;
   int32_t grid;    // blocks of the first kernel
-  int32_t stride;  // distance of consecutive blocks of a list: KV heads
+  int32_t stride;  // distance of consecutive blocks of a list: KV heads, times the cluster
 };
 
 template <typename C>
-__global__ void __launch_bounds__(kMergeGroups* C::kD / 4) merge_kernel(const __grid_constant__ MergeParams mp) {
+__global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocksPerSm) merge_kernel(const __grid_constant__ MergeParams mp) {
   const TreeParams& p = mp.t;
-  constexpr int kD = C::kD, kGroupThreads = kD / 4, kThreadsHere = kMergeGroups * kGroupThreads;
+  constexpr int kD = C::kD, kThreadsHere = kMergeWarps * 32;
   __shared__ int32_t s_rows[kMaxGrid + 1];
-  __shared__ int32_t s_warp[kThreadsHere / 32];
-  __shared__ float s_m[kMergeGroups], s_l[kMergeGroups];
-  __shared__ float4 s_o[kMergeGroups][kGroupThreads];
-  const int tid = threadIdx.x % kGroupThreads, group = threadIdx.x / kGroupThreads;
+  __shared__ int32_t s_warp[kMergeWarps];
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  __shared__ float4 s_o[kMergeWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_primary_grid();
   allow_dependent_launch();
@@ -941,7 +1096,8 @@ __global__ void __launch_bounds__(kMergeGroups* C::kD / 4) merge_kernel(const __
     if (lane == 31) s_warp[warp] = n;
     __syncthreads();
     int total = 0;
-    for (int w = 0; w < kThreadsHere / 32; ++w) {
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
       if (w < warp) n += s_warp[w];
       total += s_warp[w];
     }
@@ -949,7 +1105,12 @@ __global__ void __launch_bounds__(kMergeGroups* C::kD / 4) merge_kernel(const __
     carry += total;
     __syncthreads();
   }
-  for (int row = blockIdx.x; row < carry; row += gridDim.x) {
+  const int items = carry * C::kTiles;
+  const int team = items * 2 < static_cast<int>(gridDim.x) * kMergeWarps ? kMergeWarps : 1;
+  const int teams = static_cast<int>(gridDim.x) * kMergeWarps / team;
+  const int member = warp % team;
+  for (int item = (static_cast<int>(blockIdx.x) * kMergeWarps + warp) / team; item < items; item += teams) {
+    const int row = item / C::kTiles, d = item % C::kTiles * 128 + 4 * lane;
     int lo = 0, hi = mp.grid - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -959,18 +1120,18 @@ __global__ void __launch_bounds__(kMergeGroups* C::kD / 4) merge_kernel(const __
     const int col = row - s_rows[lo], kv = cut.y >> 8, parts = cut.w;
     float M = -INFINITY, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = group; i0 < parts; i0 += kMergeGroups * kMergeInFlight) {
+    for (int i0 = member; i0 < parts; i0 += team * kMergeInFlight) {
       float2 e[kMergeInFlight];
       float4 a[kMergeInFlight];
 #pragma unroll
       for (int u = 0; u < kMergeInFlight; ++u) {
-        const int i = i0 + u * kMergeGroups;
+        const int i = i0 + u * team;
         e[u] = make_float2(-INFINITY, 0.f);
         a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < parts) {
           const size_t at = static_cast<size_t>(i == 0 ? cut.z : 2 * (lo + i * mp.stride)) * C::kN + col;
           e[u] = p.part_ml[at];
-          a[u] = __ldcs(reinterpret_cast<const float4*>(p.part_o + at * kD + 4 * tid));
+          a[u] = __ldcs(reinterpret_cast<const float4*>(p.part_o + at * kD + d));
         }
       }
       float m = M;
@@ -991,28 +1152,31 @@ __global__ void __launch_bounds__(kMergeGroups* C::kD / 4) merge_kernel(const __
       }
       M = m;
     }
-    if (tid == 0) {
-      s_m[group] = M;
-      s_l[group] = L;
-    }
-    s_o[group][tid] = O;
-    __syncthreads();
-    if (group == 0) {
-      float m = M;
-#pragma unroll
-      for (int w = 1; w < kMergeGroups; ++w) m = fmaxf(m, s_m[w]);
-      L = 0.f;
-      O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kMergeGroups; ++w) {
-        const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - m);
-        const float4 v = s_o[w][tid];
-        L += f * s_l[w];
-        O.x += f * v.x; O.y += f * v.y; O.z += f * v.z; O.w += f * v.w;
+    if (team > 1) {  // (the same for every warp of the grid)
+      if (lane == 0) {
+        s_m[warp] = M;
+        s_l[warp] = L;
       }
+      s_o[warp][lane] = O;
+      __syncthreads();
+      if (warp == 0) {
+        float m = M;
+#pragma unroll
+        for (int w = 1; w < kMergeWarps; ++w) m = fmaxf(m, s_m[w]);
+        L = 0.f;
+        O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+          const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - m);
+          const float4 v = s_o[w][lane];
+          L += f * s_l[w];
+          O.x += f * v.x; O.y += f * v.y; O.z += f * v.z; O.w += f * v.w;
+        }
+      }
+    }
+    if (member == 0) {
       const float inv = L > 0.f ? 1.f / L : L;
-      const size_t at =
-          (static_cast<size_t>(cut.x + col / C::kG) * C::kHq + kv * C::kG + col % C::kG) * kD + 4 * tid;
+      const size_t at = (static_cast<size_t>(cut.x + col / C::kG) * C::kHq + kv * C::kG + col % C::kG) * kD + d;
       const float4 v = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
       if (p.out_f32) {
         *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = v;
@@ -1021,12 +1185,13 @@ __global__ void __launch_bounds__(kMergeGroups* C::kD / 4) merge_kernel(const __
             make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
       }
     }
-    __syncthreads();  // the shared rows were read
+    if (team > 1) __syncthreads();  // the shared partials were read
   }
 }
 
-// D = 512: 64 rows, four nodes; D = 256: 128 rows, 64 nodes, or fewer with longer rings.
+// D = 512: 64 rows, four nodes, alone or in pairs; D = 256: 128 rows, 64 nodes, or fewer with longer rings.
 using GlobalConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 4, 3>;
+using GlobalPairConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 4, 3, 2>;
 using SlidingWideConfig = Config<ATTN_SLIDING_D, ATTN_SLIDING_HQ / ATTN_SLIDING_HKV, ATTN_SLIDING_HKV, 128, 3, 5>;
 using SlidingConfig = Config<ATTN_SLIDING_D, ATTN_SLIDING_HQ / ATTN_SLIDING_HKV, ATTN_SLIDING_HKV, 32, 6, 8>;
 

@@ -15,16 +15,22 @@ namespace {
 // ---------------------------------------------------------------------------
 // A call of few, short sequences: every (sequence, group, KV head) in a block of its
 // own, and no merge kernel.
-constexpr int kTreeWholeSteps = 2;
+constexpr int kTreeWholePages = 16;
 
 struct TreePlan {
   int rows;      // of the configuration's groups
-  int groups;    // per KV head
+  int cluster;   // CTAs
+  int lists;     // of pages, per KV head: ceil(max_q / (nodes of a cluster))
   int grid;
   bool whole;
   bool merge;    // a sequence may be cut: a second kernel
   size_t part_o_bytes, part_ml_bytes, workspace_bytes;
 };
+
+// Global trees of more than four nodes: two groups of rows share their copies.
+bool paired_tree(int32_t kind, int32_t max_q) {
+  return kind == ATTN_KIND_GLOBAL && max_q > pda::tree::GlobalConfig::kQueries;
+}
 
 // The sliding configuration for trees of few nodes: 32 rows, longer rings.
 bool narrow_tree(int32_t kind, int32_t max_q) {
@@ -46,23 +52,26 @@ int32_t make_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_s
   const int d = sliding ? ATTN_SLIDING_D : ATTN_GLOBAL_D;
   const int hkv = sliding ? ATTN_SLIDING_HKV : ATTN_GLOBAL_HKV;
   out->rows = !sliding ? tr::GlobalConfig::kN : narrow_tree(kind, max_q) ? tr::SlidingConfig::kN : tr::SlidingWideConfig::kN;
-  const int queries = out->rows * hkv / 16;  // 16 query heads
-  out->groups = std::max(1, (max_q + queries - 1) / queries);
+  out->cluster = paired_tree(kind, max_q) ? tr::GlobalPairConfig::kCluster : 1;
+  const int nodes = out->rows * hkv / 16 * out->cluster;  // 16 query heads
+  out->lists = std::max(1, (max_q + nodes - 1) / nodes);
   // pages of one sequence: with a window those of window + max_q - 1 positions
   const int64_t span = window > 0 ? std::min<int64_t>(max_seq_len, static_cast<int64_t>(window) + max_q - 1) : max_seq_len;
-  const int64_t pages = std::min<int64_t>((span + 2 * ATTN_PAGE_SIZE - 2) / ATTN_PAGE_SIZE,
-                                          (static_cast<int64_t>(max_seq_len) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE);
-  const int64_t steps = std::max<int64_t>(1, (pages + tr::kStepPages - 1) / tr::kStepPages);
-  const int64_t items = static_cast<int64_t>(batch) * out->groups * hkv;
-  out->whole = num_splits == 0 && items <= num_sms && steps <= kTreeWholeSteps;
-  out->merge = !out->whole && steps > 1;
+  const int64_t pages = std::max<int64_t>(1, std::min<int64_t>((span + 2 * ATTN_PAGE_SIZE - 2) / ATTN_PAGE_SIZE,
+                                                               (static_cast<int64_t>(max_seq_len) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE));
+  const int64_t items = static_cast<int64_t>(batch) * out->lists * hkv;
+  const int64_t clusters = std::max(1, num_sms / out->cluster);
+  out->whole = num_splits == 0 && items <= clusters && pages <= kTreeWholePages;
+  out->merge = !out->whole && pages > 1;
   if (out->whole) {
-    out->grid = static_cast<int>(items);
+    out->grid = static_cast<int>(items) * out->cluster;
   } else if (num_splits > 0) {
-    out->grid = num_splits;
+    out->grid = (num_splits + out->cluster - 1) / out->cluster * out->cluster;
   } else {
-    const int64_t useful = (items * (steps + 1) + tr::kMinPer - 1) / tr::kMinPer;
-    out->grid = static_cast<int>(std::max<int64_t>(tr::kMaxGroups, std::min<int64_t>({num_sms, useful, tr::kMaxGrid})));
+    const int64_t useful = (items * (pages + tr::kSegWeight) + tr::kMinPer - 1) / tr::kMinPer;
+    const int64_t least = tr::kMaxGroups;  // a run for every list
+    out->grid = static_cast<int>(std::max<int64_t>(least, std::min<int64_t>({clusters, useful, tr::kMaxGrid / out->cluster}))) *
+                out->cluster;
   }
   const size_t rows = 2 * static_cast<size_t>(out->grid) * out->rows;
   out->part_o_bytes = out->merge ? align256(rows * d * sizeof(float)) : 0;
@@ -102,20 +111,25 @@ int32_t launch_tree(const char* name, const void* q, const void* k_pool, const v
       (st = encode_chunk_map(&tm_k, k_pool, p.num_pages, C::kHkv * C::kD, 1)) ||
       (st = encode_chunk_map(&tm_v, v_pool, p.num_pages, C::kHkv * C::kD, C::kChunks)))
     return st;
+  const auto kernel = [] {
+    if constexpr (C::kCluster > 1)
+      return tr::tree_pair_kernel<C>;
+    else
+      return tr::tree_kernel<C>;
+  }();
   static bool main_set[kMaxDevices] = {false}, merge_set[kMaxDevices] = {false};
-  if ((st = ensure_smem(tr::tree_kernel<C>, C::kSmemBytes, dev, main_set)) ||
+  if ((st = ensure_smem(kernel, C::kSmemBytes, dev, main_set)) ||
       (st = ensure_smem(tr::merge_kernel<C>, 0, dev, merge_set)))
     return st;
-  cudaError_t e = launch_pdl(tr::tree_kernel<C>, dim3(plan.grid), tr::kThreads, C::kSmemBytes, s, tm_q, tm_k, tm_v, p);
+  cudaError_t e = launch_pdl(kernel, dim3(plan.grid), tr::kThreads, C::kSmemBytes, s, tm_q, tm_k, tm_v, p);
   if (e == cudaSuccess && plan.merge) {
     tr::MergeParams mp;
     mp.t = p;
     mp.grid = plan.grid;
-    mp.stride = C::kHkv;
-    constexpr int kBlockThreads = tr::kMergeGroups * C::kD / 4;
-    const int64_t rows = static_cast<int64_t>(p.batch) * p.max_q * C::kHq;
-    const int blocks = static_cast<int>(std::min<int64_t>(rows, static_cast<int64_t>(num_sms) * (2048 / kBlockThreads)));
-    e = launch_pdl(tr::merge_kernel<C>, dim3(blocks), kBlockThreads, 0, s, mp);
+    mp.stride = C::kHkv * C::kCluster;
+    const int64_t rows = static_cast<int64_t>(p.batch) * p.max_q * C::kHq;  // a block per row's 128 dims, at most
+    const int blocks = static_cast<int>(std::min<int64_t>(rows * C::kTiles, static_cast<int64_t>(num_sms) * tr::kMergeBlocksPerSm));
+    e = launch_pdl(tr::merge_kernel<C>, dim3(blocks), tr::kMergeWarps * 32, 0, s, mp);
   }
   return launched(name, e);
 }
@@ -178,12 +192,15 @@ int32_t run_tree(int32_t kind, const void* q, const void* k_pool, const void* v_
   p.window = window;
   p.total_q = total_q;
   p.max_q = max_q;
-  p.groups = plan.groups;
+  p.lists = plan.lists;
   p.out_f32 = out_dtype == ATTN_OUT_F32;
   p.whole = plan.whole;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   namespace tr = pda::tree;
-  if (!sliding) return launch_tree<tr::GlobalConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);
+  if (!sliding)
+    return paired_tree(kind, max_q)
+               ? launch_tree<tr::GlobalPairConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s)
+               : launch_tree<tr::GlobalConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);
   return narrow_tree(kind, max_q)
              ? launch_tree<tr::SlidingConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s)
              : launch_tree<tr::SlidingWideConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);

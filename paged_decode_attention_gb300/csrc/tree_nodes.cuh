@@ -23,14 +23,20 @@ __device__ __forceinline__ T of_node(const T (&v)[2], int i) {
   return i & 32 ? b : a;
 }
 
-// The parents of n <= ATTN_MAX_TREE nodes; those outside [-1, i) count as -1.
-// Returns whether there was one (the same in every lane).
-__device__ __forceinline__ bool load_parents(const int32_t* parents, int n, int (&parent)[2]) {
-  bool bad = false;
+// The parents of n <= ATTN_MAX_TREE nodes, as they are ...
+__device__ __forceinline__ void read_parents(const int32_t* parents, int n, int (&parent)[2]) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = (threadIdx.x & 31) + 32 * u;
     parent[u] = i < n ? parents[i] : -1;
+  }
+}
+// ... and those outside [-1, i) made -1.  Returns whether there was one (the same in every lane).
+__device__ __forceinline__ bool check_parents(int n, int (&parent)[2]) {
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = (threadIdx.x & 31) + 32 * u;
     if (parent[u] < -1 || parent[u] >= i) {
       bad |= i < n;
       parent[u] = -1;

@@ -141,10 +141,11 @@ def test_tree_plan(lib):
     assert pda.attn_decode_tree_plan(S, 64, 45, 32768, 1024) == (152, 2, workspace(152, 128, 256))
     # trees of up to 16 nodes on sliding layers: 32 rows
     assert pda.attn_decode_tree_plan(S, 64, 16, 32768, 1024) == (152, 2, workspace(152, 32, 256))
-    # one step of keys: nothing to merge
-    assert pda.attn_decode_tree_plan(G, 200, 4, 128, 0)[1:] == (1, a256(152 * 16))
-    # a few short sequences: a block for each group of nodes
-    assert pda.attn_decode_tree_plan(G, 3, 9, 256, 0) == (9, 1, a256(9 * 16))
+    # one page each: nothing to merge
+    assert pda.attn_decode_tree_plan(G, 200, 4, 16, 0)[1:] == (1, a256(152 * 16))
+    # a few short sequences: a block (global trees of more than four nodes: two) for each group of nodes
+    assert pda.attn_decode_tree_plan(G, 3, 4, 256, 0) == (3, 1, a256(3 * 16))
+    assert pda.attn_decode_tree_plan(G, 3, 9, 256, 0) == (12, 1, a256(12 * 16))
     assert pda.attn_decode_tree_plan(S, 2, 9, 240, 1024) == (16, 1, a256(16 * 16))
     # forced
     assert pda.attn_decode_tree_plan(G, 1, 1, 200, 0, 16)[0] == 16
