@@ -76,13 +76,47 @@ struct ChunkParams {
   FloatPair bit_factor[kPairBits];  // theta^(-2 * 2^k / D)
 };
 
+// A node of a tree: its slot's position (-1: it is left alone), where it is rotated, the slot's page.
+struct Node {
+  int32_t pos, turned, phys;
+};
+constexpr int kAhead = kQWarps;  // nodes looked up together
+
+template <bool kTree>
 struct Smem {
   int32_t cu_q[kMaxBatch + 1];
   int32_t len[kMaxBatch];
+  Node node[kTree ? kAhead : 1];
   // cos and sin of the token's pairs, double-buffered
   alignas(16) float cos[2][1 << kPairBits];
   alignas(16) float sin[2][1 << kPairBits];
 };
+
+// Node t, by one warp.  A chain of lookups (sequence, parents, page) and the tree's depth, some 2000 cycles: in front of
+// every token's angles they cost 2032 sliding nodes 16.7 us, looked up ahead 13.4.
+__device__ __forceinline__ Node look_up_node(const ChunkParams& p, const int32_t* cu_q, const int32_t* len, int t) {
+  const int lane = threadIdx.x & 31;
+  int b = 0;
+  for (int j0 = 0; j0 < p.batch; j0 += 32) {
+    const int j = j0 + lane;
+    b += __popc(__ballot_sync(0xffffffffu, j < p.batch && cu_q[j + 1] <= t));
+  }
+  if (b >= p.batch) return {-1, 0, 0};  // rows behind the last sequence are left alone
+  const int q0 = cu_q[b], q1 = cu_q[b + 1], L = len[b];
+  const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
+  // a sequence whose numbers do not fit together is left alone as a whole
+  if (q0 < 0 || t < q0 || q1 > p.total_q || q1 - q0 > L || L > cap || q1 - q0 > ATTN_MAX_TREE) {
+    if (lane == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+    return {-1, 0, 0};
+  }
+  int parent[2], depth[2];
+  tree::read_parents(p.parents + q0, q1 - q0, parent);
+  const int pos = L - (q1 - q0) + (t - q0);
+  const int32_t phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kPage];
+  if (tree::check_parents(q1 - q0, parent) && lane == 0) report(p.status, ATTN_DEV_BAD_TREE);
+  tree::depths(parent, depth);
+  return {pos, L - (q1 - q0) + tree::of_node(depth, t - q0), phys};
+}
 
 // cos and sin of pos * (f.hi + f.lo), a frequency in half turns.  For an integer
 // 0 <= pos < 2^24 the float product and its fma remainder hold pos * f.hi
@@ -274,7 +308,7 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
   static_assert(kHq == 2 * kQWarps && (kShared ? kHkv == 1 : kHkv == kQWarps), "rows of a token by warp");
   static_assert(kPairs <= kThreads<kShared> && kPairs <= (1 << kPairBits) && kPairs % (kD / 64) == 0 && kPairs % 32 == 0,
                 "pairs by thread");
-  __shared__ Smem s;
+  __shared__ Smem<kTree> s;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -310,9 +344,11 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
   }
 
   int buf = 0;
+  [[maybe_unused]] int round = 0;
   bool beyond = false;
   const auto tokens = [&](auto wide_c) {
     constexpr bool kWide = decltype(wide_c)::value;
+    round = 0;
     for (int t = blockIdx.x; t < p.total_q; t += gridDim.x) {
       // this warp's rows, all in flight together
       const __nv_bfloat16* src = p.qkv + static_cast<size_t>(t) * kRowLen;
@@ -324,39 +360,48 @@ __global__ void __launch_bounds__(kThreads<kShared>, kBlocksPerSm) chunk_kernel(
         load_raw<kD>(src + (kHq + warp) * kD, rk);
         load_raw<kD>(src + (kHq + kHkv + warp) * kD, rv);
       }
-      // the token's sequence: the number of sequences that end at or before t
-      // (the same in every warp of the block)
       int pos = -1;  // the token is left alone
-      [[maybe_unused]] int turned = 0;  // a node's position in its text
+      int turned = 0;  // where it is rotated
       int32_t phys = 0;
-      int b = 0;
-      for (int j0 = 0; j0 < p.batch; j0 += 32) {
-        const int j = j0 + lane;
-        b += __popc(__ballot_sync(0xffffffffu, j < p.batch && s.cu_q[j + 1] <= t));
-      }
-      if (b < p.batch) {  // rows behind the last sequence are left alone
-        const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1];
-        const int L = s.len[b];
-        const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
-        // a sequence whose numbers do not fit together is left alone as a whole
-        if (q0 < 0 || t < q0 || q1 > p.total_q || q1 - q0 > L || L > cap || (kTree && q1 - q0 > ATTN_MAX_TREE)) {
-          if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
-        } else {
-          pos = L - (q1 - q0) + (t - q0);
-          if (has_kv) phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kPage];
-          if constexpr (kTree) {
-            if (threadIdx.x < kPairs) {  // (whole warps)
-              int parent[2], depth[2];
-              tree::read_parents(p.parents + q0, q1 - q0, parent);
-              if (tree::check_parents(q1 - q0, parent) && threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_TREE);
-              tree::depths(parent, depth);
-              turned = pos - (t - q0) + tree::of_node(depth, t - q0);
-            }
+      if constexpr (kTree) {
+        // nodes are looked up a warp each, as many as there are warps, ahead of the rounds that take them
+        const int k = round++ % kAhead;
+        if (k == 0) {
+          __syncthreads();  // the last ones were read
+          if (warp < kAhead) {
+            const int64_t at = t + static_cast<int64_t>(warp) * gridDim.x;
+            const Node node = at < p.total_q ? look_up_node(p, s.cu_q, s.len, static_cast<int>(at)) : Node{-1, 0, 0};
+            if (lane == 0) s.node[warp] = node;
+          }
+          __syncthreads();
+        }
+        pos = s.node[k].pos;
+        turned = s.node[k].turned;
+        phys = s.node[k].phys;
+      } else {
+        // the token's sequence: the number of sequences that end at or before t
+        // (the same in every warp of the block)
+        int b = 0;
+        for (int j0 = 0; j0 < p.batch; j0 += 32) {
+          const int j = j0 + lane;
+          b += __popc(__ballot_sync(0xffffffffu, j < p.batch && s.cu_q[j + 1] <= t));
+        }
+        if (b < p.batch) {  // rows behind the last sequence are left alone
+          const int q0 = s.cu_q[b], q1 = s.cu_q[b + 1];
+          const int L = s.len[b];
+          const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
+          // a sequence whose numbers do not fit together is left alone as a whole
+          if (q0 < 0 || t < q0 || q1 > p.total_q || q1 - q0 > L || L > cap) {
+            if (threadIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+          } else {
+            pos = L - (q1 - q0) + (t - q0);
+            if (has_kv) phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kPage];
           }
         }
+        turned = base + pos;
       }
       if (threadIdx.x < kPairs)
-        sincos_at(freq, pos < 0 ? 0 : kTree ? turned : base + pos, &s.sin[buf][threadIdx.x], &s.cos[buf][threadIdx.x]);
+        sincos_at(freq, pos < 0 ? 0 : turned, &s.sin[buf][threadIdx.x], &s.cos[buf][threadIdx.x]);
       __syncthreads();  // one per token: the buffer written next was read before this barrier
       const float* cs = s.cos[buf];
       const float* sn = s.sin[buf];

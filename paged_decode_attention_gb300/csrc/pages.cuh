@@ -24,7 +24,8 @@ namespace pda {
 namespace pages {
 
 constexpr int kBlocks = 8;     // a portable cluster
-constexpr int kThreads = 512;  // the first kMaxBatch take a request each
+constexpr int kThreads = 1024;  // the first kMaxBatch take a request each
+constexpr int kInFlight = 4;    // pages of a thread on their way
 static_assert(kThreads >= kMaxBatch, "a thread per request");
 
 struct PagesParams {
@@ -140,16 +141,30 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) assi
   const uint32_t rank = cluster_ctarank();
 
   if (!refused) {
-    const int first = static_cast<int>(rank) * kThreads + tid;
-    for (int i = first; i < total_give + total_take; i += kBlocks * kThreads) {
-      if (i < total_take) {
-        const int at = ring.x + i < p.num_pages ? ring.x + i : ring.x + i - p.num_pages;  // i < count <= num_pages
-        p.block_table[entry_of(s.take, s.take_part, p, i)] = p.free_list[at];
-      } else {
-        const int g = i - total_take;
-        const int at = static_cast<int>((static_cast<int64_t>(ring.x) + ring.y + g) % p.num_pages);
-        p.free_list[at] = p.block_table[entry_of(s.give, s.give_part, p, g)];
+    constexpr int kStride = kBlocks * kThreads;
+    const int total = total_give + total_take;
+    for (int i0 = static_cast<int>(rank) * kThreads + tid; i0 < total; i0 += kInFlight * kStride) {
+      int32_t page[kInFlight];
+      int32_t* to[kInFlight];
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int i = i0 + u * kStride;
+        to[u] = nullptr;
+        if (i < total_take) {
+          const int at = ring.x + i < p.num_pages ? ring.x + i : ring.x + i - p.num_pages;  // i < count <= num_pages
+          to[u] = p.block_table + entry_of(s.take, s.take_part, p, i);
+          page[u] = p.free_list[at];
+        } else if (i < total) {
+          const int g = i - total_take;
+          // head < num_pages, count + g < num_pages: at most once round
+          const int at = ring.x < p.num_pages - (ring.y + g) ? ring.x + ring.y + g : ring.x - (p.num_pages - (ring.y + g));
+          to[u] = p.free_list + at;
+          page[u] = p.block_table[entry_of(s.give, s.give_part, p, g)];
+        }
       }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u)
+        if (to[u] != nullptr) *to[u] = page[u];
     }
   }
   // every block has read the old state before any of it is written

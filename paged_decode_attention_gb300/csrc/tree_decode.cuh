@@ -91,7 +91,7 @@ struct TreeParams {
   int32_t whole;    // a block per (sequence, group, KV head) instead of runs
 };
 
-template <int kD_, int kG_, int kHkv_, int kN_, int kKStages_, int kVStages_, int kCluster_ = 1>
+template <int kD_, int kG_, int kHkv_, int kN_, int kPBufs_, int kKStages_, int kVStages_, int kCluster_ = 1>
 struct Config {
   static constexpr int kCluster = kCluster_;   // CTAs that share their copies of K and V
   static constexpr int kD = kD_, kG = kG_, kHkv = kHkv_, kHq = kG * kHkv;
@@ -101,6 +101,7 @@ struct Config {
   static constexpr int kQueries = kN / kG;
   static constexpr int kChunks = kD / 64;
   static constexpr int kTiles = kD / 128;      // of 128 output dims
+  static constexpr int kPBufs = kPBufs_;
   static constexpr int kKStages = kKStages_;   // K chunks
   static constexpr int kVStages = kVStages_;   // V pages
   static constexpr int kKChunk = kKeys * 128;  // bytes: [128 keys][64 dims]
@@ -116,7 +117,7 @@ struct Config {
 
   struct Smem {
     alignas(1024) uint8_t q[kChunks][kN * 128];
-    alignas(1024) uint8_t p[2][kPBytes];
+    alignas(1024) uint8_t p[kPBufs][kPBytes];
     alignas(1024) uint8_t k[kKStages][kKChunk];
     alignas(1024) uint8_t v[kVStages][kVPage];
     alignas(16) float neg_m[kN];      // minus the reference max (log2 units), 0 before there is one
@@ -127,14 +128,14 @@ struct Config {
     alignas(8) unsigned long long shallow[ATTN_MAX_TREE];  // nodes of depth <= x
     int32_t depth[ATTN_MAX_TREE];
     int32_t pre[kMaxBatch + 1];       // pages (virtual ones included) before sequence b in this block's list
-    int32_t hist[kMaxGroups + 1];     // pages of the sequences with that many clusters of groups
-    int32_t warp_sum[kMaxBatch / 32];
+    int32_t cu_q[kMaxBatch + 1], len[kMaxBatch];
     int32_t sched[4];                 // list, KV head, per, run
+    int32_t refused;                  // the call as a whole
     int32_t poison;                   // this segment: an element was zeroed that some row sees
     alignas(8) uint64_t k_full[kKStages], k_empty[kKStages];
     alignas(8) uint64_t v_full[kVStages], v_empty[kVStages];
     alignas(8) uint64_t s_full[2], s_free[2];
-    alignas(8) uint64_t p_full[2], p_empty[2];
+    alignas(8) uint64_t p_full[kPBufs], p_empty[kPBufs];
     alignas(8) uint64_t q_ready, q_empty;
     alignas(8) uint64_t o_full, o_free;
     alignas(8) uint64_t mma_done;
@@ -149,20 +150,19 @@ struct Sequence {
   int q0, n, L, ctx, lo, page0, pages;  // pages 0: nothing to do
 };
 
-__device__ __forceinline__ Sequence load_sequence(const TreeParams& p, int b, bool& refused, bool& backwards) {
+__device__ __forceinline__ Sequence make_sequence(const TreeParams& p, int q0, int q1, int L, bool& refused) {
   Sequence s{};
-  s.q0 = p.cu_q[b];
-  const int64_t n = static_cast<int64_t>(p.cu_q[b + 1]) - s.q0;
-  s.L = p.seq_lens[b];
+  s.q0 = q0;
+  s.L = L;
+  const int64_t n = static_cast<int64_t>(q1) - q0;
   const int cap = p.max_blocks < ATTN_MAX_SEQ_LEN / kPage ? p.max_blocks * kPage : ATTN_MAX_SEQ_LEN;
-  backwards = n < 0;
-  refused = n < 0 || s.q0 < 0 || s.q0 + n > p.total_q || n > p.max_q || n > s.L || s.L > cap;
+  refused = n < 0 || q0 < 0 || q1 > p.total_q || n > p.max_q || n > L || L > cap;
   if (refused || n == 0) return s;
   s.n = static_cast<int>(n);
-  s.ctx = s.L - s.n;
+  s.ctx = L - s.n;
   s.lo = p.window > 0 && s.ctx >= p.window ? s.ctx - p.window + 1 : 0;
   s.page0 = s.lo / kPage;
-  s.pages = (s.L - 1) / kPage - s.page0 + 1;
+  s.pages = (L - 1) / kPage - s.page0 + 1;
   return s;
 }
 
@@ -216,8 +216,8 @@ struct Walk {
       g.p0 = w0 > first ? w0 - first : 0;
       g.p1 = w1 - first < pages ? w1 - first : pages;
       if (g.p1 <= g.p0) continue;
-      bool refused, backwards;
-      g.q = load_sequence(p, b, refused, backwards);
+      bool refused;
+      g.q = make_sequence(p, s.cu_q[b], s.cu_q[b + 1], s.len[b], refused);
       g.b = b;
       g.row0 = g.q.q0 + group * C::kQueries;
       g.nodes = max(0, min(C::kQueries, g.q.n - group * C::kQueries));  // (0: only the cluster's other groups have any)
@@ -351,45 +351,65 @@ __device__ __forceinline__ uint32_t row_bits(int from, int to) {
   return ((1u << to) - 1u) & ~((1u << from) - 1u);
 }
 
-// The schedule: this block's list, the running sums over it, its run.  Called by
-// every thread; ends with a barrier.  Returns false when the call is refused.
+// The schedule: this block's list, the running sums over it, its run.  Warp 0 works it out, 32 sequences a round, and
+// the block waits for it once.  (Rounds are loops, not unrolled: what runs once a call is bound by fetching its
+// instructions.)  Returns false when the call is refused.
 template <typename C, typename S>
 __device__ __forceinline__ bool make_schedule(const TreeParams& p, S& s) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid <= kMaxGroups) s.hist[tid] = 0;
-  int weight = 0, groups = 0;
-  bool refused = false, backwards = false;
-  if (tid < p.batch) {
-    const Sequence q = load_sequence(p, tid, refused, backwards);
-    if (q.pages > 0) {
-      weight = q.pages + kSegWeight;
-      groups = (q.n + C::kQueries * C::kCluster - 1) / (C::kQueries * C::kCluster);
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {
+    bool refused = false, backwards = false;
+    int total = 0;  // lane r: the pages of list r (the same for every KV head)
+    // (weight, lists) of sequence b
+    const auto weigh = [&](int b, bool& bad) {
+      const Sequence q = make_sequence(p, s.cu_q[b], s.cu_q[b + 1], s.len[b], bad);
+      constexpr int kNodes = C::kQueries * C::kCluster;
+      return q.pages > 0 ? make_int2(q.pages + kSegWeight, (q.n + kNodes - 1) / kNodes) : make_int2(0, 0);
+    };
+#pragma unroll 1
+    for (int b0 = 0; b0 <= p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      if (b <= p.batch) s.cu_q[b] = p.cu_q[b];
+      if (b < p.batch) s.len[b] = p.seq_lens[b];
     }
-  }
-  if (refused && blockIdx.x == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
-  if (__syncthreads_or(backwards)) return false;  // sequences overlap
-  if (weight > 0) atomicAdd(&s.hist[groups], weight);
-  __syncthreads();
-  if (warp == 0) {
-    // lane r: the pages of list r (the same for every KV head)
-    int total = 0;
-    for (int g = lane + 1; g <= p.lists; ++g) total += s.hist[g];
-    if (lane >= p.lists) total = 0;
-    const int g = static_cast<int>(blockIdx.x / C::kCluster);
-    if (p.whole) {
-      if (lane == 0) {
-        const int per_seq = p.lists * C::kHkv;
-        s.sched[0] = g % per_seq / C::kHkv;
-        s.sched[1] = g % C::kHkv;
-        s.sched[2] = 1;
-        s.sched[3] = g / per_seq;
+    __syncwarp();
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      int2 w = make_int2(0, 0);
+      if (b < p.batch) {
+        bool bad;
+        w = weigh(b, bad);
+        refused |= bad;
+        backwards |= s.cu_q[b + 1] < s.cu_q[b];
       }
+#pragma unroll 1
+      for (int r = 0; r < p.lists; ++r) {
+        const int sum = __reduce_add_sync(0xffffffffu, w.y > r ? w.x : 0);
+        if (lane == r) total += sum;
+      }
+    }
+    refused = __any_sync(0xffffffffu, refused);
+    backwards = __any_sync(0xffffffffu, backwards);  // sequences overlap
+    if (refused && blockIdx.x == 0 && lane == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+    const int g = static_cast<int>(blockIdx.x / C::kCluster);
+    int list, kv, per, run;
+    if (p.whole) {
+      const int per_seq = p.lists * C::kHkv;
+      list = g % per_seq / C::kHkv;
+      kv = g % C::kHkv;
+      per = 1;
+      run = g / per_seq;
     } else {
       const int grid = static_cast<int>(gridDim.x / C::kCluster);
       const int sum = __reduce_add_sync(0xffffffffu, total);
-      int lo = max(kMinPer, static_cast<int>((static_cast<long long>(sum) * C::kHkv + grid - 1) / grid));
-      int hi = max(lo, __reduce_max_sync(0xffffffffu, total));
-      const auto runs = [&](int per) { return __reduce_add_sync(0xffffffffu, (total + per - 1) / per) * C::kHkv; };
+      int lo = max(kMinPer, (sum * C::kHkv + grid - 1) / grid);  // (at most 256 * 16388 pages * 8 heads a list)
+      // (every list's last run may be short: with that many runs less there is room for all)
+      const int lists = p.lists * C::kHkv;
+      int hi = __reduce_max_sync(0xffffffffu, total);
+      if (grid > lists) hi = min(hi, (sum * C::kHkv + grid - lists - 1) / (grid - lists));
+      hi = max(lo, hi);
+      const auto runs = [&](int n) { return __reduce_add_sync(0xffffffffu, (total + n - 1) / n) * C::kHkv; };
       if (runs(lo) <= grid) {
         hi = lo;
       } else {
@@ -398,7 +418,7 @@ __device__ __forceinline__ bool make_schedule(const TreeParams& p, S& s) {
           if (runs(mid) <= grid) hi = mid; else lo = mid;
         }
       }
-      const int per = hi;
+      per = hi;
       const int mine = (total + per - 1) / per * C::kHkv;  // this list's clusters
       int before = mine;
 #pragma unroll
@@ -408,40 +428,39 @@ __device__ __forceinline__ bool make_schedule(const TreeParams& p, S& s) {
       }
       before -= mine;
       const unsigned here = __ballot_sync(0xffffffffu, mine > 0 && before <= g && g < before + mine);
-      if (lane == 0) {
-        s.sched[0] = 0;
-        s.sched[1] = 0;
-        s.sched[2] = per;
-        s.sched[3] = -1;  // no run: the block has nothing to do
-      }
-      __syncwarp();
-      if (here && lane == __ffs(here) - 1) {
-        s.sched[0] = lane;
-        s.sched[1] = (g - before) % C::kHkv;
-        s.sched[3] = (g - before) / C::kHkv;
-      }
+      const int owner = here ? __ffs(here) - 1 : 0;
+      before = __shfl_sync(0xffffffffu, before, owner);
+      list = owner;
+      kv = here ? (g - before) % C::kHkv : 0;
+      run = here ? (g - before) / C::kHkv : -1;  // -1: the block has nothing to do
     }
-  }
-  __syncthreads();
-  // the running sums of this block's list
-  const int mine = groups > s.sched[0] ? weight : 0;
-  int sum = mine;
-  if (tid < kMaxBatch) {
+    // the running sums of this block's list
+    int carry = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      bool bad;
+      const int2 w = b < p.batch ? weigh(b, bad) : make_int2(0, 0);
+      int sum = w.y > list ? w.x : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += u;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (b < p.batch) s.pre[b + 1] = carry + sum;
+      carry += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 31) s.warp_sum[warp] = sum;
+    if (lane == 0) {
+      s.pre[0] = 0;
+      s.sched[0] = list;
+      s.sched[1] = kv;
+      s.sched[2] = per;
+      s.sched[3] = run;
+      s.refused = backwards;
+    }
   }
   __syncthreads();
-  if (tid < p.batch) {
-    for (int w = 0; w < warp; ++w) sum += s.warp_sum[w];
-    s.pre[tid + 1] = sum;
-  }
-  if (tid == 0) s.pre[0] = 0;
-  __syncthreads();
-  return true;
+  return s.refused == 0;
 }
 
 // Tells the merge which sequence is cut first in this block; run by one thread.
@@ -508,7 +527,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
   using prefill_tc::kSlack;
   using prefill_tc::tma_load_4d;
   constexpr int kD = C::kD, kG = C::kG, kN = C::kN, kHalf = C::kHalf, kTiles = C::kTiles, kBlock = C::kBlock;
-  constexpr int kCluster = C::kCluster;
+  constexpr int kCluster = C::kCluster, kPBufs = C::kPBufs;
   extern __shared__ uint8_t smem_raw[];
   typename C::Smem& s =
       *reinterpret_cast<typename C::Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -528,6 +547,8 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.s_free[i], 8);
+    }
+    for (int i = 0; i < kPBufs; ++i) {
       mbar_init(&s.p_full[i], 8);
       mbar_init(&s.p_empty[i], 1);
     }
@@ -558,8 +579,6 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     if (threadIdx.x == 0 && !p.whole) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp == 8) {
     // ---------------- Q and K producer: lane i < 8 copies page i of a step, chunk by chunk ----------------
-    if (lane == 0 && !p.whole) note_cut<C>(p, s);
-    __syncwarp();
     bool ok = true;
     int gt = 0, gk = 0, st = 0, st_ph = 1;  // segments, K chunks; stage and its phase
     Walk<C> walk;
@@ -689,6 +708,8 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
   } else if (warp == 11) {
     // ---------------- O^T issuer; it also cleans the rows of V that not every node sees ----------------
+    if (lane == 0 && !p.whole) note_cut<C>(p, s);
+    __syncwarp();
     bool ok = true;
     int gt = 0, gs = 0, st = 0, st_ph = 0;
     Walk<C> walk;
@@ -700,7 +721,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       bool poison = false;
       const int all0 = all_from(g.q, p.window);
       for (int pg0 = g.p0; pg0 < g.p1; pg0 += kStepPages) {
-        const int pb = gs & 1;
+        const int pb = gs % kPBufs;
         const int np = prefill_tc::warp_uniform_int(min(kStepPages, g.p1 - pg0));
         const uint32_t p_base = smem_addr(s.p[pb]);
         for (int kk = 0; kk < np; ++kk) {
@@ -714,7 +735,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (kk == 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_full[pb], (gs >> 1) & 1));
+          if (kk == 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_full[pb], (gs / kPBufs) & 1));
           tc_fence_after_sync();
 #pragma unroll
           for (int t = 0; t < kTiles; ++t)
@@ -802,7 +823,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       for (int c = 0; c < kHalf; ++c) l[c] = 0.f;
 
       for (int j = 0; j < g.steps; ++j) {
-        const int sb = gs & 1;
+        const int sb = gs & 1, pb = gs % kPBufs;
         const int step0 = seg0 + j * kKeys;
         const bool masked = step0 < all0 || step0 + kKeys > min(g.q.ctx, seg1);
         unsigned long long vis = 0;
@@ -837,8 +858,10 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
               for (int e = 0; e < 8; ++e)
                 if (!((bits >> (kG >= 8 ? 0 : e / kG)) & 1)) sv[8 * b8 + e] = -INFINITY;
             }
-          } else if (j == 0) {
-            if (key == 0) {  // first references
+          }
+          if (j == 0) {
+            // first references: the scores of a key that every node sees, if there is one
+            if (step0 + key == max(step0, all0) && step0 + key < min(g.q.ctx, seg1)) {
 #pragma unroll
               for (int c = 0; c < kBlock; ++c)
                 if (blk + c < half && sv[c] > -INFINITY && sv[c] < INFINITY) {
@@ -879,7 +902,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
               if (blk + c < half) l[blk + c] *= s.f[cb + c];
             if (j > 0) {
               // O^T holds the products up to step j - 1: wait for the last, then scale in place
-              if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[(gs - 1) & 1], ((gs - 1) >> 1) & 1));
+              if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[(gs - 1) % kPBufs], ((gs - 1) / kPBufs) & 1));
               tc_fence_after_sync();
 #pragma unroll 1
               for (int c = 0; c < kBlock && blk + c < half; c += 8) {
@@ -897,9 +920,9 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
               tmem_wait_st();
             }
           }
-          // weights; the buffer's last reader was the product of step j - 2
-          if (blk == 0 && ok && gs >= 2)
-            ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[sb], ((gs >> 1) - 1) & 1));
+          // weights; the buffer's last reader was the product of step j - kPBufs
+          if (blk == 0 && ok && gs >= kPBufs)
+            ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[pb], (gs / kPBufs - 1) & 1));
 #pragma unroll
           for (int b8 = 0; b8 < kBlock / 8; ++b8) {
             if (blk + 8 * b8 < half) {
@@ -916,7 +939,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
               }
               const int col = cb + 8 * b8;
               st_shared_v4(
-                  smem_addr(s.p[sb]) + (col >> 6) * C::kPChunk + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4),
+                  smem_addr(s.p[pb]) + (col >> 6) * C::kPChunk + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4),
                   make_uint4(pack_bf16x2(w[0].x, w[0].y), pack_bf16x2(w[1].x, w[1].y), pack_bf16x2(w[2].x, w[2].y),
                              pack_bf16x2(w[3].x, w[3].y)));
             }
@@ -925,7 +948,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.p_full[sb]);
+        if (lane == 0) mbar_arrive(&s.p_full[pb]);
         ++gs;
       }
 
@@ -1021,8 +1044,8 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       ++gt;
     }
     // the last products' commits (not all waited for above)
-    for (int k = gs >= 2 ? gs - 2 : 0; k < gs; ++k)
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[k & 1], (k >> 1) & 1));
+    for (int k = gs >= kPBufs ? gs - kPBufs : 0; k < gs; ++k)
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(&s.p_empty[k % kPBufs], (k / kPBufs) & 1));
     if (!ok && lane == 0) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
   }
 
@@ -1053,12 +1076,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // The cut sequences' rows, joined from their partials: o = sum 2^(m_i - M) O_i /
 // sum 2^(m_i - M) l_i.  Every block reads the cuts that the blocks of the first kernel
-// noted; an item is 128 dims of a row, four a lane, a warp's or, where there are fewer
-// items than half the warps, a whole block's, whose warps take the partials in turn and
-// meet in shared memory.  kMergeInFlight partials are in flight a warp.
+// noted.  Many rows: a warp takes one whole, four dims of every 128 a lane.  Few: a block
+// takes 128 dims of one, its warps the partials in turn, and they meet in shared memory.
+// Bound by latency: kMergeInFlight loads of 16 bytes are in flight a lane.
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
-constexpr int kMergeBlocksPerSm = 5;
+constexpr int kMergeBlocksPerSm = 6;
 constexpr int kMergeInFlight = 8;
 
 struct MergeParams {
@@ -1066,6 +1089,91 @@ struct MergeParams {
   int32_t grid;    // blocks of the first kernel
   int32_t stride;  // distance of consecutive blocks of a list: KV heads, times the cluster
 };
+
+template <int kT>
+struct MergeItem {
+  int row0, kv, col;  // first node of the group, KV head, row of the group
+  float m, l;
+  float4 o[kT];
+};
+
+// Partials member, member + team, .. of a row, kT * 128 dims from tile0 * 128 on, four a lane.
+template <typename C, int kT>
+__device__ __forceinline__ MergeItem<kT> merge_partials(const MergeParams& mp, const int32_t* rows, int row, int tile0,
+                                                        int member, int team) {
+  constexpr int kFly = kMergeInFlight / kT;
+  const TreeParams& p = mp.t;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = mp.grid - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (rows[mid] <= row) lo = mid; else hi = mid - 1;
+  }
+  const int4 cut = p.cuts[lo];
+  MergeItem<kT> it;
+  it.row0 = cut.x;
+  it.kv = cut.y >> 8;
+  it.col = row - rows[lo];
+  it.m = -INFINITY;
+  it.l = 0.f;
+#pragma unroll
+  for (int t = 0; t < kT; ++t) it.o[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = member; i0 < cut.w; i0 += team * kFly) {
+    float2 e[kFly];
+    float4 a[kFly][kT];
+#pragma unroll
+    for (int u = 0; u < kFly; ++u) {
+      const int i = i0 + u * team;
+      const size_t at = static_cast<size_t>(i == 0 ? cut.z : 2 * (lo + i * mp.stride)) * C::kN + it.col;
+      e[u] = i < cut.w ? p.part_ml[at] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+        a[u][t] = i < cut.w ? __ldcs(reinterpret_cast<const float4*>(p.part_o + at * C::kD + (tile0 + t) * 128 + 4 * lane))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float m = it.m;
+#pragma unroll
+    for (int u = 0; u < kFly; ++u)
+      if (e[u].y > 0.f) m = fmaxf(m, e[u].x);
+    if (m == -INFINITY) continue;
+    const float f = it.m == -INFINITY ? 0.f : exp2f(it.m - m);
+    it.m = m;
+    it.l *= f;
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      it.o[t].x *= f; it.o[t].y *= f; it.o[t].z *= f; it.o[t].w *= f;
+    }
+#pragma unroll
+    for (int u = 0; u < kFly; ++u) {
+      if (!(e[u].y > 0.f)) continue;
+      const float w = exp2f(e[u].x - m);
+      it.l += w * e[u].y;
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+        it.o[t].x += w * a[u][t].x; it.o[t].y += w * a[u][t].y; it.o[t].z += w * a[u][t].z; it.o[t].w += w * a[u][t].w;
+      }
+    }
+  }
+  return it;
+}
+
+template <typename C, int kT>
+__device__ __forceinline__ void store_merged(const TreeParams& p, const MergeItem<kT>& it, int tile0) {
+  const int lane = threadIdx.x & 31;
+  const float inv = it.l > 0.f ? 1.f / it.l : it.l;
+  const size_t at = (static_cast<size_t>(it.row0 + it.col / C::kG) * C::kHq + it.kv * C::kG + it.col % C::kG) * C::kD +
+                    tile0 * 128 + 4 * lane;
+#pragma unroll
+  for (int t = 0; t < kT; ++t) {
+    const float4 v = make_float4(it.o[t].x * inv, it.o[t].y * inv, it.o[t].z * inv, it.o[t].w * inv);
+    if (p.out_f32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at + t * 128) = v;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at + t * 128) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    }
+  }
+}
 
 template <typename C>
 __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocksPerSm) merge_kernel(const __grid_constant__ MergeParams mp) {
@@ -1105,95 +1213,45 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocksPerSm) merge_ker
     carry += total;
     __syncthreads();
   }
-  const int items = carry * C::kTiles;
-  const int team = items * 2 < static_cast<int>(gridDim.x) * kMergeWarps ? kMergeWarps : 1;
-  const int teams = static_cast<int>(gridDim.x) * kMergeWarps / team;
-  const int member = warp % team;
-  for (int item = (static_cast<int>(blockIdx.x) * kMergeWarps + warp) / team; item < items; item += teams) {
-    const int row = item / C::kTiles, d = item % C::kTiles * 128 + 4 * lane;
-    int lo = 0, hi = mp.grid - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_rows[mid] <= row) lo = mid; else hi = mid - 1;
-    }
-    const int4 cut = p.cuts[lo];
-    const int col = row - s_rows[lo], kv = cut.y >> 8, parts = cut.w;
-    float M = -INFINITY, L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = member; i0 < parts; i0 += team * kMergeInFlight) {
-      float2 e[kMergeInFlight];
-      float4 a[kMergeInFlight];
-#pragma unroll
-      for (int u = 0; u < kMergeInFlight; ++u) {
-        const int i = i0 + u * team;
-        e[u] = make_float2(-INFINITY, 0.f);
-        a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < parts) {
-          const size_t at = static_cast<size_t>(i == 0 ? cut.z : 2 * (lo + i * mp.stride)) * C::kN + col;
-          e[u] = p.part_ml[at];
-          a[u] = __ldcs(reinterpret_cast<const float4*>(p.part_o + at * kD + d));
-        }
-      }
-      float m = M;
-#pragma unroll
-      for (int u = 0; u < kMergeInFlight; ++u)
-        if (e[u].y > 0.f) m = fmaxf(m, e[u].x);
-      if (m == -INFINITY) continue;
-      const float f = M == -INFINITY ? 0.f : exp2f(M - m);
-      L *= f;
-      O.x *= f; O.y *= f; O.z *= f; O.w *= f;
-#pragma unroll
-      for (int u = 0; u < kMergeInFlight; ++u) {
-        if (e[u].y > 0.f) {
-          const float w = exp2f(e[u].x - m);
-          L += w * e[u].y;
-          O.x += w * a[u].x; O.y += w * a[u].y; O.z += w * a[u].z; O.w += w * a[u].w;
-        }
-      }
-      M = m;
-    }
-    if (team > 1) {  // (the same for every warp of the grid)
+  // few rows: an item is 128 dims of a row, a block's; many: a row, a warp's
+  if (carry * C::kTiles * 2 < static_cast<int>(gridDim.x) * kMergeWarps) {
+    for (int item = blockIdx.x; item < carry * C::kTiles; item += gridDim.x) {
+      const MergeItem<1> it = merge_partials<C, 1>(mp, s_rows, item / C::kTiles, item % C::kTiles, warp, kMergeWarps);
       if (lane == 0) {
-        s_m[warp] = M;
-        s_l[warp] = L;
+        s_m[warp] = it.m;
+        s_l[warp] = it.l;
       }
-      s_o[warp][lane] = O;
+      s_o[warp][lane] = it.o[0];
       __syncthreads();
       if (warp == 0) {
-        float m = M;
+        MergeItem<1> all = it;
 #pragma unroll
-        for (int w = 1; w < kMergeWarps; ++w) m = fmaxf(m, s_m[w]);
-        L = 0.f;
-        O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 1; w < kMergeWarps; ++w) all.m = fmaxf(all.m, s_m[w]);
+        all.l = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kMergeWarps; ++w) {
-          const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - m);
+          const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - all.m);
           const float4 v = s_o[w][lane];
-          L += f * s_l[w];
+          all.l += f * s_l[w];
           O.x += f * v.x; O.y += f * v.y; O.z += f * v.z; O.w += f * v.w;
         }
+        all.o[0] = O;
+        store_merged<C, 1>(p, all, item % C::kTiles);
       }
+      __syncthreads();  // the shared partials were read
     }
-    if (member == 0) {
-      const float inv = L > 0.f ? 1.f / L : L;
-      const size_t at = (static_cast<size_t>(cut.x + col / C::kG) * C::kHq + kv * C::kG + col % C::kG) * kD + d;
-      const float4 v = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-      if (p.out_f32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = v;
-      } else {
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at) =
-            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-      }
-    }
-    if (team > 1) __syncthreads();  // the shared partials were read
+  } else {
+    for (int row = blockIdx.x * kMergeWarps + warp; row < carry; row += gridDim.x * kMergeWarps)
+      store_merged<C, C::kTiles>(p, merge_partials<C, C::kTiles>(mp, s_rows, row, 0, 0, 1), 0);
   }
 }
 
 // D = 512: 64 rows, four nodes, alone or in pairs; D = 256: 128 rows, 64 nodes, or fewer with longer rings.
-using GlobalConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 4, 3>;
-using GlobalPairConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 4, 3, 2>;
-using SlidingWideConfig = Config<ATTN_SLIDING_D, ATTN_SLIDING_HQ / ATTN_SLIDING_HKV, ATTN_SLIDING_HKV, 128, 3, 5>;
-using SlidingConfig = Config<ATTN_SLIDING_D, ATTN_SLIDING_HQ / ATTN_SLIDING_HKV, ATTN_SLIDING_HKV, 32, 6, 8>;
+using GlobalConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 1, 4, 4>;
+using GlobalPairConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 1, 4, 4, 2>;
+using SlidingWideConfig = Config<ATTN_SLIDING_D, ATTN_SLIDING_HQ / ATTN_SLIDING_HKV, ATTN_SLIDING_HKV, 128, 2, 3, 5>;
+using SlidingConfig = Config<ATTN_SLIDING_D, ATTN_SLIDING_HQ / ATTN_SLIDING_HKV, ATTN_SLIDING_HKV, 32, 2, 6, 8>;
 
 }  // namespace tree
 }  // namespace pda
