@@ -29,12 +29,16 @@ struct TreePlan {
 
 // Global trees of more than four nodes: two groups of rows share their copies.
 bool paired_tree(int32_t kind, int32_t max_q) {
-  return kind == ATTN_KIND_GLOBAL && max_q > pda::tree::GlobalConfig::kQueries;
+  return kind == ATTN_KIND_GLOBAL && max_q > pda::tree::GlobalConfig::kNodes;
 }
 
-// The sliding configuration for trees of few nodes: 32 rows, longer rings.
-bool narrow_tree(int32_t kind, int32_t max_q) {
-  return kind == ATTN_KIND_SLIDING && max_q <= pda::tree::SlidingConfig::kQueries;
+// Rows of the configuration that holds a whole tree of max_q nodes, or the widest.
+int tree_rows(int32_t kind, int32_t max_q) {
+  namespace tr = pda::tree;
+  if (kind == ATTN_KIND_GLOBAL) return tr::GlobalConfig::kN;
+  return max_q <= tr::SlidingNarrow::kNodes ? tr::SlidingNarrow::kN
+         : max_q <= tr::SlidingMid::kNodes  ? tr::SlidingMid::kN
+                                            : tr::SlidingWide::kN;
 }
 
 int32_t make_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_seq_len, int32_t window,
@@ -51,7 +55,7 @@ int32_t make_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_s
   const bool sliding = kind == ATTN_KIND_SLIDING;
   const int d = sliding ? ATTN_SLIDING_D : ATTN_GLOBAL_D;
   const int hkv = sliding ? ATTN_SLIDING_HKV : ATTN_GLOBAL_HKV;
-  out->rows = !sliding ? tr::GlobalConfig::kN : narrow_tree(kind, max_q) ? tr::SlidingConfig::kN : tr::SlidingWideConfig::kN;
+  out->rows = tree_rows(kind, max_q);
   out->cluster = paired_tree(kind, max_q) ? tr::GlobalPairConfig::kCluster : 1;
   const int nodes = out->rows * hkv / 16 * out->cluster;  // 16 query heads
   out->lists = std::max(1, (max_q + nodes - 1) / nodes);
@@ -197,13 +201,13 @@ int32_t run_tree(int32_t kind, const void* q, const void* k_pool, const void* v_
   p.whole = plan.whole;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   namespace tr = pda::tree;
-  if (!sliding)
-    return paired_tree(kind, max_q)
-               ? launch_tree<tr::GlobalPairConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s)
-               : launch_tree<tr::GlobalConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);
-  return narrow_tree(kind, max_q)
-             ? launch_tree<tr::SlidingConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s)
-             : launch_tree<tr::SlidingWideConfig>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);
+  const auto launch = [&](auto config) {
+    return launch_tree<decltype(config)>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);
+  };
+  if (!sliding) return paired_tree(kind, max_q) ? launch(tr::GlobalPairConfig{}) : launch(tr::GlobalConfig{});
+  return plan.rows == tr::SlidingNarrow::kN ? launch(tr::SlidingNarrow{})
+         : plan.rows == tr::SlidingMid::kN  ? launch(tr::SlidingMid{})
+                                            : launch(tr::SlidingWide{});
 }
 
 // ---------------------------------------------------------------------------

@@ -136,14 +136,15 @@ def test_tree_plan(lib):
     def workspace(grid, rows, D):
         return a256(2 * grid * rows * D * 4) + a256(2 * grid * rows * 8) + a256(grid * 16)
 
-    # long sequences: a block per SM, cut sequences merged by a second kernel
+    # long sequences: a block per SM, cut sequences merged by a second kernel; global trees of more than four nodes take
+    # pairs of blocks, sliding ones as many rows as hold the longest tree
+    assert pda.attn_decode_tree_plan(G, 16, 4, 131072, 0) == (152, 2, workspace(152, 64, 512))
     assert pda.attn_decode_tree_plan(G, 16, 8, 131072, 0) == (152, 2, workspace(152, 64, 512))
-    assert pda.attn_decode_tree_plan(S, 64, 45, 32768, 1024) == (152, 2, workspace(152, 128, 256))
-    # trees of up to 16 nodes on sliding layers: 32 rows
-    assert pda.attn_decode_tree_plan(S, 64, 16, 32768, 1024) == (152, 2, workspace(152, 32, 256))
+    for max_q, rows in ((1, 32), (16, 32), (17, 64), (32, 64), (33, 128), (64, 128)):
+        assert pda.attn_decode_tree_plan(S, 64, max_q, 32768, 1024) == (152, 2, workspace(152, rows, 256))
     # one page each: nothing to merge
     assert pda.attn_decode_tree_plan(G, 200, 4, 16, 0)[1:] == (1, a256(152 * 16))
-    # a few short sequences: a block (global trees of more than four nodes: two) for each group of nodes
+    # a few short sequences: a block (or pair) for each group of nodes
     assert pda.attn_decode_tree_plan(G, 3, 4, 256, 0) == (3, 1, a256(3 * 16))
     assert pda.attn_decode_tree_plan(G, 3, 9, 256, 0) == (12, 1, a256(12 * 16))
     assert pda.attn_decode_tree_plan(S, 2, 9, 240, 1024) == (16, 1, a256(16 * 16))
