@@ -109,13 +109,12 @@ __device__ __forceinline__ Node look_up_node(const ChunkParams& p, const int32_t
     if (lane == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
     return {-1, 0, 0};
   }
-  int parent[2], depth[2];
+  int parent[2];
   tree::read_parents(p.parents + q0, q1 - q0, parent);
   const int pos = L - (q1 - q0) + (t - q0);
   const int32_t phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kPage];
   if (tree::check_parents(q1 - q0, parent) && lane == 0) report(p.status, ATTN_DEV_BAD_TREE);
-  tree::depths(parent, depth);
-  return {pos, L - (q1 - q0) + tree::of_node(depth, t - q0), phys};
+  return {pos, L - (q1 - q0) + tree::depth_of(q1 - q0, parent, t - q0), phys};
 }
 
 // cos and sin of pos * (f.hi + f.lo), a frequency in half turns.  For an integer

@@ -4,9 +4,9 @@
 //
 // A path increases, so path[j] >= j, and every row that is written, at j, lies in
 // front of every row still to be read, at path[j'] > path[j] >= j.  A block takes one
-// sequence in one pool, each thread 16 bytes of the row for all j in order, kInFlight
-// rows read before they are written; no row is read by one thread and written by
-// another.  Bound by memory where paths and batches are long (two passes over a
+// sequence in one layer, each thread 16 bytes of the row of both pools for all j in
+// order, kInFlight rows read before they are written; no row is read by one thread and
+// written by another.  Bound by memory where paths and batches are long (two passes over a
 // row's bytes), by the chain lengths, path, table, row otherwise.
 #pragma once
 
@@ -16,7 +16,7 @@
 namespace pda {
 namespace commit {
 
-constexpr int kInFlight = 8;
+constexpr int kInFlight = 4;  // rows of each pool
 
 struct CommitParams {
   uint8_t* pool[2 * ATTN_MAX_LAYERS];  // k and v of every layer
@@ -81,18 +81,25 @@ __global__ void __launch_bounds__(kRow / 16) commit_kernel(const __grid_constant
   }
   __syncthreads();
   const int count = s_count;
-  uint8_t* const pool = p.pool[blockIdx.y] + 16 * tid;
+  uint8_t* const k = p.pool[2 * blockIdx.y] + 16 * tid;
+  uint8_t* const v = p.pool[2 * blockIdx.y + 1] + 16 * tid;
   for (int j0 = 0; j0 < count; j0 += kInFlight) {
-    uint4 x[kInFlight];
+    uint4 x[kInFlight], y[kInFlight];
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
       const int j = j0 + u;
-      if (j < count && s_src[j] >= 0) x[u] = *reinterpret_cast<const uint4*>(pool + static_cast<int64_t>(s_src[j]) * kRow);
+      if (j < count && s_src[j] >= 0) {
+        x[u] = *reinterpret_cast<const uint4*>(k + static_cast<int64_t>(s_src[j]) * kRow);
+        y[u] = *reinterpret_cast<const uint4*>(v + static_cast<int64_t>(s_src[j]) * kRow);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
       const int j = j0 + u;
-      if (j < count && s_src[j] >= 0) *reinterpret_cast<uint4*>(pool + static_cast<int64_t>(s_dst[j]) * kRow) = x[u];
+      if (j < count && s_src[j] >= 0) {
+        *reinterpret_cast<uint4*>(k + static_cast<int64_t>(s_dst[j]) * kRow) = x[u];
+        *reinterpret_cast<uint4*>(v + static_cast<int64_t>(s_dst[j]) * kRow) = y[u];
+      }
     }
   }
 }

@@ -52,16 +52,39 @@ struct Smem {
   int32_t warp_sum[3][kMaxBatch / 32];
 };
 
-// The i-th of all pages given back (or taken): its request and logical page.
-__device__ __forceinline__ int64_t entry_of(const int32_t* sum, const int3* parts, const PagesParams& p, int i) {
-  int lo = 0, hi = p.batch - 1;  // the request whose part of the running sum holds i (sum[batch] > i)
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sum[mid] <= i) lo = mid; else hi = mid - 1;
+// Moves `total` pages, numbered by the running sum over the requests' parts: move(i, entry) gets the i-th one's place in
+// the block table and returns where to read it and where it goes.  A warp takes kInFlight * 32 consecutive ones at a
+// time, looks the first one's request up and walks on from there, and reads all before it writes any.
+template <typename Move>
+__device__ __forceinline__ void move_pages(const int32_t* sum, const int3* parts, const PagesParams& p, int total, int warp,
+                                           Move move) {
+  constexpr int kRun = kInFlight * 32;
+  const int lane = threadIdx.x & 31;
+  for (int base = warp * kRun; base < total; base += kBlocks * (kThreads / 32) * kRun) {
+    int lo = 0, hi = p.batch - 1;  // the request whose part of the sum holds base (sum[batch] > base)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sum[mid] <= base) lo = mid; else hi = mid - 1;
+    }
+    int32_t page[kInFlight];
+    int32_t* to[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      const int i = base + 32 * u + lane;
+      to[u] = nullptr;
+      if (i < total) {
+        while (sum[lo + 1] <= i) ++lo;
+        const int k = i - sum[lo];
+        const int3 part = parts[lo];
+        const int32_t* from;
+        move(i, static_cast<int64_t>(lo) * p.max_blocks + (k < part.y ? part.x + k : part.z + (k - part.y)), from, to[u]);
+        page[u] = *from;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u)
+      if (to[u] != nullptr) *to[u] = page[u];
   }
-  const int k = i - sum[lo];
-  const int3 part = parts[lo];
-  return static_cast<int64_t>(lo) * p.max_blocks + (k < part.y ? part.x + k : part.z + (k - part.y));
 }
 
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) assign_kernel(const __grid_constant__ PagesParams p) {
@@ -141,31 +164,17 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads) assi
   const uint32_t rank = cluster_ctarank();
 
   if (!refused) {
-    constexpr int kStride = kBlocks * kThreads;
-    const int total = total_give + total_take;
-    for (int i0 = static_cast<int>(rank) * kThreads + tid; i0 < total; i0 += kInFlight * kStride) {
-      int32_t page[kInFlight];
-      int32_t* to[kInFlight];
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const int i = i0 + u * kStride;
-        to[u] = nullptr;
-        if (i < total_take) {
-          const int at = ring.x + i < p.num_pages ? ring.x + i : ring.x + i - p.num_pages;  // i < count <= num_pages
-          to[u] = p.block_table + entry_of(s.take, s.take_part, p, i);
-          page[u] = p.free_list[at];
-        } else if (i < total) {
-          const int g = i - total_take;
-          // head < num_pages, count + g < num_pages: at most once round
-          const int at = ring.x < p.num_pages - (ring.y + g) ? ring.x + ring.y + g : ring.x - (p.num_pages - (ring.y + g));
-          to[u] = p.free_list + at;
-          page[u] = p.block_table[entry_of(s.give, s.give_part, p, g)];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u)
-        if (to[u] != nullptr) *to[u] = page[u];
-    }
+    const int mine = static_cast<int>(rank) * (kThreads / 32) + warp;
+    move_pages(s.take, s.take_part, p, total_take, mine, [&](int i, int64_t entry, const int32_t*& from, int32_t*& to) {
+      from = p.free_list + (ring.x + i < p.num_pages ? ring.x + i : ring.x + i - p.num_pages);  // i < count <= num_pages
+      to = p.block_table + entry;
+    });
+    move_pages(s.give, s.give_part, p, total_give, mine, [&](int i, int64_t entry, const int32_t*& from, int32_t*& to) {
+      // head < num_pages, count + i < num_pages: at most once round
+      const int room = p.num_pages - (ring.y + i);
+      from = p.block_table + entry;
+      to = p.free_list + (ring.x < room ? ring.x + ring.y + i : ring.x - room);
+    });
   }
   // every block has read the old state before any of it is written
   cluster_sync_all();

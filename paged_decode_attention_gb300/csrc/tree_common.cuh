@@ -3,7 +3,7 @@
 // and the merge of cut sequences.
 //
 // Schedule.  Rows come in groups of kQueries nodes; kCluster groups of KV head c of all
-// sequences that have them are a list of pages, with kSegWeight virtual pages in front of
+// sequences that have them are a list of pages, with seg_weight virtual pages in front of
 // every sequence (its Q, its end).  All lists are cut into runs of `per` pages, the fewest
 // that give no more runs than clusters: every cluster has the same work whatever the
 // lengths, and those of neighbouring lists walk the same keys at the same time.  A
@@ -27,7 +27,6 @@ namespace pda {
 namespace tree {
 
 constexpr int kMaxGroups = 16;              // of rows, per KV head; the smallest grid
-constexpr int kSegWeight = 4;               // virtual pages charged per sequence
 constexpr int kMinPer = 4;                  // pages of the smallest run
 constexpr int kSoftmaxThreads = 256;
 constexpr int kThreads = 384;
@@ -54,6 +53,7 @@ struct TreeParams {
   int32_t lists;    // per KV head: ceil(max_q / kNodes)
   int32_t q_box;    // nodes that a copy of Q brings
   int32_t out_f32;
+  int32_t seg_weight;  // virtual pages charged per sequence
   int32_t whole;    // a cluster per (sequence, group, KV head) instead of runs
 };
 
@@ -66,6 +66,7 @@ struct Shared {
   int32_t cu_q[kMaxBatch + 1], len[kMaxBatch];
   int32_t sched[4];            // list, KV head, per, run
   int32_t refused;             // the call as a whole
+  int32_t misfit;              // a sequence's numbers do not fit together
 };
 
 // One sequence as the schedule sees it.
@@ -133,9 +134,9 @@ struct Walk {
   __device__ __forceinline__ bool next(const TreeParams& p, const Shared& s, Segment& g) {
 #pragma unroll 1
     for (; b < p.batch && s.pre[b] < w1; ++b) {
-      const int pages = s.pre[b + 1] - s.pre[b] - kSegWeight;
+      const int pages = s.pre[b + 1] - s.pre[b] - p.seg_weight;
       if (pages <= 0) continue;
-      const int first = s.pre[b] + kSegWeight;
+      const int first = s.pre[b] + p.seg_weight;
       g.p0 = w0 > first ? w0 - first : 0;
       g.p1 = w1 - first < pages ? w1 - first : pages;
       if (g.p1 <= g.p0) continue;
@@ -178,7 +179,7 @@ __device__ __forceinline__ float reduce_columns(float (&v)[kW], Op op) {
 
 // All columns of a softmax thread into its warp's row of `red`.
 template <int kHalf, typename Op>
-__device__ __forceinline__ void reduce_into(const float (&v)[kHalf], float* red, Op op) {
+__device__ __forceinline__ void reduce_into(const float (&v)[kHalf], int n, float* red, Op op) {  // the first n columns
   const int lane = threadIdx.x & 31;
   if constexpr (kHalf == 16) {
     float t[16];
@@ -189,6 +190,7 @@ __device__ __forceinline__ void reduce_into(const float (&v)[kHalf], float* red,
   } else {
 #pragma unroll
     for (int c0 = 0; c0 < kHalf; c0 += 32) {
+      if (c0 >= n) break;
       float t[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) t[i] = v[c0 + i];
@@ -291,23 +293,32 @@ __device__ __forceinline__ uint32_t row_bits(int from, int to) {
 // The masks of a sequence's tree, by all softmax warps: every warp works the tree out and writes its share.
 __device__ __forceinline__ void make_masks(Shared& s, int32_t* status, int n, int parent0, int parent1) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int parent[2] = {parent0, parent1}, depth[2];
-  unsigned long long mask[2];
+  int parent[2] = {parent0, parent1};
+  uint32_t m0, m1 = 0;  // nodes lane and lane + 32: their ancestors among 32 (warp / 4) .. + 31
+  int depth0, depth1 = ATTN_MAX_TREE;
   if (check_parents(n, parent) && threadIdx.x == 0) report(status, ATTN_DEV_BAD_TREE);
-  depths(parent, depth);
-  ancestors(parent, mask);
-  if (warp == 0) {
-    s.depth[lane] = depth[0];
-    s.depth[lane + 32] = depth[1];
+  if (n <= 32) {
+    m0 = ancestors32(parent[0]);
+    depth0 = __popc(m0) - 1;
+    if (warp >= 4) m0 = 0;
+  } else {
+    unsigned long long mask[2];
+    ancestors(parent, mask);
+    depth0 = __popcll(mask[0]) - 1;
+    depth1 = __popcll(mask[1]) - 1;
+    m0 = static_cast<uint32_t>(warp < 4 ? mask[0] : mask[0] >> 32);
+    m1 = static_cast<uint32_t>(warp < 4 ? mask[1] : mask[1] >> 32);
   }
-  const uint32_t m0 = static_cast<uint32_t>(warp < 4 ? mask[0] : mask[0] >> 32);  // ancestors 8 warp .. 8 warp + 7
-  const uint32_t m1 = static_cast<uint32_t>(warp < 4 ? mask[1] : mask[1] >> 32);
+  if (lane >= n) m0 = 0;
+  if (lane + 32 >= n) m1 = 0;
+  if (warp == 0) {
+    s.depth[lane] = depth0;
+    s.depth[lane + 32] = depth1;
+  }
 #pragma unroll 2
   for (int j = 8 * warp; j < 8 * warp + 8; ++j) {
-    const uint32_t b0 = __ballot_sync(0xffffffffu, lane < n && (m0 >> (j & 31) & 1));
-    const uint32_t b1 = __ballot_sync(0xffffffffu, lane + 32 < n && (m1 >> (j & 31) & 1));
-    const uint32_t d0 = __ballot_sync(0xffffffffu, depth[0] <= j);
-    const uint32_t d1 = __ballot_sync(0xffffffffu, depth[1] <= j);
+    const uint32_t b0 = __ballot_sync(0xffffffffu, m0 >> (j & 31) & 1), b1 = __ballot_sync(0xffffffffu, m1 >> (j & 31) & 1);
+    const uint32_t d0 = __ballot_sync(0xffffffffu, depth0 <= j), d1 = __ballot_sync(0xffffffffu, depth1 <= j);
     if (lane == 0) {
       s.below[j] = b0 | static_cast<unsigned long long>(b1) << 32;
       s.shallow[j] = d0 | static_cast<unsigned long long>(d1) << 32;
@@ -315,27 +326,37 @@ __device__ __forceinline__ void make_masks(Shared& s, int32_t* status, int n, in
   }
 }
 
-// The schedule: this block's list, the running sums over it, its run.  Warp 0 works it out, 32 sequences a round, and
-// the block waits for it once.  (Rounds are loops, not unrolled: what runs once a call is bound by fetching its
-// instructions.)  Returns false when the call is refused.
+// The lengths, read into shared memory by warp 0; with `kAgain`, whether any differs from what is there.
+template <bool kAgain>
+__device__ __forceinline__ bool read_lengths(const TreeParams& p, Shared& s) {
+  bool differ = false;
+#pragma unroll 1
+  for (int b0 = 0; b0 <= p.batch; b0 += 32) {
+    const int b = b0 + (threadIdx.x & 31);
+    const int q = b <= p.batch ? __ldcg(p.cu_q + b) : 0, L = b < p.batch ? __ldcg(p.seq_lens + b) : 0;
+    if (kAgain) differ |= (b <= p.batch && s.cu_q[b] != q) || (b < p.batch && s.len[b] != L);
+    if (b <= p.batch) s.cu_q[b] = q;
+    if (b < p.batch) s.len[b] = L;
+  }
+  __syncwarp();
+  return __any_sync(0xffffffffu, differ);
+}
+
+// The schedule: this block's list, the running sums over it, its run; by warp 0, 32 sequences a round.  (Rounds are
+// loops, not unrolled: what runs once a call is bound by fetching its instructions.)  It is made before the block waits
+// for the previous kernel, whose last writes may still change the lengths, and again where they did change; what is
+// reported is reported by the second reading.
 template <typename C>
-__device__ __forceinline__ bool make_schedule(const TreeParams& p, Shared& s) {
+__device__ __noinline__ void make_schedule(const TreeParams& p, Shared& s, bool final) {
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
+  {
     bool refused = false, backwards = false;
     int total = 0;  // lane r: the pages of list r (the same for every KV head)
     // (weight, lists) of sequence b
     const auto weigh = [&](int b, bool& bad) {
       const Sequence q = make_sequence(p, s.cu_q[b], s.cu_q[b + 1], s.len[b], bad);
-      return q.pages > 0 ? make_int2(q.pages + kSegWeight, (q.n + C::kNodes - 1) / C::kNodes) : make_int2(0, 0);
+      return q.pages > 0 ? make_int2(q.pages + p.seg_weight, (q.n + C::kNodes - 1) / C::kNodes) : make_int2(0, 0);
     };
-#pragma unroll 1
-    for (int b0 = 0; b0 <= p.batch; b0 += 32) {
-      const int b = b0 + lane;
-      if (b <= p.batch) s.cu_q[b] = p.cu_q[b];
-      if (b < p.batch) s.len[b] = p.seq_lens[b];
-    }
-    __syncwarp();
 #pragma unroll 1
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + lane;
@@ -354,7 +375,7 @@ __device__ __forceinline__ bool make_schedule(const TreeParams& p, Shared& s) {
     }
     refused = __any_sync(0xffffffffu, refused);
     backwards = __any_sync(0xffffffffu, backwards);  // sequences overlap
-    if (refused && blockIdx.x == 0 && lane == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+    if (refused && final && blockIdx.x == 0 && lane == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
     const int g = static_cast<int>(blockIdx.x / C::kCluster);
     int list, kv, per, run;
     if (p.whole) {
@@ -420,10 +441,10 @@ __device__ __forceinline__ bool make_schedule(const TreeParams& p, Shared& s) {
       s.sched[2] = per;
       s.sched[3] = run;
       s.refused = backwards;
+      s.misfit = refused;
     }
   }
-  __syncthreads();
-  return s.refused == 0;
+  __syncwarp();
 }
 
 // The elements of V that were zeroed, for the rows that see them: a sum with an infinity or NaN among its terms is what
@@ -474,7 +495,7 @@ __device__ __forceinline__ void note_cut(const TreeParams& p, const Shared& s) {
   int4 cut = make_int4(0, 0, 0, 0);
   while (walk.next(p, s, g)) {
     if (g.p0 == 0 && !g.whole) {
-      const int last = (s.pre[g.b] + kSegWeight + g.q.pages - 1) / s.sched[2];  // the run that holds its last page
+      const int last = (s.pre[g.b] + p.seg_weight + g.q.pages - 1) / s.sched[2];  // the run that holds its last page
       cut = make_int4(g.row0, g.nodes | (walk.kv << 8), g.slot, last - s.sched[3] + 1);
     }
   }
@@ -611,6 +632,52 @@ struct MergeParams {
   int32_t stride;  // distance of consecutive blocks of a list: KV heads, times the cluster
 };
 
+// The cut rows of all blocks, numbered: every warp for itself, lane l the blocks l * each .. (l + 1) * each - 1.  No
+// shared memory and no barrier, so that the next call's blocks, which take nearly all of an SM's, can start beside it.
+template <typename C>
+struct CutRows {
+  int each, before, total;  // (before: rows of the lanes below)
+  __device__ __forceinline__ static int of(const TreeParams& p, int g) {
+    const int4 c = p.cuts[g];
+    return c.w > 0 ? (c.y & 255) * C::kG : 0;
+  }
+  __device__ __forceinline__ CutRows(const TreeParams& p, int grid) : each((grid + 31) / 32) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < each; i0 += 5) {  // (152 blocks: one round, all loads in flight)
+      int m[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const int g = lane * each + i0 + i;
+        m[i] = i0 + i < each && g < grid ? of(p, g) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 5; ++i) n += m[i];
+    }
+    before = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += u;
+    }
+    total = __shfl_sync(0xffffffffu, before, 31);
+    before -= n;
+  }
+  // The block whose rows hold `row` < total (the same in every lane), and its first one.
+  __device__ __forceinline__ int find(const TreeParams& p, int row, int& first) const {
+    const int owner = 31 - __clz(__ballot_sync(0xffffffffu, before <= row));
+    first = __shfl_sync(0xffffffffu, before, owner);
+    int g = owner * each;
+#pragma unroll 1
+    for (;; ++g) {
+      const int n = of(p, g);
+      if (row < first + n) return g;
+      first += n;
+    }
+  }
+};
+
 template <int kT>
 struct MergeItem {
   int row0, kv, col;  // first node of the group, KV head, row of the group
@@ -620,21 +687,18 @@ struct MergeItem {
 
 // Partials member, member + team, .. of a row, kT * 128 dims from tile0 * 128 on, four a lane.
 template <typename C, int kT>
-__device__ __forceinline__ MergeItem<kT> merge_partials(const MergeParams& mp, const int32_t* rows, int row, int tile0,
+__device__ __forceinline__ MergeItem<kT> merge_partials(const MergeParams& mp, const CutRows<C>& rows, int row, int tile0,
                                                         int member, int team) {
   constexpr int kFly = kMergeInFlight / kT;
   const TreeParams& p = mp.t;
   const int lane = threadIdx.x & 31;
-  int lo = 0, hi = mp.grid - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (rows[mid] <= row) lo = mid; else hi = mid - 1;
-  }
+  int first;
+  const int lo = rows.find(p, row, first);
   const int4 cut = p.cuts[lo];
   MergeItem<kT> it;
   it.row0 = cut.x;
   it.kv = cut.y >> 8;
-  it.col = row - rows[lo];
+  it.col = row - first;
   it.m = -INFINITY;
   it.l = 0.f;
 #pragma unroll
@@ -699,45 +763,17 @@ __device__ __forceinline__ void store_merged(const TreeParams& p, const MergeIte
 template <typename C>
 __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocksPerSm) merge_kernel(const __grid_constant__ MergeParams mp) {
   const TreeParams& p = mp.t;
-  constexpr int kThreadsHere = kMergeWarps * 32;
-  __shared__ int32_t s_rows[kMaxGrid + 1];
-  __shared__ int32_t s_warp[kMergeWarps];
   __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
   __shared__ float4 s_o[kMergeWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_primary_grid();
   allow_dependent_launch();
-  // running sum of the cut rows
-  int carry = 0;
-  if (threadIdx.x == 0) s_rows[0] = 0;
-  for (int g0 = 0; g0 < mp.grid; g0 += kThreadsHere) {
-    const int g = g0 + threadIdx.x;
-    int n = 0;
-    if (g < mp.grid) {
-      const int4 cut = p.cuts[g];
-      n = cut.w > 0 ? (cut.y & 255) * C::kG : 0;
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, n, o);
-      if (lane >= o) n += u;
-    }
-    if (lane == 31) s_warp[warp] = n;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-      if (w < warp) n += s_warp[w];
-      total += s_warp[w];
-    }
-    if (g < mp.grid) s_rows[g + 1] = carry + n;
-    carry += total;
-    __syncthreads();
-  }
+  const CutRows<C> rows(p, mp.grid);
+  const int carry = rows.total;
   // few rows: an item is 128 dims of a row, a block's; many: a row, a warp's
   if (carry * C::kTiles * 2 < static_cast<int>(gridDim.x) * kMergeWarps) {
     for (int item = blockIdx.x; item < carry * C::kTiles; item += gridDim.x) {
-      const MergeItem<1> it = merge_partials<C, 1>(mp, s_rows, item / C::kTiles, item % C::kTiles, warp, kMergeWarps);
+      const MergeItem<1> it = merge_partials<C, 1>(mp, rows, item / C::kTiles, item % C::kTiles, warp, kMergeWarps);
       if (lane == 0) {
         s_m[warp] = it.m;
         s_l[warp] = it.l;
@@ -764,7 +800,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocksPerSm) merge_ker
     }
   } else {
     for (int row = blockIdx.x * kMergeWarps + warp; row < carry; row += gridDim.x * kMergeWarps)
-      store_merged<C, C::kTiles>(p, merge_partials<C, C::kTiles>(mp, s_rows, row, 0, 0, 1), 0);
+      store_merged<C, C::kTiles>(p, merge_partials<C, C::kTiles>(mp, rows, row, 0, 0, 1), 0);
   }
 }
 

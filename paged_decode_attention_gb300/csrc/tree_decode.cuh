@@ -138,15 +138,24 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     prefetch_tensor_map(&tm_v);
   }
   if (warp == 10) tmem_alloc(&s.tmem_base, C::kTmemCols);
+  if (warp == 0) {
+    read_lengths<false>(p, s.sh);
+    make_schedule<C>(p, s.sh, false);
+  }
+  // q, the cache and the tables may be written by the previous kernel in the stream.
+  wait_for_primary_grid();
+  allow_dependent_launch();
+  if (warp == 0) {
+    if (read_lengths<true>(p, s.sh))
+      make_schedule<C>(p, s.sh, true);
+    else if (s.sh.misfit && blockIdx.x == 0 && lane == 0)
+      report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = s.tmem_base;
-
-  // q, the cache and the tables may be written by the previous kernel in the stream.
-  wait_for_primary_grid();
-  allow_dependent_launch();
-  const bool run = make_schedule<C>(p, s.sh);
+  const bool run = s.sh.refused == 0;
   if constexpr (kCluster > 1) cluster_sync_all();  // the other CTA's barriers are there
   if (!run) {
     if (threadIdx.x == 0 && !p.whole) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -525,7 +534,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       more = walk.next(p, s.sh, ahead);
       if (more) read_parents(p.parents + ahead.q.q0, ahead.q.n, ahead_parent);
       // ---- end of the segment: sums, then this thread's dim of every row ----
-      reduce_into<kHalf>(l, s.red[warp], [](float a, float b) { return a + b; });
+      reduce_into<kHalf>(l, half, s.red[warp], [](float a, float b) { return a + b; });
       named_barrier_sync(bar, 128);
       if (key < half) {
         const int w0 = h * 4, col = c0 + key;

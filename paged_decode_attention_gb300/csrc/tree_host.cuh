@@ -16,12 +16,18 @@ namespace {
 // A call of few, short sequences: every (sequence, group, KV head) in a block of its
 // own, and no merge kernel.
 constexpr int kTreeWholePages = 16;
+// What a sequence's start and end cost a block, in pages: its Q, its masks, the sums, the stores, some 12 us in all.
+// Where few sequences are spread over many blocks they pay it side by side, and a large weight would only leave blocks
+// without pages.  Weights 4, 12, 24 and 48 in us: 64 sliding trees of up to 45 nodes 127, 122, 123, 125; 8 of 26 nodes
+// 26.5, 24.8, 24.5, 27.4; 4 short ones 14.9, 16.6, 17.0, 18.5; 8 ragged global trees 44.4, 42.1, 42.6, 44.0.
+constexpr int kTreeSegWeight = 12, kTreeSegWeightFew = 4;
 
 struct TreePlan {
   int rows;      // of the configuration's groups
   int cluster;   // CTAs
   int lists;     // of pages, per KV head: ceil(max_q / (nodes of a cluster))
   int grid;
+  int seg_weight;
   bool whole;
   bool merge;    // a sequence may be cut: a second kernel
   size_t part_o_bytes, part_ml_bytes, workspace_bytes;
@@ -65,6 +71,7 @@ int32_t make_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_s
                                                                (static_cast<int64_t>(max_seq_len) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE));
   const int64_t items = static_cast<int64_t>(batch) * out->lists * hkv;
   const int64_t clusters = std::max(1, num_sms / out->cluster);
+  out->seg_weight = 4 * items >= clusters ? kTreeSegWeight : kTreeSegWeightFew;
   out->whole = num_splits == 0 && items <= clusters && pages <= kTreeWholePages;
   out->merge = !out->whole && pages > 1;
   if (out->whole) {
@@ -72,7 +79,7 @@ int32_t make_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_s
   } else if (num_splits > 0) {
     out->grid = (num_splits + out->cluster - 1) / out->cluster * out->cluster;
   } else {
-    const int64_t useful = (items * (pages + tr::kSegWeight) + tr::kMinPer - 1) / tr::kMinPer;
+    const int64_t useful = (items * (pages + out->seg_weight) + tr::kMinPer - 1) / tr::kMinPer;
     const int64_t least = tr::kMaxGroups;  // a run for every list
     out->grid = static_cast<int>(std::max<int64_t>(least, std::min<int64_t>({clusters, useful, tr::kMaxGrid / out->cluster}))) *
                 out->cluster;
@@ -198,6 +205,7 @@ int32_t run_tree(int32_t kind, const void* q, const void* k_pool, const void* v_
   p.max_q = max_q;
   p.lists = plan.lists;
   p.out_f32 = out_dtype == ATTN_OUT_F32;
+  p.seg_weight = plan.seg_weight;
   p.whole = plan.whole;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   namespace tr = pda::tree;
@@ -258,7 +266,7 @@ int32_t run_commit(int32_t kind, const void* const* k_pools, const void* const* 
   p.max_path = max_path;
   p.max_blocks = max_blocks;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(batch, 2 * layers);
+  const dim3 grid(batch, layers);
   constexpr int kSlidingRow = ATTN_SLIDING_HKV * ATTN_SLIDING_D * 2, kGlobalRow = ATTN_GLOBAL_HKV * ATTN_GLOBAL_D * 2;
   return launched(name, sliding ? launch_pdl(pda::commit::commit_kernel<kSlidingRow>, grid, kSlidingRow / 16, 0, s, p)
                                 : launch_pdl(pda::commit::commit_kernel<kGlobalRow>, grid, kGlobalRow / 16, 0, s, p));

@@ -45,32 +45,12 @@ __device__ __forceinline__ bool check_parents(int n, int (&parent)[2]) {
   return __any_sync(0xffffffffu, bad);
 }
 
-// Depth of every node.
-__device__ __forceinline__ void depths(const int (&parent)[2], int (&depth)[2]) {
-  int jump[2] = {parent[0], parent[1]};
-  depth[0] = parent[0] >= 0;
-  depth[1] = parent[1] >= 0;
-  while (__any_sync(0xffffffffu, jump[0] >= 0 || jump[1] >= 0)) {
-    int d[2], up[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      d[u] = of_node(depth, jump[u]);
-      up[u] = of_node(jump, jump[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (jump[u] < 0) continue;
-      depth[u] += d[u];
-      jump[u] = up[u];
-    }
-  }
-}
-
-// Ancestors of every node, itself included, as bits.
+// Ancestors of every node, itself included, as bits: one more than its depth.
 __device__ __forceinline__ void ancestors(const int (&parent)[2], unsigned long long (&mask)[2]) {
   int jump[2] = {parent[0], parent[1]};
 #pragma unroll
   for (int u = 0; u < 2; ++u) mask[u] = 1ull << ((threadIdx.x & 31) + 32 * u);
+#pragma unroll 1
   while (__any_sync(0xffffffffu, jump[0] >= 0 || jump[1] >= 0)) {
     unsigned long long m[2];
     int up[2];
@@ -86,6 +66,31 @@ __device__ __forceinline__ void ancestors(const int (&parent)[2], unsigned long 
       jump[u] = up[u];
     }
   }
+}
+
+// The same for at most 32 nodes, one a lane.
+__device__ __forceinline__ uint32_t ancestors32(int parent) {
+  const int lane = threadIdx.x & 31;
+  uint32_t mask = 1u << lane;
+  int jump = parent;
+#pragma unroll 1
+  while (__any_sync(0xffffffffu, jump >= 0)) {
+    const uint32_t m = __shfl_sync(0xffffffffu, mask, jump & 31);
+    const int up = __shfl_sync(0xffffffffu, jump, jump & 31);
+    if (jump >= 0) {
+      mask |= m;
+      jump = up;
+    }
+  }
+  return mask;
+}
+
+// Depth of node i of n.
+__device__ __forceinline__ int depth_of(int n, const int (&parent)[2], int i) {
+  if (n <= 32) return __popc(__shfl_sync(0xffffffffu, ancestors32(parent[0]), i)) - 1;
+  unsigned long long mask[2];
+  ancestors(parent, mask);
+  return __popcll(of_node(mask, i)) - 1;
 }
 
 }  // namespace tree
