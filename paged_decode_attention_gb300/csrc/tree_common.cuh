@@ -33,6 +33,7 @@ constexpr int kThreads = 384;
 constexpr int kMaxGrid = kMaxSplits;
 
 struct TreeParams {
+  const __nv_bfloat16* k_pool;  // (for prefetches; read through the tensor maps)
   const __nv_bfloat16* v_pool;
   const int32_t* block_table;
   const int32_t* seq_lens;
@@ -546,6 +547,16 @@ __device__ __forceinline__ void load_page(void* dst, const CUtensorMap* map, int
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_addr(bar)),
         "h"(static_cast<uint16_t>((1 << kCluster) - 1))
         : "memory");
+  }
+}
+
+// Brings one KV head of a page into L2.
+template <typename C>
+__device__ __forceinline__ void prefetch_page(const __nv_bfloat16* pool, const CUtensorMap* map, int kv, int id, int boxes) {
+  if constexpr (C::kHkv == 1) {
+    bulk_prefetch_l2(pool + static_cast<size_t>(id) * (kPage * C::kD), kPage * C::kD * 2);
+  } else {
+    for (int i = 0; i < boxes; ++i) tma_prefetch_3d(map, 0, id * kPage, kv * C::kChunks + i);
   }
 }
 

@@ -91,6 +91,12 @@ struct Config {
   static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM within the 227 KB a CTA may have");
 };
 
+// Pairs that walk at least this many pages of a sequence have them brought into L2 a step ahead of the copies: a stage
+// is refilled only once both CTAs have used it, and the 128 KB in flight do not cover DRAM's latency then.  us a call,
+// without and with: 16 x 131072 positions, 8 nodes 713 and 692 (with V 24 pages ahead instead of 12 842), 32 trees of 64
+// nodes 522 and 514; 8 short ragged ones 41.2 and 42.4.  Alone, a CTA is slower with it: 64 x 4 nodes 64 and 78.
+constexpr int kPrefetchPages = 64;
+
 template <typename C>
 __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                           const TreeParams& p) {
@@ -176,12 +182,16 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       ++gt;
       const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks + g.q.page0;
       const auto entry = [&](int pg) { return lane < kStepPages && pg + lane < g.p1 ? table[pg + lane] : 0; };
+      const bool ahead = kCluster > 1 && g.p1 - g.p0 >= kPrefetchPages;
       int next_id = entry(g.p0);
 #pragma unroll 1
       for (int pg = g.p0; pg < g.p1 && ok; pg += kStepPages) {
         const int id = next_id;
         next_id = entry(pg + kStepPages);
         const int np = min(kStepPages, g.p1 - pg);
+        if (ahead && lane < kStepPages && pg + kStepPages + lane < g.p1 && lane % kCluster == rank && next_id >= 0 &&
+            static_cast<int64_t>(next_id) < p.num_pages)
+          prefetch_page<C>(p.k_pool, &tm_k, walk.kv, next_id, C::kChunks);
         int32_t y = id * kPage;
         if (lane < np && (id < 0 || static_cast<int64_t>(id) >= p.num_pages)) {
           report(p.status, ATTN_DEV_BAD_PAGE);
@@ -216,6 +226,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     }
   } else if (warp == 9) {
     // ---------------- V producer: a page per stage ----------------
+    constexpr int kAhead = 12;  // pages that a prefetch runs ahead
     bool ok = true;
     int gv = 0, st = 0, st_ph = 1;
     Walk<C> walk;
@@ -225,6 +236,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     while (ok && walk.next(p, s.sh, g)) {
       const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks + g.q.page0;
       const auto entry = [&](int pg) { return pg < g.p1 ? table[pg] : 0; };
+      const bool ahead = kCluster > 1 && g.p1 - g.p0 >= kPrefetchPages;
       int cur = 0, nxt = entry(g.p0 + lane);
 #pragma unroll 1
       for (int pg = g.p0; pg < g.p1 && ok; ++pg) {
@@ -234,6 +246,9 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
           nxt = entry(pg + 32 + lane);
         }
         const int id = __shfl_sync(0xffffffffu, cur, u);
+        const int far = __shfl_sync(0xffffffffu, u + kAhead < 32 ? cur : nxt, (u + kAhead) & 31);
+        if (ahead && lane == 0 && pg + kAhead < g.p1 && u % kCluster == rank && far >= 0 && static_cast<int64_t>(far) < p.num_pages)
+          prefetch_page<C>(p.v_pool, &tm_v, walk.kv, far, 1);
         if (gv >= C::kVStages) ok = __all_sync(0xffffffffu, wait_for<(kCluster > 1)>(&s.v_empty[st], st_ph));
         if (!ok) break;
         if (lane == 0) {

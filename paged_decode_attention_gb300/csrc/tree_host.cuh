@@ -187,6 +187,7 @@ int32_t run_tree(int32_t kind, const void* q, const void* k_pool, const void* v_
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   pda::tree::TreeParams p{};
+  p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
   p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
   p.block_table = block_table;
   p.seq_lens = seq_lens;
