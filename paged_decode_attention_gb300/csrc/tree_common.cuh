@@ -58,11 +58,15 @@ struct TreeParams {
   int32_t whole;    // a cluster per (sequence, group, KV head) instead of runs
 };
 
-// What the schedule and the masks leave in shared memory.
-struct Shared {
+// A sequence's tree in shared memory.
+struct Masks {
   alignas(8) unsigned long long below[ATTN_MAX_TREE];    // nodes that see node j by ancestry
   alignas(8) unsigned long long shallow[ATTN_MAX_TREE];  // nodes of depth <= x
   int32_t depth[ATTN_MAX_TREE];
+};
+
+// What the schedule leaves in shared memory.
+struct Shared {
   int32_t pre[kMaxBatch + 1];  // pages (virtual ones included) before sequence b in this cluster's list
   int32_t cu_q[kMaxBatch + 1], len[kMaxBatch];
   int32_t sched[4];            // list, KV head, per, run
@@ -229,7 +233,7 @@ __device__ __forceinline__ bool barrier_or(uint32_t id, uint32_t threads, bool v
 }
 
 // The nodes (bits) that see position pos.  (The masks are there where a segment holds positions that not all nodes see.)
-__device__ __forceinline__ unsigned long long seen_by(const Sequence& q, int window, const Shared& s, int pos) {
+__device__ __forceinline__ unsigned long long seen_by(const Sequence& q, int window, const Masks& s, int pos) {
   if (pos >= all_from(q, window) && pos < q.ctx) return ~0ull;
   if (pos < q.lo || pos >= q.L) return 0;
   if (pos < q.ctx) return s.shallow[min(pos - (q.ctx - window + 1), ATTN_MAX_TREE - 1)];
@@ -292,7 +296,7 @@ __device__ __forceinline__ uint32_t row_bits(int from, int to) {
 }
 
 // The masks of a sequence's tree, by all softmax warps: every warp works the tree out and writes its share.
-__device__ __forceinline__ void make_masks(Shared& s, int32_t* status, int n, int parent0, int parent1) {
+__device__ __forceinline__ void make_masks(Masks& s, int32_t* status, int n, int parent0, int parent1) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int parent[2] = {parent0, parent1};
   uint32_t m0, m1 = 0;  // nodes lane and lane + 32: their ancestors among 32 (warp / 4) .. + 31
@@ -452,7 +456,7 @@ __device__ __noinline__ void make_schedule(const TreeParams& p, Shared& s, bool 
 // those alone add up to, whatever their weights.  By a softmax thread, for dims d0 + its index + 128 i < d1 of columns
 // [from, to), after it (or its warp) stored them.
 template <typename C>
-__device__ __noinline__ void add_back(const TreeParams& p, const Shared& s, const Segment& g, int kv, int node0, int from,
+__device__ __noinline__ void add_back(const TreeParams& p, const Masks& s, const Segment& g, int kv, int node0, int from,
                                       int to, int d0, int d1) {
   const int all0 = all_from(g.q, p.window);
   const int pos0 = max(g.q.lo, (g.q.page0 + g.p0) * kPage), pos1 = min(g.q.L, (g.q.page0 + g.p1) * kPage);

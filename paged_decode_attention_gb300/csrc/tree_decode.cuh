@@ -77,6 +77,7 @@ struct Config {
     alignas(16) float f[kN];          // first scores; factor of a moved reference; 1 / sum at the end
     alignas(16) float red[8][kN / 2]; // per softmax warp and column: max, sum
     Shared sh;
+    Masks masks[2];                   // of the segment at hand, and of the next
     int32_t poison;                   // this segment: an element was zeroed that some row sees
     alignas(8) uint64_t k_full[kKStages], k_empty[kKStages];
     alignas(8) uint64_t v_full[kVStages], v_empty[kVStages];
@@ -375,6 +376,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
   } else {
     // ---------------- softmax and epilogue: thread = key of the step, then dim of a tile ----------------
     const int h = warp >> 2;             // half of the columns
+    const int hb = h * kHalf;            // their first place in neg_m, bound and f, whatever the segment
     const int key = threadIdx.x & 127;   // tensor-memory lane, thread of the warpgroup
     const uint32_t bar = 2 + h;
     const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -384,26 +386,37 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     Walk<C> walk;
     walk.start(p, s.sh);
     Segment g, ahead;
-    int parent[2], ahead_parent[2] = {-1, -1};  // the next segment and its parents are read before this one's end
+    int parent[2];  // of the next segment, which is read and whose masks are made before this one's end
+    // (the masks are there where a segment holds positions that not all nodes see)
+    const auto prepare_masks = [&](int buf) {
+      if ((ahead.q.page0 + ahead.p0) * kPage < all_from(ahead.q, p.window) ||
+          (ahead.q.page0 + ahead.p1) * kPage > ahead.q.ctx)
+        make_masks(s.masks[buf], p.status, ahead.q.n, parent[0], parent[1]);
+    };
+    // the references of this warpgroup's columns, by the threads that have one each
+    const auto reset_references = [&] {
+      const int half = ahead.N >> 1;
+      if (key < half) {
+        s.neg_m[hb + key] = 0.f;
+        s.bound[hb + key] = -INFINITY;
+      }
+    };
     bool more = walk.next(p, s.sh, ahead);
-    if (more) read_parents(p.parents + ahead.q.q0, ahead.q.n, ahead_parent);
+    if (more) {
+      read_parents(p.parents + ahead.q.q0, ahead.q.n, parent);
+      prepare_masks(0);
+      reset_references();
+    }
 #pragma unroll 1
     while (more) {
       g = ahead;
-      parent[0] = ahead_parent[0];
-      parent[1] = ahead_parent[1];
       const int half = g.N >> 1;
       const int c0 = h * half;  // this warpgroup's first column
       const int all0 = all_from(g.q, p.window);
       const int node0 = walk.group * C::kQueries;
       const int seg0 = (g.q.page0 + g.p0) * kPage, seg1 = (g.q.page0 + g.p1) * kPage;
-      named_barrier_sync(1, kSoftmaxThreads);  // all are done with the last segment's shared state
-      if (seg0 < all0 || seg1 > g.q.ctx) make_masks(s.sh, p.status, g.q.n, parent[0], parent[1]);
-      if (key < half) {
-        s.neg_m[c0 + key] = 0.f;
-        s.bound[c0 + key] = -INFINITY;
-      }
-      named_barrier_sync(1, kSoftmaxThreads);
+      const Masks& masks = s.masks[gt & 1];
+      named_barrier_sync(1, kSoftmaxThreads);  // the masks and references are there
       float l[kHalf];
 #pragma unroll
       for (int c = 0; c < kHalf; ++c) l[c] = 0.f;
@@ -414,7 +427,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
         const int step0 = seg0 + j * kKeys;
         const bool masked = step0 < all0 || step0 + kKeys > min(g.q.ctx, seg1);
         unsigned long long vis = 0;
-        if (masked && step0 + key < seg1) vis = seen_by(g.q, p.window, s.sh, step0 + key) >> node0;
+        if (masked && step0 + key < seg1) vis = seen_by(g.q, p.window, masks, step0 + key) >> node0;
         if (ok) ok = __all_sync(0xffffffffu, wait_for(&s.s_full[sb], (gs >> 1) & 1));
         tc_fence_after_sync();
 #pragma unroll
@@ -452,16 +465,16 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
 #pragma unroll
               for (int c4 = 0; c4 < kBlock / 4; ++c4)
                 if (blk + 4 * c4 < half)
-                  *reinterpret_cast<float4*>(&s.f[cb + 4 * c4]) =
+                  *reinterpret_cast<float4*>(&s.f[hb + blk + 4 * c4]) =
                       make_float4(sv[4 * c4], sv[4 * c4 + 1], sv[4 * c4 + 2], sv[4 * c4 + 3]);
             }
             named_barrier_sync(bar, 128);
             if (key < kBlock && blk + key < half) {
-              const float x = s.f[cb + key];
+              const float x = s.f[hb + blk + key];
               if (fabsf(x) < INFINITY) {
                 const float m = fmaf(x, kLog2e, kHeadroom);
-                s.neg_m[cb + key] = -m;
-                s.bound[cb + key] = (m + kSlack) * (1.f / kLog2e);
+                s.neg_m[hb + blk + key] = -m;
+                s.bound[hb + blk + key] = (m + kSlack) * (1.f / kLog2e);
               }
             }
             named_barrier_sync(bar, 128);
@@ -470,7 +483,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
 #pragma unroll
           for (int c4 = 0; c4 < kBlock / 4; ++c4) {
             if (blk + 4 * c4 < half) {
-              const float4 t = *reinterpret_cast<const float4*>(&s.bound[cb + 4 * c4]);
+              const float4 t = *reinterpret_cast<const float4*>(&s.bound[hb + blk + 4 * c4]);
               moves |= (sv[4 * c4] > t.x) | (sv[4 * c4 + 1] > t.y) | (sv[4 * c4 + 2] > t.z) | (sv[4 * c4 + 3] > t.w);
             }
           }
@@ -479,7 +492,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
             max_into<kBlock>(sv, red);
             named_barrier_sync(bar, 128);
             if (key < kBlock && blk + key < half) {
-              const int w0 = h * 4, c = blk + key, col = c0 + c;
+              const int w0 = h * 4, c = blk + key, col = hb + c;
               const float mx = fmaxf(fmaxf(s.red[w0][c], s.red[w0 + 1][c]), fmaxf(s.red[w0 + 2][c], s.red[w0 + 3][c]));
               float f = 1.f;
               if (mx > s.bound[col]) {
@@ -493,7 +506,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
             named_barrier_sync(bar, 128);
 #pragma unroll
             for (int c = 0; c < kBlock; ++c)
-              if (blk + c < half) l[blk + c] *= s.f[cb + c];
+              if (blk + c < half) l[blk + c] *= s.f[hb + blk + c];
             if (j > 0) {
               // O^T holds the products up to step j - 1: wait for the last, then scale in place
               if (ok) ok = __all_sync(0xffffffffu, wait_for(&s.p_empty[(gs - 1) % kPBufs], ((gs - 1) / kPBufs) & 1));
@@ -507,7 +520,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
                   tmem_ld8(t_row + t * kN + cb + c, ov);
                   tmem_wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(ov[e] * s.f[cb + c + e]);
+                  for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(ov[e] * s.f[hb + blk + c + e]);
                   tmem_st8(t_row + t * kN + cb + c, w);
                 }
               }
@@ -523,7 +536,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
               float2 w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float2 m = *reinterpret_cast<const float2*>(&s.neg_m[cb + 8 * b8 + 2 * e]);
+                const float2 m = *reinterpret_cast<const float2*>(&s.neg_m[hb + blk + 8 * b8 + 2 * e]);
                 const float2 x = __ffma2_rn(make_float2(sv[8 * b8 + 2 * e], sv[8 * b8 + 2 * e + 1]), log2e2, m);
                 w[e] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                 const int c = blk + 8 * b8 + 2 * e;
@@ -547,28 +560,30 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       }
 
       more = walk.next(p, s.sh, ahead);
-      if (more) read_parents(p.parents + ahead.q.q0, ahead.q.n, ahead_parent);
+      if (more) read_parents(p.parents + ahead.q.q0, ahead.q.n, parent);
       // ---- end of the segment: sums, then this thread's dim of every row ----
       reduce_into<kHalf>(l, half, s.red[warp], [](float a, float b) { return a + b; });
       named_barrier_sync(bar, 128);
       if (key < half) {
         const int w0 = h * 4, col = c0 + key;
         const float sum = (s.red[w0][key] + s.red[w0 + 1][key]) + (s.red[w0 + 2][key] + s.red[w0 + 3][key]);
-        s.f[col] = !g.whole ? 1.f : sum > 0.f ? 1.f / sum : sum;  // 0: a row that sees nothing; NaN stays
+        s.f[hb + key] = !g.whole ? 1.f : sum > 0.f ? 1.f / sum : sum;  // 0: a row that sees nothing; NaN stays
         if (!g.whole && col < g.cols)
-          p.part_ml[static_cast<size_t>(g.slot) * kN + col] = partial_stats(-s.neg_m[col], sum);
+          p.part_ml[static_cast<size_t>(g.slot) * kN + col] = partial_stats(-s.neg_m[hb + key], sum);
       }
       named_barrier_sync(bar, 128);
+      if (more) prepare_masks((gt + 1) & 1);  // (while the last products run)
       if (ok) ok = __all_sync(0xffffffffu, wait_for(&s.o_full, gt & 1));
       tc_fence_after_sync();
       const int to = min(c0 + half, g.cols);
-      store_columns<C, kTiles, kN>(p, g, walk.kv, c0, to, t_row, s.f, 0);
+      store_columns<C, kTiles, kN>(p, g, walk.kv, c0, to, t_row, s.f + hb - c0, 0);
       if (s.poison != 0) {
         __syncwarp();  // (a lane's elements were stored by its neighbour)
-        add_back<C>(p, s.sh, g, walk.kv, node0, c0, to, 0, kD);
+        add_back<C>(p, masks, g, walk.kv, node0, c0, to, 0, kD);
       }
       tc_fence_before_sync();
       __syncwarp();
+      if (more) reset_references();  // (read by no other thread since the sums)
       if (lane == 0) mbar_arrive(&s.o_free);  // the next segment's first product may overwrite O^T
       ++gt;
     }
