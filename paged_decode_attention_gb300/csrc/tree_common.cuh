@@ -652,24 +652,26 @@ struct MergeParams {
 template <typename C>
 struct CutRows {
   int each, before, total;  // (before: rows of the lanes below)
-  __device__ __forceinline__ static int of(const TreeParams& p, int g) {
-    const int4 c = p.cuts[g];
-    return c.w > 0 ? (c.y & 255) * C::kG : 0;
-  }
+  int most;                 // partials of a row
+  __device__ __forceinline__ static int of(const int4& c) { return c.w > 0 ? (c.y & 255) * C::kG : 0; }
   __device__ __forceinline__ CutRows(const TreeParams& p, int grid) : each((grid + 31) / 32) {
     const int lane = threadIdx.x & 31;
-    int n = 0;
+    int n = 0, w = 0;
 #pragma unroll 1
     for (int i0 = 0; i0 < each; i0 += 5) {  // (152 blocks: one round, all loads in flight)
-      int m[5];
+      int4 c[5];
 #pragma unroll
       for (int i = 0; i < 5; ++i) {
         const int g = lane * each + i0 + i;
-        m[i] = i0 + i < each && g < grid ? of(p, g) : 0;
+        c[i] = i0 + i < each && g < grid ? p.cuts[g] : make_int4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int i = 0; i < 5; ++i) n += m[i];
+      for (int i = 0; i < 5; ++i) {
+        n += of(c[i]);
+        w = max(w, c[i].w);
+      }
     }
+    most = __reduce_max_sync(0xffffffffu, w);
     before = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -686,7 +688,7 @@ struct CutRows {
     int g = owner * each;
 #pragma unroll 1
     for (;; ++g) {
-      const int n = of(p, g);
+      const int n = of(p.cuts[g]);
       if (row < first + n) return g;
       first += n;
     }
@@ -785,8 +787,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocksPerSm) merge_ker
   allow_dependent_launch();
   const CutRows<C> rows(p, mp.grid);
   const int carry = rows.total;
-  // few rows: an item is 128 dims of a row, a block's; many: a row, a warp's
-  if (carry * C::kTiles * 2 < static_cast<int>(gridDim.x) * kMergeWarps) {
+  // An item is 128 dims of a row, a block's, or a row, a warp's: whichever waits less, in units of a load's latency.  A
+  // block's first takes some six and a load for every 32 partials (they meet in shared memory), a warp's one and a bit
+  // more for every kMergeInFlight / kTiles.  us a call, by blocks and by warps: 4 short sliding trees (8 partials a row)
+  // 15.2 and 13.6, a global tree of 4 nodes (15) 13.9 and 15.5, of 8 behind 30000 positions (76) 30 and 69, four of these
+  // (19, three items a block) 67 and 72, 8 of 4 nodes (13, three) 20.1 and 19.1, 32 of 64 nodes 554 and 512.
+  constexpr int kFly = kMergeInFlight / C::kTiles;
+  const float blocks = static_cast<float>(gridDim.x), most = static_cast<float>(rows.most);
+  const float by_block = 4.f + ceilf(__fdividef(carry * C::kTiles, blocks)) * (2.f + most * (1.f / (8 * kMergeWarps)));
+  const float by_warp = ceilf(__fdividef(carry, kMergeWarps * blocks)) * (1.f + 1.2f * ceilf(most * (1.f / kFly)));
+  if (by_block < by_warp) {
     for (int item = blockIdx.x; item < carry * C::kTiles; item += gridDim.x) {
       const MergeItem<1> it = merge_partials<C, 1>(mp, rows, item / C::kTiles, item % C::kTiles, warp, kMergeWarps);
       if (lane == 0) {

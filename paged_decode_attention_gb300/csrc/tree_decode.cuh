@@ -385,8 +385,8 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     int gt = 0, gs = 0;
     Walk<C> walk;
     walk.start(p, s.sh);
-    Segment g, ahead;
-    int parent[2];  // of the next segment, which is read and whose masks are made before this one's end
+    Segment g, ahead{};
+    int parent[2] = {-1, -1};  // of the next segment, which is read and whose masks are made before this one's end
     // (the masks are there where a segment holds positions that not all nodes see)
     const auto prepare_masks = [&](int buf) {
       if ((ahead.q.page0 + ahead.p0) * kPage < all_from(ahead.q, p.window) ||

@@ -13,9 +13,13 @@ namespace {
 // ---------------------------------------------------------------------------
 // Attention of trees
 // ---------------------------------------------------------------------------
-// A call of few, short sequences: every (sequence, group, KV head) in a block of its
-// own, and no merge kernel.
-constexpr int kTreeWholePages = 16;
+// Every (sequence, group, KV head) in a block of its own, and no merge kernel, where there are blocks enough and cutting
+// gains less than it costs: the longest takes its pages' time, and cut up the share of r = items / blocks of the pages of
+// all (half of the longest's, on average), but as well the merge (kTreeWholePages' time) and r further starts and ends a
+// block (kTreeWholeStarts).  us a call, whole and cut: global trees of 4 nodes, 8 behind 200 positions 13.4 and 14.9,
+// behind 380 18.0 and 14.8, 60 behind 380 18.9 and 24.8; sliding ones of 8, 4 behind 300 11.9 and 14.0, behind 600 15.6 and
+// 15.9, 16 behind 600 17.9 and 22.8.
+constexpr int kTreeWholePages = 16, kTreeWholeStarts = 32;
 // What a sequence's start and end cost a block, in pages: its Q, its masks, the sums, the stores, some 12 us in all.
 // Where few sequences are spread over many blocks they pay it side by side, and a large weight would only leave blocks
 // without pages.  Weights 4, 12, 24 and 48 in us: 64 sliding trees of up to 45 nodes 127, 122, 123, 125; 8 of 26 nodes
@@ -29,7 +33,7 @@ struct TreePlan {
   int grid;
   int seg_weight;
   bool whole;
-  bool merge;    // a sequence may be cut: a second kernel
+  bool merge;    // a sequence may be cut (however low the caller's bound on the lengths): a second kernel
   size_t part_o_bytes, part_ml_bytes, workspace_bytes;
 };
 
@@ -72,8 +76,9 @@ int32_t make_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_s
   const int64_t items = static_cast<int64_t>(batch) * out->lists * hkv;
   const int64_t clusters = std::max(1, num_sms / out->cluster);
   out->seg_weight = 4 * items >= clusters ? kTreeSegWeight : kTreeSegWeightFew;
-  out->whole = num_splits == 0 && items <= clusters && pages <= kTreeWholePages;
-  out->merge = !out->whole && pages > 1;
+  out->whole = num_splits == 0 && items <= clusters &&
+               pages * (2 * clusters - items) <= 2 * (kTreeWholePages * clusters + kTreeWholeStarts * items);
+  out->merge = !out->whole;
   if (out->whole) {
     out->grid = static_cast<int>(items) * out->cluster;
   } else if (num_splits > 0) {
@@ -251,6 +256,11 @@ int32_t run_commit(int32_t kind, const void* const* k_pools, const void* const* 
     p.pool[2 * i] = static_cast<uint8_t*>(const_cast<void*>(k_pools[i]));
     p.pool[2 * i + 1] = static_cast<uint8_t*>(const_cast<void*>(v_pools[i]));
   }
+  // the blocks of other layers read the lengths and paths while those of the first write new_lens
+  const auto apart = [&](const int32_t* in, int64_t count) { return new_lens + batch <= in || in + count <= new_lens; };
+  if (!apart(seq_lens, batch) || !apart(cu_q, batch + 1) || !apart(path, static_cast<int64_t>(batch) * max_path) ||
+      !apart(path_len, batch) || !apart(block_table, static_cast<int64_t>(batch) * max_blocks))
+    return fail(ATTN_ERR_INVALID_ARG, "%s: new_lens overlaps an input", name);
   for (int i = 0; i < 2 * layers; ++i)  // a row moved twice would be moved wrongly
     for (int j = 0; j < i; ++j)
       if (p.pool[i] == p.pool[j]) return fail(ATTN_ERR_INVALID_ARG, "%s: a pool is given twice", name);

@@ -107,6 +107,26 @@ def test_bad_arguments_are_refused_before_launch(lib, name, form, bad, code):
         lib.attn_step_destroy(h)
 
 
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_a_commit_writes_none_of_its_inputs(lib, kind):
+    name = "attn_kv_commit_" + kind
+    sizes = dict(table=4 * 70 * 4, lens=4 * 4, cu_q=4 * 5, path=4 * 8 * 4, path_len=4 * 4)
+    apart = {a: (20 + i) * FAKE for i, a in enumerate(sizes)}
+    h = ctypes.c_void_p()
+    assert lib.attn_step_create(ctypes.byref(h)) == 0
+    try:
+        for a, n in sizes.items():
+            for at in (apart[a], apart[a] - 12, apart[a] + n - 4):
+                assert call(lib, name, "commit", step=h, new_lens=at, **apart) == INVALID
+                assert "overlaps" in pda.attn_last_error()
+        assert lib.attn_step_num_calls(h) == 0
+        for a, n in sizes.items():
+            for at in (apart[a] - 16, apart[a] + n):
+                assert call(lib, name, "commit", step=h, new_lens=at, **apart) == 0
+    finally:
+        lib.attn_step_destroy(h)
+
+
 def test_headers_compile_as_c(tmp_path):
     src = tmp_path / "use.c"
     src.write_text('#include "attn_tree.h"\n#include "attn_step.h"\nint main(void){return ATTN_MAX_TREE - 64;}\n')
@@ -142,8 +162,9 @@ def test_tree_plan(lib):
     assert pda.attn_decode_tree_plan(G, 16, 8, 131072, 0) == (152, 2, workspace(152, 64, 512))
     for max_q, rows in ((1, 32), (16, 32), (17, 64), (32, 64), (33, 128), (64, 128)):
         assert pda.attn_decode_tree_plan(S, 64, max_q, 32768, 1024) == (152, 2, workspace(152, rows, 256))
-    # one page each: nothing to merge
-    assert pda.attn_decode_tree_plan(G, 200, 4, 16, 0)[1:] == (1, a256(152 * 16))
+    # one page each, by the caller's bound: the lengths may be longer, and then sequences are cut
+    for max_seq_len in (0, 1, 16):
+        assert pda.attn_decode_tree_plan(G, 200, 4, max_seq_len, 0) == (152, 2, workspace(152, 64, 512))
     # a few short sequences: a block (or pair) for each group of nodes
     assert pda.attn_decode_tree_plan(G, 3, 4, 256, 0) == (3, 1, a256(3 * 16))
     assert pda.attn_decode_tree_plan(G, 3, 9, 256, 0) == (12, 1, a256(12 * 16))

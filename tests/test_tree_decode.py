@@ -256,3 +256,13 @@ def test_bounds_only_size_the_launch(cuda_lib, kind):
     bound = decode_bound(want.double().cpu(), A, S, c.D, torch.float32, WEIGHT)
     assert ((got - want).double().cpu().abs() <= 2 * bound).all()
     assert PAGE_SIZE == 16
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("max_seq_len", [0, 1, 16, 200])
+def test_many_sequences_longer_than_the_bound(cuda_lib, kind, max_seq_len):
+    """More sequences than blocks, of more pages than the bound has: cut as any others."""
+    r = rng(max_seq_len)
+    n = 40 if kind == "sliding" else 200
+    trees = [random_tree(r.choice([1, 2, 3, 4]), r) for _ in range(n)]
+    check(TreeCase(kind, [r.randint(0, 600) for _ in range(n)], trees, seed=max_seq_len), max_seq_len=max_seq_len)
