@@ -93,7 +93,8 @@ struct Smem {
 };
 
 // Node t, by one warp.  A chain of lookups (sequence, parents, page) and the tree's depth, some 2000 cycles: in front of
-// every token's angles they cost 2032 sliding nodes 16.7 us, looked up ahead 13.4.
+// every token's angles they cost 2032 sliding nodes 16.7 us, looked up ahead 13.4 (inputs in L2; 15.0 from HBM, where
+// their bytes take 9.8).
 __device__ __forceinline__ Node look_up_node(const ChunkParams& p, const int32_t* cu_q, const int32_t* len, int t) {
   const int lane = threadIdx.x & 31;
   int b = 0;

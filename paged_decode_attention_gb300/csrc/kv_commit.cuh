@@ -7,7 +7,9 @@
 // sequence in one layer, each thread 16 bytes of the row of both pools for all j in
 // order, kInFlight rows read before they are written; no row is read by one thread and
 // written by another.  Bound by memory where paths and batches are long (two passes over a
-// row's bytes), by the chain lengths, path, table, row otherwise.
+// row's bytes): 64 sequences in 40 sliding layers, 92 MB, 18.3 us, 0.74 of the copy rate (12.6
+// with the rows in L2); a block for one pool or for two layers took 18.9 and 19.7.  One
+// sequence in 8 global layers 5.0: the chain of lengths, path, table, row.
 #pragma once
 
 #include "attn_tree.h"
@@ -16,7 +18,7 @@
 namespace pda {
 namespace commit {
 
-constexpr int kInFlight = 4;  // rows of each pool
+constexpr int kInFlight = 4;  // rows of each pool (in L2: 2 12.9 us, 8 16.7 instead of 12.6)
 
 struct CommitParams {
   uint8_t* pool[2 * ATTN_MAX_LAYERS];  // k and v of every layer

@@ -13,7 +13,9 @@
 // out for itself (at most 256 requests, a thread each), the pages are dealt out
 // over all threads, and the cluster's barrier stands between the last read of the
 // old state and the first write of the new one, which may lie in its place.  Bound
-// by latency: lengths, sums, one entry, one store.
+// by latency: lengths, sums, one entry, one store; 64 requests of a step 4.6 us (7 from
+// Python), 200 of which many come and go, 131072 pages, 10.4 (16.2 with 4 blocks, 48.5 with
+// one).
 #pragma once
 
 #include "attn_tree.h"

@@ -27,7 +27,10 @@ namespace pda {
 namespace tree {
 
 constexpr int kMaxGroups = 16;              // of rows, per KV head; the smallest grid
-constexpr int kMinPer = 4;                  // pages of the smallest run
+// Pages of the smallest run: fewer mean more partials to merge, more leave blocks without work.  us a call with 2, 4 and 8:
+// one global tree of 4 nodes behind 900 positions 13.0, 13.9, 15.6; 8 of them behind 800 25.4, 19.0, 19.4; one of 8 behind
+// 2000 19.4, 15.5, 15.7.
+constexpr int kMinPer = 4;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kThreads = 384;
 constexpr int kMaxGrid = kMaxSplits;
@@ -633,12 +636,13 @@ __device__ __forceinline__ void store_columns(const TreeParams& p, const Segment
 // ---------------------------------------------------------------------------
 // The cut sequences' rows, joined from their partials: o = sum 2^(m_i - M) O_i /
 // sum 2^(m_i - M) l_i.  Every block reads the cuts that those of the first kernel
-// noted.  Many rows: a warp takes one whole, four dims of every 128 a lane.  Few: a block
-// takes 128 dims of one, its warps the partials in turn, and they meet in shared memory.
-// Bound by latency: kMergeInFlight loads of 16 bytes are in flight a lane.
+// noted.  A warp takes a row whole, four dims of every 128 a lane, or a block 128 dims of
+// one, its warps the partials in turn, and they meet in shared memory (merge_kernel has
+// the rule).  Bound by latency: kMergeInFlight loads of 16 bytes are in flight a lane; 2 us
+// behind a small call, 12 us alone for the 29 MB of 32 trees of 64 nodes.
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
-constexpr int kMergeBlocksPerSm = 6;
+constexpr int kMergeBlocksPerSm = 6;  // (2: 64 global trees of 8 nodes 85.7 us, not 80.9; 32 of 64 nodes 515.5, not 511.6)
 constexpr int kMergeInFlight = 8;
 
 struct MergeParams {

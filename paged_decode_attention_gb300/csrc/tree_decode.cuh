@@ -31,6 +31,19 @@
 // half of the pages of K and V into both (multicast), so that L2 is read once for both;
 // a stage is free again when both have used it.
 //
+// Weights are rounded to bf16 (half a step, 2^-8 of each) because P^T is an operand of the tensor cores, as in the bf16
+// decode and prefill: outputs are 0.0024 off the 64-bit result (relative, root mean square) where bf16 outputs of exact
+// weights are 0.0017.  The sums add them unrounded: summed as rounded, single outputs were off by up to 1.25 times the
+// bound that the tests derive.
+//
+// What bounds it (GB300, 2070 MHz; copy rate 6784 GB/s).  Long contexts HBM: 16 trees of 8 nodes behind 131072 positions
+// 690 us, 0.92 of the copy rate.  Many nodes on global layers shared memory: per 128 keys and four nodes 256 KB of K
+// and V are written and read as A, 128 KB read as B, 5120 clocks at 128 bytes each: 32 trees of 64 nodes behind 4000 to
+// 8192 take 512 us, 6200 clocks a step, 785 TFLOP/s.  (Pairs on one product, cta_group::2 with 128 rows and rings of
+// 120 KB, read A once for both and took 790 us: too little in flight.)  Sliding windows the softmax's chain of a step
+// and the ends of segments: 64 trees of 17 to 45 nodes 121 us, 0.71 of the copy rate; 200 of 5 nodes 274, 0.93.  One
+// short call latency: 4 nodes behind 900 positions 13.9.
+//
 // Roles: warps 0-7 softmax and epilogue, 8 copies Q and K, 9 copies V, 10 issues S^T,
 // 11 issues O^T.  Every wait is bounded.
 #pragma once
@@ -619,7 +632,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tree_body<C>(tm_q, tm_k, tm_v, p);
 }
 
-// D = 512: 64 rows, four nodes, alone or in pairs; D = 256: 128, 64 or 32 rows, the fewer the longer the rings.
+// D = 512: 64 rows, four nodes, alone or in pairs; D = 256: 128, 64 or 32 rows, the fewer the longer the rings.  Buffers
+// share 227 KB.  P^T twice where a step's products on V are short of its softmax; us for 64 sliding trees of 17 to 45 nodes
+// (128 rows), P^T buffers / K stages / V stages: 2/3/5 120.6, 2/2/7 128.6, 1/3/9 122.3, 1/4/7 123.8, 1/5/5 131.7; for 64
+// of 26 nodes (64 rows): 2/5/8 109.0, 2/4/10 107.9, 1/5/10 107.8, 2/6/6 111.4.
 using GlobalConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 1, 4, 4>;
 using GlobalPairConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 1, 4, 4, 2>;
 template <int kN, int kKStages, int kVStages>

@@ -37,12 +37,16 @@ struct TreePlan {
   size_t part_o_bytes, part_ml_bytes, workspace_bytes;
 };
 
-// Global trees of more than four nodes: two groups of rows share their copies.
+// Global trees of more than four nodes: two groups of rows share their copies.  us a call, in pairs and alone: 16 trees of
+// 8 nodes behind 131072 positions 696 and 797, 32 of 64 nodes 512 and 598, 8 of 64 behind 8000 184 and 214, one of 8 behind
+// 30000 30.1 and 30.6; 64 of 8 behind 100 to 4000 80.9 and 78.3.
 bool paired_tree(int32_t kind, int32_t max_q) {
   return kind == ATTN_KIND_GLOBAL && max_q > pda::tree::GlobalConfig::kNodes;
 }
 
-// Rows of the configuration that holds a whole tree of max_q nodes, or the widest.
+// Rows of the configuration that holds a whole tree of max_q nodes, or the widest.  us a call with 32, 64 and 128 rows: 200
+// sliding trees of 5 nodes 276, 277, 293; 64 of 16 nodes 102, 103, 107; 4 behind 600 positions 17.4, 18.4, 18.3; 64 of 32
+// nodes with 64 and 128 rows 110 and 116.
 int tree_rows(int32_t kind, int32_t max_q) {
   namespace tr = pda::tree;
   if (kind == ATTN_KIND_GLOBAL) return tr::GlobalConfig::kN;
