@@ -190,3 +190,93 @@ def test_calls_on_another_stream_order_their_own_memory(cuda_lib, kind):
     side.synchronize()
     assert torch.equal(out, want)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_the_step_s_other_calls_on_another_stream(cuda_lib, kind):
+    """The append's rows, the commit's lengths and the page tables, each made by its call, one stream held back."""
+    _, Hkv, D = pda.SHAPES[getattr(pda, "KIND_" + kind.upper())]
+    g = torch.Generator().manual_seed(5)
+    qkv = torch.randn((12, append_row_len(kind)), generator=g).to(torch.bfloat16).to(DEV)
+    w = torch.ones(D, dtype=torch.bfloat16, device=DEV)
+    parents, path = i32([-1, 0, 0, 2, -1, 0, 1, 2, 3, 4, 5, 6]), i32([[1, 3, 0], [0, 2, 7]])
+    cached, new, path_len = i32([30, 5]), i32([4, 8]), i32([2, 3])
+    pool = torch.randn((9, PAGE_SIZE, Hkv, D), generator=g).to(torch.bfloat16).to(DEV)
+    call = lambda name: getattr(pda, name % kind)  # noqa: E731
+
+    def run(stream):
+        kw = dict(stream=stream)
+        with torch.cuda.stream(stream):
+            state = pda.new_page_state(9, 2, 3, DEV)
+            pools = [pool.clone() for _ in range(4)]
+            status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        stream.synchronize()
+        with torch.cuda.stream(side if stream != side else torch.cuda.default_stream()):
+            torch.cuda._sleep(2_000_000)
+        lens, cu = pda.attn_pages_assign(cached, new, *state, status=status, **kw)
+        q = call("attn_kv_append_%s_tree")(qkv, w, w, state[0], lens, cu, parents, *pools[:2], status=status, **kw)
+        kept = call("attn_kv_commit_%s")(pools[0::2], pools[1::2], state[0], lens, cu, path, path_len, status=status, **kw)
+        junk = [torch.full((1 << 12,), 3.0, device=DEV) for _ in range(8)]  # would take the calls' memory
+        stream.synchronize()
+        assert int(status.item()) == 0 and kept.tolist() == [32, 8] and len(junk) == 8
+        torch.cuda.synchronize()
+        return [lens, cu, q, kept, *state, *pools]
+
+    side = torch.cuda.Stream()
+    want = run(torch.cuda.default_stream())
+    for stream in (side, torch.cuda.default_stream(), side):
+        assert all(torch.equal(a, b) for a, b in zip(run(stream), want))
+
+
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_two_graphs_of_one_workspace_replayed_in_turn(cuda_lib, kind):
+    """Calls of other sizes behind one another in one workspace, each captured; nothing is kept in it between them."""
+    from _tree import TreeCase, chain, random_tree
+    cases = [TreeCase(kind, [900, 40, 3000], [chain(6), chain(9), random_tree(40, rng(1))], seed=3, fill=0.0),
+             TreeCase(kind, [5000], [random_tree(5, rng(2))], seed=4, fill=0.0)]
+    ws = torch.full((1 << 28,), 255, dtype=torch.uint8, device=DEV)  # (NaN, and cuts that name no rows)
+    graphs, calls, want = [], [], []
+    for c in cases:
+        kw = dict(window=c.window, max_q=c.max_n, max_seq_len=max(c.L), out_dtype=torch.float32)
+        want.append(getattr(pda, "attn_decode_%s_tree" % kind)(*c.args(), **kw))
+        calls.append(getattr(pda, "prepare_decode_%s_tree" % kind)(*c.args(), workspace=ws, **kw))
+        calls[-1].run()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            calls[-1].run()
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1, 0)):
+        for call in calls:
+            call.out.fill_(7.0)
+        torch.cuda.synchronize()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(call.out, w) for call, w in zip(calls, want))
+
+
+def test_pages_beyond_32_bit_offsets(cuda_lib):
+    """The last pages of a pool of more than 2^31 elements, against the same pages in a small one."""
+    from _tree import TreeCase, chain
+    c = TreeCase("sliding", [900, 40], [random_tree(30, rng(3)), chain(9)], seed=3, fill=0.0)
+    q, k, v, table, lens, cu, parents = c.args()
+    n, P = 70000, k.shape[0]
+    g = torch.Generator().manual_seed(8)
+    qkv = torch.randn((39, append_row_len("sliding")), generator=g).to(torch.bfloat16).to(DEV)
+    w = torch.ones(256, dtype=torch.bfloat16, device=DEV)
+    path, path_len = i32([list(range(1, 30, 3)), list(range(10))]), i32([10, 9])
+    results = []
+    for off in (0, n - P):
+        pools = [k.clone(), v.clone()] if off == 0 else [torch.empty((n,) + k.shape[1:], dtype=k.dtype, device=DEV)
+                                                         for _ in "kv"]
+        if off:
+            pools[0][off:], pools[1][off:] = k, v
+        at = torch.where(table >= 0, table + off, table).to(torch.int32)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = [pda.attn_kv_append_sliding_tree(qkv, w, w, at, lens, cu, parents, *pools, status=status)]
+        out.append(pda.attn_decode_sliding_tree(q, *pools, at, lens, cu, parents, status=status))
+        out.append(pda.attn_kv_commit_sliding(*pools, at, lens, cu, path, path_len, status=status))
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        results.append(out + [x[off:].clone() for x in pools])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
