@@ -592,7 +592,8 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       store_columns<C, kTiles, kN>(p, g, walk.kv, c0, to, t_row, s.f + hb - c0, 0);
       if (s.poison != 0) {
         __syncwarp();  // (a lane's elements were stored by its neighbour)
-        add_back<C>(p, masks, g, walk.kv, node0, c0, to, 0, kD);
+        const Segment same = g;  // (g itself stays in registers: no address of it is taken)
+        add_back<C>(p, masks, same, walk.kv, node0, c0, to, 0, kD);
       }
       tc_fence_before_sync();
       __syncwarp();
