@@ -41,7 +41,7 @@
 // and V are written and read as A, 128 KB read as B, 5120 clocks at 128 bytes each: 32 trees of 64 nodes behind 4000 to
 // 8192 take 512 us, 6200 clocks a step, 785 TFLOP/s.  (Pairs on one product, cta_group::2 with 128 rows and rings of
 // 120 KB, read A once for both and took 790 us: too little in flight.)  Sliding windows the softmax's chain of a step
-// and the ends of segments: 64 trees of 17 to 45 nodes 121 us, 0.71 of the copy rate; 200 of 5 nodes 274, 0.93.  One
+// and the ends of segments: 64 trees of 17 to 45 nodes 120 us, 0.72 of the copy rate; 200 of 5 nodes 269, 0.95.  One
 // short call latency: 4 nodes behind 900 positions 13.9.
 //
 // Roles: warps 0-7 softmax and epilogue, 8 copies Q and K, 9 copies V, 10 issues S^T,
