@@ -456,15 +456,15 @@ __device__ __noinline__ void make_schedule(const TreeParams& p, Shared& s, bool 
 }
 
 // The elements of V that were zeroed, for the rows that see them: a sum with an infinity or NaN among its terms is what
-// those alone add up to, whatever their weights.  By a softmax thread, for dims d0 + its index + 128 i < d1 of columns
-// [from, to), after it (or its warp) stored them.
+// those alone add up to, whatever their weights.  By a softmax thread, for dims key + 128 i of columns [from, to), after
+// it (or its warp) stored them.
 template <typename C>
 __device__ __noinline__ void add_back(const TreeParams& p, const Masks& s, const Segment& g, int kv, int node0, int from,
-                                      int to, int d0, int d1) {
+                                      int to) {
   const int all0 = all_from(g.q, p.window);
   const int pos0 = max(g.q.lo, (g.q.page0 + g.p0) * kPage), pos1 = min(g.q.L, (g.q.page0 + g.p1) * kPage);
 #pragma unroll 1
-  for (int d = d0 + (threadIdx.x & 127); d < d1; d += 128) {
+  for (int d = threadIdx.x & 127; d < C::kD; d += 128) {
 #pragma unroll 1
     for (int col = from; col < to; ++col) {
       float sum = 0.f;
@@ -557,14 +557,10 @@ __device__ __forceinline__ void load_page(void* dst, const CUtensorMap* map, int
   }
 }
 
-// Brings one KV head of a page into L2.
+// Brings a page of the one KV head into L2.
 template <typename C>
-__device__ __forceinline__ void prefetch_page(const __nv_bfloat16* pool, const CUtensorMap* map, int kv, int id, int boxes) {
-  if constexpr (C::kHkv == 1) {
-    bulk_prefetch_l2(pool + static_cast<size_t>(id) * (kPage * C::kD), kPage * C::kD * 2);
-  } else {
-    for (int i = 0; i < boxes; ++i) tma_prefetch_3d(map, 0, id * kPage, kv * C::kChunks + i);
-  }
+__device__ __forceinline__ void prefetch_page(const __nv_bfloat16* pool, int id) {
+  if constexpr (C::kHkv == 1) bulk_prefetch_l2(pool + static_cast<size_t>(id) * (kPage * C::kD), kPage * C::kD * 2);
 }
 
 // Arrives on `bar` of every CTA of the cluster once the products this thread issued before are done.
@@ -583,17 +579,17 @@ __device__ __forceinline__ void commit_all(uint64_t* bar) {
   }
 }
 
-// The rows of a segment's output from tensor memory, by the 128 threads of a warpgroup: columns [from, to), of each the dims
-// d0 + 128 t + lane of kT tiles, tile t's columns from t_row + t * kPitch on; factor f per column.
-template <typename C, int kT, int kPitch>
+// The rows of a segment's output from tensor memory, by the 128 threads of a warpgroup: columns [from, to), of each a
+// thread's dim of every tile, tile t's columns from t_row + t * kN on; factor f per column.
+template <typename C>
 __device__ __forceinline__ void store_columns(const TreeParams& p, const Segment& g, int kv, int from, int to, uint32_t t_row,
-                                              const float* f, int d0) {
-  constexpr int kG = C::kG, kD = C::kD;
+                                              const float* f) {
+  constexpr int kG = C::kG, kD = C::kD, kT = C::kTiles;
   const int key = threadIdx.x & 127, lane = threadIdx.x & 31;
   // column col's row: of a whole sequence node col / kG, head col % kG of the output, else row col of the partial
   const bool to_f32 = !g.whole || p.out_f32;
   const size_t base =
-      (g.whole ? static_cast<size_t>(g.row0) * C::kHq + kv * kG : static_cast<size_t>(g.slot) * C::kN) * kD + d0;
+      (g.whole ? static_cast<size_t>(g.row0) * C::kHq + kv * kG : static_cast<size_t>(g.slot) * C::kN) * kD;
   const int node_pitch = (g.whole ? C::kHq : kG) * kD;
   float* const out = (g.whole ? static_cast<float*>(p.o) : p.part_o) + base + key;
   __nv_bfloat16* const out16 = static_cast<__nv_bfloat16*>(p.o) + base + (key & ~1);
@@ -601,7 +597,7 @@ __device__ __forceinline__ void store_columns(const TreeParams& p, const Segment
   for (int col = from; col < to; col += 8) {
     float ov[kT][8];
 #pragma unroll
-    for (int t = 0; t < kT; ++t) tmem_ld8(t_row + t * kPitch + col, ov[t]);
+    for (int t = 0; t < kT; ++t) tmem_ld8(t_row + t * C::kN + col, ov[t]);
     tmem_wait_ld();
     const int node = col / kG, head = col % kG;
     if (to_f32) {

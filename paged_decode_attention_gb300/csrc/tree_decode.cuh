@@ -117,7 +117,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
   using prefill_tc::kHeadroom;
   using prefill_tc::kSlack;
   using prefill_tc::tma_load_4d;
-  constexpr int kD = C::kD, kG = C::kG, kN = C::kN, kHalf = C::kHalf, kTiles = C::kTiles, kBlock = C::kBlock;
+  constexpr int kG = C::kG, kN = C::kN, kHalf = C::kHalf, kTiles = C::kTiles, kBlock = C::kBlock;
   constexpr int kPBufs = C::kPBufs, kKeys = C::kKeys, kStepPages = C::kStepPages, kCluster = C::kCluster;
   extern __shared__ uint8_t smem_raw[];
   typename C::Smem& s =
@@ -205,7 +205,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
         const int np = min(kStepPages, g.p1 - pg);
         if (ahead && lane < kStepPages && pg + kStepPages + lane < g.p1 && lane % kCluster == rank && next_id >= 0 &&
             static_cast<int64_t>(next_id) < p.num_pages)
-          prefetch_page<C>(p.k_pool, &tm_k, walk.kv, next_id, C::kChunks);
+          prefetch_page<C>(p.k_pool, next_id);
         int32_t y = id * kPage;
         if (lane < np && (id < 0 || static_cast<int64_t>(id) >= p.num_pages)) {
           report(p.status, ATTN_DEV_BAD_PAGE);
@@ -262,7 +262,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
         const int id = __shfl_sync(0xffffffffu, cur, u);
         const int far = __shfl_sync(0xffffffffu, u + kAhead < 32 ? cur : nxt, (u + kAhead) & 31);
         if (ahead && lane == 0 && pg + kAhead < g.p1 && u % kCluster == rank && far >= 0 && static_cast<int64_t>(far) < p.num_pages)
-          prefetch_page<C>(p.v_pool, &tm_v, walk.kv, far, 1);
+          prefetch_page<C>(p.v_pool, far);
         if (gv >= C::kVStages) ok = __all_sync(0xffffffffu, wait_for<(kCluster > 1)>(&s.v_empty[st], st_ph));
         if (!ok) break;
         if (lane == 0) {
@@ -589,11 +589,11 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       if (ok) ok = __all_sync(0xffffffffu, wait_for(&s.o_full, gt & 1));
       tc_fence_after_sync();
       const int to = min(c0 + half, g.cols);
-      store_columns<C, kTiles, kN>(p, g, walk.kv, c0, to, t_row, s.f + hb - c0, 0);
+      store_columns<C>(p, g, walk.kv, c0, to, t_row, s.f + hb - c0);
       if (s.poison != 0) {
         __syncwarp();  // (a lane's elements were stored by its neighbour)
         const Segment same = g;  // (g itself stays in registers: no address of it is taken)
-        add_back<C>(p, masks, same, walk.kv, node0, c0, to, 0, kD);
+        add_back<C>(p, masks, same, walk.kv, node0, c0, to);
       }
       tc_fence_before_sync();
       __syncwarp();
