@@ -2,10 +2,10 @@
 // trees of drafted tokens, its masks, the cleaning of V rows that not every node sees,
 // and the merge of cut sequences.
 //
-// Schedule.  Rows come in groups of kQueries nodes; kCluster groups of KV head c of all
-// sequences that have them are a list of pages, with seg_weight virtual pages in front of
+// Schedule.  Rows come in groups of kQueries nodes; group r of KV head c of all
+// sequences that have one is a list of pages, with seg_weight virtual pages in front of
 // every sequence (its Q, its end).  All lists are cut into runs of `per` pages, the fewest
-// that give no more runs than clusters: every cluster has the same work whatever the
+// that give no more runs than blocks: every block has the same work whatever the
 // lengths, and those of neighbouring lists walk the same keys at the same time.  A
 // sequence inside one run is finished there; of a cut one every block leaves a partial
 // (O, m, sum), and merge_kernel joins them.
@@ -36,8 +36,7 @@ constexpr int kThreads = 384;
 constexpr int kMaxGrid = kMaxSplits;
 
 struct TreeParams {
-  const __nv_bfloat16* k_pool;  // (for prefetches; read through the tensor maps)
-  const __nv_bfloat16* v_pool;
+  const __nv_bfloat16* v_pool;  // (for cleaned elements; read through the tensor maps)
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* cu_q;
@@ -54,11 +53,11 @@ struct TreeParams {
   int32_t window;
   int32_t total_q;
   int32_t max_q;
-  int32_t lists;    // per KV head: ceil(max_q / kNodes)
+  int32_t lists;    // per KV head: ceil(max_q / kQueries), or more
   int32_t q_box;    // nodes that a copy of Q brings
   int32_t out_f32;
   int32_t seg_weight;  // virtual pages charged per sequence
-  int32_t whole;    // a cluster per (sequence, group, KV head) instead of runs
+  int32_t whole;    // a block per (sequence, group, KV head) instead of runs
 };
 
 // A sequence's tree in shared memory.
@@ -70,7 +69,7 @@ struct Masks {
 
 // What the schedule leaves in shared memory.
 struct Shared {
-  int32_t pre[kMaxBatch + 1];  // pages (virtual ones included) before sequence b in this cluster's list
+  int32_t pre[kMaxBatch + 1];  // pages (virtual ones included) before sequence b in this block's list
   int32_t cu_q[kMaxBatch + 1], len[kMaxBatch];
   int32_t sched[4];            // list, KV head, per, run
   int32_t refused;             // the call as a whole
@@ -112,12 +111,12 @@ struct Segment {
   int slot;                     // of its partial
 };
 
-// Walks a cluster's segments; every role does it for itself, with the same result.
+// Walks a block's segments; every role does it for itself, with the same result.
 template <typename C>
 struct Walk {
   int b, w0, w1, group, kv, index;
   __device__ __forceinline__ void start(const TreeParams& p, const Shared& s) {
-    group = s.sched[0] * C::kCluster + static_cast<int>(blockIdx.x % C::kCluster);
+    group = s.sched[0];
     kv = s.sched[1];
     index = 0;
     const int per = s.sched[2], run = s.sched[3];
@@ -152,7 +151,7 @@ struct Walk {
       g.q = make_sequence(p, s.cu_q[b], s.cu_q[b + 1], s.len[b], refused);
       g.b = b;
       g.row0 = g.q.q0 + group * C::kQueries;
-      g.nodes = max(0, min(C::kQueries, g.q.n - group * C::kQueries));  // (0: only the cluster's other groups have any)
+      g.nodes = min(C::kQueries, g.q.n - group * C::kQueries);
       g.cols = g.nodes * C::kG;
       g.N = max(16, (g.cols + 15) & ~15);
       g.steps = (g.p1 - g.p0 + C::kStepPages - 1) / C::kStepPages;
@@ -363,7 +362,7 @@ __device__ __noinline__ void make_schedule(const TreeParams& p, Shared& s, bool 
     // (weight, lists) of sequence b
     const auto weigh = [&](int b, bool& bad) {
       const Sequence q = make_sequence(p, s.cu_q[b], s.cu_q[b + 1], s.len[b], bad);
-      return q.pages > 0 ? make_int2(q.pages + p.seg_weight, (q.n + C::kNodes - 1) / C::kNodes) : make_int2(0, 0);
+      return q.pages > 0 ? make_int2(q.pages + p.seg_weight, (q.n + C::kQueries - 1) / C::kQueries) : make_int2(0, 0);
     };
 #pragma unroll 1
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -384,7 +383,7 @@ __device__ __noinline__ void make_schedule(const TreeParams& p, Shared& s, bool 
     refused = __any_sync(0xffffffffu, refused);
     backwards = __any_sync(0xffffffffu, backwards);  // sequences overlap
     if (refused && final && blockIdx.x == 0 && lane == 0) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
-    const int g = static_cast<int>(blockIdx.x / C::kCluster);
+    const int g = static_cast<int>(blockIdx.x);
     int list, kv, per, run;
     if (p.whole) {
       const int per_seq = p.lists * C::kHkv;
@@ -393,7 +392,7 @@ __device__ __noinline__ void make_schedule(const TreeParams& p, Shared& s, bool 
       per = 1;
       run = g / per_seq;
     } else {
-      const int grid = static_cast<int>(gridDim.x / C::kCluster);
+      const int grid = static_cast<int>(gridDim.x);
       const int sum = __reduce_add_sync(0xffffffffu, total);
       int lo = max(kMinPer, (sum * C::kHkv + grid - 1) / grid);  // (at most 256 * 16388 pages * 8 heads a list)
       // (every list's last run may be short: with that many runs less there is room for all)
@@ -411,7 +410,7 @@ __device__ __noinline__ void make_schedule(const TreeParams& p, Shared& s, bool 
         }
       }
       per = hi;
-      const int mine = (total + per - 1) / per * C::kHkv;  // this list's clusters
+      const int mine = (total + per - 1) / per * C::kHkv;  // this list's blocks
       int before = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -512,7 +511,6 @@ __device__ __forceinline__ void note_cut(const TreeParams& p, const Shared& s) {
 
 // mbar_wait_fast in few instructions: with some forty waits of the kernel inlined, its code outgrew the instruction
 // cache (159 KB; a sliding call of 64 sequences took 140 us).  False once kWaitLimitNs have passed.
-template <bool kWholeCluster = false>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_addr(bar);
   uint64_t t0 = 0;
@@ -520,18 +518,15 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
   for (uint32_t n = 0;; ++n) {
     uint32_t done;
     if (n == 0) {
-      if constexpr (kWholeCluster)
-        done = mbar_test_cluster(a, parity);
-      else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(a), "r"(parity)
-            : "memory");
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(done)
+          : "r"(a), "r"(parity)
+          : "memory");
     } else {
-      done = kWholeCluster ? mbar_try_cluster(a, parity) : mbar_try_wait(a, parity);
+      done = mbar_try_wait(a, parity);
     }
     if (done) return true;
     if ((n & 63) == 63) {
@@ -539,43 +534,6 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
       if (t0 == 0) t0 = now;
       if (now - t0 > kWaitLimitNs) return false;
     }
-  }
-}
-
-// Copies a tile into the same place of every CTA of the cluster, completing on the same barrier of each.
-template <int kCluster>
-__device__ __forceinline__ void load_page(void* dst, const CUtensorMap* map, int32_t y, int32_t z, uint64_t* bar) {
-  if constexpr (kCluster == 1) {
-    prefill_tc::tma_load_3d(dst, map, 0, y, z, bar);
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_addr(bar)),
-        "h"(static_cast<uint16_t>((1 << kCluster) - 1))
-        : "memory");
-  }
-}
-
-// Brings a page of the one KV head into L2.
-template <typename C>
-__device__ __forceinline__ void prefetch_page(const __nv_bfloat16* pool, int id) {
-  if constexpr (C::kHkv == 1) bulk_prefetch_l2(pool + static_cast<size_t>(id) * (kPage * C::kD), kPage * C::kD * 2);
-}
-
-// Arrives on `bar` of every CTA of the cluster once the products this thread issued before are done.
-template <int kCluster>
-__device__ __forceinline__ void commit_all(uint64_t* bar) {
-  if constexpr (kCluster == 1) {
-    umma_commit_warp(bar);
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-            smem_addr(bar)),
-        "h"(static_cast<uint16_t>((1 << kCluster) - 1))
-        : "memory");
   }
 }
 
@@ -644,7 +602,6 @@ constexpr int kMergeInFlight = 8;
 struct MergeParams {
   TreeParams t;
   int32_t grid;    // blocks of the first kernel
-  int32_t stride;  // distance of consecutive blocks of a list: KV heads, times the cluster
 };
 
 // The cut rows of all blocks, numbered: every warp for itself, lane l the blocks l * each .. (l + 1) * each - 1.  No
@@ -726,7 +683,7 @@ __device__ __forceinline__ MergeItem<kT> merge_partials(const MergeParams& mp, c
 #pragma unroll
     for (int u = 0; u < kFly; ++u) {
       const int i = i0 + u * team;
-      const size_t at = static_cast<size_t>(i == 0 ? cut.z : 2 * (lo + i * mp.stride)) * C::kN + it.col;
+      const size_t at = static_cast<size_t>(i == 0 ? cut.z : 2 * (lo + i * C::kHkv)) * C::kN + it.col;
       e[u] = i < cut.w ? p.part_ml[at] : make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int t = 0; t < kT; ++t)

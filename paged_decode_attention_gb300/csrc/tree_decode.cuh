@@ -26,23 +26,19 @@
 // keys all nodes see takes one key's scores for the first references, which the same
 // bounds then correct.
 //
-// Clusters.  On global layers a tree of more than four nodes has several groups, and
-// every group reads all keys.  Two CTAs walk a run together, a group each: each copies
-// half of the pages of K and V into both (multicast), so that L2 is read once for both;
-// a stage is free again when both have used it.
-//
 // Weights are rounded to bf16 (half a step, 2^-8 of each) because P^T is an operand of the tensor cores, as in the bf16
 // decode and prefill: outputs are 0.0024 off the 64-bit result (relative, root mean square) where bf16 outputs of exact
 // weights are 0.0017.  The sums add them unrounded: summed as rounded, single outputs were off by up to 1.25 times the
 // bound that the tests derive.
 //
-// What bounds it (GB300, 2070 MHz; copy rate 6784 GB/s).  Long contexts HBM: 16 trees of 8 nodes behind 131072 positions
-// 690 us, 0.92 of the copy rate.  Many nodes on global layers shared memory: per 128 keys and four nodes 256 KB of K
-// and V are written and read as A, 128 KB read as B, 5120 clocks at 128 bytes each: 32 trees of 64 nodes behind 4000 to
-// 8192 take 512 us, 6200 clocks a step, 785 TFLOP/s.  (Pairs on one product, cta_group::2 with 128 rows and rings of
-// 120 KB, read A once for both and took 790 us: too little in flight.)  Sliding windows the softmax's chain of a step
-// and the ends of segments: 64 trees of 17 to 45 nodes 120 us, 0.72 of the copy rate; 200 of 5 nodes 269, 0.95.  One
-// short call latency: 4 nodes behind 900 positions 13.9.
+// What bounds it (GB300, 2070 MHz; copy rate 6784 GB/s).  Long contexts HBM where a tree has one group: 16 trees of 4
+// nodes behind 131072 positions 632 us, the copy rate; with two groups L2, which gives all keys to both: 16 of 8 nodes
+// 771, 0.82 of it.  Many nodes on global layers shared memory: per 128 keys and four nodes 256 KB of K and V are
+// written and read as A, 128 KB read as B, 5120 clocks at 128 bytes each: 32 trees of 64 nodes behind 4000 to 8192 take
+// 600 us, 7300 clocks a step, 670 TFLOP/s.  (Pairs of CTAs on one product, cta_group::2 with 128 rows and rings of 120
+// KB, read A once for both and took 790 us: too little in flight.  Pages brought into L2 ahead of the copies: 600 -> 656,
+// 771 -> 863.)  Sliding windows the softmax's chain of a step and the ends of segments: 64 trees of 17 to 45 nodes 120
+// us, 0.72 of the copy rate; 200 of 5 nodes 269, 0.95.  One short call latency: 4 nodes behind 900 positions 13.7.
 //
 // Roles: warps 0-7 softmax and epilogue, 8 copies Q and K, 9 copies V, 10 issues S^T,
 // 11 issues O^T.  Every wait is bounded.
@@ -53,15 +49,13 @@
 namespace pda {
 namespace tree {
 
-template <int kD_, int kG_, int kHkv_, int kN_, int kPBufs_, int kKStages_, int kVStages_, int kCluster_ = 1>
+template <int kD_, int kG_, int kHkv_, int kN_, int kPBufs_, int kKStages_, int kVStages_>
 struct Config {
-  static constexpr int kCluster = kCluster_;   // CTAs that share their copies of K and V
   static constexpr int kD = kD_, kG = kG_, kHkv = kHkv_, kHq = kG * kHkv;
   static constexpr int kN = kN_;               // rows per group, at most
   static constexpr int kHalf = kN / 2;         // columns per softmax warpgroup
   static constexpr int kBlock = kHalf < 32 ? kHalf : 32;  // columns at a time
   static constexpr int kQueries = kN / kG;     // nodes of a group
-  static constexpr int kNodes = kQueries * kCluster;  // and of a list
   static constexpr int kKeys = 128;             // per step
   static constexpr int kStepPages = kKeys / kPage;
   static constexpr int kChunks = kD / 64;
@@ -78,7 +72,6 @@ struct Config {
   static constexpr uint32_t kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static_assert(kUsedCols <= 512 && kN % 16 == 0 && kN <= 256, "tensor memory");
   static_assert(kBlock == 16 || kBlock == 32, "column reductions");
-  static_assert(kCluster == 1 || kCluster == 2, "pages by rank");
 
   struct Smem {
     alignas(1024) uint8_t q[kChunks][kN * 128];
@@ -105,37 +98,31 @@ struct Config {
   static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM within the 227 KB a CTA may have");
 };
 
-// Pairs that walk at least this many pages of a sequence have them brought into L2 a step ahead of the copies: a stage
-// is refilled only once both CTAs have used it, and the 128 KB in flight do not cover DRAM's latency then.  us a call,
-// without and with: 16 x 131072 positions, 8 nodes 713 and 692 (with V 24 pages ahead instead of 12 842), 32 trees of 64
-// nodes 522 and 514; 8 short ragged ones 41.2 and 42.4.  Alone, a CTA is slower with it: 64 x 4 nodes 64 and 78.
-constexpr int kPrefetchPages = 64;
-
 template <typename C>
-__device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                          const TreeParams& p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
   using prefill_tc::kHeadroom;
   using prefill_tc::kSlack;
   using prefill_tc::tma_load_4d;
   constexpr int kG = C::kG, kN = C::kN, kHalf = C::kHalf, kTiles = C::kTiles, kBlock = C::kBlock;
-  constexpr int kPBufs = C::kPBufs, kKeys = C::kKeys, kStepPages = C::kStepPages, kCluster = C::kCluster;
+  constexpr int kPBufs = C::kPBufs, kKeys = C::kKeys, kStepPages = C::kStepPages;
   extern __shared__ uint8_t smem_raw[];
   typename C::Smem& s =
       *reinterpret_cast<typename C::Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(blockIdx.x % kCluster);
 
   if (threadIdx.x == 0) {
 #pragma unroll 1
     for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(&s.k_full[i], 1);
-      mbar_init(&s.k_empty[i], kCluster);
+      mbar_init(&s.k_empty[i], 1);
     }
 #pragma unroll 1
     for (int i = 0; i < C::kVStages; ++i) {
       mbar_init(&s.v_full[i], 1);
-      mbar_init(&s.v_empty[i], kCluster);
+      mbar_init(&s.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
@@ -176,7 +163,6 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
   tc_fence_after_sync();
   const uint32_t tmem = s.tmem_base;
   const bool run = s.sh.refused == 0;
-  if constexpr (kCluster > 1) cluster_sync_all();  // the other CTA's barriers are there
   if (!run) {
     if (threadIdx.x == 0 && !p.whole) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp == 8) {
@@ -196,16 +182,12 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       ++gt;
       const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks + g.q.page0;
       const auto entry = [&](int pg) { return lane < kStepPages && pg + lane < g.p1 ? table[pg + lane] : 0; };
-      const bool ahead = kCluster > 1 && g.p1 - g.p0 >= kPrefetchPages;
       int next_id = entry(g.p0);
 #pragma unroll 1
       for (int pg = g.p0; pg < g.p1 && ok; pg += kStepPages) {
         const int id = next_id;
         next_id = entry(pg + kStepPages);
         const int np = min(kStepPages, g.p1 - pg);
-        if (ahead && lane < kStepPages && pg + kStepPages + lane < g.p1 && lane % kCluster == rank && next_id >= 0 &&
-            static_cast<int64_t>(next_id) < p.num_pages)
-          prefetch_page<C>(p.k_pool, next_id);
         int32_t y = id * kPage;
         if (lane < np && (id < 0 || static_cast<int64_t>(id) >= p.num_pages)) {
           report(p.status, ATTN_DEV_BAD_PAGE);
@@ -213,12 +195,12 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
         }
 #pragma unroll 1
         for (int ch = 0; ch < C::kChunks; ++ch) {
-          if (gk >= C::kKStages) ok = __all_sync(0xffffffffu, wait_for<(kCluster > 1)>(&s.k_empty[st], st_ph));
+          if (gk >= C::kKStages) ok = __all_sync(0xffffffffu, wait_for(&s.k_empty[st], st_ph));
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&s.k_full[st], np * kPage * 128);
           __syncwarp();
-          if (lane < np && lane % kCluster == rank)
-            load_page<kCluster>(s.k[st] + lane * (kPage * 128), &tm_k, y, walk.kv * C::kChunks + ch, &s.k_full[st]);
+          if (lane < np)
+            prefill_tc::tma_load_3d(s.k[st] + lane * (kPage * 128), &tm_k, 0, y, walk.kv * C::kChunks + ch, &s.k_full[st]);
           ++gk;
           if (++st == C::kKStages) st = 0, st_ph ^= 1;
           __syncwarp();
@@ -235,12 +217,11 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       for (int i = 0; i < C::kKStages && i < gk; ++i) {
         const int uses = (gk - 1 - i) / C::kKStages;
         if (!wait_for(&s.k_full[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
-        if (ok && !wait_for<(kCluster > 1)>(&s.k_empty[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+        if (ok && !wait_for(&s.k_empty[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
       }
     }
   } else if (warp == 9) {
     // ---------------- V producer: a page per stage ----------------
-    constexpr int kAhead = 12;  // pages that a prefetch runs ahead
     bool ok = true;
     int gv = 0, st = 0, st_ph = 1;
     Walk<C> walk;
@@ -250,7 +231,6 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     while (ok && walk.next(p, s.sh, g)) {
       const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks + g.q.page0;
       const auto entry = [&](int pg) { return pg < g.p1 ? table[pg] : 0; };
-      const bool ahead = kCluster > 1 && g.p1 - g.p0 >= kPrefetchPages;
       int cur = 0, nxt = entry(g.p0 + lane);
 #pragma unroll 1
       for (int pg = g.p0; pg < g.p1 && ok; ++pg) {
@@ -260,16 +240,12 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
           nxt = entry(pg + 32 + lane);
         }
         const int id = __shfl_sync(0xffffffffu, cur, u);
-        const int far = __shfl_sync(0xffffffffu, u + kAhead < 32 ? cur : nxt, (u + kAhead) & 31);
-        if (ahead && lane == 0 && pg + kAhead < g.p1 && u % kCluster == rank && far >= 0 && static_cast<int64_t>(far) < p.num_pages)
-          prefetch_page<C>(p.v_pool, far);
-        if (gv >= C::kVStages) ok = __all_sync(0xffffffffu, wait_for<(kCluster > 1)>(&s.v_empty[st], st_ph));
+        if (gv >= C::kVStages) ok = __all_sync(0xffffffffu, wait_for(&s.v_empty[st], st_ph));
         if (!ok) break;
         if (lane == 0) {
           const bool there = id >= 0 && static_cast<int64_t>(id) < p.num_pages;  // (the K producer reports)
           mbar_arrive_expect_tx(&s.v_full[st], C::kVPage);
-          if (u % kCluster == rank)
-            load_page<kCluster>(s.v[st], &tm_v, there ? id * kPage : -kPage, walk.kv * C::kChunks, &s.v_full[st]);
+          prefill_tc::tma_load_3d(s.v[st], &tm_v, 0, there ? id * kPage : -kPage, walk.kv * C::kChunks, &s.v_full[st]);
         }
         ++gv;
         if (++st == C::kVStages) st = 0, st_ph ^= 1;
@@ -282,7 +258,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
       for (int i = 0; i < C::kVStages && i < gv; ++i) {
         const int uses = (gv - 1 - i) / C::kVStages;
         if (!wait_for(&s.v_full[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
-        if (ok && !wait_for<(kCluster > 1)>(&s.v_empty[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
+        if (ok && !wait_for(&s.v_empty[i], uses & 1)) report(p.status, ATTN_DEV_WAIT_TIMEOUT);
       }
     }
   } else if (warp == 10) {
@@ -312,7 +288,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
           for (int kk = 0; kk < 4; ++kk)
             umma_bf16_warp(d, umma_desc(k_base + kk * 32, 16, 1024, 2),
                            umma_desc(q_base + ch * (kN * 128) + kk * 32, 16, 1024, 2), idesc, (ch | kk) > 0 ? 1u : 0u);
-          commit_all<kCluster>(&s.k_empty[st]);
+          umma_commit_warp(&s.k_empty[st]);
           if (++st == C::kKStages) st = 0, st_ph ^= 1;
         }
         umma_commit_warp(&s.s_full[sb]);
@@ -367,7 +343,7 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
             umma_bf16_warp(tmem + t * kN, umma_desc(v_base + t * (2 * kPage * 128), kPage * 128, 1024, 2),
                            umma_desc(p_base + kk * (kPage * 128), C::kPChunk, 1024, 2), idesc,
                            (pg0 > g.p0 || kk > 0) ? 1u : 0u);
-          commit_all<kCluster>(&s.v_empty[st]);
+          umma_commit_warp(&s.v_empty[st]);
           if (++st == C::kVStages) st = 0, st_ph ^= 1;
         }
         umma_commit_warp(&s.p_empty[pb]);
@@ -615,30 +591,13 @@ __device__ __forceinline__ void tree_body(const CUtensorMap& tm_q, const CUtenso
     tc_fence_after_sync();
     tmem_dealloc(tmem, C::kTmemCols);
   }
-  if constexpr (kCluster > 1) cluster_sync_all();  // nothing of the other CTA may arrive in one that has left
 }
 
-template <typename C>
-__global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
-  tree_body<C>(tm_q, tm_k, tm_v, p);
-}
-
-template <typename C>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
-  static_assert(C::kCluster == 2, "as launched");
-  tree_body<C>(tm_q, tm_k, tm_v, p);
-}
-
-// D = 512: 64 rows, four nodes, alone or in pairs; D = 256: 128, 64 or 32 rows, the fewer the longer the rings.  Buffers
+// D = 512: 64 rows, four nodes; D = 256: 128, 64 or 32 rows, the fewer the longer the rings.  Buffers
 // share 227 KB.  P^T twice where a step's products on V are short of its softmax; us for 64 sliding trees of 17 to 45 nodes
 // (128 rows), P^T buffers / K stages / V stages: 2/3/5 120.6, 2/2/7 128.6, 1/3/9 122.3, 1/4/7 123.8, 1/5/5 131.7; for 64
 // of 26 nodes (64 rows): 2/5/8 109.0, 2/4/10 107.9, 1/5/10 107.8, 2/6/6 111.4.
 using GlobalConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 1, 4, 4>;
-using GlobalPairConfig = Config<ATTN_GLOBAL_D, ATTN_GLOBAL_HQ / ATTN_GLOBAL_HKV, ATTN_GLOBAL_HKV, 64, 1, 4, 4, 2>;
 template <int kN, int kKStages, int kVStages>
 using SlidingConfig =
     Config<ATTN_SLIDING_D, ATTN_SLIDING_HQ / ATTN_SLIDING_HKV, ATTN_SLIDING_HKV, kN, 2, kKStages, kVStages>;

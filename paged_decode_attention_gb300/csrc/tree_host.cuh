@@ -28,8 +28,7 @@ constexpr int kTreeSegWeight = 12, kTreeSegWeightFew = 4;
 
 struct TreePlan {
   int rows;      // of the configuration's groups
-  int cluster;   // CTAs
-  int lists;     // of pages, per KV head: ceil(max_q / (nodes of a cluster))
+  int lists;     // of pages, per KV head: a group of rows each
   int grid;
   int seg_weight;
   bool whole;
@@ -37,21 +36,14 @@ struct TreePlan {
   size_t part_o_bytes, part_ml_bytes, workspace_bytes;
 };
 
-// Global trees of more than four nodes: two groups of rows share their copies.  us a call, in pairs and alone: 16 trees of
-// 8 nodes behind 131072 positions 696 and 797, 32 of 64 nodes 512 and 598, 8 of 64 behind 8000 184 and 214, one of 8 behind
-// 30000 30.1 and 30.6; 64 of 8 behind 100 to 4000 80.9 and 78.3.
-bool paired_tree(int32_t kind, int32_t max_q) {
-  return kind == ATTN_KIND_GLOBAL && max_q > pda::tree::GlobalConfig::kNodes;
-}
-
 // Rows of the configuration that holds a whole tree of max_q nodes, or the widest.  us a call with 32, 64 and 128 rows: 200
 // sliding trees of 5 nodes 276, 277, 293; 64 of 16 nodes 102, 103, 107; 4 behind 600 positions 17.4, 18.4, 18.3; 64 of 32
 // nodes with 64 and 128 rows 110 and 116.
 int tree_rows(int32_t kind, int32_t max_q) {
   namespace tr = pda::tree;
   if (kind == ATTN_KIND_GLOBAL) return tr::GlobalConfig::kN;
-  return max_q <= tr::SlidingNarrow::kNodes ? tr::SlidingNarrow::kN
-         : max_q <= tr::SlidingMid::kNodes  ? tr::SlidingMid::kN
+  return max_q <= tr::SlidingNarrow::kQueries ? tr::SlidingNarrow::kN
+         : max_q <= tr::SlidingMid::kQueries  ? tr::SlidingMid::kN
                                             : tr::SlidingWide::kN;
 }
 
@@ -70,28 +62,30 @@ int32_t make_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_s
   const int d = sliding ? ATTN_SLIDING_D : ATTN_GLOBAL_D;
   const int hkv = sliding ? ATTN_SLIDING_HKV : ATTN_GLOBAL_HKV;
   out->rows = tree_rows(kind, max_q);
-  out->cluster = paired_tree(kind, max_q) ? tr::GlobalPairConfig::kCluster : 1;
-  const int nodes = out->rows * hkv / 16 * out->cluster;  // 16 query heads
+  const int nodes = out->rows * hkv / 16;  // of a group; 16 query heads
   out->lists = std::max(1, (max_q + nodes - 1) / nodes);
   // pages of one sequence: with a window those of window + max_q - 1 positions
   const int64_t span = window > 0 ? std::min<int64_t>(max_seq_len, static_cast<int64_t>(window) + max_q - 1) : max_seq_len;
   const int64_t pages = std::max<int64_t>(1, std::min<int64_t>((span + 2 * ATTN_PAGE_SIZE - 2) / ATTN_PAGE_SIZE,
                                                                (static_cast<int64_t>(max_seq_len) + ATTN_PAGE_SIZE - 1) / ATTN_PAGE_SIZE));
+  // Whole sequences take an even number of blocks where they have several groups, as their plans always had; one without
+  // nodes leaves at once.
+  const int whole_lists = out->lists > 1 ? (out->lists + 1) & ~1 : 1;
+  const int64_t whole_items = static_cast<int64_t>(batch) * whole_lists * hkv;
   const int64_t items = static_cast<int64_t>(batch) * out->lists * hkv;
-  const int64_t clusters = std::max(1, num_sms / out->cluster);
-  out->seg_weight = 4 * items >= clusters ? kTreeSegWeight : kTreeSegWeightFew;
-  out->whole = num_splits == 0 && items <= clusters &&
-               pages * (2 * clusters - items) <= 2 * (kTreeWholePages * clusters + kTreeWholeStarts * items);
+  out->seg_weight = 4 * items >= num_sms ? kTreeSegWeight : kTreeSegWeightFew;
+  out->whole = num_splits == 0 && whole_items <= num_sms &&
+               pages * (2 * num_sms - whole_items) <= 2 * (kTreeWholePages * num_sms + kTreeWholeStarts * whole_items);
   out->merge = !out->whole;
   if (out->whole) {
-    out->grid = static_cast<int>(items) * out->cluster;
+    out->lists = whole_lists;
+    out->grid = static_cast<int>(whole_items);
   } else if (num_splits > 0) {
-    out->grid = (num_splits + out->cluster - 1) / out->cluster * out->cluster;
+    out->grid = num_splits;
   } else {
     const int64_t useful = (items * (pages + out->seg_weight) + tr::kMinPer - 1) / tr::kMinPer;
     const int64_t least = tr::kMaxGroups;  // a run for every list
-    out->grid = static_cast<int>(std::max<int64_t>(least, std::min<int64_t>({clusters, useful, tr::kMaxGrid / out->cluster}))) *
-                out->cluster;
+    out->grid = static_cast<int>(std::max<int64_t>(least, std::min<int64_t>({num_sms, useful, tr::kMaxGrid})));
   }
   const size_t rows = 2 * static_cast<size_t>(out->grid) * out->rows;
   out->part_o_bytes = out->merge ? align256(rows * d * sizeof(float)) : 0;
@@ -131,12 +125,7 @@ int32_t launch_tree(const char* name, const void* q, const void* k_pool, const v
       (st = encode_chunk_map(&tm_k, k_pool, p.num_pages, C::kHkv * C::kD, 1)) ||
       (st = encode_chunk_map(&tm_v, v_pool, p.num_pages, C::kHkv * C::kD, C::kChunks)))
     return st;
-  const auto kernel = [] {
-    if constexpr (C::kCluster > 1)
-      return tr::tree_pair_kernel<C>;
-    else
-      return tr::tree_kernel<C>;
-  }();
+  const auto kernel = tr::tree_kernel<C>;
   static bool main_set[kMaxDevices] = {false}, merge_set[kMaxDevices] = {false};
   if ((st = ensure_smem(kernel, C::kSmemBytes, dev, main_set)) ||
       (st = ensure_smem(tr::merge_kernel<C>, 0, dev, merge_set)))
@@ -146,7 +135,6 @@ int32_t launch_tree(const char* name, const void* q, const void* k_pool, const v
     tr::MergeParams mp;
     mp.t = p;
     mp.grid = plan.grid;
-    mp.stride = C::kHkv * C::kCluster;
     const int64_t rows = static_cast<int64_t>(p.batch) * p.max_q * C::kHq;  // a block per row's 128 dims, at most
     const int blocks = static_cast<int>(std::min<int64_t>(rows * C::kTiles, static_cast<int64_t>(num_sms) * tr::kMergeBlocksPerSm));
     e = launch_pdl(tr::merge_kernel<C>, dim3(blocks), tr::kMergeWarps * 32, 0, s, mp);
@@ -196,7 +184,6 @@ int32_t run_tree(int32_t kind, const void* q, const void* k_pool, const void* v_
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   pda::tree::TreeParams p{};
-  p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
   p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
   p.block_table = block_table;
   p.seq_lens = seq_lens;
@@ -222,7 +209,7 @@ int32_t run_tree(int32_t kind, const void* q, const void* k_pool, const void* v_
   const auto launch = [&](auto config) {
     return launch_tree<decltype(config)>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);
   };
-  if (!sliding) return paired_tree(kind, max_q) ? launch(tr::GlobalPairConfig{}) : launch(tr::GlobalConfig{});
+  if (!sliding) return launch(tr::GlobalConfig{});
   return plan.rows == tr::SlidingNarrow::kN ? launch(tr::SlidingNarrow{})
          : plan.rows == tr::SlidingMid::kN  ? launch(tr::SlidingMid{})
                                             : launch(tr::SlidingWide{});
