@@ -454,9 +454,9 @@ __device__ __noinline__ void make_schedule(const TreeParams& p, Shared& s, bool 
   __syncwarp();
 }
 
-// The elements of V that were zeroed, for the rows that see them: a sum with an infinity or NaN among its terms is what
-// those alone add up to, whatever their weights.  By a softmax thread, for dims key + 128 i of columns [from, to), after
-// it (or its warp) stored them.
+// The elements of V that were zeroed, for the rows that see them: an infinity or NaN among a sum's terms adds itself,
+// whatever its weight, to what the products gave, which may be one too (of a key, or of a value that all nodes see).  By a
+// softmax thread, for dims key + 128 i of columns [from, to), after it (or its warp) stored them.
 template <typename C>
 __device__ __noinline__ void add_back(const TreeParams& p, const Masks& s, const Segment& g, int kv, int node0, int from,
                                       int to) {
@@ -481,14 +481,16 @@ __device__ __noinline__ void add_back(const TreeParams& p, const Masks& s, const
       }
       if (sum == 0.f) continue;  // (anything else is an infinity or NaN)
       if (!g.whole) {
-        p.part_o[(static_cast<size_t>(g.slot) * C::kN + col) * C::kD + d] = sum;
+        p.part_o[(static_cast<size_t>(g.slot) * C::kN + col) * C::kD + d] += sum;
         continue;
       }
       const size_t at = (static_cast<size_t>(g.row0 + col / C::kG) * C::kHq + kv * C::kG + col % C::kG) * C::kD + d;
-      if (p.out_f32)
-        static_cast<float*>(p.o)[at] = sum;
-      else
-        static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(sum);
+      if (p.out_f32) {
+        static_cast<float*>(p.o)[at] += sum;
+      } else {
+        __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.o) + at;
+        *o = __float2bfloat16_rn(__bfloat162float(*o) + sum);
+      }
     }
   }
 }
