@@ -70,8 +70,10 @@ extern "C" {
  *
  * Products run on the tensor cores on bf16 with fp32 sums; weights are rounded
  * to bf16 for their product with the values.  A visible NaN gives NaN outputs;
- * what a node does not see is not used for it, whatever it holds.  Every array
- * 16 bytes aligned, the int32 ones 4.  One or two kernels.
+ * an infinity among the values gives itself, or NaN (next to one of the other
+ * sign, or where every node sees it with a weight below fp32's range); what a
+ * node does not see is not used for it, whatever it holds.  Every array 16
+ * bytes aligned, the int32 ones 4.  One or two kernels.
  */
 int32_t attn_decode_sliding_tree(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
                                  const int32_t* seq_lens, const int32_t* cu_q, const int32_t* parents, void* o,

@@ -594,7 +594,8 @@ __device__ __forceinline__ void store_columns(const TreeParams& p, const Segment
 // sum 2^(m_i - M) l_i.  Every block reads the cuts that those of the first kernel
 // noted.  A warp takes a row whole, four dims of every 128 a lane, or a block 128 dims of
 // one, its warps the partials in turn, and they meet in shared memory (merge_kernel has
-// the rule).  Bound by latency: kMergeInFlight loads of 16 bytes are in flight a lane; 2 us
+// the rule).  A part whose weight is below fp32's range adds nothing but its infinities and NaN, which a whole sequence
+// would show, too (0 * inf would be NaN).  Bound by latency: kMergeInFlight loads of 16 bytes are in flight a lane; 2 us
 // behind a small call, 12 us alone for the 29 MB of 32 trees of 64 nodes.
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
@@ -661,6 +662,15 @@ struct MergeItem {
   float4 o[kT];
 };
 
+// acc + w * v, where w is 0 only what of v is not finite.
+__device__ __forceinline__ float4 add_weighed(float4 acc, float w, float4 v) {
+  if (w == 0.f) {
+    const auto kept = [](float x) { return fabsf(x) < INFINITY ? 0.f : x; };
+    return make_float4(acc.x + kept(v.x), acc.y + kept(v.y), acc.z + kept(v.z), acc.w + kept(v.w));
+  }
+  return make_float4(acc.x + w * v.x, acc.y + w * v.y, acc.z + w * v.z, acc.w + w * v.w);
+}
+
 // Partials member, member + team, .. of a row, kT * 128 dims from tile0 * 128 on, four a lane.
 template <typename C, int kT>
 __device__ __forceinline__ MergeItem<kT> merge_partials(const MergeParams& mp, const CutRows<C>& rows, int row, int tile0,
@@ -701,18 +711,14 @@ __device__ __forceinline__ MergeItem<kT> merge_partials(const MergeParams& mp, c
     it.m = m;
     it.l *= f;
 #pragma unroll
-    for (int t = 0; t < kT; ++t) {
-      it.o[t].x *= f; it.o[t].y *= f; it.o[t].z *= f; it.o[t].w *= f;
-    }
+    for (int t = 0; t < kT; ++t) it.o[t] = add_weighed(make_float4(0.f, 0.f, 0.f, 0.f), f, it.o[t]);
 #pragma unroll
     for (int u = 0; u < kFly; ++u) {
       if (!(e[u].y > 0.f)) continue;
       const float w = exp2f(e[u].x - m);
       it.l += w * e[u].y;
 #pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        it.o[t].x += w * a[u][t].x; it.o[t].y += w * a[u][t].y; it.o[t].z += w * a[u][t].z; it.o[t].w += w * a[u][t].w;
-      }
+      for (int t = 0; t < kT; ++t) it.o[t] = add_weighed(it.o[t], w, a[u][t]);
     }
   }
   return it;
@@ -773,9 +779,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocksPerSm) merge_ker
 #pragma unroll
         for (int w = 0; w < kMergeWarps; ++w) {
           const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - all.m);
-          const float4 v = s_o[w][lane];
           all.l += f * s_l[w];
-          O.x += f * v.x; O.y += f * v.y; O.z += f * v.z; O.w += f * v.w;
+          O = add_weighed(O, f, s_o[w][lane]);
         }
         all.o[0] = O;
         store_merged<C, 1>(p, all, item % C::kTiles);

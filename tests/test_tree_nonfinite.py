@@ -99,3 +99,33 @@ def test_two_values_of_one_path(cuda_lib, kind):
         c.v[page[0], row[0], :, 5] = INF
         c.v[page[1], row[1], :, 5] = -INF
         check(c, clean, num_splits=splits)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("far", [100, 199])
+def test_an_infinity_of_no_weight_does_not_depend_on_the_cut(cuda_lib, kind, out_dtype, far):
+    """One key's scores stand some 250 above all others, so that every other weight is below fp32's range; `far` of a
+    context of 200, or of 1200 for the cut cases.  The infinity stands in a node's row, behind the key."""
+    for ctx, splits in CUTS:
+        ctx = ctx if ctx == 200 else 1200
+        c = TreeCase(kind, [ctx, 40], [TREE, chain(3)], seed=44)
+        c.q[:, :, 0] = 1.0
+        page, row = c.slot(0, torch.tensor([ctx - 200 + far, ctx + 1]))
+        c.k[page[0], row[0], :, 0] = 256.0
+        clean = c.want()
+        c.v[page[1], row[1], :, 33] = INF
+        check(c, clean, out_dtype, num_splits=splits)
+
+
+@pytest.mark.parametrize("ahead", [100, 900, 1022])
+def test_an_infinity_at_the_window_s_edge_does_not_depend_on_the_cut(cuda_lib, ahead):
+    """The same for the first position that nodes of depth 0 see, in front of the key by `ahead`."""
+    for splits in (0, 16, 60, 152, 1024):
+        c = TreeCase("sliding", [1500, 40], [[-1, 0, -1, 1], chain(3)], seed=45)
+        c.q[:, :, 0] = 1.0
+        page, row = c.slot(0, torch.tensor([1500 - 1023, 1500 - 1023 + ahead]))
+        c.k[page[1], row[1], :, 0] = 256.0
+        clean = c.want()
+        c.v[page[0], row[0], :, 33] = -INF
+        check(c, clean, num_splits=splits)
