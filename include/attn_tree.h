@@ -55,7 +55,9 @@ extern "C" {
  *              total_q; rows of o behind it are left as they are
  * parents      int32 [total_q]
  * o            [total_q, 16, D], bf16 or fp32 per out_dtype
- * max_q        host bound on n, 0 .. ATTN_MAX_TREE (shapes the tiles)
+ * max_q        host bound on n, 0 .. ATTN_MAX_TREE (shapes the tiles); with max_q
+ *              or total_q 0 the lengths are checked, where there is a status,
+ *              and nothing else is done
  * max_seq_len  host bound on seq_lens; it only sizes the launch
  * window       sliding: > 0 (the node's is 1024); global: <= 0 none, > 0 a window
  * num_splits   thread blocks the keys are cut among: 0 = one per SM (fewer for

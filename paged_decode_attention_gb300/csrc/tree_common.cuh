@@ -97,6 +97,16 @@ __device__ __forceinline__ Sequence make_sequence(const TreeParams& p, int q0, i
   return s;
 }
 
+// A call without nodes: its lengths may deny that.  A thread per sequence.
+__global__ void __launch_bounds__(kMaxBatch) check_kernel(const __grid_constant__ TreeParams p) {
+  wait_for_primary_grid();
+  allow_dependent_launch();
+  const int b = static_cast<int>(threadIdx.x);
+  bool refused = false;
+  if (b < p.batch) make_sequence(p, p.cu_q[b], p.cu_q[b + 1], p.seq_lens[b], refused);
+  if (refused) report(p.status, ATTN_DEV_BAD_SEQ_LEN);
+}
+
 // Positions below are not seen by every node.
 __device__ __forceinline__ int all_from(const Sequence& q, int window) {
   return window > 0 ? q.ctx + (q.n - 1) - window + 1 : 0;  // (a depth is at most n - 1)

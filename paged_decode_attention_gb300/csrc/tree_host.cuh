@@ -178,9 +178,9 @@ int32_t run_tree(int32_t kind, const void* q, const void* k_pool, const void* v_
     return fail(ATTN_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)", name, plan.workspace_bytes,
                 workspace ? workspace_bytes : size_t{0});
   if (!aligned16(workspace)) return fail(ATTN_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", name);
-  const bool idle = total_q == 0 || max_q == 0;  // no nodes
-  g_last_launches = idle ? 0 : plan.merge ? 2 : 1;
-  if (idle || g_validate_only) return ATTN_OK;
+  const bool idle = total_q == 0 || max_q == 0;  // no nodes, by the caller: there are only the lengths to check
+  g_last_launches = idle ? (status ? 1 : 0) : plan.merge ? 2 : 1;
+  if (g_last_launches == 0 || g_validate_only) return ATTN_OK;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   pda::tree::TreeParams p{};
@@ -206,6 +206,7 @@ int32_t run_tree(int32_t kind, const void* q, const void* k_pool, const void* v_
   p.whole = plan.whole;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   namespace tr = pda::tree;
+  if (idle) return launched(name, launch_pdl(tr::check_kernel, dim3(1), pda::kMaxBatch, 0, s, p));
   const auto launch = [&](auto config) {
     return launch_tree<decltype(config)>(name, q, k_pool, v_pool, total_q, plan, dev, num_sms, p, s);
   };
