@@ -62,8 +62,10 @@ extern "C" {
  * window       sliding: > 0 (the node's is 1024); global: <= 0 none, > 0 a window
  * num_splits   thread blocks the keys are cut among: 0 = one per SM (fewer for
  *              small calls); > 0 forces that many, 16 to 1024
- * workspace    at least attn_decode_tree_workspace_size(...) bytes, no
- *              initialisation; not shared by calls that may overlap
+ * workspace    attn_decode_tree_workspace_size(...) bytes for the call's
+ *              arguments or larger ones (or attn_decode_tree_plan's for exactly
+ *              its arguments); no initialisation; not shared by calls that may
+ *              overlap
  * status       a sequence with n > L, n > max_q, L beyond the table or rows past
  *              total_q raises ATTN_DEV_BAD_SEQ_LEN and its rows are not
  *              written; a cu_q that decreases anywhere raises it too and nothing
@@ -91,9 +93,12 @@ int32_t attn_decode_global_tree(const void* q, const void* k_pool, const void* v
 /*
  * attn_decode_tree_plan -- the launch plan of the calls above, as pure host
  * arithmetic: thread blocks, kernels launched (1 or 2) and workspace bytes (any
- * of the three may be NULL) on a device of num_sms multiprocessors.
- * attn_decode_tree_workspace_size -- the workspace for the current CUDA device
- * (0, with attn_last_error, on bad arguments or when no device can be queried).
+ * of the three may be NULL) on a device of num_sms multiprocessors.  A call of
+ * fewer or shorter sequences may need more than one of many that are not cut.
+ * attn_decode_tree_workspace_size -- a workspace for the current CUDA device
+ * that serves these arguments and any smaller batch, max_q or max_seq_len (same
+ * window and num_splits; 0, with attn_last_error, on bad arguments or when no
+ * device can be queried).
  */
 int32_t attn_decode_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_seq_len, int32_t window,
                               int32_t num_splits, int32_t num_sms, int32_t* out_num_splits, int32_t* out_launches,

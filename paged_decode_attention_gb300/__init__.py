@@ -1079,7 +1079,8 @@ def attn_decode_tree_plan(kind, batch, max_q, max_seq_len, window, num_splits=0,
 
 
 def attn_decode_tree_workspace_size(kind, batch, max_q, max_seq_len, window, num_splits=0):
-    """Workspace bytes of attn_decode_*_tree for the current CUDA device."""
+    """Workspace bytes of attn_decode_*_tree for the current CUDA device, for these arguments and any smaller batch, max_q
+    or max_seq_len (attn_decode_tree_plan has what exactly these need)."""
     n = load().attn_decode_tree_workspace_size(kind, batch, max_q, max_seq_len, window, num_splits)
     if n == 0:
         raise AttnDecodeError(1, attn_last_error())
@@ -1111,7 +1112,8 @@ def _tree_args(kind, q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o=
         window = 1024 if kind == KIND_SLIDING else 0
     if workspace is None:
         with torch.cuda.device(device):
-            workspace = torch.empty(attn_decode_tree_workspace_size(kind, batch, max_q, max_seq_len, window, num_splits),
+            sms = torch.cuda.get_device_properties(device).multi_processor_count
+            workspace = torch.empty(attn_decode_tree_plan(kind, batch, max_q, max_seq_len, window, num_splits, sms)[2],
                                     dtype=torch.uint8, device=device)
     keep = (q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o, workspace, status)
     args = tuple(ptrs) + (batch, total_q, int(max_q), max_blocks, n, int(max_seq_len), int(window),
@@ -1358,8 +1360,8 @@ def attn_decode_sliding_tree(q, k_pool, v_pool, block_table, seq_lens, cu_q, par
     [T,16,256] packed by sequence (cu_q int32 [B+1]), pools [P,16,8,256], seq_lens int32 [B] with the nodes, parents
     int32 [T] (node of the same sequence, -1: the context) -> o [T,16,256].
 
-    max_q: host bound on a tree's nodes (default: the most there can be, MAX_TREE or T).  workspace: at least
-    attn_decode_tree_workspace_size(...) bytes; allocated per call when None."""
+    max_q: host bound on a tree's nodes (default: the most there can be, MAX_TREE or T).  workspace: uint8, of
+    attn_decode_tree_workspace_size(...) bytes for these arguments or larger ones; allocated per call when None."""
     return _once(stream, _tree_args, KIND_SLIDING, q, k_pool, v_pool, block_table, seq_lens, cu_q, parents, o,
                  max_q=max_q, max_seq_len=max_seq_len, window=window, out_dtype=out_dtype, num_splits=num_splits,
                  workspace=workspace, status=status)

@@ -34,6 +34,7 @@ struct TreePlan {
   bool whole;
   bool merge;    // a sequence may be cut (however low the caller's bound on the lengths): a second kernel
   size_t part_o_bytes, part_ml_bytes, workspace_bytes;
+  size_t covering_bytes;  // workspace of calls with these arguments or smaller batch, max_q or max_seq_len
 };
 
 // Rows of the configuration that holds a whole tree of max_q nodes, or the widest.  us a call with 32, 64 and 128 rows: 200
@@ -77,20 +78,24 @@ int32_t make_tree_plan(int32_t kind, int32_t batch, int32_t max_q, int32_t max_s
   out->whole = num_splits == 0 && whole_items <= num_sms &&
                pages * (2 * num_sms - whole_items) <= 2 * (kTreeWholePages * num_sms + kTreeWholeStarts * whole_items);
   out->merge = !out->whole;
+  const int64_t useful = (items * (pages + out->seg_weight) + tr::kMinPer - 1) / tr::kMinPer;
+  const int64_t least = tr::kMaxGroups;  // a run for every list
+  const int cut_grid = num_splits > 0 ? num_splits
+                                      : static_cast<int>(std::max<int64_t>(least, std::min<int64_t>({num_sms, useful, tr::kMaxGrid})));
+  out->grid = cut_grid;
   if (out->whole) {
     out->lists = whole_lists;
     out->grid = static_cast<int>(whole_items);
-  } else if (num_splits > 0) {
-    out->grid = num_splits;
-  } else {
-    const int64_t useful = (items * (pages + out->seg_weight) + tr::kMinPer - 1) / tr::kMinPer;
-    const int64_t least = tr::kMaxGroups;  // a run for every list
-    out->grid = static_cast<int>(std::max<int64_t>(least, std::min<int64_t>({num_sms, useful, tr::kMaxGrid})));
   }
-  const size_t rows = 2 * static_cast<size_t>(out->grid) * out->rows;
-  out->part_o_bytes = out->merge ? align256(rows * d * sizeof(float)) : 0;
-  out->part_ml_bytes = out->merge ? align256(rows * sizeof(float2)) : 0;
-  out->workspace_bytes = out->part_o_bytes + out->part_ml_bytes + align256(static_cast<size_t>(out->grid) * sizeof(int4));
+  const auto part_o = [&](int grid) { return align256(2 * static_cast<size_t>(grid) * out->rows * d * sizeof(float)); };
+  const auto part_ml = [&](int grid) { return align256(2 * static_cast<size_t>(grid) * out->rows * sizeof(float2)); };
+  const auto cuts = [](int grid) { return align256(static_cast<size_t>(grid) * sizeof(int4)); };
+  out->part_o_bytes = out->merge ? part_o(out->grid) : 0;
+  out->part_ml_bytes = out->merge ? part_ml(out->grid) : 0;
+  out->workspace_bytes = out->part_o_bytes + out->part_ml_bytes + cuts(out->grid);
+  // A call of fewer or shorter sequences may be cut where this one is not.  Rows, pages, items and the start weight grow
+  // with every argument, so the cut plan of these covers the cut plans of smaller ones, and any whole one.
+  out->covering_bytes = std::max(part_o(cut_grid) + part_ml(cut_grid) + cuts(cut_grid), cuts(num_sms));
   return ATTN_OK;
 }
 
@@ -319,7 +324,7 @@ size_t attn_decode_tree_workspace_size(int32_t kind, int32_t batch, int32_t max_
   if (current_device(&dev, &num_sms) != ATTN_OK) return 0;
   TreePlan plan;
   if (make_tree_plan(kind, batch, max_q, max_seq_len, window, num_splits, num_sms, &plan) != ATTN_OK) return 0;
-  return plan.workspace_bytes;
+  return plan.covering_bytes;
 }
 
 int32_t attn_kv_append_sliding_tree(const void* qkv, const void* w_q, const void* w_k, const int32_t* block_table,
