@@ -404,7 +404,8 @@ __device__ __noinline__ void make_schedule(const TreeParams& p, Shared& s, bool 
     } else {
       const int grid = static_cast<int>(gridDim.x);
       const int sum = __reduce_add_sync(0xffffffffu, total);
-      int lo = max(kMinPer, (sum * C::kHkv + grid - 1) / grid);  // (at most 256 * 16388 pages * 8 heads a list)
+      // (sum * kHkv <= 256 sequences * (16384 pages + seg_weight) * 16, lists times KV heads at most: 2^27)
+      int lo = max(kMinPer, (sum * C::kHkv + grid - 1) / grid);
       // (every list's last run may be short: with that many runs less there is room for all)
       const int lists = p.lists * C::kHkv;
       int hi = __reduce_max_sync(0xffffffffu, total);
