@@ -28,8 +28,8 @@ namespace tree {
 
 constexpr int kMaxGroups = 16;              // of rows, per KV head; the smallest grid
 // Pages of the smallest run: fewer mean more partials to merge, more leave blocks without work.  us a call with 2, 4 and 8:
-// one global tree of 4 nodes behind 900 positions 13.0, 13.9, 15.6; 8 of them behind 800 25.4, 19.0, 19.4; one of 8 behind
-// 2000 19.4, 15.5, 15.7.
+// one global tree of 4 nodes behind 900 positions 12.8, 13.6, 15.1; 8 of them behind 800 22.8, 20.0, 19.7; one of 8 behind
+// 2000 19.4, 15.7, 16.5.
 constexpr int kMinPer = 4;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kThreads = 384;
@@ -610,7 +610,7 @@ __device__ __forceinline__ void store_columns(const TreeParams& p, const Segment
 // behind a small call, 12 us alone for the 29 MB of 32 trees of 64 nodes.
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
-constexpr int kMergeBlocksPerSm = 6;  // (2: 64 global trees of 8 nodes 85.7 us, not 80.9; 32 of 64 nodes 515.5, not 511.6)
+constexpr int kMergeBlocksPerSm = 6;  // (2: 64 global trees of 8 nodes 85.3 us, not 77.9; 32 of 64 nodes 601.9, not 595.7)
 constexpr int kMergeInFlight = 8;
 
 struct MergeParams {
@@ -766,8 +766,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocksPerSm) merge_ker
   // An item is 128 dims of a row, a block's, or a row, a warp's: whichever waits less, in units of a load's latency.  A
   // block's first takes some six and a load for every 32 partials (they meet in shared memory), a warp's one and a bit
   // more for every kMergeInFlight / kTiles.  us a call, by blocks and by warps: 4 short sliding trees (8 partials a row)
-  // 15.2 and 13.6, a global tree of 4 nodes (15) 13.9 and 15.5, of 8 behind 30000 positions (76) 30 and 69, four of these
-  // (19, three items a block) 67 and 72, 8 of 4 nodes (13, three) 20.1 and 19.1, 32 of 64 nodes 554 and 512.
+  // 15.3 and 13.7, a global tree of 4 nodes (15) 13.8 and 16.2, of 8 behind 30000 positions (76) 31 and 70, four of these
+  // (19, three items a block) 66 and 73, 8 of 4 nodes (13, three) 20.8 and 20.9, 32 of 64 nodes 643 and 596.
   constexpr int kFly = kMergeInFlight / C::kTiles;
   const float blocks = static_cast<float>(gridDim.x), most = static_cast<float>(rows.most);
   const float by_block = 4.f + ceilf(__fdividef(carry * C::kTiles, blocks)) * (2.f + most * (1.f / (8 * kMergeWarps)));

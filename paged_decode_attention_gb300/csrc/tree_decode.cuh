@@ -32,10 +32,10 @@
 // bound that the tests derive.
 //
 // What bounds it (GB300, 2070 MHz; copy rate 6784 GB/s).  Long contexts HBM where a tree has one group: 16 trees of 4
-// nodes behind 131072 positions 632 us, the copy rate; with two groups L2, which gives all keys to both: 16 of 8 nodes
-// 771, 0.82 of it.  Many nodes on global layers shared memory: per 128 keys and four nodes 256 KB of K and V are
+// nodes behind 131072 positions 632 us, the copy rate; with two groups all keys go to both: 16 of 8 nodes 765 to 781, 0.82
+// of it, 73 KB a us into every SM with 128 KB in flight.  Many nodes on global layers shared memory: per 128 keys and four nodes 256 KB of K and V are
 // written and read as A, 128 KB read as B, 5120 clocks at 128 bytes each: 32 trees of 64 nodes behind 4000 to 8192 take
-// 600 us, 7300 clocks a step, 670 TFLOP/s.  (Pairs of CTAs on one product, cta_group::2 with 128 rows and rings of 120
+// 596 us, 7200 clocks a step, 675 TFLOP/s.  (Pairs of CTAs on one product, cta_group::2 with 128 rows and rings of 120
 // KB, read A once for both and took 790 us: too little in flight.  Pages brought into L2 ahead of the copies: 600 -> 656,
 // 771 -> 863.)  Sliding windows the softmax's chain of a step and the ends of segments: 64 trees of 17 to 45 nodes 120
 // us, 0.72 of the copy rate; 200 of 5 nodes 269, 0.95.  One short call latency: 4 nodes behind 900 positions 13.7.

@@ -23,7 +23,7 @@ constexpr int kTreeWholePages = 16, kTreeWholeStarts = 32;
 // What a sequence's start and end cost a block, in pages: its Q, its masks, the sums, the stores, some 12 us in all.
 // Where few sequences are spread over many blocks they pay it side by side, and a large weight would only leave blocks
 // without pages.  Weights 4, 12, 24 and 48 in us: 64 sliding trees of up to 45 nodes 127, 122, 123, 125; 8 of 26 nodes
-// 26.5, 24.8, 24.5, 27.4; 4 short ones 14.9, 16.6, 17.0, 18.5; 8 ragged global trees 44.4, 42.1, 42.6, 44.0.
+// 26.5, 24.8, 24.5, 27.4; 4 short ones 14.9, 16.6, 17.0, 18.5; 8 ragged global trees 42.1, 40.5, 41.1, 42.9.
 constexpr int kTreeSegWeight = 12, kTreeSegWeightFew = 4;
 
 struct TreePlan {
